@@ -264,7 +264,8 @@ def _append(codes, exps, x, table, start):
     need = _exponent(torch.where(f, v.abs(), 0.0).amax((-2, -1)))
     was = exps[page].to(torch.int32) - 127
     e = torch.where(old.any(-1)[..., None], torch.maximum(was, need), need)
-    v = torch.where(f, v * _pow2(-e)[..., None, None], torch.where(o, codes[page].float() * _pow2(was - e)[..., None, None], 0.0))
+    held = codes[page]                                                          # slots after the new tokens stay as they are
+    v = torch.where(f, v * _pow2(-e)[..., None, None], held.float() * torch.where(o, _pow2(was - e)[..., None, None], 1.0))
     there = fresh.any(-1)
     codes[page[there]] = v[there].to(F8)
     exps[page[there]] = (e + 127).to(torch.uint8)[there]
@@ -344,7 +345,7 @@ def exact(case, seed):
                 scale = _scale64(x.abs().amax((1, 2)))
                 if lo > t0:
                     scale = torch.maximum(scale, scales)
-                kept = codes * (scales / scale)[:, None, None] * (slot < lo - t0)[None, :, None]
+                kept = codes * torch.where(slot < lo - t0, (scales / scale)[:, None], 1.0)[..., None]
                 kept[:, lo - t0:hi - t0] = x / scale[:, None, None]
                 codes.copy_(_nearest(kept))
                 scales.copy_(scale)
