@@ -423,6 +423,152 @@ gptq_status gptq_debug_hessian_lost_stage(const void *X, int xdtype, int64_t n_t
                                           int64_t lost_stage, uint64_t wait_ns, void *status_ws,
                                           gptq_stream_t stream);
 
+/* ======================================================================================
+ * 8-bit serving of quantized layers
+ *
+ * The pages end with the quantized layer; the calls below run a decoder on such layers with
+ * 8-bit operands, and have no counterpart in the pages.
+ *
+ * Number format: e4m3 codes with one exponent byte E for each block of elements; an element
+ * is code * 2^(E - 127).  A block whose largest finite magnitude is a has
+ *   e = ceil(log2(a / 448)) limited to [-96, 120]  (-96 for a block of zeros),  E = e + 127,
+ * and its codes are x * 2^-e rounded to nearest even.  An element that is not finite becomes
+ * the NaN code.  A matrix [rows, d] of this format is
+ *   codes  [rows, ldc] bytes, 16-byte aligned, ldc a multiple of 16 and >= d;
+ *   exps   [rows or ceil(rows / 128), lde] bytes, 4-byte aligned, lde a multiple of 4 and
+ *          >= ceil(d / 128): blocks of 1 x 128 (activations) or 128 x 128 (weights) elements;
+ *   and optionally an fp32 factor per row (the norm's 1/rms; GPTQ's per-row step).
+ * Bytes between a row's end and its pitch are neither read into a result nor written.
+ * ====================================================================================== */
+
+/*
+ * gptq_rmsnorm_fp8: h = X + R;  u = h * weight;  rstd = (mean(h^2) + eps)^-1/2 per row;
+ * codes and exponents of u by 1 x 128 blocks.  The normalised row is rstd * u: rstd is handed
+ * to gptq_fp8_matmul as the row's scale (the codes of a floating format are the same with or
+ * without it).  h and u are taken in fp32 (u from the unrounded h); H is h rounded to xdtype.
+ *
+ *   X, R, H    [rows, d] of xdtype (F16, BF16 or F32) with row pitches ldx, ldr, ldh >= d.  R
+ *              (the residual) and H may be NULL; H may be X or R itself.  16-byte aligned
+ *              rows are read and written 16 bytes at a time, others element by element.
+ *   weight     [d] of wdtype: xdtype, or F32.
+ *   rows >= 0, d >= 1; eps >= 0.   rstd [rows] fp32 out.
+ * Asynchronous.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+gptq_status gptq_rmsnorm_fp8(const void *X, int xdtype, int64_t rows, int64_t d, int64_t ldx,
+                             const void *R, int64_t ldr, const void *weight, int wdtype,
+                             float eps, void *H, int64_t ldh, uint8_t *codes, int64_t ldc,
+                             uint8_t *exps, int64_t lde, float *rstd, gptq_stream_t stream);
+
+/*
+ * gptq_fp8_quantize: X [rows, d] of xdtype to e4m3 codes and exponents, by blocks of
+ * row_block x 128 elements: row_block 1 (activations) or 128 (weights).
+ * Asynchronous.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+gptq_status gptq_fp8_quantize(const void *X, int xdtype, int64_t rows, int64_t d, int64_t ldx,
+                              int row_block, uint8_t *codes, int64_t ldc, uint8_t *exps,
+                              int64_t lde, gptq_stream_t stream);
+
+/*
+ * gptq_fp8_from_codes: the packed codes of gptq_quantize_layer as an e4m3 weight matrix of
+ * 128 x 128 blocks: code - zero, an integer in [-15, 15] at 2, 3 and 4 bits, is an exact e4m3
+ * value; every exponent is 2^0.  With gptq_quantize_layer's scale as the row factor the
+ * matrix is exactly W_hat.  8-bit codes do not fit e4m3: UNSUPPORTED.
+ *   qpacked, bits, zero: as written by gptq_quantize_layer for [d_out, d_in].
+ * Asynchronous.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+gptq_status gptq_fp8_from_codes(const uint32_t *qpacked, int bits, const int32_t *zero,
+                                int64_t d_out, int64_t d_in, uint8_t *codes, int64_t ldc,
+                                uint8_t *exps, int64_t lde, gptq_stream_t stream);
+
+/*
+ * gptq_fp8_matmul_workspace_bytes: workspace size gptq_fp8_matmul needs.  0 for bad arguments.
+ */
+size_t gptq_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/*
+ * gptq_fp8_matmul: out [m, n] = diag(a_scale) A W^T diag(w_scale), A [m, k] in 1 x 128 blocks
+ * and W [n, k] in 128 x 128 blocks; products accumulated in fp32, rounded once to odtype.
+ *
+ *   a_scale    [m] fp32 or NULL (1);  w_scale: [n] fp32 or NULL (1).
+ *   out        [m, ldo] of odtype (F16 or BF16), ldo >= n.
+ *   m >= 0 (0: nothing is done), n >= 1, k >= 1.
+ *   ws         workspace of ws_bytes >= gptq_fp8_matmul_workspace_bytes(m, n, k).
+ * Repeated calls give identical results.  Asynchronous; a bounded device wait that gave up is
+ * recorded in ws (gptq_workspace_status).  Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED, CUDA.
+ */
+gptq_status gptq_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_exps, int64_t ldae,
+                            const float *a_scale, const uint8_t *w, int64_t ldw,
+                            const uint8_t *w_exps, int64_t ldwe, const float *w_scale, int64_t m,
+                            int64_t n, int64_t k, void *out, int odtype, int64_t ldo, void *ws,
+                            size_t ws_bytes, gptq_stream_t stream);
+
+/*
+ * The 8-bit cache of keys and values: n_blocks blocks of GPTQ_KV8_BLOCK tokens,
+ *   k       [n_blocks, n_kv, GPTQ_KV8_BLOCK, dim] e4m3 codes (16-byte aligned),
+ *   v       [n_blocks, n_kv, dim, GPTQ_KV8_BLOCK] e4m3 codes (16-byte aligned; a channel's
+ *           tokens lie together),
+ *   k_exps, v_exps   [n_blocks, n_kv] exponent bytes, one for each block and head,
+ * and for each sequence a row of `table` [n_seq, ld_table] int32: table[s][i] is the block that
+ * holds its tokens [64 i, 64 i + 64).  An index outside [0, n_blocks) stands for tokens that are
+ * not there: they are not attended to, and appends to them are dropped.
+ */
+#define GPTQ_KV8_BLOCK 64
+
+/*
+ * gptq_kv8_append: writes n_new tokens of each sequence at its tokens [start[s], start[s] + n_new).
+ * A block's exponents are raised to what the new tokens need and the codes of the block's
+ * tokens before start[s] are then re-rounded by that power of two; slots after the new tokens
+ * keep their bytes.  A block that the new tokens begin takes its exponents from them alone.  A token whose value is not
+ * finite somewhere is stored with NaN codes in its key: exactly the rows that attend to it
+ * become NaN.
+ *
+ *   new_k, new_v   [n_seq, n_new, n_kv, dim] of dtype (F16, BF16 or F32), elements of a head
+ *                  contiguous; k_strides, v_strides: HOST arrays of three element strides
+ *                  (sequence, token, head), >= 0.
+ *   dim            64 or 128 (else UNSUPPORTED).
+ *   start          [n_seq] int32; tokens past max_blocks * 64 are dropped, and so is a
+ *                  sequence whose start is negative.
+ * No two sequences may append to one block.  Asynchronous.  Errors: INVALID_ARG, UNSUPPORTED,
+ * CUDA.
+ */
+gptq_status gptq_kv8_append(const void *new_k, const int64_t *k_strides, const void *new_v,
+                            const int64_t *v_strides, int dtype, int64_t n_seq, int64_t n_new,
+                            int n_kv, int dim, uint8_t *k, uint8_t *v, uint8_t *k_exps,
+                            uint8_t *v_exps, int64_t n_blocks, const int32_t *table,
+                            int64_t ld_table, int64_t max_blocks, const int32_t *start,
+                            gptq_stream_t stream);
+
+/*
+ * gptq_kv8_attention_workspace_bytes: workspace size gptq_kv8_attention needs.  0 for bad
+ * arguments.
+ */
+size_t gptq_kv8_attention_workspace_bytes(int64_t n_seq, int64_t n_new, int n_heads, int n_kv,
+                                          int dim, int64_t max_blocks);
+
+/*
+ * gptq_kv8_attention: out = softmax(scale * q K^T) V over the cached tokens, for the last
+ * n_new tokens of each sequence (their keys and values are already in the cache).
+ *
+ *   q, out     [n_seq, n_new, n_heads, dim] of dtype (F16 or BF16), elements of a head
+ *              contiguous; q_strides, o_strides: HOST arrays of three element strides.
+ *              Query head h reads cache head h / (n_heads / n_kv).
+ *   lengths    [n_seq] int32: tokens of the sequence in the cache, the new ones included,
+ *              limited to [0, 64 * max_blocks].  With causal != 0 new token t sees the tokens
+ *              [0, length - n_new + t], otherwise all `length` of them.  A row that sees
+ *              nothing gives zeros.  Bytes of the cache past `length` never matter.
+ *   scale      factor of the scores (finite).
+ *   ws         workspace of ws_bytes >= gptq_kv8_attention_workspace_bytes(...).
+ * Repeated calls give identical results.  Asynchronous; a bounded device wait that gave up is
+ * recorded in ws (gptq_workspace_status).  Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED, CUDA.
+ */
+gptq_status gptq_kv8_attention(const void *q, const int64_t *q_strides, int dtype, int64_t n_seq,
+                               int64_t n_new, int n_heads, int n_kv, int dim, const uint8_t *k,
+                               const uint8_t *v, const uint8_t *k_exps, const uint8_t *v_exps,
+                               int64_t n_blocks, const int32_t *table, int64_t ld_table,
+                               int64_t max_blocks, const int32_t *lengths, int causal,
+                               float scale, void *out, const int64_t *o_strides, void *ws,
+                               size_t ws_bytes, gptq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -4,6 +4,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "fp8.cuh"
 
 namespace gptq {
 
@@ -295,6 +296,180 @@ gptq_status gptq_workspace_status(const void *ws, gptq_stream_t stream) {
   GPTQ_CUDA_CHECK(cudaMemcpyAsync(&st, ws, sizeof(DevStatus), cudaMemcpyDeviceToHost, s));
   GPTQ_CUDA_CHECK(cudaStreamSynchronize(s));
   return (gptq_status)st.status;
+}
+
+// A matrix of codes: base and pitch alignment, pitch >= d.
+static bool fp8_codes_ok(const uint8_t *codes, int64_t ldc, int64_t d) {
+  return codes && aligned(codes, 16) && ldc >= d && ldc % 16 == 0;
+}
+static bool fp8_exps_ok(const uint8_t *exps, int64_t lde, int64_t d) {
+  return exps && aligned(exps, 4) && lde >= ceil_div(d, 128) && lde % 4 == 0;
+}
+constexpr int64_t kFp8MaxWidth = (int64_t)1 << 20, kFp8MaxRows = (int64_t)1 << 22;
+
+gptq_status gptq_rmsnorm_fp8(const void *X, int xdtype, int64_t rows, int64_t d, int64_t ldx,
+                             const void *R, int64_t ldr, const void *weight, int wdtype,
+                             float eps, void *H, int64_t ldh, uint8_t *codes, int64_t ldc,
+                             uint8_t *exps, int64_t lde, float *rstd, gptq_stream_t stream) {
+  const size_t es = elem_size(xdtype);
+  if (es == 0 || (wdtype != xdtype && wdtype != GPTQ_F32)) return GPTQ_ERR_INVALID_ARG;
+  if (rows < 0 || d < 1 || ldx < d || (R && ldr < d) || (H && ldh < d) || !(eps >= 0.0f))
+    return GPTQ_ERR_INVALID_ARG;
+  if (!weight || !aligned(weight, elem_size(wdtype))) return GPTQ_ERR_INVALID_ARG;
+  if (rows > 0 && (!X || !rstd || !fp8_codes_ok(codes, ldc, d) || !fp8_exps_ok(exps, lde, d)))
+    return GPTQ_ERR_INVALID_ARG;
+  if (!aligned(X, es) || (R && !aligned(R, es)) || (H && !aligned(H, es)) || !aligned(rstd, 4))
+    return GPTQ_ERR_INVALID_ARG;
+  if (d > kFp8MaxWidth || rows > kFp8MaxRows) return GPTQ_ERR_UNSUPPORTED;
+  return launch_rmsnorm_fp8(X, xdtype, rows, d, ldx, R, ldr, weight, wdtype, eps, H, ldh, codes,
+                            ldc, exps, lde, rstd, (cudaStream_t)stream);
+}
+
+gptq_status gptq_fp8_quantize(const void *X, int xdtype, int64_t rows, int64_t d, int64_t ldx,
+                              int row_block, uint8_t *codes, int64_t ldc, uint8_t *exps,
+                              int64_t lde, gptq_stream_t stream) {
+  const size_t es = elem_size(xdtype);
+  if (es == 0 || rows < 0 || d < 1 || ldx < d || (row_block != 1 && row_block != fp8::kBlock))
+    return GPTQ_ERR_INVALID_ARG;
+  if (rows > 0 && (!X || !aligned(X, es) || !fp8_codes_ok(codes, ldc, d) ||
+                   !fp8_exps_ok(exps, lde, d)))
+    return GPTQ_ERR_INVALID_ARG;
+  if (d > kFp8MaxWidth || rows > kFp8MaxRows) return GPTQ_ERR_UNSUPPORTED;
+  return launch_fp8_quantize(X, xdtype, rows, d, ldx, row_block, codes, ldc, exps, lde,
+                             (cudaStream_t)stream);
+}
+
+gptq_status gptq_fp8_from_codes(const uint32_t *qpacked, int bits, const int32_t *zero,
+                                int64_t d_out, int64_t d_in, uint8_t *codes, int64_t ldc,
+                                uint8_t *exps, int64_t lde, gptq_stream_t stream) {
+  if (!(bits == 2 || bits == 3 || bits == 4 || bits == 8)) return GPTQ_ERR_INVALID_ARG;
+  if (d_out < 1 || d_in < 1 || !qpacked || !aligned(qpacked, 4) || !zero || !aligned(zero, 4))
+    return GPTQ_ERR_INVALID_ARG;
+  if (!fp8_codes_ok(codes, ldc, d_in) || !fp8_exps_ok(exps, lde, d_in))
+    return GPTQ_ERR_INVALID_ARG;
+  if (bits == 8 || d_in > kFp8MaxWidth || d_out > kFp8MaxRows) return GPTQ_ERR_UNSUPPORTED;
+  return launch_fp8_from_codes(qpacked, bits, zero, d_out, d_in, codes, ldc, exps, lde,
+                               (cudaStream_t)stream);
+}
+
+size_t gptq_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m < 0 || n < 1 || k < 1) return 0;
+  return fp8_matmul_ws_bytes(m, n, k);
+}
+
+gptq_status gptq_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_exps, int64_t ldae,
+                            const float *a_scale, const uint8_t *w, int64_t ldw,
+                            const uint8_t *w_exps, int64_t ldwe, const float *w_scale, int64_t m,
+                            int64_t n, int64_t k, void *out, int odtype, int64_t ldo, void *ws,
+                            size_t ws_bytes, gptq_stream_t stream) {
+  if (m < 0 || n < 1 || k < 1 || (odtype != GPTQ_F16 && odtype != GPTQ_BF16) || ldo < n)
+    return GPTQ_ERR_INVALID_ARG;
+  if (!fp8_codes_ok(w, ldw, k) || !fp8_exps_ok(w_exps, ldwe, k) || !aligned(w_scale, 4))
+    return GPTQ_ERR_INVALID_ARG;
+  if (m > 0 && (!fp8_codes_ok(a, lda, k) || !fp8_exps_ok(a_exps, ldae, k) || !aligned(a_scale, 4) ||
+                !out || !aligned(out, 2)))
+    return GPTQ_ERR_INVALID_ARG;
+  if (k > kFp8MaxWidth || m > kFp8MaxRows || n > kFp8MaxRows) return GPTQ_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, 256) || ws_bytes < fp8_matmul_ws_bytes(m, n, k))
+    return GPTQ_ERR_WORKSPACE;
+  Fp8MatmulArgs g{a, lda, a_exps, ldae, a_scale, w, ldw, w_exps, ldwe, w_scale, m, n, k,
+                  out, odtype, ldo};
+  return launch_fp8_matmul(g, ws, (cudaStream_t)stream);
+}
+
+// What the two cache calls share; `ok` = valid, UNSUPPORTED for sizes outside the limits.
+static gptq_status kv8_cache_check(int64_t n_seq, int64_t n_new, int n_kv, int dim,
+                                   const uint8_t *k, const uint8_t *v, const uint8_t *k_exps,
+                                   const uint8_t *v_exps, int64_t n_blocks, const int32_t *table,
+                                   int64_t ld_table, int64_t max_blocks) {
+  if (n_seq < 0 || n_new < 0 || n_kv < 1 || dim < 1 || n_blocks < 0 || max_blocks < 0 ||
+      ld_table < max_blocks)
+    return GPTQ_ERR_INVALID_ARG;
+  if (n_blocks > 0 && (!k || !v || !k_exps || !v_exps || !aligned(k, 16) || !aligned(v, 16)))
+    return GPTQ_ERR_INVALID_ARG;
+  if (max_blocks > 0 && n_seq > 0 && (!table || !aligned(table, 4))) return GPTQ_ERR_INVALID_ARG;
+  if ((dim != 64 && dim != 128) || n_kv > 4096 || n_seq > 65535 || n_new > (1 << 20) ||
+      max_blocks > (1 << 20) || n_blocks * n_kv > INT32_MAX)
+    return GPTQ_ERR_UNSUPPORTED;
+  return GPTQ_OK;
+}
+static bool strides_ok(const int64_t *st) {
+  return st && st[0] >= 0 && st[1] >= 0 && st[2] >= 0;
+}
+static bool strided_vec(const void *p, const int64_t *st, size_t es) {
+  return aligned(p, 16) && (st[0] * (int64_t)es) % 16 == 0 && (st[1] * (int64_t)es) % 16 == 0 &&
+         (st[2] * (int64_t)es) % 16 == 0;
+}
+
+gptq_status gptq_kv8_append(const void *new_k, const int64_t *k_strides, const void *new_v,
+                            const int64_t *v_strides, int dtype, int64_t n_seq, int64_t n_new,
+                            int n_kv, int dim, uint8_t *k, uint8_t *v, uint8_t *k_exps,
+                            uint8_t *v_exps, int64_t n_blocks, const int32_t *table,
+                            int64_t ld_table, int64_t max_blocks, const int32_t *start,
+                            gptq_stream_t stream) {
+  const size_t es = elem_size(dtype);
+  if (es == 0 || !strides_ok(k_strides) || !strides_ok(v_strides)) return GPTQ_ERR_INVALID_ARG;
+  GPTQ_TRY(kv8_cache_check(n_seq, n_new, n_kv, dim, k, v, k_exps, v_exps, n_blocks, table,
+                           ld_table, max_blocks));
+  if (n_seq == 0 || n_new == 0 || n_blocks == 0 || max_blocks == 0) return GPTQ_OK;
+  if (!new_k || !new_v || !aligned(new_k, es) || !aligned(new_v, es) || !start ||
+      !aligned(start, 4))
+    return GPTQ_ERR_INVALID_ARG;
+  Kv8AppendArgs g{};
+  g.new_k = new_k; g.new_v = new_v; g.dtype = dtype;
+  for (int i = 0; i < 3; ++i) {
+    g.k_stride[i] = k_strides[i];
+    g.v_stride[i] = v_strides[i];
+  }
+  g.vec_k = strided_vec(new_k, k_strides, es);
+  g.vec_v = strided_vec(new_v, v_strides, es);
+  g.n_seq = (int)n_seq; g.n_new = n_new; g.n_kv = n_kv; g.dim = dim;
+  g.k = k; g.v = v; g.k_exps = k_exps; g.v_exps = v_exps; g.n_blocks = n_blocks;
+  g.table = table; g.ld_table = ld_table; g.max_blocks = (int)max_blocks;
+  g.start = start;
+  return launch_kv8_append(g, (cudaStream_t)stream);
+}
+
+size_t gptq_kv8_attention_workspace_bytes(int64_t n_seq, int64_t n_new, int n_heads, int n_kv,
+                                          int dim, int64_t max_blocks) {
+  if (n_seq < 0 || n_seq > 65535 || n_new < 0 || n_new > (1 << 20) || n_kv < 1 || n_kv > 4096 ||
+      n_heads < 1 || n_heads % n_kv != 0 || (dim != 64 && dim != 128) || max_blocks < 0 ||
+      max_blocks > (1 << 20))
+    return 0;
+  return kv8_attention_ws_bytes((int)n_seq, n_new, n_heads, n_kv, dim, (int)max_blocks);
+}
+
+gptq_status gptq_kv8_attention(const void *q, const int64_t *q_strides, int dtype, int64_t n_seq,
+                               int64_t n_new, int n_heads, int n_kv, int dim, const uint8_t *k,
+                               const uint8_t *v, const uint8_t *k_exps, const uint8_t *v_exps,
+                               int64_t n_blocks, const int32_t *table, int64_t ld_table,
+                               int64_t max_blocks, const int32_t *lengths, int causal,
+                               float scale, void *out, const int64_t *o_strides, void *ws,
+                               size_t ws_bytes, gptq_stream_t stream) {
+  if ((dtype != GPTQ_F16 && dtype != GPTQ_BF16) || !strides_ok(q_strides) || !strides_ok(o_strides))
+    return GPTQ_ERR_INVALID_ARG;
+  if (n_heads < 1 || n_kv < 1 || n_heads % n_kv != 0 || !(scale - scale == 0.0f))
+    return GPTQ_ERR_INVALID_ARG;
+  GPTQ_TRY(kv8_cache_check(n_seq, n_new, n_kv, dim, k, v, k_exps, v_exps, n_blocks, table,
+                           ld_table, max_blocks));
+  if (n_heads > 65535) return GPTQ_ERR_UNSUPPORTED;
+  if (n_seq > 0 && n_new > 0 && (!q || !out || !aligned(q, 2) || !aligned(out, 2) || !lengths ||
+                                 !aligned(lengths, 4)))
+    return GPTQ_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256) ||
+      ws_bytes < kv8_attention_ws_bytes((int)n_seq, n_new, n_heads, n_kv, dim, (int)max_blocks))
+    return GPTQ_ERR_WORKSPACE;
+  Kv8AttentionArgs g{};
+  g.q = q; g.out = out; g.dtype = dtype;
+  for (int i = 0; i < 3; ++i) {
+    g.q_stride[i] = q_strides[i];
+    g.o_stride[i] = o_strides[i];
+  }
+  g.n_seq = (int)n_seq; g.n_new = n_new; g.n_heads = n_heads; g.n_kv = n_kv; g.dim = dim;
+  g.k = k; g.v = v; g.k_exps = k_exps; g.v_exps = v_exps; g.n_blocks = n_blocks;
+  g.table = table; g.ld_table = ld_table; g.max_blocks = (int)max_blocks;
+  g.lengths = lengths; g.causal = causal ? 1 : 0; g.scale = scale;
+  return launch_kv8_attention(g, ws, (cudaStream_t)stream);
 }
 
 }  // extern "C"

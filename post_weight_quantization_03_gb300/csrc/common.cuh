@@ -68,7 +68,7 @@ gptq_status launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   }
   return GPTQ_OK;
 }
-static inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+static inline __host__ __device__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Device-side status block at the start of every workspace.
 struct DevStatus {
@@ -189,5 +189,56 @@ gptq_status launch_quantize_obq(const void *W, int wdtype, int64_t m, int64_t d,
                                 uint32_t *qpacked, float *scale, int32_t *zero, float *W_hat,
                                 int32_t *order, void *ws, cudaStream_t s);
 size_t quantize_obq_ws_bytes(int64_t m, int64_t d);
+
+// fp8_quantize.cu: e4m3 codes with an exponent byte per block (see fp8.cuh)
+gptq_status launch_rmsnorm_fp8(const void *X, int xdtype, int64_t rows, int64_t d, int64_t ldx,
+                               const void *R, int64_t ldr, const void *weight, int wdtype,
+                               float eps, void *H, int64_t ldh, uint8_t *codes, int64_t ldc,
+                               uint8_t *exps, int64_t lde, float *rstd, cudaStream_t s);
+gptq_status launch_fp8_quantize(const void *X, int xdtype, int64_t rows, int64_t d, int64_t ldx,
+                                int row_block, uint8_t *codes, int64_t ldc, uint8_t *exps,
+                                int64_t lde, cudaStream_t s);
+gptq_status launch_fp8_from_codes(const uint32_t *qpacked, int bits, const int32_t *zero,
+                                  int64_t m, int64_t d, uint8_t *codes, int64_t ldc,
+                                  uint8_t *exps, int64_t lde, cudaStream_t s);
+
+// fp8_matmul.cu: the block-scaled product (gptq_fp8_matmul)
+struct Fp8MatmulArgs {
+  const uint8_t *a; int64_t lda;     // [M, K] codes
+  const uint8_t *ae; int64_t ldae;   // [M, ceil(K / 128)] exponents
+  const float *ra;                   // [M] row scale or null
+  const uint8_t *w; int64_t ldw;     // [N, K] codes
+  const uint8_t *we; int64_t ldwe;   // [ceil(N / 128), ceil(K / 128)] exponents
+  const float *rw;                   // [N] row scale or null
+  int64_t M, N, K;
+  void *out; int odtype; int64_t ldo;
+};
+size_t fp8_matmul_ws_bytes(int64_t M, int64_t N, int64_t K);
+gptq_status launch_fp8_matmul(const Fp8MatmulArgs &g, void *ws, cudaStream_t s);
+
+// kv8_append.cu, kv8_attention.cu: the 8-bit cache (gptq_kv8_append, gptq_kv8_attention)
+struct Kv8AppendArgs {
+  const void *new_k, *new_v; int dtype;      // [n_seq, n_new, n_kv, dim], element strides below
+  int64_t k_stride[3], v_stride[3];          // sequence, token, head
+  int vec_k, vec_v;                          // 16-byte aligned tokens
+  int n_seq; int64_t n_new; int n_kv, dim;
+  uint8_t *k, *v, *k_exps, *v_exps; int64_t n_blocks;
+  const int32_t *table; int64_t ld_table; int max_blocks;
+  const int32_t *start;
+};
+gptq_status launch_kv8_append(const Kv8AppendArgs &g, cudaStream_t s);
+struct Kv8AttentionArgs {
+  const void *q; int dtype;                  // [n_seq, n_new, n_heads, dim]
+  int64_t q_stride[3], o_stride[3];
+  void *out;
+  int n_seq; int64_t n_new; int n_heads, n_kv, dim;
+  const uint8_t *k, *v, *k_exps, *v_exps; int64_t n_blocks;
+  const int32_t *table; int64_t ld_table; int max_blocks;
+  const int32_t *lengths;
+  int causal; float scale;
+};
+size_t kv8_attention_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int dim,
+                              int max_blocks);
+gptq_status launch_kv8_attention(const Kv8AttentionArgs &g, void *ws, cudaStream_t s);
 
 }  // namespace gptq

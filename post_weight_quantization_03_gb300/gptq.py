@@ -69,10 +69,40 @@ _SIGS = {
     "gptq_debug_hessian_lost_stage": (_c.c_int, [_c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64,
                                                  _c.c_int64, _c.c_void_p, _c.c_int64,
                                                  _c.c_uint64, _c.c_void_p, _c.c_void_p]),
+    "gptq_rmsnorm_fp8": (_c.c_int, [_c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64,
+                                    _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int, _c.c_float,
+                                    _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
+                                    _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p]),
+    "gptq_fp8_quantize": (_c.c_int, [_c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64,
+                                     _c.c_int, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
+                                     _c.c_void_p]),
+    "gptq_fp8_from_codes": (_c.c_int, [_c.c_void_p, _c.c_int, _c.c_void_p, _c.c_int64,
+                                       _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_void_p,
+                                       _c.c_int64, _c.c_void_p]),
+    "gptq_fp8_matmul_workspace_bytes": (_c.c_size_t, [_c.c_int64, _c.c_int64, _c.c_int64]),
+    "gptq_fp8_matmul": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_void_p,
+                                   _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_void_p,
+                                   _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_int,
+                                   _c.c_int64, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "gptq_kv8_append": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int,
+                                   _c.c_int64, _c.c_int64, _c.c_int, _c.c_int, _c.c_void_p,
+                                   _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64,
+                                   _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p,
+                                   _c.c_void_p]),
+    "gptq_kv8_attention_workspace_bytes": (_c.c_size_t, [_c.c_int64, _c.c_int64, _c.c_int,
+                                                         _c.c_int, _c.c_int, _c.c_int64]),
+    "gptq_kv8_attention": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64,
+                                      _c.c_int, _c.c_int, _c.c_int, _c.c_void_p, _c.c_void_p,
+                                      _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_void_p,
+                                      _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_int, _c.c_float,
+                                      _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_size_t,
+                                      _c.c_void_p]),
 }
 NOALLOC_SCRATCH_BYTES = 32 << 20  # GPTQ_NOALLOC_SCRATCH_BYTES in include/gptq.h
 OBQ_MAX_D_IN = 128                # GPTQ_OBQ_MAX_D_IN in include/gptq.h
 MAX_SHARED_LAYERS = 64            # GPTQ_MAX_SHARED_LAYERS in include/gptq.h
+FP8_BLOCK = 128                   # elements of K (and weight rows) that share an exponent
+KV8_BLOCK = 64                    # GPTQ_KV8_BLOCK in include/gptq.h
 
 _lib = None
 
@@ -211,6 +241,53 @@ def gptq_debug_hessian_lost_stage(X, xdtype, n_tok, d_in, ldx, H, lost_stage, wa
                                   stream):
     return load().gptq_debug_hessian_lost_stage(X, xdtype, n_tok, d_in, ldx, H, lost_stage,
                                                 wait_ns, status_ws, stream)
+
+
+def gptq_rmsnorm_fp8(X, xdtype, rows, d, ldx, R, ldr, weight, wdtype, eps, H, ldh, codes, ldc,
+                     exps, lde, rstd, stream):
+    return load().gptq_rmsnorm_fp8(X, xdtype, rows, d, ldx, R, ldr, weight, wdtype, eps, H, ldh,
+                                   codes, ldc, exps, lde, rstd, stream)
+
+
+def gptq_fp8_quantize(X, xdtype, rows, d, ldx, row_block, codes, ldc, exps, lde, stream):
+    return load().gptq_fp8_quantize(X, xdtype, rows, d, ldx, row_block, codes, ldc, exps, lde,
+                                    stream)
+
+
+def gptq_fp8_from_codes(qpacked, bits, zero, d_out, d_in, codes, ldc, exps, lde, stream):
+    return load().gptq_fp8_from_codes(qpacked, bits, zero, d_out, d_in, codes, ldc, exps, lde,
+                                      stream)
+
+
+def gptq_fp8_matmul_workspace_bytes(m, n, k):
+    return load().gptq_fp8_matmul_workspace_bytes(m, n, k)
+
+
+def gptq_fp8_matmul(a, lda, a_exps, ldae, a_scale, w, ldw, w_exps, ldwe, w_scale, m, n, k, out,
+                    odtype, ldo, ws, ws_bytes, stream):
+    return load().gptq_fp8_matmul(a, lda, a_exps, ldae, a_scale, w, ldw, w_exps, ldwe, w_scale,
+                                  m, n, k, out, odtype, ldo, ws, ws_bytes, stream)
+
+
+def gptq_kv8_append(new_k, k_strides, new_v, v_strides, dtype, n_seq, n_new, n_kv, dim, k, v,
+                    k_exps, v_exps, n_blocks, table, ld_table, max_blocks, start, stream):
+    return load().gptq_kv8_append(new_k, k_strides, new_v, v_strides, dtype, n_seq, n_new, n_kv,
+                                  dim, k, v, k_exps, v_exps, n_blocks, table, ld_table,
+                                  max_blocks, start, stream)
+
+
+def gptq_kv8_attention_workspace_bytes(n_seq, n_new, n_heads, n_kv, dim, max_blocks):
+    return load().gptq_kv8_attention_workspace_bytes(n_seq, n_new, n_heads, n_kv, dim,
+                                                     max_blocks)
+
+
+def gptq_kv8_attention(q, q_strides, dtype, n_seq, n_new, n_heads, n_kv, dim, k, v, k_exps,
+                       v_exps, n_blocks, table, ld_table, max_blocks, lengths, causal, scale,
+                       out, o_strides, ws, ws_bytes, stream):
+    return load().gptq_kv8_attention(q, q_strides, dtype, n_seq, n_new, n_heads, n_kv, dim, k, v,
+                                     k_exps, v_exps, n_blocks, table, ld_table, max_blocks,
+                                     lengths, causal, scale, out, o_strides, ws, ws_bytes,
+                                     stream)
 
 
 # ---------------------------------------------------------------------------------------
@@ -484,3 +561,215 @@ def quantize_obq(W, U, bits=4, dead_mask=None, ws=None, stream=None):
                              _ptr(W_hat), _ptr(order), _ptr(ws), ws.numel(), _stream(stream)),
            "gptq_quantize_obq")
     return qpacked, scale, zero, W_hat, order
+
+
+# ---------------------------------------------------------------------------------------
+# 8-bit serving
+# ---------------------------------------------------------------------------------------
+
+def _lend(stream, *tensors):
+    """Tells torch's allocator that buffers made here for a call on ``stream`` are in use there."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _fp8_empty(rows, d, row_block, device, stream):
+    """Codes and exponents of a ``[rows, d]`` e4m3 matrix, in the pitches the library asks for."""
+    torch = _torch()
+    codes = torch.empty(rows, -(-d // 16) * 16, dtype=torch.float8_e4m3fn, device=device)
+    kb = -(-d // FP8_BLOCK)
+    exps = torch.empty(-(-rows // row_block), -(-kb // 4) * 4, dtype=torch.uint8, device=device)
+    _lend(stream, codes, exps)
+    return codes[:, :d], exps[:, :kb]
+
+
+def _row_major(name, t, rows=None, d=None):
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (
+            rows is not None and t.shape[0] != rows) or (d is not None and t.shape[1] != d):
+        want = f"[{'rows' if rows is None else rows}, {'d' if d is None else d}]"
+        raise ValueError(f"{name} must be a row-major {want} matrix")
+
+
+def rmsnorm_fp8(X, weight, residual=None, eps=1e-6, want_h=True, stream=None):
+    """RMS norm with the residual's addition and e4m3 output.
+
+    ``h = X + residual``; returns ``(codes, exps, rstd, h)``: the codes and exponents of
+    ``h * weight`` by 1 x 128 blocks and ``rstd`` per row, so that the normalised row is
+    ``rstd * 2**(exps - 127) * codes`` (hand ``rstd`` to ``fp8_matmul`` as ``a_scale``).
+    ``h`` is X itself when there is no residual, None when ``want_h`` is false."""
+    torch = _torch()
+    _row_major("X", X)
+    n, d = X.shape
+    if residual is not None:
+        _row_major("residual", residual, n, d)
+        if residual.dtype != X.dtype:
+            raise TypeError("residual must have X's dtype")
+    if weight.shape != (d,) or (d > 1 and weight.stride(0) != 1):
+        raise ValueError("weight must be a contiguous [d] vector")
+    codes, exps = _fp8_empty(n, d, 1, X.device, stream)
+    rstd = torch.empty(n, dtype=torch.float32, device=X.device)
+    h = X
+    if residual is not None or not want_h:
+        h = torch.empty(n, d, dtype=X.dtype, device=X.device) if want_h else None
+        _lend(stream, h)
+    _lend(stream, rstd)
+    out = h if h is not X else None
+    _check(gptq_rmsnorm_fp8(_ptr(X), _dtype_code(X), n, d, X.stride(0), _ptr(residual),
+                            residual.stride(0) if residual is not None else 0, _ptr(weight),
+                            _dtype_code(weight), eps, _ptr(out),
+                            out.stride(0) if out is not None else 0, _ptr(codes),
+                            codes.stride(0), _ptr(exps), exps.stride(0), _ptr(rstd),
+                            _stream(stream)), "gptq_rmsnorm_fp8")
+    return codes, exps, rstd, h
+
+
+def fp8_quantize(X, row_block=1, stream=None):
+    """``(codes, exps)`` of a ``[rows, d]`` matrix by ``row_block x 128`` blocks: 1 for
+    activations, 128 for weights."""
+    _row_major("X", X)
+    n, d = X.shape
+    codes, exps = _fp8_empty(n, d, row_block, X.device, stream)
+    _check(gptq_fp8_quantize(_ptr(X), _dtype_code(X), n, d, X.stride(0), row_block, _ptr(codes),
+                             codes.stride(0), _ptr(exps), exps.stride(0), _stream(stream)),
+           "gptq_fp8_quantize")
+    return codes, exps
+
+
+def fp8_from_codes(qpacked, zero, d_in, bits=4, stream=None):
+    """``(codes, exps)`` of a layer from ``quantize``'s packed 2-, 3- or 4-bit codes: exactly
+    ``code - zero``, so with ``quantize``'s scale as ``w_scale`` the product's weights are
+    exactly W_hat."""
+    m = qpacked.shape[0]
+    if qpacked.shape != (m, packed_words(d_in, bits)) or not qpacked.is_contiguous() \
+            or zero.shape != (m,) or not zero.is_contiguous():
+        raise ValueError("qpacked [d_out, ceil(d_in / 32) * bits] and zero [d_out] as quantize "
+                         "returns them")
+    codes, exps = _fp8_empty(m, d_in, FP8_BLOCK, qpacked.device, stream)
+    _check(gptq_fp8_from_codes(_ptr(qpacked), bits, _ptr(zero), m, d_in, _ptr(codes),
+                               codes.stride(0), _ptr(exps), exps.stride(0), _stream(stream)),
+           "gptq_fp8_from_codes")
+    return codes, exps
+
+
+def fp8_matmul(a, a_exps, w, w_exps, a_scale=None, w_scale=None, out_dtype=None, out=None,
+               ws=None, stream=None):
+    """``diag(a_scale) A W^T diag(w_scale)`` of e4m3 matrices ``A [m, k]`` (1 x 128 blocks) and
+    ``W [n, k]`` (128 x 128 blocks), ``[m, n]`` in float16 or bfloat16 (the default)."""
+    torch = _torch()
+    _row_major("a", a)
+    m, k = a.shape
+    _row_major("w", w, None, k)
+    n = w.shape[0]
+    kb = -(-k // FP8_BLOCK)
+    _row_major("a_exps", a_exps, m, kb)
+    _row_major("w_exps", w_exps, -(-n // FP8_BLOCK), kb)
+    if a.dtype != torch.float8_e4m3fn or w.dtype != torch.float8_e4m3fn or \
+            a_exps.dtype != torch.uint8 or w_exps.dtype != torch.uint8:
+        raise TypeError("codes are float8_e4m3fn and exponents uint8")
+    for name, t, rows in (("a_scale", a_scale, m), ("w_scale", w_scale, n)):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (rows,)
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 [{rows}] vector")
+    if out is None:
+        out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=a.device)
+        _lend(stream, out)
+    else:
+        _row_major("out", out, m, n)
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError("out must have out_dtype")
+    if ws is None:
+        ws = workspace(gptq_fp8_matmul_workspace_bytes(m, n, k), a.device)
+        _lend(stream, ws)
+    _check(gptq_fp8_matmul(_ptr(a), a.stride(0), _ptr(a_exps), a_exps.stride(0), _ptr(a_scale),
+                           _ptr(w), w.stride(0), _ptr(w_exps), w_exps.stride(0), _ptr(w_scale),
+                           m, n, k, _ptr(out), _dtype_code(out), out.stride(0), _ptr(ws),
+                           ws.numel(), _stream(stream)), "gptq_fp8_matmul")
+    return out
+
+
+def kv8_cache(n_blocks, n_kv_heads, dim, device=None):
+    """An empty 8-bit cache ``(k, v, k_exps, v_exps)`` of ``n_blocks`` blocks of 64 tokens: K
+    codes ``[n_blocks, n_kv_heads, 64, dim]``, V codes ``[n_blocks, n_kv_heads, dim, 64]`` and
+    an exponent byte per block and head for each."""
+    torch = _torch()
+    dev = torch.device(device) if device is not None else torch.device(
+        "cuda", torch.cuda.current_device())
+    k = torch.zeros(n_blocks, n_kv_heads, KV8_BLOCK, dim, dtype=torch.uint8, device=dev)
+    v = torch.zeros(n_blocks, n_kv_heads, dim, KV8_BLOCK, dtype=torch.uint8, device=dev)
+    exps = [torch.full((n_blocks, n_kv_heads), 127, dtype=torch.uint8, device=dev)
+            for _ in range(2)]
+    return (k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn), *exps)
+
+
+def _kv8_check(cache, table, seqs, lengths, what):
+    torch = _torch()
+    k, v, ke, ve = cache
+    if k.dim() != 4 or k.shape[2] != KV8_BLOCK:
+        raise ValueError(f"cache k must be [n_blocks, n_kv_heads, {KV8_BLOCK}, dim]")
+    nb, kv, _, d = k.shape
+    if v.shape != (nb, kv, d, KV8_BLOCK) or ke.shape != (nb, kv) or ve.shape != (nb, kv):
+        raise ValueError("cache v, k_exps, v_exps do not match k")
+    if k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn or \
+            ke.dtype != torch.uint8 or ve.dtype != torch.uint8:
+        raise TypeError("codes are float8_e4m3fn and exponents uint8")
+    if not (k.is_contiguous() and v.is_contiguous() and ke.is_contiguous()
+            and ve.is_contiguous()):
+        raise ValueError("the cache must be contiguous")
+    if table.dtype != torch.int32 or lengths.dtype != torch.int32:
+        raise TypeError(f"table and {what} must be int32")
+    _row_major("table", table, seqs)
+    if lengths.shape != (seqs,) or not lengths.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous [{seqs}] vector")
+    return nb, kv, d
+
+
+def _strides3(t):
+    s = t.stride()
+    return (ctypes.c_int64 * 3)(s[0], s[1], s[2])
+
+
+def kv8_append(cache, k, v, table, start, stream=None):
+    """Writes new keys and values ``[seqs, new, n_kv_heads, dim]`` into the cache at each
+    sequence's tokens ``[start, start + new)``; ``table [seqs, blocks]`` (int32) names the cache
+    blocks of each sequence, -1 for none."""
+    n_seq = k.shape[0]
+    nb, kv, d = _kv8_check(cache, table, n_seq, start, "start")
+    if k.dim() != 4 or k.shape[2:] != (kv, d) or v.shape != k.shape or k.dtype != v.dtype:
+        raise ValueError(f"k and v must be [seqs, new, {kv}, {d}] of one dtype")
+    if k.stride(3) != 1 or v.stride(3) != 1:
+        raise ValueError("a head's elements must be contiguous")
+    _check(gptq_kv8_append(_ptr(k), _strides3(k), _ptr(v), _strides3(v), _dtype_code(k), n_seq,
+                           k.shape[1], kv, d, _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]),
+                           _ptr(cache[3]), nb, _ptr(table), table.stride(0), table.shape[1],
+                           _ptr(start), _stream(stream)), "gptq_kv8_append")
+
+
+def kv8_attention(q, cache, table, lengths, scale=None, causal=True, out=None, ws=None,
+                  stream=None):
+    """Attention of the last ``new`` tokens' queries ``[seqs, new, heads, dim]`` over the cached
+    tokens of each sequence (``lengths`` of them, the new ones included); ``scale`` defaults to
+    ``dim ** -0.5``.  Rows that see no token give zeros."""
+    torch = _torch()
+    if q.dim() != 4 or q.stride(3) != 1:
+        raise ValueError("q must be [seqs, new, heads, dim] with a head's elements contiguous")
+    n_seq, new, heads, _ = q.shape
+    nb, kv, d = _kv8_check(cache, table, n_seq, lengths, "lengths")
+    if q.shape[3] != d:
+        raise ValueError(f"q's heads must be {d} wide, as the cache's")
+    if out is None:
+        out = torch.empty(n_seq, new, heads, d, dtype=q.dtype, device=q.device)
+        _lend(stream, out)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.stride(3) != 1:
+        raise ValueError("out must match q")
+    mb = table.shape[1]
+    if ws is None:
+        ws = workspace(gptq_kv8_attention_workspace_bytes(n_seq, new, heads, kv, d, mb), q.device)
+        _lend(stream, ws)
+    _check(gptq_kv8_attention(_ptr(q), _strides3(q), _dtype_code(q), n_seq, new, heads, kv, d,
+                              _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]), _ptr(cache[3]), nb,
+                              _ptr(table), table.stride(0), mb, _ptr(lengths), 1 if causal else 0,
+                              d ** -0.5 if scale is None else scale, _ptr(out), _strides3(out),
+                              _ptr(ws), ws.numel(), _stream(stream)), "gptq_kv8_attention")
+    return out
