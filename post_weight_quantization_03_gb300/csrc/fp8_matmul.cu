@@ -1,12 +1,59 @@
 // The block-scaled e4m3 product
 //   out[m, n] = ra_m rw_n sum_kb 2^(EA[m, kb] - 127) 2^(EW[n / 128, kb] - 127) sum_{k in kb} a w.
+//
+// tcgen05 kind::mxf8f6f4 takes a power-of-two scale byte per row and 32 elements of K, so both
+// block scales are applied inside the tensor core and a tile is one uninterrupted fp32 sum in
+// TMEM; the two row factors multiply it in the epilogue.
+//
+// The weights' 128 rows are the MMA's M and a tile of `tn` tokens is its N (any multiple of 16
+// up to 240: two accumulators of 240 columns and the scales' columns fill the 512 of TMEM).  So
+// a single token costs one 16-column MMA per 128 x 32 weights, which streams W at the memory's
+// rate, and the lanes of an accumulator are consecutive outputs of one token (coalesced stores).
+//
+//   warp 0     : TMA producer (one lane): (W box, A box) of 128 bytes x rows per k-block
+//   warp 1     : TMEM allocator + MMA issuer (one lane): copies the scales of four k-blocks to
+//                TMEM, then four K = 32 MMAs per k-block, the byte chosen by the descriptor
+//   warps 2..5 : epilogue, one weight row per thread
+//   warp 6     : scales: gathers four k-blocks' bytes of each row (one 32-bit word) into the
+//                32 x 16-byte arrangement that the copy to TMEM takes
+//
+// Few tokens leave few tiles; the k-blocks of a tile are then split over a cluster of up to 8
+// CTAs, whose partial sums meet through distributed shared memory in rank order.
+#include <cudaTypedefs.h>
+
 #include <type_traits>
 
 #include "fp8.cuh"
+#include "tc.cuh"
 
 namespace gptq {
 
 namespace {
+
+constexpr int BM = 128;                     // weight rows of a tile
+constexpr int BK = fp8::kBlock;             // 128 codes = 128 bytes = one swizzle row
+constexpr int kMaxTn = 240;
+constexpr int kThreads = 224;
+constexpr int kScaleStages = 4;             // groups of four k-blocks in flight
+constexpr uint32_t kScaleBytes = 3 * 512;   // W, tokens 0..127, tokens 128..239
+constexpr uint32_t kScaleCols = 12;         // TMEM columns of one group
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxStages = 12;
+constexpr uint32_t kRingBytes = 208 * 1024;
+constexpr size_t kSmem = 1024 + kRingBytes + kScaleStages * kScaleBytes + kMaxTn * 4 + 512;
+static_assert(2 * kMaxTn + 2 * kScaleCols <= kTmemCols, "TMEM columns");
+
+struct MmParams {
+  const uint8_t *ae; int64_t ldae;
+  const uint8_t *we; int64_t ldwe;
+  const float *ra, *rw;
+  void *out; int64_t ldo;
+  int64_t M, N;
+  int kb;               // k-blocks
+  int tn, stages;
+  int n_w, n_tiles;     // tiles along the weights; tiles in all
+  int splits;           // CTAs of a cluster that share a tile's k-blocks
+};
 
 template <typename TO>
 __device__ __forceinline__ TO out_f32(float x) {
@@ -14,44 +61,313 @@ __device__ __forceinline__ TO out_f32(float x) {
   else return __float2bfloat16_rn(x);
 }
 
-// CUDA cores: 64 x 64 outputs per CTA, 4 x 4 per thread, 16 elements of K at a time.
+// D[tmem] (+)= (A * 2^sa)(B * 2^sb)^T, one thread; sa, sb: TMEM addresses of the scale columns.
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
+      "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+
+// 512 bytes of shared memory (32 rows of 16 bytes) to 32 lanes x 4 columns, repeated in each of
+// the four lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
+  // no swizzle: 8 rows x 16 bytes contiguous, the next 8 rows 128 bytes on
+  const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)8 << 16) |
+                        ((uint64_t)8 << 32) | ((uint64_t)1 << 46);
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t caddr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(caddr) : "memory");
+  return v;
+}
+
+// k-blocks of this CTA: rank r of the cluster takes an even share.
+__device__ __forceinline__ void k_range(const MmParams &p, int rank, int &k0, int &k1) {
+  k0 = (int)((int64_t)p.kb * rank / p.splits);
+  k1 = (int)((int64_t)p.kb * (rank + 1) / p.splits);
+}
+
 template <typename TO>
-__global__ void __launch_bounds__(256)
-matmul_simt_kernel(const uint8_t *__restrict__ a, int64_t lda, const uint8_t *__restrict__ ae,
-                   int64_t ldae, const float *__restrict__ ra, const uint8_t *__restrict__ w,
-                   int64_t ldw, const uint8_t *__restrict__ we, int64_t ldwe,
-                   const float *__restrict__ rw, int64_t M, int64_t N, int64_t K,
-                   TO *__restrict__ out, int64_t ldo) {
-  __shared__ float As[16][64 + 4], Ws[16][64 + 4];
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int64_t m0 = (int64_t)blockIdx.y * 64, n0 = (int64_t)blockIdx.x * 64;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < K; k0 += 16) {
-    const int64_t kb = k0 / fp8::kBlock;
-    for (int e = threadIdx.x; e < 16 * 64; e += 256) {
-      const int kk = e % 16, rr = e / 16;
-      const int64_t m = m0 + rr, n = n0 + rr, k = k0 + kk;
-      As[kk][rr] = (m < M && k < K)
-                       ? fp8::unpack1(a[m * lda + k]) * fp8::exp_value(ae[m * ldae + kb]) : 0.f;
-      Ws[kk][rr] = (n < N && k < K) ? fp8::unpack1(w[n * ldw + k]) *
-                                          fp8::exp_value(we[n / fp8::kBlock * ldwe + kb]) : 0.f;
+__global__ void __launch_bounds__(kThreads, 1)
+matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap ma,
+              MmParams p, DevStatus *st) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *sscale = ring + kRingBytes;
+  float *sra = (float *)(sscale + kScaleStages * kScaleBytes);
+  uint64_t *full = (uint64_t *)(sra + kMaxTn);
+  uint64_t *empty = full + kMaxStages;
+  uint64_t *sfull = empty + kMaxStages;
+  uint64_t *sempty = sfull + kScaleStages;
+  uint64_t *tfull = sempty + kScaleStages;
+  uint64_t *tempty = tfull + 2;
+  uint32_t *tmem_slot = (uint32_t *)(tempty + 2);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t stage_bytes = (uint32_t)(BM + p.tn) * BK;
+  const int rank = p.splits > 1 ? (int)tc::cluster_ctarank() : 0;
+  const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
+  int k0, k1;
+  k_range(p, rank, k0, k1);
+
+  if (threadIdx.x == 0) {
+    // The status of the call.  A wait that gives up writes it two seconds or more after its own
+    // CTA started, so this store, by the first CTA to start, comes first.
+    if (blockIdx.x == 0) st->status = 0;
+    for (int s = 0; s < p.stages; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
     }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = fmaf(As[kk][4 * ty + i], Ws[kk][4 * tx + j], acc[i][j]);
-    __syncthreads();
+    for (int s = 0; s < kScaleStages; ++s) {
+      tc::mbar_init(&sfull[s], 32);
+      tc::mbar_init(&sempty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&tfull[b], 1);
+      tc::mbar_init(&tempty[b], 4);
+    }
+    tc::mbar_fence_init();
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + 4 * ty + i, n = n0 + 4 * tx + j;
-      if (m < M && n < N)
-        out[m * ldo + n] = out_f32<TO>(acc[i][j] * (ra ? ra[m] : 1.f) * (rw ? rw[n] : 1.f));
+  if (warp == 1) tc::tmem_alloc(tmem_slot, kTmemCols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0 && lane == 0) {
+    // ---------------- producer ----------------
+    tc::tma_prefetch_desc(&mw);
+    tc::tma_prefetch_desc(&ma);
+    int s = 0;
+    uint32_t ph = 1;
+    for (int t = first; t < p.n_tiles; t += step) {
+      const int32_t n0 = (t % p.n_w) * BM, m0 = (t / p.n_w) * p.tn;
+      bool ok = true;
+      for (int kb = k0; kb < k1; ++kb) {
+        ok = tc::mbar_wait(&empty[s], ph, st);
+        if (!ok) break;
+        uint8_t *base = ring + s * stage_bytes;
+        tc::mbar_arrive_expect_tx(&full[s], stage_bytes);
+        tc::tma_load_2d(base, &mw, kb * BK, n0, &full[s]);
+        tc::tma_load_2d(base + BM * BK, &ma, kb * BK, m0, &full[s]);
+        if (++s == p.stages) s = 0, ph ^= 1;
+      }
+      if (!ok) break;
     }
+  } else if (warp == 1 && lane == 0) {
+    // ---------------- MMA issuer ----------------
+    // kind::mxf8f6f4 instruction descriptor: e4m3 operands, K-major, power-of-two scale bytes
+    const uint32_t idesc = (1u << 23) | ((uint32_t)(p.tn >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+    int s = 0, g = 0, it = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int t = first; t < p.n_tiles && ok; t += step, ++it) {
+      const int b = it & 1;
+      ok = tc::mbar_wait(&tempty[b], ((it >> 1) & 1) ^ 1, st);
+      if (!ok) break;
+      tc::tc_fence_after();
+      const uint32_t acc = tmem + (uint32_t)(b * kMaxTn);
+      uint32_t sc = 0;
+      for (int kb = k0; kb < k1; ++kb) {
+        if (kb == k0 || (kb & 3) == 0) {
+          const int q = g % kScaleStages;
+          ok = tc::mbar_wait(&sfull[q], (g / kScaleStages) & 1, st);
+          if (!ok) break;
+          tc::tc_fence_after();
+          // two groups of columns in turn: the scale warp's ring keeps a third group's copy
+          // from starting before the first group's MMAs have completed
+          sc = tmem + 2 * kMaxTn + (uint32_t)(g & 1) * kScaleCols;
+          const uint32_t sm = tc::smem_u32(sscale + q * kScaleBytes);
+          copy_scales(sc, sm);
+          copy_scales(sc + 4, sm + 512);
+          if (p.tn > 128) copy_scales(sc + 8, sm + 1024);
+        }
+        ok = tc::mbar_wait(&full[s], ph, st);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint32_t wa = tc::smem_u32(ring + s * stage_bytes), aa = wa + BM * BK;
+        const uint32_t id = idesc | ((uint32_t)(kb & 3) << 29) | ((uint32_t)(kb & 3) << 4);
+#pragma unroll
+        for (int kk = 0; kk < BK / 32; ++kk)
+          mma_mx(acc, tc::smem_desc_sw128(wa + kk * 32, 16, 1024),
+                 tc::smem_desc_sw128(aa + kk * 32, 16, 1024), id, sc, sc + 4,
+                 (kb > k0 || kk > 0) ? 1u : 0u);
+        tc::mma_commit(&empty[s]);
+        if (++s == p.stages) s = 0, ph ^= 1;
+        if ((kb & 3) == 3 || kb + 1 == k1) {
+          tc::mma_commit(&sempty[g % kScaleStages]);
+          ++g;
+        }
+      }
+      if (ok) tc::mma_commit(&tfull[b]);
+    }
+  } else if (warp == 6) {
+    // ---------------- scales ----------------
+    int g = 0;
+    bool ok = true;
+    for (int t = first; t < p.n_tiles && ok; t += step) {
+      const int64_t m0 = (int64_t)(t / p.n_w) * p.tn;
+      const uint8_t *we = p.we + (int64_t)(t % p.n_w) * p.ldwe;
+      for (int sb = k0 / 4; sb <= (k1 - 1) / 4 && k1 > k0; ++sb, ++g) {
+        uint32_t word[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t row = m0 + lane + 32 * i;
+          word[i] = (lane + 32 * i < p.tn && row < p.M)
+                        ? *reinterpret_cast<const uint32_t *>(p.ae + row * p.ldae + 4 * sb)
+                        : 0x7F7F7F7Fu;
+        }
+        const uint32_t ww = *reinterpret_cast<const uint32_t *>(we + 4 * sb);
+        const int q = g % kScaleStages;
+        // two TMEM groups: wait for the MMAs of two groups back, not only for this slot's
+        if (g >= 2) ok = tc::mbar_wait(&sempty[(g - 2) % kScaleStages], ((g - 2) / kScaleStages) & 1, st);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        uint4 *dst = reinterpret_cast<uint4 *>(sscale + q * kScaleBytes) + lane;
+        dst[0] = make_uint4(ww, ww, ww, ww);
+        dst[32] = make_uint4(word[0], word[1], word[2], word[3]);
+        dst[64] = make_uint4(word[4], word[5], word[6], word[7]);
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(&sfull[q]);
+      }
+    }
+  } else if (warp >= 2 && warp < 6) {
+    // ---------------- epilogue ----------------
+    const int q = warp & 3, row = q * 32 + lane, et = threadIdx.x - 64;
+    int it = 0;
+    for (int t = first; t < p.n_tiles; t += step, ++it) {
+      const int b = it & 1;
+      const int64_t n = (int64_t)(t % p.n_w) * BM + row, m0 = (int64_t)(t / p.n_w) * p.tn;
+      const int cols = (int)(p.M - m0 < p.tn ? p.M - m0 : p.tn);
+      if (p.splits == 1) {
+        tc::named_barrier(2, 128);  // the previous tile's factors have been read
+        for (int j = et; j < cols; j += 128) sra[j] = p.ra ? p.ra[m0 + j] : 1.0f;
+      }
+      const float rw = (p.rw && n < p.N) ? p.rw[n] : 1.0f;
+      const bool ok = tc::mbar_wait(&tfull[b], (it >> 1) & 1, st);
+      if (!tc::named_barrier_and(1, 128, ok)) break;
+      tc::tc_fence_after();
+      TO *o = (TO *)p.out + m0 * p.ldo + n;
+      float *part = (float *)ring + row;
+#pragma unroll 1
+      for (int c = 0; c < p.tn; c += 32) {
+        uint32_t r[32];
+        tc::tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kMaxTn + c), r);
+        tc::tmem_ld_wait();
+        if (p.splits > 1) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < p.tn) part[(c + i) * BM] = __uint_as_float(r[i]);
+        } else if (n < p.N) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < cols) o[(int64_t)(c + i) * p.ldo] = out_f32<TO>(__uint_as_float(r[i]) * rw * sra[c + i]);
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&tempty[b]);
+    }
+  }
+  __syncwarp();
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tc::tmem_dealloc(tmem, kTmemCols);
+  if (p.splits > 1) {
+    // one tile per cluster: the ring holds this CTA's partial sums [tn][128]
+    tc::cluster_sync();
+    const int64_t n0 = (int64_t)(first % p.n_w) * BM, m0 = (int64_t)(first / p.n_w) * p.tn;
+    const int cols = (int)(p.M - m0 < p.tn ? p.M - m0 : p.tn);
+    const uint32_t base = tc::smem_u32(ring);
+    for (int e = threadIdx.x; e < BM * ((cols + p.splits - 1) / p.splits); e += kThreads) {
+      const int col = e / BM * p.splits + rank;
+      const int64_t n = n0 + e % BM;
+      if (col >= cols || n >= p.N) continue;
+      const uint32_t off = base + (uint32_t)(col * BM + e % BM) * 4;
+      float s = 0.0f;
+      for (int r = 0; r < p.splits; ++r) s += ld_cluster_f32(tc::mapa_shared(off, (uint32_t)r));
+      ((TO *)p.out)[(m0 + col) * p.ldo + n] = out_f32<TO>(
+          s * (p.rw ? p.rw[n] : 1.0f) * (p.ra ? p.ra[m0 + col] : 1.0f));
+    }
+    tc::cluster_sync();  // the others have read this CTA's sums
+  }
+}
+
+// Tile of tokens and splits of K.  A CTA's time is about
+//   k-blocks x max(MMA cycles, bytes / its share of the memory) + a constant,
+// and a launch takes as many rounds as its CTAs need on the SMs.
+struct Shape { int tn, splits; };
+
+Shape choose(int64_t M, int64_t N, int kb, int sms) {
+  const int64_t n_w = ceil_div(N, BM);
+  Shape best{16, 1};
+  double best_t = 1e30;
+  for (int64_t mt = ceil_div(M, kMaxTn);; ++mt) {
+    const int tn = (int)(ceil_div(ceil_div(M, mt), 16) * 16);
+    const int64_t tiles = n_w * ceil_div(M, tn);
+    for (int s = 1; s <= 8 && s <= kb; s *= 2) {
+      // a cycle per 28 codes of W streamed from memory; 2.3 MMA cycles per token column
+      const double per_kb = tn * 2.3 > 300.0 ? tn * 2.3 : 300.0;
+      const double round_t = (double)ceil_div(kb, s) * per_kb + 2500.0 + (s > 1 ? 1500.0 + 8.0 * tn : 0.0);
+      const int64_t rounds = ceil_div(tiles * s, s > 1 ? sms / s * s : sms);
+      const double t = (double)rounds * round_t;
+      if (t < best_t) best_t = t, best = Shape{tn, s};
+    }
+    if (tn <= 64 || mt > ceil_div(M, kMaxTn) + 4) break;
+  }
+  return best;
+}
+
+template <typename TO>
+gptq_status run(const Fp8MatmulArgs &g, DevStatus *st, cudaStream_t s) {
+  GPTQ_TRY(ensure_smem_attr((const void *)matmul_kernel<TO>, (int)kSmem));
+  int sms = 0;
+  GPTQ_TRY(device_sm_count(&sms));
+  const int kb = (int)ceil_div(g.K, BK);
+  const Shape sh = choose(g.M, g.N, kb, sms);
+  MmParams p{};
+  p.ae = g.ae; p.ldae = g.ldae;
+  p.we = g.we; p.ldwe = g.ldwe;
+  p.ra = g.ra; p.rw = g.rw;
+  p.out = g.out; p.ldo = g.ldo;
+  p.M = g.M; p.N = g.N;
+  p.kb = kb;
+  p.tn = sh.tn;
+  const int fit = (int)(kRingBytes / (uint32_t)((BM + sh.tn) * BK));
+  p.stages = fit < kMaxStages ? fit : kMaxStages;
+  p.n_w = (int)ceil_div(g.N, BM);
+  const int64_t tiles = p.n_w * ceil_div(g.M, sh.tn);
+  if (tiles * 8 > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  p.n_tiles = (int)tiles;
+  p.splits = sh.splits;
+  CUtensorMap mw, ma;
+  if (!tc::make_tmap_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w, g.N, g.K, g.ldw, BK, BM) ||
+      !tc::make_tmap_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, g.M, g.K, g.lda, BK, sh.tn))
+    return GPTQ_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sh.splits > 1 ? tiles * sh.splits : (tiles < sms ? tiles : sms)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)sh.splits;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  GPTQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, matmul_kernel<TO>, mw, ma, p, st));
+  return GPTQ_OK;
 }
 
 }  // namespace
@@ -59,16 +375,12 @@ matmul_simt_kernel(const uint8_t *__restrict__ a, int64_t lda, const uint8_t *__
 size_t fp8_matmul_ws_bytes(int64_t, int64_t, int64_t) { return 256; }
 
 gptq_status launch_fp8_matmul(const Fp8MatmulArgs &g, void *ws, cudaStream_t s) {
-  GPTQ_CUDA_CHECK(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s));
-  if (g.M == 0) return GPTQ_OK;
-  const dim3 grid((unsigned)ceil_div(g.N, 64), (unsigned)ceil_div(g.M, 64));
-  if (g.odtype == GPTQ_F16)
-    return launch_kernel(matmul_simt_kernel<__half>, grid, dim3(256), 0, s, g.a, g.lda, g.ae,
-                         g.ldae, g.ra, g.w, g.ldw, g.we, g.ldwe, g.rw, g.M, g.N, g.K,
-                         (__half *)g.out, g.ldo);
-  return launch_kernel(matmul_simt_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, g.a, g.lda, g.ae,
-                       g.ldae, g.ra, g.w, g.ldw, g.we, g.ldwe, g.rw, g.M, g.N, g.K,
-                       (__nv_bfloat16 *)g.out, g.ldo);
+  if (g.M == 0) {
+    GPTQ_CUDA_CHECK(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s));
+    return GPTQ_OK;
+  }
+  return g.odtype == GPTQ_F16 ? run<__half>(g, (DevStatus *)ws, s)
+                              : run<__nv_bfloat16>(g, (DevStatus *)ws, s);
 }
 
 }  // namespace gptq
