@@ -1,18 +1,600 @@
-// Attention over the 8-bit cache.
-#include <type_traits>
-
-#include "fp8.cuh"
+// Attention over the 8-bit cache, few queries (a decoding step).
+//
+// Per (sequence, cache head) the queries of the group's heads and of the new tokens are the
+// rows, at most 16, of one or two MMA tiles; the keys and values stream past once.  HBM-bound:
+// 2 D bytes a token and head, against 4 D operations a row.
+//
+//   products  e4m3 MMAs (m16n8k32, fp32 sums) straight on the cached codes.  The other operand
+//             is a sum of e4m3 terms: with 4 bits of significand each, two terms hold a bf16
+//             number exactly and three an fp16 one (down to 2^-17 of the row's maximum, to which
+//             a row of queries is first scaled by a power of two).  An MMA has 16 rows: eight
+//             rows' first terms and, below them, their second terms, so a thread finds both
+//             halves of a score in its own accumulator.  Against fp16 MMAs on converted codes:
+//             no conversions (512 a block and warp) and half the MMAs;
+//   softmax   a block's key exponent is a factor of its scores, its value exponent lv is folded
+//             into the exponential: with y = f s + lv and the running maximum m of y,
+//               p = 2^(y - m),  acc += p vc,  l += p 2^-lv   (out = acc / l),
+//             so the block scales cost one addition per block; m, l, acc are fp32, and 2^8 p is
+//             split into as many terms as the queries (9 or 12 bits; less below 2^-14);
+//   layout    tokens are dealt to the score tiles' columns so that the 16 scores a thread owns
+//             are 16 consecutive tokens: they are, unmoved, its operand of the second MMA, whose
+//             other operand is 16 consecutive bytes of a V row (V is stored channel-major).
+//
+// Each CTA takes a contiguous share of all (sequence, head, block) units.  One warp looks the
+// blocks up, 32 at a time and two batches ahead, and keeps the copies of K's and V's 64 x D bytes
+// (contiguous) running; eight warps in groups of one warp per eight rows take the units in turn,
+// each group through a ring of its own in shared memory, and meet at the end of an item.  An
+// item that lies in one share is written there; pieces of others meet in a second small kernel,
+// in order (repeatable), which also writes the rows that see nothing.
+#include "kv8.cuh"
 
 namespace gptq {
 
 namespace {
 
-constexpr int kTok = GPTQ_KV8_BLOCK;
+using namespace kv8;
 
+constexpr int kRows = 32;                 // most rows of an item
+constexpr int kMaxCtas = 160;
+constexpr int kWarps = 8;                 // that compute
+// Registers go by groups of four warps: two that compute, one with the look-up warp.  At launch
+// 384 threads have 168 each (64,512); the split below is that many: 256 x 232 + 128 x 40.
+constexpr int kThreads = 32 * (kWarps + 4);
+constexpr int kList = 128;                // units that have been looked up
+static_assert(kRows == 8 * 4, "row tiles: 1, 2 or 4");
+
+template <int D>
+struct Decode {
+  static constexpr uint32_t kHalf = kTok * D;                 // bytes of K (or V) of a block
+  static constexpr int kSlots = D == 128 ? 3 : 6;             // halves in flight per warp
+  static constexpr uint32_t kRing = kWarps * kSlots * kHalf;  // 192 KB
+  static constexpr int kWarpPart = 8 * D + 16;                // floats: acc, m, l of eight rows
+  static constexpr size_t kSmem =
+      128 + kRing + kWarps * kWarpPart * 4 + kList * 8 + 2 * kWarps * kSlots * 8;
+  static constexpr int kPart = kRows * D + 2 * kRows;         // floats of a piece of an item
+};
+
+// Blocks of a sequence that some query row sees.
+__device__ __forceinline__ int seq_blocks(const Kv8AttentionArgs &g, int seq) {
+  return (seq_length(g, seq) + kTok - 1) / kTok;
+}
+
+// Whole warp: units of the sequences [0, n), a unit being one block of one head.
+__device__ __forceinline__ int64_t units_before(const Kv8AttentionArgs &g, int n) {
+  int64_t s = 0;
+  for (int i = threadIdx.x % 32; i < n; i += 32) s += seq_blocks(g, i);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s * g.n_kv;
+}
+
+// The CTAs that share `total` units taken `turn` at a time, and the first unit of share w.
+__device__ __forceinline__ int64_t shares(int64_t total, int turn, int64_t ctas) {
+  const int64_t n = (total + turn - 1) / turn;
+  return n < ctas ? n : ctas;
+}
+__device__ __forceinline__ int64_t share_start(int64_t total, int64_t n, int64_t w) {
+  return total * w / n;
+}
+__device__ __forceinline__ int64_t share_of(int64_t total, int64_t n, int64_t u) {
+  int64_t w = u * n / total;
+  while (w + 1 < n && share_start(total, n, w + 1) <= u) ++w;
+  while (share_start(total, n, w) > u) --w;
+  return w;
+}
+
+// Position in the unit space.
+struct Cursor {
+  int seq, head, blk, nblk;
+  __device__ __forceinline__ void next_item(const Kv8AttentionArgs &g) {
+    blk = 0;
+    if (++head < g.n_kv) return;
+    head = 0;
+    do ++seq; while (seq < g.n_seq && (nblk = seq_blocks(g, seq)) == 0);
+  }
+  __device__ __forceinline__ void advance(const Kv8AttentionArgs &g, int by) {
+    while (blk + by >= nblk && seq < g.n_seq) {
+      by -= nblk - blk;
+      next_item(g);
+    }
+    blk += by;
+  }
+};
+
+// Whole warp: the cursor of unit u (0 <= u < total).
+__device__ __forceinline__ Cursor cursor_at(const Kv8AttentionArgs &g, int64_t u) {
+  const int lane = threadIdx.x % 32;
+  for (int s0 = 0;; s0 += 32) {
+    const int nb = s0 + lane < g.n_seq ? seq_blocks(g, s0 + lane) : 0;
+    int64_t incl = (int64_t)nb * g.n_kv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, incl > u);
+    if (past == 0) {
+      u -= __shfl_sync(0xffffffffu, incl, 31);
+      continue;
+    }
+    const int src = __ffs(past) - 1;
+    const int n = __shfl_sync(0xffffffffu, nb, src);
+    const int64_t at = u - (__shfl_sync(0xffffffffu, incl, src) - (int64_t)n * g.n_kv);
+    return Cursor{s0 + src, (int)(at / n), (int)(at % n), n};
+  }
+}
+
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Terms of a sum of e4m3 numbers for operands of type T.
 template <typename T>
-__device__ __forceinline__ T from_f32(float x) {
-  if constexpr (std::is_same<T, __half>::value) return __float2half_rn(x);
-  else return __float2bfloat16_rn(x);
+constexpr int kTerms = std::is_same<T, __half>::value ? 3 : 2;
+
+// x (two fp16 numbers, |x| <= 448) = term[0] + term[1] (+ term[2]), two codes each.
+template <int NT>
+__device__ __forceinline__ void split(__half2 x, uint32_t (&term)[NT]) {
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const __nv_fp8x2_storage_t c =
+        __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+    term[i] = c;
+    if (i + 1 < NT) x = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+  }
+}
+
+// Four numbers' terms, a word of codes each.
+template <int NT>
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t (&word)[NT]) {
+  uint32_t lo[NT], hi[NT];
+  split<NT>(__floats2half2_rn(a, b), lo);
+  split<NT>(__floats2half2_rn(c, d), hi);
+#pragma unroll
+  for (int i = 0; i < NT; ++i) word[i] = lo[i] | (hi[i] << 16);
+}
+
+// c[i] += (sum of the terms) b[i] for N accumulators, the MMAs on one of them kept apart: the
+// first two terms as the tile's two halves, a third one alone.  x, y: the words of the first
+// and second 16 elements of K.
+template <int NT, int N>
+__device__ __forceinline__ void mma_terms(float (&c)[N][4], const uint32_t (&x)[NT],
+                                          const uint32_t (&y)[NT], const uint32_t (&b0)[N],
+                                          const uint32_t (&b1)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) mma_e4m3(c[i], x[0], x[1], y[0], y[1], b0[i], b1[i]);
+  if constexpr (NT == 3) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) mma_e4m3(c[i], x[2], 0u, y[2], 0u, b0[i], b1[i]);
+  }
+}
+
+// Queries of eight rows as MMA operands: thread (row = lane / 4, t = lane % 4) holds elements
+// [t D/4, (t + 1) D/4), eight per K step.  f: factor that undoes the row's scaling, times the
+// softmax scale in base 2.
+template <typename T, int D>
+__device__ __forceinline__ void load_queries(const Kv8AttentionArgs &g, int seq, int head, int r,
+                                             int rows, int group,
+                                             uint32_t (&qa)[D / 16][kTerms<T>], float &f) {
+  const int t = threadIdx.x % 4;
+  float v[D / 4];
+  if (r < rows) {
+    const T *q = (const T *)g.q + seq * g.q_stride[0] + (r / group) * g.q_stride[1] +
+                 (int64_t)(head * group + r % group) * g.q_stride[2] + t * (D / 4);
+    if (((uintptr_t)q & 15) == 0) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 w = reinterpret_cast<const uint4 *>(q)[i];
+        const T *e = reinterpret_cast<const T *>(&w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * i + j] = to_f32(e[j]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) v[i] = to_f32(q[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) v[i] = 0.0f;
+  }
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fp8::finite_abs(v[i]));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const int e = row_exponent(amax) - 7;  // the row's maximum in [128, 256)
+  const float inv = fp8::pow2(-e);
+  f = fp8::pow2(e) * g.scale * kLog2e;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+    split4<kTerms<T>>(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv,
+                      qa[i]);
+}
+
+// RT: row tiles, and warps of a group (1, 2 or 4).
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(kThreads, 1)
+decode_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
+  using C = Decode<D>;
+  constexpr int NT = kTerms<T>;
+  constexpr int G = kWarps / RT;             // groups
+  constexpr int H = C::kSlots * RT;          // ring slots (halves of blocks) of a group
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 127) & ~(uintptr_t)127);
+  float *spart = (float *)(smem + C::kRing);
+  int2 *list = (int2 *)(spart + kWarps * C::kWarpPart);  // block and head (-1: none); exponents
+  uint64_t *full = (uint64_t *)(list + kList), *empty = full + kWarps * C::kSlots;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < G * H; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], RT);
+    }
+    tc::mbar_fence_init();
+  }
+  __syncthreads();
+  wait_for_grids();
+  launch_dependents();
+  // the call's status; a wait that gives up writes it, two seconds from here or later
+  if (blockIdx.x == 0 && threadIdx.x == 0) st->status = 0;
+
+  const int64_t total = units_before(g, g.n_seq);
+  const int64_t n = shares(total, G, gridDim.x);
+  if (blockIdx.x >= n) return;
+  const int64_t u0 = share_start(total, n, blockIdx.x);
+  const int count = (int)(share_start(total, n, blockIdx.x + 1) - u0);
+  Cursor at = cursor_at(g, u0);
+
+  if (warp >= kWarps) {
+    // ---------------- look-up and copies ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp > kWarps) return;
+    // Lane l looks up unit i0 + l of each batch of 32: table entries of the batch after the next
+    // and exponents of the next are on their way while a batch is written to the list.
+    Cursor c = at;
+    c.advance(g, lane);
+    int page = -1, place = -1, exps = 0, head = 0;  // of the batches after and next
+    auto load_page = [&](int i) {
+      page = -1;
+      if (i < count) {
+        page = g.table[c.seq * g.ld_table + c.blk];
+        head = c.head;
+        if (i + 32 < count) c.advance(g, 32);
+      }
+    };
+    auto load_exps = [&]() {
+      place = page < 0 || page >= g.n_blocks ? -1 : page * g.n_kv + head;
+      exps = 0;
+      if (place >= 0) exps = (int)g.k_exps[place] | ((int)g.v_exps[place] << 8);
+    };
+    int filled = 0, soon = lane;
+    load_page(soon);
+    load_exps();
+    load_page(soon += 32);
+    // Lane q keeps group q's ring full: half hn of its blocks goes to slot hn % H.
+    int i = lane, hn = 0;
+    const int last = lane < G ? count : 0;
+    uint64_t t0 = tc::global_ns();
+    while (__any_sync(0xffffffffu, i < last)) {
+      const int behind = __reduce_min_sync(0xffffffffu, i < last ? i : 0x7fffffff);
+      while (filled < count && behind >= filled - 32) {
+        list[(filled + lane) % kList] = make_int2(place, exps);
+        load_exps();
+        load_page(soon += 32);
+        filled += 32;
+        __syncwarp();
+      }
+      bool moved = false;
+      if (i < last && i < filled) {
+        const int slot = lane * H + hn % H;
+        if (hn < H || tc::mbar_try_wait(&empty[slot], (hn / H - 1) & 1)) {
+          const int ph = list[i % kList].x;
+          if (ph >= 0) {
+            tc::mbar_arrive_expect_tx(&full[slot], C::kHalf);
+            tc::bulk_load(smem + (size_t)slot * C::kHalf,
+                          ((hn & 1) ? g.v : g.k) + (int64_t)ph * C::kHalf, C::kHalf, &full[slot]);
+          } else {
+            tc::mbar_arrive(&full[slot]);
+          }
+          if (hn & 1) i += G;
+          ++hn;
+          moved = true;
+        }
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+        t0 = tc::global_ns();
+      } else if (tc::global_ns() - t0 > tc::kWaitNs) {
+        set_status(st, GPTQ_ERR_TIMEOUT);
+        break;
+      }
+    }
+    return;
+  }
+
+  // ---------------- products ----------------
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+  const int t = lane % 4, grp = warp / RT, r = (warp % RT) * 8 + lane / 4;  // this thread's row
+  const int group = g.n_heads / g.n_kv, rows = (int)g.n_new * group;
+  uint8_t *ring = smem + (size_t)grp * H * C::kHalf;
+  float *mine = spart + warp * C::kWarpPart;
+  full += grp * H;
+  empty += grp * H;
+  int hn = 0;        // halves used
+  bool ok = true;    // false once a wait has given up: the rest is skipped
+  auto arrived = [&]() {
+    if (ok) ok = tc::mbar_wait(&full[hn % H], (hn / H) & 1, st);
+    ok = __all_sync(0xffffffffu, ok);
+  };
+  auto release = [&]() {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&empty[hn % H]);
+    ++hn;
+  };
+  for (int i = grp, i0 = 0; i0 < count;) {
+    const int i1 = i0 + at.nblk - at.blk < count ? i0 + at.nblk - at.blk : count;  // item's units
+    const int length = seq_length(g, at.seq);
+    const int limit = r >= rows ? 0 : (g.causal ? length - (int)g.n_new + r / group + 1 : length);
+    uint32_t qa[D / 16][NT];
+    float f, m = -INFINITY, l = 0.0f, acc[D / 8][4];
+    load_queries<T, D>(g, at.seq, at.head, r, rows, group, qa, f);
+#pragma unroll
+    for (int q = 0; q < D / 8; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[q][j] = 0.0f;
+
+#pragma unroll 1
+    for (; i < i1; i += G) {
+      arrived();
+      const int2 what = list[i % kList];
+      if (!ok || what.x < 0) {
+        release();
+        arrived();
+        release();
+        continue;
+      }
+      const float fk = f * fp8::exp_value((uint8_t)what.y);
+      const int lv = (what.y >> 8) - fp8::kBias;
+      // column n of score tile j is token 16 (n / 2) + 2 j + n % 2 of the block
+      const uint8_t *krow = ring + (size_t)(hn % H) * C::kHalf +
+                            (16 * (lane / 8) + (lane / 4) % 2) * D + t * (D / 4);
+      float s[8][4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s[j][q] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t x[4][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 w4 = *reinterpret_cast<const uint4 *>(krow + 2 * j * D + 16 * c);
+          x[0][j] = w4.x; x[1][j] = w4.y; x[2][j] = w4.z; x[3][j] = w4.w;
+        }
+        mma_terms<NT, 8>(s, qa[4 * c], qa[4 * c + 1], x[0], x[1]);
+        mma_terms<NT, 8>(s, qa[4 * c + 2], qa[4 * c + 3], x[2], x[3]);
+      }
+      release();
+      // this thread's tokens of the block: 16 t + 2 j + {0, 1}
+      const int first = (at.blk + i - i0) * kTok, tok = first + 16 * t;
+      const bool cut = first + kTok > length - (g.causal ? (int)g.n_new - 1 : 0);
+      uint32_t pa[4][NT];
+      {
+        float y[16], mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          y[j] = fmaf(s[j / 2][j % 2] + s[j / 2][j % 2 + 2], fk, (float)lv);
+          if (cut && tok + j >= limit) y[j] = -INFINITY;
+          mx = fmaxf(mx, y[j]);
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (__any_sync(0xffffffffu, mx > m)) {
+          const float mn = fmaxf(m, mx);
+          const float shrink = ex2(m - (mn == -INFINITY ? 0.0f : mn));  // 0 for the first block
+          m = mn;
+          l *= shrink;
+#pragma unroll
+          for (int q = 0; q < D / 8; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[q][j] *= shrink;
+        }
+        const float base = (m == -INFINITY ? 0.0f : m) - 8.0f;
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          y[j] = ex2(y[j] - base);
+          sum += y[j];
+        }
+        l = fmaf(sum, 0x1p-8f * fp8::pow2(-lv), l);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          split4<NT>(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3], pa[q]);
+      }
+      arrived();
+      const uint8_t *vrow = ring + (size_t)(hn % H) * C::kHalf + (lane / 4) * kTok + 16 * t;
+      const int live = length - tok;  // of this thread's 16 tokens
+#pragma unroll
+      for (int q0 = 0; q0 < D / 8; q0 += 4) {
+        uint32_t x[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 w4 = *reinterpret_cast<const uint4 *>(vrow + 8 * (q0 + q) * kTok);
+          x[0][q] = w4.x; x[1][q] = w4.y; x[2][q] = w4.z; x[3][q] = w4.w;
+        }
+        if (cut && live < 16) {
+          // bytes past the sequence may be NaN codes, and 0 x NaN is NaN
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int keep = live - 4 * j;
+            const uint32_t mask = keep <= 0 ? 0u : (keep >= 4 ? ~0u : (1u << (8 * keep)) - 1u);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[j][q] &= mask;
+          }
+        }
+        float(&c)[4][4] = *reinterpret_cast<float(*)[4][4]>(&acc[q0]);
+        mma_terms<NT, 4>(c, pa[0], pa[1], x[0], x[1]);
+        mma_terms<NT, 4>(c, pa[2], pa[3], x[2], x[3]);
+      }
+      release();
+    }
+
+    // the item's end, here or in the next share: join the groups
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+#pragma unroll
+    for (int q = 0; q < D / 8; ++q)
+      *reinterpret_cast<float2 *>(mine + (lane / 4) * D + 8 * q + 2 * t) =
+          make_float2((acc[q][0] + acc[q][2]) * 0x1p-8f, (acc[q][1] + acc[q][3]) * 0x1p-8f);
+    if (t == 0) {
+      mine[8 * D + lane / 4] = m;
+      mine[8 * D + 8 + lane / 4] = l;
+    }
+    tc::named_barrier(1, 32 * kWarps);
+    const bool whole = at.blk == 0 && i1 - i0 == at.nblk;
+    float *piece = part + (2 * (int64_t)blockIdx.x + (i0 > 0 ? 1 : 0)) * C::kPart;
+    for (int e = threadIdx.x; e < rows * (D / 4); e += 32 * kWarps) {
+      const int row = e / (D / 4), d = e % (D / 4) * 4;
+      const float *p = spart + (row / 8) * C::kWarpPart;
+      float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+      for (int q = 0; q < G; ++q) mm = fmaxf(mm, p[q * RT * C::kWarpPart + 8 * D + row % 8]);
+      const float base = mm == -INFINITY ? 0.0f : mm;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < G; ++q, p += RT * C::kWarpPart) {
+        const float sc = ex2(p[8 * D + row % 8] - base);
+        const float4 v = *reinterpret_cast<const float4 *>(p + (row % 8) * D + d);
+        ll = fmaf(p[8 * D + 8 + row % 8], sc, ll);
+        a.x = fmaf(v.x, sc, a.x);
+        a.y = fmaf(v.y, sc, a.y);
+        a.z = fmaf(v.z, sc, a.z);
+        a.w = fmaf(v.w, sc, a.w);
+      }
+      if (whole) {
+        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+        T *o = (T *)g.out + at.seq * g.o_stride[0] + (row / group) * g.o_stride[1] +
+               (int64_t)(at.head * group + row % group) * g.o_stride[2] + d;
+        o[0] = from_f32<T>(a.x * inv);
+        o[1] = from_f32<T>(a.y * inv);
+        o[2] = from_f32<T>(a.z * inv);
+        o[3] = from_f32<T>(a.w * inv);
+      } else {
+        // the share's first item, or (an item begun inside it) its last
+        *reinterpret_cast<float4 *>(piece + row * D + d) = a;
+        if (d == 0) {
+          piece[kRows * D + row] = mm;
+          piece[kRows * D + kRows + row] = ll;
+        }
+      }
+    }
+    tc::named_barrier(1, 32 * kWarps);  // the parts have been read
+    i0 = i1;
+    if (i0 < count) at.next_item(g);
+  }
+}
+
+// Joins the pieces of one item (sequence, head): out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i.
+// It starts while the kernel above runs (which has waited for all before it, so the lengths are
+// there) and waits for it where it reads the pieces.
+template <typename T, int D>
+__global__ void __launch_bounds__(128)
+join_kernel(Kv8AttentionArgs g, const float *part, int turn, int64_t ctas) {
+  constexpr int kPart = Decode<D>::kPart;
+  constexpr int kCols = D / 4, kAt = 128 / kCols;  // threads along a row; pieces at a time
+  __shared__ float4 sa[128];
+  __shared__ float sl[128];
+  const int group = g.n_heads / g.n_kv, rows = (int)g.n_new * group;
+  const int row = blockIdx.x % rows, item = blockIdx.x / rows;
+  const int seq = item / g.n_kv, head = item % g.n_kv;
+  const int64_t nblk = seq_blocks(g, seq);
+  int64_t w0 = 0, w1 = -1;
+  bool late = false;  // the first piece is the second of its CTA
+  if (nblk > 0) {
+    const int64_t total = units_before(g, g.n_seq), n = shares(total, turn, ctas);
+    const int64_t first = units_before(g, seq) + head * nblk;
+    w0 = share_of(total, n, first);
+    w1 = share_of(total, n, first + nblk - 1);
+    late = share_start(total, n, w0) < first;
+  }
+  // also where there is nothing to do: this kernel's end has to mean that the other's came
+  wait_for_grids();
+  if (nblk > 0 && w0 == w1) return;  // one CTA had it all
+  const int c = threadIdx.x % kCols;
+  auto piece = [&](int64_t w) { return part + (2 * w + (w == w0 && late ? 1 : 0)) * kPart; };
+  float m = -INFINITY, l = 0.0f;
+  for (int64_t w = w0 + threadIdx.x % 32; w <= w1; w += 32)
+    m = fmaxf(m, piece(w)[kRows * D + row]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (m == -INFINITY) m = 0.0f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int64_t w = w0 + threadIdx.x / kCols; w <= w1; w += kAt) {
+    const float *p = piece(w);
+    const float s = ex2(p[kRows * D + row] - m);
+    const float4 v = *reinterpret_cast<const float4 *>(p + row * D + 4 * c);
+    l = fmaf(p[kRows * D + kRows + row], s, l);
+    a.x = fmaf(v.x, s, a.x);
+    a.y = fmaf(v.y, s, a.y);
+    a.z = fmaf(v.z, s, a.z);
+    a.w = fmaf(v.w, s, a.w);
+  }
+  sa[threadIdx.x] = a;
+  sl[threadIdx.x] = l;
+  __syncthreads();
+  if (threadIdx.x >= kCols) return;
+#pragma unroll
+  for (int q = 1; q < kAt; ++q) {
+    const float4 v = sa[q * kCols + c];
+    l += sl[q * kCols + c];
+    a.x += v.x;
+    a.y += v.y;
+    a.z += v.z;
+    a.w += v.w;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  T *o = (T *)g.out + seq * g.o_stride[0] + (row / group) * g.o_stride[1] +
+         (int64_t)(head * group + row % group) * g.o_stride[2] + 4 * c;
+  o[0] = from_f32<T>(a.x * inv);
+  o[1] = from_f32<T>(a.y * inv);
+  o[2] = from_f32<T>(a.z * inv);
+  o[3] = from_f32<T>(a.w * inv);
+}
+
+template <typename T, int D>
+gptq_status run_decode(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
+  using C = Decode<D>;
+  const int64_t rows = g.n_new * (g.n_heads / g.n_kv);
+  const int rt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
+  const auto kernel = rt == 1 ? decode_kernel<T, D, 1>
+                              : (rt == 2 ? decode_kernel<T, D, 2> : decode_kernel<T, D, 4>);
+  GPTQ_TRY(ensure_smem_attr((const void *)kernel, (int)C::kSmem));
+  int sms = 0;
+  GPTQ_TRY(device_sm_count(&sms));
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  float *part = (float *)((char *)ws + 256);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch(2);
+  GPTQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, kernel, g, part, (DevStatus *)ws));
+  cfg.gridDim = dim3((unsigned)(g.n_seq * g.n_kv * rows));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  GPTQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, join_kernel<T, D>, g, (const float *)part, kWarps / rt,
+                                     (int64_t)ctas));
+  return GPTQ_OK;
 }
 
 // One warp per (sequence, new token, head): 32 tokens at a time, a lane per token for the
@@ -30,9 +612,7 @@ __global__ void __launch_bounds__(128) attention_rows_kernel(Kv8AttentionArgs g)
   T *o = (T *)g.out + seq * g.o_stride[0] + t * g.o_stride[1] + head * g.o_stride[2];
   for (int d = lane; d < D; d += 32) sq[warp][d] = to_f32(q[d]) * g.scale;
   __syncwarp();
-  int64_t len = g.lengths[seq];
-  const int64_t cap = (int64_t)g.max_blocks * kTok;
-  len = len < 0 ? 0 : (len > cap ? cap : len);
+  const int64_t len = seq_length(g, (int)seq);
   int64_t end = g.causal ? len - g.n_new + t + 1 : len;
   float m = -INFINITY, l = 0.f, acc[D / 32] = {};
   for (int64_t j0 = 0; j0 < end; j0 += 32) {
@@ -69,21 +649,35 @@ __global__ void __launch_bounds__(128) attention_rows_kernel(Kv8AttentionArgs g)
     o[lane + 32 * i] = from_f32<T>(m == -INFINITY && l == 0.f ? 0.f : acc[i] / l);
 }
 
-}  // namespace
-
-size_t kv8_attention_ws_bytes(int, int64_t, int, int, int, int) { return 256; }
-
-gptq_status launch_kv8_attention(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
+template <typename T, int D>
+gptq_status run_any(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
+  if (g.n_new * (g.n_heads / g.n_kv) <= kRows) return run_decode<T, D>(g, ws, s);
   GPTQ_CUDA_CHECK(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s));
   const int64_t rows = (int64_t)g.n_seq * g.n_new * g.n_heads;
-  if (rows == 0) return GPTQ_OK;
-  const dim3 grid((unsigned)ceil_div(rows, 4));
+  return launch_kernel(attention_rows_kernel<T, D>, dim3((unsigned)ceil_div(rows, 4)), dim3(128),
+                       0, s, g);
+}
+
+}  // namespace
+
+size_t kv8_attention_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int dim,
+                              int max_blocks) {
+  if (n_new * (n_heads / n_kv) > kRows) return 256;
+  int64_t ctas = kMaxCtas;
+  const int64_t units = (int64_t)n_seq * n_kv * max_blocks;
+  if (units < ctas) ctas = units;
+  return 256 + (size_t)(2 * ctas) * (kRows * dim + 2 * kRows) * 4;
+}
+
+gptq_status launch_kv8_attention(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
+  if (g.n_seq == 0 || g.n_new == 0) {
+    GPTQ_CUDA_CHECK(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s));
+    return GPTQ_OK;
+  }
   if (g.dtype == GPTQ_F16)
-    return g.dim == 64 ? launch_kernel(attention_rows_kernel<__half, 64>, grid, dim3(128), 0, s, g)
-                       : launch_kernel(attention_rows_kernel<__half, 128>, grid, dim3(128), 0, s, g);
-  return g.dim == 64
-             ? launch_kernel(attention_rows_kernel<__nv_bfloat16, 64>, grid, dim3(128), 0, s, g)
-             : launch_kernel(attention_rows_kernel<__nv_bfloat16, 128>, grid, dim3(128), 0, s, g);
+    return g.dim == 64 ? run_any<__half, 64>(g, ws, s) : run_any<__half, 128>(g, ws, s);
+  return g.dim == 64 ? run_any<__nv_bfloat16, 64>(g, ws, s)
+                     : run_any<__nv_bfloat16, 128>(g, ws, s);
 }
 
 }  // namespace gptq
