@@ -1,4 +1,13 @@
-// What the two attention kernels over the 8-bit cache share.
+// What the attention kernels over the 8-bit cache share: the division of their work and the
+// joining of its pieces.
+//
+// The rows of a (sequence, cache head) are its new tokens' queries of the group's heads, row r
+// being token r / group and head r % group of the group.  An entry is a tile of up to kRows rows
+// of one sequence, an item an entry with a head, and a unit one step along an item's cached
+// tokens.  Units are numbered entry by entry, head by head; CTA w of n takes the units
+// [total w / n, total (w + 1) / n).  An item inside one share is finished there; otherwise each
+// share leaves a piece (acc, m, l) of it, in its CTA's first slot if the share begins with or
+// inside the item and in the second otherwise, and join_kernel adds the pieces in order.
 #pragma once
 
 #include <type_traits>
@@ -10,6 +19,7 @@ namespace gptq {
 namespace kv8 {
 
 constexpr int kTok = GPTQ_KV8_BLOCK;
+constexpr int kMaxCtas = 160;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <typename T>
@@ -38,11 +48,209 @@ __device__ __forceinline__ void wait_for_grids() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// A finite power of two next to amax (1 for 0), for rows that are scaled into fp16's range.
+// The exponent of a row's largest magnitude (0 for a row of zeros), by which queries are scaled
+// into the range of the type that the tensor cores take.
 __device__ __forceinline__ int row_exponent(float amax) {
   const int e = (int)(__float_as_uint(amax) >> 23) - 127;
-  return amax == 0.0f ? 0 : (e < -120 ? -120 : (e > 120 ? 120 : e));
+  return amax == 0.0f ? 0 : (e < -110 ? -110 : (e > 120 ? 120 : e));
+}
+
+// Entries of ROWS rows whose units are UNIT cached tokens.
+template <int ROWS, int UNIT>
+struct Plan {
+  static constexpr int kRows = ROWS, kUnit = UNIT;
+  const Kv8AttentionArgs &g;
+  int group, rows, tiles, entries;  // rows and row tiles of a sequence
+
+  __device__ __forceinline__ explicit Plan(const Kv8AttentionArgs &a) : g(a) {
+    group = a.n_heads / a.n_kv;
+    rows = (int)a.n_new * group;
+    tiles = (rows + ROWS - 1) / ROWS;
+    entries = a.n_seq * tiles;
+  }
+  // Tokens that some row of [row0, row1) of a sequence with `length` tokens sees.
+  __device__ __forceinline__ int seen(int length, int row0, int row1) const {
+    if (row1 > rows) row1 = rows;
+    if (row0 >= row1) return 0;
+    const int n = g.causal ? length - (int)g.n_new + (row1 - 1) / group + 1 : length;
+    return n < 0 ? 0 : n;
+  }
+  __device__ __forceinline__ int units(int entry) const {
+    const int seq = entry / tiles, row0 = entry % tiles * ROWS;
+    return (seen(seq_length(g, seq), row0, row0 + ROWS) + UNIT - 1) / UNIT;
+  }
+  // Whole warp: units of all items.
+  __device__ __forceinline__ int64_t total() const {
+    int64_t s = 0;
+    for (int i = threadIdx.x % 32; i < entries; i += 32) s += units(i);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s * g.n_kv;
+  }
+};
+
+// The CTAs that share `total` units, `turn` of them at a time at least, and a share's start.
+__device__ __forceinline__ int64_t shares(int64_t total, int turn, int64_t ctas) {
+  const int64_t n = (total + turn - 1) / turn;
+  return n < ctas ? n : ctas;
+}
+__device__ __forceinline__ int64_t share_start(int64_t total, int64_t n, int64_t w) {
+  return total * w / n;
+}
+
+// A unit: step `blk` of the `nblk` of an item.
+struct Cursor {
+  int entry, head, blk, nblk;
+  template <typename P>
+  __device__ __forceinline__ void next_item(const P &p) {
+    blk = 0;
+    if (++head < p.g.n_kv) return;
+    head = 0;
+    do ++entry; while (entry < p.entries && (nblk = p.units(entry)) == 0);
+  }
+  template <typename P>
+  __device__ __forceinline__ void advance(const P &p, int by) {
+    while (blk + by >= nblk && entry < p.entries) {
+      by -= nblk - blk;
+      next_item(p);
+    }
+    blk += by;
+  }
+};
+
+// Whole warp: the cursor of unit u (0 <= u < total).
+template <typename P>
+__device__ __forceinline__ Cursor cursor_at(const P &p, int64_t u) {
+  const int lane = threadIdx.x % 32;
+  for (int s0 = 0;; s0 += 32) {
+    const int nb = s0 + lane < p.entries ? p.units(s0 + lane) : 0;
+    int64_t incl = (int64_t)nb * p.g.n_kv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, incl > u);
+    if (past == 0) {
+      u -= __shfl_sync(0xffffffffu, incl, 31);
+      continue;
+    }
+    const int src = __ffs(past) - 1;
+    const int n = __shfl_sync(0xffffffffu, nb, src);
+    const int64_t at = u - (__shfl_sync(0xffffffffu, incl, src) - (int64_t)n * p.g.n_kv);
+    return Cursor{s0 + src, (int)(at / n), (int)(at % n), n};
+  }
+}
+
+// Where row `row` of a sequence's head goes.
+template <typename T>
+__device__ __forceinline__ T *out_row(const Kv8AttentionArgs &g, int group, int seq, int head,
+                                      int row) {
+  return (T *)g.out + seq * g.o_stride[0] + (row / group) * g.o_stride[1] +
+         (int64_t)(head * group + row % group) * g.o_stride[2];
+}
+
+// All threads of a CTA: zeros for the entries that see nothing (no unit of theirs exists), the
+// CTAs taking the entries in turn.
+template <typename T, int D, typename P>
+__device__ __forceinline__ void write_empty(const P &p, int thread, int threads) {
+  for (int e = blockIdx.x; e < p.entries; e += gridDim.x) {
+    if (p.units(e) > 0) continue;
+    const int row0 = e % p.tiles * P::kRows, n = min(P::kRows, p.rows - row0);
+    for (int i = thread; i < n * p.g.n_kv * D; i += threads)
+      out_row<T>(p.g, p.group, e / p.tiles, i / D % p.g.n_kv, row0 + i / D / p.g.n_kv)[i % D] =
+          from_f32<T>(0.0f);
+  }
+}
+
+template <typename P, int D>
+constexpr int kPiece = P::kRows *(D + 2);  // floats of a piece: acc [rows][D], m, l
+
+// Joins the pieces of the items that the start of share w cuts, w = blockIdx.x + 1, for every
+// gridDim.y-th row: out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i.  It starts while the
+// kernel before runs (which has waited for all before it, so the lengths are there) and waits
+// for it where it reads the pieces; it waits also where there is nothing to join, since its end
+// has to mean that the other's came.
+template <typename T, int D, typename P>
+__global__ void __launch_bounds__(128)
+join_kernel(Kv8AttentionArgs g, const float *part, int turn, int64_t ctas) {
+  constexpr int kCols = D / 4, kAt = 128 / kCols;  // threads along a row; rows at a time
+  const P p(g);
+  const int64_t total = p.total(), n = shares(total, turn, ctas);
+  const int64_t w = (int64_t)blockIdx.x + 1;
+  bool cut = w < n;
+  Cursor at{};
+  int64_t first = 0, last = w;
+  bool late = false;
+  if (cut) {
+    const int64_t s = share_start(total, n, w), before = share_start(total, n, w - 1);
+    at = cursor_at(p, s);
+    first = s - at.blk;
+    cut = at.blk > 0 && before <= first;  // a later start in the same item leaves it to the first
+    late = before < first;
+    while (last + 1 < n && share_start(total, n, last + 1) < first + at.nblk) ++last;
+  }
+  wait_for_grids();
+  if (!cut) return;
+  const int seq = at.entry / p.tiles, row0 = at.entry % p.tiles * P::kRows;
+  const int rows = min(P::kRows, p.rows - row0), c = threadIdx.x % kCols;
+  const float *p0 = part + (2 * (w - 1) + (late ? 1 : 0)) * kPiece<P, D>;
+  for (int row = blockIdx.y * kAt + threadIdx.x / kCols; row < rows; row += gridDim.y * kAt) {
+    float m = -INFINITY, l = 0.0f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float *q = p0;
+#pragma unroll 4
+    for (int64_t i = w - 1; i <= last; ++i) {
+      m = fmaxf(m, q[P::kRows * D + row]);
+      q = part + 2 * (i + 1) * kPiece<P, D>;
+    }
+    if (m == -INFINITY) m = 0.0f;
+    q = p0;
+#pragma unroll 4
+    for (int64_t i = w - 1; i <= last; ++i) {
+      const float sc = ex2(q[P::kRows * D + row] - m);
+      const float4 v = *reinterpret_cast<const float4 *>(q + row * D + 4 * c);
+      l = fmaf(q[P::kRows * (D + 1) + row], sc, l);
+      a.x = fmaf(v.x, sc, a.x);
+      a.y = fmaf(v.y, sc, a.y);
+      a.z = fmaf(v.z, sc, a.z);
+      a.w = fmaf(v.w, sc, a.w);
+      q = part + 2 * (i + 1) * kPiece<P, D>;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    T *o = out_row<T>(g, p.group, seq, at.head, row0 + row) + 4 * c;
+    o[0] = from_f32<T>(a.x * inv);
+    o[1] = from_f32<T>(a.y * inv);
+    o[2] = from_f32<T>(a.z * inv);
+    o[3] = from_f32<T>(a.w * inv);
+  }
+}
+
+// Launches a kernel that may start before the one ahead of it in the stream ends (it waits with
+// wait_for_grids).
+template <typename... KArgs, typename... Args>
+gptq_status launch_early(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t s, Args &&...args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  GPTQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...));
+  return GPTQ_OK;
 }
 
 }  // namespace kv8
+
+// kv8_prompt.cu: many queries (prompts), on the tensor cores.
+size_t kv8_prompt_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int dim,
+                           int max_blocks);
+gptq_status launch_kv8_prompt(const Kv8AttentionArgs &g, void *ws, cudaStream_t s);
+
 }  // namespace gptq

@@ -25,7 +25,7 @@
 // (contiguous) running; eight warps in groups of one warp per eight rows take the units in turn,
 // each group through a ring of its own in shared memory, and meet at the end of an item.  An
 // item that lies in one share is written there; pieces of others meet in a second small kernel,
-// in order (repeatable), which also writes the rows that see nothing.
+// in order (repeatable).
 #include "kv8.cuh"
 
 namespace gptq {
@@ -35,7 +35,7 @@ namespace {
 using namespace kv8;
 
 constexpr int kRows = 32;                 // most rows of an item
-constexpr int kMaxCtas = 160;
+using DecodePlan = Plan<kRows, kTok>;     // a unit is one block
 constexpr int kWarps = 8;                 // that compute
 // Registers go by groups of four warps: two that compute, one with the look-up warp.  At launch
 // 384 threads have 168 each (64,512); the split below is that many: 256 x 232 + 128 x 40.
@@ -51,78 +51,8 @@ struct Decode {
   static constexpr int kWarpPart = 8 * D + 16;                // floats: acc, m, l of eight rows
   static constexpr size_t kSmem =
       128 + kRing + kWarps * kWarpPart * 4 + kList * 8 + 2 * kWarps * kSlots * 8;
-  static constexpr int kPart = kRows * D + 2 * kRows;         // floats of a piece of an item
+  static constexpr int kPart = kPiece<DecodePlan, D>;
 };
-
-// Blocks of a sequence that some query row sees.
-__device__ __forceinline__ int seq_blocks(const Kv8AttentionArgs &g, int seq) {
-  return (seq_length(g, seq) + kTok - 1) / kTok;
-}
-
-// Whole warp: units of the sequences [0, n), a unit being one block of one head.
-__device__ __forceinline__ int64_t units_before(const Kv8AttentionArgs &g, int n) {
-  int64_t s = 0;
-  for (int i = threadIdx.x % 32; i < n; i += 32) s += seq_blocks(g, i);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s * g.n_kv;
-}
-
-// The CTAs that share `total` units taken `turn` at a time, and the first unit of share w.
-__device__ __forceinline__ int64_t shares(int64_t total, int turn, int64_t ctas) {
-  const int64_t n = (total + turn - 1) / turn;
-  return n < ctas ? n : ctas;
-}
-__device__ __forceinline__ int64_t share_start(int64_t total, int64_t n, int64_t w) {
-  return total * w / n;
-}
-__device__ __forceinline__ int64_t share_of(int64_t total, int64_t n, int64_t u) {
-  int64_t w = u * n / total;
-  while (w + 1 < n && share_start(total, n, w + 1) <= u) ++w;
-  while (share_start(total, n, w) > u) --w;
-  return w;
-}
-
-// Position in the unit space.
-struct Cursor {
-  int seq, head, blk, nblk;
-  __device__ __forceinline__ void next_item(const Kv8AttentionArgs &g) {
-    blk = 0;
-    if (++head < g.n_kv) return;
-    head = 0;
-    do ++seq; while (seq < g.n_seq && (nblk = seq_blocks(g, seq)) == 0);
-  }
-  __device__ __forceinline__ void advance(const Kv8AttentionArgs &g, int by) {
-    while (blk + by >= nblk && seq < g.n_seq) {
-      by -= nblk - blk;
-      next_item(g);
-    }
-    blk += by;
-  }
-};
-
-// Whole warp: the cursor of unit u (0 <= u < total).
-__device__ __forceinline__ Cursor cursor_at(const Kv8AttentionArgs &g, int64_t u) {
-  const int lane = threadIdx.x % 32;
-  for (int s0 = 0;; s0 += 32) {
-    const int nb = s0 + lane < g.n_seq ? seq_blocks(g, s0 + lane) : 0;
-    int64_t incl = (int64_t)nb * g.n_kv;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, incl > u);
-    if (past == 0) {
-      u -= __shfl_sync(0xffffffffu, incl, 31);
-      continue;
-    }
-    const int src = __ffs(past) - 1;
-    const int n = __shfl_sync(0xffffffffu, nb, src);
-    const int64_t at = u - (__shfl_sync(0xffffffffu, incl, src) - (int64_t)n * g.n_kv);
-    return Cursor{s0 + src, (int)(at / n), (int)(at % n), n};
-  }
-}
 
 __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -242,12 +172,15 @@ decode_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
   // the call's status; a wait that gives up writes it, two seconds from here or later
   if (blockIdx.x == 0 && threadIdx.x == 0) st->status = 0;
 
-  const int64_t total = units_before(g, g.n_seq);
+  const DecodePlan plan(g);
+  const int group = plan.group, rows = plan.rows;
+  write_empty<T, D>(plan, threadIdx.x, kThreads);
+  const int64_t total = plan.total();
   const int64_t n = shares(total, G, gridDim.x);
   if (blockIdx.x >= n) return;
   const int64_t u0 = share_start(total, n, blockIdx.x);
   const int count = (int)(share_start(total, n, blockIdx.x + 1) - u0);
-  Cursor at = cursor_at(g, u0);
+  Cursor at = cursor_at(plan, u0);
 
   if (warp >= kWarps) {
     // ---------------- look-up and copies ----------------
@@ -256,14 +189,14 @@ decode_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
     // Lane l looks up unit i0 + l of each batch of 32: table entries of the batch after the next
     // and exponents of the next are on their way while a batch is written to the list.
     Cursor c = at;
-    c.advance(g, lane);
+    c.advance(plan, lane);
     int page = -1, place = -1, exps = 0, head = 0;  // of the batches after and next
     auto load_page = [&](int i) {
       page = -1;
       if (i < count) {
-        page = g.table[c.seq * g.ld_table + c.blk];
+        page = g.table[c.entry * g.ld_table + c.blk];
         head = c.head;
-        if (i + 32 < count) c.advance(g, 32);
+        if (i + 32 < count) c.advance(plan, 32);
       }
     };
     auto load_exps = [&]() {
@@ -318,7 +251,6 @@ decode_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
   // ---------------- products ----------------
   asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
   const int t = lane % 4, grp = warp / RT, r = (warp % RT) * 8 + lane / 4;  // this thread's row
-  const int group = g.n_heads / g.n_kv, rows = (int)g.n_new * group;
   uint8_t *ring = smem + (size_t)grp * H * C::kHalf;
   float *mine = spart + warp * C::kWarpPart;
   full += grp * H;
@@ -336,11 +268,11 @@ decode_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
   };
   for (int i = grp, i0 = 0; i0 < count;) {
     const int i1 = i0 + at.nblk - at.blk < count ? i0 + at.nblk - at.blk : count;  // item's units
-    const int length = seq_length(g, at.seq);
+    const int length = seq_length(g, at.entry);
     const int limit = r >= rows ? 0 : (g.causal ? length - (int)g.n_new + r / group + 1 : length);
     uint32_t qa[D / 16][NT];
     float f, m = -INFINITY, l = 0.0f, acc[D / 8][4];
-    load_queries<T, D>(g, at.seq, at.head, r, rows, group, qa, f);
+    load_queries<T, D>(g, at.entry, at.head, r, rows, group, qa, f);
 #pragma unroll
     for (int q = 0; q < D / 8; ++q)
 #pragma unroll
@@ -476,8 +408,7 @@ decode_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       }
       if (whole) {
         const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-        T *o = (T *)g.out + at.seq * g.o_stride[0] + (row / group) * g.o_stride[1] +
-               (int64_t)(at.head * group + row % group) * g.o_stride[2] + d;
+        T *o = out_row<T>(g, group, at.entry, at.head, row) + d;
         o[0] = from_f32<T>(a.x * inv);
         o[1] = from_f32<T>(a.y * inv);
         o[2] = from_f32<T>(a.z * inv);
@@ -493,76 +424,8 @@ decode_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
     }
     tc::named_barrier(1, 32 * kWarps);  // the parts have been read
     i0 = i1;
-    if (i0 < count) at.next_item(g);
+    if (i0 < count) at.next_item(plan);
   }
-}
-
-// Joins the pieces of one item (sequence, head): out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i.
-// It starts while the kernel above runs (which has waited for all before it, so the lengths are
-// there) and waits for it where it reads the pieces.
-template <typename T, int D>
-__global__ void __launch_bounds__(128)
-join_kernel(Kv8AttentionArgs g, const float *part, int turn, int64_t ctas) {
-  constexpr int kPart = Decode<D>::kPart;
-  constexpr int kCols = D / 4, kAt = 128 / kCols;  // threads along a row; pieces at a time
-  __shared__ float4 sa[128];
-  __shared__ float sl[128];
-  const int group = g.n_heads / g.n_kv, rows = (int)g.n_new * group;
-  const int row = blockIdx.x % rows, item = blockIdx.x / rows;
-  const int seq = item / g.n_kv, head = item % g.n_kv;
-  const int64_t nblk = seq_blocks(g, seq);
-  int64_t w0 = 0, w1 = -1;
-  bool late = false;  // the first piece is the second of its CTA
-  if (nblk > 0) {
-    const int64_t total = units_before(g, g.n_seq), n = shares(total, turn, ctas);
-    const int64_t first = units_before(g, seq) + head * nblk;
-    w0 = share_of(total, n, first);
-    w1 = share_of(total, n, first + nblk - 1);
-    late = share_start(total, n, w0) < first;
-  }
-  // also where there is nothing to do: this kernel's end has to mean that the other's came
-  wait_for_grids();
-  if (nblk > 0 && w0 == w1) return;  // one CTA had it all
-  const int c = threadIdx.x % kCols;
-  auto piece = [&](int64_t w) { return part + (2 * w + (w == w0 && late ? 1 : 0)) * kPart; };
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t w = w0 + threadIdx.x % 32; w <= w1; w += 32)
-    m = fmaxf(m, piece(w)[kRows * D + row]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (m == -INFINITY) m = 0.0f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int64_t w = w0 + threadIdx.x / kCols; w <= w1; w += kAt) {
-    const float *p = piece(w);
-    const float s = ex2(p[kRows * D + row] - m);
-    const float4 v = *reinterpret_cast<const float4 *>(p + row * D + 4 * c);
-    l = fmaf(p[kRows * D + kRows + row], s, l);
-    a.x = fmaf(v.x, s, a.x);
-    a.y = fmaf(v.y, s, a.y);
-    a.z = fmaf(v.z, s, a.z);
-    a.w = fmaf(v.w, s, a.w);
-  }
-  sa[threadIdx.x] = a;
-  sl[threadIdx.x] = l;
-  __syncthreads();
-  if (threadIdx.x >= kCols) return;
-#pragma unroll
-  for (int q = 1; q < kAt; ++q) {
-    const float4 v = sa[q * kCols + c];
-    l += sl[q * kCols + c];
-    a.x += v.x;
-    a.y += v.y;
-    a.z += v.z;
-    a.w += v.w;
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  T *o = (T *)g.out + seq * g.o_stride[0] + (row / group) * g.o_stride[1] +
-         (int64_t)(head * group + row % group) * g.o_stride[2] + 4 * c;
-  o[0] = from_f32<T>(a.x * inv);
-  o[1] = from_f32<T>(a.y * inv);
-  o[2] = from_f32<T>(a.z * inv);
-  o[3] = from_f32<T>(a.w * inv);
 }
 
 template <typename T, int D>
@@ -577,96 +440,24 @@ gptq_status run_decode(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   GPTQ_TRY(device_sm_count(&sms));
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   float *part = (float *)((char *)ws + 256);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  count_launch(2);
-  GPTQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, kernel, g, part, (DevStatus *)ws));
-  cfg.gridDim = dim3((unsigned)(g.n_seq * g.n_kv * rows));
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
-  GPTQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, join_kernel<T, D>, g, (const float *)part, kWarps / rt,
-                                     (int64_t)ctas));
-  return GPTQ_OK;
-}
-
-// One warp per (sequence, new token, head): 32 tokens at a time, a lane per token for the
-// scores and D / 32 channels per lane for the output.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) attention_rows_kernel(Kv8AttentionArgs g) {
-  __shared__ float sq[4][D];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t r = (int64_t)blockIdx.x * 4 + warp;
-  if (r >= (int64_t)g.n_seq * g.n_new * g.n_heads) return;
-  const int head = (int)(r % g.n_heads);
-  const int64_t t = r / g.n_heads % g.n_new, seq = r / g.n_heads / g.n_new;
-  const int kvh = head / (g.n_heads / g.n_kv);
-  const T *q = (const T *)g.q + seq * g.q_stride[0] + t * g.q_stride[1] + head * g.q_stride[2];
-  T *o = (T *)g.out + seq * g.o_stride[0] + t * g.o_stride[1] + head * g.o_stride[2];
-  for (int d = lane; d < D; d += 32) sq[warp][d] = to_f32(q[d]) * g.scale;
-  __syncwarp();
-  const int64_t len = seq_length(g, (int)seq);
-  int64_t end = g.causal ? len - g.n_new + t + 1 : len;
-  float m = -INFINITY, l = 0.f, acc[D / 32] = {};
-  for (int64_t j0 = 0; j0 < end; j0 += 32) {
-    const int64_t page = g.table[seq * g.ld_table + j0 / kTok];
-    if (page < 0 || page >= g.n_blocks) continue;
-    const int64_t ph = page * g.n_kv + kvh;
-    const uint8_t *kc = g.k + ph * (kTok * D), *vc = g.v + ph * (kTok * D);
-    const float ks = fp8::exp_value(g.k_exps[ph]), vs = fp8::exp_value(g.v_exps[ph]);
-    const int slot = (int)(j0 % kTok) + lane;
-    const bool seen = j0 + lane < end;
-    float s = -INFINITY;
-    if (seen) {
-      s = 0.f;
-      for (int d = 0; d < D; ++d) s = fmaf(sq[warp][d], fp8::unpack1(kc[slot * D + d]), s);
-      s *= ks;
-    }
-    float mx = s;
-    for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    const float mn = fmaxf(m, mx), f = __expf(m - mn);
-    const float pr = seen ? __expf(s - mn) : 0.f;
-    m = mn;
-    l = l * f + pr;
-    for (int i = 0; i < D / 32; ++i) {
-      float a = 0.f;
-      for (int w = 0; w < 32; ++w) {
-        const float pw = __shfl_sync(0xffffffffu, pr, w);
-        if (j0 + w < end) a = fmaf(pw, fp8::unpack1(vc[(lane + 32 * i) * kTok + slot - lane + w]), a);
-      }
-      acc[i] = acc[i] * f + a * vs;
-    }
-  }
-  for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-  for (int i = 0; i < D / 32; ++i)
-    o[lane + 32 * i] = from_f32<T>(m == -INFINITY && l == 0.f ? 0.f : acc[i] / l);
-}
-
-template <typename T, int D>
-gptq_status run_any(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
-  if (g.n_new * (g.n_heads / g.n_kv) <= kRows) return run_decode<T, D>(g, ws, s);
-  GPTQ_CUDA_CHECK(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s));
-  const int64_t rows = (int64_t)g.n_seq * g.n_new * g.n_heads;
-  return launch_kernel(attention_rows_kernel<T, D>, dim3((unsigned)ceil_div(rows, 4)), dim3(128),
-                       0, s, g);
+  GPTQ_TRY(launch_early(kernel, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, s, g, part,
+                        (DevStatus *)ws));
+  const int at_once = 128 / (D / 4);
+  return launch_early(join_kernel<T, D, DecodePlan>,
+                      dim3((unsigned)ctas - 1, (unsigned)ceil_div(rows, at_once)), dim3(128), 0, s,
+                      g, (const float *)part, kWarps / rt, (int64_t)ctas);
 }
 
 }  // namespace
 
 size_t kv8_attention_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int dim,
                               int max_blocks) {
-  if (n_new * (n_heads / n_kv) > kRows) return 256;
+  if (n_new * (n_heads / n_kv) > kRows)
+    return kv8_prompt_ws_bytes(n_seq, n_new, n_heads, n_kv, dim, max_blocks);
   int64_t ctas = kMaxCtas;
   const int64_t units = (int64_t)n_seq * n_kv * max_blocks;
   if (units < ctas) ctas = units;
-  return 256 + (size_t)(2 * ctas) * (kRows * dim + 2 * kRows) * 4;
+  return 256 + (size_t)(2 * ctas) * kRows * (dim + 2) * 4;
 }
 
 gptq_status launch_kv8_attention(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
@@ -674,10 +465,14 @@ gptq_status launch_kv8_attention(const Kv8AttentionArgs &g, void *ws, cudaStream
     GPTQ_CUDA_CHECK(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s));
     return GPTQ_OK;
   }
+  // Up to 32 rows a cache head the products are bound by the memory on either path, and here
+  // they wait for nothing but their own copies; from there on the tensor cores' 128-row tiles
+  // are filled far enough.
+  if (g.n_new * (g.n_heads / g.n_kv) > kRows) return launch_kv8_prompt(g, ws, s);
   if (g.dtype == GPTQ_F16)
-    return g.dim == 64 ? run_any<__half, 64>(g, ws, s) : run_any<__half, 128>(g, ws, s);
-  return g.dim == 64 ? run_any<__nv_bfloat16, 64>(g, ws, s)
-                     : run_any<__nv_bfloat16, 128>(g, ws, s);
+    return g.dim == 64 ? run_decode<__half, 64>(g, ws, s) : run_decode<__half, 128>(g, ws, s);
+  return g.dim == 64 ? run_decode<__nv_bfloat16, 64>(g, ws, s)
+                     : run_decode<__nv_bfloat16, 128>(g, ws, s);
 }
 
 }  // namespace gptq
