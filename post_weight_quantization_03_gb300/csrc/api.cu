@@ -469,6 +469,8 @@ gptq_status gptq_kv8_attention(const void *q, const int64_t *q_strides, int dtyp
   g.k = k; g.v = v; g.k_exps = k_exps; g.v_exps = v_exps; g.n_blocks = n_blocks;
   g.table = table; g.ld_table = ld_table; g.max_blocks = (int)max_blocks;
   g.lengths = lengths; g.causal = causal ? 1 : 0; g.scale = scale;
+  g.vec_q = strided_vec(q, q_strides, 2);
+  g.vec_o = strided_vec(out, o_strides, 2);
   return launch_kv8_attention(g, ws, (cudaStream_t)stream);
 }
 

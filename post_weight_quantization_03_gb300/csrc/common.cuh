@@ -236,6 +236,7 @@ struct Kv8AttentionArgs {
   const int32_t *table; int64_t ld_table; int max_blocks;
   const int32_t *lengths;
   int causal; float scale;
+  int vec_q, vec_o;                          // rows of q, out are 16-byte aligned
 };
 size_t kv8_attention_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int dim,
                               int max_blocks);

@@ -4,10 +4,12 @@
 // The rows of a (sequence, cache head) are its new tokens' queries of the group's heads, row r
 // being token r / group and head r % group of the group.  An entry is a tile of up to kRows rows
 // of one sequence, an item an entry with a head, and a unit one step along an item's cached
-// tokens.  Units are numbered entry by entry, head by head; CTA w of n takes the units
-// [total w / n, total (w + 1) / n).  An item inside one share is finished there; otherwise each
-// share leaves a piece (acc, m, l) of it, in its CTA's first slot if the share begins with or
-// inside the item and in the second otherwise, and join_kernel adds the pieces in order.
+// tokens.  Units are numbered entry by entry, head by head.  For the division an item weighs its
+// units and SETUP more, for what is done once for it: CTA w of n takes the weight [total w / n,
+// total (w + 1) / n), a start inside an item's setup being its first unit.  An item inside one
+// share is finished there; otherwise each share leaves a piece (acc, m, l) of it, in its CTA's
+// first slot if the share begins with or inside the item and in the second otherwise, and
+// join_kernel adds the pieces in order.
 #pragma once
 
 #include <type_traits>
@@ -34,6 +36,18 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp16 numbers from the lower (upper) two codes of a word.
+__device__ __forceinline__ uint32_t halves_lo(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(w));
+  return h;
+}
+__device__ __forceinline__ uint32_t halves_hi(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(h) : "r"(w));
+  return h;
+}
+
 // Cached tokens of a sequence, inside the table.
 __device__ __forceinline__ int seq_length(const Kv8AttentionArgs &g, int seq) {
   const int len = g.lengths[seq], cap = g.max_blocks * kTok;
@@ -56,9 +70,9 @@ __device__ __forceinline__ int row_exponent(float amax) {
 }
 
 // Entries of ROWS rows whose units are UNIT cached tokens.
-template <int ROWS, int UNIT>
+template <int ROWS, int UNIT, int SETUP>
 struct Plan {
-  static constexpr int kRows = ROWS, kUnit = UNIT;
+  static constexpr int kRows = ROWS, kSetup = SETUP;
   const Kv8AttentionArgs &g;
   int group, rows, tiles, entries;  // rows and row tiles of a sequence
 
@@ -79,17 +93,21 @@ struct Plan {
     const int seq = entry / tiles, row0 = entry % tiles * ROWS;
     return (seen(seq_length(g, seq), row0, row0 + ROWS) + UNIT - 1) / UNIT;
   }
-  // Whole warp: units of all items.
+  // Whole warp: the weight of all items.
   __device__ __forceinline__ int64_t total() const {
     int64_t s = 0;
-    for (int i = threadIdx.x % 32; i < entries; i += 32) s += units(i);
+    for (int i = threadIdx.x % 32; i < entries; i += 32) {
+      const int n = units(i);
+      s += n > 0 ? n + SETUP : 0;
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s * g.n_kv;
   }
 };
 
-// The CTAs that share `total` units, `turn` of them at a time at least, and a share's start.
+// The CTAs that share the weight `total`, `turn` units of it at a time at least, and where share
+// w starts.
 __device__ __forceinline__ int64_t shares(int64_t total, int turn, int64_t ctas) {
   const int64_t n = (total + turn - 1) / turn;
   return n < ctas ? n : ctas;
@@ -118,28 +136,60 @@ struct Cursor {
   }
 };
 
-// Whole warp: the cursor of unit u (0 <= u < total).
+// Whole warp: the cursor at weight v (0 <= v < total), the units before it and, in `start`, the
+// weight at which its item starts.
 template <typename P>
-__device__ __forceinline__ Cursor cursor_at(const P &p, int64_t u) {
+__device__ __forceinline__ Cursor cursor_at(const P &p, int64_t v, int64_t &unit, int64_t &start) {
   const int lane = threadIdx.x % 32;
+  unit = start = 0;
   for (int s0 = 0;; s0 += 32) {
     const int nb = s0 + lane < p.entries ? p.units(s0 + lane) : 0;
-    int64_t incl = (int64_t)nb * p.g.n_kv;
+    int64_t incl = nb > 0 ? (int64_t)(nb + P::kSetup) * p.g.n_kv : 0, units = (int64_t)nb * p.g.n_kv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int64_t a = __shfl_up_sync(0xffffffffu, incl, o), b = __shfl_up_sync(0xffffffffu, units, o);
+      if (lane >= o) {
+        incl += a;
+        units += b;
+      }
     }
-    const unsigned past = __ballot_sync(0xffffffffu, incl > u);
+    const unsigned past = __ballot_sync(0xffffffffu, start + incl > v);
     if (past == 0) {
-      u -= __shfl_sync(0xffffffffu, incl, 31);
+      start += __shfl_sync(0xffffffffu, incl, 31);
+      unit += __shfl_sync(0xffffffffu, units, 31);
       continue;
     }
     const int src = __ffs(past) - 1;
-    const int n = __shfl_sync(0xffffffffu, nb, src);
-    const int64_t at = u - (__shfl_sync(0xffffffffu, incl, src) - (int64_t)n * p.g.n_kv);
-    return Cursor{s0 + src, (int)(at / n), (int)(at % n), n};
+    const int n = __shfl_sync(0xffffffffu, nb, src), weight = n + P::kSetup;
+    start += __shfl_sync(0xffffffffu, incl, src) - (int64_t)weight * p.g.n_kv;
+    unit += __shfl_sync(0xffffffffu, units, src) - (int64_t)n * p.g.n_kv;
+    const int head = (int)((v - start) / weight);
+    start += (int64_t)head * weight;
+    const int at = (int)(v - start) - P::kSetup;
+    Cursor c{s0 + src, head, at < 0 ? 0 : at, n};
+    unit += (int64_t)head * n + c.blk;
+    return c;
   }
+}
+
+// Whole warp: this CTA's share, as its first unit's cursor and the number of its units.
+template <typename P>
+__device__ __forceinline__ int my_share(const P &p, int turn, Cursor &first) {
+  const int64_t total = p.total(), n = shares(total, turn, gridDim.x);
+  if (blockIdx.x >= n) return 0;
+  const int64_t v0 = share_start(total, n, blockIdx.x), v1 = share_start(total, n, blockIdx.x + 1);
+  int64_t u0, u1, start;
+  if (v1 < total) cursor_at(p, v1, u1, start);
+  const Cursor c = cursor_at(p, v0, u0, start);
+  first = c;
+  if (v1 == total) {  // all items weigh their units and the same setup: what is left of them
+    int64_t s = 0;
+    for (int i = threadIdx.x % 32; i < p.entries; i += 32) s += p.units(i);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    u1 = s * p.g.n_kv;
+  }
+  return (int)(u1 - u0);
 }
 
 // Where row `row` of a sequence's head goes.
@@ -164,7 +214,7 @@ __device__ __forceinline__ void write_empty(const P &p, int thread, int threads)
 }
 
 template <typename P, int D>
-constexpr int kPiece = P::kRows *(D + 2);  // floats of a piece: acc [rows][D], m, l
+constexpr int kPiece = P::kRows *(D + 2);  // floats of a piece: acc [D / 4][rows][4], m, l
 
 // Joins the pieces of the items that the start of share w cuts, w = blockIdx.x + 1, for every
 // gridDim.y-th row: out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i.  It starts while the
@@ -174,28 +224,30 @@ constexpr int kPiece = P::kRows *(D + 2);  // floats of a piece: acc [rows][D], 
 template <typename T, int D, typename P>
 __global__ void __launch_bounds__(128)
 join_kernel(Kv8AttentionArgs g, const float *part, int turn, int64_t ctas) {
-  constexpr int kCols = D / 4, kAt = 128 / kCols;  // threads along a row; rows at a time
   const P p(g);
   const int64_t total = p.total(), n = shares(total, turn, ctas);
   const int64_t w = (int64_t)blockIdx.x + 1;
   bool cut = w < n;
   Cursor at{};
-  int64_t first = 0, last = w;
+  int64_t last = w;
   bool late = false;
   if (cut) {
-    const int64_t s = share_start(total, n, w), before = share_start(total, n, w - 1);
-    at = cursor_at(p, s);
-    first = s - at.blk;
-    cut = at.blk > 0 && before <= first;  // a later start in the same item leaves it to the first
+    int64_t unit, first;
+    const int64_t v = share_start(total, n, w), before = share_start(total, n, w - 1);
+    at = cursor_at(p, v, unit, first);
+    // a later start in the same item leaves it to the first
+    cut = at.blk > 0 && before <= first + P::kSetup;
     late = before < first;
-    while (last + 1 < n && share_start(total, n, last + 1) < first + at.nblk) ++last;
+    while (last + 1 < n && share_start(total, n, last + 1) < first + P::kSetup + at.nblk) ++last;
   }
   wait_for_grids();
   if (!cut) return;
   const int seq = at.entry / p.tiles, row0 = at.entry % p.tiles * P::kRows;
-  const int rows = min(P::kRows, p.rows - row0), c = threadIdx.x % kCols;
+  const int rows = min(P::kRows, p.rows - row0);
   const float *p0 = part + (2 * (w - 1) + (late ? 1 : 0)) * kPiece<P, D>;
-  for (int row = blockIdx.y * kAt + threadIdx.x / kCols; row < rows; row += gridDim.y * kAt) {
+  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < P::kRows * (D / 4); e += gridDim.y * blockDim.x) {
+    const int row = e % P::kRows, c = e / P::kRows;
+    if (row >= rows) continue;
     float m = -INFINITY, l = 0.0f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     const float *q = p0;
@@ -209,7 +261,7 @@ join_kernel(Kv8AttentionArgs g, const float *part, int turn, int64_t ctas) {
 #pragma unroll 4
     for (int64_t i = w - 1; i <= last; ++i) {
       const float sc = ex2(q[P::kRows * D + row] - m);
-      const float4 v = *reinterpret_cast<const float4 *>(q + row * D + 4 * c);
+      const float4 v = reinterpret_cast<const float4 *>(q)[e];
       l = fmaf(q[P::kRows * (D + 1) + row], sc, l);
       a.x = fmaf(v.x, sc, a.x);
       a.y = fmaf(v.y, sc, a.y);

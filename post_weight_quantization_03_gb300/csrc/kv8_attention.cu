@@ -35,7 +35,7 @@ namespace {
 using namespace kv8;
 
 constexpr int kRows = 32;                 // most rows of an item
-using DecodePlan = Plan<kRows, kTok>;     // a unit is one block
+using DecodePlan = Plan<kRows, kTok, 0>;  // a unit is one block
 constexpr int kWarps = 8;                 // that compute
 // Registers go by groups of four warps: two that compute, one with the look-up warp.  At launch
 // 384 threads have 168 each (64,512); the split below is that many: 256 x 232 + 128 x 40.
@@ -175,12 +175,9 @@ decode_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
   const DecodePlan plan(g);
   const int group = plan.group, rows = plan.rows;
   write_empty<T, D>(plan, threadIdx.x, kThreads);
-  const int64_t total = plan.total();
-  const int64_t n = shares(total, G, gridDim.x);
-  if (blockIdx.x >= n) return;
-  const int64_t u0 = share_start(total, n, blockIdx.x);
-  const int count = (int)(share_start(total, n, blockIdx.x + 1) - u0);
-  Cursor at = cursor_at(plan, u0);
+  Cursor at{};
+  const int count = my_share(plan, G, at);
+  if (count == 0) return;
 
   if (warp >= kWarps) {
     // ---------------- look-up and copies ----------------
@@ -415,7 +412,7 @@ decode_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
         o[3] = from_f32<T>(a.w * inv);
       } else {
         // the share's first item, or (an item begun inside it) its last
-        *reinterpret_cast<float4 *>(piece + row * D + d) = a;
+        reinterpret_cast<float4 *>(piece)[d / 4 * kRows + row] = a;
         if (d == 0) {
           piece[kRows * D + row] = mm;
           piece[kRows * D + kRows + row] = ll;
@@ -442,10 +439,9 @@ gptq_status run_decode(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   float *part = (float *)((char *)ws + 256);
   GPTQ_TRY(launch_early(kernel, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, s, g, part,
                         (DevStatus *)ws));
-  const int at_once = 128 / (D / 4);
-  return launch_early(join_kernel<T, D, DecodePlan>,
-                      dim3((unsigned)ctas - 1, (unsigned)ceil_div(rows, at_once)), dim3(128), 0, s,
-                      g, (const float *)part, kWarps / rt, (int64_t)ctas);
+  // a row of pieces is one thread's for each four channels; the rows that exist are the first
+  return launch_early(join_kernel<T, D, DecodePlan>, dim3((unsigned)ctas - 1, D / 16), dim3(128), 0,
+                      s, g, (const float *)part, kWarps / rt, (int64_t)ctas);
 }
 
 }  // namespace

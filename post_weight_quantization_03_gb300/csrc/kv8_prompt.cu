@@ -21,6 +21,7 @@
 //
 // Warps: 0-3 and 4-7 softmax, a tile each; 8-11 converters; 12 MMA issuer and TMEM owner.
 #include <cudaTypedefs.h>
+#include <limits.h>
 
 #include "kv8.cuh"
 
@@ -31,9 +32,9 @@ namespace {
 using namespace kv8;
 
 constexpr int kTile = 128;                      // rows of an MMA tile, tokens of a unit
-using PromptPlan = Plan<2 * kTile, kTile>;
-// Registers by warp group: 2 x 128 x 192 + 128 x 80 + 128 x 40 = 64,512 of the 65,536 that 512
-// threads have at launch.
+using PromptPlan = Plan<2 * kTile, kTile, 2>;
+// Registers by warp group: 2 x 128 x 192 + 128 x 72 + 128 x 56 = 65,536, what 512 threads have
+// at launch: a softmax thread holds its row's 128 scores.
 constexpr int kThreads = 512;
 constexpr int kInfo = 4;
 constexpr float kLazy = 6.0f;
@@ -44,7 +45,9 @@ struct Prompt {
   static constexpr uint32_t kQ = kTile * D * 2;               // a tile of queries (or keys)
   static constexpr uint32_t kV = D * kTile * 2;               // values, channel-major
   static constexpr uint32_t kVChunk = D * 128;                // 64 tokens of them
-  static constexpr size_t kSmem = 1024 + 2 * kQ + 2 * kQ + 2 * kV + kInfo * 32 + 256;
+  static constexpr uint32_t kHalf = kTok * D;                 // bytes of K (or V) of a block
+  static constexpr size_t kSmem =
+      1024 + 2 * kQ + 2 * kQ + 2 * kV + 4 * kHalf + kInfo * 32 + 2 * kTile * 4 + 192;
   static constexpr uint32_t kCols = 512;
   static constexpr uint32_t kO = 2 * kTile;                   // TMEM column of the first O
 };
@@ -67,17 +70,24 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdes
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[15])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -88,10 +98,27 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ uint32_t halves(uint32_t two) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xFFFFu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Two fp32 numbers at a time: a * b + c, a + b.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // Byte of element (row, 16-byte unit u) in a chunk of 128-byte rows with the 128-byte swizzle.
@@ -106,12 +133,15 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *sq = smem, *sk = sq + 2 * C::kQ, *sv = sk + 2 * C::kQ;
-  Info *info = (Info *)(sv + 2 * C::kV);
-  uint64_t *qfull = (uint64_t *)(info + kInfo);   // [2], by tile
+  uint8_t *raw_k = sv + 2 * C::kV, *raw_v = raw_k + 2 * C::kHalf;  // codes of a unit
+  Info *info = (Info *)(raw_v + 2 * C::kHalf);
+  float *factor = (float *)(info + kInfo);        // of each row's scores
+  uint64_t *qfull = (uint64_t *)(factor + 2 * kTile);   // [2], by tile
   uint64_t *sfull = qfull + 2, *pfull = sfull + 2, *odone = pfull + 2;
   uint64_t *kfull = odone + 2, *kempty = kfull + 2, *vfull = kempty + 2, *vempty = vfull + 2;
-  uint32_t *tmem_slot = (uint32_t *)(vempty + 2);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint64_t *kraw = vempty + 2, *vraw = kraw + 1;
+  uint32_t *tmem_slot = (uint32_t *)(vraw + 1);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
@@ -124,6 +154,8 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       tc::mbar_init(&vfull[b], 4);
       tc::mbar_init(&vempty[b], 1);
     }
+    tc::mbar_init(kraw, 1);
+    tc::mbar_init(vraw, 1);
     tc::mbar_fence_init();
   }
   if (warp == 12) tc::tmem_alloc(tmem_slot, C::kCols);
@@ -138,43 +170,49 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
 
   const PromptPlan plan(g);
   write_empty<T, D>(plan, threadIdx.x, kThreads);
-  const int64_t total = plan.total();
-  const int64_t n = shares(total, 1, gridDim.x);
-  const int64_t u0 = blockIdx.x < n ? share_start(total, n, blockIdx.x) : 0;
-  const int count = blockIdx.x < n ? (int)(share_start(total, n, blockIdx.x + 1) - u0) : 0;
   Cursor at{};
-  if (count > 0) at = cursor_at(plan, u0);
+  const int count = my_share(plan, 1, at);
   bool ok = true;  // false once a wait has given up: the rest passes without waiting
 
   if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 12 && lane == 0) {
-      // ---------------- MMA issuer ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 12) {
+      // ---------------- MMA issuer (the whole warp; one lane issues) ----------------
       constexpr uint32_t id_s = tc::instr_desc(0, 0, kTile, kTile, 0, 0);
       constexpr uint32_t id_o = tc::instr_desc(0, 0, kTile, D, 0, 0);
-      const uint32_t q0 = tc::smem_u32(sq), k0 = tc::smem_u32(sk), v0 = tc::smem_u32(sv);
+      // a descriptor holds its address in units of 16 bytes: offsets are added to it
+      const uint64_t dq = tc::smem_desc_sw128(tc::smem_u32(sq), 16, 1024);
+      const uint64_t dk = tc::smem_desc_sw128(tc::smem_u32(sk), 16, 1024);
+      const uint64_t dv = tc::smem_desc_sw128(tc::smem_u32(sv), 16, 1024);
       auto wait = [&](uint64_t *bar, int phase) {
         if (ok) ok = tc::mbar_wait(bar, phase & 1, st);
+        ok = __all_sync(0xffffffffu, ok);
         tc::tc_fence_after();
       };
+      auto commit = [&](uint64_t *bar) {
+        if (tc::elect_one()) tc::mma_commit(bar);
+      };
       auto scores = [&](int b, int u) {
-        const uint32_t q = q0 + b * C::kQ, k = k0 + (u & 1) * C::kQ;
+        if (tc::elect_one()) {
+          const uint64_t q = dq + b * (C::kQ >> 4), k = dk + (u & 1) * (C::kQ >> 4);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = (uint32_t)(i / 4) * C::kChunk + (i % 4) * 32;
-          tc::mma_f16(tmem + b * kTile, tc::smem_desc_sw128(q + off, 16, 1024),
-                      tc::smem_desc_sw128(k + off, 16, 1024), id_s, i > 0);
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = ((uint32_t)(i / 4) * C::kChunk + (i % 4) * 32) >> 4;
+            tc::mma_f16(tmem + b * kTile, q + off, k + off, id_s, i > 0);
+          }
+          tc::mma_commit(&sfull[b]);
         }
-        tc::mma_commit(&sfull[b]);
       };
       auto outputs = [&](int b, int u, bool first) {
-        const uint32_t v = v0 + (u & 1) * C::kV;
+        if (tc::elect_one()) {
+          const uint64_t v = dv + (u & 1) * (C::kV >> 4);
 #pragma unroll
-        for (int i = 0; i < kTile / 16; ++i)
-          mma_f16_ts(tmem + C::kO + b * D, tmem + b * kTile + 8 * i,
-                     tc::smem_desc_sw128(v + (uint32_t)(i / 4) * C::kVChunk + (i % 4) * 32, 16, 1024),
-                     id_o, !first || i > 0);
-        tc::mma_commit(&odone[b]);
+          for (int i = 0; i < kTile / 16; ++i)
+            mma_f16_ts(tmem + C::kO + b * D, tmem + b * kTile + 8 * i,
+                       v + (((uint32_t)(i / 4) * C::kVChunk + (i % 4) * 32) >> 4), id_o,
+                       !first || i > 0);
+          tc::mma_commit(&odone[b]);
+        }
       };
       int items[2] = {0, 0}, done[2] = {0, 0};  // by tile: items and units it took part in
       for (int i0 = 0; i0 < count && ok;) {
@@ -194,7 +232,7 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
           wait(&qfull[b], items[b]++);
           scores(b, i0);
         }
-        tc::mma_commit(&kempty[i0 & 1]);
+        commit(&kempty[i0 & 1]);
         for (int i = 0; i < m && ok; ++i) {
           const int u = i0 + i;
           wait(&vfull[u & 1], u >> 1);
@@ -207,8 +245,8 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
             ++done[b];
             if (i + 1 < to[b]) scores(b, u + 1);
           }
-          tc::mma_commit(&vempty[u & 1]);
-          if (i + 1 < m) tc::mma_commit(&kempty[(u + 1) & 1]);
+          commit(&vempty[u & 1]);
+          if (i + 1 < m) commit(&kempty[(u + 1) & 1]);
         }
         i0 += m;
         if (i0 < count) at.next_item(plan);
@@ -216,27 +254,30 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
     }
   } else if (warp >= 8) {
     // ---------------- converters ----------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    const int ct = threadIdx.x - 256;
-    // K pieces of 16 codes: four lanes a row of 64, so that eight lanes' stores of 16 bytes fall
-    // into different banks; V pieces: four lanes a channel of 64 tokens
+    // Contiguous copies bring a unit's codes; each thread turns pieces of 16 into fp16, one row
+    // of K (channel of V) in every 32: four lanes take 64 codes of a row, so that eight lanes'
+    // accesses of 16 bytes fall into different banks.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    const int ct = threadIdx.x - 256, x = ct % 4, r0 = ct / 4;
     Cursor c = at;              // of the unit whose blocks are looked up
-    int pages[2], head = 0, len = 0, blk = 0;
+    int pages[2], head = 0, len = 0, blk = 0, entry = -1;
+    const int32_t *row = g.table;
     auto look_up = [&](int u) {
       pages[0] = pages[1] = -1;
       if (u >= count) return;
-      const int seq = c.entry / plan.tiles;
-      const int32_t *row = g.table + seq * g.ld_table;
+      if (c.entry != entry) {
+        entry = c.entry;
+        row = g.table + entry / plan.tiles * g.ld_table;
+        len = seq_length(g, entry / plan.tiles);
+      }
       head = c.head;
-      len = seq_length(g, seq);
       blk = c.blk;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if ((2 * blk + h) * kTok < len) pages[h] = row[2 * blk + h];
       if (u + 1 < count) c.advance(plan, 1);
     };
-    int place[2], ex[2], left;   // of the unit whose codes are on their way
-    uint4 kq[D / 16], vq[D / 16];
+    int place[2], ex[2], left;   // of the unit that is being copied
     auto locate = [&]() {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -246,32 +287,21 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       }
       left = len - blk * kTile;  // tokens of the unit that exist
     };
-    constexpr int kPer = D / 16;          // pieces of K (of V) per thread
-    constexpr int kColsOf = D / 64;       // 64-element chunks of a K row
-    auto load_k = [&]() {
+    auto copy = [&](uint8_t *dst, const uint8_t *src, uint64_t *bar) {
+      if (ct != 0) return;
+      tc::fence_proxy_async_smem();
+      tc::mbar_arrive_expect_tx(bar, (place[0] >= 0 ? C::kHalf : 0) + (place[1] >= 0 ? C::kHalf : 0));
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int piece = ct + 128 * i, x = piece % 4, row = piece / 4 % kTile, ch = piece / (4 * kTile);
-        const int h = row / kTok;
-        kq[i] = place[h] < 0 ? make_uint4(0, 0, 0, 0)
-                             : *reinterpret_cast<const uint4 *>(
-                                   g.k + (int64_t)place[h] * (kTok * D) + (row % kTok) * D + ch * 64 + x * 16);
-      }
+      for (int h = 0; h < 2; ++h)
+        if (place[h] >= 0)
+          tc::bulk_load(dst + h * C::kHalf, src + (int64_t)place[h] * C::kHalf, C::kHalf, bar);
     };
-    auto load_v = [&]() {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int piece = ct + 128 * i, x = piece % 4, d = piece / 4 % D, h = piece / (4 * D);
-        vq[i] = place[h] < 0 ? make_uint4(0, 0, 0, 0)
-                             : *reinterpret_cast<const uint4 *>(
-                                   g.v + (int64_t)place[h] * (kTok * D) + d * kTok + x * 16);
-      }
-    };
-    auto put = [&](uint8_t *chunk, int row, int x, const uint4 &q) {
-      *reinterpret_cast<uint4 *>(chunk + swizzled(row, 2 * x)) =
-          make_uint4(halves(q.x), halves(q.x >> 16), halves(q.y), halves(q.y >> 16));
-      *reinterpret_cast<uint4 *>(chunk + swizzled(row, 2 * x + 1)) =
-          make_uint4(halves(q.z), halves(q.z >> 16), halves(q.w), halves(q.w >> 16));
+    const uint32_t at0 = swizzled(r0, 2 * x), at1 = swizzled(r0, 2 * x + 1);
+    auto put = [&](uint8_t *rows, const uint4 &q) {
+      *reinterpret_cast<uint4 *>(rows + at0) =
+          make_uint4(halves_lo(q.x), halves_hi(q.x), halves_lo(q.y), halves_hi(q.y));
+      *reinterpret_cast<uint4 *>(rows + at1) =
+          make_uint4(halves_lo(q.z), halves_hi(q.z), halves_lo(q.w), halves_hi(q.w));
     };
     auto wait = [&](uint64_t *bar, int phase) {
       if (ok) ok = tc::mbar_wait(bar, phase & 1, st);
@@ -281,18 +311,19 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar);
     };
-    static_assert(kColsOf * 4 * kTile == kPer * 128, "K pieces");
     if (count > 0) {
       look_up(0);
       locate();
-      load_k();
-      load_v();
+      copy(raw_k, g.k, kraw);
+      copy(raw_v, g.v, vraw);
       look_up(1);
     }
-    for (int u = 0; u < count && ok; ++u) {
+    for (int u = 0; u < count; ++u) {
       const int s = u & 1, tokens = left;
       // keys, and what the softmax has to know of the unit (four units back has been read: the
       // keys of two units back were multiplied after the probabilities of three units back)
+      const bool there[2] = {place[0] >= 0, place[1] >= 0};
+      wait(kraw, u);
       if (u >= 2) wait(&kempty[s], (u - 2) >> 1);
       if (ct == 0) {
         Info &f = info[u % kInfo];
@@ -300,36 +331,40 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
         for (int h = 0; h < 2; ++h) {
           f.ks[h] = fp8::exp_value((uint8_t)ex[h]);
           f.lv[h] = (ex[h] >> 8) - fp8::kBias;
-          f.there[h] = place[h] >= 0;
+          f.there[h] = there[h];
         }
       }
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int piece = ct + 128 * i, x = piece % 4, row = piece / 4 % kTile, ch = piece / (4 * kTile);
-        put(sk + s * C::kQ + ch * C::kChunk, row, x, kq[i]);
+      for (int i = 0; i < D / 16; ++i) {  // row r0 + 32 (i % 4); odd rows the other chunk first
+        const int h = i % 4 / 2, ch = D == 128 ? (i / 4) ^ (r0 & 1) : 0;
+        const uint4 q = there[h] ? *reinterpret_cast<const uint4 *>(
+                                       raw_k + (r0 + i % 4 * 32) * D + ch * 64 + x * 16)
+                                 : make_uint4(0, 0, 0, 0);
+        put(sk + s * C::kQ + ch * C::kChunk + i % 4 * 32 * 128, q);
       }
       arrive(&kfull[s]);
-      locate();                 // of the next unit
-      if (u + 1 < count) load_k();
+      tc::named_barrier(1, 128);  // the codes have been read
+      locate();                   // of the next unit
+      if (u + 1 < count) copy(raw_k, g.k, kraw);
       // values; those past the sequence's end may be NaN codes and become zeros
+      wait(vraw, u);
       if (u >= 2) wait(&vempty[s], (u - 2) >> 1);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int piece = ct + 128 * i, x = piece % 4, d = piece / 4 % D, h = piece / (4 * D);
-        const int live = tokens - h * kTok - x * 16;
+      for (int i = 0; i < D / 16; ++i) {  // channel r0 + 32 (i % (D / 32)), block i / (D / 32)
+        const int h = i / (D / 32), d = i % (D / 32) * 32, live = tokens - h * kTok - x * 16;
+        uint4 q = there[h] ? *reinterpret_cast<const uint4 *>(raw_v + h * C::kHalf + (r0 + d) * kTok + x * 16)
+                           : make_uint4(0, 0, 0, 0);
         if (live < 16) {
-          uint32_t e[4] = {vq[i].x, vq[i].y, vq[i].z, vq[i].w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int keep = live - 4 * q;
-            e[q] &= keep <= 0 ? 0u : (keep >= 4 ? ~0u : (1u << (8 * keep)) - 1u);
-          }
-          vq[i] = make_uint4(e[0], e[1], e[2], e[3]);
+          auto mask = [&](int at) {
+            return live <= at ? 0u : (live >= at + 4 ? ~0u : (1u << (8 * (live - at))) - 1u);
+          };
+          q = make_uint4(q.x & mask(0), q.y & mask(4), q.z & mask(8), q.w & mask(12));
         }
-        put(sv + s * C::kV + h * C::kVChunk, d, x, vq[i]);
+        put(sv + s * C::kV + h * C::kVChunk + d * 128, q);
       }
       arrive(&vfull[s]);
-      if (u + 1 < count) load_v();
+      tc::named_barrier(1, 128);
+      if (u + 1 < count) copy(raw_v, g.v, vraw);
       look_up(u + 2);
     }
   } else {
@@ -351,44 +386,46 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       const int len = seq_length(g, seq), r = row0 + row;
       const int nb = (plan.seen(len, row0, row0 + kTile) + kTile - 1) / kTile;
       const int mine = nb - at.blk < m ? (nb - at.blk < 0 ? 0 : nb - at.blk) : m;
-      const int limit = plan.seen(len, r, r + 1);
+      // a row that does not exist is as good as one that sees everything
+      const int limit = r < plan.rows ? plan.seen(len, r, r + 1) : INT_MAX;
       // queries: scaled to a maximum of [1, 2), fp16, K-major
+      // Queries, scaled to a maximum of [1, 2), fp16, K-major: a warp loads its tile's 32 rows with
+      // D / 8 lanes a row, all in flight at once, and leaves each row's factor for its thread.
       float f = 0.0f;
       if (mine > 0) {
-        const bool real = r < plan.rows;
-        const T *q = (const T *)g.q + seq * g.q_stride[0] + (r / plan.group) * g.q_stride[1] +
-                     (int64_t)(at.head * plan.group + r % plan.group) * g.q_stride[2];
-        const bool vec = ((uintptr_t)q & 15) == 0;
-        auto load = [&](int d, float(&v)[8]) {
-          if (!real) {
+        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kLoads = 32 / kAt;  // rows at a time
+        const int sub = lane / kLanes, piece = lane % kLanes;
+        uint4 raw[kLoads];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-          } else if (vec) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(q + d);
-            const T *e = reinterpret_cast<const T *>(&w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = to_f32(e[j]);
+        for (int i = 0; i < kLoads; ++i) {
+          const int rr = row0 + warp % 4 * 32 + i * kAt + sub;
+          const T *q = (const T *)g.q + seq * g.q_stride[0] + (rr / plan.group) * g.q_stride[1] +
+                       (int64_t)(at.head * plan.group + rr % plan.group) * g.q_stride[2] + 8 * piece;
+          if (rr >= plan.rows) {
+            raw[i] = make_uint4(0, 0, 0, 0);
+          } else if (g.vec_q) {
+            raw[i] = *reinterpret_cast<const uint4 *>(q);
           } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = to_f32(q[d + j]);
+            const uint16_t *e = reinterpret_cast<const uint16_t *>(q);
+            raw[i] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
+                                e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
           }
-        };
-        float amax = 0.0f;
-#pragma unroll
-        for (int d = 0; d < D; d += 8) {
-          float v[8];
-          load(d, v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fp8::finite_abs(v[j]));
         }
-        const int e = row_exponent(amax);
-        const float inv = g.scale < 0.0f ? -fp8::pow2(-e) : fp8::pow2(-e);
-        f = fp8::pow2(e) * fabsf(g.scale) * kLog2e;
 #pragma unroll
-        for (int d = 0; d < D; d += 8) {
-          float v[8];
-          load(d, v);
-          *reinterpret_cast<uint4 *>(q_tile + d / 64 * C::kChunk + swizzled(row, d % 64 / 8)) =
+        for (int i = 0; i < kLoads; ++i) {
+          float v[8], amax = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            v[j] = to_f32(reinterpret_cast<const T *>(&raw[i])[j]);
+            amax = fmaxf(amax, fp8::finite_abs(v[j]));
+          }
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const int e = row_exponent(amax), mr = warp % 4 * 32 + i * kAt + sub;
+          const float inv = g.scale < 0.0f ? -fp8::pow2(-e) : fp8::pow2(-e);
+          if (piece == 0) factor[b * kTile + mr] = fp8::pow2(e) * fabsf(g.scale) * kLog2e;
+          *reinterpret_cast<uint4 *>(q_tile + piece / 8 * C::kChunk + swizzled(mr, piece % 8)) =
               make_uint4(pack_half2(v[0] * inv, v[1] * inv), pack_half2(v[2] * inv, v[3] * inv),
                          pack_half2(v[4] * inv, v[5] * inv), pack_half2(v[6] * inv, v[7] * inv));
         }
@@ -396,69 +433,83 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
         tc::tc_fence_before();  // O of the item before has been read
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&qfull[b]);
+        f = factor[b * kTile + row];
       }
       float base = -INFINITY, l = 0.0f;  // the exponent that p is taken from; sum of p 2^-lv
       for (int i = 0; i < mine && ok; ++i) {
         wait(&sfull[b], seen_s++);
-        const Info in = info[(i0 + i) % kInfo];
+        const Info &in = info[(i0 + i) % kInfo];
+        const int tok = (at.blk + i) * kTile;
+        const int there = in.there[0] | in.there[1] << 1;
+        const bool cut = !__all_sync(0xffffffffu, tok + kTile <= limit) || there != 3;
         uint32_t s[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::tmem_ld32(ts + 32 * c, s[c]);
         tc::tmem_ld_wait();
-        const int tok = (at.blk + i) * kTile;
-        // a factor of 0 would turn the masked -inf into NaN
-        const float fk[2] = {fmaxf(f * in.ks[0], 1e-37f), fmaxf(f * in.ks[1], 1e-37f)};
-        if (!__all_sync(0xffffffffu, tok + kTile <= limit) || !in.there[0] || !in.there[1]) {
+        if (cut) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const int seen = (there >> (c / 2)) & 1 ? limit - tok - 32 * c : 0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (tok + 32 * c + j >= limit || !in.there[c / 2]) s[c][j] = 0xFF800000u;
+            for (int j = 0; j < 32; ++j) s[c][j] = j < seen ? s[c][j] : 0xFF800000u;
+          }
         }
-        float mx[2];
+        float top = -INFINITY, fk[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float a0 = -INFINITY, a1 = -INFINITY;
+          float a[4];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            a0 = fmaxf(a0, __uint_as_float(s[2 * h][j]));
-            a1 = fmaxf(a1, __uint_as_float(s[2 * h + 1][j]));
-          }
-          mx[h] = fmaf(fmaxf(a0, a1), fk[h], (float)in.lv[h]);
+          for (int q = 0; q < 4; ++q) a[q] = __uint_as_float(s[2 * h + q / 2][q % 2 * 16]);
+#pragma unroll
+          for (int j = 1; j < 15; j += 2)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              a[q] = max3(a[q], __uint_as_float(s[2 * h + q / 2][q % 2 * 16 + j]),
+                          __uint_as_float(s[2 * h + q / 2][q % 2 * 16 + j + 1]));
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            a[q] = fmaxf(a[q], __uint_as_float(s[2 * h + q / 2][q % 2 * 16 + 15]));
+          // a factor of 0 would turn the masked -inf into NaN
+          fk[h] = fmaxf(f * in.ks[h], 1e-37f);
+          top = fmaxf(top, fmaf(fmaxf(max3(a[0], a[1], a[2]), a[3]), fk[h], (float)in.lv[h]));
         }
-        const float top = fmaxf(mx[0], mx[1]);
         const bool raise = top > base + kLazy || (base == -INFINITY && top > base);
         if (i > 0 && __any_sync(0xffffffffu, raise)) {
           const float shrink = raise ? ex2(base - top) : 1.0f;
           l *= shrink;
           wait(&odone[b], seen_o + i - 1);
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tc::tmem_ld32(to + c, o);
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + c, o);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * shrink);
-            tmem_st32(to + c, o);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * shrink);
+            tmem_st16(to + c, o);
           }
         }
         if (raise) base = top;
-        const float ref = base == -INFINITY ? 0.0f : base;
+        const float ref = (base == -INFINITY ? 0.0f : base) - 8.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float off = (float)in.lv[h] - ref + 8.0f;
-          float sum0 = 0.0f, sum1 = 0.0f;
-          uint32_t w[32];
+          const float off = (float)in.lv[h] - ref;
+          const float2 fk2 = make_float2(fk[h], fk[h]), off2 = make_float2(off, off);
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float p0 = ex2(fmaf(__uint_as_float(s[2 * h + j / 16][2 * (j % 16)]), fk[h], off));
-            const float p1 = ex2(fmaf(__uint_as_float(s[2 * h + j / 16][2 * (j % 16) + 1]), fk[h], off));
-            sum0 += p0;
-            sum1 += p1;
-            w[j] = pack_half2(p0, p1);
+          for (int c = 2 * h; c < 2 * h + 2; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float2 y = fma2(make_float2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1])),
+                              fk2, off2);
+              y = make_float2(ex2(y.x), ex2(y.y));
+              sum[j % 2] = add2(sum[j % 2], y);
+              w[j] = pack_half2(y.x, y.y);
+            }
+            tmem_st16(ts + 16 * c, w);
           }
-          tmem_st32(ts + 32 * h, w);
-          l = fmaf((sum0 + sum1) * 0x1p-8f, fp8::pow2(-in.lv[h]), l);
+          sum[0] = add2(sum[0], sum[1]);
+          l = fmaf((sum[0].x + sum[0].y) * 0x1p-8f, fp8::pow2(-in.lv[h]), l);
         }
         tmem_st_wait();
         tc::tc_fence_before();
@@ -471,10 +522,6 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       const bool whole = at.blk == 0 && m == at.nblk;
       float *piece = part + (2 * (int64_t)blockIdx.x + (i0 > 0 ? 1 : 0)) * kPiece<PromptPlan, D>;
       const float inv = whole ? (l == 0.0f ? 0.0f : 0x1p-8f / l) : 0x1p-8f;
-      const bool real = r < plan.rows;
-      T *o = out_row<T>(g, plan.group, seq, at.head, real ? r : 0);
-      const bool vec = ((uintptr_t)o & 15) == 0;
-      float *po = piece + (b * kTile + row) * D;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t x[32];
@@ -482,28 +529,46 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
           tc::tmem_ld32(to + c, x);
           tc::tmem_ld_wait();
         }
-        if (!real) continue;
-        float y[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) y[j] = mine > 0 ? __uint_as_float(x[j]) * inv : 0.0f;
-        if (!whole) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4 *>(po + c + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-        } else if (vec) {
+        for (int j = 0; j < 32; ++j)
+          x[j] = mine > 0 ? __float_as_uint(__uint_as_float(x[j]) * inv) : 0u;
+        if (whole) {
+          // through the tile of queries, whose products are done: rows of 2 D bytes
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
             alignas(16) T e[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) e[q] = from_f32<T>(y[j + q]);
-            *reinterpret_cast<uint4 *>(o + c + j) = *reinterpret_cast<const uint4 *>(e);
+            for (int q = 0; q < 8; ++q) e[q] = from_f32<T>(__uint_as_float(x[j + q]));
+            const int u = (c + j) / 8;
+            *reinterpret_cast<uint4 *>(q_tile + u / 8 * C::kChunk + swizzled(row, u % 8)) =
+                *reinterpret_cast<const uint4 *>(e);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[c + j] = from_f32<T>(y[j]);
+          for (int j = 0; j < 32; j += 4)
+            reinterpret_cast<uint4 *>(piece)[(c + j) / 4 * 2 * kTile + b * kTile + row] =
+                make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
         }
       }
-      if (!whole && real) {
+      if (whole) {
+        __syncwarp();  // a warp's rows are its own
+        constexpr int kLanes = D / 8, kAt = 32 / kLanes;
+        const int sub = lane / kLanes, u = lane % kLanes;
+#pragma unroll 4
+        for (int i = 0; i < 32; i += kAt) {
+          const int mr = warp % 4 * 32 + i + sub, rr = row0 + mr;
+          if (rr >= plan.rows) continue;
+          const uint4 w = *reinterpret_cast<const uint4 *>(q_tile + u / 8 * C::kChunk + swizzled(mr, u % 8));
+          T *o = out_row<T>(g, plan.group, seq, at.head, rr) + 8 * u;
+          if (g.vec_o) {
+            *reinterpret_cast<uint4 *>(o) = w;
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = reinterpret_cast<const T *>(&w)[q];
+          }
+        }
+        __syncwarp();
+      } else {
         piece[2 * kTile * D + b * kTile + row] = base;
         piece[2 * kTile * (D + 1) + b * kTile + row] = l;
       }
@@ -537,8 +602,9 @@ size_t kv8_prompt_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int 
                            int max_blocks) {
   int64_t ctas = kMaxCtas;
   const int64_t rows = n_new * (n_heads / n_kv);
-  const int64_t units = ceil_div(rows, 2 * kTile) * n_seq * n_kv * ceil_div(max_blocks, 2);
-  if (units < ctas) ctas = units;
+  const int64_t weight = ceil_div(rows, 2 * kTile) * n_seq * n_kv *
+                         (ceil_div(max_blocks, 2) + PromptPlan::kSetup);
+  if (weight < ctas) ctas = weight;
   return 256 + (size_t)(2 * ctas) * (2 * kTile) * (dim + 2) * 4;
 }
 

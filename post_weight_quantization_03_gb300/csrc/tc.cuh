@@ -27,6 +27,19 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
 
+// Whole warp, converged: true in one lane, the same one every time.  A loop that the whole warp
+// runs and that issues its MMAs under this predicate keeps descriptors and addresses in uniform
+// registers, where the MMA wants them; one that only lane 0 enters moves them there for each MMA.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // ---------------------------------------------------------------------------------------
 // mbarrier
 // ---------------------------------------------------------------------------------------
