@@ -93,27 +93,28 @@ struct Plan {
     const int seq = entry / tiles, row0 = entry % tiles * ROWS;
     return (seen(seq_length(g, seq), row0, row0 + ROWS) + UNIT - 1) / UNIT;
   }
-  // Whole warp: the weight of all items.
-  __device__ __forceinline__ int64_t total() const {
-    int64_t s = 0;
+  // Whole warp: the weight of all items (the launch has checked that it fits 31 bits), or their
+  // units.
+  __device__ __forceinline__ int total(int setup = SETUP) const {
+    int s = 0;
+#pragma unroll 1
     for (int i = threadIdx.x % 32; i < entries; i += 32) {
       const int n = units(i);
-      s += n > 0 ? n + SETUP : 0;
+      s += n > 0 ? n + setup : 0;
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s * g.n_kv;
+    return __reduce_add_sync(0xffffffffu, s) * g.n_kv;
   }
 };
 
 // The CTAs that share the weight `total`, `turn` units of it at a time at least, and where share
 // w starts.
-__device__ __forceinline__ int64_t shares(int64_t total, int turn, int64_t ctas) {
-  const int64_t n = (total + turn - 1) / turn;
+__device__ __forceinline__ int shares(int total, int turn, int ctas) {
+  const int n = total / turn + (total % turn != 0 ? 1 : 0);
   return n < ctas ? n : ctas;
 }
-__device__ __forceinline__ int64_t share_start(int64_t total, int64_t n, int64_t w) {
-  return total * w / n;
+__device__ __forceinline__ int share_start(int total, int n, int w) {
+  const int q = total / n, r = total % n;
+  return q * w + (w < r ? w : r);
 }
 
 // A unit: step `blk` of the `nblk` of an item.
@@ -124,50 +125,54 @@ struct Cursor {
     blk = 0;
     if (++head < p.g.n_kv) return;
     head = 0;
+#pragma unroll 1
     do ++entry; while (entry < p.entries && (nblk = p.units(entry)) == 0);
   }
   template <typename P>
   __device__ __forceinline__ void advance(const P &p, int by) {
+#pragma unroll 1
     while (blk + by >= nblk && entry < p.entries) {
       by -= nblk - blk;
       next_item(p);
     }
     blk += by;
   }
+  template <typename P>
+  __device__ __forceinline__ void step(const P &p) {
+    if (++blk >= nblk) next_item(p);
+  }
 };
 
 // Whole warp: the cursor at weight v (0 <= v < total), the units before it and, in `start`, the
 // weight at which its item starts.
 template <typename P>
-__device__ __forceinline__ Cursor cursor_at(const P &p, int64_t v, int64_t &unit, int64_t &start) {
-  const int lane = threadIdx.x % 32;
+__device__ __forceinline__ Cursor cursor_at(const P &p, int v, int &unit, int &start) {
+  const int lane = threadIdx.x % 32, kv = p.g.n_kv;
   unit = start = 0;
+#pragma unroll 1
   for (int s0 = 0;; s0 += 32) {
     const int nb = s0 + lane < p.entries ? p.units(s0 + lane) : 0;
-    int64_t incl = nb > 0 ? (int64_t)(nb + P::kSetup) * p.g.n_kv : 0, units = (int64_t)nb * p.g.n_kv;
-#pragma unroll
+    int incl = nb > 0 ? (nb + P::kSetup) * kv : 0, units = nb * kv;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t a = __shfl_up_sync(0xffffffffu, incl, o), b = __shfl_up_sync(0xffffffffu, units, o);
+      const int a = __shfl_up_sync(0xffffffffu, incl, o), b = __shfl_up_sync(0xffffffffu, units, o);
       if (lane >= o) {
         incl += a;
         units += b;
       }
     }
     const unsigned past = __ballot_sync(0xffffffffu, start + incl > v);
-    if (past == 0) {
-      start += __shfl_sync(0xffffffffu, incl, 31);
-      unit += __shfl_sync(0xffffffffu, units, 31);
-      continue;
-    }
-    const int src = __ffs(past) - 1;
+    const int src = past ? __ffs(past) - 1 : 31;
+    start += __shfl_sync(0xffffffffu, incl, src);
+    unit += __shfl_sync(0xffffffffu, units, src);
+    if (past == 0) continue;
     const int n = __shfl_sync(0xffffffffu, nb, src), weight = n + P::kSetup;
-    start += __shfl_sync(0xffffffffu, incl, src) - (int64_t)weight * p.g.n_kv;
-    unit += __shfl_sync(0xffffffffu, units, src) - (int64_t)n * p.g.n_kv;
-    const int head = (int)((v - start) / weight);
-    start += (int64_t)head * weight;
-    const int at = (int)(v - start) - P::kSetup;
-    Cursor c{s0 + src, head, at < 0 ? 0 : at, n};
-    unit += (int64_t)head * n + c.blk;
+    start -= weight * kv;
+    const int head = (v - start) / weight;
+    start += head * weight;
+    const int at = v - start - P::kSetup;
+    const Cursor c{s0 + src, head, at < 0 ? 0 : at, n};
+    unit += (head - kv) * n + c.blk;
     return c;
   }
 }
@@ -175,21 +180,28 @@ __device__ __forceinline__ Cursor cursor_at(const P &p, int64_t v, int64_t &unit
 // Whole warp: this CTA's share, as its first unit's cursor and the number of its units.
 template <typename P>
 __device__ __forceinline__ int my_share(const P &p, int turn, Cursor &first) {
-  const int64_t total = p.total(), n = shares(total, turn, gridDim.x);
-  if (blockIdx.x >= n) return 0;
-  const int64_t v0 = share_start(total, n, blockIdx.x), v1 = share_start(total, n, blockIdx.x + 1);
-  int64_t u0, u1, start;
-  if (v1 < total) cursor_at(p, v1, u1, start);
-  const Cursor c = cursor_at(p, v0, u0, start);
-  first = c;
-  if (v1 == total) {  // all items weigh their units and the same setup: what is left of them
-    int64_t s = 0;
-    for (int i = threadIdx.x % 32; i < p.entries; i += 32) s += p.units(i);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    u1 = s * p.g.n_kv;
+  const int total = p.total(), n = shares(total, turn, gridDim.x);
+  if ((int)blockIdx.x >= n) return 0;
+  if constexpr (P::kSetup == 0) {  // weights are units
+    const int v = share_start(total, n, blockIdx.x);
+    int unit, start;
+    first = cursor_at(p, v, unit, start);
+    return share_start(total, n, blockIdx.x + 1) - v;
   }
-  return (int)(u1 - u0);
+  int u0 = 0, u1 = 0;
+#pragma unroll 1
+  for (int end = 0; end < 2; ++end) {  // one copy of the search for the share's two ends
+    const int v = share_start(total, n, blockIdx.x + end);
+    int start;
+    u0 = u1;
+    if (v == total) {
+      u1 = p.total(0);
+    } else {
+      const Cursor c = cursor_at(p, v, u1, start);
+      if (end == 0) first = c;
+    }
+  }
+  return u1 - u0;
 }
 
 // Where row `row` of a sequence's head goes.
@@ -204,9 +216,11 @@ __device__ __forceinline__ T *out_row(const Kv8AttentionArgs &g, int group, int 
 // CTAs taking the entries in turn.
 template <typename T, int D, typename P>
 __device__ __forceinline__ void write_empty(const P &p, int thread, int threads) {
+#pragma unroll 1
   for (int e = blockIdx.x; e < p.entries; e += gridDim.x) {
     if (p.units(e) > 0) continue;
     const int row0 = e % p.tiles * P::kRows, n = min(P::kRows, p.rows - row0);
+#pragma unroll 1
     for (int i = thread; i < n * p.g.n_kv * D; i += threads)
       out_row<T>(p.g, p.group, e / p.tiles, i / D % p.g.n_kv, row0 + i / D / p.g.n_kv)[i % D] =
           from_f32<T>(0.0f);
@@ -216,65 +230,90 @@ __device__ __forceinline__ void write_empty(const P &p, int thread, int threads)
 template <typename P, int D>
 constexpr int kPiece = P::kRows *(D + 2);  // floats of a piece: acc [D / 4][rows][4], m, l
 
-// Joins the pieces of the items that the start of share w cuts, w = blockIdx.x + 1, for every
-// gridDim.y-th row: out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i.  It starts while the
-// kernel before runs (which has waited for all before it, so the lengths are there) and waits
-// for it where it reads the pieces; it waits also where there is nothing to join, since its end
-// has to mean that the other's came.
+// Joins the pieces of the items that the start of share w cuts, w = blockIdx.x + 1, for 32 rows:
+// out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i.  A lane is a row (pieces keep the rows
+// next to each other), a warp every fourth group of four channels; the rows leave through shared
+// memory.  The kernel starts while the one before runs (which has waited for all before it, so
+// the lengths are there) and waits for it where it reads the pieces; it waits also where there
+// is nothing to join, since its end has to mean that the other's came.
 template <typename T, int D, typename P>
 __global__ void __launch_bounds__(128)
-join_kernel(Kv8AttentionArgs g, const float *part, int turn, int64_t ctas) {
+join_kernel(Kv8AttentionArgs g, const float *part, int turn, int ctas) {
   const P p(g);
-  const int64_t total = p.total(), n = shares(total, turn, ctas);
-  const int64_t w = (int64_t)blockIdx.x + 1;
+  const int total = p.total(), n = shares(total, turn, ctas);
+  const int w = blockIdx.x + 1;
   bool cut = w < n;
   Cursor at{};
-  int64_t last = w;
+  int last = w;
   bool late = false;
   if (cut) {
-    int64_t unit, first;
-    const int64_t v = share_start(total, n, w), before = share_start(total, n, w - 1);
+    int unit, first;
+    const int v = share_start(total, n, w), before = share_start(total, n, w - 1);
     at = cursor_at(p, v, unit, first);
     // a later start in the same item leaves it to the first
     cut = at.blk > 0 && before <= first + P::kSetup;
     late = before < first;
+#pragma unroll 1
     while (last + 1 < n && share_start(total, n, last + 1) < first + P::kSetup + at.nblk) ++last;
   }
   wait_for_grids();
   if (!cut) return;
   const int seq = at.entry / p.tiles, row0 = at.entry % p.tiles * P::kRows;
-  const int rows = min(P::kRows, p.rows - row0);
-  const float *p0 = part + (2 * (w - 1) + (late ? 1 : 0)) * kPiece<P, D>;
-  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < P::kRows * (D / 4); e += gridDim.y * blockDim.x) {
-    const int row = e % P::kRows, c = e / P::kRows;
-    if (row >= rows) continue;
-    float m = -INFINITY, l = 0.0f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float *q = p0;
-#pragma unroll 4
-    for (int64_t i = w - 1; i <= last; ++i) {
-      m = fmaxf(m, q[P::kRows * D + row]);
-      q = part + 2 * (i + 1) * kPiece<P, D>;
+  const int rows = min(P::kRows, p.rows - row0), tile = blockIdx.y * 32;
+  if (tile >= rows) return;
+  constexpr int kGroups = D / 16;                 // groups of four channels of a thread
+  __shared__ alignas(16) T stage[32][D + 8];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, row = tile + lane;
+  const float *p0 = part + (int64_t)(2 * (w - 1) + (late ? 1 : 0)) * kPiece<P, D>;
+  float m = -INFINITY, l = 0.0f;
+  const float *q = p0;
+#pragma unroll 2
+  for (int i = w - 1; i <= last; ++i) {
+    m = fmaxf(m, q[P::kRows * D + row]);
+    q = part + (int64_t)(2 * (i + 1)) * kPiece<P, D>;
+  }
+  if (m == -INFINITY) m = 0.0f;
+  float4 a[kGroups];
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  q = p0;
+#pragma unroll 1
+  for (int i = w - 1; i <= last; ++i) {
+    float4 v[kGroups];
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k)
+      v[k] = reinterpret_cast<const float4 *>(q)[(warp + 4 * k) * P::kRows + row];
+    const float sc = ex2(q[P::kRows * D + row] - m);
+    l = fmaf(q[P::kRows * (D + 1) + row], sc, l);
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      a[k].x = fmaf(v[k].x, sc, a[k].x);
+      a[k].y = fmaf(v[k].y, sc, a[k].y);
+      a[k].z = fmaf(v[k].z, sc, a[k].z);
+      a[k].w = fmaf(v[k].w, sc, a[k].w);
     }
-    if (m == -INFINITY) m = 0.0f;
-    q = p0;
-#pragma unroll 4
-    for (int64_t i = w - 1; i <= last; ++i) {
-      const float sc = ex2(q[P::kRows * D + row] - m);
-      const float4 v = reinterpret_cast<const float4 *>(q)[e];
-      l = fmaf(q[P::kRows * (D + 1) + row], sc, l);
-      a.x = fmaf(v.x, sc, a.x);
-      a.y = fmaf(v.y, sc, a.y);
-      a.z = fmaf(v.z, sc, a.z);
-      a.w = fmaf(v.w, sc, a.w);
-      q = part + 2 * (i + 1) * kPiece<P, D>;
+    q = part + (int64_t)(2 * (i + 1)) * kPiece<P, D>;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) {
+    T *o = &stage[lane][4 * (warp + 4 * k)];
+    o[0] = from_f32<T>(a[k].x * inv);
+    o[1] = from_f32<T>(a[k].y * inv);
+    o[2] = from_f32<T>(a[k].z * inv);
+    o[3] = from_f32<T>(a[k].w * inv);
+  }
+  __syncthreads();
+  constexpr int kLanes = D / 8;
+#pragma unroll 1
+  for (int r = threadIdx.x / kLanes; r < 32 && tile + r < rows; r += 128 / kLanes) {
+    const int c = threadIdx.x % kLanes * 8;
+    T *o = out_row<T>(g, p.group, seq, at.head, row0 + tile + r) + c;
+    if (g.vec_o) {
+      *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(&stage[r][c]);
+    } else {
+      for (int j = 0; j < 8; ++j) o[j] = stage[r][c + j];
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    T *o = out_row<T>(g, p.group, seq, at.head, row0 + row) + 4 * c;
-    o[0] = from_f32<T>(a.x * inv);
-    o[1] = from_f32<T>(a.y * inv);
-    o[2] = from_f32<T>(a.z * inv);
-    o[3] = from_f32<T>(a.w * inv);
   }
 }
 
@@ -299,6 +338,13 @@ gptq_status launch_early(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t s
 }
 
 }  // namespace kv8
+
+// What the kernels' 31-bit unit counts take; `rows` rows in tiles of `tile`, units of `blocks` blocks.
+static inline bool kv8_plan_fits(const Kv8AttentionArgs &g, int64_t tile, int64_t blocks, int64_t setup) {
+  const int64_t rows = g.n_new * (g.n_heads / g.n_kv), tiles = ceil_div(rows, tile);
+  return rows < INT32_MAX / 2 &&
+         (double)tiles * g.n_seq * g.n_kv * (double)(ceil_div(g.max_blocks, blocks) + setup) < INT32_MAX / 2;
+}
 
 // kv8_prompt.cu: many queries (prompts), on the tensor cores.
 size_t kv8_prompt_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int dim,

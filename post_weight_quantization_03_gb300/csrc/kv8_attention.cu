@@ -255,7 +255,7 @@ decode_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
   int hn = 0;        // halves used
   bool ok = true;    // false once a wait has given up: the rest is skipped
   auto arrived = [&]() {
-    if (ok) ok = tc::mbar_wait(&full[hn % H], (hn / H) & 1, st);
+    if (ok) ok = tc::mbar_wait_compact(&full[hn % H], (hn / H) & 1, st);
     ok = __all_sync(0xffffffffu, ok);
   };
   auto release = [&]() {
@@ -428,6 +428,7 @@ decode_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
 template <typename T, int D>
 gptq_status run_decode(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   using C = Decode<D>;
+  if (!kv8_plan_fits(g, kRows, 1, 0)) return GPTQ_ERR_UNSUPPORTED;
   const int64_t rows = g.n_new * (g.n_heads / g.n_kv);
   const int rt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
   const auto kernel = rt == 1 ? decode_kernel<T, D, 1>
@@ -439,9 +440,8 @@ gptq_status run_decode(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   float *part = (float *)((char *)ws + 256);
   GPTQ_TRY(launch_early(kernel, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, s, g, part,
                         (DevStatus *)ws));
-  // a row of pieces is one thread's for each four channels; the rows that exist are the first
-  return launch_early(join_kernel<T, D, DecodePlan>, dim3((unsigned)ctas - 1, D / 16), dim3(128), 0,
-                      s, g, (const float *)part, kWarps / rt, (int64_t)ctas);
+  return launch_early(join_kernel<T, D, DecodePlan>, dim3((unsigned)ctas - 1), dim3(128), 0, s, g,
+                      (const float *)part, kWarps / rt, ctas);
 }
 
 }  // namespace

@@ -185,7 +185,7 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       const uint64_t dk = tc::smem_desc_sw128(tc::smem_u32(sk), 16, 1024);
       const uint64_t dv = tc::smem_desc_sw128(tc::smem_u32(sv), 16, 1024);
       auto wait = [&](uint64_t *bar, int phase) {
-        if (ok) ok = tc::mbar_wait(bar, phase & 1, st);
+        if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, st);
         ok = __all_sync(0xffffffffu, ok);
         tc::tc_fence_after();
       };
@@ -214,38 +214,37 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
           tc::mma_commit(&odone[b]);
         }
       };
-      int items[2] = {0, 0}, done[2] = {0, 0};  // by tile: items and units it took part in
+      // by tile: the items that it took part in, and the units multiplied
+      int items0 = 0, items1 = 0, done0 = 0, done1 = 0;
+#pragma unroll 1
       for (int i0 = 0; i0 < count && ok;) {
         const int m = at.nblk - at.blk < count - i0 ? at.nblk - at.blk : count - i0;
         const int len = seq_length(g, at.entry / plan.tiles), row0 = at.entry % plan.tiles * 2 * kTile;
         // units of this item, counted from the share's first one, that each tile takes part in
-        int to[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        auto part_of = [&](int b) {
           const int nb = (plan.seen(len, row0 + b * kTile, row0 + (b + 1) * kTile) + kTile - 1) / kTile;
-          to[b] = nb - at.blk < m ? (nb - at.blk < 0 ? 0 : nb - at.blk) : m;
-        }
-        wait(&kfull[i0 & 1], i0 >> 1);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (to[b] == 0) continue;
-          wait(&qfull[b], items[b]++);
-          scores(b, i0);
-        }
-        commit(&kempty[i0 & 1]);
-        for (int i = 0; i < m && ok; ++i) {
+          return nb - at.blk < m ? (nb - at.blk < 0 ? 0 : nb - at.blk) : m;
+        };
+        const int to0 = part_of(0), to1 = part_of(1);
+        // step i: the outputs of unit i, then the scores of unit i + 1
+#pragma unroll 1
+        for (int i = -1; i < m && ok; ++i) {
           const int u = i0 + i;
-          wait(&vfull[u & 1], u >> 1);
+          if (i >= 0) wait(&vfull[u & 1], u >> 1);
           if (i + 1 < m) wait(&kfull[(u + 1) & 1], (u + 1) >> 1);
-#pragma unroll
+#pragma unroll 1
           for (int b = 0; b < 2; ++b) {
-            if (i >= to[b]) continue;
-            wait(&pfull[b], done[b]);
-            outputs(b, u, i == 0);
-            ++done[b];
-            if (i + 1 < to[b]) scores(b, u + 1);
+            const int to = b ? to1 : to0;
+            if (i >= to || to == 0) continue;
+            if (i < 0) {
+              wait(&qfull[b], b ? items1++ : items0++);
+            } else {
+              wait(&pfull[b], b ? done1++ : done0++);
+              outputs(b, u, i == 0);
+            }
+            if (i + 1 < to) scores(b, u + 1);
           }
-          commit(&vempty[u & 1]);
+          if (i >= 0) commit(&vempty[u & 1]);
           if (i + 1 < m) commit(&kempty[(u + 1) & 1]);
         }
         i0 += m;
@@ -275,9 +274,9 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if ((2 * blk + h) * kTok < len) pages[h] = row[2 * blk + h];
-      if (u + 1 < count) c.advance(plan, 1);
+      if (u + 1 < count) c.step(plan);
     };
-    int place[2], ex[2], left;   // of the unit that is being copied
+    int place[2] = {-1, -1}, ex[2], left = 0;   // of the unit that is being copied
     auto locate = [&]() {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -304,25 +303,21 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
           make_uint4(halves_lo(q.z), halves_hi(q.z), halves_lo(q.w), halves_hi(q.w));
     };
     auto wait = [&](uint64_t *bar, int phase) {
-      if (ok) ok = tc::mbar_wait(bar, phase & 1, st);
+      if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, st);
     };
     auto arrive = [&](uint64_t *bar) {
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar);
     };
-    if (count > 0) {
-      look_up(0);
-      locate();
-      copy(raw_k, g.k, kraw);
-      copy(raw_v, g.v, vraw);
-      look_up(1);
-    }
-    for (int u = 0; u < count; ++u) {
+    // step u: convert unit u, have unit u + 1 copied, look unit u + 2 up
+#pragma unroll 1
+    for (int u = count > 0 ? -2 : 0; u < count; ++u) {
       const int s = u & 1, tokens = left;
+      const int there = (place[0] >= 0 ? 1 : 0) | (place[1] >= 0 ? 2 : 0);
+      if (u >= 0) {
       // keys, and what the softmax has to know of the unit (four units back has been read: the
       // keys of two units back were multiplied after the probabilities of three units back)
-      const bool there[2] = {place[0] >= 0, place[1] >= 0};
       wait(kraw, u);
       if (u >= 2) wait(&kempty[s], (u - 2) >> 1);
       if (ct == 0) {
@@ -331,40 +326,61 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
         for (int h = 0; h < 2; ++h) {
           f.ks[h] = fp8::exp_value((uint8_t)ex[h]);
           f.lv[h] = (ex[h] >> 8) - fp8::kBias;
-          f.there[h] = there[h];
+          f.there[h] = there >> h & 1;
         }
       }
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {       // block; its rows r0 + 32 i, odd rows the other chunk first
+        uint4 q[D / 32];
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {  // row r0 + 32 (i % 4); odd rows the other chunk first
-        const int h = i % 4 / 2, ch = D == 128 ? (i / 4) ^ (r0 & 1) : 0;
-        const uint4 q = there[h] ? *reinterpret_cast<const uint4 *>(
-                                       raw_k + (r0 + i % 4 * 32) * D + ch * 64 + x * 16)
-                                 : make_uint4(0, 0, 0, 0);
-        put(sk + s * C::kQ + ch * C::kChunk + i % 4 * 32 * 128, q);
+        for (int i = 0; i < D / 32; ++i) {
+          const int ch = D == 128 ? (i / 2) ^ (r0 & 1) : 0;
+          q[i] = there >> h & 1 ? *reinterpret_cast<const uint4 *>(
+                                      raw_k + h * C::kHalf + (r0 + i % 2 * 32) * D + ch * 64 + x * 16)
+                                : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const int ch = D == 128 ? (i / 2) ^ (r0 & 1) : 0;
+          put(sk + s * C::kQ + ch * C::kChunk + (h * kTok + i % 2 * 32) * 128, q[i]);
+        }
       }
       arrive(&kfull[s]);
       tc::named_barrier(1, 128);  // the codes have been read
-      locate();                   // of the next unit
-      if (u + 1 < count) copy(raw_k, g.k, kraw);
+      }
+      if (u >= -1) {
+        locate();                 // of the next unit
+        if (u + 1 < count) copy(raw_k, g.k, kraw);
+      }
+      if (u >= 0) {
       // values; those past the sequence's end may be NaN codes and become zeros
       wait(vraw, u);
       if (u >= 2) wait(&vempty[s], (u - 2) >> 1);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {       // block; its channels r0 + 32 i
+        const int live = tokens - h * kTok - x * 16;
+        uint4 q[D / 32];
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {  // channel r0 + 32 (i % (D / 32)), block i / (D / 32)
-        const int h = i / (D / 32), d = i % (D / 32) * 32, live = tokens - h * kTok - x * 16;
-        uint4 q = there[h] ? *reinterpret_cast<const uint4 *>(raw_v + h * C::kHalf + (r0 + d) * kTok + x * 16)
-                           : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < D / 32; ++i)
+          q[i] = there >> h & 1 ? *reinterpret_cast<const uint4 *>(raw_v + h * C::kHalf +
+                                                                   (r0 + i * 32) * kTok + x * 16)
+                                : make_uint4(0, 0, 0, 0);
         if (live < 16) {
           auto mask = [&](int at) {
             return live <= at ? 0u : (live >= at + 4 ? ~0u : (1u << (8 * (live - at))) - 1u);
           };
-          q = make_uint4(q.x & mask(0), q.y & mask(4), q.z & mask(8), q.w & mask(12));
+          const uint4 m = make_uint4(mask(0), mask(4), mask(8), mask(12));
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            q[i] = make_uint4(q[i].x & m.x, q[i].y & m.y, q[i].z & m.z, q[i].w & m.w);
         }
-        put(sv + s * C::kV + h * C::kVChunk + d * 128, q);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) put(sv + s * C::kV + h * C::kVChunk + i * 32 * 128, q[i]);
       }
       arrive(&vfull[s]);
       tc::named_barrier(1, 128);
-      if (u + 1 < count) copy(raw_v, g.v, vraw);
+      }
+      if (u >= -1 && u + 1 < count) copy(raw_v, g.v, vraw);
       look_up(u + 2);
     }
   } else {
@@ -376,7 +392,7 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
     uint8_t *q_tile = sq + b * C::kQ;
     int seen_s = 0, seen_o = 0;  // phases of sfull and odone that have been waited for
     auto wait = [&](uint64_t *bar, int phase) {
-      if (ok) ok = tc::mbar_wait(bar, phase & 1, st);
+      if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, st);
       ok = __all_sync(0xffffffffu, ok);
       tc::tc_fence_after();
     };
@@ -389,45 +405,66 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       // a row that does not exist is as good as one that sees everything
       const int limit = r < plan.rows ? plan.seen(len, r, r + 1) : INT_MAX;
       // queries: scaled to a maximum of [1, 2), fp16, K-major
-      // Queries, scaled to a maximum of [1, 2), fp16, K-major: a warp loads its tile's 32 rows with
-      // D / 8 lanes a row, all in flight at once, and leaves each row's factor for its thread.
+      // Where this thread's row of queries starts, and of outputs (rows that do not exist: row 0).
+      const int rq = r < plan.rows ? r / plan.group : 0, hq = r < plan.rows ? r % plan.group : 0;
+      const int64_t q_at = seq * g.q_stride[0] + rq * g.q_stride[1] +
+                           (int64_t)(at.head * plan.group + hq) * g.q_stride[2];
+      const int64_t o_at = seq * g.o_stride[0] + rq * g.o_stride[1] +
+                           (int64_t)(at.head * plan.group + hq) * g.o_stride[2];
+      // Rows move D / 8 lanes to a row, 16 bytes a lane; `kAt` rows of the warp's 32 at a time.
+      constexpr int kLanes = D / 8, kAt = 32 / kLanes;
+      const int sub = lane / kLanes, part8 = lane % kLanes, wrow = warp % 4 * 32;
+      uint8_t *const mine8 = q_tile + part8 / 8 * C::kChunk;
+      // Queries, scaled to a maximum of [1, 2), fp16, K-major; all loads in flight at once, the
+      // rest in a small loop (code that runs once an item costs its instructions' fetch).
       float f = 0.0f;
       if (mine > 0) {
-        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kLoads = 32 / kAt;  // rows at a time
-        const int sub = lane / kLanes, piece = lane % kLanes;
-        uint4 raw[kLoads];
+        const T *q = (const T *)g.q + 8 * part8;
+        const int exist = plan.rows - row0 - wrow;  // of the warp's rows
+        if (g.vec_q) {
+#pragma unroll 1
+          for (int i0 = 0; i0 < 32; i0 += 8 * kAt) {
+            uint4 raw[8];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int rr = row0 + warp % 4 * 32 + i * kAt + sub;
-          const T *q = (const T *)g.q + seq * g.q_stride[0] + (rr / plan.group) * g.q_stride[1] +
-                       (int64_t)(at.head * plan.group + rr % plan.group) * g.q_stride[2] + 8 * piece;
-          if (rr >= plan.rows) {
-            raw[i] = make_uint4(0, 0, 0, 0);
-          } else if (g.vec_q) {
-            raw[i] = *reinterpret_cast<const uint4 *>(q);
-          } else {
-            const uint16_t *e = reinterpret_cast<const uint16_t *>(q);
-            raw[i] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
-                                e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+            for (int i = 0; i < 8; ++i) {
+              const int mr = i0 + i * kAt + sub;
+              const int64_t off = __shfl_sync(0xffffffffu, q_at, mr);
+              raw[i] = mr < exist ? *reinterpret_cast<const uint4 *>(q + off) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4 *>(mine8 + swizzled(wrow + i0 + i * kAt + sub, part8 % 8)) = raw[i];
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 32; i += kAt) {
+            const int64_t off = __shfl_sync(0xffffffffu, q_at, i + sub);
+            alignas(16) T e[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = i + sub < exist ? q[off + j] : from_f32<T>(0.0f);
+            *reinterpret_cast<uint4 *>(mine8 + swizzled(wrow + i + sub, part8 % 8)) =
+                *reinterpret_cast<const uint4 *>(e);
           }
         }
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
+#pragma unroll 2
+        for (int i = 0; i < 32; i += kAt) {
+          const int mr = wrow + i + sub;
+          uint4 *const slot = reinterpret_cast<uint4 *>(mine8 + swizzled(mr, part8 % 8));
+          const uint4 w = *slot;
           float v[8], amax = 0.0f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            v[j] = to_f32(reinterpret_cast<const T *>(&raw[i])[j]);
+            v[j] = to_f32(reinterpret_cast<const T *>(&w)[j]);
             amax = fmaxf(amax, fp8::finite_abs(v[j]));
           }
 #pragma unroll
           for (int o = 1; o < kLanes; o <<= 1)
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          const int e = row_exponent(amax), mr = warp % 4 * 32 + i * kAt + sub;
+          const int e = row_exponent(amax);
           const float inv = g.scale < 0.0f ? -fp8::pow2(-e) : fp8::pow2(-e);
-          if (piece == 0) factor[b * kTile + mr] = fp8::pow2(e) * fabsf(g.scale) * kLog2e;
-          *reinterpret_cast<uint4 *>(q_tile + piece / 8 * C::kChunk + swizzled(mr, piece % 8)) =
-              make_uint4(pack_half2(v[0] * inv, v[1] * inv), pack_half2(v[2] * inv, v[3] * inv),
-                         pack_half2(v[4] * inv, v[5] * inv), pack_half2(v[6] * inv, v[7] * inv));
+          if (part8 == 0) factor[b * kTile + mr] = fp8::pow2(e) * fabsf(g.scale) * kLog2e;
+          *slot = make_uint4(pack_half2(v[0] * inv, v[1] * inv), pack_half2(v[2] * inv, v[3] * inv),
+                             pack_half2(v[4] * inv, v[5] * inv), pack_half2(v[6] * inv, v[7] * inv));
         }
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();  // O of the item before has been read
@@ -552,14 +589,13 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       }
       if (whole) {
         __syncwarp();  // a warp's rows are its own
-        constexpr int kLanes = D / 8, kAt = 32 / kLanes;
-        const int sub = lane / kLanes, u = lane % kLanes;
-#pragma unroll 4
+        const int exist = plan.rows - row0 - wrow;
+#pragma unroll 2
         for (int i = 0; i < 32; i += kAt) {
-          const int mr = warp % 4 * 32 + i + sub, rr = row0 + mr;
-          if (rr >= plan.rows) continue;
-          const uint4 w = *reinterpret_cast<const uint4 *>(q_tile + u / 8 * C::kChunk + swizzled(mr, u % 8));
-          T *o = out_row<T>(g, plan.group, seq, at.head, rr) + 8 * u;
+          const int64_t off = __shfl_sync(0xffffffffu, o_at, i + sub);
+          if (i + sub >= exist) continue;
+          const uint4 w = *reinterpret_cast<const uint4 *>(mine8 + swizzled(wrow + i + sub, part8 % 8));
+          T *o = (T *)g.out + off + 8 * part8;
           if (g.vec_o) {
             *reinterpret_cast<uint4 *>(o) = w;
           } else {
@@ -593,7 +629,7 @@ gptq_status run(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   GPTQ_TRY(launch_early(prompt_kernel<T, D>, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, s, g,
                         part, (DevStatus *)ws));
   return launch_early(join_kernel<T, D, PromptPlan>, dim3((unsigned)ctas - 1, 8), dim3(128), 0, s,
-                      g, (const float *)part, 1, (int64_t)ctas);
+                      g, (const float *)part, 1, ctas);
 }
 
 }  // namespace
@@ -609,9 +645,7 @@ size_t kv8_prompt_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int 
 }
 
 gptq_status launch_kv8_prompt(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
-  const int64_t rows = g.n_new * (g.n_heads / g.n_kv);
-  if (rows > INT32_MAX / 2 || ceil_div(rows, 2 * kTile) * g.n_seq > INT32_MAX / 2)
-    return GPTQ_ERR_UNSUPPORTED;
+  if (!kv8_plan_fits(g, 2 * kTile, 2, PromptPlan::kSetup)) return GPTQ_ERR_UNSUPPORTED;
   if (g.dtype == GPTQ_F16)
     return g.dim == 64 ? run<__half, 64>(g, ws, s) : run<__half, 128>(g, ws, s);
   return g.dim == 64 ? run<__nv_bfloat16, 64>(g, ws, s) : run<__nv_bfloat16, 128>(g, ws, s);

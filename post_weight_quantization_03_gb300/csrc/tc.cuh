@@ -89,6 +89,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, DevSta
   return false;
 }
 
+// mbar_wait in fewer instructions, for kernels with many waits in many roles, whose code would
+// otherwise outgrow the instruction cache.
+__device__ __forceinline__ bool mbar_wait_compact(uint64_t *bar, uint32_t parity, DevStatus *st) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    const uint64_t t = global_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitNs) {
+      if (st) atomicCAS(&st->status, 0, (int)GPTQ_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------------------------------
 // TMA (tiled tensor copies global -> shared, completion on an mbarrier)
 // ---------------------------------------------------------------------------------------
