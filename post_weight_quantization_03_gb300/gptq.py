@@ -564,7 +564,8 @@ def quantize_obq(W, U, bits=4, dead_mask=None, ws=None, stream=None):
 
 
 # ---------------------------------------------------------------------------------------
-# 8-bit serving
+# 8-bit serving (helpers of a step that runs for each token: their own cost is host time, so
+# they read each tensor attribute once and pass plain integers)
 # ---------------------------------------------------------------------------------------
 
 def _lend(stream, *tensors):
@@ -575,21 +576,52 @@ def _lend(stream, *tensors):
                 t.record_stream(stream)
 
 
+def _stream_of(device, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(
+        index if index is not None else torch.cuda.current_device())
+
+
+_SERVING_DTYPES = {}
+
+
+def _serving_dtype(dtype):
+    if not _SERVING_DTYPES:
+        torch = _torch()
+        _SERVING_DTYPES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+    code = _SERVING_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
 def _fp8_empty(rows, d, row_block, device, stream):
     """Codes and exponents of a ``[rows, d]`` e4m3 matrix, in the pitches the library asks for."""
     torch = _torch()
-    codes = torch.empty(rows, -(-d // 16) * 16, dtype=torch.float8_e4m3fn, device=device)
-    kb = -(-d // FP8_BLOCK)
-    exps = torch.empty(-(-rows // row_block), -(-kb // 4) * 4, dtype=torch.uint8, device=device)
-    _lend(stream, codes, exps)
-    return codes[:, :d], exps[:, :kb]
+    pitch, kb = (d + 15) & ~15, (d + FP8_BLOCK - 1) // FP8_BLOCK
+    codes = torch.empty((rows, pitch), dtype=torch.float8_e4m3fn, device=device)
+    erows, epitch = (rows + row_block - 1) // row_block, (kb + 3) & ~3
+    exps = torch.empty((erows, epitch), dtype=torch.uint8, device=device)
+    if stream is not None:
+        _lend(stream, codes, exps)
+    if pitch != d:
+        codes = codes[:, :d]
+    if epitch != kb:
+        exps = exps[:, :kb]
+    return codes, pitch, exps, epitch
 
 
-def _row_major(name, t, rows=None, d=None):
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (
-            rows is not None and t.shape[0] != rows) or (d is not None and t.shape[1] != d):
+def _rows_of(name, t, rows=None, d=None):
+    """Row pitch of a row-major matrix of the given size."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (
+            d is not None and shape[1] != d) or (stride[1] != 1 and shape[1] != 1):
         want = f"[{'rows' if rows is None else rows}, {'d' if d is None else d}]"
         raise ValueError(f"{name} must be a row-major {want} matrix")
+    return stride[0] if shape[0] != 1 else max(stride[0], shape[1])
 
 
 def rmsnorm_fp8(X, weight, residual=None, eps=1e-6, want_h=True, stream=None):
@@ -600,40 +632,43 @@ def rmsnorm_fp8(X, weight, residual=None, eps=1e-6, want_h=True, stream=None):
     ``rstd * 2**(exps - 127) * codes`` (hand ``rstd`` to ``fp8_matmul`` as ``a_scale``).
     ``h`` is X itself when there is no residual, None when ``want_h`` is false."""
     torch = _torch()
-    _row_major("X", X)
+    ldx = _rows_of("X", X)
     n, d = X.shape
+    dtype, device = X.dtype, X.device
+    ldr = 0
     if residual is not None:
-        _row_major("residual", residual, n, d)
-        if residual.dtype != X.dtype:
+        ldr = _rows_of("residual", residual, n, d)
+        if residual.dtype != dtype:
             raise TypeError("residual must have X's dtype")
     if weight.shape != (d,) or (d > 1 and weight.stride(0) != 1):
         raise ValueError("weight must be a contiguous [d] vector")
-    codes, exps = _fp8_empty(n, d, 1, X.device, stream)
-    rstd = torch.empty(n, dtype=torch.float32, device=X.device)
-    h = X
-    if residual is not None or not want_h:
-        h = torch.empty(n, d, dtype=X.dtype, device=X.device) if want_h else None
-        _lend(stream, h)
-    _lend(stream, rstd)
-    out = h if h is not X else None
-    _check(gptq_rmsnorm_fp8(_ptr(X), _dtype_code(X), n, d, X.stride(0), _ptr(residual),
-                            residual.stride(0) if residual is not None else 0, _ptr(weight),
-                            _dtype_code(weight), eps, _ptr(out),
-                            out.stride(0) if out is not None else 0, _ptr(codes),
-                            codes.stride(0), _ptr(exps), exps.stride(0), _ptr(rstd),
-                            _stream(stream)), "gptq_rmsnorm_fp8")
+    codes, ldc, exps, lde = _fp8_empty(n, d, 1, device, stream)
+    rstd = torch.empty((n,), dtype=torch.float32, device=device)
+    h, h_ptr = X, None
+    if not want_h:
+        h = None
+    elif residual is not None:
+        h = torch.empty((n, d), dtype=dtype, device=device)
+        h_ptr = h.data_ptr()
+    if stream is not None:
+        _lend(stream, rstd, h)
+    _check(load().gptq_rmsnorm_fp8(
+        X.data_ptr(), _serving_dtype(dtype), n, d, ldx,
+        residual.data_ptr() if residual is not None else None, ldr, weight.data_ptr(),
+        _serving_dtype(weight.dtype), eps, h_ptr, d, codes.data_ptr(), ldc, exps.data_ptr(), lde,
+        rstd.data_ptr(), _stream_of(device, stream)), "gptq_rmsnorm_fp8")
     return codes, exps, rstd, h
 
 
 def fp8_quantize(X, row_block=1, stream=None):
     """``(codes, exps)`` of a ``[rows, d]`` matrix by ``row_block x 128`` blocks: 1 for
     activations, 128 for weights."""
-    _row_major("X", X)
+    ldx = _rows_of("X", X)
     n, d = X.shape
-    codes, exps = _fp8_empty(n, d, row_block, X.device, stream)
-    _check(gptq_fp8_quantize(_ptr(X), _dtype_code(X), n, d, X.stride(0), row_block, _ptr(codes),
-                             codes.stride(0), _ptr(exps), exps.stride(0), _stream(stream)),
-           "gptq_fp8_quantize")
+    codes, ldc, exps, lde = _fp8_empty(n, d, row_block, X.device, stream)
+    _check(load().gptq_fp8_quantize(X.data_ptr(), _serving_dtype(X.dtype), n, d, ldx, row_block,
+                                    codes.data_ptr(), ldc, exps.data_ptr(), lde,
+                                    _stream_of(X.device, stream)), "gptq_fp8_quantize")
     return codes, exps
 
 
@@ -646,10 +681,10 @@ def fp8_from_codes(qpacked, zero, d_in, bits=4, stream=None):
             or zero.shape != (m,) or not zero.is_contiguous():
         raise ValueError("qpacked [d_out, ceil(d_in / 32) * bits] and zero [d_out] as quantize "
                          "returns them")
-    codes, exps = _fp8_empty(m, d_in, FP8_BLOCK, qpacked.device, stream)
-    _check(gptq_fp8_from_codes(_ptr(qpacked), bits, _ptr(zero), m, d_in, _ptr(codes),
-                               codes.stride(0), _ptr(exps), exps.stride(0), _stream(stream)),
-           "gptq_fp8_from_codes")
+    codes, ldc, exps, lde = _fp8_empty(m, d_in, FP8_BLOCK, qpacked.device, stream)
+    _check(load().gptq_fp8_from_codes(qpacked.data_ptr(), bits, zero.data_ptr(), m, d_in,
+                                      codes.data_ptr(), ldc, exps.data_ptr(), lde,
+                                      _stream_of(qpacked.device, stream)), "gptq_fp8_from_codes")
     return codes, exps
 
 
@@ -658,34 +693,40 @@ def fp8_matmul(a, a_exps, w, w_exps, a_scale=None, w_scale=None, out_dtype=None,
     """``diag(a_scale) A W^T diag(w_scale)`` of e4m3 matrices ``A [m, k]`` (1 x 128 blocks) and
     ``W [n, k]`` (128 x 128 blocks), ``[m, n]`` in float16 or bfloat16 (the default)."""
     torch = _torch()
-    _row_major("a", a)
     m, k = a.shape
-    _row_major("w", w, None, k)
     n = w.shape[0]
-    kb = -(-k // FP8_BLOCK)
-    _row_major("a_exps", a_exps, m, kb)
-    _row_major("w_exps", w_exps, -(-n // FP8_BLOCK), kb)
-    if a.dtype != torch.float8_e4m3fn or w.dtype != torch.float8_e4m3fn or \
-            a_exps.dtype != torch.uint8 or w_exps.dtype != torch.uint8:
+    kb = (k + FP8_BLOCK - 1) // FP8_BLOCK
+    lda, ldw = _rows_of("a", a), _rows_of("w", w, n, k)
+    ldae = _rows_of("a_exps", a_exps, m, kb)
+    ldwe = _rows_of("w_exps", w_exps, (n + FP8_BLOCK - 1) // FP8_BLOCK, kb)
+    f8, u8 = torch.float8_e4m3fn, torch.uint8
+    if a.dtype != f8 or w.dtype != f8 or a_exps.dtype != u8 or w_exps.dtype != u8:
         raise TypeError("codes are float8_e4m3fn and exponents uint8")
     for name, t, rows in (("a_scale", a_scale, m), ("w_scale", w_scale, n)):
         if t is not None and (t.dtype != torch.float32 or t.shape != (rows,)
                               or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous float32 [{rows}] vector")
+    device = a.device
     if out is None:
-        out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=a.device)
-        _lend(stream, out)
+        out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=device)
+        ldo = n
+        if stream is not None:
+            _lend(stream, out)
     else:
-        _row_major("out", out, m, n)
+        ldo = _rows_of("out", out, m, n)
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError("out must have out_dtype")
+    lib = load()
     if ws is None:
-        ws = workspace(gptq_fp8_matmul_workspace_bytes(m, n, k), a.device)
-        _lend(stream, ws)
-    _check(gptq_fp8_matmul(_ptr(a), a.stride(0), _ptr(a_exps), a_exps.stride(0), _ptr(a_scale),
-                           _ptr(w), w.stride(0), _ptr(w_exps), w_exps.stride(0), _ptr(w_scale),
-                           m, n, k, _ptr(out), _dtype_code(out), out.stride(0), _ptr(ws),
-                           ws.numel(), _stream(stream)), "gptq_fp8_matmul")
+        ws = torch.empty((lib.gptq_fp8_matmul_workspace_bytes(m, n, k),), dtype=u8, device=device)
+        if stream is not None:
+            _lend(stream, ws)
+    _check(lib.gptq_fp8_matmul(
+        a.data_ptr(), lda, a_exps.data_ptr(), ldae,
+        a_scale.data_ptr() if a_scale is not None else None, w.data_ptr(), ldw, w_exps.data_ptr(),
+        ldwe, w_scale.data_ptr() if w_scale is not None else None, m, n, k, out.data_ptr(),
+        _serving_dtype(out.dtype), ldo, ws.data_ptr(), ws.numel(), _stream_of(device, stream)),
+        "gptq_fp8_matmul")
     return out
 
 
@@ -703,47 +744,50 @@ def kv8_cache(n_blocks, n_kv_heads, dim, device=None):
     return (k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn), *exps)
 
 
-def _kv8_check(cache, table, seqs, lengths, what):
+def _kv8_args(cache, table, seqs, lengths, what):
+    """``(n_blocks, n_kv_heads, dim, table pitch, blocks of the table)`` of matching arguments."""
     torch = _torch()
     k, v, ke, ve = cache
-    if k.dim() != 4 or k.shape[2] != KV8_BLOCK:
+    shape = k.shape
+    if len(shape) != 4 or shape[2] != KV8_BLOCK:
         raise ValueError(f"cache k must be [n_blocks, n_kv_heads, {KV8_BLOCK}, dim]")
-    nb, kv, _, d = k.shape
+    nb, kv, _, d = shape
     if v.shape != (nb, kv, d, KV8_BLOCK) or ke.shape != (nb, kv) or ve.shape != (nb, kv):
         raise ValueError("cache v, k_exps, v_exps do not match k")
-    if k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn or \
-            ke.dtype != torch.uint8 or ve.dtype != torch.uint8:
+    f8, u8, i32 = torch.float8_e4m3fn, torch.uint8, torch.int32
+    if k.dtype != f8 or v.dtype != f8 or ke.dtype != u8 or ve.dtype != u8:
         raise TypeError("codes are float8_e4m3fn and exponents uint8")
     if not (k.is_contiguous() and v.is_contiguous() and ke.is_contiguous()
             and ve.is_contiguous()):
         raise ValueError("the cache must be contiguous")
-    if table.dtype != torch.int32 or lengths.dtype != torch.int32:
+    if table.dtype != i32 or lengths.dtype != i32:
         raise TypeError(f"table and {what} must be int32")
-    _row_major("table", table, seqs)
+    pitch = _rows_of("table", table, seqs)
     if lengths.shape != (seqs,) or not lengths.is_contiguous():
         raise ValueError(f"{what} must be a contiguous [{seqs}] vector")
-    return nb, kv, d
+    return nb, kv, d, pitch, table.shape[1]
 
 
-def _strides3(t):
-    s = t.stride()
-    return (ctypes.c_int64 * 3)(s[0], s[1], s[2])
+_Strides3 = ctypes.c_int64 * 3
 
 
 def kv8_append(cache, k, v, table, start, stream=None):
     """Writes new keys and values ``[seqs, new, n_kv_heads, dim]`` into the cache at each
     sequence's tokens ``[start, start + new)``; ``table [seqs, blocks]`` (int32) names the cache
     blocks of each sequence, -1 for none."""
-    n_seq = k.shape[0]
-    nb, kv, d = _kv8_check(cache, table, n_seq, start, "start")
-    if k.dim() != 4 or k.shape[2:] != (kv, d) or v.shape != k.shape or k.dtype != v.dtype:
+    shape, ks, vs = k.shape, k.stride(), v.stride()
+    nb, kv, d, pitch, mb = _kv8_args(cache, table, shape[0], start, "start")
+    if len(shape) != 4 or shape[2] != kv or shape[3] != d or v.shape != shape \
+            or k.dtype != v.dtype:
         raise ValueError(f"k and v must be [seqs, new, {kv}, {d}] of one dtype")
-    if k.stride(3) != 1 or v.stride(3) != 1:
+    if ks[3] != 1 or vs[3] != 1:
         raise ValueError("a head's elements must be contiguous")
-    _check(gptq_kv8_append(_ptr(k), _strides3(k), _ptr(v), _strides3(v), _dtype_code(k), n_seq,
-                           k.shape[1], kv, d, _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]),
-                           _ptr(cache[3]), nb, _ptr(table), table.stride(0), table.shape[1],
-                           _ptr(start), _stream(stream)), "gptq_kv8_append")
+    kc, vc, ke, ve = cache
+    _check(load().gptq_kv8_append(
+        k.data_ptr(), _Strides3(ks[0], ks[1], ks[2]), v.data_ptr(),
+        _Strides3(vs[0], vs[1], vs[2]), _serving_dtype(k.dtype), shape[0], shape[1], kv, d,
+        kc.data_ptr(), vc.data_ptr(), ke.data_ptr(), ve.data_ptr(), nb, table.data_ptr(), pitch,
+        mb, start.data_ptr(), _stream_of(k.device, stream)), "gptq_kv8_append")
 
 
 def kv8_attention(q, cache, table, lengths, scale=None, causal=True, out=None, ws=None,
@@ -752,24 +796,34 @@ def kv8_attention(q, cache, table, lengths, scale=None, causal=True, out=None, w
     tokens of each sequence (``lengths`` of them, the new ones included); ``scale`` defaults to
     ``dim ** -0.5``.  Rows that see no token give zeros."""
     torch = _torch()
-    if q.dim() != 4 or q.stride(3) != 1:
+    shape, qs = q.shape, q.stride()
+    if len(shape) != 4 or qs[3] != 1:
         raise ValueError("q must be [seqs, new, heads, dim] with a head's elements contiguous")
-    n_seq, new, heads, _ = q.shape
-    nb, kv, d = _kv8_check(cache, table, n_seq, lengths, "lengths")
-    if q.shape[3] != d:
+    n_seq, new, heads, dim = shape
+    nb, kv, d, pitch, mb = _kv8_args(cache, table, n_seq, lengths, "lengths")
+    if dim != d:
         raise ValueError(f"q's heads must be {d} wide, as the cache's")
+    device, dtype = q.device, q.dtype
     if out is None:
-        out = torch.empty(n_seq, new, heads, d, dtype=q.dtype, device=q.device)
-        _lend(stream, out)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.stride(3) != 1:
-        raise ValueError("out must match q")
-    mb = table.shape[1]
+        out = torch.empty(shape, dtype=dtype, device=device)
+        os_ = out.stride()
+        if stream is not None:
+            _lend(stream, out)
+    else:
+        os_ = out.stride()
+        if out.shape != shape or out.dtype != dtype or os_[3] != 1:
+            raise ValueError("out must match q")
+    lib = load()
     if ws is None:
-        ws = workspace(gptq_kv8_attention_workspace_bytes(n_seq, new, heads, kv, d, mb), q.device)
-        _lend(stream, ws)
-    _check(gptq_kv8_attention(_ptr(q), _strides3(q), _dtype_code(q), n_seq, new, heads, kv, d,
-                              _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]), _ptr(cache[3]), nb,
-                              _ptr(table), table.stride(0), mb, _ptr(lengths), 1 if causal else 0,
-                              d ** -0.5 if scale is None else scale, _ptr(out), _strides3(out),
-                              _ptr(ws), ws.numel(), _stream(stream)), "gptq_kv8_attention")
+        ws = torch.empty((lib.gptq_kv8_attention_workspace_bytes(n_seq, new, heads, kv, d, mb),),
+                         dtype=torch.uint8, device=device)
+        if stream is not None:
+            _lend(stream, ws)
+    kc, vc, ke, ve = cache
+    _check(lib.gptq_kv8_attention(
+        q.data_ptr(), _Strides3(qs[0], qs[1], qs[2]), _serving_dtype(dtype), n_seq, new, heads,
+        kv, d, kc.data_ptr(), vc.data_ptr(), ke.data_ptr(), ve.data_ptr(), nb, table.data_ptr(),
+        pitch, mb, lengths.data_ptr(), 1 if causal else 0, d ** -0.5 if scale is None else scale,
+        out.data_ptr(), _Strides3(os_[0], os_[1], os_[2]), ws.data_ptr(), ws.numel(),
+        _stream_of(device, stream)), "gptq_kv8_attention")
     return out
