@@ -68,7 +68,41 @@ gptq_status launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   }
   return GPTQ_OK;
 }
+// launch_kernel for a kernel that may start before the one ahead of it in the stream ends: it
+// sets itself up and then waits with wait_for_grids.  `cluster` CTAs form a cluster.
+template <typename... KArgs, typename... Args>
+gptq_status launch_early(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
+                         cudaStream_t s, Args &&...args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  count_launch();
+  if (cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GPTQ_ERR_CUDA;
+  }
+  return GPTQ_OK;
+}
+
 static inline __host__ __device__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Starts a kernel's dependents early, and waits for the kernels it depends on to complete.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_grids() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // Device-side status block at the start of every workspace.
 struct DevStatus {

@@ -39,9 +39,11 @@ constexpr uint32_t kScaleBytes = 3 * 512;   // W, tokens 0..127, tokens 128..239
 constexpr uint32_t kScaleCols = 12;         // TMEM columns of one group
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 12;
-constexpr uint32_t kRingBytes = 208 * 1024;
-constexpr size_t kSmem = 1024 + kRingBytes + kScaleStages * kScaleBytes + kMaxTn * 4 + 512;
+constexpr uint32_t kRingBytes = 208 * 1024;      // one CTA on an SM
+constexpr uint32_t kRingBytesTwo = 96 * 1024;    // two
+constexpr size_t kSmemBesides = 1024 + kScaleStages * kScaleBytes + kMaxTn * 4 + 512;
 static_assert(2 * kMaxTn + 2 * kScaleCols <= kTmemCols, "TMEM columns");
+static_assert(2 * (kRingBytesTwo + kSmemBesides + 1024) <= 228 * 1024, "two CTAs on an SM");
 
 struct MmParams {
   const uint8_t *ae; int64_t ldae;
@@ -53,6 +55,8 @@ struct MmParams {
   int tn, stages;
   int n_w, n_tiles;     // tiles along the weights; tiles in all
   int splits;           // CTAs of a cluster that share a tile's k-blocks
+  uint32_t ring_bytes;
+  int acc_cols, tmem_cols;  // columns of an accumulator; allocated
 };
 
 template <typename TO>
@@ -96,12 +100,12 @@ __device__ __forceinline__ void k_range(const MmParams &p, int rank, int &k0, in
 }
 
 template <typename TO>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
 matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap ma,
               MmParams p, DevStatus *st) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *sscale = ring + kRingBytes;
+  uint8_t *sscale = ring + p.ring_bytes;
   float *sra = (float *)(sscale + kScaleStages * kScaleBytes);
   uint64_t *full = (uint64_t *)(sra + kMaxTn);
   uint64_t *empty = full + kMaxStages;
@@ -111,7 +115,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   uint64_t *tempty = tfull + 2;
   uint32_t *tmem_slot = (uint32_t *)(tempty + 2);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t stage_bytes = (uint32_t)(BM + p.tn) * BK;
   const int rank = p.splits > 1 ? (int)tc::cluster_ctarank() : 0;
   const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
@@ -119,9 +123,6 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   k_range(p, rank, k0, k1);
 
   if (threadIdx.x == 0) {
-    // The status of the call.  A wait that gives up writes it two seconds or more after its own
-    // CTA started, so this store, by the first CTA to start, comes first.
-    if (blockIdx.x == 0) st->status = 0;
     for (int s = 0; s < p.stages; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
@@ -136,11 +137,18 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     }
     tc::mbar_fence_init();
   }
-  if (warp == 1) tc::tmem_alloc(tmem_slot, kTmemCols);
+  if (warp == 1) tc::tmem_alloc(tmem_slot, p.tmem_cols);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_for_grids();
+  launch_dependents();
+  // The status of the call.  A wait that gives up writes it two seconds or more after its own
+  // CTA started, so this store, by the first CTA to start, comes first.
+  if (blockIdx.x == 0 && threadIdx.x == 0) st->status = 0;
+  // with few tiles every CTA has one and a second accumulator is not allocated
+  const uint32_t second = (uint32_t)p.acc_cols, sc_cols = tmem + (p.tmem_cols == (int)kTmemCols ? 2 : 1) * second;
 
   if (warp == 0 && lane == 0) {
     // ---------------- producer ----------------
@@ -162,52 +170,56 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       }
       if (!ok) break;
     }
-  } else if (warp == 1 && lane == 0) {
-    // ---------------- MMA issuer ----------------
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (the whole warp; one lane issues) ----------------
     // kind::mxf8f6f4 instruction descriptor: e4m3 operands, K-major, power-of-two scale bytes
     const uint32_t idesc = (1u << 23) | ((uint32_t)(p.tn >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+    // a descriptor holds its address in units of 16 bytes: offsets are added to it
+    const uint64_t dw = tc::smem_desc_sw128(tc::smem_u32(ring), 16, 1024);
     int s = 0, g = 0, it = 0;
     uint32_t ph = 0;
     bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_compact(bar, parity, st));
+      tc::tc_fence_after();
+      return ok;
+    };
+#pragma unroll 1
     for (int t = first; t < p.n_tiles && ok; t += step, ++it) {
       const int b = it & 1;
-      ok = tc::mbar_wait(&tempty[b], ((it >> 1) & 1) ^ 1, st);
-      if (!ok) break;
-      tc::tc_fence_after();
-      const uint32_t acc = tmem + (uint32_t)(b * kMaxTn);
+      if (!wait(&tempty[b], ((it >> 1) & 1) ^ 1)) break;
+      const uint32_t acc = tmem + b * second;
       uint32_t sc = 0;
+#pragma unroll 1
       for (int kb = k0; kb < k1; ++kb) {
         if (kb == k0 || (kb & 3) == 0) {
           const int q = g % kScaleStages;
-          ok = tc::mbar_wait(&sfull[q], (g / kScaleStages) & 1, st);
-          if (!ok) break;
-          tc::tc_fence_after();
+          if (!wait(&sfull[q], (g / kScaleStages) & 1)) break;
           // two groups of columns in turn: the scale warp's ring keeps a third group's copy
           // from starting before the first group's MMAs have completed
-          sc = tmem + 2 * kMaxTn + (uint32_t)(g & 1) * kScaleCols;
+          sc = sc_cols + (uint32_t)(g & 1) * kScaleCols;
           const uint32_t sm = tc::smem_u32(sscale + q * kScaleBytes);
-          copy_scales(sc, sm);
-          copy_scales(sc + 4, sm + 512);
-          if (p.tn > 128) copy_scales(sc + 8, sm + 1024);
+          if (tc::elect_one()) {
+            copy_scales(sc, sm);
+            copy_scales(sc + 4, sm + 512);
+            if (p.tn > 128) copy_scales(sc + 8, sm + 1024);
+          }
         }
-        ok = tc::mbar_wait(&full[s], ph, st);
-        if (!ok) break;
-        tc::tc_fence_after();
-        const uint32_t wa = tc::smem_u32(ring + s * stage_bytes), aa = wa + BM * BK;
-        const uint32_t id = idesc | ((uint32_t)(kb & 3) << 29) | ((uint32_t)(kb & 3) << 4);
+        if (!wait(&full[s], ph)) break;
+        const bool group_ends = (kb & 3) == 3 || kb + 1 == k1;
+        if (tc::elect_one()) {
+          const uint64_t da = dw + (uint32_t)(s * stage_bytes >> 4), db = da + (BM * BK >> 4);
+          const uint32_t id = idesc | ((uint32_t)(kb & 3) << 29) | ((uint32_t)(kb & 3) << 4);
 #pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk)
-          mma_mx(acc, tc::smem_desc_sw128(wa + kk * 32, 16, 1024),
-                 tc::smem_desc_sw128(aa + kk * 32, 16, 1024), id, sc, sc + 4,
-                 (kb > k0 || kk > 0) ? 1u : 0u);
-        tc::mma_commit(&empty[s]);
-        if (++s == p.stages) s = 0, ph ^= 1;
-        if ((kb & 3) == 3 || kb + 1 == k1) {
-          tc::mma_commit(&sempty[g % kScaleStages]);
-          ++g;
+          for (int kk = 0; kk < BK / 32; ++kk)
+            mma_mx(acc, da + 2 * kk, db + 2 * kk, id, sc, sc + 4, (kb > k0 || kk > 0) ? 1u : 0u);
+          tc::mma_commit(&empty[s]);
+          if (group_ends) tc::mma_commit(&sempty[g % kScaleStages]);
+          if (kb + 1 == k1) tc::mma_commit(&tfull[b]);
         }
+        if (++s == p.stages) s = 0, ph ^= 1;
+        if (group_ends) ++g;
       }
-      if (ok) tc::mma_commit(&tfull[b]);
     }
   } else if (warp == 6) {
     // ---------------- scales ----------------
@@ -262,7 +274,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
 #pragma unroll 1
       for (int c = 0; c < p.tn; c += 32) {
         uint32_t r[32];
-        tc::tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kMaxTn + c), r);
+        tc::tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + b * second + (uint32_t)c, r);
         tc::tmem_ld_wait();
         if (p.splits > 1) {
 #pragma unroll
@@ -282,7 +294,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 1) tc::tmem_dealloc(tmem, kTmemCols);
+  if (warp == 1) tc::tmem_dealloc(tmem, p.tmem_cols);
   if (p.splits > 1) {
     // one tile per cluster: the ring holds this CTA's partial sums [tn][128]
     tc::cluster_sync();
@@ -303,14 +315,12 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   }
 }
 
-// Tile of tokens and splits of K.  A CTA's time is about
-//   k-blocks x max(MMA cycles, bytes / its share of the memory) + a constant,
-// and a launch takes as many rounds as its CTAs need on the SMs.
-struct Shape { int tn, splits; };
+// Tile of tokens, splits of K and CTAs on an SM.
+struct Shape { int tn, splits, per_sm; };
 
 Shape choose(int64_t M, int64_t N, int kb, int sms) {
   const int64_t n_w = ceil_div(N, BM);
-  Shape best{16, 1};
+  Shape best{16, 1, 1};
   double best_t = 1e30;
   for (int64_t mt = ceil_div(M, kMaxTn);; ++mt) {
     const int tn = (int)(ceil_div(ceil_div(M, mt), 16) * 16);
@@ -321,7 +331,7 @@ Shape choose(int64_t M, int64_t N, int kb, int sms) {
       const double round_t = (double)ceil_div(kb, s) * per_kb + 2500.0 + (s > 1 ? 1500.0 + 8.0 * tn : 0.0);
       const int64_t rounds = ceil_div(tiles * s, s > 1 ? sms / s * s : sms);
       const double t = (double)rounds * round_t;
-      if (t < best_t) best_t = t, best = Shape{tn, s};
+      if (t < best_t) best_t = t, best = Shape{tn, s, 1};
     }
     if (tn <= 64 || mt > ceil_div(M, kMaxTn) + 4) break;
   }
@@ -330,7 +340,7 @@ Shape choose(int64_t M, int64_t N, int kb, int sms) {
 
 template <typename TO>
 gptq_status run(const Fp8MatmulArgs &g, DevStatus *st, cudaStream_t s) {
-  GPTQ_TRY(ensure_smem_attr((const void *)matmul_kernel<TO>, (int)kSmem));
+  GPTQ_TRY(ensure_smem_attr((const void *)matmul_kernel<TO>, (int)(kRingBytes + kSmemBesides)));
   int sms = 0;
   GPTQ_TRY(device_sm_count(&sms));
   const int kb = (int)ceil_div(g.K, BK);
@@ -343,31 +353,28 @@ gptq_status run(const Fp8MatmulArgs &g, DevStatus *st, cudaStream_t s) {
   p.M = g.M; p.N = g.N;
   p.kb = kb;
   p.tn = sh.tn;
-  const int fit = (int)(kRingBytes / (uint32_t)((BM + sh.tn) * BK));
-  p.stages = fit < kMaxStages ? fit : kMaxStages;
   p.n_w = (int)ceil_div(g.N, BM);
   const int64_t tiles = p.n_w * ceil_div(g.M, sh.tn);
   if (tiles * 8 > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
   p.n_tiles = (int)tiles;
   p.splits = sh.splits;
+  const bool one_tile = sh.splits > 1 || tiles <= (int64_t)sms * sh.per_sm;
+  p.ring_bytes = sh.per_sm > 1 ? kRingBytesTwo : kRingBytes;
+  const int fit = (int)(p.ring_bytes / (uint32_t)((BM + sh.tn) * BK));
+  p.stages = fit < kMaxStages ? fit : kMaxStages;
+  // an accumulator for the tile at hand and one for the next, or one and 256 columns at most
+  p.acc_cols = one_tile && sh.tn <= 224 ? (sh.tn + 31) / 32 * 32 : kMaxTn;
+  p.tmem_cols = kTmemCols;
+  if (one_tile && sh.tn <= 224)
+    for (p.tmem_cols = 64; p.tmem_cols < p.acc_cols + 2 * (int)kScaleCols;) p.tmem_cols *= 2;
   CUtensorMap mw, ma;
   if (!tc::make_tmap_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w, g.N, g.K, g.ldw, BK, BM) ||
       !tc::make_tmap_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, g.M, g.K, g.lda, BK, sh.tn))
     return GPTQ_ERR_UNSUPPORTED;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(sh.splits > 1 ? tiles * sh.splits : (tiles < sms ? tiles : sms)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)sh.splits;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  count_launch();
-  GPTQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, matmul_kernel<TO>, mw, ma, p, st));
-  return GPTQ_OK;
+  const int64_t slots = (int64_t)sms * sh.per_sm;
+  const int64_t ctas = sh.splits > 1 ? tiles * sh.splits : (tiles < slots ? tiles : slots);
+  return launch_early(matmul_kernel<TO>, dim3((unsigned)ctas), dim3(kThreads),
+                      p.ring_bytes + kSmemBesides, sh.splits, s, mw, ma, p, st);
 }
 
 }  // namespace

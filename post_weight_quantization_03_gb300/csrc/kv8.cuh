@@ -54,14 +54,6 @@ __device__ __forceinline__ int seq_length(const Kv8AttentionArgs &g, int seq) {
   return len < 0 ? 0 : (len > cap ? cap : len);
 }
 
-// Starts a kernel's dependents early, and waits for the kernels it depends on to complete.
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_grids() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // The exponent of a row's largest magnitude (0 for a row of zeros), by which queries are scaled
 // into the range of the type that the tensor cores take.
 __device__ __forceinline__ int row_exponent(float amax) {
@@ -315,26 +307,6 @@ join_kernel(Kv8AttentionArgs g, const float *part, int turn, int ctas) {
       for (int j = 0; j < 8; ++j) o[j] = stage[r][c + j];
     }
   }
-}
-
-// Launches a kernel that may start before the one ahead of it in the stream ends (it waits with
-// wait_for_grids).
-template <typename... KArgs, typename... Args>
-gptq_status launch_early(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                         cudaStream_t s, Args &&...args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  count_launch();
-  GPTQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...));
-  return GPTQ_OK;
 }
 
 }  // namespace kv8

@@ -438,9 +438,9 @@ gptq_status run_decode(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   GPTQ_TRY(device_sm_count(&sms));
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   float *part = (float *)((char *)ws + 256);
-  GPTQ_TRY(launch_early(kernel, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, s, g, part,
+  GPTQ_TRY(launch_early(kernel, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, 1, s, g, part,
                         (DevStatus *)ws));
-  return launch_early(join_kernel<T, D, DecodePlan>, dim3((unsigned)ctas - 1), dim3(128), 0, s, g,
+  return launch_early(join_kernel<T, D, DecodePlan>, dim3((unsigned)ctas - 1), dim3(128), 0, 1, s, g,
                       (const float *)part, kWarps / rt, ctas);
 }
 

@@ -626,9 +626,9 @@ gptq_status run(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   GPTQ_TRY(device_sm_count(&sms));
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   float *part = (float *)((char *)ws + 256);
-  GPTQ_TRY(launch_early(prompt_kernel<T, D>, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, s, g,
+  GPTQ_TRY(launch_early(prompt_kernel<T, D>, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, 1, s, g,
                         part, (DevStatus *)ws));
-  return launch_early(join_kernel<T, D, PromptPlan>, dim3((unsigned)ctas - 1, 8), dim3(128), 0, s,
+  return launch_early(join_kernel<T, D, PromptPlan>, dim3((unsigned)ctas - 1, 8), dim3(128), 0, 1, s,
                       g, (const float *)part, 1, ctas);
 }
 
