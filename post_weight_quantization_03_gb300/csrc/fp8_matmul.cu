@@ -65,15 +65,18 @@ __device__ __forceinline__ TO out_f32(float x) {
   else return __float2bfloat16_rn(x);
 }
 
-// D[tmem] (+)= (A * 2^sa)(B * 2^sb)^T, one thread; sa, sb: TMEM addresses of the scale columns.
-__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t sa, uint32_t sb, uint32_t accumulate) {
+// D[tmem] (+)= (A * 2^sa)(B * 2^sb)^T, one thread; sa, sb: TMEM addresses of the scale columns;
+// the operands' descriptors by their lower words (the upper one is the layout's).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8 rows on; version; swizzle
+__device__ __forceinline__ void mma_mx(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t sa, uint32_t sb, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
       "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
-      "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      "[%0], a, b, %4, [%5], [%6], p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)accumulate)
       : "memory");
 }
 
@@ -93,10 +96,11 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t caddr) {
   return v;
 }
 
-// k-blocks of this CTA: rank r of the cluster takes an even share.
+// k-blocks of this CTA: rank r of the cluster takes an even share of the groups of four.
 __device__ __forceinline__ void k_range(const MmParams &p, int rank, int &k0, int &k1) {
-  k0 = (int)((int64_t)p.kb * rank / p.splits);
-  k1 = (int)((int64_t)p.kb * (rank + 1) / p.splits);
+  const int groups = (p.kb + 3) / 4;
+  k0 = groups * rank / p.splits * 4;
+  k1 = min(groups * (rank + 1) / p.splits * 4, p.kb);
 }
 
 template <typename TO>
@@ -150,7 +154,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   // with few tiles every CTA has one and a second accumulator is not allocated
   const uint32_t second = (uint32_t)p.acc_cols, sc_cols = tmem + (p.tmem_cols == (int)kTmemCols ? 2 : 1) * second;
 
-  if (warp == 0 && lane == 0) {
+  // (inside elect_one() one thread is known to run, and addresses stay in uniform registers)
+  if (warp == 0 && tc::elect_one()) {
     // ---------------- producer ----------------
     tc::tma_prefetch_desc(&mw);
     tc::tma_prefetch_desc(&ma);
@@ -170,56 +175,52 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       }
       if (!ok) break;
     }
-  } else if (warp == 1) {
-    // ---------------- MMA issuer (the whole warp; one lane issues) ----------------
+  } else if (warp == 1 && tc::elect_one()) {
+    // ---------------- MMA issuer ----------------
     // kind::mxf8f6f4 instruction descriptor: e4m3 operands, K-major, power-of-two scale bytes
     const uint32_t idesc = (1u << 23) | ((uint32_t)(p.tn >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
-    // a descriptor holds its address in units of 16 bytes: offsets are added to it
-    const uint64_t dw = tc::smem_desc_sw128(tc::smem_u32(ring), 16, 1024);
+    const uint32_t ring0 = (tc::smem_u32(ring) >> 4) | (1u << 16), stage16 = stage_bytes >> 4;
+    const uint32_t sc0 = tc::smem_u32(sscale);
     int s = 0, g = 0, it = 0;
-    uint32_t ph = 0;
+    uint32_t ph = 0, at = ring0;    // lower word of the stage's first descriptor
     bool ok = true;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait_compact(bar, parity, st));
-      tc::tc_fence_after();
-      return ok;
-    };
 #pragma unroll 1
     for (int t = first; t < p.n_tiles && ok; t += step, ++it) {
       const int b = it & 1;
-      if (!wait(&tempty[b], ((it >> 1) & 1) ^ 1)) break;
+      ok = tc::mbar_wait_compact(&tempty[b], ((it >> 1) & 1) ^ 1, st);
+      if (!ok) break;
+      tc::tc_fence_after();
       const uint32_t acc = tmem + b * second;
-      uint32_t sc = 0;
 #pragma unroll 1
-      for (int kb = k0; kb < k1; ++kb) {
-        if (kb == k0 || (kb & 3) == 0) {
-          const int q = g % kScaleStages;
-          if (!wait(&sfull[q], (g / kScaleStages) & 1)) break;
-          // two groups of columns in turn: the scale warp's ring keeps a third group's copy
-          // from starting before the first group's MMAs have completed
-          sc = sc_cols + (uint32_t)(g & 1) * kScaleCols;
-          const uint32_t sm = tc::smem_u32(sscale + q * kScaleBytes);
-          if (tc::elect_one()) {
-            copy_scales(sc, sm);
-            copy_scales(sc + 4, sm + 512);
-            if (p.tn > 128) copy_scales(sc + 8, sm + 1024);
-          }
-        }
-        if (!wait(&full[s], ph)) break;
-        const bool group_ends = (kb & 3) == 3 || kb + 1 == k1;
-        if (tc::elect_one()) {
-          const uint64_t da = dw + (uint32_t)(s * stage_bytes >> 4), db = da + (BM * BK >> 4);
-          const uint32_t id = idesc | ((uint32_t)(kb & 3) << 29) | ((uint32_t)(kb & 3) << 4);
+      for (int kb = k0; kb < k1 && ok; kb += 4, ++g) {
+        const int q = g % kScaleStages;
+        ok = tc::mbar_wait_compact(&sfull[q], (g / kScaleStages) & 1, st);
+        if (!ok) break;
+        tc::tc_fence_after();
+        // two groups of columns in turn: the scale warp's ring keeps a third group's copy from
+        // starting before the first group's MMAs have completed
+        const uint32_t sc = sc_cols + (uint32_t)(g & 1) * kScaleCols, sm = sc0 + q * kScaleBytes;
+        copy_scales(sc, sm);
+        copy_scales(sc + 4, sm + 512);
+        if (p.tn > 128) copy_scales(sc + 8, sm + 1024);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (kb + j >= k1) break;
+          ok = tc::mbar_wait_compact(&full[s], ph, st);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint32_t id = idesc | ((uint32_t)j << 29) | ((uint32_t)j << 4);
 #pragma unroll
           for (int kk = 0; kk < BK / 32; ++kk)
-            mma_mx(acc, da + 2 * kk, db + 2 * kk, id, sc, sc + 4, (kb > k0 || kk > 0) ? 1u : 0u);
+            mma_mx(acc, at + 2 * kk, at + (BM * BK >> 4) + 2 * kk, id, sc, sc + 4,
+                   j > 0 || kk > 0 || kb > k0);
           tc::mma_commit(&empty[s]);
-          if (group_ends) tc::mma_commit(&sempty[g % kScaleStages]);
-          if (kb + 1 == k1) tc::mma_commit(&tfull[b]);
+          at += stage16;
+          if (++s == p.stages) s = 0, ph ^= 1, at = ring0;
         }
-        if (++s == p.stages) s = 0, ph ^= 1;
-        if (group_ends) ++g;
+        tc::mma_commit(&sempty[q]);
       }
+      if (ok) tc::mma_commit(&tfull[b]);
     }
   } else if (warp == 6) {
     // ---------------- scales ----------------
@@ -228,7 +229,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     for (int t = first; t < p.n_tiles && ok; t += step) {
       const int64_t m0 = (int64_t)(t / p.n_w) * p.tn;
       const uint8_t *we = p.we + (int64_t)(t % p.n_w) * p.ldwe;
-      for (int sb = k0 / 4; sb <= (k1 - 1) / 4 && k1 > k0; ++sb, ++g) {
+#pragma unroll 1
+      for (int sb = k0 / 4; 4 * sb < k1; ++sb, ++g) {
         uint32_t word[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -325,7 +327,7 @@ Shape choose(int64_t M, int64_t N, int kb, int sms) {
   for (int64_t mt = ceil_div(M, kMaxTn);; ++mt) {
     const int tn = (int)(ceil_div(ceil_div(M, mt), 16) * 16);
     const int64_t tiles = n_w * ceil_div(M, tn);
-    for (int s = 1; s <= 8 && s <= kb; s *= 2) {
+    for (int s = 1; s <= 8 && s <= (kb + 3) / 4; s *= 2) {
       // a cycle per 28 codes of W streamed from memory; 2.3 MMA cycles per token column
       const double per_kb = tn * 2.3 > 300.0 ? tn * 2.3 : 300.0;
       const double round_t = (double)ceil_div(kb, s) * per_kb + 2500.0 + (s > 1 ? 1500.0 + 8.0 * tn : 0.0);
