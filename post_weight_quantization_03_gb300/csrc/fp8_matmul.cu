@@ -20,6 +20,7 @@
 // Few tokens leave few tiles; the k-blocks of a tile are then split over a cluster of up to 8
 // CTAs, whose partial sums meet through distributed shared memory in rank order.
 #include <cudaTypedefs.h>
+#include <math.h>
 
 #include <type_traits>
 
@@ -90,9 +91,12 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
                : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t caddr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(caddr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(caddr)
+               : "memory");
   return v;
 }
 
@@ -302,40 +306,83 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     tc::cluster_sync();
     const int64_t n0 = (int64_t)(first % p.n_w) * BM, m0 = (int64_t)(first / p.n_w) * p.tn;
     const int cols = (int)(p.M - m0 < p.tn ? p.M - m0 : p.tn);
-    const uint32_t base = tc::smem_u32(ring);
-    for (int e = threadIdx.x; e < BM * ((cols + p.splits - 1) / p.splits); e += kThreads) {
-      const int col = e / BM * p.splits + rank;
-      const int64_t n = n0 + e % BM;
-      if (col >= cols || n >= p.N) continue;
-      const uint32_t off = base + (uint32_t)(col * BM + e % BM) * 4;
-      float s = 0.0f;
-      for (int r = 0; r < p.splits; ++r) s += ld_cluster_f32(tc::mapa_shared(off, (uint32_t)r));
-      ((TO *)p.out)[(m0 + col) * p.ldo + n] = out_f32<TO>(
-          s * (p.rw ? p.rw[n] : 1.0f) * (p.ra ? p.ra[m0 + col] : 1.0f));
+    // this CTA's columns are rank, rank + splits, ...; a thread takes four rows of one
+    const uint32_t base = tc::smem_u32(ring) + (threadIdx.x % 32) * 16;
+    const int64_t n = n0 + threadIdx.x % 32 * 4;
+    float rw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rw[j] = p.rw && n + j < p.N ? p.rw[n + j] : 1.0f;
+    const bool pairs = (p.ldo & 1) == 0 && ((uintptr_t)p.out & 3) == 0 && n + 3 < p.N;
+#pragma unroll 2
+    for (int col = rank + (threadIdx.x / 32) * p.splits; col < cols; col += kThreads / 32 * p.splits) {
+      const uint32_t off = base + (uint32_t)col * BM * 4;
+      float4 v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        v[r] = r < p.splits ? ld_cluster_f32x4(tc::mapa_shared(off, (uint32_t)r))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 s = v[0];
+#pragma unroll
+      for (int r = 1; r < 8; ++r) {
+        s.x += v[r].x;
+        s.y += v[r].y;
+        s.z += v[r].z;
+        s.w += v[r].w;
+      }
+      const float ra = p.ra ? p.ra[m0 + col] : 1.0f;
+      alignas(8) TO o[4] = {out_f32<TO>(s.x * rw[0] * ra), out_f32<TO>(s.y * rw[1] * ra),
+                            out_f32<TO>(s.z * rw[2] * ra), out_f32<TO>(s.w * rw[3] * ra)};
+      TO *dst = (TO *)p.out + (m0 + col) * p.ldo + n;
+      if (pairs) {
+        reinterpret_cast<uint32_t *>(dst)[0] = reinterpret_cast<const uint32_t *>(o)[0];
+        reinterpret_cast<uint32_t *>(dst)[1] = reinterpret_cast<const uint32_t *>(o)[1];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j < p.N) dst[j] = o[j];
+      }
     }
     tc::cluster_sync();  // the others have read this CTA's sums
   }
 }
 
-// Tile of tokens, splits of K and CTAs on an SM.
+// Tile of tokens, splits of K and CTAs on an SM: the least of an estimate in SM cycles, whose
+// constants are fits to sweeps over all shapes at 1 to 2048 tokens.
+//   - a k-block of a tile takes max(300 + 1.7 tn, 3.45 tn): the MMAs, below about 170 tokens the
+//     issue of them and their waits;
+//   - the busiest SM has `busy` tiles, together or one after another;
+//   - the memory brings each operand once at 3500 bytes a cycle, L2 what the tiles fill again;
+//     the two times overlap in part (root of the sum of squares);
+//   - a launch costs 6400, splitting K 1400 + 8 tn (two cluster barriers and the exchange).
+// Two CTAs on an SM cover each other's waits and ends, where the tile is small enough for three
+// stages each.
 struct Shape { int tn, splits, per_sm; };
 
-Shape choose(int64_t M, int64_t N, int kb, int sms) {
-  const int64_t n_w = ceil_div(N, BM);
+Shape choose(int64_t M, int64_t N, int64_t K, int sms) {
+  const int64_t n_w = ceil_div(N, BM), groups = ceil_div(ceil_div(K, BK), 4);
+  const double once = (double)(M + N) * K / 3500.0;
   Shape best{16, 1, 1};
   double best_t = 1e30;
-  for (int64_t mt = ceil_div(M, kMaxTn);; ++mt) {
+  const int64_t least = ceil_div(M, kMaxTn);
+  for (int64_t mt = least; mt < least + 6; ++mt) {
     const int tn = (int)(ceil_div(ceil_div(M, mt), 16) * 16);
     const int64_t tiles = n_w * ceil_div(M, tn);
-    for (int s = 1; s <= 8 && s <= (kb + 3) / 4; s *= 2) {
-      // a cycle per 28 codes of W streamed from memory; 2.3 MMA cycles per token column
-      const double per_kb = tn * 2.3 > 300.0 ? tn * 2.3 : 300.0;
-      const double round_t = (double)ceil_div(kb, s) * per_kb + 2500.0 + (s > 1 ? 1500.0 + 8.0 * tn : 0.0);
-      const int64_t rounds = ceil_div(tiles * s, s > 1 ? sms / s * s : sms);
-      const double t = (double)rounds * round_t;
-      if (t < best_t) best_t = t, best = Shape{tn, s, 1};
+    const double c = tn < 172 ? 300 + 1.7 * tn : 3.45 * tn;
+    const double fill = (double)tiles * K * (BM + tn) / 20000.0;
+    for (int s = 1; s <= 8 && s <= groups; ++s) {
+      for (int per = 1; per <= 2; ++per) {
+        const int64_t ctas = tiles * s;
+        if (per == 2 && ((uint32_t)(BM + tn) * BK * 3 > kRingBytesTwo || ctas <= sms || ctas > 2 * sms))
+          continue;
+        if (s > 1 && ctas > (int64_t)per * sms) continue;
+        const int64_t busy = ceil_div(ctas, sms);
+        const double work = (double)busy * 4 * ceil_div(groups, s) * c * (per == 2 ? 0.95 : 1.0);
+        double t = sqrt(work * work + (once + fill) * (once + fill));
+        t += 6400.0 + (s > 1 ? 1400.0 + 8.0 * tn : 0.0) + (per == 1 ? 800.0 * (busy - 1) : 0.0);
+        if (t < best_t) best_t = t, best = Shape{tn, s, per};
+      }
     }
-    if (tn <= 64 || mt > ceil_div(M, kMaxTn) + 4) break;
+    if (tn <= 32) break;
   }
   return best;
 }
@@ -346,7 +393,7 @@ gptq_status run(const Fp8MatmulArgs &g, DevStatus *st, cudaStream_t s) {
   int sms = 0;
   GPTQ_TRY(device_sm_count(&sms));
   const int kb = (int)ceil_div(g.K, BK);
-  const Shape sh = choose(g.M, g.N, kb, sms);
+  const Shape sh = choose(g.M, g.N, g.K, sms);
   MmParams p{};
   p.ae = g.ae; p.ldae = g.ldae;
   p.we = g.we; p.ldwe = g.ldwe;

@@ -27,9 +27,10 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
 
-// Whole warp, converged: true in one lane, the same one every time.  A loop that the whole warp
-// runs and that issues its MMAs under this predicate keeps descriptors and addresses in uniform
-// registers, where the MMA wants them; one that only lane 0 enters moves them there for each MMA.
+// Whole warp, converged: true in one lane.  In code under this predicate the compiler knows that
+// one thread runs, and keeps descriptors and addresses in the uniform registers that the MMA
+// instructions take; under `lane == 0` it moves them there for each MMA (measured: an MMA issued
+// every 330 cycles against every 60).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(
