@@ -176,8 +176,8 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
 
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 12 && tc::elect_one()) {
-      // ---------------- MMA issuer ----------------
+    if (warp == 12) {
+      // ---------------- MMA issuer (the whole warp; one lane issues) ----------------
       constexpr uint32_t id_s = tc::instr_desc(0, 0, kTile, kTile, 0, 0);
       constexpr uint32_t id_o = tc::instr_desc(0, 0, kTile, D, 0, 0);
       // a descriptor holds its address in units of 16 bytes: offsets are added to it
@@ -186,25 +186,33 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       const uint64_t dv = tc::smem_desc_sw128(tc::smem_u32(sv), 16, 1024);
       auto wait = [&](uint64_t *bar, int phase) {
         if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, st);
+        ok = __all_sync(0xffffffffu, ok);
         tc::tc_fence_after();
       };
+      auto commit = [&](uint64_t *bar) {
+        if (tc::elect_one()) tc::mma_commit(bar);
+      };
       auto scores = [&](int b, int u) {
-        const uint64_t q = dq + b * (C::kQ >> 4), k = dk + (u & 1) * (C::kQ >> 4);
+        if (tc::elect_one()) {
+          const uint64_t q = dq + b * (C::kQ >> 4), k = dk + (u & 1) * (C::kQ >> 4);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = ((uint32_t)(i / 4) * C::kChunk + (i % 4) * 32) >> 4;
-          tc::mma_f16(tmem + b * kTile, q + off, k + off, id_s, i > 0);
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = ((uint32_t)(i / 4) * C::kChunk + (i % 4) * 32) >> 4;
+            tc::mma_f16(tmem + b * kTile, q + off, k + off, id_s, i > 0);
+          }
+          tc::mma_commit(&sfull[b]);
         }
-        tc::mma_commit(&sfull[b]);
       };
       auto outputs = [&](int b, int u, bool first) {
-        const uint64_t v = dv + (u & 1) * (C::kV >> 4);
+        if (tc::elect_one()) {
+          const uint64_t v = dv + (u & 1) * (C::kV >> 4);
 #pragma unroll
-        for (int i = 0; i < kTile / 16; ++i)
-          mma_f16_ts(tmem + C::kO + b * D, tmem + b * kTile + 8 * i,
-                     v + (((uint32_t)(i / 4) * C::kVChunk + (i % 4) * 32) >> 4), id_o,
-                     !first || i > 0);
-        tc::mma_commit(&odone[b]);
+          for (int i = 0; i < kTile / 16; ++i)
+            mma_f16_ts(tmem + C::kO + b * D, tmem + b * kTile + 8 * i,
+                       v + (((uint32_t)(i / 4) * C::kVChunk + (i % 4) * 32) >> 4), id_o,
+                       !first || i > 0);
+          tc::mma_commit(&odone[b]);
+        }
       };
       // by tile: the items that it took part in, and the units multiplied
       int items0 = 0, items1 = 0, done0 = 0, done1 = 0;
@@ -236,8 +244,8 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
             }
             if (i + 1 < to) scores(b, u + 1);
           }
-          if (i >= 0) tc::mma_commit(&vempty[u & 1]);
-          if (i + 1 < m) tc::mma_commit(&kempty[(u + 1) & 1]);
+          if (i >= 0) commit(&vempty[u & 1]);
+          if (i + 1 < m) commit(&kempty[(u + 1) & 1]);
         }
         i0 += m;
         if (i0 < count) at.next_item(plan);
