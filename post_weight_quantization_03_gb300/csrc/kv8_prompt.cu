@@ -8,8 +8,8 @@
 //             and writes them to shared memory in the layout that the MMAs read: one conversion
 //             of a key serves 256 rows.  (e4m3 MMAs would run at twice the rate, but a 16-bit
 //             operand costs two or three e4m3 terms, and splitting the probabilities costs the
-//             softmax warps more than converting the values costs here.)  A row of queries is
-//             scaled by a power of two to a maximum of [1, 2); the scores are fp32 in TMEM.
+//             softmax warps more than converting the values costs here.)  A row of bf16 queries
+//             is scaled by a power of two to a maximum of [1, 2); the scores are fp32 in TMEM.
 //   softmax   one row per thread, no exchange between threads.  A block's key exponent is a
 //             factor of its scores, its value exponent lv goes into the exponential:
 //             y = f s + lv,  p = 2^(y - b + 8),  O += p vc,  l += p 2^-lv;  out = O / l.
@@ -22,6 +22,7 @@
 // Warps: 0-3 and 4-7 softmax, a tile each; 8-11 converters; 12 MMA issuer and TMEM owner.
 #include <cudaTypedefs.h>
 #include <limits.h>
+#include <string.h>
 
 #include "kv8.cuh"
 
@@ -446,25 +447,34 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
                 *reinterpret_cast<const uint4 *>(e);
           }
         }
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < 32; i += kAt) {
           const int mr = wrow + i + sub;
           uint4 *const slot = reinterpret_cast<uint4 *>(mine8 + swizzled(mr, part8 % 8));
-          const uint4 w = *slot;
-          float v[8], amax = 0.0f;
+          uint4 w = *slot;
+          float rf = fabsf(g.scale) * kLog2e;
+          if constexpr (std::is_same<T, __half>::value) {  // as they are, but for a negative scale
+            const uint32_t flip = g.scale < 0.0f ? 0x80008000u : 0u;
+            w = make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
+          } else {
+            __nv_bfloat162 h[4];
+            memcpy(h, &w, 16);
+            const __nv_bfloat162 top = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])),
+                                               __hmax2(__habs2(h[2]), __habs2(h[3])));
+            float amax = fmaxf(__low2float(top), __high2float(top));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            v[j] = to_f32(reinterpret_cast<const T *>(&w)[j]);
-            amax = fmaxf(amax, fp8::finite_abs(v[j]));
+            for (int o = 1; o < kLanes; o <<= 1)
+              amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const int e = row_exponent(amax);
+            const float inv = g.scale < 0.0f ? -fp8::pow2(-e) : fp8::pow2(-e);
+            rf *= fp8::pow2(e);
+            w = make_uint4(pack_half2(__low2float(h[0]) * inv, __high2float(h[0]) * inv),
+                           pack_half2(__low2float(h[1]) * inv, __high2float(h[1]) * inv),
+                           pack_half2(__low2float(h[2]) * inv, __high2float(h[2]) * inv),
+                           pack_half2(__low2float(h[3]) * inv, __high2float(h[3]) * inv));
           }
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          const int e = row_exponent(amax);
-          const float inv = g.scale < 0.0f ? -fp8::pow2(-e) : fp8::pow2(-e);
-          if (part8 == 0) factor[b * kTile + mr] = fp8::pow2(e) * fabsf(g.scale) * kLog2e;
-          *slot = make_uint4(pack_half2(v[0] * inv, v[1] * inv), pack_half2(v[2] * inv, v[3] * inv),
-                             pack_half2(v[4] * inv, v[5] * inv), pack_half2(v[6] * inv, v[7] * inv));
+          if (part8 == 0) factor[b * kTile + mr] = rf;
+          *slot = w;
         }
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();  // O of the item before has been read
@@ -590,7 +600,7 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       if (whole) {
         __syncwarp();  // a warp's rows are its own
         const int exist = plan.rows - row0 - wrow;
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < 32; i += kAt) {
           const int64_t off = __shfl_sync(0xffffffffu, o_at, i + sub);
           if (i + sub >= exist) continue;

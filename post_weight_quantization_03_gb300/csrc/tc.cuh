@@ -95,7 +95,8 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, DevSta
 __device__ __forceinline__ bool mbar_wait_compact(uint64_t *bar, uint32_t parity, DevStatus *st) {
   uint64_t t0 = 0;
 #pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
+  for (uint32_t n = 0; !mbar_try_wait(bar, parity); ++n) {
+    if ((n & 31) != 31) continue;  // the timer is read now and then
     const uint64_t t = global_ns();
     if (t0 == 0) t0 = t;
     if (t - t0 > kWaitNs) {
