@@ -36,6 +36,32 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Terms of a sum of e4m3 numbers for operands of type T.
+template <typename T>
+constexpr int kTerms = std::is_same<T, __half>::value ? 3 : 2;
+
+// x (two fp16 numbers, |x| <= 448) = term[0] + term[1] (+ term[2]), two codes each.
+template <int NT>
+__device__ __forceinline__ void split(__half2 x, uint32_t (&term)[NT]) {
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const __nv_fp8x2_storage_t c =
+        __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+    term[i] = c;
+    if (i + 1 < NT) x = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+  }
+}
+
+// Four numbers' terms, a word of codes each.
+template <int NT>
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t (&word)[NT]) {
+  uint32_t lo[NT], hi[NT];
+  split<NT>(__floats2half2_rn(a, b), lo);
+  split<NT>(__floats2half2_rn(c, d), hi);
+#pragma unroll
+  for (int i = 0; i < NT; ++i) word[i] = lo[i] | (hi[i] << 16);
+}
+
 // Two fp16 numbers from the lower (upper) two codes of a word.
 __device__ __forceinline__ uint32_t halves_lo(uint32_t w) {
   uint32_t h;

@@ -62,32 +62,6 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Terms of a sum of e4m3 numbers for operands of type T.
-template <typename T>
-constexpr int kTerms = std::is_same<T, __half>::value ? 3 : 2;
-
-// x (two fp16 numbers, |x| <= 448) = term[0] + term[1] (+ term[2]), two codes each.
-template <int NT>
-__device__ __forceinline__ void split(__half2 x, uint32_t (&term)[NT]) {
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const __nv_fp8x2_storage_t c =
-        __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
-    term[i] = c;
-    if (i + 1 < NT) x = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
-  }
-}
-
-// Four numbers' terms, a word of codes each.
-template <int NT>
-__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t (&word)[NT]) {
-  uint32_t lo[NT], hi[NT];
-  split<NT>(__floats2half2_rn(a, b), lo);
-  split<NT>(__floats2half2_rn(c, d), hi);
-#pragma unroll
-  for (int i = 0; i < NT; ++i) word[i] = lo[i] | (hi[i] << 16);
-}
-
 // c[i] += (sum of the terms) b[i] for N accumulators, the MMAs on one of them kept apart: the
 // first two terms as the tile's two halves, a third one alone.  x, y: the words of the first
 // and second 16 elements of K.

@@ -4,12 +4,13 @@
 // cache head for 256 rows.  The heads of a group and the new tokens are the rows; an item is 256
 // rows of one cache head, two MMA tiles of 128 that share every key and value.
 //
-//   operands  kind::f16.  A converter warp group reads the codes, turns them into fp16 (exact)
-//             and writes them to shared memory in the layout that the MMAs read: one conversion
-//             of a key serves 256 rows.  (e4m3 MMAs would run at twice the rate, but a 16-bit
-//             operand costs two or three e4m3 terms, and splitting the probabilities costs the
-//             softmax warps more than converting the values costs here.)  A row of bf16 queries
-//             is scaled by a power of two to a maximum of [1, 2); the scores are fp32 in TMEM.
+//   scores    kind::f8f6f4 straight on the cached codes, which TMA brings into the layout that the
+//             MMA reads.  The queries are sums of two (bf16) or three (fp16) e4m3 terms, exact down
+//             to 2^-17 of the row's maximum: as many MMAs as fp16 operands would take (half as
+//             many again for fp16 queries), and the keys need no conversion.
+//   outputs   kind::f16: a converter warp group turns the value codes into fp16 (exact), once for
+//             256 rows.  (Splitting the probabilities into e4m3 terms instead costs the softmax
+//             warps more than converting the values costs here.)
 //   softmax   one row per thread, no exchange between threads.  A block's key exponent is a
 //             factor of its scores, its value exponent lv goes into the exponential:
 //             y = f s + lv,  p = 2^(y - b + 8),  O += p vc,  l += p 2^-lv;  out = O / l.
@@ -19,7 +20,8 @@
 //             the second product's A operand.
 //   overlap   while one tile's softmax runs, the tensor core multiplies for the other.
 //
-// Warps: 0-3 and 4-7 softmax, a tile each; 8-11 converters; 12 MMA issuer and TMEM owner.
+// Warps: 0-3 and 4-7 softmax, a tile each; 8-11 copies and converters; 12 MMA issuer and TMEM
+// owner.
 #include <cudaTypedefs.h>
 #include <limits.h>
 #include <string.h>
@@ -38,17 +40,21 @@ using PromptPlan = Plan<2 * kTile, kTile, 2>;
 // at launch: a softmax thread holds its row's 128 scores.
 constexpr int kThreads = 512;
 constexpr int kInfo = 4;
+constexpr uint32_t kChunk = kTile * 128;        // 128 rows of 128 bytes
 constexpr float kLazy = 6.0f;
 
-template <int D>
+constexpr int kKStages = 3, kVStages = 2;
+
+template <int D, int NT>
 struct Prompt {
-  static constexpr uint32_t kChunk = kTile * 128;             // 128 rows of 128 bytes
-  static constexpr uint32_t kQ = kTile * D * 2;               // a tile of queries (or keys)
-  static constexpr uint32_t kV = D * kTile * 2;               // values, channel-major
+  static constexpr uint32_t kTerm = kTile * D;                // a term of a tile of queries
+  static constexpr uint32_t kQ = NT * kTerm;                  // its rows of 2 D bytes fit, too
+  static constexpr uint32_t kK = kTile * D;                   // a unit's keys
+  static constexpr uint32_t kV = D * kTile * 2;               // its values, fp16, channel-major
   static constexpr uint32_t kVChunk = D * 128;                // 64 tokens of them
   static constexpr uint32_t kHalf = kTok * D;                 // bytes of K (or V) of a block
-  static constexpr size_t kSmem =
-      1024 + 2 * kQ + 2 * kQ + 2 * kV + 4 * kHalf + kInfo * 32 + 2 * kTile * 4 + 192;
+  static constexpr size_t kSmem = 1024 + 2 * kQ + kKStages * kK + kVStages * kV + 2 * kHalf +
+                                  kInfo * 32 + 2 * kTile * 4 + 256;
   static constexpr uint32_t kCols = 512;
   static constexpr uint32_t kO = 2 * kTile;                   // TMEM column of the first O
 };
@@ -99,6 +105,24 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// D[tmem] (+)= A[smem] B[smem]^T, kind::f8f6f4 (e4m3), one thread.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Descriptor of K-major rows of D bytes (64 or 128) with the swizzle of that width.
+template <int D>
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) |
+         ((uint64_t)(8 * D >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)(D == 128 ? 2 : 4) << 61);
+}
+
 // Two fp32 numbers at a time: a * b + c, a + b.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -127,20 +151,28 @@ __device__ __forceinline__ uint32_t swizzled(int row, int u) {
   return (uint32_t)(row * 128 + ((u ^ (row & 7)) << 4));
 }
 
+// The same for rows of D bytes.
+template <int D>
+__device__ __forceinline__ uint32_t swizzled_row(int row, int u) {
+  return (uint32_t)(row * D + ((D == 128 ? u ^ (row & 7) : u ^ (row >> 1 & 3)) << 4));
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
-  using C = Prompt<D>;
+prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float *part,
+              DevStatus *st) {
+  constexpr int NT = kTerms<T>;
+  using C = Prompt<D, NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *sq = smem, *sk = sq + 2 * C::kQ, *sv = sk + 2 * C::kQ;
-  uint8_t *raw_k = sv + 2 * C::kV, *raw_v = raw_k + 2 * C::kHalf;  // codes of a unit
+  uint8_t *sq = smem, *sk = sq + 2 * C::kQ, *sv = sk + kKStages * C::kK;
+  uint8_t *raw_v = sv + kVStages * C::kV;         // codes of a unit's values
   Info *info = (Info *)(raw_v + 2 * C::kHalf);
   float *factor = (float *)(info + kInfo);        // of each row's scores
   uint64_t *qfull = (uint64_t *)(factor + 2 * kTile);   // [2], by tile
   uint64_t *sfull = qfull + 2, *pfull = sfull + 2, *odone = pfull + 2;
-  uint64_t *kfull = odone + 2, *kempty = kfull + 2, *vfull = kempty + 2, *vempty = vfull + 2;
-  uint64_t *kraw = vempty + 2, *vraw = kraw + 1;
+  uint64_t *kfull = odone + 2, *kempty = kfull + kKStages;
+  uint64_t *vfull = kempty + kKStages, *vempty = vfull + kVStages, *vraw = vempty + kVStages;
   uint32_t *tmem_slot = (uint32_t *)(vraw + 1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
@@ -150,12 +182,13 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       tc::mbar_init(&sfull[b], 1);
       tc::mbar_init(&pfull[b], 4);
       tc::mbar_init(&odone[b], 1);
-      tc::mbar_init(&kfull[b], 4);
-      tc::mbar_init(&kempty[b], 1);
       tc::mbar_init(&vfull[b], 4);
       tc::mbar_init(&vempty[b], 1);
     }
-    tc::mbar_init(kraw, 1);
+    for (int i = 0; i < kKStages; ++i) {
+      tc::mbar_init(&kfull[i], 1);
+      tc::mbar_init(&kempty[i], 1);
+    }
     tc::mbar_init(vraw, 1);
     tc::mbar_fence_init();
   }
@@ -182,8 +215,7 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       constexpr uint32_t id_s = tc::instr_desc(0, 0, kTile, kTile, 0, 0);
       constexpr uint32_t id_o = tc::instr_desc(0, 0, kTile, D, 0, 0);
       // a descriptor holds its address in units of 16 bytes: offsets are added to it
-      const uint64_t dq = tc::smem_desc_sw128(tc::smem_u32(sq), 16, 1024);
-      const uint64_t dk = tc::smem_desc_sw128(tc::smem_u32(sk), 16, 1024);
+      const uint64_t dq = desc_rows<D>(tc::smem_u32(sq)), dk = desc_rows<D>(tc::smem_u32(sk));
       const uint64_t dv = tc::smem_desc_sw128(tc::smem_u32(sv), 16, 1024);
       auto wait = [&](uint64_t *bar, int phase) {
         if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, st);
@@ -195,12 +227,11 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       };
       auto scores = [&](int b, int u) {
         if (tc::elect_one()) {
-          const uint64_t q = dq + b * (C::kQ >> 4), k = dk + (u & 1) * (C::kQ >> 4);
+          const uint64_t q = dq + b * (C::kQ >> 4), k = dk + u % kKStages * (C::kK >> 4);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t off = ((uint32_t)(i / 4) * C::kChunk + (i % 4) * 32) >> 4;
-            tc::mma_f16(tmem + b * kTile, q + off, k + off, id_s, i > 0);
-          }
+          for (int i = 0; i < NT * (D / 32); ++i)
+            mma_f8(tmem + b * kTile, q + ((i / (D / 32) * C::kTerm + i % (D / 32) * 32) >> 4),
+                   k + 2 * (i % (D / 32)), id_s, i > 0);
           tc::mma_commit(&sfull[b]);
         }
       };
@@ -232,7 +263,7 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
         for (int i = -1; i < m && ok; ++i) {
           const int u = i0 + i;
           if (i >= 0) wait(&vfull[u & 1], u >> 1);
-          if (i + 1 < m) wait(&kfull[(u + 1) & 1], (u + 1) >> 1);
+          if (i + 1 < m) wait(&kfull[(u + 1) % kKStages], (u + 1) / kKStages);
 #pragma unroll 1
           for (int b = 0; b < 2; ++b) {
             const int to = b ? to1 : to0;
@@ -246,17 +277,17 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
             if (i + 1 < to) scores(b, u + 1);
           }
           if (i >= 0) commit(&vempty[u & 1]);
-          if (i + 1 < m) commit(&kempty[(u + 1) & 1]);
+          if (i + 1 < m) commit(&kempty[(u + 1) % kKStages]);
         }
         i0 += m;
         if (i0 < count) at.next_item(plan);
       }
     }
   } else if (warp >= 8) {
-    // ---------------- converters ----------------
-    // Contiguous copies bring a unit's codes; each thread turns pieces of 16 into fp16, one row
-    // of K (channel of V) in every 32: four lanes take 64 codes of a row, so that eight lanes'
-    // accesses of 16 bytes fall into different banks.
+    // ---------------- copies and converters ----------------
+    // One thread asks for a unit's keys (TMA) and value codes (contiguous copies); all turn pieces
+    // of 16 value codes into fp16, one channel in every 32 a thread: four lanes take the 64 tokens
+    // of a block, so that eight lanes' accesses of 16 bytes fall into different banks.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int ct = threadIdx.x - 256, x = ct % 4, r0 = ct / 4;
     Cursor c = at;              // of the unit whose blocks are looked up
@@ -287,15 +318,6 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       }
       left = len - blk * kTile;  // tokens of the unit that exist
     };
-    auto copy = [&](uint8_t *dst, const uint8_t *src, uint64_t *bar) {
-      if (ct != 0) return;
-      tc::fence_proxy_async_smem();
-      tc::mbar_arrive_expect_tx(bar, (place[0] >= 0 ? C::kHalf : 0) + (place[1] >= 0 ? C::kHalf : 0));
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (place[h] >= 0)
-          tc::bulk_load(dst + h * C::kHalf, src + (int64_t)place[h] * C::kHalf, C::kHalf, bar);
-    };
     const uint32_t at0 = swizzled(r0, 2 * x), at1 = swizzled(r0, 2 * x + 1);
     auto put = [&](uint8_t *rows, const uint4 &q) {
       *reinterpret_cast<uint4 *>(rows + at0) =
@@ -306,82 +328,71 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
     auto wait = [&](uint64_t *bar, int phase) {
       if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, st);
     };
-    auto arrive = [&](uint64_t *bar) {
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar);
-    };
     // step u: convert unit u, have unit u + 1 copied, look unit u + 2 up
 #pragma unroll 1
     for (int u = count > 0 ? -2 : 0; u < count; ++u) {
-      const int s = u & 1, tokens = left;
-      const int there = (place[0] >= 0 ? 1 : 0) | (place[1] >= 0 ? 2 : 0);
-      if (u >= 0) {
-      // keys, and what the softmax has to know of the unit (four units back has been read: the
-      // keys of two units back were multiplied after the probabilities of three units back)
-      wait(kraw, u);
-      if (u >= 2) wait(&kempty[s], (u - 2) >> 1);
-      if (ct == 0) {
-        Info &f = info[u % kInfo];
+      const int tokens = left, there = (place[0] >= 0 ? 1 : 0) | (place[1] >= 0 ? 2 : 0);
+      const bool next = u >= -1 && u + 1 < count;
+      uint32_t bytes = 0;
+      if (u >= -1) locate();    // the next unit
+      if (next && ct == 0) {
+        // its keys, and what the softmax has to know of it (the unit four back has been read: the
+        // keys of three units back were multiplied after the probabilities of four back)
+        const int n = u + 1, s = n % kKStages;
+        if (n >= kKStages) wait(&kempty[s], n / kKStages - 1);
+        Info &f = info[n % kInfo];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           f.ks[h] = fp8::exp_value((uint8_t)ex[h]);
           f.lv[h] = (ex[h] >> 8) - fp8::kBias;
-          f.there[h] = there >> h & 1;
+          f.there[h] = place[h] >= 0;
+          bytes += place[h] >= 0 ? C::kHalf : 0;
         }
-      }
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {       // block; its rows r0 + 32 i, odd rows the other chunk first
-        uint4 q[D / 32];
+        tc::mbar_arrive_expect_tx(&kfull[s], bytes);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const int ch = D == 128 ? (i / 2) ^ (r0 & 1) : 0;
-          q[i] = there >> h & 1 ? *reinterpret_cast<const uint4 *>(
-                                      raw_k + h * C::kHalf + (r0 + i % 2 * 32) * D + ch * 64 + x * 16)
-                                : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const int ch = D == 128 ? (i / 2) ^ (r0 & 1) : 0;
-          put(sk + s * C::kQ + ch * C::kChunk + (h * kTok + i % 2 * 32) * 128, q[i]);
-        }
-      }
-      arrive(&kfull[s]);
-      tc::named_barrier(1, 128);  // the codes have been read
-      }
-      if (u >= -1) {
-        locate();                 // of the next unit
-        if (u + 1 < count) copy(raw_k, g.k, kraw);
+        for (int h = 0; h < 2; ++h)
+          if (place[h] >= 0)
+            tc::tma_load_3d(sk + s * C::kK + h * C::kHalf, &mk, 0, 0, place[h], &kfull[s]);
       }
       if (u >= 0) {
-      // values; those past the sequence's end may be NaN codes and become zeros
-      wait(vraw, u);
-      if (u >= 2) wait(&vempty[s], (u - 2) >> 1);
+        // values; those past the sequence's end may be NaN codes and become zeros
+        const int s = u % kVStages;
+        wait(vraw, u);
+        if (u >= kVStages) wait(&vempty[s], u / kVStages - 1);
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {       // block; its channels r0 + 32 i
-        const int live = tokens - h * kTok - x * 16;
-        uint4 q[D / 32];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          q[i] = there >> h & 1 ? *reinterpret_cast<const uint4 *>(raw_v + h * C::kHalf +
-                                                                   (r0 + i * 32) * kTok + x * 16)
-                                : make_uint4(0, 0, 0, 0);
-        if (live < 16) {
-          auto mask = [&](int at) {
-            return live <= at ? 0u : (live >= at + 4 ? ~0u : (1u << (8 * (live - at))) - 1u);
-          };
-          const uint4 m = make_uint4(mask(0), mask(4), mask(8), mask(12));
+        for (int h = 0; h < 2; ++h) {       // block; its channels r0 + 32 i
+          const int live = tokens - h * kTok - x * 16;
+          uint4 q[D / 32];
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
-            q[i] = make_uint4(q[i].x & m.x, q[i].y & m.y, q[i].z & m.z, q[i].w & m.w);
-        }
+            q[i] = there >> h & 1 ? *reinterpret_cast<const uint4 *>(raw_v + h * C::kHalf +
+                                                                     (r0 + i * 32) * kTok + x * 16)
+                                  : make_uint4(0, 0, 0, 0);
+          if (live < 16) {
+            auto mask = [&](int at) {
+              return live <= at ? 0u : (live >= at + 4 ? ~0u : (1u << (8 * (live - at))) - 1u);
+            };
+            const uint4 m = make_uint4(mask(0), mask(4), mask(8), mask(12));
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) put(sv + s * C::kV + h * C::kVChunk + i * 32 * 128, q[i]);
+            for (int i = 0; i < D / 32; ++i)
+              q[i] = make_uint4(q[i].x & m.x, q[i].y & m.y, q[i].z & m.z, q[i].w & m.w);
+          }
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) put(sv + s * C::kV + h * C::kVChunk + i * 32 * 128, q[i]);
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&vfull[s]);
+        tc::named_barrier(1, 128);  // the codes have been read
       }
-      arrive(&vfull[s]);
-      tc::named_barrier(1, 128);
+      if (next && ct == 0) {
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive_expect_tx(vraw, bytes);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (place[h] >= 0)
+            tc::bulk_load(raw_v + h * C::kHalf, g.v + (int64_t)place[h] * C::kHalf, C::kHalf, vraw);
       }
-      if (u >= -1 && u + 1 < count) copy(raw_v, g.v, vraw);
       look_up(u + 2);
     }
   } else {
@@ -412,69 +423,69 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
                            (int64_t)(at.head * plan.group + hq) * g.q_stride[2];
       const int64_t o_at = seq * g.o_stride[0] + rq * g.o_stride[1] +
                            (int64_t)(at.head * plan.group + hq) * g.o_stride[2];
-      // Rows move D / 8 lanes to a row, 16 bytes a lane; `kAt` rows of the warp's 32 at a time.
-      constexpr int kLanes = D / 8, kAt = 32 / kLanes;
-      const int sub = lane / kLanes, part8 = lane % kLanes, wrow = warp % 4 * 32;
-      uint8_t *const mine8 = q_tile + part8 / 8 * C::kChunk;
-      // Queries, scaled to a maximum of [1, 2), fp16, K-major; all loads in flight at once, the
-      // rest in a small loop (code that runs once an item costs its instructions' fetch).
+      // Queries: 16 elements a lane, D / 16 lanes to a row, `kAt` rows of the warp's 32 at a time;
+      // scaled to a maximum of [128, 256) and split into terms, K-major.  All loads in flight at
+      // once, left in the lane's own slots; the rest in a small loop (code that runs once an item
+      // costs its instructions' fetch).
       float f = 0.0f;
       if (mine > 0) {
-        const T *q = (const T *)g.q + 8 * part8;
+        constexpr int kLanes = D / 16, kAt = 32 / kLanes;
+        const int sub = lane / kLanes, piece16 = lane % kLanes, wrow = warp % 4 * 32;
+        const T *q = (const T *)g.q + 16 * piece16;
         const int exist = plan.rows - row0 - wrow;  // of the warp's rows
+        auto slot = [&](int mr, int term) {
+          return reinterpret_cast<uint4 *>(q_tile + term * C::kTerm + swizzled_row<D>(mr, piece16));
+        };
         if (g.vec_q) {
-#pragma unroll 1
-          for (int i0 = 0; i0 < 32; i0 += 8 * kAt) {
-            uint4 raw[8];
+          uint4 raw[2 * 32 / kAt];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int mr = i0 + i * kAt + sub;
-              const int64_t off = __shfl_sync(0xffffffffu, q_at, mr);
-              raw[i] = mr < exist ? *reinterpret_cast<const uint4 *>(q + off) : make_uint4(0, 0, 0, 0);
-            }
+          for (int i = 0; i < 32 / kAt; ++i) {
+            const int mr = i * kAt + sub;
+            const uint4 *at16 = reinterpret_cast<const uint4 *>(q + __shfl_sync(0xffffffffu, q_at, mr));
+            raw[2 * i] = mr < exist ? at16[0] : make_uint4(0, 0, 0, 0);
+            raw[2 * i + 1] = mr < exist ? at16[1] : make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4 *>(mine8 + swizzled(wrow + i0 + i * kAt + sub, part8 % 8)) = raw[i];
+          for (int i = 0; i < 32 / kAt; ++i) {
+            *slot(wrow + i * kAt + sub, 0) = raw[2 * i];
+            *slot(wrow + i * kAt + sub, 1) = raw[2 * i + 1];
           }
         } else {
 #pragma unroll 1
-          for (int i = 0; i < 32; i += kAt) {
-            const int64_t off = __shfl_sync(0xffffffffu, q_at, i + sub);
+          for (int i = 0; i < 64 / kAt; ++i) {
+            const int mr = i / 2 * kAt + sub;
+            const int64_t off = __shfl_sync(0xffffffffu, q_at, mr) + 8 * (i % 2);
             alignas(16) T e[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = i + sub < exist ? q[off + j] : from_f32<T>(0.0f);
-            *reinterpret_cast<uint4 *>(mine8 + swizzled(wrow + i + sub, part8 % 8)) =
-                *reinterpret_cast<const uint4 *>(e);
+            for (int j = 0; j < 8; ++j) e[j] = mr < exist ? q[off + j] : from_f32<T>(0.0f);
+            *slot(wrow + mr, i % 2) = *reinterpret_cast<const uint4 *>(e);
           }
         }
-#pragma unroll 4
-        for (int i = 0; i < 32; i += kAt) {
-          const int mr = wrow + i + sub;
-          uint4 *const slot = reinterpret_cast<uint4 *>(mine8 + swizzled(mr, part8 % 8));
-          uint4 w = *slot;
-          float rf = fabsf(g.scale) * kLog2e;
-          if constexpr (std::is_same<T, __half>::value) {  // as they are, but for a negative scale
-            const uint32_t flip = g.scale < 0.0f ? 0x80008000u : 0u;
-            w = make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
-          } else {
-            __nv_bfloat162 h[4];
-            memcpy(h, &w, 16);
-            const __nv_bfloat162 top = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])),
-                                               __hmax2(__habs2(h[2]), __habs2(h[3])));
-            float amax = fmaxf(__low2float(top), __high2float(top));
+#pragma unroll 2
+        for (int i = 0; i < 32 / kAt; ++i) {
+          const int mr = wrow + i * kAt + sub;
+          const uint4 w[2] = {*slot(mr, 0), *slot(mr, 1)};
+          const T *e16 = reinterpret_cast<const T *>(w);
+          float v[16], amax = 0.0f;
 #pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1)
-              amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const int e = row_exponent(amax);
-            const float inv = g.scale < 0.0f ? -fp8::pow2(-e) : fp8::pow2(-e);
-            rf *= fp8::pow2(e);
-            w = make_uint4(pack_half2(__low2float(h[0]) * inv, __high2float(h[0]) * inv),
-                           pack_half2(__low2float(h[1]) * inv, __high2float(h[1]) * inv),
-                           pack_half2(__low2float(h[2]) * inv, __high2float(h[2]) * inv),
-                           pack_half2(__low2float(h[3]) * inv, __high2float(h[3]) * inv));
+          for (int j = 0; j < 16; ++j) {
+            v[j] = to_f32(e16[j]);
+            amax = fmaxf(amax, fp8::finite_abs(v[j]));
           }
-          if (part8 == 0) factor[b * kTile + mr] = rf;
-          *slot = w;
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const int e = row_exponent(amax) - 7;
+          const float inv = g.scale < 0.0f ? -fp8::pow2(-e) : fp8::pow2(-e);
+          if (piece16 == 0) factor[b * kTile + mr] = fp8::pow2(e) * fabsf(g.scale) * kLog2e;
+          uint32_t word[4][NT];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            split4<NT>(v[4 * j] * inv, v[4 * j + 1] * inv, v[4 * j + 2] * inv, v[4 * j + 3] * inv,
+                       word[j]);
+#pragma unroll
+          for (int term = 0; term < NT; ++term)
+            *slot(mr, term) = make_uint4(word[0][term], word[1][term], word[2][term], word[3][term]);
         }
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();  // O of the item before has been read
@@ -587,7 +598,7 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) e[q] = from_f32<T>(__uint_as_float(x[j + q]));
             const int u = (c + j) / 8;
-            *reinterpret_cast<uint4 *>(q_tile + u / 8 * C::kChunk + swizzled(row, u % 8)) =
+            *reinterpret_cast<uint4 *>(q_tile + u / 8 * kChunk + swizzled(row, u % 8)) =
                 *reinterpret_cast<const uint4 *>(e);
           }
         } else {
@@ -599,6 +610,9 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
       }
       if (whole) {
         __syncwarp();  // a warp's rows are its own
+        constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // 16 bytes a lane
+        const int sub = lane / kLanes, part8 = lane % kLanes, wrow = warp % 4 * 32;
+        const uint8_t *mine8 = q_tile + part8 / 8 * kChunk;
         const int exist = plan.rows - row0 - wrow;
 #pragma unroll 4
         for (int i = 0; i < 32; i += kAt) {
@@ -630,14 +644,18 @@ prompt_kernel(Kv8AttentionArgs g, float *part, DevStatus *st) {
 
 template <typename T, int D>
 gptq_status run(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
-  using C = Prompt<D>;
+  using C = Prompt<D, kTerms<T>>;
   GPTQ_TRY(ensure_smem_attr((const void *)prompt_kernel<T, D>, (int)C::kSmem));
   int sms = 0;
   GPTQ_TRY(device_sm_count(&sms));
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   float *part = (float *)((char *)ws + 256);
-  GPTQ_TRY(launch_early(prompt_kernel<T, D>, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, 1, s, g,
-                        part, (DevStatus *)ws));
+  CUtensorMap mk;
+  memset(&mk, 0, sizeof(mk));  // an empty cache is never read
+  if (g.n_blocks > 0 && !tc::make_tmap_bytes_3d(&mk, g.k, g.n_blocks * g.n_kv, kTok, D))
+    return GPTQ_ERR_UNSUPPORTED;
+  GPTQ_TRY(launch_early(prompt_kernel<T, D>, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, 1, s, mk,
+                        g, part, (DevStatus *)ws));
   return launch_early(join_kernel<T, D, PromptPlan>, dim3((unsigned)ctas - 1, 8), dim3(128), 0, 1, s,
                       g, (const float *)part, 1, ctas);
 }

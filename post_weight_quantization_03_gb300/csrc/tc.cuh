@@ -125,6 +125,16 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *m, int
       : "memory");
 }
 
+// tma_load_2d for three coordinates.
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
+                                            int32_t z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)m), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Contiguous global -> shared bulk copy (no tensor map); `bytes` a multiple of 16, both
 // addresses 16-byte aligned; completion counted on `bar`.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
@@ -418,6 +428,10 @@ __host__ __device__ constexpr uint32_t instr_desc(uint32_t a_fmt, uint32_t b_fmt
 // ---------------------------------------------------------------------------------------
 bool make_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, int64_t rows,
                   int64_t cols, int64_t ld_bytes, int box_cols, int box_rows);
+
+// 3D tensor map over [n, rows, cols] bytes without gaps, box = one [rows, cols] matrix; cols is 64
+// or 128 and the swizzle is that wide.
+bool make_tmap_bytes_3d(CUtensorMap *m, const void *base, int64_t n, int rows, int cols);
 
 }  // namespace tc
 }  // namespace gptq

@@ -492,6 +492,19 @@ bool tc::make_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tc::make_tmap_bytes_3d(CUtensorMap *m, const void *base, int64_t n, int rows, int cols) {
+  auto fn = encode_fn();
+  if (!fn || ((uintptr_t)base & 15) || n < 1 || (cols != 64 && cols != 128)) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
+  cuuint64_t strides[2] = {(cuuint64_t)cols, (cuuint64_t)cols * rows};
+  cuuint32_t box[3] = {(cuuint32_t)cols, (cuuint32_t)rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, (void *)base, dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Tensor-core path of launch_gemm_nt.  Requirements (else returns UNSUPPORTED so the
 // caller can take the CUDA-core kernel): both operands have head and tail, 16-byte
 // aligned bases and row pitches, and K offsets that are multiples of 4 elements.
