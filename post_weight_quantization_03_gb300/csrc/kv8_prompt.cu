@@ -15,13 +15,14 @@
 //             factor of its scores, its value exponent lv goes into the exponential:
 //             y = f s + lv,  p = 2^(y - b + 8),  O += p vc,  l += p 2^-lv;  out = O / l.
 //             b follows the maximum of y lazily: O (in TMEM) and l are rescaled only when y
-//             exceeds b by 2^6 (p stays within fp16's range), which past a row's first tiles is
-//             rare.  p is rounded to fp16 once and replaces the scores in TMEM, from where it is
-//             the second product's A operand.
+//             exceeds b by 6 (p stays within fp16's range), which past a row's first blocks is
+//             rare; so the maximum is taken beside the exponentials, not before them.  p is
+//             rounded to fp16 once and replaces the scores in TMEM, from where it is the second
+//             product's A operand, a block of 64 tokens at a time.
 //   overlap   while one tile's softmax runs, the tensor core multiplies for the other.
 //
-// Warps: 0-3 and 4-7 softmax, a tile each; 8-11 copies and converters; 12 MMA issuer and TMEM
-// owner.
+// Warps: 0-3 and 4-7 softmax, a tile each; 8-11 copies and converters; 12 and 13 MMA issuers, a
+// tile each (12 owns TMEM).
 #include <cudaTypedefs.h>
 #include <limits.h>
 #include <string.h>
@@ -170,8 +171,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
   Info *info = (Info *)(raw_v + 2 * C::kHalf);
   float *factor = (float *)(info + kInfo);        // of each row's scores
   uint64_t *qfull = (uint64_t *)(factor + 2 * kTile);   // [2], by tile
-  uint64_t *sfull = qfull + 2, *pfull = sfull + 2, *odone = pfull + 2;
-  uint64_t *kfull = odone + 2, *kempty = kfull + kKStages;
+  // by tile and block of a unit (a barrier has one phase a unit: its waiters never fall two behind)
+  uint64_t *sfull = qfull + 2, *pfull = sfull + 4, *odone = pfull + 4;
+  uint64_t *kfull = odone + 4, *kempty = kfull + kKStages;
   uint64_t *vfull = kempty + kKStages, *vempty = vfull + kVStages, *vraw = vempty + kVStages;
   uint32_t *tmem_slot = (uint32_t *)(vraw + 1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
@@ -179,15 +181,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&qfull[b], 4);
-      tc::mbar_init(&sfull[b], 1);
-      tc::mbar_init(&pfull[b], 4);
-      tc::mbar_init(&odone[b], 1);
+      tc::mbar_init(&sfull[2 * b], 1);
+      tc::mbar_init(&sfull[2 * b + 1], 1);
+      tc::mbar_init(&pfull[2 * b], 4);
+      tc::mbar_init(&pfull[2 * b + 1], 4);
+      tc::mbar_init(&odone[2 * b], 1);
+      tc::mbar_init(&odone[2 * b + 1], 1);
       tc::mbar_init(&vfull[b], 4);
-      tc::mbar_init(&vempty[b], 1);
+      tc::mbar_init(&vempty[b], 2);
     }
     for (int i = 0; i < kKStages; ++i) {
       tc::mbar_init(&kfull[i], 1);
-      tc::mbar_init(&kempty[i], 1);
+      tc::mbar_init(&kempty[i], 2);
     }
     tc::mbar_init(vraw, 1);
     tc::mbar_fence_init();
@@ -210,9 +215,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
 
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 12) {
-      // ---------------- MMA issuer (the whole warp; one lane issues) ----------------
-      constexpr uint32_t id_s = tc::instr_desc(0, 0, kTile, kTile, 0, 0);
+    if (warp < 14) {
+      // ---------------- MMA issuers, one for each tile (the whole warp; one lane issues) ----------------
+      const int b = warp - 12;
+      constexpr uint32_t id_s = tc::instr_desc(0, 0, kTile, kTok, 0, 0);
       constexpr uint32_t id_o = tc::instr_desc(0, 0, kTile, D, 0, 0);
       // a descriptor holds its address in units of 16 bytes: offsets are added to it
       const uint64_t dq = desc_rows<D>(tc::smem_u32(sq)), dk = desc_rows<D>(tc::smem_u32(sk));
@@ -225,56 +231,54 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
       auto commit = [&](uint64_t *bar) {
         if (tc::elect_one()) tc::mma_commit(bar);
       };
-      auto scores = [&](int b, int u) {
+      auto scores = [&](int u, int h) {               // of the unit's block h
         if (tc::elect_one()) {
-          const uint64_t q = dq + b * (C::kQ >> 4), k = dk + u % kKStages * (C::kK >> 4);
+          const uint64_t q = dq + b * (C::kQ >> 4);
+          const uint64_t k = dk + (u % kKStages * C::kK + h * C::kHalf >> 4);
 #pragma unroll
           for (int i = 0; i < NT * (D / 32); ++i)
-            mma_f8(tmem + b * kTile, q + ((i / (D / 32) * C::kTerm + i % (D / 32) * 32) >> 4),
+            mma_f8(tmem + b * kTile + h * kTok, q + ((i / (D / 32) * C::kTerm + i % (D / 32) * 32) >> 4),
                    k + 2 * (i % (D / 32)), id_s, i > 0);
-          tc::mma_commit(&sfull[b]);
+          tc::mma_commit(&sfull[2 * b + h]);
         }
       };
-      auto outputs = [&](int b, int u, bool first) {
+      auto outputs = [&](int u, int h, bool first) {  // of the unit's block h
         if (tc::elect_one()) {
-          const uint64_t v = dv + (u & 1) * (C::kV >> 4);
+          const uint64_t v = dv + ((u & 1) * C::kV + h * C::kVChunk >> 4);
+          const uint32_t p = tmem + b * kTile + h * kTok;
 #pragma unroll
-          for (int i = 0; i < kTile / 16; ++i)
-            mma_f16_ts(tmem + C::kO + b * D, tmem + b * kTile + 8 * i,
-                       v + (((uint32_t)(i / 4) * C::kVChunk + (i % 4) * 32) >> 4), id_o,
-                       !first || i > 0);
-          tc::mma_commit(&odone[b]);
+          for (int i = 0; i < kTok / 16; ++i)
+            mma_f16_ts(tmem + C::kO + b * D, p + 8 * i, v + 2 * i, id_o, !first || i > 0);
+          tc::mma_commit(&odone[2 * b + h]);
         }
       };
-      // by tile: the items that it took part in, and the units multiplied
-      int items0 = 0, items1 = 0, done0 = 0, done1 = 0;
+      int items = 0, done = 0;  // that the tile took part in: items; units multiplied
 #pragma unroll 1
       for (int i0 = 0; i0 < count && ok;) {
         const int m = at.nblk - at.blk < count - i0 ? at.nblk - at.blk : count - i0;
-        const int len = seq_length(g, at.entry / plan.tiles), row0 = at.entry % plan.tiles * 2 * kTile;
-        // units of this item, counted from the share's first one, that each tile takes part in
-        auto part_of = [&](int b) {
-          const int nb = (plan.seen(len, row0 + b * kTile, row0 + (b + 1) * kTile) + kTile - 1) / kTile;
-          return nb - at.blk < m ? (nb - at.blk < 0 ? 0 : nb - at.blk) : m;
-        };
-        const int to0 = part_of(0), to1 = part_of(1);
-        // step i: the outputs of unit i, then the scores of unit i + 1
+        const int len = seq_length(g, at.entry / plan.tiles);
+        const int row0 = at.entry % plan.tiles * 2 * kTile + b * kTile;
+        // units of this item, counted from the share's first one, that the tile takes part in
+        const int nb = (plan.seen(len, row0, row0 + kTile) + kTile - 1) / kTile - at.blk;
+        const int to = nb < m ? (nb < 0 ? 0 : nb) : m;
+        // step i: block by block, the outputs of unit i and then, where the scores were, those of
+        // unit i + 1: they are there before the softmax is done with the other block
 #pragma unroll 1
         for (int i = -1; i < m && ok; ++i) {
           const int u = i0 + i;
-          if (i >= 0) wait(&vfull[u & 1], u >> 1);
           if (i + 1 < m) wait(&kfull[(u + 1) % kKStages], (u + 1) / kKStages);
+          if (i >= 0) wait(&vfull[u & 1], u >> 1);
+          if (i < to && to > 0) {
+            if (i < 0) wait(&qfull[b], items++);
 #pragma unroll 1
-          for (int b = 0; b < 2; ++b) {
-            const int to = b ? to1 : to0;
-            if (i >= to || to == 0) continue;
-            if (i < 0) {
-              wait(&qfull[b], b ? items1++ : items0++);
-            } else {
-              wait(&pfull[b], b ? done1++ : done0++);
-              outputs(b, u, i == 0);
+            for (int h = 0; h < 2; ++h) {
+              if (i >= 0) {
+                wait(&pfull[2 * b + h], done);
+                outputs(u, h, i == 0 && h == 0);
+              }
+              if (i + 1 < to) scores(u + 1, h);
             }
-            if (i + 1 < to) scores(b, u + 1);
+            if (i >= 0) ++done;
           }
           if (i >= 0) commit(&vempty[u & 1]);
           if (i + 1 < m) commit(&kempty[(u + 1) % kKStages]);
@@ -402,7 +406,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
     const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
     const uint32_t ts = tmem + lanes + b * kTile, to = tmem + lanes + C::kO + b * D;
     uint8_t *q_tile = sq + b * C::kQ;
-    int seen_s = 0, seen_o = 0;  // phases of sfull and odone that have been waited for
+    int seen = 0;  // units before this item: phases of sfull and odone
     auto wait = [&](uint64_t *bar, int phase) {
       if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, st);
       ok = __all_sync(0xffffffffu, ok);
@@ -494,89 +498,83 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
         f = factor[b * kTile + row];
       }
       float base = -INFINITY, l = 0.0f;  // the exponent that p is taken from; sum of p 2^-lv
-      for (int i = 0; i < mine && ok; ++i) {
-        wait(&sfull[b], seen_s++);
-        const Info &in = info[(i0 + i) % kInfo];
-        const int tok = (at.blk + i) * kTile;
-        const int there = in.there[0] | in.there[1] << 1;
-        const bool cut = !__all_sync(0xffffffffu, tok + kTile <= limit) || there != 3;
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::tmem_ld32(ts + 32 * c, s[c]);
-        tc::tmem_ld_wait();
-        if (cut) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int seen = (there >> (c / 2)) & 1 ? limit - tok - 32 * c : 0;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[c][j] = j < seen ? s[c][j] : 0xFF800000u;
-          }
-        }
-        float top = -INFINITY, fk[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float a[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) a[q] = __uint_as_float(s[2 * h + q / 2][q % 2 * 16]);
-#pragma unroll
-          for (int j = 1; j < 15; j += 2)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              a[q] = max3(a[q], __uint_as_float(s[2 * h + q / 2][q % 2 * 16 + j]),
-                          __uint_as_float(s[2 * h + q / 2][q % 2 * 16 + j + 1]));
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            a[q] = fmaxf(a[q], __uint_as_float(s[2 * h + q / 2][q % 2 * 16 + 15]));
-          // a factor of 0 would turn the masked -inf into NaN
-          fk[h] = fmaxf(f * in.ks[h], 1e-37f);
-          top = fmaxf(top, fmaf(fmaxf(max3(a[0], a[1], a[2]), a[3]), fk[h], (float)in.lv[h]));
-        }
-        const bool raise = top > base + kLazy || (base == -INFINITY && top > base);
-        if (i > 0 && __any_sync(0xffffffffu, raise)) {
-          const float shrink = raise ? ex2(base - top) : 1.0f;
-          l *= shrink;
-          wait(&odone[b], seen_o + i - 1);
+      // Block by block: probabilities from the base as it is, with the scores' maximum beside
+      // them; where that lies too far above the base (rare past a row's first blocks), what the row
+      // has is rescaled and the block's probabilities are taken again.
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(to + c, o);
-            tc::tmem_ld_wait();
+      for (int i2 = 0; i2 < 2 * mine && ok; ++i2) {
+        const int i = i2 >> 1, h = i2 & 1;
+        wait(&sfull[2 * b + h], seen + i);
+        const Info &in = info[(i0 + i) % kInfo];
+        const float lv = (float)in.lv[h], ks = in.ks[h];
+        const int left = in.there[h] ? limit - (at.blk + i) * kTile - h * kTok : 0;  // visible tokens
+        const uint32_t tb = ts + h * kTok;
+        uint32_t s[2][32];
+        tc::tmem_ld32(tb, s[0]);
+        tc::tmem_ld32(tb + 32, s[1]);
+        // a factor of 0 would turn the masked -inf into NaN
+        const float fk = fmaxf(f * ks, 1e-37f), back = 0x1p-8f * fp8::pow2(-in.lv[h]);
+        tc::tmem_ld_wait();
+        if (!__all_sync(0xffffffffu, left >= kTok)) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * shrink);
-            tmem_st16(to + c, o);
-          }
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[c][j] = 32 * c + j < left ? s[c][j] : 0xFF800000u;
         }
-        if (raise) base = top;
-        const float ref = (base == -INFINITY ? 0.0f : base) - 8.0f;
+        float2 sum[2];
+#pragma unroll 1
+        for (;;) {
+          const float off = lv - (base == -INFINITY ? 0.0f : base) + 8.0f;
+          const float2 fk2 = make_float2(fk, fk), off2 = make_float2(off, off);
+          sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float off = (float)in.lv[h] - ref;
-          const float2 fk2 = make_float2(fk[h], fk[h]), off2 = make_float2(off, off);
-          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-          for (int c = 2 * h; c < 2 * h + 2; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              float2 y = fma2(make_float2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1])),
-                              fk2, off2);
+              const float2 x = make_float2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1]));
+              top[j % 2] = max3(top[j % 2], x.x, x.y);
+              float2 y = fma2(x, fk2, off2);
               y = make_float2(ex2(y.x), ex2(y.y));
               sum[j % 2] = add2(sum[j % 2], y);
               w[j] = pack_half2(y.x, y.y);
             }
-            tmem_st16(ts + 16 * c, w);
+            tmem_st16(tb + 16 * c, w);
           }
-          sum[0] = add2(sum[0], sum[1]);
-          l = fmaf((sum[0].x + sum[0].y) * 0x1p-8f, fp8::pow2(-in.lv[h]), l);
+          const float high = fmaf(fmaxf(top[0], top[1]), fk, lv);
+          const bool raise = high > base + kLazy || (base == -INFINITY && high > base);
+          if (!__any_sync(0xffffffffu, raise)) break;
+          if (i2 > 0) {
+            const float shrink = raise ? ex2(base - high) : 1.0f;
+            l *= shrink;
+            wait(&odone[2 * b + 1 - h], seen + i + h - 1);  // the block before
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + c, o);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * shrink);
+              tmem_st16(to + c, o);
+            }
+          }
+          if (raise) base = high;
+          tmem_st_wait();  // the probabilities are written again
         }
+        sum[0] = add2(sum[0], sum[1]);
+        l = fmaf(sum[0].x + sum[0].y, back, l);
         tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&pfull[b]);
+        if (lane == 0) tc::mbar_arrive(&pfull[2 * b + h]);
       }
       // the item's end, here or in the next share
-      seen_o += mine;
-      if (mine > 0) wait(&odone[b], seen_o - 1);
+      seen += mine;
+      if (mine > 0) {
+        wait(&odone[2 * b], seen - 1);
+        wait(&odone[2 * b + 1], seen - 1);
+      }
       const bool whole = at.blk == 0 && m == at.nblk;
       float *piece = part + (2 * (int64_t)blockIdx.x + (i0 > 0 ? 1 : 0)) * kPiece<PromptPlan, D>;
       const float inv = whole ? (l == 0.0f ? 0.0f : 0x1p-8f / l) : 0x1p-8f;
