@@ -19,27 +19,6 @@ namespace {
 constexpr int kVec = 8;               // elements per lane: 16 lanes cover one 128-element block
 constexpr int kMaxRowThreads = 512;
 
-// Eight elements at p (the first `n` exist; the others give 0).  `vec`: p is 16-byte aligned.
-template <typename T>
-__device__ __forceinline__ void load8(const T *__restrict__ p, int64_t n, bool vec, float (&v)[8]) {
-  if (vec && n >= kVec) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = reinterpret_cast<const float4 *>(p)[0];
-      const float4 b = reinterpret_cast<const float4 *>(p)[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const uint4 q = *reinterpret_cast<const uint4 *>(p);
-      const T *e = reinterpret_cast<const T *>(&q);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = to_f32(e[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
-  }
-}
-
 template <typename T>
 __device__ __forceinline__ T from_f32(float x) {
   if constexpr (sizeof(T) == 4) return x;
@@ -47,21 +26,88 @@ __device__ __forceinline__ T from_f32(float x) {
   else return __float2bfloat16_rn(x);
 }
 
+// Eight elements as they are stored.  `align`: what the rows' addresses are a multiple of (16, 8,
+// 4, else single elements); only the first n elements exist, the others read as 0.
 template <typename T>
-__device__ __forceinline__ void store8(T *__restrict__ p, int64_t n, bool vec, const float (&v)[8]) {
-  if (vec && n >= kVec) {
-    alignas(16) T e[kVec];
+struct Raw8 {
+  static constexpr int kWords = 2 * sizeof(T);
+  uint32_t q[kWords];
+  __device__ __forceinline__ void load(const T *__restrict__ p, int64_t n, int align) {
+    if (n >= kVec && align >= 4) {
+      if (align >= 16) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) e[i] = from_f32<T>(v[i]);
+        for (int i = 0; i < kWords / 4; ++i) {
+          const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+          q[4 * i] = v.x; q[4 * i + 1] = v.y; q[4 * i + 2] = v.z; q[4 * i + 3] = v.w;
+        }
+      } else if (align >= 8) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(e) / 16; ++i)
-      reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(e)[i];
-  } else {
+        for (int i = 0; i < kWords / 2; ++i) {
+          const uint2 v = reinterpret_cast<const uint2 *>(p)[i];
+          q[2 * i] = v.x; q[2 * i + 1] = v.y;
+        }
+      } else {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
-      if (i < n) p[i] = from_f32<T>(v[i]);
+        for (int i = 0; i < kWords; ++i) q[i] = reinterpret_cast<const uint32_t *>(p)[i];
+      }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) q[i] = i < n ? __float_as_uint(p[i]) : 0u;
+    } else {
+      const uint16_t *e = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        q[i] = (2 * i < n ? (uint32_t)e[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)e[2 * i + 1] << 16 : 0u);
+    }
   }
-}
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(q[i]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      return __half2float(__ushort_as_half((unsigned short)(q[i / 2] >> (16 * (i % 2)))));
+    } else {
+      return __uint_as_float(i % 2 ? q[i / 2] & 0xFFFF0000u : q[i / 2] << 16);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[kVec]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) q[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const T lo = from_f32<T>(v[2 * i]), hi = from_f32<T>(v[2 * i + 1]);
+        q[i] = (uint32_t) * reinterpret_cast<const uint16_t *>(&lo) |
+               (uint32_t) * reinterpret_cast<const uint16_t *>(&hi) << 16;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T *__restrict__ p, int64_t n, int align) const {
+    if (n >= kVec && align >= 4) {
+      if (align >= 16) {
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i)
+          reinterpret_cast<uint4 *>(p)[i] = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+      } else if (align >= 8) {
+#pragma unroll
+        for (int i = 0; i < kWords / 2; ++i)
+          reinterpret_cast<uint2 *>(p)[i] = make_uint2(q[2 * i], q[2 * i + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t *>(p)[i] = q[i];
+      }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (i < n) p[i] = __uint_as_float(q[i]);
+    } else {
+      uint16_t *e = reinterpret_cast<uint16_t *>(p);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (i < n) e[i] = (uint16_t)(q[i / 2] >> (16 * (i % 2)));
+    }
+  }
+};
 
 // Codes of eight elements scaled by `inv`; rows of codes are 16-byte aligned.
 __device__ __forceinline__ void store_codes8(uint8_t *__restrict__ p, int64_t n,
@@ -89,54 +135,110 @@ struct RowsParams {
   float *rstd;                     // null: plain quantizer
   int64_t rows, d;
   float eps;
-  int vx, vr, vw, vh;              // 16-byte alignment of each pointer's rows
+  int vx, vr, vw, vh;              // alignment of each pointer's rows
 };
 
-// One CTA per row; half-warps take its 128-element blocks in turn.
-template <typename T, typename TW>
-__global__ void __launch_bounds__(kMaxRowThreads) rows_kernel(RowsParams p) {
+// One CTA per row; half-warps take 128-element blocks, a thread VPT pieces of eight.  All of a
+// thread's loads are asked for before its stores, which the compiler may not move them past.
+template <typename T, typename TW, int VPT>
+__global__ void __launch_bounds__(kMaxRowThreads, VPT == 4 || sizeof(T) == 4 ? 2 : 1)
+rows_kernel(RowsParams p) {
   __shared__ float part[kMaxRowThreads / 32];
+  wait_for_grids();
+  launch_dependents();
+  const int lane = threadIdx.x % 32;
+  const int64_t row = blockIdx.x;
+  Raw8<T> x[VPT], r[VPT];
+  Raw8<TW> w[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int64_t c = ((int64_t)threadIdx.x + (int64_t)j * blockDim.x) * kVec, n = p.d - c;
+    x[j].load((const T *)p.x + row * p.ldx + c, n, p.vx);
+    if (p.r) r[j].load((const T *)p.r + row * p.ldr + c, n, p.vr);
+    if (p.w) w[j].load((const TW *)p.w + c, n, p.vw);
+  }
+  float sq = 0.0f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int64_t c = ((int64_t)threadIdx.x + (int64_t)j * blockDim.x) * kVec, n = p.d - c;
+    float v[kVec], amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      v[i] = p.r ? x[j].get(i) + r[j].get(i) : x[j].get(i);
+      sq = fmaf(v[i], v[i], sq);
+    }
+    if (p.h && n > 0) {
+      Raw8<T> h;
+      h.set(v);
+      h.store((T *)p.h + row * p.ldh + c, n, p.vh);
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      if (p.w) v[i] *= w[j].get(i);
+      amax = fmaxf(amax, fp8::finite_abs(v[i]));
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const int e = fp8::block_exponent(amax);
+    if (n > 0) {
+      store_codes8(p.codes + row * p.ldc + c, n, v, fp8::pow2(-e));
+      if ((lane & 15) == 0) p.exps[row * p.lde + c / fp8::kBlock] = (uint8_t)(e + fp8::kBias);
+    }
+  }
+  if (!p.rstd) return;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+  if (lane == 0) part[threadIdx.x / 32] = sq;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    float s = threadIdx.x < blockDim.x / 32 ? part[threadIdx.x] : 0.0f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x == 0) p.rstd[row] = 1.0f / sqrtf(s / (float)p.d + p.eps);
+  }
+}
+
+// Rows too wide for a thread's registers: one CTA per row, its pieces in a loop.
+template <typename T, typename TW>
+__global__ void __launch_bounds__(kMaxRowThreads) wide_rows_kernel(RowsParams p) {
+  __shared__ float part[kMaxRowThreads / 32];
+  wait_for_grids();
+  launch_dependents();
   const int64_t row = blockIdx.x;
   const T *x = (const T *)p.x + row * p.ldx;
   const T *r = p.r ? (const T *)p.r + row * p.ldr : nullptr;
-  T *h = p.h ? (T *)p.h + row * p.ldh : nullptr;
-  const TW *w = (const TW *)p.w;
-  uint8_t *codes = p.codes + row * p.ldc;
-  uint8_t *exps = p.exps + row * p.lde;
   const int lane = threadIdx.x % 32;
   float sq = 0.0f;
   // whole warps iterate together: the half-warp past the row's end computes on zeros
   for (int64_t base = (int64_t)(threadIdx.x - lane) * kVec; base < p.d;
        base += (int64_t)blockDim.x * kVec) {
     const int64_t c = base + lane * kVec, n = p.d - c;
-    float v[8], u[8];
-    load8(x + c, n, p.vx, v);
-    if (r) {
-      load8(r + c, n, p.vr, u);
+    Raw8<T> xq, rq;
+    Raw8<TW> wq;
+    xq.load(x + c, n, p.vx);
+    if (r) rq.load(r + c, n, p.vr);
+    if (p.w) wq.load((const TW *)p.w + c, n, p.vw);
+    float v[8];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] += u[i];
-    }
-    if (h && n > 0) store8(h + c, n, p.vh, v);
-    if (w) {
-      load8(w + c, n, p.vw, u);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        sq = fmaf(v[i], v[i], sq);
-        u[i] *= v[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) u[i] = v[i];
+    for (int i = 0; i < kVec; ++i) v[i] = r ? xq.get(i) + rq.get(i) : xq.get(i);
+    if (p.h && n > 0) {
+      Raw8<T> h;
+      h.set(v);
+      h.store((T *)p.h + row * p.ldh + c, n, p.vh);
     }
     float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) amax = fmaxf(amax, fp8::finite_abs(u[i]));
+    for (int i = 0; i < kVec; ++i) {
+      sq = fmaf(v[i], v[i], sq);
+      if (p.w) v[i] *= wq.get(i);
+      amax = fmaxf(amax, fp8::finite_abs(v[i]));
+    }
 #pragma unroll
     for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const int e = fp8::block_exponent(amax);
     if (n > 0) {
-      store_codes8(codes + c, n, u, fp8::pow2(-e));
-      if ((lane & 15) == 0) exps[c / fp8::kBlock] = (uint8_t)(e + fp8::kBias);
+      store_codes8(p.codes + row * p.ldc + c, n, v, fp8::pow2(-e));
+      if ((lane & 15) == 0) p.exps[row * p.lde + c / fp8::kBlock] = (uint8_t)(e + fp8::kBias);
     }
   }
   if (!p.rstd) return;
@@ -165,7 +267,10 @@ tiles_kernel(const T *__restrict__ x, int64_t ldx, int vx, int64_t rows, int64_t
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int64_t row = r0 + 16 * j;
-    load8(x + row * ldx + c, row < rows ? n : 0, vx, v[j]);
+    Raw8<T> q;
+    q.load(x + row * ldx + c, row < rows ? n : 0, vx);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[j][i] = q.get(i);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) amax = fmaxf(amax, fp8::finite_abs(v[j][i]));
   }
@@ -214,30 +319,45 @@ from_codes_kernel(const uint32_t *__restrict__ qp, int64_t words, int bits,
   }
 }
 
-bool rows_aligned(const void *p, int64_t ld, size_t es) {
-  return ((uintptr_t)p % 16) == 0 && (ld * (int64_t)es) % 16 == 0;
+// What all rows' addresses are a multiple of: 16, 8, 4 or less.
+int rows_aligned(const void *p, int64_t ld, size_t es) {
+  const uintptr_t bits = (uintptr_t)p | (uintptr_t)(ld * (int64_t)es);
+  return bits % 16 == 0 ? 16 : (bits % 8 == 0 ? 8 : (bits % 4 == 0 ? 4 : 1));
+}
+
+template <typename T, typename TW>
+gptq_status run_rows_of(const RowsParams &p, cudaStream_t s) {
+  int sms = 0;
+  GPTQ_TRY(device_sm_count(&sms));
+  const int64_t pieces = ceil_div(p.d, kVec);
+  // pieces a thread: one while all rows run at once (latency), two where they queue (loads in
+  // flight); what is wider than four pieces of 512 threads goes in a loop
+  const int vpt = pieces > 2 * kMaxRowThreads ? 4 : (pieces > kMaxRowThreads || p.rows > 8 * sms ? 2 : 1);
+  if (pieces > 4 * kMaxRowThreads)
+    return launch_early(wide_rows_kernel<T, TW>, dim3((unsigned)p.rows), dim3(kMaxRowThreads), 0, 1,
+                        s, p);
+  const dim3 grid((unsigned)p.rows), block((unsigned)(ceil_div(ceil_div(pieces, vpt), 32) * 32));
+  switch (vpt) {
+    case 1: return launch_early(rows_kernel<T, TW, 1>, grid, block, 0, 1, s, p);
+    case 2: return launch_early(rows_kernel<T, TW, 2>, grid, block, 0, 1, s, p);
+    default: return launch_early(rows_kernel<T, TW, 4>, grid, block, 0, 1, s, p);
+  }
 }
 
 gptq_status run_rows(RowsParams p, int xdtype, int wdtype, cudaStream_t s) {
   if (p.rows == 0) return GPTQ_OK;
   const size_t es = xdtype == GPTQ_F32 ? 4 : 2, wes = wdtype == GPTQ_F32 ? 4 : 2;
   p.vx = rows_aligned(p.x, p.ldx, es);
-  p.vr = p.r && rows_aligned(p.r, p.ldr, es);
-  p.vh = p.h && rows_aligned(p.h, p.ldh, es);
-  p.vw = p.w && rows_aligned(p.w, 0, wes);
-  int64_t threads = ceil_div(ceil_div(p.d, kVec), 32) * 32;
-  if (threads > kMaxRowThreads) threads = kMaxRowThreads;
-  const dim3 grid((unsigned)p.rows), block((unsigned)threads);
+  p.vr = rows_aligned(p.r, p.ldr, es);
+  p.vh = rows_aligned(p.h, p.ldh, es);
+  p.vw = rows_aligned(p.w, 0, wes);
   switch (xdtype) {
-    case GPTQ_F32: return launch_kernel(rows_kernel<float, float>, grid, block, 0, s, p);
+    case GPTQ_F32: return run_rows_of<float, float>(p, s);
     case GPTQ_F16:
-      return wdtype == GPTQ_F32
-                 ? launch_kernel(rows_kernel<__half, float>, grid, block, 0, s, p)
-                 : launch_kernel(rows_kernel<__half, __half>, grid, block, 0, s, p);
+      return wdtype == GPTQ_F32 ? run_rows_of<__half, float>(p, s) : run_rows_of<__half, __half>(p, s);
     default:
-      return wdtype == GPTQ_F32
-                 ? launch_kernel(rows_kernel<__nv_bfloat16, float>, grid, block, 0, s, p)
-                 : launch_kernel(rows_kernel<__nv_bfloat16, __nv_bfloat16>, grid, block, 0, s, p);
+      return wdtype == GPTQ_F32 ? run_rows_of<__nv_bfloat16, float>(p, s)
+                                : run_rows_of<__nv_bfloat16, __nv_bfloat16>(p, s);
   }
 }
 
