@@ -396,9 +396,8 @@ static gptq_status kv8_cache_check(int64_t n_seq, int64_t n_new, int n_kv, int d
 static bool strides_ok(const int64_t *st) {
   return st && st[0] >= 0 && st[1] >= 0 && st[2] >= 0;
 }
-static bool strided_vec(const void *p, const int64_t *st, size_t es) {
-  return aligned(p, 16) && (st[0] * (int64_t)es) % 16 == 0 && (st[1] * (int64_t)es) % 16 == 0 &&
-         (st[2] * (int64_t)es) % 16 == 0;
+static int strided_alignment(const void *p, const int64_t *st, size_t es) {
+  return fp8::alignment(p, st[0] * (int64_t)es, st[1] * (int64_t)es, st[2] * (int64_t)es);
 }
 
 gptq_status gptq_kv8_append(const void *new_k, const int64_t *k_strides, const void *new_v,
@@ -421,8 +420,8 @@ gptq_status gptq_kv8_append(const void *new_k, const int64_t *k_strides, const v
     g.k_stride[i] = k_strides[i];
     g.v_stride[i] = v_strides[i];
   }
-  g.vec_k = strided_vec(new_k, k_strides, es);
-  g.vec_v = strided_vec(new_v, v_strides, es);
+  g.align_k = strided_alignment(new_k, k_strides, es);
+  g.align_v = strided_alignment(new_v, v_strides, es);
   g.n_seq = (int)n_seq; g.n_new = n_new; g.n_kv = n_kv; g.dim = dim;
   g.k = k; g.v = v; g.k_exps = k_exps; g.v_exps = v_exps; g.n_blocks = n_blocks;
   g.table = table; g.ld_table = ld_table; g.max_blocks = (int)max_blocks;
@@ -469,8 +468,8 @@ gptq_status gptq_kv8_attention(const void *q, const int64_t *q_strides, int dtyp
   g.k = k; g.v = v; g.k_exps = k_exps; g.v_exps = v_exps; g.n_blocks = n_blocks;
   g.table = table; g.ld_table = ld_table; g.max_blocks = (int)max_blocks;
   g.lengths = lengths; g.causal = causal ? 1 : 0; g.scale = scale;
-  g.vec_q = strided_vec(q, q_strides, 2);
-  g.vec_o = strided_vec(out, o_strides, 2);
+  g.vec_q = strided_alignment(q, q_strides, 2) == 16;
+  g.vec_o = strided_alignment(out, o_strides, 2) == 16;
   return launch_kv8_attention(g, ws, (cudaStream_t)stream);
 }
 

@@ -254,7 +254,7 @@ gptq_status launch_fp8_matmul(const Fp8MatmulArgs &g, void *ws, cudaStream_t s);
 struct Kv8AppendArgs {
   const void *new_k, *new_v; int dtype;      // [n_seq, n_new, n_kv, dim], element strides below
   int64_t k_stride[3], v_stride[3];          // sequence, token, head
-  int vec_k, vec_v;                          // 16-byte aligned tokens
+  int align_k, align_v;                      // what tokens' addresses are a multiple of (16, 8, 4, 1)
   int n_seq; int64_t n_new; int n_kv, dim;
   uint8_t *k, *v, *k_exps, *v_exps; int64_t n_blocks;
   const int32_t *table; int64_t ld_table; int max_blocks;

@@ -16,98 +16,10 @@ namespace gptq {
 
 namespace {
 
-constexpr int kVec = 8;               // elements per lane: 16 lanes cover one 128-element block
+using fp8::from_f32;
+using fp8::kVec;   // elements per lane: 16 lanes cover one 128-element block
+using fp8::Raw8;
 constexpr int kMaxRowThreads = 512;
-
-template <typename T>
-__device__ __forceinline__ T from_f32(float x) {
-  if constexpr (sizeof(T) == 4) return x;
-  else if constexpr (std::is_same<T, __half>::value) return __float2half_rn(x);
-  else return __float2bfloat16_rn(x);
-}
-
-// Eight elements as they are stored.  `align`: what the rows' addresses are a multiple of (16, 8,
-// 4, else single elements); only the first n elements exist, the others read as 0.
-template <typename T>
-struct Raw8 {
-  static constexpr int kWords = 2 * sizeof(T);
-  uint32_t q[kWords];
-  __device__ __forceinline__ void load(const T *__restrict__ p, int64_t n, int align) {
-    if (n >= kVec && align >= 4) {
-      if (align >= 16) {
-#pragma unroll
-        for (int i = 0; i < kWords / 4; ++i) {
-          const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
-          q[4 * i] = v.x; q[4 * i + 1] = v.y; q[4 * i + 2] = v.z; q[4 * i + 3] = v.w;
-        }
-      } else if (align >= 8) {
-#pragma unroll
-        for (int i = 0; i < kWords / 2; ++i) {
-          const uint2 v = reinterpret_cast<const uint2 *>(p)[i];
-          q[2 * i] = v.x; q[2 * i + 1] = v.y;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) q[i] = reinterpret_cast<const uint32_t *>(p)[i];
-      }
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) q[i] = i < n ? __float_as_uint(p[i]) : 0u;
-    } else {
-      const uint16_t *e = reinterpret_cast<const uint16_t *>(p);
-#pragma unroll
-      for (int i = 0; i < kWords; ++i)
-        q[i] = (2 * i < n ? (uint32_t)e[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)e[2 * i + 1] << 16 : 0u);
-    }
-  }
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (sizeof(T) == 4) {
-      return __uint_as_float(q[i]);
-    } else if constexpr (std::is_same<T, __half>::value) {
-      return __half2float(__ushort_as_half((unsigned short)(q[i / 2] >> (16 * (i % 2)))));
-    } else {
-      return __uint_as_float(i % 2 ? q[i / 2] & 0xFFFF0000u : q[i / 2] << 16);
-    }
-  }
-  __device__ __forceinline__ void set(const float (&v)[kVec]) {
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) q[i] = __float_as_uint(v[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        const T lo = from_f32<T>(v[2 * i]), hi = from_f32<T>(v[2 * i + 1]);
-        q[i] = (uint32_t) * reinterpret_cast<const uint16_t *>(&lo) |
-               (uint32_t) * reinterpret_cast<const uint16_t *>(&hi) << 16;
-      }
-    }
-  }
-  __device__ __forceinline__ void store(T *__restrict__ p, int64_t n, int align) const {
-    if (n >= kVec && align >= 4) {
-      if (align >= 16) {
-#pragma unroll
-        for (int i = 0; i < kWords / 4; ++i)
-          reinterpret_cast<uint4 *>(p)[i] = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
-      } else if (align >= 8) {
-#pragma unroll
-        for (int i = 0; i < kWords / 2; ++i)
-          reinterpret_cast<uint2 *>(p)[i] = make_uint2(q[2 * i], q[2 * i + 1]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t *>(p)[i] = q[i];
-      }
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        if (i < n) p[i] = __uint_as_float(q[i]);
-    } else {
-      uint16_t *e = reinterpret_cast<uint16_t *>(p);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        if (i < n) e[i] = (uint16_t)(q[i / 2] >> (16 * (i % 2)));
-    }
-  }
-};
 
 // Codes of eight elements scaled by `inv`; rows of codes are 16-byte aligned.
 __device__ __forceinline__ void store_codes8(uint8_t *__restrict__ p, int64_t n,
@@ -319,11 +231,7 @@ from_codes_kernel(const uint32_t *__restrict__ qp, int64_t words, int bits,
   }
 }
 
-// What all rows' addresses are a multiple of: 16, 8, 4 or less.
-int rows_aligned(const void *p, int64_t ld, size_t es) {
-  const uintptr_t bits = (uintptr_t)p | (uintptr_t)(ld * (int64_t)es);
-  return bits % 16 == 0 ? 16 : (bits % 8 == 0 ? 8 : (bits % 4 == 0 ? 4 : 1));
-}
+int rows_aligned(const void *p, int64_t ld, size_t es) { return fp8::alignment(p, ld * (int64_t)es); }
 
 template <typename T, typename TW>
 gptq_status run_rows_of(const RowsParams &p, cudaStream_t s) {

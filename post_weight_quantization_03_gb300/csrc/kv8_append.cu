@@ -9,93 +9,125 @@
 // A token whose value vector holds something that is not finite gets zero codes there and NaN
 // codes in its key: whoever attends to it gets NaN (as it should), and whoever does not is
 // untouched, since a masked score is replaced while a masked value is only multiplied by zero.
+//
+// HBM-bound for prompts (a bf16 token read, half its bytes written); for single tokens it is the
+// chain of loads (start, table, token) and a launch.
 #include "fp8.cuh"
 
 namespace gptq {
 
 namespace {
 
+using fp8::Raw8;
+
 constexpr int kTok = GPTQ_KV8_BLOCK;
 constexpr int kAThreads = 256;
+constexpr int kFew = 4;        // up to so many new tokens take append_few_kernel
 
-// One CTA per (touched block, head, sequence); D is the head's width (64 or 128).
+// Where a touched block of a sequence is, and which of its slots [lo, hi) are new.
+struct Touched {
+  int64_t ph;   // block and head; negative: nothing to write
+  int lo, hi;
+  int64_t tok;  // new token in slot 0 (negative where older tokens come first)
+};
+__device__ __forceinline__ Touched touched(const Kv8AppendArgs &g, int seq, int head, int nth) {
+  Touched t{-1, 0, 0, 0};
+  const int64_t start = g.start[seq];
+  if (start < 0) return t;
+  const int64_t blk = start / kTok + nth, t0 = blk * kTok;
+  t.tok = t0 - start;
+  const int64_t lo = t.tok < 0 ? -t.tok : 0, hi = g.n_new - t.tok < kTok ? g.n_new - t.tok : kTok;
+  if (lo >= hi || blk >= g.max_blocks) return t;
+  const int64_t page = g.table[seq * g.ld_table + blk];
+  if (page < 0 || page >= g.n_blocks) return t;
+  t.ph = page * g.n_kv + head;
+  t.lo = (int)lo;
+  t.hi = (int)hi;
+  return t;
+}
+
+// The exponent of a block whose new tokens need `need`, and by how much its older codes' rises.
+__device__ __forceinline__ int raised(int need, int lo, uint8_t was_byte, int &rise) {
+  rise = 0;
+  if (lo == 0) return need;
+  const int was = (int)was_byte - fp8::kBias;
+  if (was >= need) return was;
+  rise = need - was;
+  return need;
+}
+// 2^-rise; a rise past 126 leaves only zeros.
+__device__ __forceinline__ float fall(int rise) { return rise > 126 ? 0.0f : fp8::pow2(-rise); }
+
+// Older keys under a raised exponent: two codes at a time.
+__device__ __forceinline__ void lower_keys(uint8_t *kc, int codes, int rise, int thread, int threads) {
+  const float f = fall(rise);
+  for (int i = thread; i < codes / 2; i += threads) {
+    uint16_t *p = reinterpret_cast<uint16_t *>(kc) + i;
+    const float2 c = fp8::unpack2(*p);
+    *p = (uint16_t)fp8::pack2(c.x * f, c.y * f);
+  }
+}
+
+// Prompts: one CTA per (touched block, head, sequence).  Keys: a thread takes pieces of eight
+// elements of a token.  Values: eight channels of four tokens, so that the transposed codes go to
+// shared memory as whole words in different banks and from there to the cache in rows.
 template <typename T, int D>
 __global__ void __launch_bounds__(kAThreads) append_kernel(Kv8AppendArgs g) {
-  constexpr int kVecs = D / 8;                       // 8-element pieces of a token
-  constexpr int kIter = kTok * kVecs / kAThreads;    // pieces per thread: 2 or 4
+  constexpr int kVecs = D / 8;                       // pieces of a token
+  constexpr int kIter = kTok * kVecs / kAThreads;    // keys: pieces per thread, 2 or 4
   __shared__ alignas(16) uint8_t sv[D * kTok];
   __shared__ float part[2][kAThreads / 32];
   __shared__ int bad[kTok];
+  wait_for_grids();
+  launch_dependents();
+  const int seq = blockIdx.z, head = blockIdx.y, tid = threadIdx.x;
+  const Touched b = touched(g, seq, head, blockIdx.x);
+  if (b.ph < 0) return;
+  const int lo = b.lo, hi = b.hi;
+  uint8_t *kc = g.k + b.ph * (int64_t)(kTok * D), *vc = g.v + b.ph * (int64_t)(kTok * D);
+  const uint8_t k_was = g.k_exps[b.ph], v_was = g.v_exps[b.ph];
 
-  const int seq = blockIdx.z, head = blockIdx.y;
-  const int64_t start = g.start[seq];
-  if (start < 0) return;
-  const int64_t blk = start / kTok + blockIdx.x;
-  const int64_t t0 = blk * kTok;
-  const int64_t lo64 = start > t0 ? start - t0 : 0;
-  int64_t hi64 = start + g.n_new - t0;
-  if (hi64 > kTok) hi64 = kTok;
-  if (lo64 >= hi64 || blk >= g.max_blocks) return;
-  const int lo = (int)lo64, hi = (int)hi64;
-  const int64_t page = g.table[seq * g.ld_table + blk];
-  if (page < 0 || page >= g.n_blocks) return;
-  const int64_t ph = page * g.n_kv + head;
-  uint8_t *kc = g.k + ph * (int64_t)(kTok * D), *vc = g.v + ph * (int64_t)(kTok * D);
-
-  if (threadIdx.x < kTok) bad[threadIdx.x] = 0;
-  __syncthreads();
-
-  // the new tokens' pieces, in registers between the maximum and the conversion
   const T *ks = (const T *)g.new_k + seq * g.k_stride[0] + head * g.k_stride[2];
   const T *vs = (const T *)g.new_v + seq * g.v_stride[0] + head * g.v_stride[2];
-  float kx[kIter][8], vx[kIter][8];
-  float ka = 0.f, va = 0.f;
+  const int quad = tid % (kTok / 4) * 4, vd = tid / (kTok / 4) * 8;  // values: tokens, channels
+  const bool has_v = vd < D;
+  Raw8<T> kx[kIter], vx[4];
 #pragma unroll
   for (int j = 0; j < kIter; ++j) {
-    const int i = threadIdx.x + kAThreads * j, slot = i / kVecs, d = i % kVecs * 8;
-    const bool fresh = slot >= lo && slot < hi;
-    const int64_t tok = t0 + slot - start;
-    const T *kp = ks + tok * g.k_stride[1] + d, *vp = vs + tok * g.v_stride[1] + d;
-    if (fresh && g.vec_k) {
-      alignas(16) T e[8];
+    const int i = tid + kAThreads * j, slot = i / kVecs, d = i % kVecs * 8;
+    kx[j].load(ks + (b.tok + slot) * g.k_stride[1] + d, slot >= lo && slot < hi ? 8 : 0, g.align_k);
+  }
 #pragma unroll
-      for (int q = 0; q < (int)sizeof(e) / 16; ++q)
-        reinterpret_cast<uint4 *>(e)[q] = reinterpret_cast<const uint4 *>(kp)[q];
+  for (int j = 0; j < 4; ++j) {
+    const int slot = quad + j;
+    vx[j].load(vs + (b.tok + slot) * g.v_stride[1] + vd, has_v && slot >= lo && slot < hi ? 8 : 0,
+               g.align_v);
+  }
+  if (tid < kTok) bad[tid] = 0;
+  __syncthreads();
+  float ka = 0.f, va = 0.f;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) kx[j][q] = to_f32(e[q]);
-    } else {
+  for (int j = 0; j < kIter; ++j)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) kx[j][q] = fresh ? to_f32(kp[q]) : 0.f;
-    }
-    if (fresh && g.vec_v) {
-      alignas(16) T e[8];
+    for (int q = 0; q < 8; ++q) ka = fmaxf(ka, fp8::finite_abs(kx[j].get(q)));
 #pragma unroll
-      for (int q = 0; q < (int)sizeof(e) / 16; ++q)
-        reinterpret_cast<uint4 *>(e)[q] = reinterpret_cast<const uint4 *>(vp)[q];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) vx[j][q] = to_f32(e[q]);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) vx[j][q] = fresh ? to_f32(vp[q]) : 0.f;
-    }
-    bool b = false;
+  for (int j = 0; j < 4; ++j) {
+    bool odd = false;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      ka = fmaxf(ka, fp8::finite_abs(kx[j][q]));
-      va = fmaxf(va, fp8::finite_abs(vx[j][q]));
-      b |= !fp8::finite(vx[j][q]);
-      if (!fp8::finite(vx[j][q])) vx[j][q] = 0.f;
+      va = fmaxf(va, fp8::finite_abs(vx[j].get(q)));
+      odd |= !fp8::finite(vx[j].get(q));
     }
-    if (b) bad[slot] = 1;
+    if (odd) bad[quad + j] = 1;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
     va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
   }
-  if (threadIdx.x % 32 == 0) {
-    part[0][threadIdx.x / 32] = ka;
-    part[1][threadIdx.x / 32] = va;
+  if (tid % 32 == 0) {
+    part[0][tid / 32] = ka;
+    part[1][tid / 32] = va;
   }
   __syncthreads();
 #pragma unroll
@@ -103,80 +135,149 @@ __global__ void __launch_bounds__(kAThreads) append_kernel(Kv8AppendArgs g) {
     ka = fmaxf(ka, part[0][i]);
     va = fmaxf(va, part[1][i]);
   }
-  int ke = fp8::block_exponent(ka), ve = fp8::block_exponent(va);
-  int kd = 0, vd = 0;  // how far the older codes' exponents are raised
-  if (lo > 0) {
-    const int k_was = (int)g.k_exps[ph] - fp8::kBias, v_was = (int)g.v_exps[ph] - fp8::kBias;
-    if (k_was >= ke) ke = k_was; else kd = ke - k_was;
-    if (v_was >= ve) ve = v_was; else vd = ve - v_was;
-  }
+  int k_rise, v_rise;
+  const int ke = raised(fp8::block_exponent(ka), lo, k_was, k_rise);
+  const int ve = raised(fp8::block_exponent(va), lo, v_was, v_rise);
   const float ki = fp8::pow2(-ke), vi = fp8::pow2(-ve);
 #pragma unroll
   for (int j = 0; j < kIter; ++j) {
-    const int i = threadIdx.x + kAThreads * j, slot = i / kVecs, d = i % kVecs * 8;
+    const int i = tid + kAThreads * j, slot = i / kVecs, d = i % kVecs * 8;
     if (slot < lo || slot >= hi) continue;
     float c[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      c[q] = bad[slot] ? __uint_as_float(0x7FC00000u) : fp8::inf_to_nan(kx[j][q]) * ki;
+      c[q] = bad[slot] ? __uint_as_float(0x7FC00000u) : fp8::inf_to_nan(kx[j].get(q)) * ki;
     *reinterpret_cast<uint2 *>(kc + slot * D + d) =
         make_uint2(fp8::pack4(c[0], c[1], c[2], c[3]), fp8::pack4(c[4], c[5], c[6], c[7]));
+  }
+  if (has_v) {
 #pragma unroll
-    for (int q = 0; q < 8; q += 2) {
-      const uint32_t two = fp8::pack2(vx[j][q] * vi, vx[j][q + 1] * vi);
-      sv[(d + q) * kTok + slot] = (uint8_t)two;
-      sv[(d + q + 1) * kTok + slot] = (uint8_t)(two >> 8);
+    for (int q = 0; q < 8; ++q) {
+      float c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] = fp8::finite(vx[j].get(q)) ? vx[j].get(q) * vi : 0.0f;
+      *reinterpret_cast<uint32_t *>(sv + (vd + q) * kTok + quad) = fp8::pack4(c[0], c[1], c[2], c[3]);
     }
   }
-  // older codes under a raised exponent (a difference past 126 leaves only zeros)
-  if (kd > 0) {
-    const float f = kd > 126 ? 0.f : fp8::pow2(-kd);
-    for (int i = threadIdx.x; i < lo * D / 2; i += kAThreads) {
-      uint16_t *p = reinterpret_cast<uint16_t *>(kc) + i;
-      const float2 c = fp8::unpack2(*p);
-      *p = (uint16_t)fp8::pack2(c.x * f, c.y * f);
-    }
-  }
-  if (vd > 0) {
-    const float f = vd > 126 ? 0.f : fp8::pow2(-vd);
-    for (int i = threadIdx.x; i < lo * D; i += kAThreads) {
-      const int at = i / lo * kTok + i % lo;
-      sv[at] = (uint8_t)fp8::pack2(fp8::unpack1(vc[at]) * f, 0.f);
-    }
-  }
+  if (k_rise > 0) lower_keys(kc, lo * D, k_rise, tid, kAThreads);
   __syncthreads();
-  const int from = vd > 0 ? 0 : lo, width = hi - from;
-  if (width == kTok) {
-    for (int i = threadIdx.x; i < D * kTok / 16; i += kAThreads)
+  if (lo == 0 && hi == kTok) {
+    for (int i = tid; i < D * kTok / 16; i += kAThreads)
       reinterpret_cast<uint4 *>(vc)[i] = reinterpret_cast<const uint4 *>(sv)[i];
   } else {
-    for (int i = threadIdx.x; i < D * width; i += kAThreads) {
-      const int at = i / width * kTok + from + i % width;
-      vc[at] = sv[at];
+    const float f = fall(v_rise);
+    const int from = v_rise > 0 ? 0 : lo, width = hi - from;
+    for (int i = tid; i < D * width; i += kAThreads) {
+      const int slot = from + i % width, at = i / width * kTok + slot;
+      vc[at] = slot >= lo ? sv[at] : (uint8_t)fp8::pack2(fp8::unpack1(vc[at]) * f, 0.f);
     }
   }
-  if (threadIdx.x == 0) {
-    g.k_exps[ph] = (uint8_t)(ke + fp8::kBias);
-    g.v_exps[ph] = (uint8_t)(ve + fp8::kBias);
+  if (tid == 0) {
+    g.k_exps[b.ph] = (uint8_t)(ke + fp8::kBias);
+    g.v_exps[b.ph] = (uint8_t)(ve + fp8::kBias);
   }
 }
 
+// A few tokens (decoding): one warp per (touched block, head, sequence), a lane D / 32 channels.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) append_few_kernel(Kv8AppendArgs g) {
+  constexpr int C = D / 32;
+  wait_for_grids();
+  launch_dependents();
+  const int lane = threadIdx.x % 32;
+  const int64_t item = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+  if (item >= (int64_t)g.n_seq * g.n_kv * 2) return;
+  const int head = (int)(item / 2 % g.n_kv), seq = (int)(item / 2 / g.n_kv);
+  const Touched b = touched(g, seq, head, (int)(item % 2));
+  if (b.ph < 0) return;
+  const int lo = b.lo, n = b.hi - b.lo;
+  uint8_t *kc = g.k + b.ph * (int64_t)(kTok * D), *vc = g.v + b.ph * (int64_t)(kTok * D);
+  const uint8_t k_was = g.k_exps[b.ph], v_was = g.v_exps[b.ph];
+  const T *ks = (const T *)g.new_k + seq * g.k_stride[0] + head * g.k_stride[2] +
+                (b.tok + lo) * g.k_stride[1] + lane * C;
+  const T *vs = (const T *)g.new_v + seq * g.v_stride[0] + head * g.v_stride[2] +
+                (b.tok + lo) * g.v_stride[1] + lane * C;
+  float kx[kFew][C], vx[kFew][C], ka = 0.f, va = 0.f;
+#pragma unroll
+  for (int j = 0; j < kFew; ++j)
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+      kx[j][q] = j < n ? to_f32(ks[j * g.k_stride[1] + q]) : 0.0f;
+      vx[j][q] = j < n ? to_f32(vs[j * g.v_stride[1] + q]) : 0.0f;
+    }
+  unsigned bad = 0;
+#pragma unroll
+  for (int j = 0; j < kFew; ++j)
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+      ka = fmaxf(ka, fp8::finite_abs(kx[j][q]));
+      va = fmaxf(va, fp8::finite_abs(vx[j][q]));
+      bad |= fp8::finite(vx[j][q]) ? 0u : 1u << j;
+    }
+  bad = __reduce_or_sync(0xffffffffu, bad);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
+    va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
+  }
+  int k_rise, v_rise;
+  const int ke = raised(fp8::block_exponent(ka), lo, k_was, k_rise);
+  const int ve = raised(fp8::block_exponent(va), lo, v_was, v_rise);
+  const float ki = fp8::pow2(-ke), vi = fp8::pow2(-ve);
+#pragma unroll
+  for (int j = 0; j < kFew; ++j) {
+    if (j >= n) break;
+    float c[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+      c[q] = bad >> j & 1 ? __uint_as_float(0x7FC00000u) : fp8::inf_to_nan(kx[j][q]) * ki;
+      v[q] = fp8::finite(vx[j][q]) ? vx[j][q] * vi : 0.0f;
+    }
+    const uint32_t kw = fp8::pack4(c[0], c[1], c[2], c[3]), vw = fp8::pack4(v[0], v[1], v[2], v[3]);
+    uint8_t *kd = kc + (lo + j) * D + lane * C;
+    if constexpr (C == 4) *reinterpret_cast<uint32_t *>(kd) = kw;
+    else *reinterpret_cast<uint16_t *>(kd) = (uint16_t)kw;
+#pragma unroll
+    for (int q = 0; q < C; ++q) vc[(lane * C + q) * kTok + lo + j] = (uint8_t)(vw >> (8 * q));
+  }
+  if (k_rise > 0) lower_keys(kc, lo * D, k_rise, lane, 32);
+  if (v_rise > 0) {
+    const float f = fall(v_rise);
+    for (int i = lane; i < D * lo; i += 32) {
+      uint8_t *p = vc + i / lo * kTok + i % lo;
+      *p = (uint8_t)fp8::pack2(fp8::unpack1(*p) * f, 0.f);
+    }
+  }
+  if (lane == 0) {
+    g.k_exps[b.ph] = (uint8_t)(ke + fp8::kBias);
+    g.v_exps[b.ph] = (uint8_t)(ve + fp8::kBias);
+  }
+}
+
+template <typename T, int D>
+gptq_status launch_of(const Kv8AppendArgs &g, cudaStream_t s) {
+  if (g.n_new <= kFew)
+    return launch_early(append_few_kernel<T, D>,
+                        dim3((unsigned)ceil_div((int64_t)g.n_seq * g.n_kv * 2, 4)), dim3(128), 0, 1,
+                        s, g);
+  const dim3 grid((unsigned)((g.n_new + 2 * (kTok - 1)) / kTok), (unsigned)g.n_kv,
+                  (unsigned)g.n_seq);
+  return launch_early(append_kernel<T, D>, grid, dim3(kAThreads), 0, 1, s, g);
+}
+
 template <typename T>
-gptq_status launch_any(const Kv8AppendArgs &g, dim3 grid, cudaStream_t s) {
-  if (g.dim == 64) return launch_kernel(append_kernel<T, 64>, grid, dim3(kAThreads), 0, s, g);
-  return launch_kernel(append_kernel<T, 128>, grid, dim3(kAThreads), 0, s, g);
+gptq_status launch_any(const Kv8AppendArgs &g, cudaStream_t s) {
+  return g.dim == 64 ? launch_of<T, 64>(g, s) : launch_of<T, 128>(g, s);
 }
 
 }  // namespace
 
 gptq_status launch_kv8_append(const Kv8AppendArgs &g, cudaStream_t s) {
   if (g.n_seq == 0 || g.n_new == 0) return GPTQ_OK;
-  const dim3 grid((unsigned)((g.n_new + 2 * (kTok - 1)) / kTok), (unsigned)g.n_kv,
-                  (unsigned)g.n_seq);
   switch (g.dtype) {
-    case GPTQ_F32: return launch_any<float>(g, grid, s);
-    case GPTQ_F16: return launch_any<__half>(g, grid, s);
-    default: return launch_any<__nv_bfloat16>(g, grid, s);
+    case GPTQ_F32: return launch_any<float>(g, s);
+    case GPTQ_F16: return launch_any<__half>(g, s);
+    default: return launch_any<__nv_bfloat16>(g, s);
   }
 }
 
