@@ -222,6 +222,24 @@ __device__ __forceinline__ int my_share(const P &p, int turn, Cursor &first) {
   return u1 - u0;
 }
 
+// The same with the items dealt whole: nothing is left to join.
+template <typename P>
+__device__ __forceinline__ int my_items(const P &p, Cursor &first) {
+  const int items = p.entries * p.g.n_kv, n = items < (int)gridDim.x ? items : gridDim.x;
+  if ((int)blockIdx.x >= n) return 0;
+  const int i0 = share_start(items, n, blockIdx.x), i1 = share_start(items, n, blockIdx.x + 1);
+  int count = 0;
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) count += p.units(i / p.g.n_kv);
+  if (count == 0) return 0;
+  first = Cursor{i0 / p.g.n_kv, i0 % p.g.n_kv, 0, p.units(i0 / p.g.n_kv)};
+  if (first.nblk == 0) {
+    first.head = p.g.n_kv - 1;  // on to the next entry that has units
+    first.next_item(p);
+  }
+  return count;
+}
+
 // Where row `row` of a sequence's head goes.
 template <typename T>
 __device__ __forceinline__ T *out_row(const Kv8AttentionArgs &g, int group, int seq, int head,

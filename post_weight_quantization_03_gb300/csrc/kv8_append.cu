@@ -72,7 +72,7 @@ __device__ __forceinline__ void lower_keys(uint8_t *kc, int codes, int rise, int
 // elements of a token.  Values: eight channels of four tokens, so that the transposed codes go to
 // shared memory as whole words in different banks and from there to the cache in rows.
 template <typename T, int D>
-__global__ void __launch_bounds__(kAThreads) append_kernel(Kv8AppendArgs g) {
+__global__ void __launch_bounds__(kAThreads, sizeof(T) == 4 ? 2 : 3) append_kernel(Kv8AppendArgs g) {
   constexpr int kVecs = D / 8;                       // pieces of a token
   constexpr int kIter = kTok * kVecs / kAThreads;    // keys: pieces per thread, 2 or 4
   __shared__ alignas(16) uint8_t sv[D * kTok];
