@@ -374,6 +374,31 @@ def test_attention(seqs, new, kv, group, d, lengths, mb, dtype):
     _check_attention(full, q, cache, table, lengths, scale=0.05, causal=False)
 
 
+@pytest.mark.parametrize("seqs,new,kv,group,d,longest", [
+    (5, 1, 3, 4, 128, 5000), (40, 1, 2, 8, 64, 1500), (7, 2, 1, 8, 128, 3000), (3, 4, 2, 8, 64, 2500), (200, 1, 1, 2, 64, 1300),
+    (3, 40, 2, 4, 128, 3000), (30, 9, 1, 4, 64, 1200)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_attention_many_lengths(seqs, new, kv, group, d, longest, dtype):
+    # more blocks than are dealt whole: items cut by the shares, empty sequences between them
+    rng = np.random.default_rng(seqs)
+    lengths = rng.integers(0, longest + 1, seqs)
+    lengths[0], lengths[seqs // 2], lengths[-1] = longest, 0, 1
+    n_blocks, mb = 64, -(-longest // 64)
+    cache, table = _cache(new, n_blocks, kv, d), rng.integers(0, n_blocks, (seqs, mb)).astype(np.int32)
+    q = _randn(9, seqs, new, kv * group, d, dtype=dtype)
+    out = gptq.kv8_attention(q.to(DEV), _dev_cache(cache), _i32(table), _i32(lengths))
+    _check_attention(out, q, cache, table, lengths)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+@pytest.mark.parametrize("new", [1, 50])
+def test_attention_scales(new, scale):
+    cache, table = _cache(3, 6, 2, 64), np.array([[3, 1, 5, 0]], np.int32)
+    q = _randn(4, 1, new, 8, 64, dtype="bf16")
+    out = gptq.kv8_attention(q.to(DEV), _dev_cache(cache), _i32(table), _i32([230]), scale=scale)
+    _check_attention(out, q, cache, table, [230], scale=scale)
+
+
 @pytest.mark.parametrize("new,group", [(1, 8), (100, 4)])
 def test_attention_ignores_what_is_past_the_length(new, group):
     d, kv, length = 128, 2, 330
