@@ -84,7 +84,13 @@ __device__ __forceinline__ int seq_length(const Kv8AttentionArgs &g, int seq) {
 // into the range of the type that the tensor cores take.
 __device__ __forceinline__ int row_exponent(float amax) {
   const int e = (int)(__float_as_uint(amax) >> 23) - 127;
-  return amax == 0.0f ? 0 : (e < -110 ? -110 : (e > 120 ? 120 : e));
+  return amax == 0.0f ? 0 : (e < -110 ? -110 : e);
+}
+
+// Magnitudes as integers are in their order, infinities and NaN above all numbers.  A row with
+// one of these has no softmax: scaled by NaN, all of it becomes NaN codes.
+__device__ __forceinline__ float row_scale(float amax, int e) {
+  return fp8::finite(amax) ? fp8::pow2(-e) : __uint_as_float(0x7FC00000u);
 }
 
 // Entries of ROWS rows whose units are UNIT cached tokens.

@@ -105,13 +105,14 @@ __device__ __forceinline__ void load_queries(const Kv8AttentionArgs &g, int seq,
 #pragma unroll
     for (int i = 0; i < D / 4; ++i) v[i] = 0.0f;
   }
-  float amax = 0.0f;
+  uint32_t most = 0;
 #pragma unroll
-  for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fp8::finite_abs(v[i]));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  for (int i = 0; i < D / 4; ++i) most = max(most, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+  const float amax = __uint_as_float(most);
   const int e = row_exponent(amax) - 7;  // the row's maximum in [128, 256)
-  const float inv = fp8::pow2(-e);
+  const float inv = row_scale(amax, e);
   f = fp8::pow2(e) * g.scale * kLog2e;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)

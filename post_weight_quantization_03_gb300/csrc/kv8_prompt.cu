@@ -14,10 +14,12 @@
 //   softmax   one row per thread, no exchange between threads.  A block's key exponent is a
 //             factor of its scores, its value exponent lv goes into the exponential:
 //             y = f s + lv,  p = 2^(y - b + 8),  O += p vc,  l += p 2^-lv;  out = O / l.
-//             b follows the maximum of y lazily: O (in TMEM) and l are rescaled only when y
-//             exceeds b by 6 (p stays within fp16's range), which past a row's first blocks is
-//             rare; so the maximum is taken beside the exponentials, not before them.  p is
-//             rounded to fp16 once and replaces the scores in TMEM, from where it is the second
+//             b is the maximum of y when it was last set.  It stays while a block's sum of p is
+//             at most 2^15 (p within fp16's range), so that the maximum is looked for, and O (in
+//             TMEM) and l are rescaled, only where the sum exceeds that: past a row's first
+//             blocks rarely.  A maximum beside every block's exponentials takes two of the
+//             twelve issue slots of a pair of scores (1 x 4096: 131 us, without 127).  p is rounded
+//             to fp16 once and replaces the scores in TMEM, from where it is the second
 //             product's A operand, a block of 64 tokens at a time.
 //   overlap   while one tile's softmax runs, the tensor core multiplies for the other.
 //
@@ -45,7 +47,7 @@ using PromptPlan = Plan<2 * kTile, kTile, 5>;
 constexpr int kThreads = 512;
 constexpr int kInfo = 4;
 constexpr uint32_t kChunk = kTile * 128;        // 128 rows of 128 bytes
-constexpr float kLazy = 6.0f;
+constexpr float kMostSum = 0x1p15f;
 
 constexpr int kKStages = 3, kVStages = 2;
 
@@ -148,6 +150,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// The two elements of a word.
+template <typename T>
+__device__ __forceinline__ float2 pair(uint32_t w) {
+  if constexpr (std::is_same<T, __half>::value)
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  else
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  if constexpr (std::is_same<T, __half>::value) return pack_half2(a, b);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // Byte of element (row, 16-byte unit u) in a chunk of 128-byte rows with the 128-byte swizzle.
@@ -471,25 +488,24 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
 #pragma unroll 2
         for (int i = 0; i < 32 / kAt; ++i) {
           const int mr = wrow + i * kAt + sub;
-          const uint4 w[2] = {*slot(mr, 0), *slot(mr, 1)};
-          const T *e16 = reinterpret_cast<const T *>(w);
-          float v[16], amax = 0.0f;
+          const uint4 lo = *slot(mr, 0), hi = *slot(mr, 1);
+          const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+          uint32_t most = 0;  // magnitudes of the even and of the odd elements
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            v[j] = to_f32(e16[j]);
-            amax = fmaxf(amax, fp8::finite_abs(v[j]));
-          }
+          for (int j = 0; j < 8; ++j) most = __vmaxu2(most, w[j] & 0x7FFF7FFFu);
 #pragma unroll
           for (int o = 1; o < kLanes; o <<= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, o));
+          const float amax = pair<T>(max(most & 0xFFFFu, most >> 16)).x;
           const int e = row_exponent(amax) - 7;
-          const float inv = g.scale < 0.0f ? -fp8::pow2(-e) : fp8::pow2(-e);
+          const float scale = row_scale(amax, e), inv = g.scale < 0.0f ? -scale : scale;
           if (piece16 == 0) factor[b * kTile + mr] = fp8::pow2(e) * fabsf(g.scale) * kLog2e;
           uint32_t word[4][NT];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            split4<NT>(v[4 * j] * inv, v[4 * j + 1] * inv, v[4 * j + 2] * inv, v[4 * j + 3] * inv,
-                       word[j]);
+          for (int j = 0; j < 4; ++j) {
+            const float2 a = pair<T>(w[2 * j]), c = pair<T>(w[2 * j + 1]);
+            split4<NT>(a.x * inv, a.y * inv, c.x * inv, c.y * inv, word[j]);
+          }
 #pragma unroll
           for (int term = 0; term < NT; ++term)
             *slot(mr, term) = make_uint4(word[0][term], word[1][term], word[2][term], word[3][term]);
@@ -501,9 +517,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
         f = factor[b * kTile + row];
       }
       float base = -INFINITY, l = 0.0f;  // the exponent that p is taken from; sum of p 2^-lv
-      // Block by block: probabilities from the base as it is, with the scores' maximum beside
-      // them; where that lies too far above the base (rare past a row's first blocks), what the row
-      // has is rescaled and the block's probabilities are taken again.
+      // Block by block: probabilities from the base as it is; where they are too large for it (rare
+      // past a row's first blocks), the base is raised to the block's maximum, what the row has is
+      // rescaled and the block's probabilities are taken again: 64 of 2^8 at most, below the limit.
 #pragma unroll 1
       for (int i2 = 0; i2 < 2 * mine && ok; ++i2) {
         const int i = i2 >> 1, h = i2 & 1;
@@ -530,14 +546,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
           const float off = lv - (base == -INFINITY ? 0.0f : base) + 8.0f;
           const float2 fk2 = make_float2(fk, fk), off2 = make_float2(off, off);
           sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const float2 x = make_float2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1]));
-              top[j % 2] = max3(top[j % 2], x.x, x.y);
               float2 y = fma2(x, fk2, off2);
               y = make_float2(ex2(y.x), ex2(y.y));
               sum[j % 2] = add2(sum[j % 2], y);
@@ -545,8 +559,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
             }
             tmem_st16(tb + 16 * c, w);
           }
+          sum[0] = add2(sum[0], sum[1]);
+          const bool large = sum[0].x + sum[0].y > kMostSum || base == -INFINITY;
+          if (!__any_sync(0xffffffffu, large)) break;
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              top[j / 2 % 2] = max3(top[j / 2 % 2], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
           const float high = fmaf(fmaxf(top[0], top[1]), fk, lv);
-          const bool raise = high > base + kLazy || (base == -INFINITY && high > base);
+          const bool raise = large && high > base;
           if (!__any_sync(0xffffffffu, raise)) break;
           if (i2 > 0) {
             const float shrink = raise ? ex2(base - high) : 1.0f;
@@ -565,7 +588,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
           if (raise) base = high;
           tmem_st_wait();  // the probabilities are written again
         }
-        sum[0] = add2(sum[0], sum[1]);
         l = fmaf(sum[0].x + sum[0].y, back, l);
         tmem_st_wait();
         tc::tc_fence_before();
@@ -595,12 +617,13 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
           // through the tile of queries, whose products are done: rows of 2 D bytes
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
-            alignas(16) T e[8];
+            uint32_t e[4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) e[q] = from_f32<T>(__uint_as_float(x[j + q]));
+            for (int q = 0; q < 4; ++q)
+              e[q] = pack<T>(__uint_as_float(x[j + 2 * q]), __uint_as_float(x[j + 2 * q + 1]));
             const int u = (c + j) / 8;
             *reinterpret_cast<uint4 *>(q_tile + u / 8 * kChunk + swizzled(row, u % 8)) =
-                *reinterpret_cast<const uint4 *>(e);
+                make_uint4(e[0], e[1], e[2], e[3]);
           }
         } else {
 #pragma unroll

@@ -342,6 +342,36 @@ def test_append_marks_tokens_that_are_not_finite():
 # Cache: attention
 # ---------------------------------------------------------------------------------------
 
+@pytest.mark.parametrize("seqs,new,group,length,dtype", [(2, 1, 4, 150, "bf16"), (2, 1, 4, 150, "f16"), (2, 1, 8, 4000, "bf16"),
+                                                         (1, 70, 8, 200, "bf16"), (1, 70, 8, 200, "f16"), (1, 300, 4, 2000, "bf16")])
+def test_attention_queries_that_are_not_finite(seqs, new, group, length, dtype):
+    # a row of queries with an infinity or a NaN in it has no softmax: it becomes NaN, and only it
+    kv, d, mb = 2, 64, -(-length // 64)
+    cache, table = _cache(11, seqs * mb, kv, d), np.arange(seqs * mb, dtype=np.int32).reshape(seqs, mb)
+    q = _randn(12, seqs, new, kv * group, d, dtype=dtype)
+    clean = gptq.kv8_attention(q.to(DEV), _dev_cache(cache), _i32(table), _i32([length] * seqs))
+    bad = np.zeros((seqs, new, kv * group), bool)
+    for i, x in enumerate((math.inf, -math.inf, math.nan)):
+        at = (i % seqs, (37 * i) % new, (3 * i + 1) % (kv * group))
+        q[at + (5 + 20 * i,)] = x
+        bad[at] = True
+    out = gptq.kv8_attention(q.to(DEV), _dev_cache(cache), _i32(table), _i32([length] * seqs))
+    nan = torch.isnan(out)
+    assert np.array_equal(_np(nan.all(-1)), bad) and np.array_equal(_np(nan.any(-1)), bad)
+    ok = torch.from_numpy(~bad).to(DEV)
+    assert torch.equal(out[ok], clean[ok])
+
+
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("top", [2.0 ** -110, 2.0 ** -60, 2.0 ** 60, 2.0 ** 100, 2.0 ** 121, 3.3e38])
+def test_attention_queries_at_the_ends_of_their_range(new, top):
+    cache, table = _cache(13, 3, 1, 64), np.array([[2, 0, 1]], np.int32)
+    q = _randn(14, 1, new, 8, 64).double()
+    q = (q / q.abs().amax(-1, keepdim=True) * top).to(torch.bfloat16)
+    out = gptq.kv8_attention(q.to(DEV), _dev_cache(cache), _i32(table), _i32([180]), scale=0.5 / top)
+    _check_attention(out, q, cache, table, [180], scale=0.5 / top)
+
+
 def _check_attention(out, q, cache, table, lengths, **kw):
     want, mag, terms = SO.kv_attention(_np(q), cache, table, lengths, **kw)
     tol = ULP[out.dtype] * np.abs(want) + (2.0 ** -8 + 2 * 2.0 ** -18 * max(terms, 1.0)) * mag + 1e-7
