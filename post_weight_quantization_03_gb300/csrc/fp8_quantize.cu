@@ -21,12 +21,37 @@ using fp8::kVec;   // elements per lane: 16 lanes cover one 128-element block
 using fp8::Raw8;
 constexpr int kMaxRowThreads = 512;
 
-// Codes of eight elements scaled by `inv`; rows of codes are 16-byte aligned.
+// The largest finite magnitude of a half-warp's 128 elements; infinities become NaN (they would
+// saturate).  Whole warp.  Looking at each element's exponent takes as many instructions as the
+// rest of the element's way, so only a block in which the plain maximum is infinite does it.
+__device__ __forceinline__ float block_max(float (&v)[kVec]) {
+  auto reduce = [](float a) {
+#pragma unroll
+    for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+  };
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  amax = reduce(amax);
+  if (__any_sync(0xffffffffu, amax == INFINITY)) {
+    amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      amax = fmaxf(amax, fp8::finite_abs(v[i]));
+      v[i] = fp8::inf_to_nan(v[i]);
+    }
+    amax = reduce(amax);
+  }
+  return amax;
+}
+
+// Codes of eight elements (none infinite) scaled by `inv`; rows of codes are 16-byte aligned.
 __device__ __forceinline__ void store_codes8(uint8_t *__restrict__ p, int64_t n,
                                              const float (&u)[8], float inv) {
   float c[8];
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) c[i] = fp8::inf_to_nan(u[i]) * inv;
+  for (int i = 0; i < kVec; ++i) c[i] = u[i] * inv;
   const uint2 w = make_uint2(fp8::pack4(c[0], c[1], c[2], c[3]), fp8::pack4(c[4], c[5], c[6], c[7]));
   if (n >= kVec) {
     *reinterpret_cast<uint2 *>(p) = w;
@@ -52,8 +77,13 @@ struct RowsParams {
 
 // One CTA per row; half-warps take 128-element blocks, a thread VPT pieces of eight.  All of a
 // thread's loads are asked for before its stores, which the compiler may not move them past.
-template <typename T, typename TW, int VPT>
-__global__ void __launch_bounds__(kMaxRowThreads, VPT == 4 || sizeof(T) == 4 ? 2 : 1)
+// CTAS an SM at least (of 512 threads): two, or three where rows queue for long.  Three leave 40
+// registers a thread, so a row's loads are not all in flight, but more rows' are: what the
+// memory's latency is hidden by in a long queue, and a longer way for each row in a short one
+// (bf16 with a residual: 8192 x 8192 85 us with two and 76 us, 6.2 TB/s, with three; 4000 x 4096
+// 22.8 and 20.6; but 907 x 6144 7.2 and 7.9, 1336 x 1728 4.5 and 5.5).
+template <typename T, typename TW, int VPT, int CTAS>
+__global__ void __launch_bounds__(kMaxRowThreads, CTAS)
 rows_kernel(RowsParams p) {
   __shared__ float part[kMaxRowThreads / 32];
   wait_for_grids();
@@ -73,7 +103,7 @@ rows_kernel(RowsParams p) {
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int64_t c = ((int64_t)threadIdx.x + (int64_t)j * blockDim.x) * kVec, n = p.d - c;
-    float v[kVec], amax = 0.0f;
+    float v[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       v[i] = p.r ? x[j].get(i) + r[j].get(i) : x[j].get(i);
@@ -84,14 +114,11 @@ rows_kernel(RowsParams p) {
       h.set(v);
       h.store((T *)p.h + row * p.ldh + c, n, p.vh);
     }
+    if (p.w) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      if (p.w) v[i] *= w[j].get(i);
-      amax = fmaxf(amax, fp8::finite_abs(v[i]));
+      for (int i = 0; i < kVec; ++i) v[i] *= w[j].get(i);
     }
-#pragma unroll
-    for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const int e = fp8::block_exponent(amax);
+    const int e = fp8::block_exponent(block_max(v));
     if (n > 0) {
       store_codes8(p.codes + row * p.ldc + c, n, v, fp8::pow2(-e));
       if ((lane & 15) == 0) p.exps[row * p.lde + c / fp8::kBlock] = (uint8_t)(e + fp8::kBias);
@@ -138,16 +165,12 @@ __global__ void __launch_bounds__(kMaxRowThreads) wide_rows_kernel(RowsParams p)
       h.set(v);
       h.store((T *)p.h + row * p.ldh + c, n, p.vh);
     }
-    float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       sq = fmaf(v[i], v[i], sq);
       if (p.w) v[i] *= wq.get(i);
-      amax = fmaxf(amax, fp8::finite_abs(v[i]));
     }
-#pragma unroll
-    for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const int e = fp8::block_exponent(amax);
+    const int e = fp8::block_exponent(block_max(v));
     if (n > 0) {
       store_codes8(p.codes + row * p.ldc + c, n, v, fp8::pow2(-e));
       if ((lane & 15) == 0) p.exps[row * p.lde + c / fp8::kBlock] = (uint8_t)(e + fp8::kBias);
@@ -184,7 +207,10 @@ tiles_kernel(const T *__restrict__ x, int64_t ldx, int vx, int64_t rows, int64_t
 #pragma unroll
     for (int i = 0; i < kVec; ++i) v[j][i] = q.get(i);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) amax = fmaxf(amax, fp8::finite_abs(v[j][i]));
+    for (int i = 0; i < kVec; ++i) {
+      amax = fmaxf(amax, fp8::finite_abs(v[j][i]));
+      v[j][i] = fp8::inf_to_nan(v[j][i]);
+    }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -245,10 +271,13 @@ gptq_status run_rows_of(const RowsParams &p, cudaStream_t s) {
     return launch_early(wide_rows_kernel<T, TW>, dim3((unsigned)p.rows), dim3(kMaxRowThreads), 0, 1,
                         s, p);
   const dim3 grid((unsigned)p.rows), block((unsigned)(ceil_div(ceil_div(pieces, vpt), 32) * 32));
+  if constexpr (sizeof(T) + sizeof(TW) == 4)
+    if (vpt == 2 && (double)p.rows * block.x > 4.0 * sms * 2 * kMaxRowThreads)
+      return launch_early(rows_kernel<T, TW, 2, 3>, grid, block, 0, 1, s, p);
   switch (vpt) {
-    case 1: return launch_early(rows_kernel<T, TW, 1>, grid, block, 0, 1, s, p);
-    case 2: return launch_early(rows_kernel<T, TW, 2>, grid, block, 0, 1, s, p);
-    default: return launch_early(rows_kernel<T, TW, 4>, grid, block, 0, 1, s, p);
+    case 1: return launch_early(rows_kernel<T, TW, 1, 2>, grid, block, 0, 1, s, p);
+    case 2: return launch_early(rows_kernel<T, TW, 2, 2>, grid, block, 0, 1, s, p);
+    default: return launch_early(rows_kernel<T, TW, 4, 2>, grid, block, 0, 1, s, p);
   }
 }
 
