@@ -448,8 +448,8 @@ gptq_status gptq_debug_hessian_lost_stage(const void *X, int xdtype, int64_t n_t
  * without it).  h and u are taken in fp32 (u from the unrounded h); H is h rounded to xdtype.
  *
  *   X, R, H    [rows, d] of xdtype (F16, BF16 or F32) with row pitches ldx, ldr, ldh >= d.  R
- *              (the residual) and H may be NULL; H may be X or R itself.  16-byte aligned
- *              rows are read and written 16 bytes at a time, others element by element.
+ *              (the residual) and H may be NULL; H may be X or R itself.  Rows are read and
+ *              written in the widest words (16, 8, 4 bytes) that their alignment allows.
  *   weight     [d] of wdtype: xdtype, or F32.
  *   rows >= 0, d >= 1; eps >= 0.   rstd [rows] fp32 out.
  * Asynchronous.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
@@ -518,9 +518,9 @@ gptq_status gptq_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_exps
  * gptq_kv8_append: writes n_new tokens of each sequence at its tokens [start[s], start[s] + n_new).
  * A block's exponents are raised to what the new tokens need and the codes of the block's
  * tokens before start[s] are then re-rounded by that power of two; slots after the new tokens
- * keep their bytes.  A block that the new tokens begin takes its exponents from them alone.  A token whose value is not
- * finite somewhere is stored with NaN codes in its key: exactly the rows that attend to it
- * become NaN.
+ * keep their bytes.  A block that the new tokens begin takes its exponents from them alone.  A
+ * token whose value is not finite somewhere is stored with NaN codes in its key: exactly the
+ * rows that attend to it become NaN.
  *
  *   new_k, new_v   [n_seq, n_new, n_kv, dim] of dtype (F16, BF16 or F32), elements of a head
  *                  contiguous; k_strides, v_strides: HOST arrays of three element strides
@@ -550,12 +550,14 @@ size_t gptq_kv8_attention_workspace_bytes(int64_t n_seq, int64_t n_new, int n_he
  * n_new tokens of each sequence (their keys and values are already in the cache).
  *
  *   q, out     [n_seq, n_new, n_heads, dim] of dtype (F16 or BF16), elements of a head
- *              contiguous; q_strides, o_strides: HOST arrays of three element strides.
+ *              contiguous; q_strides, o_strides: HOST arrays of three element strides.  Rows of
+ *              q may coincide, rows of out may not overlap.
  *              Query head h reads cache head h / (n_heads / n_kv).
  *   lengths    [n_seq] int32: tokens of the sequence in the cache, the new ones included,
  *              limited to [0, 64 * max_blocks].  With causal != 0 new token t sees the tokens
  *              [0, length - n_new + t], otherwise all `length` of them.  A row that sees
- *              nothing gives zeros.  Bytes of the cache past `length` never matter.
+ *              nothing gives zeros; one whose query is not finite gives NaN.  Bytes of the
+ *              cache past `length` never matter.
  *   scale      factor of the scores (finite).
  *   ws         workspace of ws_bytes >= gptq_kv8_attention_workspace_bytes(...).
  * Repeated calls give identical results.  Asynchronous; a bounded device wait that gave up is

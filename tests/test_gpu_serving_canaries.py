@@ -128,7 +128,7 @@ def test_append_and_attention(seqs, new, kv, group, d, longest):
     strides = (ctypes.c_int64 * 3)(new * kv * d, kv * d, d)
     k, v = _randn(5, seqs, new, kv, d, dtype=torch.bfloat16), _randn(6, seqs, new, kv, d, dtype=torch.bfloat16)
     q = _randn(7, seqs, new, heads, d, dtype=torch.bfloat16)
-    ostr = (new * heads * d + 24, heads * d + 8, d)
+    ostr = (new * (heads * d + 8) + 16, heads * d + 8, d)
     o_strides = (ctypes.c_int64 * 3)(*ostr)
     q_strides = (ctypes.c_int64 * 3)(new * heads * d, heads * d, d)
     elems = (seqs - 1) * ostr[0] + (new - 1) * ostr[1] + heads * d
