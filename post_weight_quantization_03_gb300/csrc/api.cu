@@ -389,7 +389,7 @@ static gptq_status kv8_cache_check(int64_t n_seq, int64_t n_new, int n_kv, int d
     return GPTQ_ERR_INVALID_ARG;
   if (max_blocks > 0 && n_seq > 0 && (!table || !aligned(table, 4))) return GPTQ_ERR_INVALID_ARG;
   if ((dim != 64 && dim != 128) || n_kv > 4096 || n_seq > 65535 || n_new > (1 << 20) ||
-      max_blocks > (1 << 20) || n_blocks * n_kv > INT32_MAX)
+      max_blocks > (1 << 20) || n_blocks > INT32_MAX / n_kv)
     return GPTQ_ERR_UNSUPPORTED;
   return GPTQ_OK;
 }

@@ -115,6 +115,24 @@ struct Raw8 {
       return __uint_as_float(i % 2 ? q[i / 2] & 0xFFFF0000u : q[i / 2] << 16);
     }
   }
+  // The larger of `m` and the elements' magnitudes, as integers (of the even and the odd elements
+  // where two share a word): infinities and NaN are above all numbers.
+  __device__ __forceinline__ uint32_t most(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4) m = max(m, q[i] & 0x7FFFFFFFu);
+      else m = __vmaxu2(m, q[i] & 0x7FFF7FFFu);
+    }
+    return m;
+  }
+  // That as the bits of an fp32 number.
+  __device__ __forceinline__ static uint32_t most_bits(uint32_t m) {
+    if constexpr (sizeof(T) == 4) return m;
+    m = max(m & 0xFFFFu, m >> 16);
+    if constexpr (std::is_same<T, __half>::value)
+      return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+    return m << 16;
+  }
   __device__ __forceinline__ void set(const float (&v)[kVec]) {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll

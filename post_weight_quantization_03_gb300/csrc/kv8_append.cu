@@ -72,11 +72,11 @@ __device__ __forceinline__ void lower_keys(uint8_t *kc, int codes, int rise, int
 // elements of a token.  Values: eight channels of four tokens, so that the transposed codes go to
 // shared memory as whole words in different banks and from there to the cache in rows.
 template <typename T, int D>
-__global__ void __launch_bounds__(kAThreads, sizeof(T) == 4 ? 2 : 3) append_kernel(Kv8AppendArgs g) {
+__global__ void __launch_bounds__(kAThreads, sizeof(T) == 4 ? 2 : 4) append_kernel(Kv8AppendArgs g) {
   constexpr int kVecs = D / 8;                       // pieces of a token
   constexpr int kIter = kTok * kVecs / kAThreads;    // keys: pieces per thread, 2 or 4
   __shared__ alignas(16) uint8_t sv[D * kTok];
-  __shared__ float part[2][kAThreads / 32];
+  __shared__ uint32_t part[2][kAThreads / 32];
   __shared__ int bad[kTok];
   wait_for_grids();
   launch_dependents();
@@ -103,38 +103,63 @@ __global__ void __launch_bounds__(kAThreads, sizeof(T) == 4 ? 2 : 3) append_kern
     vx[j].load(vs + (b.tok + slot) * g.v_stride[1] + vd, has_v && slot >= lo && slot < hi ? 8 : 0,
                g.align_v);
   }
-  if (tid < kTok) bad[tid] = 0;
-  __syncthreads();
-  float ka = 0.f, va = 0.f;
+  uint32_t km = 0, vm = 0;  // largest magnitudes as fp32 bits
 #pragma unroll
-  for (int j = 0; j < kIter; ++j)
+  for (int j = 0; j < kIter; ++j) km = kx[j].most(km);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) ka = fmaxf(ka, fp8::finite_abs(kx[j].get(q)));
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    bool odd = false;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      va = fmaxf(va, fp8::finite_abs(vx[j].get(q)));
-      odd |= !fp8::finite(vx[j].get(q));
+  for (int j = 0; j < 4; ++j) vm = vx[j].most(vm);
+  auto of_block = [&]() {
+    km = __reduce_max_sync(0xffffffffu, km);
+    vm = __reduce_max_sync(0xffffffffu, vm);
+    if (tid % 32 == 0) {
+      part[0][tid / 32] = km;
+      part[1][tid / 32] = vm;
     }
-    if (odd) bad[quad + j] = 1;
-  }
+    __syncthreads();
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
-    va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
-  }
-  if (tid % 32 == 0) {
-    part[0][tid / 32] = ka;
-    part[1][tid / 32] = va;
-  }
-  __syncthreads();
+    for (int i = 0; i < kAThreads / 32; ++i) {
+      km = max(km, part[0][i]);
+      vm = max(vm, part[1][i]);
+    }
+  };
+  km = Raw8<T>::most_bits(km);
+  vm = Raw8<T>::most_bits(vm);
+  of_block();
+  if (max(km, vm) >= 0x7F800000u) {
+    // Something is not finite (the whole CTA sees it): NaN in keys, and in all of the keys of a
+    // token with such a value, zeros in values; the maxima are the others'.
+    if (tid < kTok) bad[tid] = 0;
+    __syncthreads();
+    km = vm = 0;
+    float e[8];
 #pragma unroll
-  for (int i = 0; i < kAThreads / 32; ++i) {
-    ka = fmaxf(ka, part[0][i]);
-    va = fmaxf(va, part[1][i]);
+    for (int j = 0; j < 4; ++j) {
+      bool odd = false;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float x = vx[j].get(q);
+        odd |= !fp8::finite(x);
+        e[q] = fp8::finite(x) ? x : 0.0f;
+        vm = max(vm, __float_as_uint(fabsf(e[q])));
+      }
+      vx[j].set(e);
+      if (odd) bad[quad + j] = 1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kIter; ++j) {
+      const int slot = (tid + kAThreads * j) / kVecs;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float x = kx[j].get(q);
+        km = max(km, __float_as_uint(fp8::finite_abs(x)));
+        e[q] = bad[slot] ? __uint_as_float(0x7FC00000u) : fp8::inf_to_nan(x);
+      }
+      kx[j].set(e);
+    }
+    of_block();
   }
+  const float ka = __uint_as_float(km), va = __uint_as_float(vm);
   int k_rise, v_rise;
   const int ke = raised(fp8::block_exponent(ka), lo, k_was, k_rise);
   const int ve = raised(fp8::block_exponent(va), lo, v_was, v_rise);
@@ -146,7 +171,7 @@ __global__ void __launch_bounds__(kAThreads, sizeof(T) == 4 ? 2 : 3) append_kern
     float c[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      c[q] = bad[slot] ? __uint_as_float(0x7FC00000u) : fp8::inf_to_nan(kx[j].get(q)) * ki;
+      c[q] = kx[j].get(q) * ki;
     *reinterpret_cast<uint2 *>(kc + slot * D + d) =
         make_uint2(fp8::pack4(c[0], c[1], c[2], c[3]), fp8::pack4(c[4], c[5], c[6], c[7]));
   }
@@ -155,7 +180,7 @@ __global__ void __launch_bounds__(kAThreads, sizeof(T) == 4 ? 2 : 3) append_kern
     for (int q = 0; q < 8; ++q) {
       float c[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] = fp8::finite(vx[j].get(q)) ? vx[j].get(q) * vi : 0.0f;
+      for (int j = 0; j < 4; ++j) c[j] = vx[j].get(q) * vi;
       *reinterpret_cast<uint32_t *>(sv + (vd + q) * kTok + quad) = fp8::pack4(c[0], c[1], c[2], c[3]);
     }
   }
