@@ -439,6 +439,7 @@ gptq_status gptq_debug_hessian_lost_stage(const void *X, int xdtype, int64_t n_t
  *          >= ceil(d / 128): blocks of 1 x 128 (activations) or 128 x 128 (weights) elements;
  *   and optionally an fp32 factor per row (the norm's 1/rms; GPTQ's per-row step).
  * Bytes between a row's end and its pitch are neither read into a result nor written.
+ * Matrices of more than 2^20 columns or 2^22 rows are refused (UNSUPPORTED).
  * ====================================================================================== */
 
 /*
@@ -511,6 +512,9 @@ gptq_status gptq_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_exps
  * and for each sequence a row of `table` [n_seq, ld_table] int32: table[s][i] is the block that
  * holds its tokens [64 i, 64 i + 64).  An index outside [0, n_blocks) stands for tokens that are
  * not there: they are not attended to, and appends to them are dropped.
+ * Limits, beyond which the calls return UNSUPPORTED: dim 64 or 128; n_seq, n_heads <= 65535;
+ * n_kv <= 4096; n_new, max_blocks <= 2^20; n_blocks * n_kv < 2^31; and, for the attention,
+ * n_seq * n_kv * (tiles of n_new * n_heads / n_kv rows) * max_blocks below about 2^30.
  */
 #define GPTQ_KV8_BLOCK 64
 

@@ -1,1 +1,1 @@
-"""GB300-native GPTQ per-layer quantization: a C-ABI CUDA library plus a thin binding."""
+"""GB300-native GPTQ per-layer quantization, and 8-bit serving of the quantized layers: a C-ABI CUDA library plus a thin binding."""

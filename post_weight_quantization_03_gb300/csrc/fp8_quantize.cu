@@ -7,7 +7,8 @@
 // (which the product's epilogue applies) loses nothing against quantizing y, and the codes do
 // not wait for the row's sum: the kernel reads x and r once, writes h and the codes in the same
 // pass, and only the 4-byte rstd needs the whole row.  HBM-bound: 7 bytes an element for 16-bit
-// x with a residual.
+// x with a residual (8192 x 8192: 75.6 us, 6.2 TB/s; 1 x 4096: 2.4 us, a launch and two
+// latencies).
 #include <type_traits>
 
 #include "fp8.cuh"

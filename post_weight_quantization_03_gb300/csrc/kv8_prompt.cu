@@ -23,6 +23,12 @@
 //             product's A operand, a block of 64 tokens at a time.
 //   overlap   while one tile's softmax runs, the tensor core multiplies for the other.
 //
+// Measured: 4096 tokens of 32 heads of 128 (8 in the cache, causal) 124 us, 1.1 PFLOP/s; 2 x 777
+// of up to 16000 tokens, heads of 64, fp16 queries 240 us, 0.8 PFLOP/s of 4 D a pair (1.2 executed:
+// a third term).  Neither the tensor core (49 and 43 % busy) nor the exponentials (26 and 35 %) are
+// full: a block of 64 tokens passes from one to the other and back, two blocks and two tiles at a
+// time, and each passage costs its latency.
+//
 // Warps: 0-3 and 4-7 softmax, a tile each; 8-11 copies and converters; 12 and 13 MMA issuers, a
 // tile each (12 owns TMEM).
 #include <cudaTypedefs.h>

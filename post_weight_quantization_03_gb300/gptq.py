@@ -608,9 +608,9 @@ def _fp8_empty(rows, d, row_block, device, stream):
     if stream is not None:
         _lend(stream, codes, exps)
     if pitch != d:
-        codes = codes[:, :d]
+        codes = codes.as_strided((rows, d), (pitch, 1))
     if epitch != kb:
-        exps = exps[:, :kb]
+        exps = exps.as_strided((erows, kb), (epitch, 1))
     return codes, pitch, exps, epitch
 
 
