@@ -23,10 +23,12 @@
 // Bounds, and what it measured (GPU time, m x n x k): up to a few hundred tokens W's bytes
 // (1 x 4096 x 4096 5.4 us, of which 2.5 are the bytes; 24 x 11008 x 4096 11.2 us, 4.1 TB/s;
 // 128 x 8192 x 28672 43.5 us, 5.5 TB/s), the rest of it being the launch, the first copies and the
-// exchange of split sums.  Beyond, the tensor core: 515 x 4096 x 11008 27 us, 1.7 PFLOP/s;
+// exchange of split sums.  Beyond, the tensor core: 515 x 4096 x 11008 26 us, 1.8 PFLOP/s;
 // 8192 x 11008 x 4096 243 us, 3.0 PFLOP/s, the pipe busy 72 % of the time.
 #include <cudaTypedefs.h>
 #include <math.h>
+
+#include <atomic>
 
 #include <type_traits>
 
@@ -364,6 +366,33 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
 // stages each.
 struct Shape { int tn, splits, per_sm; };
 
+// Clusters of `splits` CTAs, one on an SM, that run at once.  They lie within groups of SMs, so
+// there is room for fewer than SMs / splits: 152 SMs take 46 clusters of three (52 x 6144 x 2896
+// has 48 tiles of 64 tokens: split in three it took 13.7 us, in two rounds; now 8.8).
+template <typename TO>
+int clusters_at_once(int splits, int sms) {
+  static std::atomic<int> known[9];
+  int n = known[splits].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)splits;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(splits * sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRingBytes + kSmemBesides;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, (const void *)matmul_kernel<TO>, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    n = sms / splits * 7 / 8;
+  }
+  known[splits].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <typename TO>
 Shape choose(int64_t M, int64_t N, int64_t K, int sms) {
   const int64_t n_w = ceil_div(N, BM), groups = ceil_div(ceil_div(K, BK), 4);
   const double once = (double)(M + N) * K / 3500.0;
@@ -380,7 +409,7 @@ Shape choose(int64_t M, int64_t N, int64_t K, int sms) {
         const int64_t ctas = tiles * s;
         if (per == 2 && ((uint32_t)(BM + tn) * BK * 3 > kRingBytesTwo || ctas <= sms || ctas > 2 * sms))
           continue;
-        if (s > 1 && ctas > (int64_t)per * sms) continue;
+        if (s > 1 && tiles > (int64_t)per * clusters_at_once<TO>(s, sms)) continue;
         const int64_t busy = ceil_div(ctas, sms);
         const double work = (double)busy * 4 * ceil_div(groups, s) * c * (per == 2 ? 0.95 : 1.0);
         double t = sqrt(work * work + (once + fill) * (once + fill));
@@ -399,7 +428,7 @@ gptq_status run(const Fp8MatmulArgs &g, DevStatus *st, cudaStream_t s) {
   int sms = 0;
   GPTQ_TRY(device_sm_count(&sms));
   const int kb = (int)ceil_div(g.K, BK);
-  const Shape sh = choose(g.M, g.N, g.K, sms);
+  const Shape sh = choose<TO>(g.M, g.N, g.K, sms);
   MmParams p{};
   p.ae = g.ae; p.ldae = g.ldae;
   p.we = g.we; p.ldwe = g.ldwe;
