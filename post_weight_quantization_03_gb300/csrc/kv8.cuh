@@ -319,7 +319,7 @@ join_kernel(Kv8AttentionArgs g, const float *part, int turn, int ctas) {
 #pragma unroll
   for (int k = 0; k < kGroups; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   q = p0;
-#pragma unroll 1
+#pragma unroll 2
   for (int i = w - 1; i <= last; ++i) {
     float4 v[kGroups];
 #pragma unroll

@@ -1,8 +1,8 @@
 // Attention over the 8-bit cache, few queries (a decoding step).
 //
 // Per (sequence, cache head) the queries of the group's heads and of the new tokens are the
-// rows, at most 16, of one or two MMA tiles; the keys and values stream past once.  HBM-bound:
-// 2 D bytes a token and head, against 4 D operations a row.
+// rows, at most 32, eight to an MMA tile; the keys and values stream past once.  HBM-bound for
+// up to 16 rows or so: 2 D bytes a token and head, against 4 D operations a row.
 //
 //   products  e4m3 MMAs (m16n8k32, fp32 sums) straight on the cached codes.  The other operand
 //             is a sum of e4m3 terms: with 4 bits of significand each, two terms hold a bf16
@@ -427,16 +427,32 @@ gptq_status run_decode(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
                       (const float *)part, kWarps / rt, ctas);
 }
 
+// Whether `rows` rows of a cache head go to the other kernel's 128-row tiles.  More than 32 always
+// do; fewer where the products here (a pass of MMAs for each eight rows and three terms) outweigh
+// the copies, and the history is long enough for that kernel's set-up (32 sequences of up to
+// 4000 tokens, here and there):
+//   17 to 32 rows   bf16, 128 channels 120 and 86 us (4 of 500: 21.7 and 20.8, 2 of 120: 12.5 and
+//                   16.2); fp16, 64 channels 104 and 73; but bf16, 64 channels 71.5 and 70.7
+//   9 to 16 rows    fp16, 128 channels 112 and 87 (8 of 1500: 28.1 and 26.6, 16 of 500: 20.0 and
+//                   25.9); but fp16, 64 channels 64 and 72; bf16, 128 channels 76 and 84
+bool takes_tiles(int64_t rows, bool half, int dim, int64_t max_blocks) {
+  if (rows > kRows) return true;
+  if (rows > 16) return (half || dim == 128) && max_blocks > 6;
+  return rows > 8 && half && dim == 128 && max_blocks > 20;
+}
+
 }  // namespace
 
 size_t kv8_attention_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int dim,
                               int max_blocks) {
-  if (n_new * (n_heads / n_kv) > kRows)
-    return kv8_prompt_ws_bytes(n_seq, n_new, n_heads, n_kv, dim, max_blocks);
+  const int64_t rows = n_new * (n_heads / n_kv);
   int64_t ctas = kMaxCtas;
   const int64_t units = (int64_t)n_seq * n_kv * max_blocks;
   if (units < ctas) ctas = units;
-  return 256 + (size_t)(2 * ctas) * kRows * (dim + 2) * 4;
+  const size_t here = rows > kRows ? 0 : 256 + (size_t)(2 * ctas) * kRows * (dim + 2) * 4;
+  if (!takes_tiles(rows, true, dim, max_blocks)) return here;  // (with fp16 wherever with bf16)
+  const size_t there = kv8_prompt_ws_bytes(n_seq, n_new, n_heads, n_kv, dim, max_blocks);
+  return there > here ? there : here;
 }
 
 gptq_status launch_kv8_attention(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
@@ -444,10 +460,8 @@ gptq_status launch_kv8_attention(const Kv8AttentionArgs &g, void *ws, cudaStream
     GPTQ_CUDA_CHECK(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s));
     return GPTQ_OK;
   }
-  // Up to 32 rows a cache head the products are bound by the memory on either path, and here
-  // they wait for nothing but their own copies; from there on the tensor cores' 128-row tiles
-  // are filled far enough.
-  if (g.n_new * (g.n_heads / g.n_kv) > kRows) return launch_kv8_prompt(g, ws, s);
+  if (takes_tiles(g.n_new * (g.n_heads / g.n_kv), g.dtype == GPTQ_F16, g.dim, g.max_blocks))
+    return launch_kv8_prompt(g, ws, s);
   if (g.dtype == GPTQ_F16)
     return g.dim == 64 ? run_decode<__half, 64>(g, ws, s) : run_decode<__half, 128>(g, ws, s);
   return g.dim == 64 ? run_decode<__nv_bfloat16, 64>(g, ws, s)

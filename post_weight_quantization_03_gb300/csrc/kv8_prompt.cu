@@ -48,6 +48,10 @@ constexpr int kTile = 128;                      // rows of an MMA tile, tokens o
 // them) weigh as much as five units of its 128 tokens: 1 x 4096 tokens take 204 us with 2, 161
 // with 3, 143 with 4, 129 with 5 and 6, 132 with 8.
 using PromptPlan = Plan<2 * kTile, kTile, 5>;
+// Least weight of a share: cut finer, an item's set-ups and the joining of its pieces cost more
+// than the units (2 sequences of 48 rows over up to 8588 tokens: 71 us with 1, 28 with 4 and 6,
+// 30 with 10; 13 of 168 rows over up to 1149: 29.4, 27.0, 29.3, 34.6).
+constexpr int kTurn = 4;
 // Registers by warp group: 2 x 128 x 192 + 128 x 72 + 128 x 56 = 65,536, what 512 threads have
 // at launch: a softmax thread holds its row's 128 scores.
 constexpr int kThreads = 512;
@@ -186,7 +190,7 @@ __device__ __forceinline__ uint32_t swizzled_row(int row, int u) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float *part,
+prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int uncut, float *part,
               DevStatus *st) {
   constexpr int NT = kTerms<T>;
   using C = Prompt<D, NT>;
@@ -236,7 +240,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, float 
   const PromptPlan plan(g);
   write_empty<T, D>(plan, threadIdx.x, kThreads);
   Cursor at{};
-  const int count = my_share(plan, 1, at);
+  const int count = uncut ? my_items(plan, at) : my_share(plan, kTurn, at);
   bool ok = true;  // false once a wait has given up: the rest passes without waiting
 
   if (warp >= 12) {
@@ -684,10 +688,16 @@ gptq_status run(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   memset(&mk, 0, sizeof(mk));  // an empty cache is never read
   if (g.n_blocks > 0 && !tc::make_tmap_bytes_3d(&mk, g.k, g.n_blocks * g.n_kv, kTok, D))
     return GPTQ_ERR_UNSUPPORTED;
+  // Short histories, with a CTA for each item, gain nothing from being cut, and uncut they need no
+  // second kernel (37 sequences with 182 new tokens of up to 241: 22.4 us cut, 15.9 uncut; 500 of
+  // 500 with 32 heads: 26.8 and 23.4).
+  const int64_t rows = g.n_new * (g.n_heads / g.n_kv);
+  const int uncut = g.max_blocks <= 8 && ceil_div(rows, 2 * kTile) * g.n_seq * g.n_kv <= ctas;
   GPTQ_TRY(launch_early(prompt_kernel<T, D>, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, 1, s, mk,
-                        g, part, (DevStatus *)ws));
+                        g, uncut, part, (DevStatus *)ws));
+  if (uncut) return GPTQ_OK;
   return launch_early(join_kernel<T, D, PromptPlan>, dim3((unsigned)ctas - 1, 8), dim3(128), 0, 1, s,
-                      g, (const float *)part, 1, ctas);
+                      g, (const float *)part, kTurn, ctas);
 }
 
 }  // namespace
