@@ -25,7 +25,8 @@
 // (contiguous) running; eight warps in groups of one warp per eight rows take the units in turn,
 // each group through a ring of its own in shared memory, and meet at the end of an item.  An
 // item that lies in one share is written there; pieces of others meet in a second small kernel,
-// in order (repeatable).
+// in order (repeatable).  Short histories are dealt whole, to CTAs or, where there are many, to
+// groups.
 //
 // Measured: 48 sequences of up to 8000 tokens (8 cache heads of 128, 64 heads: 596 MB) 111 us,
 // 5.4 TB/s; each further 100 MB takes 15 us (6.6 TB/s), the rest is the start of the copies and
@@ -45,6 +46,7 @@ constexpr int kWarps = 8;                 // that compute
 // 384 threads have 168 each (64,512); the split below is that many: 256 x 232 + 128 x 40.
 constexpr int kThreads = 32 * (kWarps + 4);
 constexpr int kList = 128;                // units that have been looked up
+constexpr int kItem = 5;                  // an item's start and end, in blocks
 static_assert(kRows == 8 * 4, "row tiles: 1, 2 or 4");
 
 template <int D>
@@ -124,10 +126,15 @@ __device__ __forceinline__ void load_queries(const Kv8AttentionArgs &g, int seq,
                       qa[i]);
 }
 
+// How the work is dealt: by units, items whole to CTAs (whose groups share an item's units), or
+// items whole to the groups of a CTA in turn (each finishes its own; all of a CTA's units then fit
+// the list).
+enum Deal { kUnits, kItemsToCtas, kItemsToGroups };
+
 // RT: row tiles, and warps of a group (1, 2 or 4).
 template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kThreads, 1)
-decode_kernel(Kv8AttentionArgs g, int whole, float *part, DevStatus *st) {
+decode_kernel(Kv8AttentionArgs g, int deal, float *part, DevStatus *st) {
   using C = Decode<D>;
   constexpr int NT = kTerms<T>;
   constexpr int G = kWarps / RT;             // groups
@@ -155,8 +162,11 @@ decode_kernel(Kv8AttentionArgs g, int whole, float *part, DevStatus *st) {
   const int group = plan.group, rows = plan.rows;
   write_empty<T, D>(plan, threadIdx.x, kThreads);
   Cursor at{};
-  const int count = whole ? my_items(plan, at) : my_share(plan, G, at);
+  const int count = deal == kUnits ? my_share(plan, G, at) : my_items(plan, at);
   if (count == 0) return;
+  const bool to_groups = deal == kItemsToGroups;
+  const int item0 = at.entry * g.n_kv + at.head;
+  auto owner = [&](const Cursor &c) { return (c.entry * g.n_kv + c.head - item0) % G; };
 
   if (warp >= kWarps) {
     // ---------------- look-up and copies ----------------
@@ -166,26 +176,27 @@ decode_kernel(Kv8AttentionArgs g, int whole, float *part, DevStatus *st) {
     // and exponents of the next are on their way while a batch is written to the list.
     Cursor c = at;
     c.advance(plan, lane);
-    int page = -1, place = -1, exps = 0, head = 0;  // of the batches after and next
+    int page = -1, place = -1, exps = 0, head = 0, own = 0;  // of the batches after and next
     auto load_page = [&](int i) {
       page = -1;
       if (i < count) {
         page = g.table[c.entry * g.ld_table + c.blk];
         head = c.head;
+        own = owner(c);
         if (i + 32 < count) c.advance(plan, 32);
       }
     };
     auto load_exps = [&]() {
       place = page < 0 || page >= g.n_blocks ? -1 : page * g.n_kv + head;
-      exps = 0;
-      if (place >= 0) exps = (int)g.k_exps[place] | ((int)g.v_exps[place] << 8);
+      exps = own << 16;
+      if (place >= 0) exps |= (int)g.k_exps[place] | ((int)g.v_exps[place] << 8);
     };
     int filled = 0, soon = lane;
     load_page(soon);
     load_exps();
     load_page(soon += 32);
     // Lane q keeps group q's ring full: half hn of its blocks goes to slot hn % H.
-    int i = lane, hn = 0;
+    int i = to_groups ? 0 : lane, hn = 0;
     const int last = lane < G ? count : 0;
     uint64_t t0 = tc::global_ns();
     while (__any_sync(0xffffffffu, i < last)) {
@@ -198,6 +209,8 @@ decode_kernel(Kv8AttentionArgs g, int whole, float *part, DevStatus *st) {
         __syncwarp();
       }
       bool moved = false;
+      if (to_groups)
+        while (i < last && i < filled && list[i % kList].y >> 16 != lane) ++i;
       if (i < last && i < filled) {
         const int slot = lane * H + hn % H;
         if (hn < H || tc::mbar_try_wait(&empty[slot], (hn / H - 1) & 1)) {
@@ -209,7 +222,7 @@ decode_kernel(Kv8AttentionArgs g, int whole, float *part, DevStatus *st) {
           } else {
             tc::mbar_arrive(&full[slot]);
           }
-          if (hn & 1) i += G;
+          if (hn & 1) i += to_groups ? 1 : G;
           ++hn;
           moved = true;
         }
@@ -244,6 +257,14 @@ decode_kernel(Kv8AttentionArgs g, int whole, float *part, DevStatus *st) {
   };
   for (int i = grp, i0 = 0; i0 < count;) {
     const int i1 = i0 + at.nblk - at.blk < count ? i0 + at.nblk - at.blk : count;  // item's units
+    if (to_groups) {
+      i = i0;
+      if (owner(at) != grp) {
+        i0 = i1;
+        if (i0 < count) at.next_item(plan);
+        continue;
+      }
+    }
     const int length = seq_length(g, at.entry);
     const int limit = r >= rows ? 0 : (g.causal ? length - (int)g.n_new + r / group + 1 : length);
     uint32_t qa[D / 16][NT];
@@ -255,7 +276,7 @@ decode_kernel(Kv8AttentionArgs g, int whole, float *part, DevStatus *st) {
       for (int j = 0; j < 4; ++j) acc[q][j] = 0.0f;
 
 #pragma unroll 1
-    for (; i < i1; i += G) {
+    for (; i < i1; i += to_groups ? 1 : G) {
       arrived();
       const int2 what = list[i % kList];
       if (!ok || what.x < 0) {
@@ -265,7 +286,7 @@ decode_kernel(Kv8AttentionArgs g, int whole, float *part, DevStatus *st) {
         continue;
       }
       const float fk = f * fp8::exp_value((uint8_t)what.y);
-      const int lv = (what.y >> 8) - fp8::kBias;
+      const int lv = (what.y >> 8 & 0xFF) - fp8::kBias;
       // column n of score tile j is token 16 (n / 2) + 2 j + n % 2 of the block
       const uint8_t *krow = ring + (size_t)(hn % H) * C::kHalf +
                             (16 * (lane / 8) + (lane / 4) % 2) * D + t * (D / 4);
@@ -353,6 +374,20 @@ decode_kernel(Kv8AttentionArgs g, int whole, float *part, DevStatus *st) {
     // the item's end, here or in the next share: join the groups
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (to_groups) {
+      if (r < rows) {
+        const float inv = l == 0.0f ? 0.0f : 0x1p-8f / l;
+        T *o = out_row<T>(g, group, at.entry, at.head, r) + 2 * t;
+#pragma unroll
+        for (int q = 0; q < D / 8; ++q) {
+          o[8 * q] = from_f32<T>((acc[q][0] + acc[q][2]) * inv);
+          o[8 * q + 1] = from_f32<T>((acc[q][1] + acc[q][3]) * inv);
+        }
+      }
+      i0 = i1;
+      if (i0 < count) at.next_item(plan);
+      continue;
+    }
 #pragma unroll
     for (int q = 0; q < D / 8; ++q)
       *reinterpret_cast<float2 *>(mine + (lane / 4) * D + 8 * q + 2 * t) =
@@ -419,10 +454,18 @@ gptq_status run_decode(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   float *part = (float *)((char *)ws + 256);
   // Short histories (two rounds of the groups) gain nothing from being cut, and uncut they need
   // no second kernel: 9.8 -> 7.4 us for one token of 500 with 32 heads.
-  const int whole = g.max_blocks <= 2 * kWarps / rt;
-  GPTQ_TRY(launch_early(kernel, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, 1, s, g, whole, part,
+  // More items than CTAs: a group an item leaves no group without blocks and joins nothing, where
+  // the estimate in blocks says so (one token, 100 sequences of 60: 47 us by CTAs, 20.6 by groups;
+  // 15 of 86, 32 cache heads: 22.4 and 14.8; but 8 of 500, 32 cache heads: 18.5 and 24.2).
+  const int groups = kWarps / rt;
+  int deal = g.max_blocks <= 2 * groups ? kItemsToCtas : kUnits;
+  const int64_t items = ceil_div(g.n_seq * g.n_kv, ctas);  // of a CTA
+  if (deal == kItemsToCtas && items * g.max_blocks <= kList &&
+      ceil_div(items, groups) * (g.max_blocks + kItem) < items * (ceil_div(g.max_blocks, groups) + kItem))
+    deal = kItemsToGroups;
+  GPTQ_TRY(launch_early(kernel, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, 1, s, g, deal, part,
                         (DevStatus *)ws));
-  if (whole) return GPTQ_OK;
+  if (deal != kUnits) return GPTQ_OK;
   return launch_early(join_kernel<T, D, DecodePlan>, dim3((unsigned)ctas - 1), dim3(128), 0, 1, s, g,
                       (const float *)part, kWarps / rt, ctas);
 }

@@ -406,7 +406,9 @@ def test_attention(seqs, new, kv, group, d, lengths, mb, dtype):
 
 @pytest.mark.parametrize("seqs,new,kv,group,d,longest", [
     (5, 1, 3, 4, 128, 5000), (40, 1, 2, 8, 64, 1500), (7, 2, 1, 8, 128, 3000), (3, 4, 2, 8, 64, 2500), (200, 1, 1, 2, 64, 1300),
-    (3, 40, 2, 4, 128, 3000), (30, 9, 1, 4, 64, 1200)])
+    (3, 40, 2, 4, 128, 3000), (30, 9, 1, 4, 64, 1200),
+    # more items than there are CTAs, of a few blocks each
+    (200, 1, 2, 4, 64, 300), (170, 1, 1, 1, 128, 1000), (90, 3, 4, 4, 128, 400), (80, 8, 4, 4, 64, 250), (700, 1, 2, 2, 64, 64)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_attention_many_lengths(seqs, new, kv, group, d, longest, dtype):
     # more blocks than are dealt whole: items cut by the shares, empty sequences between them
