@@ -439,12 +439,19 @@ decode_kernel(Kv8AttentionArgs g, int deal, float *part, DevStatus *st) {
   }
 }
 
+int row_tiles(int64_t rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
+
+// Whether items are dealt whole: histories of at most two rounds of the groups.
+bool stays_whole(int64_t rows, int64_t max_blocks) {
+  return max_blocks <= 2 * kWarps / row_tiles(rows);
+}
+
 template <typename T, int D>
 gptq_status run_decode(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   using C = Decode<D>;
   if (!kv8_plan_fits(g, kRows, 1, 0)) return GPTQ_ERR_UNSUPPORTED;
   const int64_t rows = g.n_new * (g.n_heads / g.n_kv);
-  const int rt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
+  const int rt = row_tiles(rows);
   const auto kernel = rt == 1 ? decode_kernel<T, D, 1>
                               : (rt == 2 ? decode_kernel<T, D, 2> : decode_kernel<T, D, 4>);
   GPTQ_TRY(ensure_smem_attr((const void *)kernel, (int)C::kSmem));
@@ -458,7 +465,7 @@ gptq_status run_decode(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   // the estimate in blocks says so (one token, 100 sequences of 60: 47 us by CTAs, 20.6 by groups;
   // 15 of 86, 32 cache heads: 22.4 and 14.8; but 8 of 500, 32 cache heads: 18.5 and 24.2).
   const int groups = kWarps / rt;
-  int deal = g.max_blocks <= 2 * groups ? kItemsToCtas : kUnits;
+  int deal = stays_whole(rows, g.max_blocks) ? kItemsToCtas : kUnits;
   const int64_t items = ceil_div(g.n_seq * g.n_kv, ctas);  // of a CTA
   if (deal == kItemsToCtas && items * g.max_blocks <= kList &&
       ceil_div(items, groups) * (g.max_blocks + kItem) < items * (ceil_div(g.max_blocks, groups) + kItem))
@@ -492,7 +499,10 @@ size_t kv8_attention_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, i
   int64_t ctas = kMaxCtas;
   const int64_t units = (int64_t)n_seq * n_kv * max_blocks;
   if (units < ctas) ctas = units;
-  const size_t here = rows > kRows ? 0 : 256 + (size_t)(2 * ctas) * kRows * (dim + 2) * 4;
+  const size_t here = rows > kRows ? 0
+                      : stays_whole(rows, max_blocks)
+                          ? 256  // the status alone
+                          : 256 + (size_t)(2 * ctas) * kRows * (dim + 2) * 4;
   if (!takes_tiles(rows, true, dim, max_blocks)) return here;  // (with fp16 wherever with bf16)
   const size_t there = kv8_prompt_ws_bytes(n_seq, n_new, n_heads, n_kv, dim, max_blocks);
   return there > here ? there : here;

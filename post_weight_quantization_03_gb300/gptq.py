@@ -688,9 +688,18 @@ def fp8_from_codes(qpacked, zero, d_in, bits=4, stream=None):
     return codes, exps
 
 
-# The product's workspace is its status block alone.  Calls without one share a block by device,
-# which is not read back: making a tensor takes 3 us of a call's 18.
+# The workspace of a product, and of an attention that cuts no item, is its status block alone.
+# Calls without one share a block by device, which is not read back: making a tensor takes 3 to 5
+# us of a call's host time.
 _STATUS_BLOCKS = {}
+
+
+def _status_block(device):
+    block = _STATUS_BLOCKS.get(device)
+    if block is None:
+        torch = _torch()
+        block = _STATUS_BLOCKS[device] = torch.empty((256,), dtype=torch.uint8, device=device)
+    return block
 
 
 def fp8_matmul(a, a_exps, w, w_exps, a_scale=None, w_scale=None, out_dtype=None, out=None,
@@ -724,9 +733,7 @@ def fp8_matmul(a, a_exps, w, w_exps, a_scale=None, w_scale=None, out_dtype=None,
             raise TypeError("out must have out_dtype")
     lib = load()
     if ws is None:
-        ws = _STATUS_BLOCKS.get(device)
-        if ws is None:
-            ws = _STATUS_BLOCKS[device] = torch.empty((256,), dtype=u8, device=device)
+        ws = _status_block(device)
     _check(lib.gptq_fp8_matmul(
         a.data_ptr(), lda, a_exps.data_ptr(), ldae,
         a_scale.data_ptr() if a_scale is not None else None, w.data_ptr(), ldw, w_exps.data_ptr(),
@@ -821,10 +828,13 @@ def kv8_attention(q, cache, table, lengths, scale=None, causal=True, out=None, w
             raise ValueError("out must match q")
     lib = load()
     if ws is None:
-        ws = torch.empty((lib.gptq_kv8_attention_workspace_bytes(n_seq, new, heads, kv, d, mb),),
-                         dtype=torch.uint8, device=device)
-        if stream is not None:
-            _lend(stream, ws)
+        need = lib.gptq_kv8_attention_workspace_bytes(n_seq, new, heads, kv, d, mb)
+        if need <= 256:
+            ws = _status_block(device)
+        else:
+            ws = torch.empty((need,), dtype=torch.uint8, device=device)
+            if stream is not None:
+                _lend(stream, ws)
     kc, vc, ke, ve = cache
     _check(lib.gptq_kv8_attention(
         q.data_ptr(), _Strides3(qs[0], qs[1], qs[2]), _serving_dtype(dtype), n_seq, new, heads,
