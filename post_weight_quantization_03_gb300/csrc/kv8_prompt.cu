@@ -56,7 +56,6 @@ constexpr int kTurn = 4;
 // at launch: a softmax thread holds its row's 128 scores.
 constexpr int kThreads = 512;
 constexpr int kInfo = 4;
-constexpr uint32_t kChunk = kTile * 128;        // 128 rows of 128 bytes
 constexpr float kMostSum = 0x1p15f;
 
 constexpr int kKStages = 3, kVStages = 2;
@@ -184,9 +183,33 @@ __device__ __forceinline__ uint32_t swizzled(int row, int u) {
 
 // The same for rows of D bytes.
 template <int D>
-__device__ __forceinline__ uint32_t swizzled_row(int row, int u) {
+__host__ __device__ constexpr uint32_t swizzled_row(int row, int u) {
   return (uint32_t)(row * D + ((D == 128 ? u ^ (row & 7) : u ^ (row >> 1 & 3)) << 4));
 }
+
+// A tile of queries: byte of the 16-byte unit u of a row's term.
+template <int D>
+__host__ __device__ constexpr uint32_t query_byte(int row, int term, int u) {
+  return (uint32_t)(term * kTile * D) + swizzled_row<D>(row, u);
+}
+// The same memory holds an item's outputs, rows of 2 D bytes: byte of the 16-byte unit u, in the
+// row's own first two terms.
+template <int D>
+__host__ __device__ constexpr uint32_t output_byte(int row, int u) {
+  return query_byte<D>(row, u / (D / 16), u % (D / 16));
+}
+// The four warps of a tile pass from an item's outputs to the next item's queries one by one, so
+// the outputs of a warp's 32 rows may lie only where queries of these rows lie.
+template <int D>
+constexpr bool outputs_in_own_rows() {
+  for (int row = 0; row < kTile; ++row)
+    for (int u = 0; u < D / 8; ++u) {
+      const uint32_t at = output_byte<D>(row, u), in_term = at % (uint32_t)(kTile * D);
+      if (at / (uint32_t)(kTile * D) > 1 || in_term / (32 * D) != (uint32_t)(row / 32)) return false;
+    }
+  return true;
+}
+static_assert(outputs_in_own_rows<64>() && outputs_in_own_rows<128>(), "outputs in other warps' queries");
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -468,7 +491,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
         const T *q = (const T *)g.q + 16 * piece16;
         const int exist = plan.rows - row0 - wrow;  // of the warp's rows
         auto slot = [&](int mr, int term) {
-          return reinterpret_cast<uint4 *>(q_tile + term * C::kTerm + swizzled_row<D>(mr, piece16));
+          return reinterpret_cast<uint4 *>(q_tile + query_byte<D>(mr, term, piece16));
         };
         if (g.vec_q) {
           uint4 raw[2 * 32 / kAt];
@@ -624,15 +647,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
         for (int j = 0; j < 32; ++j)
           x[j] = mine > 0 ? __float_as_uint(__uint_as_float(x[j]) * inv) : 0u;
         if (whole) {
-          // through the tile of queries, whose products are done: rows of 2 D bytes
+          // through the tile of queries, whose products are done
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
             uint32_t e[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               e[q] = pack<T>(__uint_as_float(x[j + 2 * q]), __uint_as_float(x[j + 2 * q + 1]));
-            const int u = (c + j) / 8;
-            *reinterpret_cast<uint4 *>(q_tile + u / 8 * kChunk + swizzled(row, u % 8)) =
+            *reinterpret_cast<uint4 *>(q_tile + output_byte<D>(row, (c + j) / 8)) =
                 make_uint4(e[0], e[1], e[2], e[3]);
           }
         } else {
@@ -646,13 +668,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
         __syncwarp();  // a warp's rows are its own
         constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // 16 bytes a lane
         const int sub = lane / kLanes, part8 = lane % kLanes, wrow = warp % 4 * 32;
-        const uint8_t *mine8 = q_tile + part8 / 8 * kChunk;
         const int exist = plan.rows - row0 - wrow;
 #pragma unroll 4
         for (int i = 0; i < 32; i += kAt) {
           const int64_t off = __shfl_sync(0xffffffffu, o_at, i + sub);
           if (i + sub >= exist) continue;
-          const uint4 w = *reinterpret_cast<const uint4 *>(mine8 + swizzled(wrow + i + sub, part8 % 8));
+          const uint4 w = *reinterpret_cast<const uint4 *>(q_tile + output_byte<D>(wrow + i + sub, part8));
           T *o = (T *)g.out + off + 8 * part8;
           if (g.vec_o) {
             *reinterpret_cast<uint4 *>(o) = w;
