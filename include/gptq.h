@@ -563,6 +563,10 @@ size_t gptq_kv8_attention_workspace_bytes(int64_t n_seq, int64_t n_new, int n_he
  *              nothing gives zeros; one whose query is not finite gives NaN.  Bytes of the
  *              cache past `length` never matter.
  *   scale      factor of the scores (finite).
+ *   Scores, their statistics and sums are fp32, of queries held to 2^-17 of their largest element
+ *   or better; a probability is held in 8 bits of significand or more (9 for BF16 and 12 for F16 up
+ *   to 32 rows of a cache head, 11 beyond).  Weighted by its block's value scale, what is below
+ *   2^-33 of a row's largest adds to the softmax's sum and not to the output.
  *   ws         workspace of ws_bytes >= gptq_kv8_attention_workspace_bytes(...).
  * Repeated calls give identical results.  Asynchronous; a bounded device wait that gave up is
  * recorded in ws (gptq_workspace_status).  Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED, CUDA.

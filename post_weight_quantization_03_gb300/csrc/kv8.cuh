@@ -40,26 +40,36 @@ __device__ __forceinline__ float ex2(float x) {
 template <typename T>
 constexpr int kTerms = std::is_same<T, __half>::value ? 3 : 2;
 
-// x (two fp16 numbers, |x| <= 448) = term[0] + term[1] (+ term[2]), two codes each.
-template <int NT>
+// x (two fp16 numbers, |x| <= 256) = term[0] + 2^-LOW (term[1] (+ term[2])), two codes each.  The
+// first term leaves 8 at most, so LOW may be up to 5 where the lower terms' products are summed
+// apart.  What is left out is 2^(-10 - LOW) at most, or the terms' 9 or 12 bits.
+template <int NT, int LOW>
 __device__ __forceinline__ void split(__half2 x, uint32_t (&term)[NT]) {
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const __nv_fp8x2_storage_t c =
-        __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
-    term[i] = c;
-    if (i + 1 < NT) x = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
-  }
+  const auto code = [](__half2 v) {
+    return __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v), __NV_SATFINITE, __NV_E4M3);
+  };
+  const auto value = [](__nv_fp8x2_storage_t c) {
+    return __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3));
+  };
+  const __half2 up = __float2half2_rn((float)(1 << LOW)), down = __float2half2_rn(-(float)(1 << LOW));
+  term[0] = code(x);
+  x = __hfma2(value(term[0]), down, __hmul2(x, up));  // exact
+  term[1] = code(x);
+  if constexpr (NT == 3) term[2] = code(__hsub2(x, value(term[1])));
 }
 
 // Four numbers' terms, a word of codes each.
-template <int NT>
-__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t (&word)[NT]) {
+template <int NT, int LOW>
+__device__ __forceinline__ void split4(__half2 ab, __half2 cd, uint32_t (&word)[NT]) {
   uint32_t lo[NT], hi[NT];
-  split<NT>(__floats2half2_rn(a, b), lo);
-  split<NT>(__floats2half2_rn(c, d), hi);
+  split<NT, LOW>(ab, lo);
+  split<NT, LOW>(cd, hi);
 #pragma unroll
   for (int i = 0; i < NT; ++i) word[i] = lo[i] | (hi[i] << 16);
+}
+template <int NT, int LOW>
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t (&word)[NT]) {
+  split4<NT, LOW>(__floats2half2_rn(a, b), __floats2half2_rn(c, d), word);
 }
 
 // Two fp16 numbers from the lower (upper) two codes of a word.

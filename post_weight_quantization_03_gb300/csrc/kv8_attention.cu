@@ -6,16 +6,26 @@
 //
 //   products  e4m3 MMAs (m16n8k32, fp32 sums) straight on the cached codes.  The other operand
 //             is a sum of e4m3 terms: with 4 bits of significand each, two terms hold a bf16
-//             number exactly and three an fp16 one (down to 2^-17 of the row's maximum, to which
+//             number exactly and three an fp16 one (down to 2^-22 of the row's maximum, to which
 //             a row of queries is first scaled by a power of two).  An MMA has 16 rows: eight
-//             rows' first terms and, below them, their second terms, so a thread finds both
-//             halves of a score in its own accumulator.  Against fp16 MMAs on converted codes:
-//             no conversions (512 a block and warp) and half the MMAs;
+//             rows' first terms and, below them, their lower terms times 2^5, so a thread finds
+//             both halves of a score in its own accumulator.  Against fp16 MMAs on converted
+//             codes: no conversions (512 a block and warp) and half the MMAs;
 //   softmax   a block's key exponent is a factor of its scores, its value exponent lv is folded
-//             into the exponential: with y = f s + lv and the running maximum m of y,
-//               p = 2^(y - m),  acc += p vc,  l += p 2^-lv   (out = acc / l),
+//             into the exponential: with y = f s + lv, the running maximum m of y and a base b,
+//               p = 2^(y - b),  acc += p vc,  l += p 2^(b - m - lv)   (out = 2^(b - m) acc / l),
 //             so the block scales cost one addition per block; m, l, acc are fp32, and 2^8 p is
-//             split into as many terms as the queries (9 or 12 bits; less below 2^-14);
+//             split into as many terms as the queries: 9 or 12 bits, but no finer than 2^-23 of
+//             b.  What that leaves out stays in l and leaves acc, which shows behind a dominant
+//             token of small value (a sink).  So b is not m but the maximum of the block at hand
+//             (or up to kSlack above it), acc moving along, which costs nothing.  Within a block,
+//             tokens below 2^-15 of b hold fewer than 8 bits.  Where the row's sums are not
+//             large enough beside b for that to be lost in them, a second pass of products over
+//             the block adds what the terms left out: the first blocks of wide histories, blocks
+//             with a sink.  (Its code, mostly not run, costs 2 to 10 %: 48 sequences of up to
+//             8000 tokens 109.0 -> 112.5 us, 32 of 4000 with 16 rows 72.2 -> 75.9; where scores
+//             spread over tens of powers of two and it runs 124 and 91.  Scores taken again for
+//             the pass, or the pass in a loop with the first: up to 2.3 times as long.)
 //   layout    tokens are dealt to the score tiles' columns so that the 16 scores a thread owns
 //             are 16 consecutive tokens: they are, unmoved, its operand of the second MMA, whose
 //             other operand is 16 consecutive bytes of a V row (V is stored channel-major).
@@ -47,6 +57,17 @@ constexpr int kWarps = 8;                 // that compute
 constexpr int kThreads = 32 * (kWarps + 4);
 constexpr int kList = 128;                // units that have been looked up
 constexpr int kItem = 5;                  // an item's start and end, in blocks
+constexpr int kLow = 5;                   // power of two of the lower terms
+constexpr float kLowValue = 1.0f / (1 << kLow);
+// In powers of two: how far a block's maximum may lie below the base of its products, and below
+// the running maximum: acc cannot grow past fp32, and 2^20 blocks below that add 2^-14.
+constexpr float kSlack = 1.0f, kFar = 40.0f;
+// Of 2^8 p: the terms of what is smaller than kFew hold fewer than 8 bits, what is below kNone
+// never counts.  What the terms of a number below kFew leave out is 2^-15 at most, so that times
+// kRest it is a number for two terms again.
+constexpr float kFew = 0x1p-7f, kNone = 0x1p-32f, kRest = 0x1p23f;
+// A row's sums that hide what a block leaves out, at most 64 x 2^-15 x 448, to 2^-9.
+constexpr float kHide = 64 * 0x1p-15f * 448 * 0x1p9f;
 static_assert(kRows == 8 * 4, "row tiles: 1, 2 or 4");
 
 template <int D>
@@ -69,8 +90,8 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // c[i] += (sum of the terms) b[i] for N accumulators, the MMAs on one of them kept apart: the
-// first two terms as the tile's two halves, a third one alone.  x, y: the words of the first
-// and second 16 elements of K.
+// first two terms as the tile's two halves, a third one to the second's half.  x, y: the words of
+// the first and second 16 elements of K.
 template <int NT, int N>
 __device__ __forceinline__ void mma_terms(float (&c)[N][4], const uint32_t (&x)[NT],
                                           const uint32_t (&y)[NT], const uint32_t (&b0)[N],
@@ -79,7 +100,7 @@ __device__ __forceinline__ void mma_terms(float (&c)[N][4], const uint32_t (&x)[
   for (int i = 0; i < N; ++i) mma_e4m3(c[i], x[0], x[1], y[0], y[1], b0[i], b1[i]);
   if constexpr (NT == 3) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) mma_e4m3(c[i], x[2], 0u, y[2], 0u, b0[i], b1[i]);
+    for (int i = 0; i < N; ++i) mma_e4m3(c[i], 0u, x[2], 0u, y[2], b0[i], b1[i]);
   }
 }
 
@@ -122,8 +143,8 @@ __device__ __forceinline__ void load_queries(const Kv8AttentionArgs &g, int seq,
   f = fp8::pow2(e) * g.scale * kLog2e;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
-    split4<kTerms<T>>(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv,
-                      qa[i]);
+    split4<kTerms<T>, kLow>(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv,
+                            v[4 * i + 3] * inv, qa[i]);
 }
 
 // How the work is dealt: by units, items whole to CTAs (whose groups share an item's units), or
@@ -268,7 +289,8 @@ decode_kernel(Kv8AttentionArgs g, int deal, float *part, DevStatus *st) {
     const int length = seq_length(g, at.entry);
     const int limit = r >= rows ? 0 : (g.causal ? length - (int)g.n_new + r / group + 1 : length);
     uint32_t qa[D / 16][NT];
-    float f, m = -INFINITY, l = 0.0f, acc[D / 8][4];
+    // lift: 2^(b - m); hidden: the b up to which the row's sums hide what the terms leave out
+    float f, m = -INFINITY, b = -INFINITY, lift = 0.0f, hidden = -INFINITY, l = 0.0f, acc[D / 8][4];
     load_queries<T, D>(g, at.entry, at.head, r, rows, group, qa, f);
 #pragma unroll
     for (int q = 0; q < D / 8; ++q)
@@ -310,78 +332,129 @@ decode_kernel(Kv8AttentionArgs g, int deal, float *part, DevStatus *st) {
       // this thread's tokens of the block: 16 t + 2 j + {0, 1}
       const int first = (at.blk + i - i0) * kTok, tok = first + 16 * t;
       const bool cut = first + kTok > length - (g.causal ? (int)g.n_new - 1 : 0);
+      const uint8_t *vrow = ring + (size_t)(hn % H) * C::kHalf + (lane / 4) * kTok + 16 * t;
+      const int live = length - tok;  // of this thread's 16 tokens
+      auto products = [&](const uint32_t (&p)[4][NT]) {  // acc += p V
+#pragma unroll
+        for (int q0 = 0; q0 < D / 8; q0 += 4) {
+          uint32_t x[4][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint4 w4 = *reinterpret_cast<const uint4 *>(vrow + 8 * (q0 + q) * kTok);
+            x[0][q] = w4.x; x[1][q] = w4.y; x[2][q] = w4.z; x[3][q] = w4.w;
+          }
+          if (cut && live < 16) {
+            // bytes past the sequence may be NaN codes, and 0 x NaN is NaN
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int keep = live - 4 * j;
+              const uint32_t mask = keep <= 0 ? 0u : (keep >= 4 ? ~0u : (1u << (8 * keep)) - 1u);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) x[j][q] &= mask;
+            }
+          }
+          float(&c)[4][4] = *reinterpret_cast<float(*)[4][4]>(&acc[q0]);
+          mma_terms<NT, 4>(c, p[0], p[1], x[0], x[1]);
+          mma_terms<NT, 4>(c, p[2], p[3], x[2], x[3]);
+        }
+      };
+      auto scale_acc = [&](float by) {
+#pragma unroll
+        for (int q = 0; q < D / 8; ++q)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[q][j] *= by;
+      };
       uint32_t pa[4][NT];
       {
         float y[16], mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          y[j] = fmaf(s[j / 2][j % 2] + s[j / 2][j % 2 + 2], fk, (float)lv);
+          y[j] = fmaf(fmaf(s[j / 2][j % 2 + 2], kLowValue, s[j / 2][j % 2]), fk, (float)lv);
           if (cut && tok + j >= limit) y[j] = -INFINITY;
           mx = fmaxf(mx, y[j]);
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if (__any_sync(0xffffffffu, mx > m)) {
-          const float mn = fmaxf(m, mx);
-          const float shrink = ex2(m - (mn == -INFINITY ? 0.0f : mn));  // 0 for the first block
+        const bool move = mx > b || (mx < b - kSlack && mx >= m - kFar);
+        if (__any_sync(0xffffffffu, move)) {
+          const float to = move ? mx : b, by = move ? ex2(b - to) : 1.0f;  // 0 for the first block
+          const float mn = fmaxf(m, to), unit = mn == -INFINITY ? 0.0f : mn;
+          l *= ex2(m - unit);
+          b = to;
           m = mn;
-          l *= shrink;
-#pragma unroll
-          for (int q = 0; q < D / 8; ++q)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[q][j] *= shrink;
+          lift = ex2(b - unit);
+          scale_acc(by);
         }
-        const float base = (m == -INFINITY ? 0.0f : m) - 8.0f;
+        const float base = (b == -INFINITY ? 0.0f : b) - 8.0f;
         float sum = 0.0f;
+        __half2 x[8];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           y[j] = ex2(y[j] - base);
           sum += y[j];
         }
-        l = fmaf(sum, 0x1p-8f * fp8::pow2(-lv), l);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          split4<NT>(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3], pa[q]);
-      }
-      arrived();
-      const uint8_t *vrow = ring + (size_t)(hn % H) * C::kHalf + (lane / 4) * kTok + 16 * t;
-      const int live = length - tok;  // of this thread's 16 tokens
+        for (int j = 0; j < 8; ++j) x[j] = __floats2half2_rn(y[2 * j], y[2 * j + 1]);
+        l = fmaf(sum * lift, 0x1p-8f * fp8::pow2(-lv), l);
+        __half2 low = x[0];
 #pragma unroll
-      for (int q0 = 0; q0 < D / 8; q0 += 4) {
-        uint32_t x[4][4];
+        for (int j = 1; j < 8; ++j) low = __hmin2(low, x[j]);
+        low = __hmin2(low, __lowhigh2highlow(low));
+        if (__builtin_expect(__any_sync(0xffffffffu, __low2float(low) < kFew && b > hidden), 0)) {
+          float mass = 0.0f;  // of the row's sums
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint4 w4 = *reinterpret_cast<const uint4 *>(vrow + 8 * (q0 + q) * kTok);
-          x[0][q] = w4.x; x[1][q] = w4.y; x[2][q] = w4.z; x[3][q] = w4.w;
-        }
-        if (cut && live < 16) {
-          // bytes past the sequence may be NaN codes, and 0 x NaN is NaN
+          for (int q = 0; q < D / 8; ++q)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int keep = live - 4 * j;
-            const uint32_t mask = keep <= 0 ? 0u : (keep >= 4 ? ~0u : (1u << (8 * keep)) - 1u);
+            for (int j = 0; j < 2; ++j) mass += fabsf(fmaf(acc[q][j + 2], kLowValue, acc[q][j]));
+          mass += __shfl_xor_sync(0xffffffffu, mass, 1);
+          mass += __shfl_xor_sync(0xffffffffu, mass, 2);
+          hidden = fmaxf(hidden, b + __log2f(mass / (kHide * D)));
+          bool few = false;  // without the zeros of masked tokens
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[j][q] &= mask;
+          for (int j = 0; j < 16; ++j) few |= y[j] < kFew && y[j] >= kNone;
+          if (__builtin_expect(__any_sync(0xffffffffu, few && b > hidden), 0)) {
+            uint32_t rest[4][NT];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t term[NT];
+              split4<NT, kLow>(x[2 * q], x[2 * q + 1], term);
+              float left[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float had = 0.0f;
+#pragma unroll
+                for (int i = NT - 1; i >= 0; --i)
+                  had = fmaf(i == 0 ? kLowValue : 1.0f, had, fp8::unpack1((uint8_t)(term[i] >> (8 * j))));
+                left[j] = y[4 * q + j] < kFew ? (y[4 * q + j] - had) * kRest : 0.0f;
+              }
+              split4<NT, kLow>(left[0], left[1], left[2], left[3], rest[q]);
+            }
+            scale_acc(kRest);
+            arrived();
+            products(rest);
+            scale_acc(1.0f / kRest);
           }
         }
-        float(&c)[4][4] = *reinterpret_cast<float(*)[4][4]>(&acc[q0]);
-        mma_terms<NT, 4>(c, pa[0], pa[1], x[0], x[1]);
-        mma_terms<NT, 4>(c, pa[2], pa[3], x[2], x[3]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) split4<NT, kLow>(x[2 * q], x[2 * q + 1], pa[q]);
       }
+      arrived();
+      products(pa);
       release();
     }
 
     // the item's end, here or in the next share: join the groups
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
+    const float of_m = 0x1p-8f * lift;  // acc in units of 2^m
     if (to_groups) {
       if (r < rows) {
-        const float inv = l == 0.0f ? 0.0f : 0x1p-8f / l;
+        const float inv = l == 0.0f ? 0.0f : of_m / l;
         T *o = out_row<T>(g, group, at.entry, at.head, r) + 2 * t;
 #pragma unroll
         for (int q = 0; q < D / 8; ++q) {
-          o[8 * q] = from_f32<T>((acc[q][0] + acc[q][2]) * inv);
-          o[8 * q + 1] = from_f32<T>((acc[q][1] + acc[q][3]) * inv);
+          o[8 * q] = from_f32<T>(fmaf(acc[q][2], kLowValue, acc[q][0]) * inv);
+          o[8 * q + 1] = from_f32<T>(fmaf(acc[q][3], kLowValue, acc[q][1]) * inv);
         }
       }
       i0 = i1;
@@ -391,7 +464,7 @@ decode_kernel(Kv8AttentionArgs g, int deal, float *part, DevStatus *st) {
 #pragma unroll
     for (int q = 0; q < D / 8; ++q)
       *reinterpret_cast<float2 *>(mine + (lane / 4) * D + 8 * q + 2 * t) =
-          make_float2((acc[q][0] + acc[q][2]) * 0x1p-8f, (acc[q][1] + acc[q][3]) * 0x1p-8f);
+          make_float2(fmaf(acc[q][2], kLowValue, acc[q][0]) * of_m, fmaf(acc[q][3], kLowValue, acc[q][1]) * of_m);
     if (t == 0) {
       mine[8 * D + lane / 4] = m;
       mine[8 * D + 8 + lane / 4] = l;

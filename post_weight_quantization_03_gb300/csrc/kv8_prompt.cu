@@ -537,7 +537,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float2 a = pair<T>(w[2 * j]), c = pair<T>(w[2 * j + 1]);
-            split4<NT>(a.x * inv, a.y * inv, c.x * inv, c.y * inv, word[j]);
+            split4<NT, 0>(a.x * inv, a.y * inv, c.x * inv, c.y * inv, word[j]);
           }
 #pragma unroll
           for (int term = 0; term < NT; ++term)

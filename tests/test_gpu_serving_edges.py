@@ -41,3 +41,95 @@ def test_prompts_of_many_short_items(seqs, new, kv, group, longest, d, dtype, al
         assert torch.equal(results[0], other)
     some = rng.permutation(seqs)[:8]
     _check_attention(results[0][some], q[some], cache, table[some], lengths[some])
+
+
+# ---------------------------------------------------------------------------------------
+# A dominant token (an attention sink) with a small value
+# ---------------------------------------------------------------------------------------
+
+def _sink_case(seqs, kv, new, group, d, tokens, weight, dtype, at):
+    """Queries, cache and table of sequences with ``tokens`` tokens, of which token ``at`` takes
+    ``weight`` of every row's softmax and has values of 1 %; the others' scores are a unit normal
+    and their values have mean 0.5 and variance 1."""
+    rng = np.random.default_rng(tokens + new)
+    mb, kinds = -(-tokens // 64), min(seqs, 3)              # further sequences read the same blocks
+    n = kinds * mb
+    ones = rng.choice([-1.0, 1.0], d)                       # the direction that the queries share
+    k = rng.standard_normal((n, kv, 64, d))
+    v = 0.5 + rng.standard_normal((n, kv, d, 64))
+    table = rng.permutation(n).reshape(kinds, mb).astype(np.int32)
+    level = np.log(weight / (1 - weight)) + np.log(tokens) + 0.5
+    pages = table[:, at // 64]
+    k[pages, :, at % 64] = level / np.sqrt(d) * ones         # q = ones * sqrt(scores' variance)
+    v[pages, :, :, at % 64] = 0.01 * rng.standard_normal((kinds, kv, d))
+    cache = (SO.encode(k * 64), SO.encode(v * 64), np.full((n, kv), 121, np.uint8), np.full((n, kv), 121, np.uint8))
+    q = ones + 0.02 * rng.standard_normal((seqs, new, kv * group, d))
+    return torch.from_numpy(q).to(DT[dtype]), cache, table[np.arange(seqs) % kinds]
+
+
+SINKS = [  # rows: one, eight, sixteen and thirty-two; long histories
+    (1, 1, 1, 1, 128, 4000, 0.99), (1, 2, 1, 1, 64, 32768, 0.97), (2, 1, 1, 8, 64, 1000, 0.999), (1, 1, 1, 8, 128, 8000, 0.999),
+    (1, 1, 1, 8, 64, 16000, 0.97), (1, 1, 1, 8, 64, 32768, 0.9), (1, 1, 2, 8, 64, 4000, 0.99), (1, 1, 2, 8, 128, 2000, 0.999),
+    (1, 1, 2, 16, 64, 1000, 0.999), (1, 1, 4, 8, 64, 4000, 0.99), (1, 1, 4, 8, 64, 32768, 0.97), (1, 1, 2, 16, 64, 16000, 0.97),
+    # long ones inside one share
+    (160, 1, 1, 8, 128, 4000, 0.99), (160, 1, 2, 8, 64, 4000, 0.99), (160, 1, 4, 8, 64, 4000, 0.99), (152, 1, 1, 8, 64, 16000, 0.97),
+    (152, 1, 4, 8, 64, 16000, 0.97),
+    # short ones: dealt whole to CTAs and to groups
+    (3, 2, 1, 8, 128, 1000, 0.999), (4, 1, 2, 8, 64, 500, 0.999), (3, 1, 4, 8, 64, 250, 0.999), (200, 1, 1, 4, 64, 180, 0.9999),
+    (90, 2, 3, 4, 128, 250, 0.999), (170, 1, 4, 8, 64, 120, 0.999),
+    # and one that leaves the others 2^-25 to 2^-28 each
+    (1, 1, 1, 8, 64, 8000, 0.99995), (1, 1, 4, 8, 64, 8000, 0.99995),
+]
+
+
+@pytest.mark.parametrize("seqs,kv,new,group,d,tokens,weight", SINKS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("first", [True, False])
+def test_attention_with_a_dominant_token(seqs, kv, new, group, d, tokens, weight, dtype, first):
+    q, cache, table = _sink_case(seqs, kv, new, group, d, tokens, weight, dtype, 3 if first else tokens * 2 // 3)
+    lengths = [tokens] * seqs
+    dev = _dev_cache(cache)
+    out = gptq.kv8_attention(q.to(DEV), dev, _i32(table), _i32(lengths), causal=False)
+    assert torch.equal(out, gptq.kv8_attention(q.to(DEV), dev, _i32(table), _i32(lengths), causal=False))
+    some = slice(0, 4)
+    _check_attention(out[some], q[some], cache, table[some], lengths[some], causal=False)
+
+
+@pytest.mark.parametrize("new,group", [(1, 8), (2, 8), (4, 8)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_attention_with_dominant_tokens_of_many_levels(new, group, dtype):
+    # in every block a few tokens 2^10, 2^20, 2^30 above the rest, whose values are as small as they are large
+    d, tokens = 64, 3000
+    rng = np.random.default_rng(1)
+    n = -(-tokens // 64)
+    ones = rng.choice([-1.0, 1.0], d)
+    level = rng.choice([0, 7, 14, 21], (n, 1, 64, 1), p=[0.9, 0.05, 0.03, 0.02])     # nats
+    k = rng.standard_normal((n, 1, 64, d)) * 0.3 + level / np.sqrt(d) * ones
+    v = (0.5 + rng.standard_normal((n, 1, 64, d))) * np.exp2(-10.0 * (level / 7) / 3)
+    cache = (SO.encode(k * 64), SO.encode(v.transpose(0, 1, 3, 2).copy() * 64), np.full((n, 1), 121, np.uint8),
+             np.full((n, 1), 121, np.uint8))
+    table = rng.permutation(n).reshape(1, n).astype(np.int32)
+    q = torch.from_numpy(ones + 0.02 * rng.standard_normal((1, new, group, d))).to(DT[dtype])
+    out = gptq.kv8_attention(q.to(DEV), _dev_cache(cache), _i32(table), _i32([tokens]))
+    _check_attention(out, q, cache, table, [tokens])
+
+
+@pytest.mark.parametrize("new,group,d,tokens", [(1, 1, 128, 700), (1, 8, 128, 3000), (1, 8, 64, 100), (2, 8, 64, 3000), (4, 8, 64, 700),
+                                                (4, 8, 128, 3000)])
+@pytest.mark.parametrize("level", [10.0, 14.0, 17.0])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_attention_behind_tokens_without_values(new, group, d, tokens, level, dtype):
+    # in every block eight tokens that take nearly all of the weight and have no value at all
+    rng = np.random.default_rng(int(level) + tokens)
+    n = -(-tokens // 64)
+    ones = rng.choice([-1.0, 1.0], d)
+    k = rng.standard_normal((n, 1, 64, d))
+    v = 0.5 + rng.standard_normal((n, 1, 64, d))
+    k[:, :, 5::8] = level / np.sqrt(d) * ones
+    v[:, :, 5::8] = 0
+    cache = (SO.encode(k * 64), SO.encode(v.transpose(0, 1, 3, 2).copy() * 64), np.full((n, 1), 121, np.uint8),
+             np.full((n, 1), 121 + 16, np.uint8))
+    table = rng.permutation(n).reshape(1, n).astype(np.int32)
+    q = torch.from_numpy(ones + 0.02 * rng.standard_normal((1, new, group, d))).to(DT[dtype])
+    out = gptq.kv8_attention(q.to(DEV), _dev_cache(cache), _i32(table), _i32([tokens]))
+    _check_attention(out, q, cache, table, [tokens])
