@@ -579,6 +579,33 @@ gptq_status gptq_kv8_attention(const void *q, const int64_t *q_strides, int dtyp
                                float scale, void *out, const int64_t *o_strides, void *ws,
                                size_t ws_bytes, gptq_stream_t stream);
 
+/*
+ * gptq_debug_fp8_matmul_lost_copy, gptq_debug_kv8_attention_lost_copy: test hooks of the bounded
+ * device waits, as gptq_debug_hessian_lost_stage.
+ *
+ * They run gptq_fp8_matmul (without row factors) and gptq_kv8_attention with copy number lost_copy
+ * of every CTA left out (of W and A: one for 128 elements of K; of keys: one for 128 tokens, or, up
+ * to 32 rows of a cache head, of keys and values in turn, for 64 tokens of a group of warps), and
+ * every wait of the kernel limited to wait_ns (1e3 .. 1e10) nanoseconds.  The waits for that copy
+ * give up; the kernel records GPTQ_ERR_TIMEOUT in ws and ends with none of its copies and
+ * tensor-core operations in flight.  out is then undefined.  Where no CTA has such a copy the call
+ * is the regular one.
+ * SYNCHRONIZE `stream` and return the device status.  Errors: as the regular calls.
+ */
+gptq_status gptq_debug_fp8_matmul_lost_copy(const uint8_t *a, int64_t lda, const uint8_t *a_exps,
+                                            int64_t ldae, const uint8_t *w, int64_t ldw,
+                                            const uint8_t *w_exps, int64_t ldwe, int64_t m,
+                                            int64_t n, int64_t k, void *out, int odtype,
+                                            int64_t ldo, int64_t lost_copy, uint64_t wait_ns,
+                                            void *ws, size_t ws_bytes, gptq_stream_t stream);
+gptq_status gptq_debug_kv8_attention_lost_copy(
+    const void *q, const int64_t *q_strides, int dtype, int64_t n_seq, int64_t n_new, int n_heads,
+    int n_kv, int dim, const uint8_t *k, const uint8_t *v, const uint8_t *k_exps,
+    const uint8_t *v_exps, int64_t n_blocks, const int32_t *table, int64_t ld_table,
+    int64_t max_blocks, const int32_t *lengths, int causal, float scale, void *out,
+    const int64_t *o_strides, int64_t lost_copy, uint64_t wait_ns, void *ws, size_t ws_bytes,
+    gptq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

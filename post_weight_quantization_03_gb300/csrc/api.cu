@@ -357,24 +357,48 @@ size_t gptq_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   return fp8_matmul_ws_bytes(m, n, k);
 }
 
+static gptq_status fp8_matmul_checked(const Fp8MatmulArgs &g, void *ws, size_t ws_bytes,
+                                      gptq_stream_t stream) {
+  if (g.M < 0 || g.N < 1 || g.K < 1 || (g.odtype != GPTQ_F16 && g.odtype != GPTQ_BF16) || g.ldo < g.N)
+    return GPTQ_ERR_INVALID_ARG;
+  if (!fp8_codes_ok(g.w, g.ldw, g.K) || !fp8_exps_ok(g.we, g.ldwe, g.K) || !aligned(g.rw, 4))
+    return GPTQ_ERR_INVALID_ARG;
+  if (g.M > 0 && (!fp8_codes_ok(g.a, g.lda, g.K) || !fp8_exps_ok(g.ae, g.ldae, g.K) ||
+                  !aligned(g.ra, 4) || !g.out || !aligned(g.out, 2)))
+    return GPTQ_ERR_INVALID_ARG;
+  if (g.K > kFp8MaxWidth || g.M > kFp8MaxRows || g.N > kFp8MaxRows) return GPTQ_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, 256) || ws_bytes < fp8_matmul_ws_bytes(g.M, g.N, g.K))
+    return GPTQ_ERR_WORKSPACE;
+  return launch_fp8_matmul(g, ws, (cudaStream_t)stream);
+}
+
 gptq_status gptq_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_exps, int64_t ldae,
                             const float *a_scale, const uint8_t *w, int64_t ldw,
                             const uint8_t *w_exps, int64_t ldwe, const float *w_scale, int64_t m,
                             int64_t n, int64_t k, void *out, int odtype, int64_t ldo, void *ws,
                             size_t ws_bytes, gptq_stream_t stream) {
-  if (m < 0 || n < 1 || k < 1 || (odtype != GPTQ_F16 && odtype != GPTQ_BF16) || ldo < n)
-    return GPTQ_ERR_INVALID_ARG;
-  if (!fp8_codes_ok(w, ldw, k) || !fp8_exps_ok(w_exps, ldwe, k) || !aligned(w_scale, 4))
-    return GPTQ_ERR_INVALID_ARG;
-  if (m > 0 && (!fp8_codes_ok(a, lda, k) || !fp8_exps_ok(a_exps, ldae, k) || !aligned(a_scale, 4) ||
-                !out || !aligned(out, 2)))
-    return GPTQ_ERR_INVALID_ARG;
-  if (k > kFp8MaxWidth || m > kFp8MaxRows || n > kFp8MaxRows) return GPTQ_ERR_UNSUPPORTED;
-  if (!ws || !aligned(ws, 256) || ws_bytes < fp8_matmul_ws_bytes(m, n, k))
-    return GPTQ_ERR_WORKSPACE;
-  Fp8MatmulArgs g{a, lda, a_exps, ldae, a_scale, w, ldw, w_exps, ldwe, w_scale, m, n, k,
+  return fp8_matmul_checked({a, lda, a_exps, ldae, a_scale, w, ldw, w_exps, ldwe, w_scale, m, n, k,
+                             out, odtype, ldo}, ws, ws_bytes, stream);
+}
+
+// A test hook's copy that is left out, and budget of the waits.
+static bool lost_ok(int64_t lost, uint64_t wait_ns) {
+  return lost >= 0 && lost <= INT32_MAX && wait_ns >= 1000 && wait_ns <= 10000000000ull;
+}
+
+gptq_status gptq_debug_fp8_matmul_lost_copy(const uint8_t *a, int64_t lda, const uint8_t *a_exps,
+                                            int64_t ldae, const uint8_t *w, int64_t ldw,
+                                            const uint8_t *w_exps, int64_t ldwe, int64_t m,
+                                            int64_t n, int64_t k, void *out, int odtype,
+                                            int64_t ldo, int64_t lost_copy, uint64_t wait_ns,
+                                            void *ws, size_t ws_bytes, gptq_stream_t stream) {
+  if (!lost_ok(lost_copy, wait_ns) || m < 1) return GPTQ_ERR_INVALID_ARG;
+  Fp8MatmulArgs g{a, lda, a_exps, ldae, nullptr, w, ldw, w_exps, ldwe, nullptr, m, n, k,
                   out, odtype, ldo};
-  return launch_fp8_matmul(g, ws, (cudaStream_t)stream);
+  g.wait_ns = wait_ns;
+  g.lost = lost_copy;
+  GPTQ_TRY(fp8_matmul_checked(g, ws, ws_bytes, stream));
+  return gptq_workspace_status(ws, stream);
 }
 
 // What the two cache calls share; `ok` = valid, UNSUPPORTED for sizes outside the limits.
@@ -438,13 +462,13 @@ size_t gptq_kv8_attention_workspace_bytes(int64_t n_seq, int64_t n_new, int n_he
   return kv8_attention_ws_bytes((int)n_seq, n_new, n_heads, n_kv, dim, (int)max_blocks);
 }
 
-gptq_status gptq_kv8_attention(const void *q, const int64_t *q_strides, int dtype, int64_t n_seq,
-                               int64_t n_new, int n_heads, int n_kv, int dim, const uint8_t *k,
-                               const uint8_t *v, const uint8_t *k_exps, const uint8_t *v_exps,
-                               int64_t n_blocks, const int32_t *table, int64_t ld_table,
-                               int64_t max_blocks, const int32_t *lengths, int causal,
-                               float scale, void *out, const int64_t *o_strides, void *ws,
-                               size_t ws_bytes, gptq_stream_t stream) {
+static gptq_status kv8_attention_checked(
+    const void *q, const int64_t *q_strides, int dtype, int64_t n_seq, int64_t n_new, int n_heads,
+    int n_kv, int dim, const uint8_t *k, const uint8_t *v, const uint8_t *k_exps,
+    const uint8_t *v_exps, int64_t n_blocks, const int32_t *table, int64_t ld_table,
+    int64_t max_blocks, const int32_t *lengths, int causal, float scale, void *out,
+    const int64_t *o_strides, int64_t lost, uint64_t wait_ns, void *ws, size_t ws_bytes,
+    gptq_stream_t stream) {
   if ((dtype != GPTQ_F16 && dtype != GPTQ_BF16) || !strides_ok(q_strides) || !strides_ok(o_strides))
     return GPTQ_ERR_INVALID_ARG;
   if (n_heads < 1 || n_kv < 1 || n_heads % n_kv != 0 || !(scale - scale == 0.0f))
@@ -470,7 +494,34 @@ gptq_status gptq_kv8_attention(const void *q, const int64_t *q_strides, int dtyp
   g.lengths = lengths; g.causal = causal ? 1 : 0; g.scale = scale;
   g.vec_q = strided_alignment(q, q_strides, 2) == 16;
   g.vec_o = strided_alignment(out, o_strides, 2) == 16;
+  g.lost = lost; g.wait_ns = wait_ns;
   return launch_kv8_attention(g, ws, (cudaStream_t)stream);
+}
+
+gptq_status gptq_kv8_attention(const void *q, const int64_t *q_strides, int dtype, int64_t n_seq,
+                               int64_t n_new, int n_heads, int n_kv, int dim, const uint8_t *k,
+                               const uint8_t *v, const uint8_t *k_exps, const uint8_t *v_exps,
+                               int64_t n_blocks, const int32_t *table, int64_t ld_table,
+                               int64_t max_blocks, const int32_t *lengths, int causal,
+                               float scale, void *out, const int64_t *o_strides, void *ws,
+                               size_t ws_bytes, gptq_stream_t stream) {
+  return kv8_attention_checked(q, q_strides, dtype, n_seq, n_new, n_heads, n_kv, dim, k, v, k_exps,
+                               v_exps, n_blocks, table, ld_table, max_blocks, lengths, causal,
+                               scale, out, o_strides, -1, tc::kWaitNs, ws, ws_bytes, stream);
+}
+
+gptq_status gptq_debug_kv8_attention_lost_copy(
+    const void *q, const int64_t *q_strides, int dtype, int64_t n_seq, int64_t n_new, int n_heads,
+    int n_kv, int dim, const uint8_t *k, const uint8_t *v, const uint8_t *k_exps,
+    const uint8_t *v_exps, int64_t n_blocks, const int32_t *table, int64_t ld_table,
+    int64_t max_blocks, const int32_t *lengths, int causal, float scale, void *out,
+    const int64_t *o_strides, int64_t lost_copy, uint64_t wait_ns, void *ws, size_t ws_bytes,
+    gptq_stream_t stream) {
+  if (!lost_ok(lost_copy, wait_ns)) return GPTQ_ERR_INVALID_ARG;
+  GPTQ_TRY(kv8_attention_checked(q, q_strides, dtype, n_seq, n_new, n_heads, n_kv, dim, k, v, k_exps,
+                                 v_exps, n_blocks, table, ld_table, max_blocks, lengths, causal,
+                                 scale, out, o_strides, lost_copy, wait_ns, ws, ws_bytes, stream));
+  return gptq_workspace_status(ws, stream);
 }
 
 }  // extern "C"

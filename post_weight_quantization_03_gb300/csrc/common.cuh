@@ -104,6 +104,10 @@ __device__ __forceinline__ void wait_for_grids() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+namespace tc {
+constexpr uint64_t kWaitNs = 2000000000ull;  // a device wait's budget, 2 s: far beyond any legitimate one
+}
+
 // Device-side status block at the start of every workspace.
 struct DevStatus {
   int status;        // gptq_status recorded by kernels (0 = OK); first writer wins
@@ -246,6 +250,8 @@ struct Fp8MatmulArgs {
   const float *rw;                   // [N] row scale or null
   int64_t M, N, K;
   void *out; int odtype; int64_t ldo;
+  uint64_t wait_ns = tc::kWaitNs;
+  int64_t lost = -1;                 // test hook: a copy of each CTA that is left out
 };
 size_t fp8_matmul_ws_bytes(int64_t M, int64_t N, int64_t K);
 gptq_status launch_fp8_matmul(const Fp8MatmulArgs &g, void *ws, cudaStream_t s);
@@ -271,6 +277,8 @@ struct Kv8AttentionArgs {
   const int32_t *lengths;
   int causal; float scale;
   int vec_q, vec_o;                          // rows of q, out are 16-byte aligned
+  uint64_t wait_ns = tc::kWaitNs;
+  int64_t lost = -1;                         // test hook: a copy of each CTA that is left out
 };
 size_t kv8_attention_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int dim,
                               int max_blocks);

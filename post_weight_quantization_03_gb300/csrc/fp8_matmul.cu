@@ -66,6 +66,8 @@ struct MmParams {
   int splits;           // CTAs of a cluster that share a tile's k-blocks
   uint32_t ring_bytes;
   int acc_cols, tmem_cols;  // columns of an accumulator; allocated
+  uint64_t wait_ns;
+  int lost;             // test hook: this copy of the producer's is left out
 };
 
 template <typename TO>
@@ -129,7 +131,9 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   uint64_t *sempty = sfull + kScaleStages;
   uint64_t *tfull = sempty + kScaleStages;
   uint64_t *tempty = tfull + 2;
-  uint32_t *tmem_slot = (uint32_t *)(tempty + 2);
+  uint64_t *mdone = tempty + 2;       // every MMA has completed
+  uint32_t *tmem_slot = (uint32_t *)(mdone + 1);
+  const tc::Waits waits{st, p.wait_ns};
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t stage_bytes = (uint32_t)(BM + p.tn) * BK;
@@ -151,6 +155,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
       tc::mbar_init(&tfull[b], 1);
       tc::mbar_init(&tempty[b], 4);
     }
+    tc::mbar_init(mdone, 1);
     tc::mbar_fence_init();
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, p.tmem_cols);
@@ -166,26 +171,26 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   // with few tiles every CTA has one and a second accumulator is not allocated
   const uint32_t second = (uint32_t)p.acc_cols, sc_cols = tmem + (p.tmem_cols == (int)kTmemCols ? 2 : 1) * second;
 
+  bool ok = true;                   // false once a wait has given up: the role ends
+  int s = 0, n = 0;                 // producer and issuer: stage of the ring; copies
+  uint32_t ph = 1;
   // (inside elect_one() one thread is known to run, and addresses stay in uniform registers)
   if (warp == 0 && tc::elect_one()) {
     // ---------------- producer ----------------
     tc::tma_prefetch_desc(&mw);
     tc::tma_prefetch_desc(&ma);
-    int s = 0;
-    uint32_t ph = 1;
-    for (int t = first; t < p.n_tiles; t += step) {
+    for (int t = first; t < p.n_tiles && ok; t += step) {
       const int32_t n0 = (t % p.n_w) * BM, m0 = (t / p.n_w) * p.tn;
-      bool ok = true;
       for (int kb = k0; kb < k1; ++kb) {
-        ok = tc::mbar_wait(&empty[s], ph, st);
+        ok = tc::mbar_wait_compact(&empty[s], ph, waits);
         if (!ok) break;
         uint8_t *base = ring + s * stage_bytes;
-        tc::mbar_arrive_expect_tx(&full[s], stage_bytes);
+        // (a lost copy is one whose last bytes never arrive)
+        tc::mbar_arrive_expect_tx(&full[s], stage_bytes + (n++ == p.lost ? 16u : 0u));
         tc::tma_load_2d(base, &mw, kb * BK, n0, &full[s]);
         tc::tma_load_2d(base + BM * BK, &ma, kb * BK, m0, &full[s]);
         if (++s == p.stages) s = 0, ph ^= 1;
       }
-      if (!ok) break;
     }
   } else if (warp == 1 && tc::elect_one()) {
     // ---------------- MMA issuer ----------------
@@ -193,20 +198,20 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     const uint32_t idesc = (1u << 23) | ((uint32_t)(p.tn >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
     const uint32_t ring0 = (tc::smem_u32(ring) >> 4) | (1u << 16), stage16 = stage_bytes >> 4;
     const uint32_t sc0 = tc::smem_u32(sscale);
-    int s = 0, g = 0, it = 0;
-    uint32_t ph = 0, at = ring0;    // lower word of the stage's first descriptor
-    bool ok = true;
+    int g = 0, it = 0;
+    uint32_t at = ring0;            // lower word of the stage's first descriptor
+    ph = 0;
 #pragma unroll 1
     for (int t = first; t < p.n_tiles && ok; t += step, ++it) {
       const int b = it & 1;
-      ok = tc::mbar_wait_compact(&tempty[b], ((it >> 1) & 1) ^ 1, st);
+      ok = tc::mbar_wait_compact(&tempty[b], ((it >> 1) & 1) ^ 1, waits);
       if (!ok) break;
       tc::tc_fence_after();
       const uint32_t acc = tmem + b * second;
 #pragma unroll 1
       for (int kb = k0; kb < k1 && ok; kb += 4, ++g) {
         const int q = g % kScaleStages;
-        ok = tc::mbar_wait_compact(&sfull[q], (g / kScaleStages) & 1, st);
+        ok = tc::mbar_wait_compact(&sfull[q], (g / kScaleStages) & 1, waits);
         if (!ok) break;
         tc::tc_fence_after();
         // two groups of columns in turn: the scale warp's ring keeps a third group's copy from
@@ -218,7 +223,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (kb + j >= k1) break;
-          ok = tc::mbar_wait_compact(&full[s], ph, st);
+          ok = tc::mbar_wait_compact(&full[s], ph, waits);
           if (!ok) break;
           tc::tc_fence_after();
           const uint32_t id = idesc | ((uint32_t)j << 29) | ((uint32_t)j << 4);
@@ -237,7 +242,6 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   } else if (warp == 6) {
     // ---------------- scales ----------------
     int g = 0;
-    bool ok = true;
     for (int t = first; t < p.n_tiles && ok; t += step) {
       const int64_t m0 = (int64_t)(t / p.n_w) * p.tn;
       const uint8_t *we = p.we + (int64_t)(t % p.n_w) * p.ldwe;
@@ -254,7 +258,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         const uint32_t ww = *reinterpret_cast<const uint32_t *>(we + 4 * sb);
         const int q = g % kScaleStages;
         // two TMEM groups: wait for the MMAs of two groups back, not only for this slot's
-        if (g >= 2) ok = tc::mbar_wait(&sempty[(g - 2) % kScaleStages], ((g - 2) / kScaleStages) & 1, st);
+        if (g >= 2) ok = tc::mbar_wait_compact(&sempty[(g - 2) % kScaleStages], ((g - 2) / kScaleStages) & 1, waits);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -280,7 +284,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
         for (int j = et; j < cols; j += 128) sra[j] = p.ra ? p.ra[m0 + j] : 1.0f;
       }
       const float rw = (p.rw && n < p.N) ? p.rw[n] : 1.0f;
-      const bool ok = tc::mbar_wait(&tfull[b], (it >> 1) & 1, st);
+      ok = tc::mbar_wait_compact(&tfull[b], (it >> 1) & 1, waits);
       if (!tc::named_barrier_and(1, 128, ok)) break;
       tc::tc_fence_after();
       TO *o = (TO *)p.out + m0 * p.ldo + n;
@@ -307,7 +311,21 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   }
   __syncwarp();
   tc::tc_fence_before();
-  __syncthreads();
+  if (!__syncthreads_and(ok)) {
+    // A wait has given up: what is in flight gets one more, bounded, to land or to complete before
+    // the CTA leaves and the TMEM is released.  (In the regular course all of it has been waited
+    // for; waiting here again costs a single token's product 0.3 us of 5.4.)
+    if (warp == 0 && tc::elect_one()) {
+      // stages before s are of this round of the ring, the others of the one before
+#pragma unroll 1
+      for (int i = 0; i < (n < p.stages ? s : p.stages); ++i)
+        tc::mbar_wait_compact(&full[i], i < s ? ph ^ 1 : ph, waits);
+    } else if (warp == 1 && tc::elect_one()) {
+      tc::mma_commit(mdone);
+      tc::mbar_wait_compact(mdone, 0, waits);
+    }
+    __syncwarp();
+  }
   if (warp == 1) tc::tmem_dealloc(tmem, p.tmem_cols);
   if (p.splits > 1) {
     // one tile per cluster: the ring holds this CTA's partial sums [tn][128]
@@ -442,6 +460,8 @@ gptq_status run(const Fp8MatmulArgs &g, DevStatus *st, cudaStream_t s) {
   if (tiles * 8 > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
   p.n_tiles = (int)tiles;
   p.splits = sh.splits;
+  p.wait_ns = g.wait_ns;
+  p.lost = (int)g.lost;
   const bool one_tile = sh.splits > 1 || tiles <= (int64_t)sms * sh.per_sm;
   p.ring_bytes = sh.per_sm > 1 ? kRingBytesTwo : kRingBytes;
   const int fit = (int)(p.ring_bytes / (uint32_t)((BM + sh.tn) * BK));

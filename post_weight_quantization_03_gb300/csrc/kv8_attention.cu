@@ -166,6 +166,7 @@ decode_kernel(Kv8AttentionArgs g, int deal, float *part, DevStatus *st) {
   int2 *list = (int2 *)(spart + kWarps * C::kWarpPart);  // block and head (-1: none); exponents
   uint64_t *full = (uint64_t *)(list + kList), *empty = full + kWarps * C::kSlots;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const tc::Waits waits{st, g.wait_ns};
   if (threadIdx.x == 0) {
     for (int s = 0; s < G * H; ++s) {
       tc::mbar_init(&full[s], 1);
@@ -236,12 +237,12 @@ decode_kernel(Kv8AttentionArgs g, int deal, float *part, DevStatus *st) {
         const int slot = lane * H + hn % H;
         if (hn < H || tc::mbar_try_wait(&empty[slot], (hn / H - 1) & 1)) {
           const int ph = list[i % kList].x;
-          if (ph >= 0) {
+          if (ph < 0) {
+            tc::mbar_arrive(&full[slot]);
+          } else if (hn != g.lost) {
             tc::mbar_arrive_expect_tx(&full[slot], C::kHalf);
             tc::bulk_load(smem + (size_t)slot * C::kHalf,
                           ((hn & 1) ? g.v : g.k) + (int64_t)ph * C::kHalf, C::kHalf, &full[slot]);
-          } else {
-            tc::mbar_arrive(&full[slot]);
           }
           if (hn & 1) i += to_groups ? 1 : G;
           ++hn;
@@ -250,11 +251,15 @@ decode_kernel(Kv8AttentionArgs g, int deal, float *part, DevStatus *st) {
       }
       if (__any_sync(0xffffffffu, moved)) {
         t0 = tc::global_ns();
-      } else if (tc::global_ns() - t0 > tc::kWaitNs) {
-        set_status(st, GPTQ_ERR_TIMEOUT);
+      } else if (tc::global_ns() - t0 > waits.ns) {
+        tc::give_up(waits);
         break;
       }
     }
+    // the copies have landed before the CTA leaves, also where nobody waits for them any more
+    if (lane < G)
+      for (int h = hn > H ? hn - H : 0; h < hn; ++h)
+        if (h != g.lost) tc::mbar_wait_compact(&full[lane * H + h % H], (h / H) & 1, waits);
     return;
   }
 
@@ -266,14 +271,15 @@ decode_kernel(Kv8AttentionArgs g, int deal, float *part, DevStatus *st) {
   full += grp * H;
   empty += grp * H;
   int hn = 0;        // halves used
-  bool ok = true;    // false once a wait has given up: the rest is skipped
+  // false once a wait has given up: the rest is skipped, and no slot is given back
+  bool ok = true;
   auto arrived = [&]() {
-    if (ok) ok = tc::mbar_wait_compact(&full[hn % H], (hn / H) & 1, st);
+    if (ok) ok = tc::mbar_wait_compact(&full[hn % H], (hn / H) & 1, waits);
     ok = __all_sync(0xffffffffu, ok);
   };
   auto release = [&]() {
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&empty[hn % H]);
+    if (lane == 0 && ok) tc::mbar_arrive(&empty[hn % H]);
     ++hn;
   };
   for (int i = grp, i0 = 0; i0 < count;) {

@@ -228,7 +228,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
   uint64_t *sfull = qfull + 2, *pfull = sfull + 4, *odone = pfull + 4;
   uint64_t *kfull = odone + 4, *kempty = kfull + kKStages;
   uint64_t *vfull = kempty + kKStages, *vempty = vfull + kVStages, *vraw = vempty + kVStages;
-  uint32_t *tmem_slot = (uint32_t *)(vraw + 1);
+  uint64_t *mdone = vraw + 1;   // [2]: every MMA of the issuer's has completed
+  uint32_t *tmem_slot = (uint32_t *)(mdone + 2);
+  const tc::Waits waits{st, g.wait_ns};
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
@@ -242,6 +244,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
       tc::mbar_init(&odone[2 * b + 1], 1);
       tc::mbar_init(&vfull[b], 4);
       tc::mbar_init(&vempty[b], 2);
+      tc::mbar_init(&mdone[b], 1);
     }
     for (int i = 0; i < kKStages; ++i) {
       tc::mbar_init(&kfull[i], 1);
@@ -277,15 +280,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
       const uint64_t dq = desc_rows<D>(tc::smem_u32(sq)), dk = desc_rows<D>(tc::smem_u32(sk));
       const uint64_t dv = tc::smem_desc_sw128(tc::smem_u32(sv), 16, 1024);
       auto wait = [&](uint64_t *bar, int phase) {
-        if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, st);
+        if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, waits);
         ok = __all_sync(0xffffffffu, ok);
         tc::tc_fence_after();
       };
       auto commit = [&](uint64_t *bar) {
-        if (tc::elect_one()) tc::mma_commit(bar);
+        if (ok && tc::elect_one()) tc::mma_commit(bar);
       };
       auto scores = [&](int u, int h) {               // of the unit's block h
-        if (tc::elect_one()) {
+        if (ok && tc::elect_one()) {
           const uint64_t q = dq + b * (C::kQ >> 4);
           const uint64_t k = dk + (u % kKStages * C::kK + h * C::kHalf >> 4);
 #pragma unroll
@@ -296,7 +299,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
         }
       };
       auto outputs = [&](int u, int h, bool first) {  // of the unit's block h
-        if (tc::elect_one()) {
+        if (ok && tc::elect_one()) {
           const uint64_t v = dv + ((u & 1) * C::kV + h * C::kVChunk >> 4);
           const uint32_t p = tmem + b * kTile + h * kTok;
 #pragma unroll
@@ -339,6 +342,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
         i0 += m;
         if (i0 < count) at.next_item(plan);
       }
+      // nothing of these MMAs may still be running when the TMEM is released
+      if (tc::elect_one()) tc::mma_commit(&mdone[b]);
+      tc::mbar_wait_compact(&mdone[b], 0, waits);
     }
   } else if (warp >= 8) {
     // ---------------- copies and converters ----------------
@@ -383,8 +389,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
           make_uint4(halves_lo(q.z), halves_hi(q.z), halves_lo(q.w), halves_hi(q.w));
     };
     auto wait = [&](uint64_t *bar, int phase) {
-      if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, st);
+      if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, waits);
     };
+    int keys = 0, codes = 0;  // units whose keys, value codes have been asked for; none once a wait gave up
     // step u: convert unit u, have unit u + 1 copied, look unit u + 2 up
 #pragma unroll 1
     for (int u = count > 0 ? -2 : 0; u < count; ++u) {
@@ -405,11 +412,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
           f.there[h] = place[h] >= 0;
           bytes += place[h] >= 0 ? C::kHalf : 0;
         }
-        tc::mbar_arrive_expect_tx(&kfull[s], bytes);
+        if (ok && n != g.lost) {
+          tc::mbar_arrive_expect_tx(&kfull[s], bytes);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (place[h] >= 0)
-            tc::tma_load_3d(sk + s * C::kK + h * C::kHalf, &mk, 0, 0, place[h], &kfull[s]);
+          for (int h = 0; h < 2; ++h)
+            if (place[h] >= 0)
+              tc::tma_load_3d(sk + s * C::kK + h * C::kHalf, &mk, 0, 0, place[h], &kfull[s]);
+        }
+        keys += ok;
       }
       if (u >= 0) {
         // values; those past the sequence's end may be NaN codes and become zeros
@@ -442,7 +452,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
         if (lane == 0) tc::mbar_arrive(&vfull[s]);
         tc::named_barrier(1, 128);  // the codes have been read
       }
-      if (next && ct == 0) {
+      if (next && ct == 0 && ok) {
+        codes = u + 2;
         tc::fence_proxy_async_smem();
         tc::mbar_arrive_expect_tx(vraw, bytes);
 #pragma unroll
@@ -451,6 +462,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
             tc::bulk_load(raw_v + h * C::kHalf, g.v + (int64_t)place[h] * C::kHalf, C::kHalf, vraw);
       }
       look_up(u + 2);
+    }
+    if (ct == 0) {
+      // the copies have landed before the CTA leaves, also where nobody waits for them any more
+      for (int n = keys > kKStages ? keys - kKStages : 0; n < keys; ++n)
+        if (n != g.lost) tc::mbar_wait_compact(&kfull[n % kKStages], (n / kKStages) & 1, waits);
+      if (codes > 0) tc::mbar_wait_compact(vraw, (codes - 1) & 1, waits);
     }
   } else {
     // ---------------- softmax ----------------
@@ -461,7 +478,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
     uint8_t *q_tile = sq + b * C::kQ;
     int seen = 0;  // units before this item: phases of sfull and odone
     auto wait = [&](uint64_t *bar, int phase) {
-      if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, st);
+      if (ok) ok = tc::mbar_wait_compact(bar, phase & 1, waits);
       ok = __all_sync(0xffffffffu, ok);
       tc::tc_fence_after();
     };

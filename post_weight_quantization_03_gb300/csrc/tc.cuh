@@ -14,8 +14,6 @@
 namespace gptq {
 namespace tc {
 
-constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far beyond any legitimate wait here
-
 // The GPU's global nanosecond timer.
 __device__ __forceinline__ uint64_t global_ns() {
   uint64_t t;
@@ -90,17 +88,26 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, DevSta
   return false;
 }
 
+// What a kernel's waits have in common: their budget, and where one that gave up is recorded.
+struct Waits {
+  DevStatus *st;
+  uint64_t ns;
+};
+__device__ __forceinline__ void give_up(const Waits &w) {
+  set_status(w.st, GPTQ_ERR_TIMEOUT);
+}
+
 // mbar_wait in fewer instructions, for kernels with many waits in many roles, whose code would
 // otherwise outgrow the instruction cache.
-__device__ __forceinline__ bool mbar_wait_compact(uint64_t *bar, uint32_t parity, DevStatus *st) {
+__device__ __forceinline__ bool mbar_wait_compact(uint64_t *bar, uint32_t parity, const Waits &w) {
   uint64_t t0 = 0;
 #pragma unroll 1
   for (uint32_t n = 0; !mbar_try_wait(bar, parity); ++n) {
     if ((n & 31) != 31) continue;  // the timer is read now and then
     const uint64_t t = global_ns();
     if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitNs) {
-      if (st) atomicCAS(&st->status, 0, (int)GPTQ_ERR_TIMEOUT);
+    if (t - t0 > w.ns) {
+      give_up(w);
       return false;
     }
   }

@@ -97,6 +97,16 @@ _SIGS = {
                                       _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_int, _c.c_float,
                                       _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_size_t,
                                       _c.c_void_p]),
+    "gptq_debug_fp8_matmul_lost_copy": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
+                                                   _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
+                                                   _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p,
+                                                   _c.c_int, _c.c_int64, _c.c_int64, _c.c_uint64,
+                                                   _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "gptq_debug_kv8_attention_lost_copy": (_c.c_int, [
+        _c.c_void_p, _c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int, _c.c_int, _c.c_int,
+        _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
+        _c.c_int64, _c.c_void_p, _c.c_int, _c.c_float, _c.c_void_p, _c.c_void_p, _c.c_int64,
+        _c.c_uint64, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
 }
 NOALLOC_SCRATCH_BYTES = 32 << 20  # GPTQ_NOALLOC_SCRATCH_BYTES in include/gptq.h
 OBQ_MAX_D_IN = 128                # GPTQ_OBQ_MAX_D_IN in include/gptq.h
@@ -288,6 +298,24 @@ def gptq_kv8_attention(q, q_strides, dtype, n_seq, n_new, n_heads, n_kv, dim, k,
                                      k_exps, v_exps, n_blocks, table, ld_table, max_blocks,
                                      lengths, causal, scale, out, o_strides, ws, ws_bytes,
                                      stream)
+
+
+def gptq_debug_fp8_matmul_lost_copy(a, lda, a_exps, ldae, w, ldw, w_exps, ldwe, m, n, k, out, odtype,
+                                    ldo, lost_copy, wait_ns, ws, ws_bytes, stream):
+    return load().gptq_debug_fp8_matmul_lost_copy(a, lda, a_exps, ldae, w, ldw, w_exps, ldwe, m, n, k,
+                                                  out, odtype, ldo, lost_copy, wait_ns, ws, ws_bytes,
+                                                  stream)
+
+
+def gptq_debug_kv8_attention_lost_copy(q, q_strides, dtype, n_seq, n_new, n_heads, n_kv, dim, k, v,
+                                       k_exps, v_exps, n_blocks, table, ld_table, max_blocks, lengths,
+                                       causal, scale, out, o_strides, lost_copy, wait_ns, ws,
+                                       ws_bytes, stream):
+    return load().gptq_debug_kv8_attention_lost_copy(q, q_strides, dtype, n_seq, n_new, n_heads, n_kv,
+                                                     dim, k, v, k_exps, v_exps, n_blocks, table,
+                                                     ld_table, max_blocks, lengths, causal, scale,
+                                                     out, o_strides, lost_copy, wait_ns, ws,
+                                                     ws_bytes, stream)
 
 
 # ---------------------------------------------------------------------------------------
