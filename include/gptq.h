@@ -580,6 +580,16 @@ gptq_status gptq_kv8_attention(const void *q, const int64_t *q_strides, int dtyp
                                size_t ws_bytes, gptq_stream_t stream);
 
 /*
+ * gptq_serving_status: synchronize `stream`, then return GPTQ_ERR_TIMEOUT if a bounded device wait
+ * of a gptq_fp8_matmul or gptq_kv8_attention on the current device, on whichever stream and
+ * workspace, has given up since the last such query (the outputs of that call are undefined), else
+ * GPTQ_OK.  It is recorded beside the workspaces' status, which the next call on a workspace resets:
+ * a program that runs many calls asks once, after them.  (In a stream that is captured: CUDA.)
+ * Errors of its own: CUDA.
+ */
+gptq_status gptq_serving_status(gptq_stream_t stream);
+
+/*
  * gptq_debug_fp8_matmul_lost_copy, gptq_debug_kv8_attention_lost_copy: test hooks of the bounded
  * device waits, as gptq_debug_hessian_lost_stage.
  *

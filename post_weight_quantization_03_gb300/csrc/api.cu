@@ -401,6 +401,13 @@ gptq_status gptq_debug_fp8_matmul_lost_copy(const uint8_t *a, int64_t lda, const
   return gptq_workspace_status(ws, stream);
 }
 
+gptq_status gptq_serving_status(gptq_stream_t stream) {
+  int product = 0, attention = 0;
+  GPTQ_TRY(fp8_matmul_take_timeout(&product, (cudaStream_t)stream));
+  GPTQ_TRY(kv8_attention_take_timeout(&attention, (cudaStream_t)stream));
+  return (gptq_status)(product != 0 ? product : attention);
+}
+
 // What the two cache calls share; `ok` = valid, UNSUPPORTED for sizes outside the limits.
 static gptq_status kv8_cache_check(int64_t n_seq, int64_t n_new, int n_kv, int dim,
                                    const uint8_t *k, const uint8_t *v, const uint8_t *k_exps,

@@ -108,6 +108,17 @@ namespace tc {
 constexpr uint64_t kWaitNs = 2000000000ull;  // a device wait's budget, 2 s: far beyond any legitimate one
 }
 
+// Reads and clears a flag that a kernel's waits set (a __device__ int of the caller's file).
+template <typename Symbol>
+gptq_status take_flag(Symbol &flag, int *out, cudaStream_t s) {
+  const int none = 0;
+  GPTQ_CUDA_CHECK(cudaMemcpyFromSymbolAsync(out, flag, sizeof(int), 0, cudaMemcpyDeviceToHost, s));
+  GPTQ_CUDA_CHECK(cudaStreamSynchronize(s));
+  if (*out != 0)
+    GPTQ_CUDA_CHECK(cudaMemcpyToSymbolAsync(flag, &none, sizeof(int), 0, cudaMemcpyHostToDevice, s));
+  return GPTQ_OK;
+}
+
 // Device-side status block at the start of every workspace.
 struct DevStatus {
   int status;        // gptq_status recorded by kernels (0 = OK); first writer wins
@@ -255,6 +266,7 @@ struct Fp8MatmulArgs {
 };
 size_t fp8_matmul_ws_bytes(int64_t M, int64_t N, int64_t K);
 gptq_status launch_fp8_matmul(const Fp8MatmulArgs &g, void *ws, cudaStream_t s);
+gptq_status fp8_matmul_take_timeout(int *out, cudaStream_t s);  // since it was last asked for
 
 // kv8_append.cu, kv8_attention.cu: the 8-bit cache (gptq_kv8_append, gptq_kv8_attention)
 struct Kv8AppendArgs {
@@ -283,5 +295,6 @@ struct Kv8AttentionArgs {
 size_t kv8_attention_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int dim,
                               int max_blocks);
 gptq_status launch_kv8_attention(const Kv8AttentionArgs &g, void *ws, cudaStream_t s);
+gptq_status kv8_attention_take_timeout(int *out, cudaStream_t s);
 
 }  // namespace gptq

@@ -70,6 +70,8 @@ struct MmParams {
   int lost;             // test hook: this copy of the producer's is left out
 };
 
+__device__ int g_gave_up;  // a wait ran out since it was last asked for
+
 template <typename TO>
 __device__ __forceinline__ TO out_f32(float x) {
   if constexpr (std::is_same<TO, __half>::value) return __float2half_rn(x);
@@ -133,7 +135,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
   uint64_t *tempty = tfull + 2;
   uint64_t *mdone = tempty + 2;       // every MMA has completed
   uint32_t *tmem_slot = (uint32_t *)(mdone + 1);
-  const tc::Waits waits{st, p.wait_ns};
+  const tc::Waits waits{st, &g_gave_up, p.wait_ns};
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t stage_bytes = (uint32_t)(BM + p.tn) * BK;
@@ -484,6 +486,8 @@ gptq_status run(const Fp8MatmulArgs &g, DevStatus *st, cudaStream_t s) {
 }  // namespace
 
 size_t fp8_matmul_ws_bytes(int64_t, int64_t, int64_t) { return 256; }
+
+gptq_status fp8_matmul_take_timeout(int *out, cudaStream_t s) { return take_flag(g_gave_up, out, s); }
 
 gptq_status launch_fp8_matmul(const Fp8MatmulArgs &g, void *ws, cudaStream_t s) {
   if (g.M == 0) {

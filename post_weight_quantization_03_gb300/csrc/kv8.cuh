@@ -382,5 +382,6 @@ static inline bool kv8_plan_fits(const Kv8AttentionArgs &g, int64_t tile, int64_
 size_t kv8_prompt_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int dim,
                            int max_blocks);
 gptq_status launch_kv8_prompt(const Kv8AttentionArgs &g, void *ws, cudaStream_t s);
+gptq_status kv8_prompt_take_timeout(int *out, cudaStream_t s);
 
 }  // namespace gptq

@@ -70,6 +70,8 @@ constexpr float kFew = 0x1p-7f, kNone = 0x1p-32f, kRest = 0x1p23f;
 constexpr float kHide = 64 * 0x1p-15f * 448 * 0x1p9f;
 static_assert(kRows == 8 * 4, "row tiles: 1, 2 or 4");
 
+__device__ int g_gave_up;  // a wait ran out since it was last asked for
+
 template <int D>
 struct Decode {
   static constexpr uint32_t kHalf = kTok * D;                 // bytes of K (or V) of a block
@@ -166,7 +168,7 @@ decode_kernel(Kv8AttentionArgs g, int deal, float *part, DevStatus *st) {
   int2 *list = (int2 *)(spart + kWarps * C::kWarpPart);  // block and head (-1: none); exponents
   uint64_t *full = (uint64_t *)(list + kList), *empty = full + kWarps * C::kSlots;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const tc::Waits waits{st, g.wait_ns};
+  const tc::Waits waits{st, &g_gave_up, g.wait_ns};
   if (threadIdx.x == 0) {
     for (int s = 0; s < G * H; ++s) {
       tc::mbar_init(&full[s], 1);
@@ -585,6 +587,14 @@ size_t kv8_attention_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, i
   if (!takes_tiles(rows, true, dim, max_blocks)) return here;  // (with fp16 wherever with bf16)
   const size_t there = kv8_prompt_ws_bytes(n_seq, n_new, n_heads, n_kv, dim, max_blocks);
   return there > here ? there : here;
+}
+
+gptq_status kv8_attention_take_timeout(int *out, cudaStream_t s) {
+  int prompt = 0;
+  GPTQ_TRY(take_flag(g_gave_up, out, s));
+  GPTQ_TRY(kv8_prompt_take_timeout(&prompt, s));
+  if (prompt != 0) *out = prompt;
+  return GPTQ_OK;
 }
 
 gptq_status launch_kv8_attention(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {

@@ -60,6 +60,8 @@ constexpr float kMostSum = 0x1p15f;
 
 constexpr int kKStages = 3, kVStages = 2;
 
+__device__ int g_gave_up;  // a wait ran out since it was last asked for
+
 template <int D, int NT>
 struct Prompt {
   static constexpr uint32_t kTerm = kTile * D;                // a term of a tile of queries
@@ -230,7 +232,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
   uint64_t *vfull = kempty + kKStages, *vempty = vfull + kVStages, *vraw = vempty + kVStages;
   uint64_t *mdone = vraw + 1;   // [2]: every MMA of the issuer's has completed
   uint32_t *tmem_slot = (uint32_t *)(mdone + 2);
-  const tc::Waits waits{st, g.wait_ns};
+  const tc::Waits waits{st, &g_gave_up, g.wait_ns};
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
@@ -749,6 +751,8 @@ size_t kv8_prompt_ws_bytes(int n_seq, int64_t n_new, int n_heads, int n_kv, int 
   if (weight < ctas) ctas = weight;
   return 256 + (size_t)(2 * ctas) * (2 * kTile) * (dim + 2) * 4;
 }
+
+gptq_status kv8_prompt_take_timeout(int *out, cudaStream_t s) { return take_flag(g_gave_up, out, s); }
 
 gptq_status launch_kv8_prompt(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   if (!kv8_plan_fits(g, 2 * kTile, 2, PromptPlan::kSetup)) return GPTQ_ERR_UNSUPPORTED;

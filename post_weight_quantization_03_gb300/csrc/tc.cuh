@@ -88,13 +88,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, DevSta
   return false;
 }
 
-// What a kernel's waits have in common: their budget, and where one that gave up is recorded.
+// What a kernel's waits have in common: their budget, and where one that gave up is recorded: in
+// the call's status block, which its next user resets, and in a flag that stays until it is asked
+// for.
 struct Waits {
   DevStatus *st;
+  int *gave_up;
   uint64_t ns;
 };
 __device__ __forceinline__ void give_up(const Waits &w) {
   set_status(w.st, GPTQ_ERR_TIMEOUT);
+  atomicExch(w.gave_up, (int)GPTQ_ERR_TIMEOUT);
 }
 
 // mbar_wait in fewer instructions, for kernels with many waits in many roles, whose code would

@@ -179,6 +179,7 @@ def main(argv=None):
         outs.append(layer.step(x[:, at:at + new], cache, table, start, start + new))
         at += new
     out = torch.cat(outs, 1).float()
+    gptq.serving_status()
     for name, w in (("quantized", layer.dequantized()), ("original", weights)):
         want = reference(w, n1, n2, x, a.heads, a.kv_heads)
         print(f"against fp32 on the {name} weights: relative error "

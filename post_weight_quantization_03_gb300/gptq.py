@@ -97,6 +97,7 @@ _SIGS = {
                                       _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_int, _c.c_float,
                                       _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_size_t,
                                       _c.c_void_p]),
+    "gptq_serving_status": (_c.c_int, [_c.c_void_p]),
     "gptq_debug_fp8_matmul_lost_copy": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
                                                    _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
                                                    _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p,
@@ -298,6 +299,10 @@ def gptq_kv8_attention(q, q_strides, dtype, n_seq, n_new, n_heads, n_kv, dim, k,
                                      k_exps, v_exps, n_blocks, table, ld_table, max_blocks,
                                      lengths, causal, scale, out, o_strides, ws, ws_bytes,
                                      stream)
+
+
+def gptq_serving_status(stream):
+    return load().gptq_serving_status(stream)
 
 
 def gptq_debug_fp8_matmul_lost_copy(a, lda, a_exps, ldae, w, ldw, w_exps, ldwe, m, n, k, out, odtype,
@@ -716,9 +721,16 @@ def fp8_from_codes(qpacked, zero, d_in, bits=4, stream=None):
     return codes, exps
 
 
+def serving_status(stream=None):
+    """Waits for ``stream`` and raises if a device wait of ``fp8_matmul`` or ``kv8_attention`` gave up
+    since the last such query, whatever the stream and workspace of the call: its output is then
+    undefined."""
+    _check(gptq_serving_status(_stream(stream)), "gptq_serving_status")
+
+
 # The workspace of a product, and of an attention that cuts no item, is its status block alone.
-# Calls without one share a block by device, which is not read back: making a tensor takes 3 to 5
-# us of a call's host time.
+# Calls without one share a block by device, which is not read back (``serving_status`` tells of a
+# wait that gave up): making a tensor takes 3 to 5 us of a call's host time.
 _STATUS_BLOCKS = {}
 
 
@@ -734,7 +746,8 @@ def fp8_matmul(a, a_exps, w, w_exps, a_scale=None, w_scale=None, out_dtype=None,
                ws=None, stream=None):
     """``diag(a_scale) A W^T diag(w_scale)`` of e4m3 matrices ``A [m, k]`` (1 x 128 blocks) and
     ``W [n, k]`` (128 x 128 blocks), ``[m, n]`` in float16 or bfloat16 (the default).  ``ws``
-    (``gptq_fp8_matmul_workspace_bytes``) keeps the call's status for ``gptq_workspace_status``."""
+    (``gptq_fp8_matmul_workspace_bytes``) keeps the call's status for ``gptq_workspace_status``;
+    without one ``serving_status`` tells of it."""
     torch = _torch()
     m, k = a.shape
     n = w.shape[0]
@@ -835,7 +848,7 @@ def kv8_attention(q, cache, table, lengths, scale=None, causal=True, out=None, w
                   stream=None):
     """Attention of the last ``new`` tokens' queries ``[seqs, new, heads, dim]`` over the cached
     tokens of each sequence (``lengths`` of them, the new ones included); ``scale`` defaults to
-    ``dim ** -0.5``.  Rows that see no token give zeros."""
+    ``dim ** -0.5``.  Rows that see no token give zeros.  ``ws`` as for ``fp8_matmul``."""
     torch = _torch()
     shape, qs = q.shape, q.stride()
     if len(shape) != 4 or qs[3] != 1:

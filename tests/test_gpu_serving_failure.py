@@ -96,3 +96,19 @@ def test_hooks_reject_bad_requests():
     assert lost(-1) == 1
     call, lost, _, _ = _attention(1, 1, 1, 4, 64, 100, "bf16")
     assert lost(-1) == 1
+
+
+def test_timeouts_of_calls_whose_status_is_gone():
+    # the helpers' calls share a status block or drop their workspace: a wait that gave up is told all the same, once
+    gptq.gptq_serving_status(gptq._stream(None))            # (of the tests before)
+    regular, lost, _, _ = _product(8, 512, 8192)
+    attend, lost_attend, _, _ = _attention(2, 100, 2, 4, 128, 3000, "bf16")
+    other = torch.cuda.Stream()
+    for hook in (lost, lost_attend, _attention(4, 1, 2, 4, 128, 6000, "bf16")[1]):
+        assert hook(0) == TIMEOUT
+        regular(), attend()                                 # later calls reset what they use
+        with pytest.raises(gptq.GptqError) as e:
+            gptq.serving_status(other)
+        assert e.value.status == TIMEOUT
+        regular(), attend()
+        gptq.serving_status()
