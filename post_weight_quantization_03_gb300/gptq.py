@@ -618,6 +618,11 @@ def _stream_of(device, stream):
         index if index is not None else torch.cuda.current_device())
 
 
+# The kernels take addresses: every tensor of a call has to be on one GPU (asked for in place, a
+# function over the tensors takes twice as long).
+_ONE_GPU = "a call's tensors must be on one GPU"
+
+
 _SERVING_DTYPES = {}
 
 
@@ -675,6 +680,9 @@ def rmsnorm_fp8(X, weight, residual=None, eps=1e-6, want_h=True, stream=None):
             raise TypeError("residual must have X's dtype")
     if weight.shape != (d,) or (d > 1 and weight.stride(0) != 1):
         raise ValueError("weight must be a contiguous [d] vector")
+    gpu = X.get_device()
+    if gpu < 0 or weight.get_device() != gpu or (residual is not None and residual.get_device() != gpu):
+        raise ValueError(_ONE_GPU)
     codes, ldc, exps, lde = _fp8_empty(n, d, 1, device, stream)
     rstd = torch.empty((n,), dtype=torch.float32, device=device)
     h, h_ptr = X, None
@@ -698,6 +706,10 @@ def fp8_quantize(X, row_block=1, stream=None):
     activations, 128 for weights."""
     ldx = _rows_of("X", X)
     n, d = X.shape
+    if row_block not in (1, FP8_BLOCK):
+        raise ValueError(f"row_block must be 1 or {FP8_BLOCK}")
+    if X.get_device() < 0:
+        raise ValueError(_ONE_GPU)
     codes, ldc, exps, lde = _fp8_empty(n, d, row_block, X.device, stream)
     _check(load().gptq_fp8_quantize(X.data_ptr(), _serving_dtype(X.dtype), n, d, ldx, row_block,
                                     codes.data_ptr(), ldc, exps.data_ptr(), lde,
@@ -714,6 +726,10 @@ def fp8_from_codes(qpacked, zero, d_in, bits=4, stream=None):
             or zero.shape != (m,) or not zero.is_contiguous():
         raise ValueError("qpacked [d_out, ceil(d_in / 32) * bits] and zero [d_out] as quantize "
                          "returns them")
+    if qpacked.dtype != zero.dtype or zero.dtype != _torch().int32:
+        raise TypeError("qpacked and zero must be int32, as quantize returns them")
+    if qpacked.get_device() < 0 or zero.get_device() != qpacked.get_device():
+        raise ValueError(_ONE_GPU)
     codes, ldc, exps, lde = _fp8_empty(m, d_in, FP8_BLOCK, qpacked.device, stream)
     _check(load().gptq_fp8_from_codes(qpacked.data_ptr(), bits, zero.data_ptr(), m, d_in,
                                       codes.data_ptr(), ldc, exps.data_ptr(), lde,
@@ -762,6 +778,11 @@ def fp8_matmul(a, a_exps, w, w_exps, a_scale=None, w_scale=None, out_dtype=None,
         if t is not None and (t.dtype != torch.float32 or t.shape != (rows,)
                               or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous float32 [{rows}] vector")
+    gpu = a.get_device()
+    if gpu < 0 or w.get_device() != gpu or a_exps.get_device() != gpu or w_exps.get_device() != gpu \
+            or (a_scale is not None and a_scale.get_device() != gpu) \
+            or (w_scale is not None and w_scale.get_device() != gpu):
+        raise ValueError(_ONE_GPU)
     device = a.device
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=device)
@@ -772,9 +793,13 @@ def fp8_matmul(a, a_exps, w, w_exps, a_scale=None, w_scale=None, out_dtype=None,
         ldo = _rows_of("out", out, m, n)
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError("out must have out_dtype")
+        if out.get_device() != gpu:
+            raise ValueError(_ONE_GPU)
     lib = load()
     if ws is None:
         ws = _status_block(device)
+    elif ws.get_device() != gpu:
+        raise ValueError(_ONE_GPU)
     _check(lib.gptq_fp8_matmul(
         a.data_ptr(), lda, a_exps.data_ptr(), ldae,
         a_scale.data_ptr() if a_scale is not None else None, w.data_ptr(), ldw, w_exps.data_ptr(),
@@ -799,7 +824,7 @@ def kv8_cache(n_blocks, n_kv_heads, dim, device=None):
 
 
 def _kv8_args(cache, table, seqs, lengths, what):
-    """``(n_blocks, n_kv_heads, dim, table pitch, blocks of the table)`` of matching arguments."""
+    """``(n_blocks, n_kv_heads, dim, table pitch, blocks of the table, GPU)`` of matching arguments."""
     torch = _torch()
     k, v, ke, ve = cache
     shape = k.shape
@@ -819,7 +844,11 @@ def _kv8_args(cache, table, seqs, lengths, what):
     pitch = _rows_of("table", table, seqs)
     if lengths.shape != (seqs,) or not lengths.is_contiguous():
         raise ValueError(f"{what} must be a contiguous [{seqs}] vector")
-    return nb, kv, d, pitch, table.shape[1]
+    gpu = k.get_device()
+    if v.get_device() != gpu or ke.get_device() != gpu or ve.get_device() != gpu \
+            or table.get_device() != gpu or lengths.get_device() != gpu:
+        gpu = -1
+    return nb, kv, d, pitch, table.shape[1], gpu
 
 
 _Strides3 = ctypes.c_int64 * 3
@@ -830,12 +859,14 @@ def kv8_append(cache, k, v, table, start, stream=None):
     sequence's tokens ``[start, start + new)``; ``table [seqs, blocks]`` (int32) names the cache
     blocks of each sequence, -1 for none."""
     shape, ks, vs = k.shape, k.stride(), v.stride()
-    nb, kv, d, pitch, mb = _kv8_args(cache, table, shape[0], start, "start")
+    nb, kv, d, pitch, mb, gpu = _kv8_args(cache, table, shape[0], start, "start")
     if len(shape) != 4 or shape[2] != kv or shape[3] != d or v.shape != shape \
             or k.dtype != v.dtype:
         raise ValueError(f"k and v must be [seqs, new, {kv}, {d}] of one dtype")
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("a head's elements must be contiguous")
+    if gpu < 0 or k.get_device() != gpu or v.get_device() != gpu:
+        raise ValueError(_ONE_GPU)
     kc, vc, ke, ve = cache
     _check(load().gptq_kv8_append(
         k.data_ptr(), _Strides3(ks[0], ks[1], ks[2]), v.data_ptr(),
@@ -854,7 +885,7 @@ def kv8_attention(q, cache, table, lengths, scale=None, causal=True, out=None, w
     if len(shape) != 4 or qs[3] != 1:
         raise ValueError("q must be [seqs, new, heads, dim] with a head's elements contiguous")
     n_seq, new, heads, dim = shape
-    nb, kv, d, pitch, mb = _kv8_args(cache, table, n_seq, lengths, "lengths")
+    nb, kv, d, pitch, mb, gpu = _kv8_args(cache, table, n_seq, lengths, "lengths")
     if dim != d:
         raise ValueError(f"q's heads must be {d} wide, as the cache's")
     device, dtype = q.device, q.dtype
@@ -867,6 +898,10 @@ def kv8_attention(q, cache, table, lengths, scale=None, causal=True, out=None, w
         os_ = out.stride()
         if out.shape != shape or out.dtype != dtype or os_[3] != 1:
             raise ValueError("out must match q")
+    if gpu < 0 or q.get_device() != gpu or out.get_device() != gpu \
+            or (ws is not None and ws.get_device() != gpu):
+        raise ValueError(_ONE_GPU)
+    kc, vc, ke, ve = cache
     lib = load()
     if ws is None:
         need = lib.gptq_kv8_attention_workspace_bytes(n_seq, new, heads, kv, d, mb)
@@ -876,7 +911,6 @@ def kv8_attention(q, cache, table, lengths, scale=None, causal=True, out=None, w
             ws = torch.empty((need,), dtype=torch.uint8, device=device)
             if stream is not None:
                 _lend(stream, ws)
-    kc, vc, ke, ve = cache
     _check(lib.gptq_kv8_attention(
         q.data_ptr(), _Strides3(qs[0], qs[1], qs[2]), _serving_dtype(dtype), n_seq, new, heads,
         kv, d, kc.data_ptr(), vc.data_ptr(), ke.data_ptr(), ve.data_ptr(), nb, table.data_ptr(),
