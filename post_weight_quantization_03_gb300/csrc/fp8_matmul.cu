@@ -28,11 +28,10 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
-#include <atomic>
-
 #include <type_traits>
 
 #include "fp8.cuh"
+#include "per_device.cuh"
 #include "tc.cuh"
 
 namespace gptq {
@@ -390,30 +389,28 @@ struct Shape { int tn, splits, per_sm; };
 // there is room for fewer than SMs / splits: 152 SMs take 46 clusters of three (52 x 6144 x 2896
 // has 48 tiles of 64 tokens: split in three it took 13.7 us, in two rounds; now 8.8).
 template <typename TO>
-int clusters_at_once(int splits, int sms) {
-  static std::atomic<int> known[9];
-  int n = known[splits].load(std::memory_order_relaxed);
-  if (n > 0) return n;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)splits;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(splits * sms));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kRingBytes + kSmemBesides;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, (const void *)matmul_kernel<TO>, &cfg) != cudaSuccess || n < 1) {
+int clusters_at_once(int dev, int splits, int sms) {
+  static PerDevice<9> known;
+  return known.get(dev, splits, [splits, sms]() {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(splits * sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kRingBytes + kSmemBesides;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, (const void *)matmul_kernel<TO>, &cfg) == cudaSuccess) return n;
     (void)cudaGetLastError();
-    n = sms / splits * 7 / 8;
-  }
-  known[splits].store(n, std::memory_order_relaxed);
-  return n;
+    return 0;
+  }, sms / splits * 7 / 8);
 }
 
 template <typename TO>
-Shape choose(int64_t M, int64_t N, int64_t K, int sms) {
+Shape choose(int64_t M, int64_t N, int64_t K, int dev, int sms) {
   const int64_t n_w = ceil_div(N, BM), groups = ceil_div(ceil_div(K, BK), 4);
   const double once = (double)(M + N) * K / 3500.0;
   Shape best{16, 1, 1};
@@ -429,7 +426,7 @@ Shape choose(int64_t M, int64_t N, int64_t K, int sms) {
         const int64_t ctas = tiles * s;
         if (per == 2 && ((uint32_t)(BM + tn) * BK * 3 > kRingBytesTwo || ctas <= sms || ctas > 2 * sms))
           continue;
-        if (s > 1 && tiles > (int64_t)per * clusters_at_once<TO>(s, sms)) continue;
+        if (s > 1 && tiles > (int64_t)per * clusters_at_once<TO>(dev, s, sms)) continue;
         const int64_t busy = ceil_div(ctas, sms);
         const double work = (double)busy * 4 * ceil_div(groups, s) * c * (per == 2 ? 0.95 : 1.0);
         double t = sqrt(work * work + (once + fill) * (once + fill));
@@ -448,7 +445,9 @@ gptq_status run(const Fp8MatmulArgs &g, DevStatus *st, cudaStream_t s) {
   int sms = 0;
   GPTQ_TRY(device_sm_count(&sms));
   const int kb = (int)ceil_div(g.K, BK);
-  const Shape sh = choose<TO>(g.M, g.N, g.K, sms);
+  int dev = -1;
+  GPTQ_CUDA_CHECK(cudaGetDevice(&dev));
+  const Shape sh = choose<TO>(g.M, g.N, g.K, dev, sms);
   MmParams p{};
   p.ae = g.ae; p.ldae = g.ldae;
   p.we = g.we; p.ldwe = g.ldwe;
