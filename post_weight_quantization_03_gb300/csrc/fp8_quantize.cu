@@ -76,6 +76,39 @@ struct RowsParams {
   int vx, vr, vw, vh;              // alignment of each pointer's rows
 };
 
+// Whole CTA: (mean square + eps)^-1/2 of its row, `sq` being a thread's sum of squares.  A row whose
+// sum passes fp32's range is read again by one warp (as H, where H has replaced X or R) and its
+// squares summed as multiples of 2^192; an infinity gives 0 still, a NaN has not come here.
+template <typename T>
+__device__ __forceinline__ void store_rstd(const RowsParams &p, int64_t row, float sq) {
+  __shared__ float part[kMaxRowThreads / 32];
+  const int lane = threadIdx.x % 32;
+  auto reduce = [](float a) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
+  };
+  sq = reduce(sq);
+  if (lane == 0) part[threadIdx.x / 32] = sq;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  sq = reduce(threadIdx.x < blockDim.x / 32 ? part[threadIdx.x] : 0.0f);
+  float rstd = 1.0f / sqrtf(sq / (float)p.d + p.eps);
+  if (sq == INFINITY) {
+    const bool in_place = p.h && (p.h == p.x || p.h == p.r);
+    const T *x = in_place ? (const T *)p.h + row * p.ldh : (const T *)p.x + row * p.ldx;
+    const T *r = in_place || !p.r ? nullptr : (const T *)p.r + row * p.ldr;
+    float big = 0.0f;
+#pragma unroll 1
+    for (int64_t c = lane; c < p.d; c += 32) {
+      const float v = (r ? to_f32(x[c]) + to_f32(r[c]) : to_f32(x[c])) * 0x1p-96f;
+      big = fmaf(v, v, big);
+    }
+    rstd = 0x1p-96f / sqrtf(reduce(big) / (float)p.d);
+  }
+  if (threadIdx.x == 0) p.rstd[row] = rstd;
+}
+
 // One CTA per row; half-warps take 128-element blocks, a thread VPT pieces of eight.  All of a
 // thread's loads are asked for before its stores, which the compiler may not move them past.
 // CTAS an SM at least (of 512 threads): two, or three where rows queue for long.  Three leave 40
@@ -86,7 +119,6 @@ struct RowsParams {
 template <typename T, typename TW, int VPT, int CTAS>
 __global__ void __launch_bounds__(kMaxRowThreads, CTAS)
 rows_kernel(RowsParams p) {
-  __shared__ float part[kMaxRowThreads / 32];
   wait_for_grids();
   launch_dependents();
   const int lane = threadIdx.x % 32;
@@ -125,23 +157,12 @@ rows_kernel(RowsParams p) {
       if ((lane & 15) == 0) p.exps[row * p.lde + c / fp8::kBlock] = (uint8_t)(e + fp8::kBias);
     }
   }
-  if (!p.rstd) return;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-  if (lane == 0) part[threadIdx.x / 32] = sq;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    float s = threadIdx.x < blockDim.x / 32 ? part[threadIdx.x] : 0.0f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (threadIdx.x == 0) p.rstd[row] = 1.0f / sqrtf(s / (float)p.d + p.eps);
-  }
+  if (p.rstd) store_rstd<T>(p, row, sq);
 }
 
 // Rows too wide for a thread's registers: one CTA per row, its pieces in a loop.
 template <typename T, typename TW>
 __global__ void __launch_bounds__(kMaxRowThreads) wide_rows_kernel(RowsParams p) {
-  __shared__ float part[kMaxRowThreads / 32];
   wait_for_grids();
   launch_dependents();
   const int64_t row = blockIdx.x;
@@ -177,16 +198,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) wide_rows_kernel(RowsParams p)
       if ((lane & 15) == 0) p.exps[row * p.lde + c / fp8::kBlock] = (uint8_t)(e + fp8::kBias);
     }
   }
-  if (!p.rstd) return;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-  if (lane == 0) part[threadIdx.x / 32] = sq;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float s = 0.0f;
-    for (int i = 0; i < (int)blockDim.x / 32; ++i) s += part[i];
-    p.rstd[row] = 1.0f / sqrtf(s / (float)p.d + p.eps);
-  }
+  if (p.rstd) store_rstd<T>(p, row, sq);
 }
 
 // Weights: one CTA per 128 x 128 block, its values held in registers between the maximum and

@@ -133,3 +133,42 @@ def test_attention_behind_tokens_without_values(new, group, d, tokens, level, dt
     q = torch.from_numpy(ones + 0.02 * rng.standard_normal((1, new, group, d))).to(DT[dtype])
     out = gptq.kv8_attention(q.to(DEV), _dev_cache(cache), _i32(table), _i32([tokens]))
     _check_attention(out, q, cache, table, [tokens])
+
+
+# ---------------------------------------------------------------------------------------
+# Norm: squares past fp32's range
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,d", [(3, 40), (5, 4096), (2, 20000)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("top", [2.0 ** 50, 2.0 ** 58, 2.0 ** 63, 2.0 ** 64, 2.0 ** 100, 2.0 ** 125])
+def test_norm_of_large_rows(rows, d, dtype, top):
+    # rows of such elements, rows with one among ordinary ones, and ordinary rows beside them
+    x = _randn(31, rows, d)
+    x[0] = x[0] / x[0].abs().max() * top
+    x[1, d // 3] = top
+    x = x.to(DT[dtype])
+    w = _randn(32, d, dtype=dtype) * 0.1
+    c, e, rstd, h = gptq.rmsnorm_fp8(x.to(DEV), w.to(DEV), eps=1e-6)
+    oc, oe, orstd, _ = SO.rmsnorm(_np(x), _np(w), None, 1e-6)
+    np.testing.assert_allclose(_np(rstd), orstd, rtol=4e-6)
+    np.testing.assert_array_equal(_np(c), oc)
+    np.testing.assert_array_equal(_np(e), oe)
+    y = rstd.double().cpu().numpy()[:, None] * SO.dequantize(_np(c), _np(e))
+    want = _np(x).astype(np.float64) * orstd[:, None] * _np(w).astype(np.float64)
+    assert np.all(np.abs(y - want) <= np.abs(want) / 15 + np.abs(want).max(1, keepdims=True) * 2.0 ** -17)
+
+
+@pytest.mark.parametrize("where", ["x", "r"])
+def test_norm_of_large_rows_in_place(where):
+    # h replaces X or R; fp32, so that it is h itself
+    x, r, w = _randn(1, 6, 700).to(DEV) * 2.0 ** 70, _randn(2, 6, 700).to(DEV) * 2.0 ** 69, _randn(3, 700).to(DEV) * 0.1
+    want = gptq.rmsnorm_fp8(x, w, r)
+    h = (x if where == "x" else r).clone()
+    c, e = torch.empty(6, 704, dtype=torch.uint8, device=DEV), torch.empty(6, 8, dtype=torch.uint8, device=DEV)
+    rstd = torch.zeros(6, device=DEV)
+    p = gptq._ptr
+    st = gptq.gptq_rmsnorm_fp8(p(h) if where == "x" else p(x), 2, 6, 700, 700, p(r) if where == "x" else p(h), 700, p(w), 2, 1e-6,
+                               p(h), 700, p(c), 704, p(e), 8, p(rstd), gptq._stream(None))
+    assert st == 0 and torch.equal(h, want[3]) and torch.equal(c[:, :700], want[0].view(torch.uint8))
+    np.testing.assert_allclose(_np(rstd), SO.rmsnorm(_np(x), _np(w), _np(r), 1e-6)[2], rtol=4e-6)
