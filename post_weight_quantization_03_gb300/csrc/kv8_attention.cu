@@ -541,10 +541,11 @@ gptq_status run_decode(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   float *part = (float *)((char *)ws + 256);
   // Short histories (two rounds of the groups) gain nothing from being cut, and uncut they need
-  // no second kernel: 9.8 -> 7.4 us for one token of 500 with 32 heads.
+  // no second kernel: 8.8 -> 7.7 us for one token of 500 with 32 heads.
   // More items than CTAs: a group an item leaves no group without blocks and joins nothing, where
-  // the estimate in blocks says so (one token, 100 sequences of 60: 47 us by CTAs, 20.6 by groups;
-  // 15 of 86, 32 cache heads: 22.4 and 14.8; but 8 of 500, 32 cache heads: 18.5 and 24.2).
+  // the estimate in blocks says so (one token, 100 sequences of 60, 8 cache heads: 24.5 us by CTAs,
+  // 11.0 by groups; 15 of 86, 32 cache heads: 21.9 and 11.5; but 8 of 500, 32 cache heads: 13.9
+  // and 19.4).
   const int groups = kWarps / rt;
   int deal = stays_whole(rows, g.max_blocks) ? kItemsToCtas : kUnits;
   const int64_t items = ceil_div(g.n_seq * g.n_kv, ctas);  // of a CTA
@@ -561,14 +562,15 @@ gptq_status run_decode(const Kv8AttentionArgs &g, void *ws, cudaStream_t s) {
 // Whether `rows` rows of a cache head go to the other kernel's 128-row tiles.  More than 32 always
 // do; fewer where the products here (a pass of MMAs for each eight rows and three terms) outweigh
 // the copies, and the history is long enough for that kernel's set-up (32 sequences of up to
-// 4000 tokens, here and there):
-//   17 to 32 rows   bf16, 128 channels 120 and 86 us (4 of 500: 21.7 and 20.8, 2 of 120: 12.5 and
-//                   16.2); fp16, 64 channels 104 and 73; but bf16, 64 channels 71.5 and 70.7
-//   9 to 16 rows    fp16, 128 channels 112 and 87 (8 of 1500: 28.1 and 26.6, 16 of 500: 20.0 and
-//                   25.9); but fp16, 64 channels 64 and 72; bf16, 128 channels 76 and 84
+// 4000 tokens of 8 cache heads, here and there):
+//   17 to 32 rows   bf16 78 and 67 us with 64 channels (4 of 500: 14.8 and 10.2, 16 of 700: 18.3
+//                   and 18.0), 124 and 80 with 128 (4 of 500: 19.7 and 12.5, 2 of 120: 9.5 and
+//                   9.3); fp16 108 and 67, 222 and 84
+//   9 to 16 rows    fp16, 128 channels 129 and 83 (8 of 1500: 29.5 and 23.3, 16 of 500: 16.4 and
+//                   14.6); but fp16, 64 channels 65 and 67; bf16 48 and 66, 75 and 80
 bool takes_tiles(int64_t rows, bool half, int dim, int64_t max_blocks) {
   if (rows > kRows) return true;
-  if (rows > 16) return (half || dim == 128) && max_blocks > 6;
+  if (rows > 16) return max_blocks > 6;
   return rows > 8 && half && dim == 128 && max_blocks > 20;
 }
 
