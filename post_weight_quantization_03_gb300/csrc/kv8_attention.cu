@@ -38,9 +38,9 @@
 // in order (repeatable).  Short histories are dealt whole, to CTAs or, where there are many, to
 // groups.
 //
-// Measured: 48 sequences of up to 8000 tokens (8 cache heads of 128, 64 heads: 596 MB) 111 us,
-// 5.4 TB/s; each further 100 MB takes 15 us (6.6 TB/s), the rest is the start of the copies and
-// the joining kernel.  One sequence of 500 tokens, 32 heads: 7.3 us, latency.
+// Measured: 48 sequences of up to 8000 tokens (8 cache heads of 128, 64 heads: 596 MB) 112.5 us,
+// 5.3 TB/s; each further 100 MB takes 15.7 us (6.4 TB/s), the rest is the start of the copies and
+// the joining kernel.  One sequence of 500 tokens, 32 heads: 7.5 us, latency.
 #include "kv8.cuh"
 
 namespace gptq {
@@ -409,18 +409,22 @@ decode_kernel(Kv8AttentionArgs g, int deal, float *part, DevStatus *st) {
         for (int j = 1; j < 8; ++j) low = __hmin2(low, x[j]);
         low = __hmin2(low, __lowhigh2highlow(low));
         if (__builtin_expect(__any_sync(0xffffffffu, __low2float(low) < kFew && b > hidden), 0)) {
-          float mass = 0.0f;  // of the row's sums
-#pragma unroll
-          for (int q = 0; q < D / 8; ++q)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) mass += fabsf(fmaf(acc[q][j + 2], kLowValue, acc[q][j]));
-          mass += __shfl_xor_sync(0xffffffffu, mass, 1);
-          mass += __shfl_xor_sync(0xffffffffu, mass, 2);
-          hidden = fmaxf(hidden, b + __log2f(mass / (kHide * D)));
           bool few = false;  // without the zeros of masked tokens
 #pragma unroll
           for (int j = 0; j < 16; ++j) few |= y[j] < kFew && y[j] >= kNone;
-          if (__builtin_expect(__any_sync(0xffffffffu, few && b > hidden), 0)) {
+          few &= b > hidden;
+          if (__any_sync(0xffffffffu, few)) {
+            float mass = 0.0f;  // of the row's sums
+#pragma unroll
+            for (int q = 0; q < D / 8; ++q)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) mass += fabsf(fmaf(acc[q][j + 2], kLowValue, acc[q][j]));
+            mass += __shfl_xor_sync(0xffffffffu, mass, 1);
+            mass += __shfl_xor_sync(0xffffffffu, mass, 2);
+            hidden = fmaxf(hidden, b + __log2f(mass / (kHide * D)));
+            few &= b > hidden;
+          }
+          if (__builtin_expect(__any_sync(0xffffffffu, few), 0)) {
             uint32_t rest[4][NT];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
