@@ -564,9 +564,14 @@ size_t gptq_kv8_attention_workspace_bytes(int64_t n_seq, int64_t n_new, int n_he
  *              cache past `length` never matter.
  *   scale      factor of the scores (finite).
  *   Scores, their statistics and sums are fp32, of queries held to 2^-17 of their largest element
- *   or better; a probability is held in 8 bits of significand or more (9 for BF16 and 12 for F16 up
- *   to 32 rows of a cache head, 11 beyond).  Weighted by its block's value scale, what is below
- *   2^-33 of a row's largest adds to the softmax's sum and not to the output.
+ *   or better.  Probabilities, weighted by their block's value scale, are multiplied as numbers
+ *   - of 9 bits (BF16) or 12 bits (F16) where few rows share a cache head (a decoding step): a small
+ *     one may be off by 2^-23 of its block's largest where that is hidden, to 2^-9, in the row's sums,
+ *     and one below 2^-40 of the row's largest adds to the softmax's sum alone;
+ *   - of 11 bits (fp16) in prompts: with fewer from 2^-24 of the row's largest on, and one below 2^-33
+ *     adds to the softmax's sum alone.
+ *   The width max_blocks of the table, not the lengths, chooses the kernel and the way that its work
+ *   is dealt (and sizes ws): a table much wider than the histories in it costs short ones time.
  *   ws         workspace of ws_bytes >= gptq_kv8_attention_workspace_bytes(...).
  * Repeated calls give identical results.  Asynchronous; a bounded device wait that gave up is
  * recorded in ws (gptq_workspace_status).  Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED, CUDA.

@@ -21,10 +21,11 @@
 // CTAs, whose partial sums meet through distributed shared memory in rank order.
 //
 // Bounds, and what it measured (GPU time, m x n x k): up to a few hundred tokens W's bytes
-// (1 x 4096 x 4096 5.4 us, of which 2.5 are the bytes; 24 x 11008 x 4096 11.2 us, 4.1 TB/s;
-// 128 x 8192 x 28672 43.5 us, 5.5 TB/s), the rest of it being the launch, the first copies and the
-// exchange of split sums.  Beyond, the tensor core: 515 x 4096 x 11008 26 us, 1.8 PFLOP/s;
-// 8192 x 11008 x 4096 243 us, 3.0 PFLOP/s, the pipe busy 72 % of the time.
+// (1 x 4096 x 4096 5.7 us, of which 2.5 are the bytes; 24 x 11008 x 4096 11.3 us, 4.0 TB/s;
+// 128 x 8192 x 28672 44 us, 5.4 TB/s), the rest of it being the launch, the first copies and the
+// exchange of split sums.  Beyond, the tensor core: 515 x 4096 x 11008 25.5 us, 1.8 PFLOP/s;
+// 8192 x 11008 x 4096 244 us, 3.0 PFLOP/s, the pipe busy 72 % of the time (281 us, 2.6 PFLOP/s, in a
+// row of calls that the power limit holds back).
 #include <cudaTypedefs.h>
 #include <math.h>
 

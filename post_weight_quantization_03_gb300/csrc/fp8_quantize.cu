@@ -7,8 +7,8 @@
 // (which the product's epilogue applies) loses nothing against quantizing y, and the codes do
 // not wait for the row's sum: the kernel reads x and r once, writes h and the codes in the same
 // pass, and only the 4-byte rstd needs the whole row.  HBM-bound: 7 bytes an element for 16-bit
-// x with a residual (8192 x 8192: 75.6 us, 6.2 TB/s; 1 x 4096: 2.4 us, a launch and two
-// latencies).
+// x with a residual (8192 x 8192: 73 us, 6.4 TB/s; 1 x 4096: 2.3 us, a launch and two latencies).
+// Without one, 3 bytes, the issue slots come first (73 % taken): 51 us, 3.9 TB/s.
 #include <type_traits>
 
 #include "fp8.cuh"
@@ -114,8 +114,8 @@ __device__ __forceinline__ void store_rstd(const RowsParams &p, int64_t row, flo
 // CTAS an SM at least (of 512 threads): two, or three where rows queue for long.  Three leave 40
 // registers a thread, so a row's loads are not all in flight, but more rows' are: what the
 // memory's latency is hidden by in a long queue, and a longer way for each row in a short one
-// (bf16 with a residual: 8192 x 8192 85 us with two and 76 us, 6.2 TB/s, with three; 4000 x 4096
-// 22.8 and 20.6; but 907 x 6144 7.2 and 7.9, 1336 x 1728 4.5 and 5.5).
+// (bf16 with a residual: 8192 x 8192 85 us with two and 73 us, 6.4 TB/s, with three; 4000 x 4096
+// 22.7 and 19.5; but 1336 x 1728 4.5 and 5.4, 907 x 6144 6.9 and 6.8).
 template <typename T, typename TW, int VPT, int CTAS>
 __global__ void __launch_bounds__(kMaxRowThreads, CTAS)
 rows_kernel(RowsParams p) {

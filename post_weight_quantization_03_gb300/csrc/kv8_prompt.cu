@@ -26,8 +26,9 @@
 // Measured: 4096 tokens of 32 heads of 128 (8 in the cache, causal) 124 us, 1.1 PFLOP/s; 2 x 777
 // of up to 16000 tokens, heads of 64, fp16 queries 240 us, 0.8 PFLOP/s of 4 D a pair (1.2 executed:
 // a third term).  Neither the tensor core (49 and 43 % busy) nor the exponentials (26 and 35 %) are
-// full: a block of 64 tokens passes from one to the other and back, two blocks and two tiles at a
-// time, and each passage costs its latency.
+// full: a block of 64 tokens of both tiles takes about the sum of its softmax and its MMAs (1900 and
+// 1470 cycles), so that the two run nearly one after the other though two blocks of two tiles are in
+// flight.  Which wait holds which role has not been measured.
 //
 // Warps: 0-3 and 4-7 softmax, a tile each; 8-11 copies and converters; 12 and 13 MMA issuers, a
 // tile each (12 owns TMEM).
@@ -492,7 +493,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap mk, Kv8AttentionArgs g, int un
       const int mine = nb - at.blk < m ? (nb - at.blk < 0 ? 0 : nb - at.blk) : m;
       // a row that does not exist is as good as one that sees everything
       const int limit = r < plan.rows ? plan.seen(len, r, r + 1) : INT_MAX;
-      // queries: scaled to a maximum of [1, 2), fp16, K-major
       // Where this thread's row of queries starts, and of outputs (rows that do not exist: row 0).
       const int rq = r < plan.rows ? r / plan.group : 0, hq = r < plan.rows ? r % plan.group : 0;
       const int64_t q_at = seq * g.q_stride[0] + rq * g.q_stride[1] +
