@@ -66,8 +66,10 @@ constexpr float kSlack = 1.0f, kFar = 40.0f;
 // never counts.  What the terms of a number below kFew leave out is 2^-15 at most, so that times
 // kRest it is a number for two terms again.
 constexpr float kFew = 0x1p-7f, kNone = 0x1p-32f, kRest = 0x1p23f;
-// A row's sums that hide what a block leaves out, at most 64 x 2^-15 x 448, to 2^-9.
-constexpr float kHide = 64 * 0x1p-15f * 448 * 0x1p9f;
+// What a block's terms leave out, up to 64 x 2^-15 x 56 with values' codes of middling size, over a
+// row's sums is to be 2^-9 at most in the mean of the channels (so the sums count by their harmonic
+// mean: by the plain one, tokens with values in a few channels would hide what the others lose).
+constexpr float kHide = 64 * 0x1p-15f * 56 * 0x1p9f;
 static_assert(kRows == 8 * 4, "row tiles: 1, 2 or 4");
 
 __device__ int g_gave_up;  // a wait ran out since it was last asked for
@@ -414,14 +416,15 @@ decode_kernel(Kv8AttentionArgs g, int deal, float *part, DevStatus *st) {
           for (int j = 0; j < 16; ++j) few |= y[j] < kFew && y[j] >= kNone;
           few &= b > hidden;
           if (__any_sync(0xffffffffu, few)) {
-            float mass = 0.0f;  // of the row's sums
+            float inverse = 0.0f;  // of the row's sums: a sum of 0 hides nothing
 #pragma unroll
             for (int q = 0; q < D / 8; ++q)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) mass += fabsf(fmaf(acc[q][j + 2], kLowValue, acc[q][j]));
-            mass += __shfl_xor_sync(0xffffffffu, mass, 1);
-            mass += __shfl_xor_sync(0xffffffffu, mass, 2);
-            hidden = fmaxf(hidden, b + __log2f(mass / (kHide * D)));
+              for (int j = 0; j < 2; ++j)
+                inverse += __fdividef(1.0f, fabsf(fmaf(acc[q][j + 2], kLowValue, acc[q][j])));
+            inverse += __shfl_xor_sync(0xffffffffu, inverse, 1);
+            inverse += __shfl_xor_sync(0xffffffffu, inverse, 2);
+            hidden = fmaxf(hidden, b - __log2f(inverse * (kHide / D)));
             few &= b > hidden;
           }
           if (__builtin_expect(__any_sync(0xffffffffu, few), 0)) {

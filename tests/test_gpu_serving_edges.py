@@ -172,3 +172,23 @@ def test_norm_of_large_rows_in_place(where):
                                p(h), 700, p(c), 704, p(e), 8, p(rstd), gptq._stream(None))
     assert st == 0 and torch.equal(h, want[3]) and torch.equal(c[:, :700], want[0].view(torch.uint8))
     np.testing.assert_allclose(_np(rstd), SO.rmsnorm(_np(x), _np(w), _np(r), 1e-6)[2], rtol=4e-6)
+
+
+@pytest.mark.parametrize("new,group,d,tokens", [(1, 1, 128, 3000), (1, 8, 64, 3000), (2, 8, 64, 3000), (1, 8, 128, 700), (2, 8, 128, 1500)])
+@pytest.mark.parametrize("channels", [1, 8, 32])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_attention_behind_tokens_with_values_in_few_channels(new, group, d, tokens, channels, dtype):
+    # the other channels are the other tokens' alone, however large the first ones are
+    rng = np.random.default_rng(channels + tokens)
+    n = -(-tokens // 64)
+    ones = rng.choice([-1.0, 1.0], d)
+    k = rng.standard_normal((n, 1, 64, d))
+    v = 0.5 + rng.standard_normal((n, 1, 64, d))
+    k[:, :, 5::8] = 14.0 / np.sqrt(d) * ones
+    v[:, :, 5::8, channels:] = 0
+    cache = (SO.encode(k * 64), SO.encode(v.transpose(0, 1, 3, 2).copy() * 64), np.full((n, 1), 121, np.uint8),
+             np.full((n, 1), 121 + 16, np.uint8))
+    table = rng.permutation(n).reshape(1, n).astype(np.int32)
+    q = torch.from_numpy(ones + 0.02 * rng.standard_normal((1, new, group, d))).to(DT[dtype])
+    out = gptq.kv8_attention(q.to(DEV), _dev_cache(cache), _i32(table), _i32([tokens]))
+    _check_attention(out, q, cache, table, [tokens])
