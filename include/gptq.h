@@ -586,8 +586,8 @@ gptq_status gptq_kv8_attention(const void *q, const int64_t *q_strides, int dtyp
 
 /*
  * gptq_serving_status: synchronize `stream`, then return GPTQ_ERR_TIMEOUT if a bounded device wait
- * of a gptq_fp8_matmul or gptq_kv8_attention on the current device, on whichever stream and
- * workspace, has given up since the last such query (the outputs of that call are undefined), else
+ * of a gptq_fp8_matmul, gptq_kv8_attention or one of the products of feed-forward blocks on the
+ * current device, on whichever stream and workspace, has given up since the last such query (the outputs of that call are undefined), else
  * GPTQ_OK.  It is recorded beside the workspaces' status, which the next call on a workspace resets:
  * a program that runs many calls asks once, after them.  (In a stream that is captured: CUDA.)
  * Errors of its own: CUDA.
@@ -620,6 +620,145 @@ gptq_status gptq_debug_kv8_attention_lost_copy(
     int64_t max_blocks, const int32_t *lengths, int causal, float scale, void *out,
     const int64_t *o_strides, int64_t lost_copy, uint64_t wait_ns, void *ws, size_t ws_bytes,
     gptq_stream_t stream);
+
+/* ======================================================================================
+ * Feed-forward blocks on quantized layers: what lies between their products, and experts
+ * ====================================================================================== */
+
+/* Activation functions, taken in fp32: x, max(x, 0) (NaN stays), x / (1 + exp(-x)),
+ * x (1 + erf(x / sqrt 2)) / 2. */
+typedef enum gptq_act {
+  GPTQ_ACT_NONE = 0, GPTQ_ACT_RELU = 1, GPTQ_ACT_SILU = 2, GPTQ_ACT_GELU = 3
+} gptq_act;
+
+/*
+ * gptq_fp8_weights (a HOST struct): the weights W [n, k] of a product in 128 x 128 blocks as in
+ * gptq_fp8_matmul, or one such matrix for each of several experts.
+ *   codes      [n, ld];  exps: [ceil(n / 128), ld_exps];
+ *   next_codes, next_exps   elements from one expert's matrix to the next: multiples of 16 and 4 that
+ *              are at least n * ld and ceil(n / 128) * ld_exps (read where there are experts alone).
+ *   scale, bias   [n] fp32, or [n_experts, n], or NULL (1, 0).
+ */
+typedef struct gptq_fp8_weights {
+  const uint8_t *codes;
+  int64_t ld, next_codes;
+  const uint8_t *exps;
+  int64_t ld_exps, next_exps;
+  const float *scale, *bias;
+} gptq_fp8_weights;
+
+/*
+ * gptq_fp8_linear_workspace_bytes: workspace size of the four products below; rows: m, or
+ * n_tokens * top_k.  0 for bad arguments.
+ */
+size_t gptq_fp8_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k);
+
+/*
+ * gptq_fp8_linear: out [m, n] = act(diag(a_scale) A W^T diag(scale) + bias) + residual, summed in
+ * fp32 and rounded once to odtype.
+ *
+ *   a, a_exps, a_scale, out, ws   as in gptq_fp8_matmul.
+ *   act        a gptq_act.
+ *   residual   [m, ldr] of odtype, or NULL; it may be out itself (with ldr = ldo).
+ * Repeated calls give identical results.  Asynchronous; a bounded device wait that gave up is
+ * recorded in ws (gptq_workspace_status).  Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED, CUDA.
+ */
+gptq_status gptq_fp8_linear(const uint8_t *a, int64_t lda, const uint8_t *a_exps, int64_t ldae,
+                            const float *a_scale, const gptq_fp8_weights *w, int act,
+                            const void *residual, int64_t ldr, int64_t m, int64_t n, int64_t k,
+                            void *out, int odtype, int64_t ldo, void *ws, size_t ws_bytes,
+                            gptq_stream_t stream);
+
+/*
+ * gptq_fp8_gated: codes and exponents, by 1 x 128 blocks, of act(G) * U [m, n], where
+ * G = diag(a_scale) A Gate^T diag(scale) + bias and U the same of `up`; all in fp32 until it is
+ * rounded to the codes.  What is not finite becomes the NaN code.
+ * Otherwise as gptq_fp8_linear.
+ */
+gptq_status gptq_fp8_gated(const uint8_t *a, int64_t lda, const uint8_t *a_exps, int64_t ldae,
+                           const float *a_scale, const gptq_fp8_weights *gate,
+                           const gptq_fp8_weights *up, int act, int64_t m, int64_t n, int64_t k,
+                           uint8_t *codes, int64_t ldc, uint8_t *exps, int64_t lde, void *ws,
+                           size_t ws_bytes, gptq_stream_t stream);
+
+/*
+ * gptq_moe_route: which top_k experts each token goes to, with which weights, and the tokens of
+ * each expert.
+ *
+ *   s_e = softmax over the token's logits, or 1 / (1 + exp(-logit)).
+ *   c_e = s_e + bias_e; where there is neither a bias nor groups, the logit.
+ *   groups > 1: the experts fall into `groups` runs of n_experts / groups; a run's value is the sum
+ *         of its group_top (1 or 2) largest c, and only the top_groups best runs are looked at.
+ *   ids   the top_k experts of largest c, largest first; equals: the lowest index first.  The
+ *         choice is that of 64-bit arithmetic: c nearer to one another than fp32 tells are taken
+ *         again in fp64.
+ *   weights: s of the chosen experts, with renormalize over their sum, times scale.
+ * An expert whose logit or bias is not finite is never chosen and adds nothing to the softmax's sum;
+ * where too few are left, the last ids of the token are -1 and their weights 0.
+ *
+ *   logits     [n_tokens, ld] of dtype (F16, BF16, F32), ld >= n_experts.
+ *   bias       [n_experts] fp32 or NULL.   scores: 0 softmax, 1 sigmoid.
+ *   ids [n_tokens, top_k] int32, weights [n_tokens, top_k] fp32 out.
+ *   offsets [n_experts + 1] int32, order [n_tokens * top_k] int32 out: order lists the assignments
+ *              (token * top_k + place among its ids) by expert, in increasing order for each;
+ *              expert e has order[offsets[e]] to order[offsets[e + 1] - 1].  -1 after the last.
+ *   1 <= top_k <= 32; n_experts <= 1024, groups <= 32, n_tokens * top_k <= 2^22 (else UNSUPPORTED);
+ *   groups divides n_experts, 1 <= top_groups <= groups, group_top <= n_experts / groups and
+ *   top_k <= top_groups * n_experts / groups; scale finite.
+ *   ws         workspace of ws_bytes >= gptq_moe_route_workspace_bytes(n_tokens, n_experts, top_k).
+ * Asynchronous.  Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED, CUDA.
+ */
+size_t gptq_moe_route_workspace_bytes(int64_t n_tokens, int n_experts, int top_k);
+gptq_status gptq_moe_route(const void *logits, int dtype, int64_t ld, int64_t n_tokens,
+                           int n_experts, int top_k, const float *bias, int scores, int groups,
+                           int top_groups, int group_top, int renormalize, float scale,
+                           int32_t *ids, float *weights, int32_t *offsets, int32_t *order,
+                           void *ws, size_t ws_bytes, gptq_stream_t stream);
+
+/*
+ * gptq_fp8_experts_gated: gptq_fp8_gated of the rows of each expert.  Position p of the order takes
+ * A's row order[p] / top_k and the weights of the expert e with offsets[e] <= p < offsets[e + 1],
+ * and is row p of the codes.
+ *   a          [n_tokens, lda];  a_exps, a_scale likewise.
+ *   offsets, order   as written by gptq_moe_route for n_experts and n_tokens * top_k.  Offsets are
+ *              limited to [0, n_tokens * top_k] and read as increasing; a position whose order
+ *              names no row of A is computed as of zeros.
+ *   codes, exps   [n_tokens * top_k, ...]; rows from offsets[n_experts] on stay as they are.
+ *   n_experts  1 .. 1024 (else UNSUPPORTED).
+ * Otherwise as gptq_fp8_gated.
+ */
+gptq_status gptq_fp8_experts_gated(const uint8_t *a, int64_t lda, const uint8_t *a_exps,
+                                   int64_t ldae, const float *a_scale,
+                                   const gptq_fp8_weights *gate, const gptq_fp8_weights *up,
+                                   int act, int n_experts, const int32_t *offsets,
+                                   const int32_t *order, int top_k, int64_t n_tokens, int64_t n,
+                                   int64_t k, uint8_t *codes, int64_t ldc, uint8_t *exps,
+                                   int64_t lde, void *ws, size_t ws_bytes, gptq_stream_t stream);
+
+/*
+ * gptq_fp8_experts: out[order[p]] = act(A_p W_e^T diag(scale_e) + bias_e) for each position p, e its
+ * expert: from rows in the experts' order to rows in the tokens'.
+ *   a          [rows, lda], as written by gptq_fp8_experts_gated.
+ *   out        [rows, ldo] of odtype; rows that no order names stay as they are.  No two positions
+ *              may name one row.
+ * Otherwise as gptq_fp8_linear.
+ */
+gptq_status gptq_fp8_experts(const uint8_t *a, int64_t lda, const uint8_t *a_exps, int64_t ldae,
+                             const gptq_fp8_weights *w, int act, int n_experts,
+                             const int32_t *offsets, const int32_t *order, int64_t rows, int64_t n,
+                             int64_t k, void *out, int odtype, int64_t ldo, void *ws,
+                             size_t ws_bytes, gptq_stream_t stream);
+
+/*
+ * gptq_moe_combine: out[t] = residual[t] + sum_j weights[t, j] y[t * top_k + j], summed in fp32 in
+ * that order and rounded once.  A row whose weight is 0 is not read.
+ *   y [n_tokens * top_k, ldy], residual [n_tokens, ldr] or NULL, out [n_tokens, ldo] of dtype (F16,
+ *   BF16 or F32); out may be the residual.   weights [n_tokens, top_k] fp32.   1 <= top_k <= 32.
+ * Asynchronous.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+gptq_status gptq_moe_combine(const void *y, int dtype, int64_t ldy, int64_t n_tokens, int top_k,
+                             int64_t d, const float *weights, const void *residual, int64_t ldr,
+                             void *out, int64_t ldo, gptq_stream_t stream);
 
 #ifdef __cplusplus
 }

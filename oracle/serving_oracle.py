@@ -172,3 +172,92 @@ def kv_attention(q, cache, table, lengths, scale=None, causal=True):
                     if np.isfinite(x).all():
                         terms = max(terms, float((np.abs(K[see]) @ np.abs(qv)).max() * abs(scale)))
     return out, mag, terms
+
+
+# ---------------------------------------------------------------------------------------
+# Feed-forward blocks
+# ---------------------------------------------------------------------------------------
+
+def activate(x, act):
+    if act == "relu":
+        return np.where(x < 0, 0.0, x)
+    if act == "silu":
+        with np.errstate(over="ignore"):
+            return x / (1 + np.exp(-x))
+    if act == "gelu":
+        return 0.5 * x * (1 + np.vectorize(math.erf)(x / math.sqrt(2)))
+    return x
+
+
+def linear(a, ae, w, we, ra=None, rw=None, bias=None):
+    """(product with its bias, sum of the magnitudes of its terms)."""
+    x, mag = matmul(a, ae, w, we, ra, rw)
+    if bias is not None:
+        x, mag = x + np.asarray(bias, np.float64), mag + np.abs(bias)
+    return x, mag
+
+
+def route(logits, top_k, bias=None, scores="softmax", groups=1, top_groups=1, group_top=1,
+          renormalize=True, scale=1.0):
+    """(ids, weights, offsets, order), token by token."""
+    x = np.asarray(logits, np.float64)
+    t, n = x.shape
+    b = None if bias is None else np.asarray(bias, np.float64)
+    size = n // groups
+    ids, weights = np.full((t, top_k), -1, np.int32), np.zeros((t, top_k))
+    for i in range(t):
+        ok = np.isfinite(x[i])
+        if not ok.any():
+            continue
+        v = np.where(ok, x[i], -np.inf)
+        if scores == "softmax":
+            e = np.exp(v - v.max())
+            s = e / e.sum()
+        else:
+            with np.errstate(over="ignore"):
+                s = np.where(ok, 1 / (1 + np.exp(-v)), 0.0)
+        c = v.copy() if b is None and groups == 1 else s if b is None else s + b
+        c = np.where(ok & np.isfinite(c), c, -np.inf)
+        if groups > 1:
+            g = -np.sort(-c.reshape(groups, size), 1)[:, :group_top]
+            value = np.where(np.isfinite(g), g, 0.0).sum(1) + np.where(np.isfinite(g[:, 0]), 0.0, -np.inf)
+            open_ = np.zeros(groups, bool)
+            open_[np.argsort(-value, kind="stable")[:top_groups]] = True
+            c = np.where(np.repeat(open_ & np.isfinite(value), size), c, -np.inf)
+        best = np.argsort(-c, kind="stable")[:top_k]
+        best = best[np.isfinite(c[best])]
+        ids[i, :len(best)] = best
+        if len(best) == 0:
+            continue
+        if not renormalize:
+            w = s[best]
+        elif scores == "softmax":
+            w = np.exp(v[best] - v[best].max())
+            w = w / w.sum()
+        else:                                    # log(sigmoid), so that all may be tiny
+            ls = np.minimum(v[best], 0) - np.log1p(np.exp(-np.abs(v[best])))
+            w = np.exp(ls - ls.max())
+            w = w / w.sum()
+        weights[i, :len(best)] = w * scale
+    return (ids, weights, *plan(ids, n))
+
+
+def plan(ids, n_experts):
+    """(offsets, order) of the assignments by expert."""
+    flat = ids.reshape(-1)
+    order = np.argsort(np.where(flat < 0, n_experts, flat), kind="stable").astype(np.int32)
+    count = np.bincount(flat[flat >= 0], minlength=n_experts)
+    offsets = np.concatenate([[0], np.cumsum(count)]).astype(np.int32)
+    order[offsets[-1]:] = -1
+    return offsets, order
+
+
+def combine(y, weights, residual=None):
+    """(sum, sum of the magnitudes of its terms); rows of weight 0 are left out."""
+    t, k = weights.shape
+    w = np.asarray(weights, np.float64)
+    terms = np.where(w[..., None] != 0, np.where(w != 0, w, 1)[..., None] * np.asarray(y, np.float64).reshape(t, k, -1), 0.0)
+    x, mag = terms.sum(1), np.abs(terms).sum(1)
+    if residual is not None:
+        x, mag = x + residual, mag + np.abs(residual)
+    return x, mag

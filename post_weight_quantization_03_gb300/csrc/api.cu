@@ -402,10 +402,166 @@ gptq_status gptq_debug_fp8_matmul_lost_copy(const uint8_t *a, int64_t lda, const
 }
 
 gptq_status gptq_serving_status(gptq_stream_t stream) {
-  int product = 0, attention = 0;
+  int product = 0, attention = 0, linear = 0;
   GPTQ_TRY(fp8_matmul_take_timeout(&product, (cudaStream_t)stream));
   GPTQ_TRY(kv8_attention_take_timeout(&attention, (cudaStream_t)stream));
-  return (gptq_status)(product != 0 ? product : attention);
+  GPTQ_TRY(fp8_linear_take_timeout(&linear, (cudaStream_t)stream));
+  return (gptq_status)(product != 0 ? product : attention != 0 ? attention : linear);
+}
+
+constexpr int kMaxExperts = 1024, kMaxTopK = 32;
+
+// n_experts: 0 for one matrix.
+static bool fp8_weights_ok(const gptq_fp8_weights *w, int n_experts, int64_t n, int64_t k) {
+  if (!w || !fp8_codes_ok(w->codes, w->ld, k) || !fp8_exps_ok(w->exps, w->ld_exps, k) ||
+      !aligned(w->scale, 4) || !aligned(w->bias, 4))
+    return false;
+  return n_experts < 2 || (w->next_codes % 16 == 0 && w->next_codes / w->ld >= n && w->next_exps % 4 == 0 &&
+                           w->next_exps / w->ld_exps >= ceil_div(n, (int64_t)fp8::kBlock));
+}
+
+size_t gptq_fp8_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k) {
+  if (rows < 0 || n < 1 || k < 1) return 0;
+  return fp8_linear_ws_bytes(rows, n, k);
+}
+
+// What the four products share.
+static gptq_status fp8_linear_checked(const Fp8LinearArgs &g, void *ws, size_t ws_bytes,
+                                      gptq_stream_t stream) {
+  if (g.M < 0 || g.N < 1 || g.K < 1 || g.a_rows < 0 || g.act < GPTQ_ACT_NONE || g.act > GPTQ_ACT_GELU)
+    return GPTQ_ERR_INVALID_ARG;
+  if (!fp8_weights_ok(&g.w[0], g.n_experts, g.N, g.K) ||
+      (g.gated && !fp8_weights_ok(&g.w[1], g.n_experts, g.N, g.K)))
+    return GPTQ_ERR_INVALID_ARG;
+  if (!g.gated && ((g.odtype != GPTQ_F16 && g.odtype != GPTQ_BF16) || g.ldo < g.N ||
+                   (g.residual && (g.ldr < g.N || !aligned(g.residual, 2)))))
+    return GPTQ_ERR_INVALID_ARG;
+  if (g.M > 0) {
+    if (!fp8_codes_ok(g.a, g.lda, g.K) || !fp8_exps_ok(g.ae, g.ldae, g.K) || !aligned(g.ra, 4))
+      return GPTQ_ERR_INVALID_ARG;
+    if (g.gated ? !fp8_codes_ok((const uint8_t *)g.out, g.ldo, g.N) || !fp8_exps_ok(g.oe, g.ldoe, g.N)
+                : !g.out || !aligned(g.out, 2))
+      return GPTQ_ERR_INVALID_ARG;
+    if (g.n_experts > 0 && (!g.offsets || !g.order || !aligned(g.offsets, 4) || !aligned(g.order, 4)))
+      return GPTQ_ERR_INVALID_ARG;
+  }
+  if (g.K > kFp8MaxWidth || g.M > kFp8MaxRows || g.a_rows > kFp8MaxRows || g.N > kFp8MaxRows ||
+      (g.gated && g.N > kFp8MaxWidth) || g.n_experts > kMaxExperts)
+    return GPTQ_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, 256) || ws_bytes < fp8_linear_ws_bytes(g.M, g.N, g.K))
+    return GPTQ_ERR_WORKSPACE;
+  return launch_fp8_linear(g, ws, (cudaStream_t)stream);
+}
+
+gptq_status gptq_fp8_linear(const uint8_t *a, int64_t lda, const uint8_t *a_exps, int64_t ldae,
+                            const float *a_scale, const gptq_fp8_weights *w, int act,
+                            const void *residual, int64_t ldr, int64_t m, int64_t n, int64_t k,
+                            void *out, int odtype, int64_t ldo, void *ws, size_t ws_bytes,
+                            gptq_stream_t stream) {
+  if (!w) return GPTQ_ERR_INVALID_ARG;
+  Fp8LinearArgs g{};
+  g.a = a; g.lda = lda; g.ae = a_exps; g.ldae = ldae; g.ra = a_scale; g.a_rows = m;
+  g.w[0] = *w;
+  g.act = act;
+  g.residual = residual; g.ldr = ldr;
+  g.M = m; g.N = n; g.K = k;
+  g.out = out; g.odtype = odtype; g.ldo = ldo;
+  return fp8_linear_checked(g, ws, ws_bytes, stream);
+}
+
+gptq_status gptq_fp8_gated(const uint8_t *a, int64_t lda, const uint8_t *a_exps, int64_t ldae,
+                           const float *a_scale, const gptq_fp8_weights *gate,
+                           const gptq_fp8_weights *up, int act, int64_t m, int64_t n, int64_t k,
+                           uint8_t *codes, int64_t ldc, uint8_t *exps, int64_t lde, void *ws,
+                           size_t ws_bytes, gptq_stream_t stream) {
+  if (!gate || !up) return GPTQ_ERR_INVALID_ARG;
+  Fp8LinearArgs g{};
+  g.a = a; g.lda = lda; g.ae = a_exps; g.ldae = ldae; g.ra = a_scale; g.a_rows = m;
+  g.w[0] = *gate; g.w[1] = *up; g.gated = true;
+  g.act = act;
+  g.M = m; g.N = n; g.K = k;
+  g.out = codes; g.ldo = ldc; g.oe = exps; g.ldoe = lde;
+  return fp8_linear_checked(g, ws, ws_bytes, stream);
+}
+
+gptq_status gptq_fp8_experts_gated(const uint8_t *a, int64_t lda, const uint8_t *a_exps,
+                                   int64_t ldae, const float *a_scale,
+                                   const gptq_fp8_weights *gate, const gptq_fp8_weights *up,
+                                   int act, int n_experts, const int32_t *offsets,
+                                   const int32_t *order, int top_k, int64_t n_tokens, int64_t n,
+                                   int64_t k, uint8_t *codes, int64_t ldc, uint8_t *exps,
+                                   int64_t lde, void *ws, size_t ws_bytes, gptq_stream_t stream) {
+  if (!gate || !up || n_experts < 1 || top_k < 1 || n_tokens < 0) return GPTQ_ERR_INVALID_ARG;
+  if (top_k > kMaxTopK || n_tokens > kFp8MaxRows) return GPTQ_ERR_UNSUPPORTED;
+  Fp8LinearArgs g{};
+  g.a = a; g.lda = lda; g.ae = a_exps; g.ldae = ldae; g.ra = a_scale; g.a_rows = n_tokens;
+  g.w[0] = *gate; g.w[1] = *up; g.gated = true;
+  g.act = act;
+  g.M = n_tokens * top_k; g.N = n; g.K = k;
+  g.out = codes; g.ldo = ldc; g.oe = exps; g.ldoe = lde;
+  g.n_experts = n_experts; g.offsets = offsets; g.order = order; g.top_k = top_k;
+  return fp8_linear_checked(g, ws, ws_bytes, stream);
+}
+
+gptq_status gptq_fp8_experts(const uint8_t *a, int64_t lda, const uint8_t *a_exps, int64_t ldae,
+                             const gptq_fp8_weights *w, int act, int n_experts,
+                             const int32_t *offsets, const int32_t *order, int64_t rows, int64_t n,
+                             int64_t k, void *out, int odtype, int64_t ldo, void *ws,
+                             size_t ws_bytes, gptq_stream_t stream) {
+  if (!w || n_experts < 1) return GPTQ_ERR_INVALID_ARG;
+  Fp8LinearArgs g{};
+  g.a = a; g.lda = lda; g.ae = a_exps; g.ldae = ldae; g.a_rows = rows;
+  g.w[0] = *w;
+  g.act = act;
+  g.M = rows; g.N = n; g.K = k;
+  g.out = out; g.odtype = odtype; g.ldo = ldo;
+  g.n_experts = n_experts; g.offsets = offsets; g.order = order; g.top_k = 1;
+  return fp8_linear_checked(g, ws, ws_bytes, stream);
+}
+
+size_t gptq_moe_route_workspace_bytes(int64_t n_tokens, int n_experts, int top_k) {
+  if (n_tokens < 0 || n_experts < 1 || n_experts > kMaxExperts || top_k < 1 || top_k > kMaxTopK ||
+      n_tokens > kFp8MaxRows / top_k)
+    return 0;
+  return moe_route_ws_bytes(n_tokens, n_experts, top_k);
+}
+
+gptq_status gptq_moe_route(const void *logits, int dtype, int64_t ld, int64_t n_tokens,
+                           int n_experts, int top_k, const float *bias, int scores, int groups,
+                           int top_groups, int group_top, int renormalize, float scale,
+                           int32_t *ids, float *weights, int32_t *offsets, int32_t *order,
+                           void *ws, size_t ws_bytes, gptq_stream_t stream) {
+  const size_t es = elem_size(dtype);
+  if (es == 0 || n_tokens < 0 || n_experts < 1 || ld < n_experts || top_k < 1 ||
+      (scores != 0 && scores != 1) || groups < 1 || n_experts % groups != 0 || top_groups < 1 ||
+      top_groups > groups || (group_top != 1 && group_top != 2) || group_top > n_experts / groups ||
+      top_k > (int64_t)top_groups * (n_experts / groups) || !(scale - scale == 0.0f))
+    return GPTQ_ERR_INVALID_ARG;
+  if (!offsets || !aligned(offsets, 4) || !aligned(bias, 4)) return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!logits || !aligned(logits, es) || !ids || !aligned(ids, 4) || !weights ||
+                       !aligned(weights, 4) || !order || !aligned(order, 4)))
+    return GPTQ_ERR_INVALID_ARG;
+  if (top_k > kMaxTopK || n_experts > kMaxExperts || groups > 32 || n_tokens > kFp8MaxRows / top_k)
+    return GPTQ_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, 256) || ws_bytes < moe_route_ws_bytes(n_tokens, n_experts, top_k))
+    return GPTQ_ERR_WORKSPACE;
+  return launch_moe_route({logits, dtype, ld, n_tokens, n_experts, top_k, bias, scores, groups, top_groups,
+                           group_top, renormalize ? 1 : 0, scale, ids, weights, offsets, order},
+                          ws, (cudaStream_t)stream);
+}
+
+gptq_status gptq_moe_combine(const void *y, int dtype, int64_t ldy, int64_t n_tokens, int top_k,
+                             int64_t d, const float *weights, const void *residual, int64_t ldr,
+                             void *out, int64_t ldo, gptq_stream_t stream) {
+  const size_t es = elem_size(dtype);
+  if (es == 0 || n_tokens < 0 || top_k < 1 || d < 1 || ldy < d || ldo < d || (residual && ldr < d))
+    return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!y || !aligned(y, es) || !weights || !aligned(weights, 4) || !out ||
+                       !aligned(out, es) || !aligned(residual, es)))
+    return GPTQ_ERR_INVALID_ARG;
+  if (top_k > kMaxTopK || d > kFp8MaxWidth || n_tokens > kFp8MaxRows / top_k) return GPTQ_ERR_UNSUPPORTED;
+  return launch_moe_combine(y, dtype, ldy, n_tokens, top_k, d, weights, residual, ldr, out, ldo,
+                            (cudaStream_t)stream);
 }
 
 // What the two cache calls share; `ok` = valid, UNSUPPORTED for sizes outside the limits.

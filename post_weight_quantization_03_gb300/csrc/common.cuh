@@ -268,6 +268,46 @@ size_t fp8_matmul_ws_bytes(int64_t M, int64_t N, int64_t K);
 gptq_status launch_fp8_matmul(const Fp8MatmulArgs &g, void *ws, cudaStream_t s);
 gptq_status fp8_matmul_take_timeout(int *out, cudaStream_t s);  // since it was last asked for
 
+// fp8_linear.cu: products with an epilogue, of one matrix or of one for each expert (gptq_fp8_linear,
+// gptq_fp8_gated, gptq_fp8_experts, gptq_fp8_experts_gated)
+struct Fp8LinearArgs {
+  const uint8_t *a; int64_t lda;     // [a_rows, K] codes
+  const uint8_t *ae; int64_t ldae;   // [a_rows, ceil(K / 128)] exponents
+  const float *ra;                   // [a_rows] row scale or null
+  int64_t a_rows;
+  gptq_fp8_weights w[2];             // [N, K]; gated: the gate and what it multiplies
+  bool gated;
+  int act;
+  const void *residual; int64_t ldr;
+  int64_t M, N, K;                   // M: rows of the output
+  void *out; int odtype; int64_t ldo;   // gated: codes
+  uint8_t *oe; int64_t ldoe;            // gated: exponents
+  int n_experts;                     // 0: one matrix, position p is row p of A and of the output
+  const int32_t *offsets;            // [n_experts + 1]: positions where each expert's rows begin
+  const int32_t *order;              // [M]: gated: of a position, A's row * top_k + ..; else the output's row
+  int top_k;
+  uint64_t wait_ns = tc::kWaitNs;
+  int64_t lost = -1;                 // test hook: a copy of each CTA that is left out
+};
+size_t fp8_linear_ws_bytes(int64_t rows, int64_t N, int64_t K);
+gptq_status launch_fp8_linear(const Fp8LinearArgs &g, void *ws, cudaStream_t s);
+gptq_status fp8_linear_take_timeout(int *out, cudaStream_t s);
+
+// moe.cu: routing to experts, and the weighted sum of what they give
+struct MoeRouteArgs {
+  const void *logits; int dtype; int64_t ld;
+  int64_t n_tokens; int n_experts, top_k;
+  const float *bias;
+  int sigmoid, groups, top_groups, group_top, renormalize;
+  float scale;
+  int32_t *ids; float *weights; int32_t *offsets, *order;
+};
+size_t moe_route_ws_bytes(int64_t n_tokens, int n_experts, int top_k);
+gptq_status launch_moe_route(const MoeRouteArgs &g, void *ws, cudaStream_t s);
+gptq_status launch_moe_combine(const void *y, int dtype, int64_t ldy, int64_t n_tokens, int top_k,
+                               int64_t d, const float *weights, const void *residual, int64_t ldr,
+                               void *out, int64_t ldo, cudaStream_t s);
+
 // kv8_append.cu, kv8_attention.cu: the 8-bit cache (gptq_kv8_append, gptq_kv8_attention)
 struct Kv8AppendArgs {
   const void *new_k, *new_v; int dtype;      // [n_seq, n_new, n_kv, dim], element strides below
