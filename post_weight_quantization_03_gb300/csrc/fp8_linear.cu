@@ -1,88 +1,736 @@
 // Block-scaled e4m3 products with an epilogue, of one weight matrix or of one for each expert:
 //   out = act(ra rw (A W^T) + bias) + residual                       (16 bits)
 //   v = act(G) * U, G and U two such products of one A               (e4m3 codes by 1 x 128 blocks)
-// Plain kernel: a CTA takes one position and 128 columns, a thread one column.
+//
+// The tile and the roles are those of the plain product (fp8_matmul.cu): the weights' 128 rows are
+// the MMA's M, up to `tn` tokens its N, both block scales are applied in the tensor core.
+//
+//   warp 0     : TMA producer: (gate, up, tokens) of 128 bytes x rows per k-block
+//   warp 1     : TMEM allocator + MMA issuer (one lane)
+//   warps 2..5 : epilogue, one weight row per thread
+//   warp 6     : scales
+//
+// Gated: a tile has 128 rows of both weights and two accumulators, so the 128 outputs that share an
+// exponent are one column of the tile: a maximum over each warp (redux) and one over the four.
+//
+// Experts: a tile is (expert, up to tn of its positions, 128 weight rows).  Each CTA counts the
+// tiles from the offsets by itself.  The gated product takes its token rows by index, four to a TMA
+// gather; the other takes them as they lie and stores each where the order says, so that neither
+// the rows nor the results are moved by a kernel of their own.
+//
+// Few tokens leave few tiles; the k-blocks of a tile are then split over a cluster of up to 8
+// CTAs, whose partial sums meet through distributed shared memory in rank order.
+#include <cudaTypedefs.h>
 #include <math.h>
 
-#include <type_traits>
-
-#include "fp8.cuh"
+#include "mx.cuh"
+#include "per_device.cuh"
 
 namespace gptq {
 
 namespace {
 
-constexpr int BM = 128;
+using mx::BK;
+using mx::BM;
+using mx::copy_scales;
+using mx::ld_cluster_f32x4;
+using mx::out_f32;
+
+constexpr int kThreads = 224;
+constexpr int kMaxTn = 240;
+constexpr int kMaxTnGated = 112;            // two accumulators, for this tile and the next
+constexpr int kScaleStages = 4;             // groups of four k-blocks in flight
+constexpr uint32_t kScaleBytes = 4 * 512;   // weights, second weights, tokens 0..127, tokens 128..239
+constexpr uint32_t kScaleCols = 16;         // TMEM columns of one group
+constexpr int kMaxStages = 12;
+constexpr int kMaxExperts = 1024;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kRingBytes = 192 * 1024;
+constexpr size_t kSmemBesides = 1024 + kScaleStages * kScaleBytes + kMaxTn * 8 + 2 * 4 * 32 * 4 + 512;
+constexpr size_t kPlanBytes = 2 * (kMaxExperts + 4) * sizeof(int);
+static_assert(2 * kMaxTn + 2 * kScaleCols <= kTmemCols, "TMEM columns");
+static_assert(4 * kMaxTnGated + 2 * kScaleCols <= kTmemCols, "TMEM columns");
+static_assert(kRingBytes + kSmemBesides + kPlanBytes <= 227 * 1024, "shared memory");
+
+struct Params {
+  const uint8_t *ae; int64_t ldae;
+  const float *ra;
+  const uint8_t *we[2]; int64_t ldwe[2], next_we[2];
+  const float *rw[2], *bias[2];
+  const void *residual; int64_t ldr;
+  void *out; int64_t ldo;
+  uint8_t *oe; int64_t ldoe;
+  int64_t a_rows, M, N;
+  int act;
+  int kb;               // k-blocks
+  int tn, stages;
+  int n_w, n_m;         // tiles along the weights; along the tokens (not of experts)
+  int splits;           // CTAs of a cluster that share a tile's k-blocks
+  int acc_cols;         // columns of an accumulator
+  int buffers;          // sets of accumulators
+  int tmem_cols;
+  const int32_t *offsets, *order;
+  int n_experts, top_k;
+  uint64_t wait_ns;
+  int lost;             // test hook: this copy of the producer's is left out
+};
 
 __device__ int g_gave_up;  // a wait ran out since it was last asked for
 
-__device__ __forceinline__ float activate(float x, int act) {
-  switch (act) {
-    case GPTQ_ACT_RELU: return x < 0.0f ? 0.0f : x;
-    case GPTQ_ACT_SILU: return x / (1.0f + expf(-x));
-    case GPTQ_ACT_GELU: return 0.5f * x * (1.0f + erff(x * 0.70710678f));
-    default: return x;
+// (1 + exp(-x) overflows, or passes 2^126, only where x / that is below 2^-119 or so: 0)
+__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
+__device__ __forceinline__ float gelu(float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678f)); }
+__device__ __forceinline__ float relu(float x) { return x < 0.0f ? 0.0f : x; }
+template <int N>
+__device__ __forceinline__ void activate(float (&x)[N], int act) {
+  if (act == GPTQ_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = silu(x[i]);
+  } else if (act == GPTQ_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = gelu(x[i]);
+  } else if (act == GPTQ_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = relu(x[i]);
   }
 }
 
-// Where expert e's positions end, limited and increasing.
-__device__ __forceinline__ int64_t ends(const Fp8LinearArgs &g, int e) {
-  int64_t most = 0;
-  for (int i = 0; i <= e; ++i) most = max(most, (int64_t)g.offsets[i + 1]);
-  return min(most, g.M);
+// k-blocks of this CTA: rank r of the cluster takes an even share of the groups of four.
+__device__ __forceinline__ void k_range(const Params &p, int rank, int &k0, int &k1) {
+  const int groups = (p.kb + 3) / 4;
+  k0 = groups * rank / p.splits * 4;
+  k1 = min(groups * (rank + 1) / p.splits * 4, p.kb);
 }
 
-template <typename TO>
-__global__ void __launch_bounds__(BM) plain_kernel(Fp8LinearArgs g) {
-  __shared__ float part[BM / 32];
-  const int64_t n_w = ceil_div(g.N, (int64_t)BM), pos = blockIdx.x / n_w, nb = blockIdx.x % n_w;
-  const int64_t n = nb * BM + threadIdx.x;
-  int64_t e = 0, row = pos, out_row = pos;
-  if (g.n_experts > 0) {
-    for (e = 0; e < g.n_experts && pos >= ends(g, (int)e); ++e) {}
-    if (e == g.n_experts || pos < min(max(g.offsets[0], 0), (int)g.M)) return;
-    const int64_t o = g.order[pos];
-    if (g.gated) row = o < 0 ? -1 : o / g.top_k;
-    else out_row = o;
-    if (row >= g.a_rows) row = -1;
-    if (out_row < 0 || out_row >= g.M) return;
+// Where the experts' positions and tiles begin, in shared memory.
+struct Plan {
+  int *at;      // [n_experts + 1] positions
+  int *tiles;   // [n_experts + 1] tiles of tn positions
+};
+
+struct Tile {
+  int e, n;             // expert; tile along the weights
+  int m0, cols;         // positions
+};
+
+template <bool EXPERTS>
+__device__ __forceinline__ Tile tile_of(const Params &p, const Plan &plan, int t) {
+  Tile r;
+  r.n = t % p.n_w;
+  const int m = t / p.n_w;
+  if constexpr (EXPERTS) {
+    int lo = 0, hi = p.n_experts;   // tiles[lo] <= m < tiles[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (plan.tiles[mid] <= m) lo = mid;
+      else hi = mid;
+    }
+    r.e = lo;
+    r.m0 = plan.at[lo] + (m - plan.tiles[lo]) * p.tn;
+    r.cols = min(plan.at[lo + 1] - r.m0, p.tn);
+  } else {
+    r.e = 0;
+    r.m0 = m * p.tn;
+    r.cols = (int)min(p.M - r.m0, (int64_t)p.tn);
   }
-  float acc[2] = {0.0f, 0.0f};
-  if (n < g.N && row >= 0) {
-    for (int j = 0; j < (g.gated ? 2 : 1); ++j) {
-      const uint8_t *w = g.w[j].codes + e * g.w[j].next_codes + n * g.w[j].ld;
-      const uint8_t *we = g.w[j].exps + e * g.w[j].next_exps + nb * g.w[j].ld_exps;
-      for (int64_t kb = 0; kb * BM < g.K; ++kb) {
-        float s = 0.0f;
-        for (int64_t k = kb * BM; k < min(g.K, (kb + 1) * BM); ++k)
-          s = fmaf(fp8::unpack1(g.a[row * g.lda + k]), fp8::unpack1(w[k]), s);
-        acc[j] = fmaf(s, fp8::exp_value(g.ae[row * g.ldae + kb]) * fp8::exp_value(we[kb]), acc[j]);
+  return r;
+}
+
+// A's row of a position, a_rows (read as zeros) for none.
+template <bool GATHER>
+__device__ __forceinline__ int a_row(const Params &p, int pos) {
+  if constexpr (GATHER) {
+    const int o = p.order[pos], row = o < 0 ? -1 : o / p.top_k;
+    return row >= 0 && row < p.a_rows ? row : (int)p.a_rows;
+  }
+  return pos;
+}
+
+// One warp: the plan from the offsets, which are limited to [0, M] and read as increasing.
+__device__ __forceinline__ void make_plan(const Params &p, const Plan &plan, int lane) {
+  const int each = (p.n_experts + 31) / 32, e0 = lane * each;
+  const int most = (int)p.M;
+  int top = 0;   // the largest offset up to this lane's last expert
+  for (int i = 0; i < each; ++i)
+    if (e0 + i <= p.n_experts) top = max(top, min(plan.at[e0 + i], most));
+  int run = top;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run = max(run, v);
+  }
+  int at = __shfl_up_sync(0xffffffffu, run, 1);
+  if (lane == 0) at = 0;
+  const int all = max(__shfl_sync(0xffffffffu, run, 31), min(plan.at[p.n_experts], most));
+  for (int i = 0; i < each; ++i)
+    if (e0 + i < p.n_experts) plan.at[e0 + i] = at = max(at, min(plan.at[e0 + i], most));
+  __syncwarp();
+  if (lane == 0) plan.at[p.n_experts] = all;
+  __syncwarp();
+  int mine = 0;
+  for (int i = 0; i < each; ++i)
+    if (e0 + i < p.n_experts) mine += (plan.at[e0 + i + 1] - plan.at[e0 + i] + p.tn - 1) / p.tn;
+  int sum = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  int tiles = sum - mine;
+  for (int i = 0; i < each; ++i)
+    if (e0 + i < p.n_experts) {
+      plan.tiles[e0 + i] = tiles;
+      tiles += (plan.at[e0 + i + 1] - plan.at[e0 + i] + p.tn - 1) / p.tn;
+    }
+  if (lane == 31) plan.tiles[p.n_experts] = sum;
+}
+
+// TO: type of the output, if it is not gated.
+template <typename TO, bool GATED, bool EXPERTS>
+__global__ void __launch_bounds__(kThreads, 1)
+linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ CUtensorMap mw1,
+              const __grid_constant__ CUtensorMap ma, Params p, DevStatus *st) {
+  constexpr int W = GATED ? 2 : 1;
+  constexpr bool GATHER = GATED && EXPERTS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *sscale = ring + kRingBytes;
+  float *sra = (float *)(sscale + kScaleStages * kScaleBytes);   // of each token: factor,
+  int *srow = (int *)(sra + kMaxTn);                             // row of the output (-1: none)
+  float *smax = (float *)(srow + kMaxTn);                        // [2][4 warps][32 tokens]
+  uint64_t *full = (uint64_t *)(smax + 2 * 4 * 32);
+  uint64_t *empty = full + kMaxStages;
+  uint64_t *sfull = empty + kMaxStages;
+  uint64_t *sempty = sfull + kScaleStages;
+  uint64_t *tfull = sempty + kScaleStages;
+  uint64_t *tempty = tfull + 2;
+  uint64_t *mdone = tempty + 2;       // every MMA has completed
+  uint32_t *tmem_slot = (uint32_t *)(mdone + 1);
+  Plan plan{(int *)(tmem_slot + 4), (int *)(tmem_slot + 4) + kMaxExperts + 4};
+  const tc::Waits waits{st, &g_gave_up, p.wait_ns};
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+  const uint32_t stage_bytes = (uint32_t)(W * BM + p.tn) * BK;
+  const int rank = p.splits > 1 ? (int)tc::cluster_ctarank() : 0;
+  const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
+  int k0, k1;
+  k_range(p, rank, k0, k1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kScaleStages; ++s) {
+      tc::mbar_init(&sfull[s], 32);
+      tc::mbar_init(&sempty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&tfull[b], 1);
+      tc::mbar_init(&tempty[b], 4);
+    }
+    tc::mbar_init(mdone, 1);
+    tc::mbar_fence_init();
+  }
+  if (warp == 1) tc::tmem_alloc(tmem_slot, p.tmem_cols);
+  if constexpr (EXPERTS) {
+    wait_for_grids();
+    for (int e = threadIdx.x; e <= p.n_experts; e += kThreads) plan.at[e] = p.offsets[e];
+    __syncthreads();
+    if (warp == 0) make_plan(p, plan, lane);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if constexpr (!EXPERTS) wait_for_grids();
+  launch_dependents();
+  // The status of the call.  A wait that gives up writes it two seconds or more after its own
+  // CTA started, so this store, by the first CTA to start, comes first.
+  if (blockIdx.x == 0 && threadIdx.x == 0) st->status = 0;
+  const int n_tiles = p.n_w * (EXPERTS ? plan.tiles[p.n_experts] : p.n_m);
+  const uint32_t set_cols = (uint32_t)(W * p.acc_cols);          // accumulators of a tile
+  const uint32_t sc_cols = tmem + (uint32_t)p.buffers * set_cols;
+
+  bool ok = true;                   // false once a wait has given up: the role ends
+  int s = 0, n = 0;                 // producer and issuer: stage of the ring; copies
+  uint32_t ph = 1;
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    // (a whole warp: its lanes issue the gathers; the other copies one lane)
+    const bool elected = tc::elect_one();
+    if (elected) {
+      tc::tma_prefetch_desc(&mw0);
+      if constexpr (GATED) tc::tma_prefetch_desc(&mw1);
+      tc::tma_prefetch_desc(&ma);
+    }
+    for (int t = first; t < n_tiles && ok; t += step) {
+      const Tile tile = tile_of<EXPERTS>(p, plan, t);
+      // rows that the MMA reads: of experts, whole groups of 16
+      const int rows = EXPERTS ? (tile.cols + 15) / 16 * 16 : p.tn;
+      int row[2][4];
+      if constexpr (GATHER) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = (lane + 32 * h) * 4 + i;
+            row[h][i] = j < tile.cols ? a_row<true>(p, tile.m0 + j) : (int)p.a_rows;
+          }
+      }
+      const uint32_t bytes = (uint32_t)(W * BM + rows) * BK;
+      for (int kb = k0; kb < k1; ++kb) {
+        ok = tc::mbar_wait_compact(&empty[s], ph, waits);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        uint8_t *base = ring + s * stage_bytes;
+        if (elected) {
+          // (a lost copy is one whose last bytes never arrive)
+          tc::mbar_arrive_expect_tx(&full[s], bytes + (n == p.lost ? 16u : 0u));
+          tc::tma_load_3d(base, &mw0, kb * BK, tile.n * BM, tile.e, &full[s]);
+          if constexpr (GATED) tc::tma_load_3d(base + BM * BK, &mw1, kb * BK, tile.n * BM, tile.e, &full[s]);
+          if constexpr (!EXPERTS) {
+            tc::tma_load_2d(base + W * BM * BK, &ma, kb * BK, tile.m0, &full[s]);
+          } else if constexpr (!GATHER) {
+            for (int j = 0; j < rows; j += 16)
+              tc::tma_load_2d(base + (W * BM + j) * BK, &ma, kb * BK, tile.m0 + j, &full[s]);
+          }
+        }
+        if constexpr (GATHER) {
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if ((lane + 32 * h) * 4 < rows)
+              tc::tma_gather4(base + (W * BM + (lane + 32 * h) * 4) * BK, &ma, kb * BK, row[h][0], row[h][1],
+                              row[h][2], row[h][3], &full[s]);
+        }
+        ++n;
+        if (++s == p.stages) s = 0, ph ^= 1;
       }
     }
+  } else if (warp == 1 && tc::elect_one()) {
+    // ---------------- MMA issuer ----------------
+    const uint32_t ring0 = (tc::smem_u32(ring) >> 4) | (1u << 16), stage16 = stage_bytes >> 4;
+    const uint32_t sc0 = tc::smem_u32(sscale);
+    int g = 0, it = 0;
+    uint32_t at = ring0;            // lower word of the stage's first descriptor
+    ph = 0;
+#pragma unroll 1
+    for (int t = first; t < n_tiles && ok; t += step, ++it) {
+      const int b = p.buffers > 1 ? it & 1 : 0, use = p.buffers > 1 ? it >> 1 : it;
+      const int rows = EXPERTS ? (tile_of<EXPERTS>(p, plan, t).cols + 15) / 16 * 16 : p.tn;
+      const uint32_t idesc = mx::instr_desc(rows);
+      ok = tc::mbar_wait_compact(&tempty[b], (use & 1) ^ 1, waits);
+      if (!ok) break;
+      tc::tc_fence_after();
+      const uint32_t acc = tmem + b * set_cols;
+#pragma unroll 1
+      for (int kb = k0; kb < k1 && ok; kb += 4, ++g) {
+        const int q = g % kScaleStages;
+        ok = tc::mbar_wait_compact(&sfull[q], (g / kScaleStages) & 1, waits);
+        if (!ok) break;
+        tc::tc_fence_after();
+        // two groups of columns in turn: the scale warp's ring keeps a third group's copy from
+        // starting before the first group's MMAs have completed
+        const uint32_t sc = sc_cols + (uint32_t)(g & 1) * kScaleCols, sm = sc0 + q * kScaleBytes;
+        copy_scales(sc, sm);
+        if constexpr (GATED) copy_scales(sc + 4, sm + 512);
+        copy_scales(sc + 8, sm + 1024);
+        if (rows > 128) copy_scales(sc + 12, sm + 1536);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (kb + j >= k1) break;
+          ok = tc::mbar_wait_compact(&full[s], ph, waits);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint32_t id = idesc | ((uint32_t)j << 29) | ((uint32_t)j << 4);
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)
+              mx::mma(acc + w * p.acc_cols, at + (w * BM * BK >> 4) + 2 * kk, at + (W * BM * BK >> 4) + 2 * kk,
+                      id, sc + 4 * w, sc + 8, j > 0 || kk > 0 || kb > k0);
+          tc::mma_commit(&empty[s]);
+          at += stage16;
+          if (++s == p.stages) s = 0, ph ^= 1, at = ring0;
+        }
+        tc::mma_commit(&sempty[q]);
+      }
+      if (ok) tc::mma_commit(&tfull[b]);
+    }
+  } else if (warp == 6) {
+    // ---------------- scales ----------------
+    int g = 0;
+    for (int t = first; t < n_tiles && ok; t += step) {
+      const Tile tile = tile_of<EXPERTS>(p, plan, t);
+      int64_t row[8];               // offsets of the lane's rows (-1: none)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        row[i] = -1;
+        if (lane + 32 * i < tile.cols) {
+          const int r = a_row<GATHER>(p, tile.m0 + lane + 32 * i);
+          if (r < p.a_rows) row[i] = r * p.ldae;
+        }
+      }
+      const uint8_t *we[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) we[w] = p.we[w] + tile.e * p.next_we[w] + tile.n * p.ldwe[w];
+#pragma unroll 1
+      for (int sb = k0 / 4; 4 * sb < k1; ++sb, ++g) {
+        uint32_t word[8], ww[W];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          word[i] = row[i] >= 0 ? *reinterpret_cast<const uint32_t *>(p.ae + row[i] + 4 * sb) : 0x7F7F7F7Fu;
+#pragma unroll
+        for (int w = 0; w < W; ++w) ww[w] = *reinterpret_cast<const uint32_t *>(we[w] + 4 * sb);
+        const int q = g % kScaleStages;
+        // two TMEM groups: wait for the MMAs of two groups back, not only for this slot's
+        if (g >= 2) ok = tc::mbar_wait_compact(&sempty[(g - 2) % kScaleStages], ((g - 2) / kScaleStages) & 1, waits);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        uint4 *dst = reinterpret_cast<uint4 *>(sscale + q * kScaleBytes) + lane;
+#pragma unroll
+        for (int w = 0; w < W; ++w) dst[32 * w] = make_uint4(ww[w], ww[w], ww[w], ww[w]);
+        dst[64] = make_uint4(word[0], word[1], word[2], word[3]);
+        dst[96] = make_uint4(word[4], word[5], word[6], word[7]);
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(&sfull[q]);
+      }
+    }
+  } else if (warp >= 2 && warp < 6) {
+    // ---------------- epilogue ----------------
+    const int q = warp & 3, lrow = q * 32 + lane, et = threadIdx.x - 64;
+    int it = 0, turn = 0;
+    for (int t = first; t < n_tiles; t += step, ++it) {
+      const int b = p.buffers > 1 ? it & 1 : 0, use = p.buffers > 1 ? it >> 1 : it;
+      const Tile tile = tile_of<EXPERTS>(p, plan, t);
+      const int64_t nn = (int64_t)tile.n * BM + lrow;
+      const bool in = nn < p.N;
+      if (p.splits == 1) {
+        tc::named_barrier(2, 128);  // the previous tile's factors have been read
+        for (int j = et; j < tile.cols; j += 128) {
+          const int pos = tile.m0 + j, r = a_row<GATHER>(p, pos);
+          sra[j] = p.ra && r < p.a_rows ? p.ra[r] : 1.0f;
+          if constexpr (EXPERTS && !GATED) {
+            const int o = p.order[pos];
+            srow[j] = o >= 0 && o < p.M ? o : -1;
+          }
+        }
+      }
+      float rw[W], bias[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const int64_t at = (int64_t)tile.e * p.N + nn;
+        rw[w] = p.rw[w] && in ? p.rw[w][at] : 1.0f;
+        bias[w] = p.bias[w] && in ? p.bias[w][at] : 0.0f;
+      }
+      ok = tc::mbar_wait_compact(&tfull[b], use & 1, waits);
+      if (!tc::named_barrier_and(1, 128, ok)) break;
+      tc::tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * set_cols;
+#pragma unroll 1
+      for (int c = 0; c < tile.cols; c += 32) {
+        uint32_t r[W][32];
+#pragma unroll
+        for (int w = 0; w < W; ++w) tc::tmem_ld32(acc + w * p.acc_cols + (uint32_t)c, r[w]);
+        if (p.splits > 1) {
+          tc::tmem_ld_wait();
+          float *part = (float *)ring + lrow;
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c + i < p.tn) part[(w * p.tn + c + i) * BM] = __uint_as_float(r[w][i]);
+          continue;
+        }
+        float v[32];
+        if constexpr (!GATED) {
+          TO res[32];
+          if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              res[i] = in && c + i < tile.cols ? ((const TO *)p.residual)[(int64_t)(tile.m0 + c + i) * p.ldr + nn] : out_f32<TO>(0.0f);
+          }
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(r[0][i]) * rw[0], sra[(c + i) % kMaxTn], bias[0]);
+          activate(v, p.act);
+          if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += to_f32(res[i]);
+          }
+          if (in) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (c + i >= tile.cols) break;
+              const int64_t row = EXPERTS ? srow[c + i] : tile.m0 + c + i;
+              if (!EXPERTS || row >= 0) ((TO *)p.out)[row * p.ldo + nn] = out_f32<TO>(v[i]);
+            }
+          }
+        } else {
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(r[0][i]) * rw[0], sra[(c + i) % kMaxTn], bias[0]);
+          activate(v, p.act);
+          float *sm = smax + (turn++ & 1) * 128;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[i] *= fmaf(__uint_as_float(r[1][i]) * rw[1], sra[(c + i) % kMaxTn], bias[1]);
+            const uint32_t most = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(fp8::finite_abs(v[i])) : 0u);
+            if (lane == i) sm[q * 32 + i] = __uint_as_float(most);
+          }
+          tc::named_barrier(3, 128);
+          // this lane has token c + lane's exponent
+          const float most = fmaxf(fmaxf(sm[lane], sm[32 + lane]), fmaxf(sm[64 + lane], sm[96 + lane]));
+          const int ex = fp8::block_exponent(most);
+          if (q == 0 && c + lane < tile.cols)
+            p.oe[(int64_t)(tile.m0 + c + lane) * p.ldoe + tile.n] = (uint8_t)(ex + fp8::kBias);
+          uint8_t *o = (uint8_t *)p.out + (int64_t)(tile.m0 + c) * p.ldo + nn;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float s0 = fp8::pow2(-__shfl_sync(0xffffffffu, ex, i)), s1 = fp8::pow2(-__shfl_sync(0xffffffffu, ex, i + 1));
+            const uint32_t two = fp8::pack2(fp8::inf_to_nan(v[i]) * s0, fp8::inf_to_nan(v[i + 1]) * s1);
+            if (in && c + i < tile.cols) o[i * p.ldo] = (uint8_t)two;
+            if (in && c + i + 1 < tile.cols) o[(i + 1) * p.ldo] = (uint8_t)(two >> 8);
+          }
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&tempty[b]);
+    }
   }
-  const float ra = g.ra && row >= 0 ? g.ra[row] : 1.0f;
-  float v[2];
-  for (int j = 0; j < (g.gated ? 2 : 1); ++j) {
-    const int64_t at = e * g.N + n;
-    v[j] = acc[j] * (g.w[j].scale && n < g.N ? g.w[j].scale[at] : 1.0f) * ra;
-    if (g.w[j].bias && n < g.N) v[j] += g.w[j].bias[at];
+  __syncwarp();
+  tc::tc_fence_before();
+  if (!__syncthreads_and(ok)) {
+    // A wait has given up: what is in flight gets one more, bounded, to land or to complete before
+    // the CTA leaves and the TMEM is released.
+    if (warp == 0 && tc::elect_one()) {
+      // stages before s are of this round of the ring, the others of the one before
+#pragma unroll 1
+      for (int i = 0; i < (n < p.stages ? s : p.stages); ++i)
+        tc::mbar_wait_compact(&full[i], i < s ? ph ^ 1 : ph, waits);
+    } else if (warp == 1 && tc::elect_one()) {
+      tc::mma_commit(mdone);
+      tc::mbar_wait_compact(mdone, 0, waits);
+    }
+    __syncwarp();
   }
-  float x = activate(v[0], g.act);
-  if (!g.gated) {
-    if (n >= g.N) return;
-    if (g.residual) x += to_f32(((const TO *)g.residual)[out_row * g.ldr + n]);
-    ((TO *)g.out)[out_row * g.ldo + n] = fp8::from_f32<TO>(x);
-    return;
+  if (warp == 1) tc::tmem_dealloc(tmem, p.tmem_cols);
+  if (p.splits > 1) {
+    // one tile per cluster: the ring holds this CTA's partial sums [W][tn][128]
+    tc::cluster_sync();
+    if (first < n_tiles) {
+      const Tile tile = tile_of<EXPERTS>(p, plan, first);
+      // this CTA's columns are rank, rank + splits, ...; a warp takes one, a lane four rows of it
+      const uint32_t base = tc::smem_u32(ring) + lane * 16;
+      const int64_t nn = (int64_t)tile.n * BM + lane * 4;
+      float rw[W][4], bias[W][4];
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t at = (int64_t)tile.e * p.N + nn + j;
+          rw[w][j] = p.rw[w] && nn + j < p.N ? p.rw[w][at] : 1.0f;
+          bias[w][j] = p.bias[w] && nn + j < p.N ? p.bias[w][at] : 0.0f;
+        }
+      const bool pairs = (p.ldo & 1) == 0 && ((uintptr_t)p.out & 3) == 0 && nn + 3 < p.N;
+#pragma unroll 1
+      for (int col = rank + warp * p.splits; col < tile.cols; col += kThreads / 32 * p.splits) {
+        const int pos = tile.m0 + col, r = a_row<GATHER>(p, pos);
+        const float ra = p.ra && r < p.a_rows ? p.ra[r] : 1.0f;
+        int64_t row = pos;
+        if constexpr (EXPERTS && !GATED) row = p.order[pos] >= 0 && p.order[pos] < p.M ? p.order[pos] : -1;
+        TO res[4];
+        if constexpr (!GATED)
+          if (p.residual) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              res[j] = nn + j < p.N ? ((const TO *)p.residual)[row * p.ldr + nn + j] : out_f32<TO>(0.0f);
+          }
+        float x[W][4];
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const uint32_t off = base + (uint32_t)(w * p.tn + col) * BM * 4;
+          float4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[i] = i < p.splits ? ld_cluster_f32x4(tc::mapa_shared(off, (uint32_t)i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          float4 sum = v[0];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) {
+            sum.x += v[i].x;
+            sum.y += v[i].y;
+            sum.z += v[i].z;
+            sum.w += v[i].w;
+          }
+          x[w][0] = fmaf(sum.x * rw[w][0], ra, bias[w][0]);
+          x[w][1] = fmaf(sum.y * rw[w][1], ra, bias[w][1]);
+          x[w][2] = fmaf(sum.z * rw[w][2], ra, bias[w][2]);
+          x[w][3] = fmaf(sum.w * rw[w][3], ra, bias[w][3]);
+        }
+        activate(x[0], p.act);
+        if constexpr (GATED) {
+          float most = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[0][j] *= x[1][j];
+            if (nn + j < p.N) most = fmaxf(most, fp8::finite_abs(x[0][j]));
+          }
+          most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+          const int ex = fp8::block_exponent(most);
+          const float sc = fp8::pow2(-ex);
+          const uint32_t four = fp8::pack4(fp8::inf_to_nan(x[0][0]) * sc, fp8::inf_to_nan(x[0][1]) * sc,
+                                           fp8::inf_to_nan(x[0][2]) * sc, fp8::inf_to_nan(x[0][3]) * sc);
+          uint8_t *dst = (uint8_t *)p.out + row * p.ldo + nn;   // (rows are 16-byte aligned)
+          if (nn + 3 < p.N) {
+            *reinterpret_cast<uint32_t *>(dst) = four;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (nn + j < p.N) dst[j] = (uint8_t)(four >> (8 * j));
+          }
+          if (lane == 0) p.oe[row * p.ldoe + tile.n] = (uint8_t)(ex + fp8::kBias);
+        } else if (row >= 0) {
+          alignas(8) TO o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = out_f32<TO>(p.residual ? x[0][j] + to_f32(res[j]) : x[0][j]);
+          TO *dst = (TO *)p.out + row * p.ldo + nn;
+          if (pairs) {
+            reinterpret_cast<uint32_t *>(dst)[0] = reinterpret_cast<const uint32_t *>(o)[0];
+            reinterpret_cast<uint32_t *>(dst)[1] = reinterpret_cast<const uint32_t *>(o)[1];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (nn + j < p.N) dst[j] = o[j];
+          }
+        }
+      }
+    }
+    tc::cluster_sync();  // the others have read this CTA's sums
   }
-  x = n < g.N ? x * v[1] : 0.0f;
-  float most = fp8::finite_abs(x);
-  for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = most;
-  __syncthreads();
-  for (int i = 0; i < BM / 32; ++i) most = fmaxf(most, part[i]);
-  const int ex = fp8::block_exponent(most);
-  if (n < g.N) ((uint8_t *)g.out)[pos * g.ldo + n] = (uint8_t)fp8::pack2(fp8::inf_to_nan(x) * fp8::pow2(-ex), 0.0f);
-  if (threadIdx.x == 0) g.oe[pos * g.ldoe + nb] = (uint8_t)(ex + fp8::kBias);
+}
+
+size_t smem_bytes(bool experts) { return kRingBytes + kSmemBesides + (experts ? kPlanBytes : 0); }
+
+// Clusters of `splits` CTAs, one on an SM, that run at once.  They lie within groups of SMs, so
+// there is room for fewer than SMs / splits.
+template <typename TO, bool GATED, bool EXPERTS>
+int clusters_at_once(int dev, int splits, int sms) {
+  static PerDevice<9> known;
+  return known.get(dev, splits, [splits, sms]() {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(splits * sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes(EXPERTS);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, (const void *)linear_kernel<TO, GATED, EXPERTS>, &cfg) == cudaSuccess) return n;
+    (void)cudaGetLastError();
+    return 0;
+  }, sms / splits * 7 / 8);
+}
+
+// Tile of tokens and splits of K: the least of an estimate in SM cycles, as for the plain product:
+// a k-block of a tile takes the MMAs' time or that of their issue, the memory brings each operand once
+// at 3500 bytes a cycle, L2 what the tiles fill again.  Of experts the number of tiles is not known
+// here: as many as if the rows were dealt evenly, or what there can be at most where K is split (one
+// tile a cluster).
+struct Shape { int tn, splits; };
+
+template <typename TO, bool GATED, bool EXPERTS>
+Shape choose(const Fp8LinearArgs &g, int dev, int sms) {
+  constexpr int W = GATED ? 2 : 1;
+  const int64_t n_w = ceil_div(g.N, (int64_t)BM), groups = ceil_div(ceil_div(g.K, (int64_t)BK), (int64_t)4);
+  const int most = GATED ? kMaxTnGated : kMaxTn;
+  // matrices in use, and rows of each
+  const double used = EXPERTS ? g.n_experts * (1.0 - pow(1.0 - 1.0 / g.n_experts, (double)g.M)) : 1.0;
+  const double rows = g.M / used;
+  const double once = ((double)g.M + W * used * g.N) * g.K / 3500.0;
+  Shape best{16, 1};
+  double best_t = 1e30;
+  for (int tn = 16; tn <= most; tn += 16) {
+    if (!EXPERTS && tn - 16 >= g.M) break;
+    const double per = EXPERTS ? rows / tn + 0.5 : (double)ceil_div(g.M, (int64_t)tn);   // tiles along the tokens
+    const double tiles = n_w * used * (per < 1.0 ? 1.0 : per);
+    const int64_t at_most = n_w * (EXPERTS ? (g.n_experts < g.M ? g.n_experts : g.M) + g.M / tn : ceil_div(g.M, (int64_t)tn));
+    const double mma = W * 3.45 * tn, issue = 300 + W * 1.7 * tn;
+    const double c = mma > issue ? mma : issue;
+    const double fill = tiles * g.K * (W * BM + tn) / 20000.0;
+    for (int s = 1; s <= 8 && s <= groups; ++s) {
+      if (s > 1 && (at_most > clusters_at_once<TO, GATED, EXPERTS>(dev, s, sms) ||
+                    (uint32_t)(W * tn * BM * 4) > kRingBytes))
+        continue;
+      const double busy = ceil(tiles * s / sms);
+      const double work = busy * 4 * ceil_div(groups, (int64_t)s) * c;
+      double t = sqrt(work * work + (once + fill) * (once + fill));
+      t += 6400.0 + (s > 1 ? 1400.0 + 8.0 * W * tn : 0.0) + 800.0 * (busy - 1);
+      if (t < best_t) best_t = t, best = Shape{tn, s};
+    }
+  }
+  return best;
+}
+
+template <typename TO, bool GATED, bool EXPERTS>
+gptq_status run(const Fp8LinearArgs &g, DevStatus *st, cudaStream_t s) {
+  constexpr int W = GATED ? 2 : 1;
+  GPTQ_TRY(ensure_smem_attr((const void *)linear_kernel<TO, GATED, EXPERTS>, (int)smem_bytes(EXPERTS)));
+  int sms = 0, dev = -1;
+  GPTQ_TRY(device_sm_count(&sms));
+  GPTQ_CUDA_CHECK(cudaGetDevice(&dev));
+  const Shape sh = choose<TO, GATED, EXPERTS>(g, dev, sms);
+  Params p{};
+  p.ae = g.ae; p.ldae = g.ldae;
+  p.ra = g.ra;
+  for (int w = 0; w < W; ++w) {
+    p.we[w] = g.w[w].exps; p.ldwe[w] = g.w[w].ld_exps; p.next_we[w] = g.w[w].next_exps;
+    p.rw[w] = g.w[w].scale;
+    p.bias[w] = g.w[w].bias;
+  }
+  p.residual = g.residual; p.ldr = g.ldr;
+  p.out = g.out; p.ldo = g.ldo;
+  p.oe = g.oe; p.ldoe = g.ldoe;
+  p.a_rows = g.a_rows; p.M = g.M; p.N = g.N;
+  p.act = g.act;
+  p.kb = (int)ceil_div(g.K, (int64_t)BK);
+  p.tn = sh.tn;
+  p.splits = sh.splits;
+  p.n_w = (int)ceil_div(g.N, (int64_t)BM);
+  p.n_m = (int)ceil_div(g.M, (int64_t)sh.tn);
+  const int64_t along = EXPERTS ? (g.n_experts < g.M ? g.n_experts : g.M) + g.M / sh.tn : p.n_m;
+  const int64_t tiles = p.n_w * along;   // at most
+  if (tiles * 8 > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  p.acc_cols = sh.tn;
+  p.buffers = 2;
+  p.tmem_cols = (int)kTmemCols;
+  p.offsets = g.offsets; p.order = g.order;
+  p.n_experts = g.n_experts; p.top_k = g.top_k;
+  p.wait_ns = g.wait_ns;
+  p.lost = (int)g.lost;
+  const int fit = (int)(kRingBytes / (uint32_t)((W * BM + sh.tn) * BK));
+  p.stages = fit < kMaxStages ? fit : kMaxStages;
+  const int64_t mats = EXPERTS ? g.n_experts : 1;
+  CUtensorMap mw[2], ma;
+  for (int w = 0; w < W; ++w)
+    if (!tc::make_tmap_matrices(&mw[w], g.w[w].codes, mats, g.N, g.K, g.w[w].ld,
+                                mats > 1 ? g.w[w].next_codes : g.N * g.w[w].ld, BM))
+      return GPTQ_ERR_UNSUPPORTED;
+  if (W == 1) mw[1] = mw[0];
+  if (!tc::make_tmap_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, g.a_rows, g.K, g.lda, BK,
+                        !EXPERTS ? sh.tn : GATED ? 1 : 16))
+    return GPTQ_ERR_UNSUPPORTED;
+  const int64_t ctas = sh.splits > 1 ? tiles * sh.splits : (tiles < sms ? tiles : sms);
+  return launch_early(linear_kernel<TO, GATED, EXPERTS>, dim3((unsigned)ctas), dim3(kThreads), smem_bytes(EXPERTS),
+                      sh.splits, s, mw[0], mw[1], ma, p, st);
 }
 
 }  // namespace
@@ -92,13 +740,19 @@ size_t fp8_linear_ws_bytes(int64_t, int64_t, int64_t) { return 256; }
 gptq_status fp8_linear_take_timeout(int *out, cudaStream_t s) { return take_flag(g_gave_up, out, s); }
 
 gptq_status launch_fp8_linear(const Fp8LinearArgs &g, void *ws, cudaStream_t s) {
-  GPTQ_CUDA_CHECK(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s));
-  if (g.M == 0) return GPTQ_OK;
-  const int64_t ctas = g.M * ceil_div(g.N, (int64_t)BM);
-  if (ctas > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-  return !g.gated && g.odtype == GPTQ_F16
-             ? launch_kernel(plain_kernel<__half>, dim3((unsigned)ctas), dim3(BM), 0, s, g)
-             : launch_kernel(plain_kernel<__nv_bfloat16>, dim3((unsigned)ctas), dim3(BM), 0, s, g);
+  if (g.M == 0) {
+    GPTQ_CUDA_CHECK(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s));
+    return GPTQ_OK;
+  }
+  DevStatus *st = (DevStatus *)ws;
+  using Half = __half;
+  using Bf16 = __nv_bfloat16;
+  if (g.n_experts > 0) {
+    if (g.gated) return run<Bf16, true, true>(g, st, s);
+    return g.odtype == GPTQ_F16 ? run<Half, false, true>(g, st, s) : run<Bf16, false, true>(g, st, s);
+  }
+  if (g.gated) return run<Bf16, true, false>(g, st, s);
+  return g.odtype == GPTQ_F16 ? run<Half, false, false>(g, st, s) : run<Bf16, false, false>(g, st, s);
 }
 
 }  // namespace gptq

@@ -29,18 +29,18 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
-#include <type_traits>
-
-#include "fp8.cuh"
+#include "mx.cuh"
 #include "per_device.cuh"
-#include "tc.cuh"
 
 namespace gptq {
 
 namespace {
 
-constexpr int BM = 128;                     // weight rows of a tile
-constexpr int BK = fp8::kBlock;             // 128 codes = 128 bytes = one swizzle row
+using mx::BK;
+using mx::BM;
+using mx::copy_scales;
+using mx::ld_cluster_f32x4;
+using mx::out_f32;
 constexpr int kMaxTn = 240;
 constexpr int kThreads = 224;
 constexpr int kScaleStages = 4;             // groups of four k-blocks in flight
@@ -71,46 +71,6 @@ struct MmParams {
 };
 
 __device__ int g_gave_up;  // a wait ran out since it was last asked for
-
-template <typename TO>
-__device__ __forceinline__ TO out_f32(float x) {
-  if constexpr (std::is_same<TO, __half>::value) return __float2half_rn(x);
-  else return __float2bfloat16_rn(x);
-}
-
-// D[tmem] (+)= (A * 2^sa)(B * 2^sb)^T, one thread; sa, sb: TMEM addresses of the scale columns;
-// the operands' descriptors by their lower words (the upper one is the layout's).
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8 rows on; version; swizzle
-__device__ __forceinline__ void mma_mx(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                       uint32_t sa, uint32_t sb, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 p, %7, 0;\n\t"
-      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
-      "[%0], a, b, %4, [%5], [%6], p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)accumulate)
-      : "memory");
-}
-
-// 512 bytes of shared memory (32 rows of 16 bytes) to 32 lanes x 4 columns, repeated in each of
-// the four lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
-  // no swizzle: 8 rows x 16 bytes contiguous, the next 8 rows 128 bytes on
-  const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)8 << 16) |
-                        ((uint64_t)8 << 32) | ((uint64_t)1 << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-               : "memory");
-}
-
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(caddr)
-               : "memory");
-  return v;
-}
 
 // k-blocks of this CTA: rank r of the cluster takes an even share of the groups of four.
 __device__ __forceinline__ void k_range(const MmParams &p, int rank, int &k0, int &k1) {
@@ -196,8 +156,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
     }
   } else if (warp == 1 && tc::elect_one()) {
     // ---------------- MMA issuer ----------------
-    // kind::mxf8f6f4 instruction descriptor: e4m3 operands, K-major, power-of-two scale bytes
-    const uint32_t idesc = (1u << 23) | ((uint32_t)(p.tn >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+    const uint32_t idesc = mx::instr_desc(p.tn);
     const uint32_t ring0 = (tc::smem_u32(ring) >> 4) | (1u << 16), stage16 = stage_bytes >> 4;
     const uint32_t sc0 = tc::smem_u32(sscale);
     int g = 0, it = 0;
@@ -231,8 +190,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CU
           const uint32_t id = idesc | ((uint32_t)j << 29) | ((uint32_t)j << 4);
 #pragma unroll
           for (int kk = 0; kk < BK / 32; ++kk)
-            mma_mx(acc, at + 2 * kk, at + (BM * BK >> 4) + 2 * kk, id, sc, sc + 4,
-                   j > 0 || kk > 0 || kb > k0);
+            mx::mma(acc, at + 2 * kk, at + (BM * BK >> 4) + 2 * kk, id, sc, sc + 4,
+                    j > 0 || kk > 0 || kb > k0);
           tc::mma_commit(&empty[s]);
           at += stage16;
           if (++s == p.stages) s = 0, ph ^= 1, at = ring0;

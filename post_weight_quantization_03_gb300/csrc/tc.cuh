@@ -146,6 +146,17 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, int
       : "memory");
 }
 
+// Four rows r.. of a tensor map whose box is one row, from column x on, one after another in `dst`.
+// Rows outside the tensor read as zeros.
+__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *m, int32_t x, int32_t r0,
+                                            int32_t r1, int32_t r2, int32_t r3, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)m), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Contiguous global -> shared bulk copy (no tensor map); `bytes` a multiple of 16, both
 // addresses 16-byte aligned; completion counted on `bar`.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
@@ -439,6 +450,11 @@ __host__ __device__ constexpr uint32_t instr_desc(uint32_t a_fmt, uint32_t b_fmt
 // ---------------------------------------------------------------------------------------
 bool make_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, int64_t rows,
                   int64_t cols, int64_t ld_bytes, int box_cols, int box_rows);
+
+// 3D tensor map over n matrices [rows, cols] of bytes with row pitch `ld`, `next` bytes from one to
+// the next, box = 128 columns x box_rows of one matrix, 128-byte swizzle, zero fill.
+bool make_tmap_matrices(CUtensorMap *m, const void *base, int64_t n, int64_t rows, int64_t cols,
+                        int64_t ld, int64_t next, int box_rows);
 
 // 3D tensor map over [n, rows, cols] bytes without gaps, box = one [rows, cols] matrix; cols is 64
 // or 128 and the swizzle is that wide.

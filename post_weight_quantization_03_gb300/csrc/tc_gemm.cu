@@ -492,6 +492,19 @@ bool tc::make_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tc::make_tmap_matrices(CUtensorMap *m, const void *base, int64_t n, int64_t rows, int64_t cols,
+                            int64_t ld, int64_t next, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn || ((uintptr_t)base & 15) || (ld & 15) || (next & 15) || n < 1 || rows < 1 || cols < 1) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
+  cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)next};
+  cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, (void *)base, dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tc::make_tmap_bytes_3d(CUtensorMap *m, const void *base, int64_t n, int rows, int cols) {
   auto fn = encode_fn();
   if (!fn || ((uintptr_t)base & 15) || n < 1 || (cols != 64 && cols != 128)) return false;
