@@ -9,14 +9,21 @@
 //   warp 1     : TMEM allocator + MMA issuer (one lane)
 //   warps 2..5 : epilogue, one weight row per thread
 //   warp 6     : scales
+//   warps 7..10: token rows of the experts' gated product
 //
 // Gated: a tile has 128 rows of both weights and two accumulators, so the 128 outputs that share an
 // exponent are one column of the tile: a maximum over each warp (redux) and one over the four.
 //
 // Experts: a tile is (expert, up to tn of its positions, 128 weight rows).  Each CTA counts the
-// tiles from the offsets by itself.  The gated product takes its token rows by index, four to a TMA
-// gather; the other takes them as they lie and stores each where the order says, so that neither
-// the rows nor the results are moved by a kernel of their own.
+// tiles from the offsets by itself.  The gated product takes its token rows by index, the other takes
+// them as they lie and stores each where the order says, so that neither the rows nor the results
+// are moved by a kernel of their own.  Rows by index are copied by four warps (16 bytes a
+// lane, three k-blocks in flight), which write the swizzle that the MMA reads: TMA's gather of four
+// rows takes about 80 cycles, 2300 for a k-block whose MMAs take 770 (4096 tokens of 64 experts, 4096
+// x 1376: 709 us).
+//
+// An epilogue warp turns its 32 rows by 32 tokens around in shared memory, so that a store writes
+// 64 contiguous bytes of four tokens.
 //
 // Few tokens leave few tiles; the k-blocks of a tile are then split over a cluster of up to 8
 // CTAs, whose partial sums meet through distributed shared memory in rank order.
@@ -37,6 +44,8 @@ using mx::ld_cluster_f32x4;
 using mx::out_f32;
 
 constexpr int kThreads = 224;
+constexpr int kLoaders = 4;                 // warps that copy rows by index
+constexpr int kAhead = 3;                   // k-blocks that they have in flight
 constexpr int kMaxTn = 240;
 constexpr int kMaxTnGated = 112;            // two accumulators, for this tile and the next
 constexpr int kScaleStages = 4;             // groups of four k-blocks in flight
@@ -44,15 +53,19 @@ constexpr uint32_t kScaleBytes = 4 * 512;   // weights, second weights, tokens 0
 constexpr uint32_t kScaleCols = 16;         // TMEM columns of one group
 constexpr int kMaxStages = 12;
 constexpr int kMaxExperts = 1024;
+constexpr int64_t kAcross = 16;            // (about as many tiles along the tokens run with them)
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kRingBytes = 192 * 1024;
-constexpr size_t kSmemBesides = 1024 + kScaleStages * kScaleBytes + kMaxTn * 8 + 2 * 4 * 32 * 4 + 512;
+constexpr uint32_t kRingBytes = 4 * (BM + kMaxTn) * BK;
+constexpr uint32_t kTurnBytes = 4 * 32 * 32 * 4;   // each epilogue warp's 32 x 32 outputs
+constexpr size_t kSmemBesides = 1024 + kTurnBytes + kScaleStages * kScaleBytes + 2 * 256 * 4 + 2 * 4 * 32 * 4 + 512;
 constexpr size_t kPlanBytes = 2 * (kMaxExperts + 4) * sizeof(int);
+static_assert(kRingBytes / ((2 * BM + kMaxTnGated) * BK) >= kAhead, "stages for the copies in flight");
 static_assert(2 * kMaxTn + 2 * kScaleCols <= kTmemCols, "TMEM columns");
 static_assert(4 * kMaxTnGated + 2 * kScaleCols <= kTmemCols, "TMEM columns");
 static_assert(kRingBytes + kSmemBesides + kPlanBytes <= 227 * 1024, "shared memory");
 
 struct Params {
+  const uint8_t *a; int64_t lda, K;
   const uint8_t *ae; int64_t ldae;
   const float *ra;
   const uint8_t *we[2]; int64_t ldwe[2], next_we[2];
@@ -63,8 +76,10 @@ struct Params {
   int64_t a_rows, M, N;
   int act;
   int kb;               // k-blocks
+  int wide;             // rows of the output and the residual allow 8 bytes at a time
   int tn, stages;
   int n_w, n_m;         // tiles along the weights; along the tokens (not of experts)
+  int across;           // tiles along the weights that are gone through for all tokens before the next
   int splits;           // CTAs of a cluster that share a tile's k-blocks
   int acc_cols;         // columns of an accumulator
   int buffers;          // sets of accumulators
@@ -116,9 +131,10 @@ struct Tile {
 template <bool EXPERTS>
 __device__ __forceinline__ Tile tile_of(const Params &p, const Plan &plan, int t) {
   Tile r;
-  r.n = t % p.n_w;
-  const int m = t / p.n_w;
+  int m;
   if constexpr (EXPERTS) {
+    r.n = t % p.n_w;
+    m = t / p.n_w;
     int lo = 0, hi = p.n_experts;   // tiles[lo] <= m < tiles[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -129,6 +145,11 @@ __device__ __forceinline__ Tile tile_of(const Params &p, const Plan &plan, int t
     r.m0 = plan.at[lo] + (m - plan.tiles[lo]) * p.tn;
     r.cols = min(plan.at[lo + 1] - r.m0, p.tn);
   } else {
+    // runs of `across` tiles along the weights, each for all tokens
+    const int run = t / (p.across * p.n_m), n0 = run * p.across, width = min(p.across, p.n_w - n0);
+    const int in_run = t - n0 * p.n_m;
+    r.n = n0 + in_run % width;
+    m = in_run / width;
     r.e = 0;
     r.m0 = m * p.tn;
     r.cols = (int)min(p.M - r.m0, (int64_t)p.tn);
@@ -186,18 +207,27 @@ __device__ __forceinline__ void make_plan(const Params &p, const Plan &plan, int
 }
 
 // TO: type of the output, if it is not gated.
+template <bool GATED, bool EXPERTS>
+constexpr int kThreadsOf = kThreads + (GATED && EXPERTS ? 32 * kLoaders : 0);
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <typename TO, bool GATED, bool EXPERTS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<GATED, EXPERTS>, 1)
 linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ CUtensorMap mw1,
               const __grid_constant__ CUtensorMap ma, Params p, DevStatus *st) {
   constexpr int W = GATED ? 2 : 1;
   constexpr bool GATHER = GATED && EXPERTS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *sscale = ring + kRingBytes;
-  float *sra = (float *)(sscale + kScaleStages * kScaleBytes);   // of each token: factor,
-  int *srow = (int *)(sra + kMaxTn);                             // row of the output (-1: none)
-  float *smax = (float *)(srow + kMaxTn);                        // [2][4 warps][32 tokens]
+  float *turned = (float *)(ring + kRingBytes);
+  uint8_t *sscale = (uint8_t *)turned + kTurnBytes;
+  float *sra = (float *)(sscale + kScaleStages * kScaleBytes);   // [256] of each token: factor,
+  int *srow = (int *)(sra + 256);                                // row of the output (-1: none)
+  float *smax = (float *)(srow + 256);                           // [2][4 warps][32 tokens]
   uint64_t *full = (uint64_t *)(smax + 2 * 4 * 32);
   uint64_t *empty = full + kMaxStages;
   uint64_t *sfull = empty + kMaxStages;
@@ -218,7 +248,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&full[s], GATHER ? 1 + kLoaders : 1);
       tc::mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kScaleStages; ++s) {
@@ -235,7 +265,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
   if (warp == 1) tc::tmem_alloc(tmem_slot, p.tmem_cols);
   if constexpr (EXPERTS) {
     wait_for_grids();
-    for (int e = threadIdx.x; e <= p.n_experts; e += kThreads) plan.at[e] = p.offsets[e];
+    for (int e = threadIdx.x; e <= p.n_experts; e += blockDim.x) plan.at[e] = p.offsets[e];
     __syncthreads();
     if (warp == 0) make_plan(p, plan, lane);
   }
@@ -257,38 +287,22 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
   uint32_t ph = 1;
   if (warp == 0) {
     // ---------------- producer ----------------
-    // (a whole warp: its lanes issue the gathers; the other copies one lane)
-    const bool elected = tc::elect_one();
-    if (elected) {
+    if (tc::elect_one()) {
       tc::tma_prefetch_desc(&mw0);
       if constexpr (GATED) tc::tma_prefetch_desc(&mw1);
-      tc::tma_prefetch_desc(&ma);
-    }
-    for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile tile = tile_of<EXPERTS>(p, plan, t);
-      // rows that the MMA reads: of experts, whole groups of 16
-      const int rows = EXPERTS ? (tile.cols + 15) / 16 * 16 : p.tn;
-      int row[2][4];
-      if constexpr (GATHER) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = (lane + 32 * h) * 4 + i;
-            row[h][i] = j < tile.cols ? a_row<true>(p, tile.m0 + j) : (int)p.a_rows;
-          }
-      }
-      const uint32_t bytes = (uint32_t)(W * BM + rows) * BK;
-      for (int kb = k0; kb < k1; ++kb) {
-        ok = tc::mbar_wait_compact(&empty[s], ph, waits);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        uint8_t *base = ring + s * stage_bytes;
-        if (elected) {
+      if constexpr (!GATHER) tc::tma_prefetch_desc(&ma);
+#pragma unroll 1
+      for (int t = first; t < n_tiles && ok; t += step) {
+        const Tile tile = tile_of<EXPERTS>(p, plan, t);
+        // rows that the MMA reads: of experts, whole groups of 16
+        const int rows = EXPERTS ? (tile.cols + 15) / 16 * 16 : p.tn;
+        const uint32_t bytes = (uint32_t)(W * BM + (GATHER ? 0 : rows)) * BK;
+        for (int kb = k0; kb < k1; ++kb) {
+          ok = tc::mbar_wait_compact(&empty[s], ph, waits);
+          if (!ok) break;
+          uint8_t *base = ring + s * stage_bytes;
           // (a lost copy is one whose last bytes never arrive)
-          tc::mbar_arrive_expect_tx(&full[s], bytes + (n == p.lost ? 16u : 0u));
+          tc::mbar_arrive_expect_tx(&full[s], bytes + (n++ == p.lost ? 16u : 0u));
           tc::tma_load_3d(base, &mw0, kb * BK, tile.n * BM, tile.e, &full[s]);
           if constexpr (GATED) tc::tma_load_3d(base + BM * BK, &mw1, kb * BK, tile.n * BM, tile.e, &full[s]);
           if constexpr (!EXPERTS) {
@@ -297,19 +311,65 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
             for (int j = 0; j < rows; j += 16)
               tc::tma_load_2d(base + (W * BM + j) * BK, &ma, kb * BK, tile.m0 + j, &full[s]);
           }
+          if (++s == p.stages) s = 0, ph ^= 1;
         }
-        if constexpr (GATHER) {
-          __syncwarp();
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if ((lane + 32 * h) * 4 < rows)
-              tc::tma_gather4(base + (W * BM + (lane + 32 * h) * 4) * BK, &ma, kb * BK, row[h][0], row[h][1],
-                              row[h][2], row[h][3], &full[s]);
-        }
-        ++n;
-        if (++s == p.stages) s = 0, ph ^= 1;
       }
     }
+  } else if (GATHER && warp >= 7) {
+    // ---------------- token rows by index ----------------
+    // A copy of a warp takes four rows of 128 bytes; the MMA's swizzle exchanges a row's 16-byte
+    // pieces by its number modulo 8.  Zeros past K, and for positions that name no row.
+    constexpr int kQuads = kMaxTnGated / 4 / kLoaders;
+    const int piece = lane % 8, sub = lane / 8;
+    int held = 0, hs = 0;           // k-blocks in flight; stage of the first
+#pragma unroll 1
+    for (int t = first; t < n_tiles && ok; t += step) {
+      const Tile tile = tile_of<EXPERTS>(p, plan, t);
+      const int quads = (tile.cols + 15) / 16 * 4;
+      int64_t src[kQuads];          // the lane's row of each copy (-1: none)
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) {
+        const int j = (warp - 7 + kLoaders * i) * 4 + sub;
+        const int r = j < tile.cols ? a_row<GATHER>(p, tile.m0 + j) : (int)p.a_rows;
+        src[i] = r < p.a_rows ? r * p.lda : -1;
+      }
+#pragma unroll 1
+      for (int kb = k0; kb < k1; ++kb) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_compact(&empty[s], ph, waits));
+        if (!ok) break;
+        const int64_t k = (int64_t)kb * BK + piece * 16;
+        const int here = k >= p.K ? 0 : (p.K - k < 16 ? (int)(p.K - k) : 16);
+        const uint32_t base = tc::smem_u32(ring) + s * stage_bytes + W * BM * BK;
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+          const int quad = warp - 7 + kLoaders * i, j = quad * 4 + sub;
+          if (quad < quads) {
+            const bool there = src[i] >= 0 && here > 0;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + j * BK + ((piece ^ (j & 7)) * 16)),
+                         "l"(p.a + (there ? src[i] + k : 0)), "r"(there ? here : 0)
+                         : "memory");
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++s == p.stages) s = 0, ph ^= 1;
+        if (++held == kAhead) {
+          wait_copies<kAhead - 1>();
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&full[hs]);
+          if (++hs == p.stages) hs = 0;
+          --held;
+        }
+      }
+    }
+    wait_copies<0>();
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (ok && lane == 0)
+      for (; held > 0; --held) {
+        tc::mbar_arrive(&full[hs]);
+        if (++hs == p.stages) hs = 0;
+      }
   } else if (warp == 1 && tc::elect_one()) {
     // ---------------- MMA issuer ----------------
     const uint32_t ring0 = (tc::smem_u32(ring) >> 4) | (1u << 16), stage16 = stage_bytes >> 4;
@@ -410,6 +470,8 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
       const Tile tile = tile_of<EXPERTS>(p, plan, t);
       const int64_t nn = (int64_t)tile.n * BM + lrow;
       const bool in = nn < p.N;
+      // the warp's 32 rows are all there, and rows of the output allow 8 bytes at a time (codes do)
+      const bool wide = (p.wide || GATED) && (int64_t)tile.n * BM + q * 32 + 32 <= p.N;
       if (p.splits == 1) {
         tc::named_barrier(2, 128);  // the previous tile's factors have been read
         for (int j = et; j < tile.cols; j += 128) {
@@ -448,38 +510,79 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
           continue;
         }
         float v[32];
+        const int left = tile.cols - c;                      // tokens of this chunk, if below 32
+        float *turn32 = turned + q * 32 * 32;                // this warp's [32 tokens][32 rows]
+        const float4 *ra4 = reinterpret_cast<const float4 *>(sra + c);
         if constexpr (!GATED) {
-          TO res[32];
-          if (p.residual) {
+          // the lane has four outputs of the tokens lane / 8, + 4, ...
+          const int64_t n4 = (int64_t)tile.n * BM + q * 32 + lane % 8 * 4;
+          uint2 res[8];
+          if (wide && p.residual) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              res[i] = in && c + i < tile.cols ? ((const TO *)p.residual)[(int64_t)(tile.m0 + c + i) * p.ldr + nn] : out_f32<TO>(0.0f);
+            for (int i = 0; i < 8; ++i) {
+              const int j = lane / 8 + 4 * i;
+              if (j < left) res[i] = *reinterpret_cast<const uint2 *>((const TO *)p.residual + (int64_t)(tile.m0 + c + j) * p.ldr + n4);
+            }
           }
           tc::tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(r[0][i]) * rw[0], sra[(c + i) % kMaxTn], bias[0]);
-          activate(v, p.act);
-          if (p.residual) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += to_f32(res[i]);
+          for (int i = 0; i < 8; ++i) {
+            const float4 f = ra4[i];
+            v[4 * i] = fmaf(__uint_as_float(r[0][4 * i]) * rw[0], f.x, bias[0]);
+            v[4 * i + 1] = fmaf(__uint_as_float(r[0][4 * i + 1]) * rw[0], f.y, bias[0]);
+            v[4 * i + 2] = fmaf(__uint_as_float(r[0][4 * i + 2]) * rw[0], f.z, bias[0]);
+            v[4 * i + 3] = fmaf(__uint_as_float(r[0][4 * i + 3]) * rw[0], f.w, bias[0]);
           }
-          if (in) {
+          activate(v, p.act);
+          if (wide) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) turn32[i * 32 + lane] = v[i];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int j = lane / 8 + 4 * i;
+              const int64_t row = EXPERTS ? srow[c + j] : tile.m0 + c + j;
+              if (j >= left || (EXPERTS && row < 0)) continue;
+              float4 x = *reinterpret_cast<const float4 *>(turn32 + j * 32 + lane % 8 * 4);
+              if (p.residual) {
+                const TO *h = reinterpret_cast<const TO *>(&res[i]);
+                x.x += to_f32(h[0]);
+                x.y += to_f32(h[1]);
+                x.z += to_f32(h[2]);
+                x.w += to_f32(h[3]);
+              }
+              alignas(8) const TO o[4] = {out_f32<TO>(x.x), out_f32<TO>(x.y), out_f32<TO>(x.z), out_f32<TO>(x.w)};
+              *reinterpret_cast<uint2 *>((TO *)p.out + row * p.ldo + n4) = *reinterpret_cast<const uint2 *>(o);
+            }
+            __syncwarp();
+          } else if (in) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              if (c + i >= tile.cols) break;
               const int64_t row = EXPERTS ? srow[c + i] : tile.m0 + c + i;
-              if (!EXPERTS || row >= 0) ((TO *)p.out)[row * p.ldo + nn] = out_f32<TO>(v[i]);
+              if (i >= left || (EXPERTS && row < 0)) continue;
+              const float x = p.residual ? v[i] + to_f32(((const TO *)p.residual)[row * p.ldr + nn]) : v[i];
+              ((TO *)p.out)[row * p.ldo + nn] = out_f32<TO>(x);
             }
           }
         } else {
           tc::tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(r[0][i]) * rw[0], sra[(c + i) % kMaxTn], bias[0]);
+          for (int i = 0; i < 8; ++i) {
+            const float4 f = ra4[i];
+            const float fs[4] = {f.x, f.y, f.z, f.w};
+            float u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[4 * i + j] = fmaf(__uint_as_float(r[0][4 * i + j]) * rw[0], fs[j], bias[0]);
+              u[j] = fmaf(__uint_as_float(r[1][4 * i + j]) * rw[1], fs[j], bias[1]);
+              r[1][4 * i + j] = __float_as_uint(u[j]);
+            }
+          }
           activate(v, p.act);
           float *sm = smax + (turn++ & 1) * 128;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            v[i] *= fmaf(__uint_as_float(r[1][i]) * rw[1], sra[(c + i) % kMaxTn], bias[1]);
+            v[i] *= __uint_as_float(r[1][i]);
             const uint32_t most = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(fp8::finite_abs(v[i])) : 0u);
             if (lane == i) sm[q * 32 + i] = __uint_as_float(most);
           }
@@ -487,16 +590,33 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
           // this lane has token c + lane's exponent
           const float most = fmaxf(fmaxf(sm[lane], sm[32 + lane]), fmaxf(sm[64 + lane], sm[96 + lane]));
           const int ex = fp8::block_exponent(most);
-          if (q == 0 && c + lane < tile.cols)
+          if (q == 0 && lane < left)
             p.oe[(int64_t)(tile.m0 + c + lane) * p.ldoe + tile.n] = (uint8_t)(ex + fp8::kBias);
-          uint8_t *o = (uint8_t *)p.out + (int64_t)(tile.m0 + c) * p.ldo + nn;
+          uint8_t *o = (uint8_t *)p.out + (int64_t)(tile.m0 + c) * p.ldo;
+          uint8_t *codes = reinterpret_cast<uint8_t *>(turn32);   // [32 tokens][32 rows]
+          const float inv = fp8::pow2(-ex);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const float s0 = fp8::pow2(-__shfl_sync(0xffffffffu, ex, i)), s1 = fp8::pow2(-__shfl_sync(0xffffffffu, ex, i + 1));
+            const float s0 = __shfl_sync(0xffffffffu, inv, i), s1 = __shfl_sync(0xffffffffu, inv, i + 1);
             const uint32_t two = fp8::pack2(fp8::inf_to_nan(v[i]) * s0, fp8::inf_to_nan(v[i + 1]) * s1);
-            if (in && c + i < tile.cols) o[i * p.ldo] = (uint8_t)two;
-            if (in && c + i + 1 < tile.cols) o[(i + 1) * p.ldo] = (uint8_t)(two >> 8);
+            codes[i * 32 + lane] = (uint8_t)two;
+            codes[(i + 1) * 32 + lane] = (uint8_t)(two >> 8);
           }
+          __syncwarp();
+          if (wide) {
+            // (rows of codes are 16-byte aligned)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int j = lane / 2 + 16 * i;
+              if (j < left)
+                *reinterpret_cast<uint4 *>(o + j * p.ldo + (int64_t)tile.n * BM + q * 32 + lane % 2 * 16) =
+                    *reinterpret_cast<const uint4 *>(codes + j * 32 + lane % 2 * 16);
+            }
+          } else if (in) {
+#pragma unroll 4
+            for (int j = 0; j < 32 && j < left; ++j) o[j * p.ldo + nn] = codes[j * 32 + lane];
+          }
+          __syncwarp();
         }
       }
       tc::tc_fence_before();
@@ -540,7 +660,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
         }
       const bool pairs = (p.ldo & 1) == 0 && ((uintptr_t)p.out & 3) == 0 && nn + 3 < p.N;
 #pragma unroll 1
-      for (int col = rank + warp * p.splits; col < tile.cols; col += kThreads / 32 * p.splits) {
+      for (int col = rank + warp * p.splits; col < tile.cols; col += kThreadsOf<GATED, EXPERTS> / 32 * p.splits) {
         const int pos = tile.m0 + col, r = a_row<GATHER>(p, pos);
         const float ra = p.ra && r < p.a_rows ? p.ra[r] : 1.0f;
         int64_t row = pos;
@@ -629,7 +749,7 @@ int clusters_at_once(int dev, int splits, int sms) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(splits * sms));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreadsOf<GATED, EXPERTS>);
     cfg.dynamicSmemBytes = smem_bytes(EXPERTS);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -689,8 +809,10 @@ gptq_status run(const Fp8LinearArgs &g, DevStatus *st, cudaStream_t s) {
   GPTQ_CUDA_CHECK(cudaGetDevice(&dev));
   const Shape sh = choose<TO, GATED, EXPERTS>(g, dev, sms);
   Params p{};
+  p.a = g.a; p.lda = g.lda; p.K = g.K;
   p.ae = g.ae; p.ldae = g.ldae;
   p.ra = g.ra;
+  p.wide = fp8::alignment(g.out, 2 * g.ldo) >= 8 && (!g.residual || fp8::alignment(g.residual, 2 * g.ldr) >= 8);
   for (int w = 0; w < W; ++w) {
     p.we[w] = g.w[w].exps; p.ldwe[w] = g.w[w].ld_exps; p.next_we[w] = g.w[w].next_exps;
     p.rw[w] = g.w[w].scale;
@@ -706,6 +828,7 @@ gptq_status run(const Fp8LinearArgs &g, DevStatus *st, cudaStream_t s) {
   p.splits = sh.splits;
   p.n_w = (int)ceil_div(g.N, (int64_t)BM);
   p.n_m = (int)ceil_div(g.M, (int64_t)sh.tn);
+  p.across = (int)ceil_div(p.n_w, ceil_div(p.n_w, kAcross));
   const int64_t along = EXPERTS ? (g.n_experts < g.M ? g.n_experts : g.M) + g.M / sh.tn : p.n_m;
   const int64_t tiles = p.n_w * along;   // at most
   if (tiles * 8 > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
@@ -726,10 +849,10 @@ gptq_status run(const Fp8LinearArgs &g, DevStatus *st, cudaStream_t s) {
       return GPTQ_ERR_UNSUPPORTED;
   if (W == 1) mw[1] = mw[0];
   if (!tc::make_tmap_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, g.a_rows, g.K, g.lda, BK,
-                        !EXPERTS ? sh.tn : GATED ? 1 : 16))
+                        EXPERTS ? 16 : sh.tn))
     return GPTQ_ERR_UNSUPPORTED;
   const int64_t ctas = sh.splits > 1 ? tiles * sh.splits : (tiles < sms ? tiles : sms);
-  return launch_early(linear_kernel<TO, GATED, EXPERTS>, dim3((unsigned)ctas), dim3(kThreads), smem_bytes(EXPERTS),
+  return launch_early(linear_kernel<TO, GATED, EXPERTS>, dim3((unsigned)ctas), dim3(kThreadsOf<GATED, EXPERTS>), smem_bytes(EXPERTS),
                       sh.splits, s, mw[0], mw[1], ma, p, st);
 }
 

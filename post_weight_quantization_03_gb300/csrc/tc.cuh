@@ -146,17 +146,6 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, int
       : "memory");
 }
 
-// Four rows r.. of a tensor map whose box is one row, from column x on, one after another in `dst`.
-// Rows outside the tensor read as zeros.
-__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *m, int32_t x, int32_t r0,
-                                            int32_t r1, int32_t r2, int32_t r3, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"((uint64_t)m), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // Contiguous global -> shared bulk copy (no tensor map); `bytes` a multiple of 16, both
 // addresses 16-byte aligned; completion counted on `bar`.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
