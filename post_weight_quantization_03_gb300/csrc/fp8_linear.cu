@@ -7,9 +7,8 @@
 //
 //   warp 0     : TMA producer: (gate, up, tokens) of 128 bytes x rows per k-block
 //   warp 1     : TMEM allocator + MMA issuer (one lane)
-//   warps 2..5 : epilogue, one weight row per thread
-//   warp 6     : scales
-//   warps 7..10: token rows of the experts' gated product
+//   then       : 4 (gated) or 8 warps of epilogue, one weight row per thread; one warp that makes up
+//                the scales; 8 warps that copy token rows (the experts' gated product)
 //
 // Gated: a tile has 128 rows of both weights and two accumulators, so the 128 outputs that share an
 // exponent are one column of the tile: a maximum over each warp (redux) and one over the four.
@@ -17,8 +16,8 @@
 // Experts: a tile is (expert, up to tn of its positions, 128 weight rows).  Each CTA counts the
 // tiles from the offsets by itself.  The gated product takes its token rows by index, the other takes
 // them as they lie and stores each where the order says, so that neither the rows nor the results
-// are moved by a kernel of their own.  Rows by index are copied by four warps (16 bytes a
-// lane, three k-blocks in flight), which write the swizzle that the MMA reads: TMA's gather of four
+// are moved by a kernel of their own.  Rows by index are copied by four warps, 16 bytes a
+// lane, into the swizzle that the MMA reads: TMA's gather of four
 // rows takes about 80 cycles, 2300 for a k-block whose MMAs take 770 (4096 tokens of 64 experts, 4096
 // x 1376: 709 us).
 //
@@ -43,9 +42,7 @@ using mx::copy_scales;
 using mx::ld_cluster_f32x4;
 using mx::out_f32;
 
-constexpr int kThreads = 224;
-constexpr int kLoaders = 4;                 // warps that copy rows by index
-constexpr int kAhead = 3;                   // k-blocks that they have in flight
+constexpr int kLoaders = 8;                 // warps that copy rows by index
 constexpr int kMaxTn = 240;
 constexpr int kMaxTnGated = 112;            // two accumulators, for this tile and the next
 constexpr int kScaleStages = 4;             // groups of four k-blocks in flight
@@ -56,10 +53,9 @@ constexpr int kMaxExperts = 1024;
 constexpr int64_t kAcross = 16;            // (about as many tiles along the tokens run with them)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kRingBytes = 4 * (BM + kMaxTn) * BK;
-constexpr uint32_t kTurnBytes = 4 * 32 * 32 * 4;   // each epilogue warp's 32 x 32 outputs
+constexpr uint32_t kTurnBytes = 8 * 16 * 32 * 4;   // each epilogue warp's 16 tokens x 32 rows
 constexpr size_t kSmemBesides = 1024 + kTurnBytes + kScaleStages * kScaleBytes + 2 * 256 * 4 + 2 * 4 * 32 * 4 + 512;
 constexpr size_t kPlanBytes = 2 * (kMaxExperts + 4) * sizeof(int);
-static_assert(kRingBytes / ((2 * BM + kMaxTnGated) * BK) >= kAhead, "stages for the copies in flight");
 static_assert(2 * kMaxTn + 2 * kScaleCols <= kTmemCols, "TMEM columns");
 static_assert(4 * kMaxTnGated + 2 * kScaleCols <= kTmemCols, "TMEM columns");
 static_assert(kRingBytes + kSmemBesides + kPlanBytes <= 227 * 1024, "shared memory");
@@ -141,9 +137,12 @@ __device__ __forceinline__ Tile tile_of(const Params &p, const Plan &plan, int t
       if (plan.tiles[mid] <= m) lo = mid;
       else hi = mid;
     }
+    // an expert's tiles are of even size, in whole groups of 16
+    const int tiles = plan.tiles[lo + 1] - plan.tiles[lo], count = plan.at[lo + 1] - plan.at[lo];
+    const int size = ((count + tiles - 1) / tiles + 15) / 16 * 16, from = (m - plan.tiles[lo]) * size;
     r.e = lo;
-    r.m0 = plan.at[lo] + (m - plan.tiles[lo]) * p.tn;
-    r.cols = min(plan.at[lo + 1] - r.m0, p.tn);
+    r.m0 = plan.at[lo] + from;
+    r.cols = min(count - from, size);   // (above 0: size is at most tn)
   } else {
     // runs of `across` tiles along the weights, each for all tokens
     const int run = t / (p.across * p.n_m), n0 = run * p.across, width = min(p.across, p.n_w - n0);
@@ -207,13 +206,12 @@ __device__ __forceinline__ void make_plan(const Params &p, const Plan &plan, int
 }
 
 // TO: type of the output, if it is not gated.
+// Warps of the epilogue: two for each 32 rows, which take 32 tokens in turn; gated one, which the
+// MMAs of two weights hide (and whose registers, with the loaders', would not go round).
+template <bool GATED>
+constexpr int kEpilogue = GATED ? 4 : 8;
 template <bool GATED, bool EXPERTS>
-constexpr int kThreadsOf = kThreads + (GATED && EXPERTS ? 32 * kLoaders : 0);
-
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+constexpr int kThreadsOf = 32 * (3 + kEpilogue<GATED> + (GATED && EXPERTS ? kLoaders : 0));
 
 template <typename TO, bool GATED, bool EXPERTS>
 __global__ void __launch_bounds__(kThreadsOf<GATED, EXPERTS>, 1)
@@ -221,6 +219,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
               const __grid_constant__ CUtensorMap ma, Params p, DevStatus *st) {
   constexpr int W = GATED ? 2 : 1;
   constexpr bool GATHER = GATED && EXPERTS;
+  constexpr int E = kEpilogue<GATED>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   float *turned = (float *)(ring + kRingBytes);
@@ -248,7 +247,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      tc::mbar_init(&full[s], GATHER ? 1 + kLoaders : 1);
+      tc::mbar_init(&full[s], GATHER ? 1 + 32 * kLoaders : 1);
       tc::mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kScaleStages; ++s) {
@@ -257,7 +256,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&tfull[b], 1);
-      tc::mbar_init(&tempty[b], 4);
+      tc::mbar_init(&tempty[b], E);
     }
     tc::mbar_init(mdone, 1);
     tc::mbar_fence_init();
@@ -315,61 +314,60 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
         }
       }
     }
-  } else if (GATHER && warp >= 7) {
+  } else if (GATHER && warp >= 3 + E) {
     // ---------------- token rows by index ----------------
     // A copy of a warp takes four rows of 128 bytes; the MMA's swizzle exchanges a row's 16-byte
     // pieces by its number modulo 8.  Zeros past K, and for positions that name no row.
     constexpr int kQuads = kMaxTnGated / 4 / kLoaders;
     const int piece = lane % 8, sub = lane / 8;
-    int held = 0, hs = 0;           // k-blocks in flight; stage of the first
+    // where the lane's piece goes, of its first copy: quads are 512 bytes, which the warps take in turn
+    const int row0 = (warp - 3 - E) * 4 + sub;
+    const uint32_t to = tc::smem_u32(ring) + W * BM * BK + row0 * BK + (piece ^ (row0 & 7)) * 16;
+    static_assert(kLoaders % 2 == 0, "a lane's rows are the same modulo 8");
 #pragma unroll 1
     for (int t = first; t < n_tiles && ok; t += step) {
       const Tile tile = tile_of<EXPERTS>(p, plan, t);
-      const int quads = (tile.cols + 15) / 16 * 4;
-      int64_t src[kQuads];          // the lane's row of each copy (-1: none)
+      const int rows = (tile.cols + 15) / 16 * 16;
+      const uint8_t *src[kQuads];
+      bool there[kQuads];           // (zeros for what is not)
 #pragma unroll
       for (int i = 0; i < kQuads; ++i) {
-        const int j = (warp - 7 + kLoaders * i) * 4 + sub;
+        const int j = row0 + 4 * kLoaders * i;
         const int r = j < tile.cols ? a_row<GATHER>(p, tile.m0 + j) : (int)p.a_rows;
-        src[i] = r < p.a_rows ? r * p.lda : -1;
+        there[i] = r < p.a_rows;
+        src[i] = p.a + (there[i] ? r * p.lda : 0) + piece * 16;
       }
 #pragma unroll 1
       for (int kb = k0; kb < k1; ++kb) {
         ok = __all_sync(0xffffffffu, tc::mbar_wait_compact(&empty[s], ph, waits));
         if (!ok) break;
-        const int64_t k = (int64_t)kb * BK + piece * 16;
-        const int here = k >= p.K ? 0 : (p.K - k < 16 ? (int)(p.K - k) : 16);
-        const uint32_t base = tc::smem_u32(ring) + s * stage_bytes + W * BM * BK;
+        const uint32_t dst = to + s * stage_bytes;
+        const int64_t k = (int64_t)kb * BK;
+        if (k + BK <= p.K) {
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-          const int quad = warp - 7 + kLoaders * i, j = quad * 4 + sub;
-          if (quad < quads) {
-            const bool there = src[i] >= 0 && here > 0;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + j * BK + ((piece ^ (j & 7)) * 16)),
-                         "l"(p.a + (there ? src[i] + k : 0)), "r"(there ? here : 0)
-                         : "memory");
-          }
+          for (int i = 0; i < kQuads; ++i)
+            if (row0 + 4 * kLoaders * i < rows)
+              asm volatile(
+                  "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %2, 0;\n\t"
+                  "cp.async.cg.shared.global [%0], [%1], 16, p;\n\t}" ::"r"(dst + 4 * kLoaders * BK * i),
+                  "l"(src[i] + k), "r"((uint32_t)there[i])
+                  : "memory");
+        } else {
+          const int64_t left = p.K - k - piece * 16;
+          const int here = left <= 0 ? 0 : left < 16 ? (int)left : 16;
+#pragma unroll
+          for (int i = 0; i < kQuads; ++i)
+            if (row0 + 4 * kLoaders * i < rows)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 4 * kLoaders * BK * i),
+                           "l"(here > 0 ? src[i] + k : p.a), "r"(there[i] ? here : 0)
+                           : "memory");
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        // arrives when the lane's copies have landed
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&full[s])) : "memory");
         if (++s == p.stages) s = 0, ph ^= 1;
-        if (++held == kAhead) {
-          wait_copies<kAhead - 1>();
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&full[hs]);
-          if (++hs == p.stages) hs = 0;
-          --held;
-        }
       }
     }
-    wait_copies<0>();
-    tc::fence_proxy_async_smem();
-    __syncwarp();
-    if (ok && lane == 0)
-      for (; held > 0; --held) {
-        tc::mbar_arrive(&full[hs]);
-        if (++hs == p.stages) hs = 0;
-      }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1 && tc::elect_one()) {
     // ---------------- MMA issuer ----------------
     const uint32_t ring0 = (tc::smem_u32(ring) >> 4) | (1u << 16), stage16 = stage_bytes >> 4;
@@ -404,6 +402,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
           if (kb + j >= k1) break;
           ok = tc::mbar_wait_compact(&full[s], ph, waits);
           if (!ok) break;
+          if constexpr (GATHER) tc::fence_proxy_async_smem();   // the rows were not written by TMA
           tc::tc_fence_after();
           const uint32_t id = idesc | ((uint32_t)j << 29) | ((uint32_t)j << 4);
 #pragma unroll
@@ -420,7 +419,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
       }
       if (ok) tc::mma_commit(&tfull[b]);
     }
-  } else if (warp == 6) {
+  } else if (warp == 2 + E) {
     // ---------------- scales ----------------
     int g = 0;
     for (int t = first; t < n_tiles && ok; t += step) {
@@ -461,9 +460,9 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
         tc::mbar_arrive(&sfull[q]);
       }
     }
-  } else if (warp >= 2 && warp < 6) {
+  } else if (warp >= 2 && warp < 2 + E) {
     // ---------------- epilogue ----------------
-    const int q = warp & 3, lrow = q * 32 + lane, et = threadIdx.x - 64;
+    const int q = warp & 3, lrow = q * 32 + lane, et = threadIdx.x - 64, half = (warp - 2) / 4;
     int it = 0, turn = 0;
     for (int t = first; t < n_tiles; t += step, ++it) {
       const int b = p.buffers > 1 ? it & 1 : 0, use = p.buffers > 1 ? it >> 1 : it;
@@ -473,8 +472,8 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
       // the warp's 32 rows are all there, and rows of the output allow 8 bytes at a time (codes do)
       const bool wide = (p.wide || GATED) && (int64_t)tile.n * BM + q * 32 + 32 <= p.N;
       if (p.splits == 1) {
-        tc::named_barrier(2, 128);  // the previous tile's factors have been read
-        for (int j = et; j < tile.cols; j += 128) {
+        tc::named_barrier(2, 32 * E);  // the previous tile's factors have been read
+        for (int j = et; j < tile.cols; j += 32 * E) {
           const int pos = tile.m0 + j, r = a_row<GATHER>(p, pos);
           sra[j] = p.ra && r < p.a_rows ? p.ra[r] : 1.0f;
           if constexpr (EXPERTS && !GATED) {
@@ -490,12 +489,24 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
         rw[w] = p.rw[w] && in ? p.rw[w][at] : 1.0f;
         bias[w] = p.bias[w] && in ? p.bias[w][at] : 0.0f;
       }
+      // the lane's four outputs of the tokens lane / 8, + 4, ... of a chunk; their residuals are asked
+      // for a chunk ahead
+      const int64_t n4 = (int64_t)tile.n * BM + q * 32 + lane % 8 * 4;
+      uint2 res[8];
+      auto ask = [&](int c) {
+        if (GATED || !wide || !p.residual || p.splits > 1) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + lane / 8 + 4 * i < tile.cols)
+            res[i] = *reinterpret_cast<const uint2 *>((const TO *)p.residual + (int64_t)(tile.m0 + c + lane / 8 + 4 * i) * p.ldr + n4);
+      };
+      ask(32 * half);
       ok = tc::mbar_wait_compact(&tfull[b], use & 1, waits);
-      if (!tc::named_barrier_and(1, 128, ok)) break;
+      if (!tc::named_barrier_and(1, 32 * E, ok)) break;
       tc::tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * set_cols;
 #pragma unroll 1
-      for (int c = 0; c < tile.cols; c += 32) {
+      for (int c = 32 * half; c < tile.cols; c += 8 * E) {
         uint32_t r[W][32];
 #pragma unroll
         for (int w = 0; w < W; ++w) tc::tmem_ld32(acc + w * p.acc_cols + (uint32_t)c, r[w]);
@@ -511,19 +522,9 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
         }
         float v[32];
         const int left = tile.cols - c;                      // tokens of this chunk, if below 32
-        float *turn32 = turned + q * 32 * 32;                // this warp's [32 tokens][32 rows]
+        float *mine = turned + (warp - 2) * 16 * 32;         // this warp's to turn
         const float4 *ra4 = reinterpret_cast<const float4 *>(sra + c);
         if constexpr (!GATED) {
-          // the lane has four outputs of the tokens lane / 8, + 4, ...
-          const int64_t n4 = (int64_t)tile.n * BM + q * 32 + lane % 8 * 4;
-          uint2 res[8];
-          if (wide && p.residual) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int j = lane / 8 + 4 * i;
-              if (j < left) res[i] = *reinterpret_cast<const uint2 *>((const TO *)p.residual + (int64_t)(tile.m0 + c + j) * p.ldr + n4);
-            }
-          }
           tc::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -535,26 +536,33 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
           }
           activate(v, p.act);
           if (wide) {
+            uint2 add[8];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) turn32[i * 32 + lane] = v[i];
-            __syncwarp();
+            for (int i = 0; i < 8; ++i) add[i] = res[i];
+            ask(c + 8 * E);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int j = lane / 8 + 4 * i;
-              const int64_t row = EXPERTS ? srow[c + j] : tile.m0 + c + j;
-              if (j >= left || (EXPERTS && row < 0)) continue;
-              float4 x = *reinterpret_cast<const float4 *>(turn32 + j * 32 + lane % 8 * 4);
-              if (p.residual) {
-                const TO *h = reinterpret_cast<const TO *>(&res[i]);
-                x.x += to_f32(h[0]);
-                x.y += to_f32(h[1]);
-                x.z += to_f32(h[2]);
-                x.w += to_f32(h[3]);
+            for (int h = 0; h < 2; ++h) {                    // 16 tokens at a time
+#pragma unroll
+              for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = v[16 * h + i];
+              __syncwarp();
+#pragma unroll
+              for (int i = 4 * h; i < 4 * h + 4; ++i) {
+                const int j = lane / 8 + 4 * i;
+                const int64_t row = EXPERTS ? srow[c + j] : tile.m0 + c + j;
+                if (j >= left || (EXPERTS && row < 0)) continue;
+                float4 x = *reinterpret_cast<const float4 *>(mine + (j - 16 * h) * 32 + lane % 8 * 4);
+                if (p.residual) {
+                  const TO *r4 = reinterpret_cast<const TO *>(&add[i]);
+                  x.x += to_f32(r4[0]);
+                  x.y += to_f32(r4[1]);
+                  x.z += to_f32(r4[2]);
+                  x.w += to_f32(r4[3]);
+                }
+                alignas(8) const TO o[4] = {out_f32<TO>(x.x), out_f32<TO>(x.y), out_f32<TO>(x.z), out_f32<TO>(x.w)};
+                *reinterpret_cast<uint2 *>((TO *)p.out + row * p.ldo + n4) = *reinterpret_cast<const uint2 *>(o);
               }
-              alignas(8) const TO o[4] = {out_f32<TO>(x.x), out_f32<TO>(x.y), out_f32<TO>(x.z), out_f32<TO>(x.w)};
-              *reinterpret_cast<uint2 *>((TO *)p.out + row * p.ldo + n4) = *reinterpret_cast<const uint2 *>(o);
+              __syncwarp();
             }
-            __syncwarp();
           } else if (in) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -593,7 +601,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
           if (q == 0 && lane < left)
             p.oe[(int64_t)(tile.m0 + c + lane) * p.ldoe + tile.n] = (uint8_t)(ex + fp8::kBias);
           uint8_t *o = (uint8_t *)p.out + (int64_t)(tile.m0 + c) * p.ldo;
-          uint8_t *codes = reinterpret_cast<uint8_t *>(turn32);   // [32 tokens][32 rows]
+          uint8_t *codes = reinterpret_cast<uint8_t *>(mine);      // [32 tokens][32 rows]
           const float inv = fp8::pow2(-ex);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
