@@ -686,7 +686,7 @@ gptq_status gptq_fp8_gated(const uint8_t *a, int64_t lda, const uint8_t *a_exps,
  * each expert.
  *
  *   s_e = softmax over the token's logits, or 1 / (1 + exp(-logit)).
- *   c_e = s_e + bias_e; where there is neither a bias nor groups, the logit.
+ *   c_e = s_e + bias_e; without a bias, whose order is that of the logits, these are compared.
  *   groups > 1: the experts fall into `groups` runs of n_experts / groups; a run's value is the sum
  *         of its group_top (1 or 2) largest c, and only the top_groups best runs are looked at.
  *   ids   the top_k experts of largest c, largest first; equals: the lowest index first.  The
@@ -751,7 +751,7 @@ gptq_status gptq_fp8_experts(const uint8_t *a, int64_t lda, const uint8_t *a_exp
 
 /*
  * gptq_moe_combine: out[t] = residual[t] + sum_j weights[t, j] y[t * top_k + j], summed in fp32 in
- * that order and rounded once.  A row whose weight is 0 is not read.
+ * that order and rounded once.  A row whose weight is 0 is left out, whatever it holds.
  *   y [n_tokens * top_k, ldy], residual [n_tokens, ldr] or NULL, out [n_tokens, ldo] of dtype (F16,
  *   BF16 or F32); out may be the residual.   weights [n_tokens, top_k] fp32.   1 <= top_k <= 32.
  * Asynchronous.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.

@@ -4,15 +4,18 @@
 // their largest c, the top_k largest c among those; weights from s; then the assignments (token *
 // top_k + place) sorted by expert.
 //
-// A warp takes a token: lane l holds the experts l, l + 32, ...; each of the top_k rounds is a
-// maximum over the lane's own and one over the warp (redux).  c is taken in fp32, and where two that
-// decide something lie nearer to one another than its error bound the token is chosen again in
-// fp64.  A softmax without bias and groups is monotone: the logits themselves are compared.
+// A warp takes a token; a lane holds `each` experts next to one another, so that a group is a run of
+// lanes where its size allows.  Each of the top_k rounds is a maximum over the lane's own and one
+// over the warp, of integers that are ordered as the c (redux; the lowest lane of equals has the
+// lowest index).  c is taken in fp32, and where two that decide something lie nearer to one
+// another than its error bound the token is chosen again in fp64, which is slow here (two fp64
+// operations a cycle and SM: about 5 us a token), so the bound is tight.  Without a bias the order of
+// the c is that of the logits, which are compared themselves.
 //
 // The sort is a count by expert and chunk of tokens, then for each chunk the sum of the counts before
-// it; a thread for each expert (or several, by parts) goes through the chunk's assignments in their
-// order, so that the result does not depend on how the GPU schedules it.  Two launches, or
-// one for up to 32 tokens.  A few bytes a token: bound by the latency of the launches.
+// it.  Within 64 tokens an assignment's place among its expert's is the number of lower bits in the
+// expert's word of tokens, so that the result does not depend on how the GPU schedules it.  Two
+// launches, or one for up to 32 tokens.
 //
 // Combine: HBM-bound, one pass.
 #include <type_traits>
@@ -26,25 +29,43 @@ namespace {
 using fp8::kVec;
 using fp8::Raw8;
 
-constexpr int kMaxChunks = 128;       // of tokens, while a chunk's assignments fit kChunkIds
-constexpr int kChunkIds = 8192;
+constexpr int kMaxChunks = 128;       // of tokens
+constexpr int kWord = 64;             // tokens that are sorted at once
 constexpr int kPlanThreads = 1024;
 constexpr int kOneTokens = 32;        // up to these, one CTA does everything
 
 struct RouteParams {
-  const void *logits; int64_t ld;
+  const void *logits; int dtype; int64_t ld;
   int64_t n_tokens; int n_experts, top_k;
   const float *bias;
   int sigmoid, groups, top_groups, group_top, renormalize;
   int size;                           // experts of a group
+  int each;                           // experts of a lane
+  int lanes;                          // lanes of a group; 0: groups do not begin at lanes
   float scale;
   int32_t *ids; float *weights; int32_t *offsets, *order;
-  uint16_t *counts;                   // [chunks, n_experts]
+  uint32_t *counts;                   // [chunks, pairs]: of two neighbouring experts, 16 bits each (a
+                                      // chunk has at most 2^22 / kMaxChunks tokens)
+  int pairs;
   int chunk;                          // tokens of a chunk
   int chunks;
 };
 
-template <typename C> __device__ __forceinline__ C minus_inf() { return -(C)INFINITY; }
+// Integers in the order of the numbers; none: 0, below all of them.
+__device__ __forceinline__ uint32_t to_key(float c) {
+  const uint32_t b = __float_as_uint(c + 0.0f);   // (-0 counts as 0)
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ uint64_t to_key(double c) {
+  const uint64_t b = (uint64_t)__double_as_longlong(c + 0.0);
+  return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double of_key(uint64_t k) {
+  return __longlong_as_double((int64_t)(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
+}
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -57,44 +78,35 @@ __device__ __forceinline__ C warp_sum(C v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-
-// The largest c of the warp and the lowest index that has it (`e` of a lane without one: any).
-__device__ __forceinline__ void warp_best(float &c, int &e) {
-  const uint32_t b = __float_as_uint(c + 0.0f);  // (-0 counts as 0)
-  const uint32_t key = b & 0x80000000u ? ~b : b | 0x80000000u;
-  const uint32_t top = __reduce_max_sync(0xffffffffu, key);
-  e = (int)__reduce_min_sync(0xffffffffu, key == top ? (uint32_t)e : 0xffffffffu);
-  c = __uint_as_float(top & 0x80000000u ? top & 0x7fffffffu : ~top);
-}
-__device__ __forceinline__ void warp_best(double &c, int &e) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const double oc = __shfl_xor_sync(0xffffffffu, c, o);
-    const int oe = __shfl_xor_sync(0xffffffffu, e, o);
-    if (oc > c || (oc == c && oe < e)) c = oc, e = oe;
-  }
+__device__ __forceinline__ uint32_t warp_max_key(uint32_t k) { return __reduce_max_sync(0xffffffffu, k); }
+__device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return (uint64_t)hi << 32 | lo;
 }
 
-// What a warp found for a token: lane j has the j-th chosen expert (-1: none) and its logit.
+// What a warp found for a token: lane j has the j-th chosen expert (-1: none).
 struct Chosen {
   int id;
-  float x;
-  float top, sum;   // largest logit; sum of exp(logit - top), where it is asked for
+  float top, sum;   // largest logit; sum of exp(logit - top), where the weights need it
 };
 
 // A whole warp chooses a token's experts, c in type C; false where fp32 does not tell.
 template <typename C, int VPL>
 __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams &p, int lane, Chosen &out) {
-  const bool by_logit = !p.bias && p.groups == 1;
+  using K = typename std::conditional<std::is_same<C, float>::value, uint32_t, uint64_t>::type;
+  constexpr bool kSingle = std::is_same<C, float>::value;
+  const bool by_logit = !p.bias;                        // the order of the c is that of the logits
+  const bool scored = !by_logit || (p.groups > 1 && p.group_top > 1);
   bool sure = true;
-  C c[VPL];
+  const int e0 = lane * p.each;
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) top = fmaxf(top, fp8::finite(x[i]) ? x[i] : -INFINITY);
   top = warp_max(top);
   out.top = top;
-  C sum = 0;
-  if (!p.sigmoid && (!by_logit || !p.renormalize)) {
+  C c[VPL], sum = 0;
+  if (!p.sigmoid && (scored || !p.renormalize)) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       c[i] = fp8::finite(x[i]) ? (C)exp((C)x[i] - (C)top) : (C)0;
@@ -103,123 +115,134 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
     sum = warp_sum(sum);
   }
   out.sum = (float)sum;
-  // Error of c in fp32, both sides of a comparison: a sigmoid's is at most 4 2^-24 of max(1, |c|)
-  // (exp 2 ulp, whose effect is a quarter; sum, quotient, addition of the bias), a softmax's has the
-  // sum's (VPL + 5) 2^-24 too.
-  const float tau = p.sigmoid ? 0x1p-20f : (VPL + 16) * 0x1p-23f;
+  // Error of an fp32 c, both sides of a comparison.  A sigmoid's: 2^-24 each from the exponential (2
+  // ulp, a quarter of which gets through), the sum and the quotient.  A softmax's, relative to s,
+  // which is at most 1 / sum: VPL + 5 additions, the exponential's 2^-22 and what rounding its
+  // argument x does, x e^x <= 0.37, the quotient.  And the addition of the bias, 2^-24 |c|.
+  const float tau = p.sigmoid ? 3 * 0x1p-23f : (VPL + 14) * 0x1p-23f / (float)sum;
+  if (scored) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * 32 + lane;
-    if (by_logit) {
-      c[i] = fp8::finite(x[i]) ? (C)x[i] : minus_inf<C>();
-    } else {
+    for (int i = 0; i < VPL; ++i) {
       const C s = p.sigmoid ? (C)1 / ((C)1 + (C)exp(-(C)x[i])) : c[i] / sum;
-      const float b = p.bias && e < p.n_experts ? p.bias[e] : 0.0f;
-      c[i] = fp8::finite(x[i]) && fp8::finite(b) ? s + (C)b : minus_inf<C>();
+      const float b = p.bias && e0 + i < p.n_experts && i < p.each ? p.bias[e0 + i] : 0.0f;
+      c[i] = fp8::finite(x[i]) && fp8::finite(b) ? s + (C)b : -(C)INFINITY;
     }
   }
   auto near = [&](C hi, C lo, float of) {
-    return std::is_same<C, float>::value && !by_logit && lo > minus_inf<C>() &&
-           (float)(hi - lo) <= of * tau * fmaxf(1.0f, fmaxf(fabsf((float)hi), fabsf((float)lo)));
+    return kSingle && (float)(hi - lo) <= of * (tau + 0x1p-23f * fmaxf(fabsf((float)hi), fabsf((float)lo)));
   };
+  K key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    if (by_logit) key[i] = fp8::finite(x[i]) ? to_key((C)x[i]) : 0;
+    else key[i] = c[i] > -(C)INFINITY ? to_key(c[i]) : 0;
+  }
   if (p.groups > 1) {
-    C mine = minus_inf<C>();
-    for (int g = 0; g < p.groups; ++g) {
-      C a = minus_inf<C>(), b = minus_inf<C>();
+    // the group's value in its first lane (or in the lane of its number); 0: nothing to choose in it
+    const bool sums = p.group_top > 1;
+    K value = 0;
+    auto join = [&](K &a, K &b, K oa, K ob) {
+      const K low = oa > a ? a : oa, high = ob > b ? ob : b;
+      a = oa > a ? oa : a;
+      b = low > high ? low : high;
+    };
+    // with sums of scores the keys compared are the scores'; else those of the choice itself
+    auto key_of = [&](int i) -> K { return !by_logit || !sums ? key[i] : key[i] ? to_key(c[i]) : 0; };
+    auto value_of = [&](K a, K b) -> K { return sums && b ? to_key(of_key(a) + of_key(b)) : a; };
+    if (p.lanes > 0) {
+      K a = 0, b = 0;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = i * 32 + lane;
-        if (e >= g * p.size && e < (g + 1) * p.size) {
-          b = c[i] > a ? a : (c[i] > b ? c[i] : b);
-          a = c[i] > a ? c[i] : a;
-        }
-      }
+      for (int i = 0; i < VPL; ++i) join(a, b, key_of(i), 0);
+      for (int o = 1; o < p.lanes; o *= 2) join(a, b, __shfl_xor_sync(0xffffffffu, a, o), __shfl_xor_sync(0xffffffffu, b, o));
+      value = value_of(a, b);
+      if (lane % p.lanes != 0 || lane >= p.lanes * p.groups) value = 0;
+    } else {
+      for (int g = 0; g < p.groups; ++g) {
+        K a = 0, b = 0;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const C oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
-        const C low = oa > a ? a : oa, high = ob > b ? ob : b;
-        a = oa > a ? oa : a;
-        b = low > high ? low : high;
+        for (int i = 0; i < VPL; ++i)
+          if (i < p.each && e0 + i >= g * p.size && e0 + i < (g + 1) * p.size) join(a, b, key_of(i), 0);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) join(a, b, __shfl_xor_sync(0xffffffffu, a, o), __shfl_xor_sync(0xffffffffu, b, o));
+        if (lane == g) value = value_of(a, b);
       }
-      if (lane == g) mine = p.group_top == 2 && b > minus_inf<C>() ? a + b : a;
     }
     uint32_t open = 0;
-    C last = minus_inf<C>();
+    K last = 0;
     for (int j = 0; j <= p.top_groups && j < p.groups; ++j) {
-      C v = mine;
-      int g = lane;
-      warp_best(v, g);
+      const K best = warp_max_key(value);
+      if (best == 0) break;
       if (j == p.top_groups) {
-        if (near(last, v, 2.0f)) sure = false;
-      } else if (v > minus_inf<C>()) {
-        open |= 1u << g;
-        if (lane == g) mine = minus_inf<C>();
-        last = v;
+        if ((!by_logit || sums) && near(of_key(last), of_key(best), sums ? 2.0f : 1.0f)) sure = false;
+        break;
       }
+      const int w = __ffs(__ballot_sync(0xffffffffu, value == best)) - 1;
+      open |= 1u << (p.lanes > 0 ? w / p.lanes : w);
+      if (lane == w) value = 0;
+      last = best;
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (!(open >> ((i * 32 + lane) / p.size & 31) & 1) || i * 32 + lane >= p.n_experts) c[i] = minus_inf<C>();
+      if (!(open >> ((p.lanes > 0 ? lane / p.lanes : (e0 + i) / p.size) & 31) & 1)) key[i] = 0;
   }
   out.id = -1;
-  out.x = 0.0f;
-  C last = minus_inf<C>();
-  for (int j = 0; j <= p.top_k; ++j) {
-    if (j == p.top_k && (by_logit || !std::is_same<C, float>::value)) break;
-    C best = c[0];
-    int e = lane;
-    float of = x[0];
+  K last = 0;
+  // one round more, where the best of the others may be too near to the last chosen
+  const int rounds = p.top_k + (kSingle && !by_logit ? 1 : 0);
+  for (int j = 0; j < rounds; ++j) {
+    K mine = key[0];
 #pragma unroll
-    for (int i = 1; i < VPL; ++i)
-      if (c[i] > best) best = c[i], e = i * 32 + lane, of = x[i];
-    const int own = e;
-    warp_best(best, e);
-    if (!(best > minus_inf<C>())) break;   // (the same in the whole warp)
-    if (j > 0 && near(last, best, 1.0f)) sure = false;
+    for (int i = 1; i < VPL; ++i) mine = key[i] > mine ? key[i] : mine;
+    const K best = warp_max_key(mine);
+    if (best == 0) break;
+    if (kSingle && !by_logit && j > 0 && near(of_key(last), of_key(best), 1.0f)) sure = false;
     last = best;
-    if (j == p.top_k) break;
-    of = __shfl_sync(0xffffffffu, of, e & 31);
-    if (lane == j) out.id = e, out.x = of;
-    if (own == e) {
+    const int w = __ffs(__ballot_sync(0xffffffffu, mine == best)) - 1;
+    int at = 0;
+    if (lane == w) {
+      // the first of the lane's that has it is taken
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i * 32 + lane == e) c[i] = minus_inf<C>();
+      for (int i = VPL - 1; i >= 0; --i) at = key[i] == best ? i : at;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = i == at ? 0 : key[i];
     }
+    at = __shfl_sync(0xffffffffu, at, w);
+    if (lane == j) out.id = w * p.each + at;   // (of the round more: lane top_k, which has none)
   }
+  if (lane >= p.top_k) out.id = -1;
   return sure;
 }
 
 template <typename T, int VPL>
 __device__ __forceinline__ void load_logits(float (&x)[VPL], const RouteParams &p, int64_t t, int lane) {
-  const T *row = (const T *)p.logits + t * p.ld;
+  const T *row = (const T *)p.logits + t * p.ld + lane * p.each;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * 32 + lane;
-    x[i] = e < p.n_experts ? to_f32(row[e]) : -INFINITY;
-  }
+  for (int i = 0; i < VPL; ++i) x[i] = i < p.each && lane * p.each + i < p.n_experts ? to_f32(row[i]) : -INFINITY;
 }
 
-// (apart, so that its registers are not those of every token)
-template <typename T, int VPL>
-__device__ __noinline__ void choose_again(const RouteParams &p, int64_t t, int lane, Chosen &out) {
+// (apart, so that its registers are not those of every token, and for all types of the logits)
+template <int VPL>
+__device__ __noinline__ int choose_again(const RouteParams &p, int64_t t, int lane) {
   float x[VPL];
-  load_logits<T, VPL>(x, p, t, lane);
-  const float sum = out.sum;
+  if (p.dtype == GPTQ_F32) load_logits<float, VPL>(x, p, t, lane);
+  else if (p.dtype == GPTQ_F16) load_logits<__half, VPL>(x, p, t, lane);
+  else load_logits<__nv_bfloat16, VPL>(x, p, t, lane);
+  Chosen out;
   choose<double, VPL>(x, p, lane, out);
-  out.sum = sum;
+  return out.id;
 }
 
-// The weight of this lane's chosen expert.
-__device__ __forceinline__ float weight_of(const Chosen &ch, const RouteParams &p) {
+// The weight of this lane's chosen expert, whose logit is x.
+__device__ __forceinline__ float weight_of(const Chosen &ch, float x, const RouteParams &p) {
   const bool any = ch.id >= 0;
   if (!p.renormalize) {
-    const float s = p.sigmoid ? 1.0f / (1.0f + expf(-ch.x)) : expf(ch.x - ch.top) / ch.sum;
+    const float s = p.sigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - ch.top) / ch.sum;
     return any ? s * p.scale : 0.0f;
   }
   // Relative to the largest chosen, so that not all can vanish: exactly so for a softmax; a
   // sigmoid of less than -60 is exp(x) to 2^-86.
-  const float top = warp_max(any ? ch.x : -INFINITY);
-  const float s = !any ? 0.0f : (p.sigmoid && top > -60.0f) ? 1.0f / (1.0f + expf(-ch.x)) : expf(ch.x - top);
+  const float top = warp_max(any ? x : -INFINITY);
+  const float s = !any ? 0.0f : (p.sigmoid && top > -60.0f) ? 1.0f / (1.0f + expf(-x)) : expf(x - top);
   const float sum = warp_sum(s);
   return any ? s / sum * p.scale : 0.0f;
 }
@@ -229,8 +252,9 @@ __device__ __forceinline__ int route_token(const RouteParams &p, int64_t t, int 
   float x[VPL];
   load_logits<T, VPL>(x, p, t, lane);
   Chosen ch;
-  if (!choose<float, VPL>(x, p, lane, ch)) choose_again<T, VPL>(p, t, lane, ch);
-  const float w = weight_of(ch, p);
+  if (!choose<float, VPL>(x, p, lane, ch)) ch.id = choose_again<VPL>(p, t, lane);
+  const float of = ch.id >= 0 ? to_f32(((const T *)p.logits)[t * p.ld + ch.id]) : 0.0f;
+  const float w = weight_of(ch, of, p);
   if (lane < p.top_k) {
     p.ids[t * p.top_k + lane] = ch.id;
     p.weights[t * p.top_k + lane] = w;
@@ -238,90 +262,106 @@ __device__ __forceinline__ int route_token(const RouteParams &p, int64_t t, int 
   return ch.id;
 }
 
-// A CTA's part of the order: the assignments of chunk `mine`, n of them, go to their places.  `ids`
-// has them in shared memory, 16-byte aligned, -1 up to a multiple of four.  kPlanThreads threads, of
-// which (part, e) counts and places expert e's in one of `parts` runs of them, and adds up one run of
-// the chunks' counts.
+// The order of a chunk's assignments (kPlanThreads threads).
 struct PlanSmem {
-  int a[kPlanThreads], b[kPlanThreads];
+  uint32_t word[2][1024];       // of each expert: which of 64 tokens go to it
+  int at[1024];                 // where its next assignment goes
+  int part[2][kPlanThreads];
   int warp[32];
-  int total;
 };
-__device__ __forceinline__ void plan(const RouteParams &p, int mine, const int *ids, int n, PlanSmem &sm) {
-  int span = 32;
-  while (span < p.n_experts) span *= 2;
-  const int parts = kPlanThreads / span, tid = threadIdx.x, lane = tid % 32;
-  const int part = tid / span, e = tid % span;
-  const int first = mine * p.chunk * p.top_k;
-  const int4 *quads = reinterpret_cast<const int4 *>(ids);
-  const int n4 = (n + 3) / 4, q0 = n4 * part / parts, q1 = n4 * (part + 1) / parts;
-  int here = 0, all = 0, before = 0;
-  for (int q = q0; q < q1; ++q) {
-    const int4 v = quads[q];
-    here += (v.x == e) + (v.y == e) + (v.z == e) + (v.w == e);
-  }
-  if (p.chunks == 1) {
-    all = here;
-  } else if (e < p.n_experts) {
-    const int c0 = p.chunks * part / parts, c1 = p.chunks * (part + 1) / parts;
-#pragma unroll 16
-    for (int c = c0; c < c1; ++c) {
-      const int k = p.counts[(int64_t)c * p.n_experts + e];
-      all += k;
-      before += c < mine ? k : 0;
-    }
-  }
-  sm.a[tid] = all;
-  sm.b[tid] = before;
+
+// The words of the assignments [i0, i1), which belong to the 64 tokens from t0 on.
+__device__ __forceinline__ void fill_words(const RouteParams &p, const int *ids, int i0, int i1, int t0, PlanSmem &sm) {
+  for (int e = threadIdx.x; e < p.n_experts; e += kPlanThreads) sm.word[0][e] = sm.word[1][e] = 0;
   __syncthreads();
-  // threads of part 0: an expert's total, and the sum of those of the experts before it
-  int sum = 0, base = 0;
-  if (part == 0)
-    for (int q = 0; q < parts; ++q) {
-      sum += sm.a[q * span + e];
-      base += sm.b[q * span + e];
+  for (int i = i0 + threadIdx.x; i < i1; i += kPlanThreads) {
+    const int e = ids[i], t = i / p.top_k - t0;
+    if (e >= 0) atomicOr(&sm.word[t >> 5][e], 1u << (t & 31));
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void plan(const RouteParams &p, int mine, const int *ids, PlanSmem &sm) {
+  const int tid = threadIdx.x, lane = tid % 32;
+  const int t0 = mine * p.chunk, t1 = min(t0 + p.chunk, (int)p.n_tokens);
+  fill_words(p, ids, t0 * p.top_k, min(t0 + kWord, t1) * p.top_k, t0, sm);
+  // an expert's assignments in all chunks, and in those before this one
+  int sum = 0, before = 0;
+  if (p.chunks == 1) {
+    if (tid < p.n_experts) sum = __popc(sm.word[0][tid]) + __popc(sm.word[1][tid]);
+  } else {
+    int span = 32;              // threads of a part: each has two experts, and every parts-th chunk
+    while (span < p.pairs) span *= 2;
+    const int parts = kPlanThreads / span, part = tid / span, e2 = tid % span;
+    int all[2] = {0, 0}, pre[2] = {0, 0};
+    if (e2 < p.pairs) {
+#pragma unroll 16
+      for (int c = part; c < p.chunks; c += parts) {
+        const uint32_t two = p.counts[(int64_t)c * p.pairs + e2];
+        all[0] += two & 0xffffu;
+        all[1] += two >> 16;
+        pre[0] += c < mine ? two & 0xffffu : 0;
+        pre[1] += c < mine ? two >> 16 : 0;
+      }
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sm.part[0][tid] = all[h];
+      sm.part[1][tid] = pre[h];
+      __syncthreads();
+      if (tid < p.n_experts && (tid & 1) == h)
+        for (int q = 0; q < parts; ++q) {
+          sum += sm.part[0][q * span + tid / 2];
+          before += sm.part[1][q * span + tid / 2];
+        }
+      __syncthreads();
+    }
+  }
   int scan = sum;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
     const int v = __shfl_up_sync(0xffffffffu, scan, o);
     if (lane >= o) scan += v;
   }
-  if (lane == 31) sm.warp[tid / 32] = scan;   // (warps of other parts: 0)
+  if (lane == 31) sm.warp[tid / 32] = scan;
   __syncthreads();
-  for (int w = 0; w < tid / 32 && part == 0; ++w) scan += sm.warp[w];
-  if (part == 0) {
-    base += scan - sum;
-    if (mine == 0 && e < p.n_experts) {
-      p.offsets[e] = scan - sum;
-      if (e == p.n_experts - 1) p.offsets[e + 1] = scan;
-    }
-    if (e == p.n_experts - 1) sm.total = scan;
+  {
+    const int w = sm.warp[lane];
+    const int below = __reduce_add_sync(0xffffffffu, lane < tid / 32 ? w : 0);
+    scan += below;
   }
-  // where each part's run of an expert begins
-  __syncthreads();
-  sm.a[tid] = here;
-  if (part == 0) sm.b[e] = base;
-  __syncthreads();
-  int at = sm.b[e];
-  for (int q = 0; q < part; ++q) at += sm.a[q * span + e];
-  if (here > 0)   // (-1 is nobody's)
-    for (int q = q0; q < q1; ++q) {
-      const int4 v = quads[q];
-      if (v.x == e) p.order[at++] = first + 4 * q;
-      if (v.y == e) p.order[at++] = first + 4 * q + 1;
-      if (v.z == e) p.order[at++] = first + 4 * q + 2;
-      if (v.w == e) p.order[at++] = first + 4 * q + 3;
+  if (tid < p.n_experts) {
+    sm.at[tid] = scan - sum + before;
+    if (mine == 0) {
+      p.offsets[tid] = scan - sum;
+      if (tid == p.n_experts - 1) p.offsets[tid + 1] = scan;
     }
-  for (int i = first + tid; i < first + n; i += kPlanThreads)
-    if (i >= sm.total) p.order[i] = -1;
+  }
+  const int total = __reduce_add_sync(0xffffffffu, sm.warp[lane]);
+  __syncthreads();
+  for (int w0 = t0; w0 < t1; w0 += kWord) {
+    const int i0 = w0 * p.top_k, i1 = min(w0 + kWord, t1) * p.top_k;
+    if (w0 > t0) fill_words(p, ids, i0, i1, w0, sm);
+    for (int i = i0 + tid; i < i1; i += kPlanThreads) {
+      const int e = ids[i], t = i / p.top_k - w0;
+      if (e >= 0) {
+        const uint32_t lo = sm.word[0][e];
+        const int rank = t < 32 ? __popc(lo & ((1u << t) - 1)) : __popc(lo) + __popc(sm.word[1][e] & ((1u << (t - 32)) - 1));
+        p.order[sm.at[e] + rank] = i;
+      }
+      if (i >= total) p.order[i] = -1;
+    }
+    __syncthreads();
+    if (w0 + kWord < t1 && tid < p.n_experts) sm.at[tid] += __popc(sm.word[0][tid]) + __popc(sm.word[1][tid]);
+    // (fill_words waits for all before the words are filled again)
+  }
 }
 
 // A chunk of tokens for each CTA, a warp for each token in turn; the chunk's counts.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(VPL <= 8 ? 1024 : 512) route_kernel(RouteParams p) {
-  __shared__ int count[VPL * 32];
-  for (int e = threadIdx.x; e < p.n_experts; e += blockDim.x) count[e] = 0;
+  __shared__ int count[VPL * 32 + 2];
+  for (int e = threadIdx.x; e < VPL * 32 + 2; e += blockDim.x) count[e] = 0;
   wait_for_grids();
   launch_dependents();
   __syncthreads();
@@ -332,44 +372,37 @@ __global__ void __launch_bounds__(VPL <= 8 ? 1024 : 512) route_kernel(RouteParam
     if (id >= 0) atomicAdd(&count[id], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.n_experts; e += blockDim.x)
-    p.counts[(int64_t)blockIdx.x * p.n_experts + e] = (uint16_t)count[e];
+  for (int e = threadIdx.x; e < p.pairs; e += blockDim.x)
+    p.counts[(int64_t)blockIdx.x * p.pairs + e] = (uint32_t)count[2 * e] | (uint32_t)count[2 * e + 1] << 16;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(RouteParams p) {
   __shared__ PlanSmem sm;
-  __shared__ __align__(16) int ids[kChunkIds];
   wait_for_grids();
   launch_dependents();
-  const int64_t first = (int64_t)blockIdx.x * p.chunk * p.top_k, end = p.n_tokens * p.top_k;
-  const int n = (int)min((int64_t)p.chunk * p.top_k, end - first);
-  for (int i = threadIdx.x; i < ((n + 3) & ~3); i += kPlanThreads) ids[i] = i < n ? p.ids[first + i] : -1;
-  __syncthreads();
-  plan(p, blockIdx.x, ids, n, sm);
+  plan(p, blockIdx.x, p.ids, sm);
 }
 
 // Both, for a few tokens.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kPlanThreads) route_few_kernel(RouteParams p) {
   __shared__ PlanSmem sm;
-  __shared__ __align__(16) int ids[kOneTokens * 32 + 4];
+  __shared__ int ids[kOneTokens * 32];
   wait_for_grids();
   launch_dependents();
-  const int lane = threadIdx.x % 32, t = threadIdx.x / 32, n = (int)p.n_tokens * p.top_k;
+  const int lane = threadIdx.x % 32, t = threadIdx.x / 32;
   if (t < p.n_tokens) {
     const int id = route_token<T, VPL>(p, t, lane);
     if (lane < p.top_k) ids[t * p.top_k + lane] = id;
   }
-  if (threadIdx.x < 3) ids[n + threadIdx.x] = -1;
   __syncthreads();
-  plan(p, 0, ids, n, sm);
+  plan(p, 0, ids, sm);
 }
 
-int chunk_tokens(int64_t n_tokens, int top_k, int threads) {
+int chunk_tokens(int64_t n_tokens, int threads) {
   int64_t c = ceil_div(n_tokens, kMaxChunks);
   if (c < threads / 32) c = threads / 32;   // (one for each warp)
-  if (c * top_k > kChunkIds) c = kChunkIds / top_k;
-  return (int)c;
+  return (int)(c > kWord ? ceil_div(c, kWord) * kWord : c);
 }
 int route_threads(int64_t n_tokens, int n_experts) { return n_experts > 256 || n_tokens < 2048 ? 512 : 1024; }
 
@@ -422,8 +455,11 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
     float w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      w[j] = j0 + j < p.top_k ? p.weights[t * p.top_k + j0 + j] : 0.0f;
-      if (w[j] != 0.0f) y[j].load((const T *)p.y + (t * p.top_k + j0 + j) * p.ldy + c, n, p.vy);
+      w[j] = 0.0f;
+      if (j0 + j < p.top_k) {
+        y[j].load((const T *)p.y + (t * p.top_k + j0 + j) * p.ldy + c, n, p.vy);
+        w[j] = p.weights[t * p.top_k + j0 + j];
+      }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -443,10 +479,10 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
 
 }  // namespace
 
-size_t moe_route_ws_bytes(int64_t n_tokens, int n_experts, int top_k) {
+size_t moe_route_ws_bytes(int64_t n_tokens, int n_experts, int) {
   if (n_tokens <= kOneTokens && n_experts <= 256) return 256;
-  const int chunk = chunk_tokens(n_tokens, top_k, route_threads(n_tokens, n_experts));
-  return round_up(sizeof(uint16_t) * (size_t)ceil_div(n_tokens, chunk) * n_experts + 1, 256);
+  const int chunk = chunk_tokens(n_tokens, route_threads(n_tokens, n_experts));
+  return round_up(sizeof(uint32_t) * (size_t)ceil_div(n_tokens, chunk) * ((n_experts + 1) / 2) + 1, 256);
 }
 
 gptq_status launch_moe_route(const MoeRouteArgs &g, void *ws, cudaStream_t s) {
@@ -455,16 +491,20 @@ gptq_status launch_moe_route(const MoeRouteArgs &g, void *ws, cudaStream_t s) {
     return GPTQ_OK;
   }
   RouteParams p{};
-  p.logits = g.logits; p.ld = g.ld;
+  p.logits = g.logits; p.dtype = g.dtype; p.ld = g.ld;
   p.n_tokens = g.n_tokens; p.n_experts = g.n_experts; p.top_k = g.top_k;
   p.bias = g.bias;
   p.sigmoid = g.sigmoid; p.groups = g.groups; p.top_groups = g.top_groups; p.group_top = g.group_top;
   p.size = g.n_experts / g.groups;
   p.renormalize = g.renormalize; p.scale = g.scale;
   p.ids = g.ids; p.weights = g.weights; p.offsets = g.offsets; p.order = g.order;
-  p.counts = (uint16_t *)ws;
+  p.counts = (uint32_t *)ws;
+  p.pairs = (g.n_experts + 1) / 2;
+  p.each = (g.n_experts + 31) / 32;
+  // groups of whole lanes whose number is a power of two are joined by exchanges within them
+  if (p.size % p.each == 0 && (p.size / p.each & (p.size / p.each - 1)) == 0) p.lanes = p.size / p.each;
   const int threads = route_threads(g.n_tokens, g.n_experts);
-  p.chunk = g.n_tokens <= kOneTokens && g.n_experts <= 256 ? kOneTokens : chunk_tokens(g.n_tokens, g.top_k, threads);
+  p.chunk = g.n_tokens <= kOneTokens && g.n_experts <= 256 ? kOneTokens : chunk_tokens(g.n_tokens, threads);
   p.chunks = (int)ceil_div(g.n_tokens, p.chunk);
   switch (g.dtype) {
     case GPTQ_F32: return route<float>(p, threads, s);

@@ -1264,7 +1264,8 @@ def fp8_experts(a, a_exps, w, w_exps, offsets, order, w_scale=None, bias=None, a
 
 def moe_combine(y, weights, residual=None, out=None, stream=None):
     """``residual[t] + sum_j weights[t, j] y[t * top_k + j]``, ``[tokens, d]``: the experts' outputs
-    ``y [tokens * top_k, d]`` with ``moe_route``'s weights.  A row whose weight is 0 is not read.
+    ``y [tokens * top_k, d]`` with ``moe_route``'s weights.  A row whose weight is 0 is left out,
+    whatever it holds.
     ``out`` may be the residual."""
     torch = _torch()
     n, top_k = weights.shape
