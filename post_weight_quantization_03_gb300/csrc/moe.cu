@@ -8,8 +8,9 @@
 // lanes where its size allows.  Each of the top_k rounds is a maximum over the lane's own and one
 // over the warp, of integers that are ordered as the c (redux; the lowest lane of equals has the
 // lowest index).  c is taken in fp32, and where two that decide something lie nearer to one
-// another than its error bound the token is chosen again in fp64, which is slow here (two fp64
-// operations a cycle and SM: about 5 us a token), so the bound is tight.  Without a bias the order of
+// another than its error bound fp64 decides.  That is slow here (two operations a cycle and SM), so the
+// bound is tight, and of sigmoids only the few in question are taken again, one in a lane; a softmax's
+// need the sum too, and a sum of a group's the scores (about 10 us a token).  Without a bias the order of
 // the c is that of the logits, which are compared themselves.
 //
 // The sort is a count by expert and chunk of tokens, then for each chunk the sum of the counts before
@@ -88,11 +89,13 @@ __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
 // What a warp found for a token: lane j has the j-th chosen expert (-1: none).
 struct Chosen {
   int id;
+  int near;         // > 0: so many lanes have one, the chosen among them, but fp32 does not tell which
   float top, sum;   // largest logit; sum of exp(logit - top), where the weights need it
 };
 
-// A whole warp chooses a token's experts, c in type C; false where fp32 does not tell.
-template <typename C, int VPL>
+// A whole warp chooses a token's experts, c in type C; false where fp32 does not tell.  LIST: then
+// with the few that are in question.
+template <typename C, int VPL, bool LIST = false>
 __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams &p, int lane, Chosen &out) {
   using K = typename std::conditional<std::is_same<C, float>::value, uint32_t, uint64_t>::type;
   constexpr bool kSingle = std::is_same<C, float>::value;
@@ -186,16 +189,26 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
       if (!(open >> ((p.lanes > 0 ? lane / p.lanes : (e0 + i) / p.size) & 31) & 1)) key[i] = 0;
   }
   out.id = -1;
+  out.near = 0;
+  if (!sure) return false;
+  // fp32: a round more, for the best of the others, which may be too near to the last chosen; or more
+  // while the next is too near, so that what is not among these cannot be chosen
+  const bool watch = kSingle && !by_logit;
+  const int rounds = !watch ? p.top_k : LIST ? 32 : min(p.top_k + 1, 32);
   K last = 0;
-  // one round more, where the best of the others may be too near to the last chosen
-  const int rounds = p.top_k + (kSingle && !by_logit ? 1 : 0);
-  for (int j = 0; j < rounds; ++j) {
+  int j = 0;
+  for (; j < rounds; ++j) {
     K mine = key[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) mine = key[i] > mine ? key[i] : mine;
     const K best = warp_max_key(mine);
     if (best == 0) break;
-    if (kSingle && !by_logit && j > 0 && near(of_key(last), of_key(best), 1.0f)) sure = false;
+    if (watch && j > 0) {
+      const bool close = near(of_key(last), of_key(best), 1.0f);
+      if (close && !LIST) return false;
+      if (j >= p.top_k && !close) break;
+      sure = sure && !close;
+    }
     last = best;
     const int w = __ffs(__ballot_sync(0xffffffffu, mine == best)) - 1;
     int at = 0;
@@ -207,29 +220,53 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
       for (int i = 0; i < VPL; ++i) key[i] = i == at ? 0 : key[i];
     }
     at = __shfl_sync(0xffffffffu, at, w);
-    if (lane == j) out.id = w * p.each + at;   // (of the round more: lane top_k, which has none)
+    if (lane == j) out.id = w * p.each + at;
   }
-  if (lane >= p.top_k) out.id = -1;
-  return sure;
+  if (LIST && j < 32) out.near = j;   // (32 rounds without an end may have left one out)
+  // with 32 to choose there is no round more
+  return sure && !(watch && !LIST && p.top_k == 32 && p.n_experts > 32);
 }
 
+// (the type at run time: a kernel is a long one, and reads a few numbers a lane)
+__device__ __forceinline__ float logit(const RouteParams &p, int64_t at) {
+  if (p.dtype == GPTQ_F32) return ((const float *)p.logits)[at];
+  if (p.dtype == GPTQ_F16) return to_f32(((const __half *)p.logits)[at]);
+  return to_f32(((const __nv_bfloat16 *)p.logits)[at]);
+}
 template <typename T, int VPL>
-__device__ __forceinline__ void load_logits(float (&x)[VPL], const RouteParams &p, int64_t t, int lane) {
+__device__ __forceinline__ void load_logits_of(float (&x)[VPL], const RouteParams &p, int64_t t, int lane) {
   const T *row = (const T *)p.logits + t * p.ld + lane * p.each;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) x[i] = i < p.each && lane * p.each + i < p.n_experts ? to_f32(row[i]) : -INFINITY;
 }
-
-// (apart, so that its registers are not those of every token, and for all types of the logits)
 template <int VPL>
-__device__ __noinline__ int choose_again(const RouteParams &p, int64_t t, int lane) {
-  float x[VPL];
-  if (p.dtype == GPTQ_F32) load_logits<float, VPL>(x, p, t, lane);
-  else if (p.dtype == GPTQ_F16) load_logits<__half, VPL>(x, p, t, lane);
-  else load_logits<__nv_bfloat16, VPL>(x, p, t, lane);
-  Chosen out;
-  choose<double, VPL>(x, p, lane, out);
-  return out.id;
+__device__ __forceinline__ void load_logits(float (&x)[VPL], const RouteParams &p, int64_t t, int lane) {
+  if (p.dtype == GPTQ_F32) load_logits_of<float>(x, p, t, lane);
+  else if (p.dtype == GPTQ_F16) load_logits_of<__half>(x, p, t, lane);
+  else load_logits_of<__nv_bfloat16>(x, p, t, lane);
+}
+
+// A sigmoid's c of the few that are too near to one another, in fp64, one in a lane; their order.
+__device__ __forceinline__ int sort_near(const RouteParams &p, int64_t t, int lane, const Chosen &ch) {
+  const int id = ch.id;
+  uint64_t key = 0;
+  if (lane < ch.near) {
+    const double x = logit(p, t * p.ld + id);
+    key = to_key(1.0 / (1.0 + exp(-x)) + (p.bias ? (double)p.bias[id] : 0.0));
+  }
+  int rank = 0;
+  for (int j = 0; j < ch.near; ++j) {
+    const uint64_t k = __shfl_sync(0xffffffffu, key, j);
+    const int i = __shfl_sync(0xffffffffu, id, j);
+    rank += k > key || (k == key && i < id);
+  }
+  int mine = -1;
+  for (int j = 0; j < p.top_k; ++j) {
+    const uint32_t who = __ballot_sync(0xffffffffu, lane < ch.near && rank == j);
+    const int i = __shfl_sync(0xffffffffu, id, who ? __ffs(who) - 1 : 0);
+    if (lane == j && who) mine = i;
+  }
+  return mine;
 }
 
 // The weight of this lane's chosen expert, whose logit is x.
@@ -247,13 +284,25 @@ __device__ __forceinline__ float weight_of(const Chosen &ch, float x, const Rout
   return any ? s / sum * p.scale : 0.0f;
 }
 
-template <typename T, int VPL>
+// This lane's expert of the token (-1: none); -2 in all lanes, and nothing written, where fp32 does not
+// tell, unless AGAIN.
+template <int VPL, bool AGAIN>
 __device__ __forceinline__ int route_token(const RouteParams &p, int64_t t, int lane) {
   float x[VPL];
-  load_logits<T, VPL>(x, p, t, lane);
+  load_logits(x, p, t, lane);
   Chosen ch;
-  if (!choose<float, VPL>(x, p, lane, ch)) ch.id = choose_again<VPL>(p, t, lane);
-  const float of = ch.id >= 0 ? to_f32(((const T *)p.logits)[t * p.ld + ch.id]) : 0.0f;
+  if (!choose<float, VPL, AGAIN>(x, p, lane, ch)) {
+    if constexpr (!AGAIN) return -2;
+    if (p.sigmoid && ch.near > 0) {
+      ch.id = sort_near(p, t, lane, ch);
+    } else {
+      const float sum = ch.sum;
+      choose<double, VPL>(x, p, lane, ch);
+      ch.sum = sum;
+    }
+  }
+  if (lane >= p.top_k) ch.id = -1;
+  const float of = ch.id >= 0 ? logit(p, t * p.ld + ch.id) : 0.0f;
   const float w = weight_of(ch, of, p);
   if (lane < p.top_k) {
     p.ids[t * p.top_k + lane] = ch.id;
@@ -358,7 +407,7 @@ __device__ __forceinline__ void plan(const RouteParams &p, int mine, const int *
 }
 
 // A chunk of tokens for each CTA, a warp for each token in turn; the chunk's counts.
-template <typename T, int VPL>
+template <int VPL>
 __global__ void __launch_bounds__(VPL <= 8 ? 1024 : 512) route_kernel(RouteParams p) {
   __shared__ int count[VPL * 32 + 2];
   for (int e = threadIdx.x; e < VPL * 32 + 2; e += blockDim.x) count[e] = 0;
@@ -367,9 +416,18 @@ __global__ void __launch_bounds__(VPL <= 8 ? 1024 : 512) route_kernel(RouteParam
   __syncthreads();
   const int lane = threadIdx.x % 32;
   const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
-  for (int i = threadIdx.x / 32; i < p.chunk && t0 + i < p.n_tokens; i += blockDim.x / 32) {
-    const int id = route_token<T, VPL>(p, t0 + i, lane);
-    if (id >= 0) atomicAdd(&count[id], 1);
+  const int step = blockDim.x / 32, end = (int)min((int64_t)p.chunk, p.n_tokens - t0);
+  for (int i0 = threadIdx.x / 32; i0 < end; i0 += 32 * step) {
+    uint32_t again = 0;   // of the warp's next 32 tokens: those for fp64 (apart: its registers are not theirs)
+    for (int k = 0; k < 32 && i0 + k * step < end; ++k) {
+      const int id = route_token<VPL, false>(p, t0 + i0 + k * step, lane);
+      if (id == -2) again |= 1u << k;
+      else if (id >= 0) atomicAdd(&count[id], 1);
+    }
+    for (; again; again &= again - 1) {
+      const int id = route_token<VPL, true>(p, t0 + i0 + (__ffs(again) - 1) * step, lane);
+      if (id >= 0) atomicAdd(&count[id], 1);
+    }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < p.pairs; e += blockDim.x)
@@ -384,7 +442,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(RouteParams p) {
 }
 
 // Both, for a few tokens.
-template <typename T, int VPL>
+template <int VPL>
 __global__ void __launch_bounds__(kPlanThreads) route_few_kernel(RouteParams p) {
   __shared__ PlanSmem sm;
   __shared__ int ids[kOneTokens * 32];
@@ -392,7 +450,8 @@ __global__ void __launch_bounds__(kPlanThreads) route_few_kernel(RouteParams p) 
   launch_dependents();
   const int lane = threadIdx.x % 32, t = threadIdx.x / 32;
   if (t < p.n_tokens) {
-    const int id = route_token<T, VPL>(p, t, lane);
+    int id = route_token<VPL, false>(p, t, lane);
+    if (id == -2) id = route_token<VPL, true>(p, t, lane);
     if (lane < p.top_k) ids[t * p.top_k + lane] = id;
   }
   __syncthreads();
@@ -406,23 +465,13 @@ int chunk_tokens(int64_t n_tokens, int threads) {
 }
 int route_threads(int64_t n_tokens, int n_experts) { return n_experts > 256 || n_tokens < 2048 ? 512 : 1024; }
 
-template <typename T, int VPL>
+template <int VPL>
 gptq_status route_of(const RouteParams &p, int threads, cudaStream_t s) {
   if constexpr (VPL <= 8)
     if (p.n_tokens <= kOneTokens)
-      return launch_early(route_few_kernel<T, VPL>, dim3(1), dim3(kPlanThreads), 0, 1, s, p);
-  GPTQ_TRY(launch_early(route_kernel<T, VPL>, dim3((unsigned)p.chunks), dim3(threads), 0, 1, s, p));
+      return launch_early(route_few_kernel<VPL>, dim3(1), dim3(kPlanThreads), 0, 1, s, p);
+  GPTQ_TRY(launch_early(route_kernel<VPL>, dim3((unsigned)p.chunks), dim3(threads), 0, 1, s, p));
   return launch_early(plan_kernel, dim3((unsigned)p.chunks), dim3(kPlanThreads), 0, 1, s, p);
-}
-template <typename T>
-gptq_status route(const RouteParams &p, int threads, cudaStream_t s) {
-  const int e = p.n_experts;
-  if (e <= 32) return route_of<T, 1>(p, threads, s);
-  if (e <= 64) return route_of<T, 2>(p, threads, s);
-  if (e <= 128) return route_of<T, 4>(p, threads, s);
-  if (e <= 256) return route_of<T, 8>(p, threads, s);
-  if (e <= 512) return route_of<T, 16>(p, threads, s);
-  return route_of<T, 32>(p, threads, s);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -506,11 +555,12 @@ gptq_status launch_moe_route(const MoeRouteArgs &g, void *ws, cudaStream_t s) {
   const int threads = route_threads(g.n_tokens, g.n_experts);
   p.chunk = g.n_tokens <= kOneTokens && g.n_experts <= 256 ? kOneTokens : chunk_tokens(g.n_tokens, threads);
   p.chunks = (int)ceil_div(g.n_tokens, p.chunk);
-  switch (g.dtype) {
-    case GPTQ_F32: return route<float>(p, threads, s);
-    case GPTQ_F16: return route<__half>(p, threads, s);
-    default: return route<__nv_bfloat16>(p, threads, s);
-  }
+  if (p.each == 1) return route_of<1>(p, threads, s);
+  if (p.each == 2) return route_of<2>(p, threads, s);
+  if (p.each <= 4) return route_of<4>(p, threads, s);
+  if (p.each <= 8) return route_of<8>(p, threads, s);
+  if (p.each <= 16) return route_of<16>(p, threads, s);
+  return route_of<32>(p, threads, s);
 }
 
 gptq_status launch_moe_combine(const void *y, int dtype, int64_t ldy, int64_t n_tokens, int top_k,
