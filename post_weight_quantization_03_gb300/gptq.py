@@ -726,15 +726,13 @@ def _fp8_empty(rows, d, row_block, device, stream):
     """Codes and exponents of a ``[rows, d]`` e4m3 matrix, in the pitches the library asks for."""
     torch = _torch()
     pitch, kb = (d + 15) & ~15, (d + FP8_BLOCK - 1) // FP8_BLOCK
-    codes = torch.empty((rows, pitch), dtype=torch.float8_e4m3fn, device=device)
     erows, epitch = (rows + row_block - 1) // row_block, (kb + 3) & ~3
-    exps = torch.empty((erows, epitch), dtype=torch.uint8, device=device)
+    # (one torch operation each: in a loop of calls every one takes 3 us of host time.  The kernels read
+    # a last row's exponents by words; torch's allocations end at multiples of 512 bytes)
+    codes = torch.empty_strided((rows, d), (pitch, 1), dtype=torch.float8_e4m3fn, device=device)
+    exps = torch.empty_strided((erows, kb), (epitch, 1), dtype=torch.uint8, device=device)
     if stream is not None:
         _lend(stream, codes, exps)
-    if pitch != d:
-        codes = codes.as_strided((rows, d), (pitch, 1))
-    if epitch != kb:
-        exps = exps.as_strided((erows, kb), (epitch, 1))
     return codes, pitch, exps, epitch
 
 
@@ -1040,35 +1038,52 @@ def _fp8_a(a, a_exps, a_scale):
 def _fp8_w(name, w, exps, scale, bias, k, gpu, n=None, experts=None):
     """``(n, struct)`` of a product's weights, one matrix or (``experts``) one for each."""
     torch = _torch()
-    shape, st, es = w.shape, w.stride(), exps.stride()
-    if len(shape) != (2 if experts is None else 3):
-        raise ValueError(f"{name} must be [{'' if experts is None else 'experts, '}n, k]")
-    rows = shape[-2]
-    head = () if experts is None else (experts,)
-    kb, nb = (k + FP8_BLOCK - 1) // FP8_BLOCK, (rows + FP8_BLOCK - 1) // FP8_BLOCK
-    if shape != (*head, rows, k) or (n is not None and rows != n) or st[-1] != 1:
-        raise ValueError(f"{name} must be row-major {[*head, 'n' if n is None else n, k]}")
-    if exps.shape != (*head, nb, kb) or (es[-1] != 1 and kb != 1):
-        raise ValueError(f"the exponents of {name} must be row-major {[*head, nb, kb]}")
+    shape, st, eshape, es = w.shape, w.stride(), exps.shape, exps.stride()
+    kb = (k + FP8_BLOCK - 1) // FP8_BLOCK
+    if experts is None:
+        if len(shape) != 2 or shape[1] != k or st[1] != 1 or (n is not None and shape[0] != n):
+            raise ValueError(f"{name} must be a row-major [{'n' if n is None else n}, {k}] matrix")
+        rows, ld, next_codes = shape[0], st[0], 0
+        nb = (rows + FP8_BLOCK - 1) // FP8_BLOCK
+        if len(eshape) != 2 or eshape[0] != nb or eshape[1] != kb or (es[1] != 1 and kb != 1):
+            raise ValueError(f"the exponents of {name} must be a row-major [{nb}, {kb}] matrix")
+        lde, next_exps = es[0], 0
+        vector = (rows,)
+    else:
+        if len(shape) != 3 or shape[0] != experts or shape[2] != k or st[2] != 1 \
+                or (n is not None and shape[1] != n):
+            raise ValueError(f"{name} must be row-major [{experts}, {'n' if n is None else n}, {k}]")
+        rows, ld, next_codes = shape[1], st[1], st[0]
+        nb = (rows + FP8_BLOCK - 1) // FP8_BLOCK
+        if len(eshape) != 3 or eshape[0] != experts or eshape[1] != nb or eshape[2] != kb \
+                or (es[2] != 1 and kb != 1):
+            raise ValueError(f"the exponents of {name} must be row-major [{experts}, {nb}, {kb}]")
+        lde, next_exps = es[1], es[0]
+        vector = (experts, rows)
+    # a matrix of one row may have any pitch
+    if rows == 1:
+        ld = max(ld, (k + 15) & ~15)
+    if nb == 1:
+        lde = max(lde, (kb + 3) & ~3)
     if w.dtype != torch.float8_e4m3fn or exps.dtype != torch.uint8:
         raise TypeError("codes are float8_e4m3fn and exponents uint8")
     if w.get_device() != gpu or exps.get_device() != gpu:
         raise ValueError(_ONE_GPU)
-    given = []
-    for what, t in (("scale", scale), ("bias", bias)):
-        if t is None:
-            given.append(None)
-            continue
-        if t.dtype != torch.float32 or t.shape != (*head, rows) or not t.is_contiguous():
-            raise ValueError(f"the {what} of {name} must be contiguous float32 {[*head, rows]}")
-        if t.get_device() != gpu:
-            raise ValueError(_ONE_GPU)
-        given.append(t.data_ptr())
-    # a matrix of one row may have any pitch
-    ld = st[-2] if rows > 1 else max(st[-2], (k + 15) & ~15)
-    lde = es[-2] if nb > 1 else max(es[-2], (kb + 3) & ~3)
-    return rows, Fp8Weights(w.data_ptr(), ld, st[0] if experts else 0, exps.data_ptr(), lde,
-                            es[0] if experts else 0, *given)
+    scale_ptr = bias_ptr = None
+    if scale is not None:
+        scale_ptr = _vector(name, "scale", scale, vector, gpu, torch.float32)
+    if bias is not None:
+        bias_ptr = _vector(name, "bias", bias, vector, gpu, torch.float32)
+    return rows, Fp8Weights(w.data_ptr(), ld, next_codes, exps.data_ptr(), lde, next_exps, scale_ptr,
+                            bias_ptr)
+
+
+def _vector(name, what, t, shape, gpu, f32):
+    if t.dtype != f32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"the {what} of {name} must be contiguous float32 {list(shape)}")
+    if t.get_device() != gpu:
+        raise ValueError(_ONE_GPU)
+    return t.data_ptr()
 
 
 def _act(act):
