@@ -750,6 +750,20 @@ gptq_status gptq_fp8_experts(const uint8_t *a, int64_t lda, const uint8_t *a_exp
                              size_t ws_bytes, gptq_stream_t stream);
 
 /*
+ * gptq_debug_fp8_gated_lost_copy: test hook of the bounded device waits of the products above, as
+ * gptq_debug_fp8_matmul_lost_copy: gptq_fp8_experts_gated, or with n_experts = 0 gptq_fp8_gated
+ * (offsets and order are then not read, and top_k is 1), with copy number lost_copy of every CTA (128
+ * elements of K of both weights and, of gptq_fp8_gated, of A) left out and every wait limited to
+ * wait_ns.  SYNCHRONIZES `stream` and returns the device status.  Errors: as the regular calls.
+ */
+gptq_status gptq_debug_fp8_gated_lost_copy(
+    const uint8_t *a, int64_t lda, const uint8_t *a_exps, int64_t ldae, const gptq_fp8_weights *gate,
+    const gptq_fp8_weights *up, int act, int n_experts, const int32_t *offsets,
+    const int32_t *order, int top_k, int64_t n_tokens, int64_t n, int64_t k, uint8_t *codes,
+    int64_t ldc, uint8_t *exps, int64_t lde, int64_t lost_copy, uint64_t wait_ns, void *ws,
+    size_t ws_bytes, gptq_stream_t stream);
+
+/*
  * gptq_moe_combine: out[t] = residual[t] + sum_j weights[t, j] y[t * top_k + j], summed in fp32 in
  * that order and rounded once.  A row whose weight is 0 is left out, whatever it holds.
  *   y [n_tokens * top_k, ldy], residual [n_tokens, ldr] or NULL, out [n_tokens, ldo] of dtype (F16,

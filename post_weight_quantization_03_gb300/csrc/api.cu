@@ -519,6 +519,28 @@ gptq_status gptq_fp8_experts(const uint8_t *a, int64_t lda, const uint8_t *a_exp
   return fp8_linear_checked(g, ws, ws_bytes, stream);
 }
 
+gptq_status gptq_debug_fp8_gated_lost_copy(
+    const uint8_t *a, int64_t lda, const uint8_t *a_exps, int64_t ldae, const gptq_fp8_weights *gate,
+    const gptq_fp8_weights *up, int act, int n_experts, const int32_t *offsets,
+    const int32_t *order, int top_k, int64_t n_tokens, int64_t n, int64_t k, uint8_t *codes,
+    int64_t ldc, uint8_t *exps, int64_t lde, int64_t lost_copy, uint64_t wait_ns, void *ws,
+    size_t ws_bytes, gptq_stream_t stream) {
+  if (!gate || !up || n_experts < 0 || top_k < 1 || top_k > kMaxTopK || (n_experts == 0 && top_k != 1) ||
+      n_tokens < 1 || n_tokens > kFp8MaxRows || !lost_ok(lost_copy, wait_ns))
+    return GPTQ_ERR_INVALID_ARG;
+  Fp8LinearArgs g{};
+  g.a = a; g.lda = lda; g.ae = a_exps; g.ldae = ldae; g.a_rows = n_tokens;
+  g.w[0] = *gate; g.w[1] = *up; g.gated = true;
+  g.act = act;
+  g.M = n_tokens * top_k; g.N = n; g.K = k;
+  g.out = codes; g.ldo = ldc; g.oe = exps; g.ldoe = lde;
+  g.n_experts = n_experts; g.offsets = offsets; g.order = order; g.top_k = top_k;
+  g.wait_ns = wait_ns;
+  g.lost = lost_copy;
+  GPTQ_TRY(fp8_linear_checked(g, ws, ws_bytes, stream));
+  return gptq_workspace_status(ws, stream);
+}
+
 size_t gptq_moe_route_workspace_bytes(int64_t n_tokens, int n_experts, int top_k) {
   if (n_tokens < 0 || n_experts < 1 || n_experts > kMaxExperts || top_k < 1 || top_k > kMaxTopK ||
       n_tokens > kFp8MaxRows / top_k)

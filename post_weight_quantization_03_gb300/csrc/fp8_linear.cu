@@ -318,7 +318,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
     // ---------------- token rows by index ----------------
     // A copy of a warp takes four rows of 128 bytes; the MMA's swizzle exchanges a row's 16-byte
     // pieces by its number modulo 8.  Zeros past K, and for positions that name no row.
-    constexpr int kQuads = kMaxTnGated / 4 / kLoaders;
+    constexpr int kQuads = (kMaxTnGated / 4 + kLoaders - 1) / kLoaders;   // copies of a lane
     const int piece = lane % 8, sub = lane / 8;
     // where the lane's piece goes, of its first copy: quads are 512 bytes, which the warps take in turn
     const int row0 = (warp - 3 - E) * 4 + sub;

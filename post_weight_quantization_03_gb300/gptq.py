@@ -138,6 +138,11 @@ _SIGS = {
     "gptq_moe_combine": (_c.c_int, [_c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int,
                                     _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_void_p,
                                     _c.c_int64, _c.c_void_p]),
+    "gptq_debug_fp8_gated_lost_copy": (_c.c_int, [
+        _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64, _Weights, _Weights, _c.c_int, _c.c_int,
+        _c.c_void_p, _c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p,
+        _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_uint64, _c.c_void_p, _c.c_size_t,
+        _c.c_void_p]),
     "gptq_debug_fp8_matmul_lost_copy": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
                                                    _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
                                                    _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p,
@@ -389,6 +394,14 @@ def gptq_moe_route(logits, dtype, ld, n_tokens, n_experts, top_k, bias, scores, 
 def gptq_moe_combine(y, dtype, ldy, n_tokens, top_k, d, weights, residual, ldr, out, ldo, stream):
     return load().gptq_moe_combine(y, dtype, ldy, n_tokens, top_k, d, weights, residual, ldr, out,
                                    ldo, stream)
+
+
+def gptq_debug_fp8_gated_lost_copy(a, lda, a_exps, ldae, gate, up, act, n_experts, offsets, order, top_k,
+                                   n_tokens, n, k, codes, ldc, exps, lde, lost_copy, wait_ns, ws,
+                                   ws_bytes, stream):
+    return load().gptq_debug_fp8_gated_lost_copy(a, lda, a_exps, ldae, gate, up, act, n_experts, offsets,
+                                                 order, top_k, n_tokens, n, k, codes, ldc, exps, lde,
+                                                 lost_copy, wait_ns, ws, ws_bytes, stream)
 
 
 def gptq_debug_fp8_matmul_lost_copy(a, lda, a_exps, ldae, w, ldw, w_exps, ldwe, m, n, k, out, odtype,

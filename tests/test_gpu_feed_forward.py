@@ -139,6 +139,18 @@ def test_linear_onto_its_residual_in_a_wider_buffer_and_again(m, n, k):
         assert torch.equal(out, gptq.fp8_linear(*args, residual=r[:, pad:pad + n].to(DEV)))
 
 
+@pytest.mark.parametrize("m", [15, 16, 17, 100, 111, 112, 113, 150, 224, 239, 240, 241, 400, 480, 700])
+def test_tiles_of_every_size(m):
+    n, k = 130, 300
+    a, ae = _fp8_matrix(m, m, k, 1, 0.5)
+    w = _weights(1, n, k)
+    dev = _on_dev(w)
+    want, tol = _want_linear(a, ae, w, None, "relu", None, k)
+    _check16(gptq.fp8_linear(_dev_codes(a), _dev_exps(ae), dev[0], dev[1], None, dev[2], act="relu"), want, tol)
+    want, tol = _want_gated(a, ae, w, w, None, "silu", k)
+    _check_codes(*gptq.fp8_gated(_dev_codes(a), _dev_exps(ae), dev, dev), want, tol)
+
+
 def test_linear_without_an_epilogue_is_the_product():
     for m, n, k in ((1, 513, 4096), (70, 300, 1500), (515, 1000, 640)):
         a, ae = _fp8_matrix(1, m, k, 1, 0.5)
@@ -343,6 +355,27 @@ def test_experts_gated(tokens, experts, top_k, n, k, kind):
             t = order[lo:hi] // top_k
             want, tol = _want_gated(a[t], ae[t], gate[e], up[e], ra[t], "silu", k)
             _check_codes(codes[lo:hi], exps[lo:hi], want, tol)
+
+
+@pytest.mark.parametrize("tokens", [15, 16, 17, 31, 48, 65, 80, 96, 97, 104, 111, 112, 113, 150, 220, 224, 240, 241, 330, 336, 448, 670, 1000])
+def test_experts_tiles_of_every_size(tokens):
+    """One expert of `tokens` rows and a second of a few: tiles of all sizes, and rows at every place in them."""
+    n, k, few = 130, 300, 5
+    a, ae = _fp8_matrix(tokens, tokens + few, k, 1, 0.5)
+    order = np.random.default_rng(tokens).permutation(tokens + few).astype(np.int32)
+    order[:tokens].sort()
+    order[tokens:].sort()
+    offsets = np.array([0, tokens, tokens + few], np.int32)
+    ws = [_weights(1, n, k), _weights(2, n, k)]
+    dev = _experts_on_dev(ws)
+    codes, exps = gptq.fp8_experts_gated(_dev_codes(a), _dev_exps(ae), dev, dev, _dev(offsets), _dev(order), 1)
+    out = gptq.fp8_experts(_dev_codes(a), _dev_exps(ae), dev[0], dev[1], _dev(offsets), _dev(order), dev[2])
+    for e, (lo, hi) in enumerate(((0, tokens), (tokens, tokens + few))):
+        t = order[lo:hi]
+        want, tol = _want_gated(a[t], ae[t], ws[e], ws[e], None, "silu", k)
+        _check_codes(codes[lo:hi], exps[lo:hi], want, tol)
+        want, tol = _want_linear(a[lo:hi], ae[lo:hi], ws[e], None, None, None, k)
+        _check16(out[torch.from_numpy(t.astype(np.int64)).to(DEV)], want, tol)
 
 
 @pytest.mark.parametrize("tokens,experts,top_k,n,k", EXPERTS)

@@ -1,0 +1,266 @@
+"""The feed-forward operators as programs use them: in graphs, on several streams at once, between guard
+bytes, in a layer of experts, and where a device wait runs out."""
+
+import ctypes
+import math
+import time
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving_oracle as SO
+from post_weight_quantization_03_gb300 import build_lib, decoder, gptq
+from tests.test_gpu_canaries import PAT, Guarded
+from tests.test_gpu_feed_forward import _dev, _experts_on_dev, _on_dev, _routes, _weights
+from tests.test_gpu_serving import DEV, DT, _dev_codes, _dev_exps, _fp8_matrix, _randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build_lib.build()
+    gptq.load()
+    torch.cuda.init()
+
+
+def _p(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _u8(t):
+    return t.view(torch.uint8)
+
+
+class _Block:
+    """A block of experts on operands of its own."""
+
+    def __init__(self, seed, tokens, experts, top_k, d, n):
+        self.top_k = top_k
+        self.x = _randn(seed, tokens, d, dtype="bf16").to(DEV)
+        self.norm = (1 + 0.1 * _randn(seed + 1, d)).to(torch.bfloat16).to(DEV)
+        self.router = (_randn(seed + 2, experts, d) / math.sqrt(d)).to(DEV)
+        self.gate, self.up, self.down = (
+            _experts_on_dev([_weights(s + i, *shape) for i in range(experts)]) for s, shape in ((10, (n, d)), (200, (n, d)), (400, (d, n))))
+
+    def __call__(self, stream=None):
+        codes, exps, rstd, _ = gptq.rmsnorm_fp8(self.x, self.norm, stream=stream)
+        logits = self.x.float() @ self.router.t() if stream is None else self.logits
+        ids, w, offsets, order = gptq.moe_route(logits, self.top_k, stream=stream)
+        inner = gptq.fp8_experts_gated(codes, exps, self.gate, self.up, offsets, order, self.top_k, rstd, stream=stream)
+        y = gptq.fp8_experts(*inner, self.down[0], self.down[1], offsets, order, self.down[2], stream=stream)
+        return gptq.moe_combine(y, w, self.x, stream=stream)
+
+
+@pytest.mark.parametrize("tokens", [1, 20, 300])
+def test_a_captured_block_follows_its_inputs(tokens):
+    block = _Block(1, tokens, 8, 2, 256, 200)
+    other = _randn(50, tokens, 256, dtype="bf16").to(DEV)
+    first = block().clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = block()
+    graph.replay()
+    assert torch.equal(out, first)
+    before = block.x.clone()
+    block.x.copy_(other)
+    want = block().clone()
+    graph.replay()
+    assert torch.equal(out, want) and not torch.equal(out, first)
+    block.x.copy_(before)
+    graph.replay()
+    assert torch.equal(out, first)
+    gptq.serving_status()
+
+
+def test_blocks_on_two_streams_at_once():
+    blocks = [_Block(1, 40, 8, 2, 256, 200), _Block(7, 333, 16, 4, 384, 130)]
+    want = [b().clone() for b in blocks]
+    for b in blocks:
+        b.logits = b.x.float() @ b.router.t()
+    streams = [torch.cuda.Stream() for _ in blocks]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(20):
+        for i, (b, s) in enumerate(zip(blocks, streams)):
+            got[i].append(b(s))
+    torch.cuda.synchronize()
+    for outs, w in zip(got, want):
+        assert all(torch.equal(o, w) for o in outs)
+    gptq.serving_status()
+
+
+def test_calls_repeat():
+    a, ae = _fp8_matrix(3, 500, 512, 1, 0.5)
+    w = [_weights(10 + i, 384, 512) for i in range(8)]
+    _, offsets, order = _routes(4, 500, 8, 2)
+    ew = _experts_on_dev(w)
+    args = (_dev_codes(a), _dev_exps(ae), ew, ew, _dev(offsets), _dev(order), 2)
+    c, e = gptq.fp8_experts_gated(*args)
+    for _ in range(5):
+        c2, e2 = gptq.fp8_experts_gated(*args)
+        assert torch.equal(_u8(c), _u8(c2)) and torch.equal(e, e2)
+
+
+# ---------------------------------------------------------------------------------------
+# Guard bytes
+# ---------------------------------------------------------------------------------------
+
+def _struct(w, experts=False):
+    codes, exps, scale, bias = w
+    st, es = codes.stride(), exps.stride()
+    return gptq.Fp8Weights(codes.data_ptr(), st[-2], st[0] if experts else 0, exps.data_ptr(), es[-2], es[0] if experts else 0,
+                           None if scale is None else scale.data_ptr(), None if bias is None else bias.data_ptr())
+
+
+def _ok(st):
+    assert st == 0, gptq.gptq_status_str(st)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1, 16), (3, 130, 200), (17, 257, 1000), (130, 640, 384), (300, 1999, 96), (1, 512, 4096)])
+def test_products_write_their_rows_alone(m, n, k):
+    a, ae = _fp8_matrix(m + k, m, k, 1, 0.5)
+    w = _on_dev(_weights(n + k, n, k, bias=True))
+    A, AE = _dev_codes(a), _dev_exps(ae)
+    ws = gptq.workspace(256, DEV)
+    tail = (_p(ws), 256, gptq._stream(None))
+    for extra in (0, 3, 4):
+        out = Guarded(m * (n + extra) * 2)
+        r = _randn(1, m, n + 1, dtype="bf16").to(DEV)
+        _ok(gptq.gptq_fp8_linear(_p(A), A.stride(0), _p(AE), AE.stride(0), None, _struct(w), 2, _p(r), n + 1, m, n, k, out.ptr, 1, n + extra,
+                                 *tail))
+        assert out.intact() and bool((out.view(torch.uint8, (m, (n + extra) * 2))[:, n * 2:] == PAT).all())
+        ldc, lde = -(-n // 16) * 16 + 16 * (extra > 0), -(-(-(-n // 128)) // 4) * 4 + 4 * (extra > 0)
+        codes, exps = Guarded(m * ldc), Guarded(m * lde)
+        _ok(gptq.gptq_fp8_gated(_p(A), A.stride(0), _p(AE), AE.stride(0), None, _struct(w), _struct(w), 2, m, n, k, codes.ptr, ldc, exps.ptr,
+                                lde, *tail))
+        assert codes.intact() and exps.intact()
+        assert bool((codes.view(torch.uint8, (m, ldc))[:, n:] == PAT).all())
+        assert bool((exps.view(torch.uint8, (m, lde))[:, -(-n // 128):] == PAT).all())
+
+
+@pytest.mark.parametrize("tokens,experts,top_k,n,k", [(1, 4, 2, 200, 300), (40, 16, 4, 130, 256), (300, 3, 1, 257, 128)])
+def test_experts_write_their_rows_alone(tokens, experts, top_k, n, k):
+    rows = tokens * top_k
+    _, offsets, order = _routes(1, tokens, experts, top_k, dropped=True)
+    a, ae = _fp8_matrix(2, rows, k, 1, 0.5)
+    w = _experts_on_dev([_weights(10 + i, n, k) for i in range(experts)])
+    A, AE, O, R = _dev_codes(a), _dev_exps(ae), _dev(offsets), _dev(order)
+    ws = gptq.workspace(256, DEV)
+    tail = (_p(ws), 256, gptq._stream(None))
+    ldc, lde, nb = -(-n // 16) * 16 + 16, -(-(-(-n // 128)) // 4) * 4 + 4, -(-n // 128)
+    codes, exps, out = Guarded(rows * ldc), Guarded(rows * lde), Guarded(rows * (n + 3) * 2)
+    _ok(gptq.gptq_fp8_experts_gated(_p(A), A.stride(0), _p(AE), AE.stride(0), None, _struct(w, True), _struct(w, True), 2, experts, _p(O), _p(R),
+                                    top_k, tokens, n, k, codes.ptr, ldc, exps.ptr, lde, *tail))
+    _ok(gptq.gptq_fp8_experts(_p(A), A.stride(0), _p(AE), AE.stride(0), _struct(w, True), 0, experts, _p(O), _p(R), rows, n, k, out.ptr, 1, n + 3,
+                              *tail))
+    used = int(offsets[-1])
+    assert codes.intact() and exps.intact() and out.intact()
+    c, e = codes.view(torch.uint8, (rows, ldc)), exps.view(torch.uint8, (rows, lde))
+    assert bool((c[:, n:] == PAT).all()) and bool((c[used:] == PAT).all()) and bool((e[:, nb:] == PAT).all()) and bool((e[used:] == PAT).all())
+    o = out.view(torch.uint8, (rows, (n + 3) * 2))
+    unnamed = torch.from_numpy(np.setdiff1d(np.arange(rows), order[:used])).to(DEV)
+    assert bool((o[:, n * 2:] == PAT).all()) and bool((o[unnamed] == PAT).all())
+
+
+@pytest.mark.parametrize("tokens,experts,top_k,d", [(1, 7, 3, 5), (33, 100, 8, 130), (3000, 17, 2, 64), (9000, 64, 4, 8)])
+def test_routing_and_combine_write_their_rows_alone(tokens, experts, top_k, d):
+    logits = _randn(1, tokens, experts).to(DEV)
+    ids, w = Guarded(tokens * top_k * 4), Guarded(tokens * top_k * 4)
+    offsets, order = Guarded((experts + 1) * 4), Guarded(tokens * top_k * 4)
+    need = gptq.gptq_moe_route_workspace_bytes(tokens, experts, top_k)
+    ws = Guarded(need)
+    _ok(gptq.gptq_moe_route(_p(logits), 2, experts, tokens, experts, top_k, None, 1, 1, 1, 1, 1, 1.0, ids.ptr, w.ptr, offsets.ptr, order.ptr,
+                            ws.ptr, need, gptq._stream(None)))
+    assert all(g.intact() for g in (ids, w, offsets, order, ws))
+    y, out = _randn(2, tokens * top_k, d, dtype="bf16").to(DEV), Guarded(tokens * (d + 3) * 2)
+    _ok(gptq.gptq_moe_combine(_p(y), 1, d, tokens, top_k, d, w.ptr, None, 0, out.ptr, d + 3, gptq._stream(None)))
+    assert out.intact() and bool((out.view(torch.uint8, (tokens, (d + 3) * 2))[:, d * 2:] == PAT).all())
+
+
+# ---------------------------------------------------------------------------------------
+# Waits that run out
+# ---------------------------------------------------------------------------------------
+
+TIMEOUT, BUDGET = 4, 50_000_000
+
+
+@pytest.mark.parametrize("experts,tokens,top_k,n,k", [(0, 1, 1, 256, 4096), (0, 300, 1, 2000, 512), (4, 1, 2, 256, 2048), (8, 500, 2, 640, 1024)])
+@pytest.mark.parametrize("copy", [0, 3])
+def test_a_wait_that_gives_up(experts, tokens, top_k, n, k, copy):
+    rows = tokens * top_k
+    a, ae = _fp8_matrix(1, tokens, k, 1, 0.5)
+    A, AE = _dev_codes(a), _dev_exps(ae)
+    w = _experts_on_dev([_weights(10 + i, n, k) for i in range(experts)]) if experts else _on_dev(_weights(10, n, k))
+    _, offsets, order = _routes(1, tokens, max(experts, 1), top_k) if experts else (None, None, None)
+    O, R = (_dev(offsets), _dev(order)) if experts else (None, None)
+    ws = gptq.workspace(256, DEV)
+    codes = torch.zeros(rows, -(-n // 16) * 16, dtype=torch.uint8, device=DEV)
+    exps = torch.zeros(rows, -(-n // 512) * 4, dtype=torch.uint8, device=DEV)
+
+    def regular():
+        if experts:
+            return gptq.fp8_experts_gated(A, AE, w, w, O, R, top_k, ws=ws)
+        return gptq.fp8_gated(A, AE, w, w, ws=ws)
+
+    want = regular()
+    gptq.serving_status()
+    t = time.monotonic()
+    st = gptq.gptq_debug_fp8_gated_lost_copy(_p(A), A.stride(0), _p(AE), AE.stride(0), _struct(w, bool(experts)), _struct(w, bool(experts)), 2,
+                                             experts, _p(O), _p(R), top_k, tokens, n, k, _p(codes), codes.stride(0), _p(exps), exps.stride(0),
+                                             copy, BUDGET, _p(ws), 256, gptq._stream(None))
+    assert st == TIMEOUT and time.monotonic() - t < 5
+    with pytest.raises(gptq.GptqError, match="TIMEOUT"):
+        gptq.serving_status()
+    gptq.serving_status()
+    again = regular()
+    assert torch.equal(_u8(again[0]), _u8(want[0])) and torch.equal(again[1], want[1])
+    assert gptq.gptq_workspace_status(_p(ws), gptq._stream(None)) == 0
+
+
+# ---------------------------------------------------------------------------------------
+# A layer of experts
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("hidden,mlp,experts,routing", [
+    (256, 200, 4, dict(top_k=2)), (256, 128, 8, dict(top_k=3, scores="sigmoid", groups=4, top_groups=2, scale=1.5)),
+    (512, 96, 12, dict(top_k=1, renormalize=False))])
+def test_a_layer_of_experts(hidden, mlp, experts, routing):
+    heads, kv_heads, dim = 4, 2, 64
+    weights, (n1, n2) = decoder.random_layer(hidden, mlp, heads, kv_heads, dim, experts=experts)
+    calib = _randn(3, 2, 160, hidden, dtype="bf16").to(DEV)
+    layer = decoder.ExpertsLayer.quantize(weights, n1, n2, calib, heads, kv_heads, 4, routing=routing)
+    for codes, exps, scale in layer.experts.values():
+        v = codes.float()
+        assert codes.shape[0] == experts and torch.equal(v, v.round()) and float(v.abs().max()) <= 15 and bool((exps == 127).all())
+    # the feed-forward part on hidden states given to it, against fp32 on the same weights
+    h = _randn(4, 90, hidden, dtype="bf16").to(DEV)
+    codes, exps, rstd, _ = gptq.rmsnorm_fp8(h, n2, eps=layer.eps)
+    got = layer._feed_forward(codes, exps, rstd, h).float()
+    w = layer.dequantized()
+    g = h.float() * torch.rsqrt(h.float().square().mean(-1, keepdim=True) + layer.eps) * n2.float()
+    dense = (torch.nn.functional.silu(g @ w["gate"].t()) * (g @ w["up"].t())) @ w["down"].t()
+    branch = dense + decoder.experts_reference(w, routing, g)
+    # operands of e4m3 on the way: 2^-5.3 of the norm each for the normed rows (which count twice, in both
+    # factors) and the inner ones
+    err = float((got - (h.float() + branch)).norm())
+    assert err <= 3 ** 0.5 * 2 ** -5.3 * float(branch.norm()) + 2.0 ** -8 * float(h.float().norm())
+    # a whole layer in steps
+    seqs, total = 2, 70
+    x = _randn(5, seqs, total, hidden, dtype="bf16").to(DEV)
+    cache = gptq.kv8_cache(seqs * 2, kv_heads, dim)
+    table = torch.arange(seqs * 2, dtype=torch.int32, device=DEV).view(seqs, 2)
+    at = 0
+    for new in (50, 1, 1, 18):
+        start = torch.full((seqs,), at, dtype=torch.int32, device=DEV)
+        out = layer.step(x[:, at:at + new], cache, table, start, start + new)
+        assert out.shape == (seqs, new, hidden) and bool(torch.isfinite(out.float()).all())
+        at += new
+    gptq.serving_status()
+
+
+def test_the_decoder_command_runs_experts(capsys):
+    decoder.main(["--hidden", "256", "--mlp", "256", "--heads", "4", "--dim", "64", "--prompt", "40", "--tokens", "3", "--experts", "4"])
+    assert "quantized weights" in capsys.readouterr().out
