@@ -7,11 +7,13 @@
 //
 //   warp 0     : TMA producer: (gate, up, tokens) of 128 bytes x rows per k-block
 //   warp 1     : TMEM allocator + MMA issuer (one lane)
-//   then       : 4 (gated) or 8 warps of epilogue, one weight row per thread; one warp that makes up
-//                the scales; 8 warps that copy token rows (the experts' gated product)
+//   warps 2..9 : epilogue, two warps for each 32 weight rows, which take tokens in turn
+//   warp 10    : scales
+//   11..18     : copy token rows (the experts' gated product)
 //
 // Gated: a tile has 128 rows of both weights and two accumulators, so the 128 outputs that share an
-// exponent are one column of the tile: a maximum over each warp (redux) and one over the four.
+// exponent are one column of the tile.  A warp turns 32 rows by 16 tokens around in shared memory, so
+// that two lanes have a token's 32 outputs; their maximum meets those of three other warps.
 //
 // Experts: a tile is (expert, up to tn of its positions, 128 weight rows).  Each CTA counts the
 // tiles from the offsets by itself.  The gated product takes its token rows by index, the other takes
@@ -21,8 +23,7 @@
 // rows takes about 80 cycles, 2300 for a k-block whose MMAs take 770 (4096 tokens of 64 experts, 4096
 // x 1376: 709 us).
 //
-// An epilogue warp turns its 32 rows by 32 tokens around in shared memory, so that a store writes
-// 64 contiguous bytes of four tokens.
+// 16-bit outputs are turned around likewise, so that a store writes 64 contiguous bytes of four tokens.
 //
 // Few tokens leave few tiles; the k-blocks of a tile are then split over a cluster of up to 8
 // CTAs, whose partial sums meet through distributed shared memory in rank order.
@@ -49,11 +50,14 @@ constexpr int kScaleStages = 4;             // groups of four k-blocks in flight
 constexpr uint32_t kScaleBytes = 4 * 512;   // weights, second weights, tokens 0..127, tokens 128..239
 constexpr uint32_t kScaleCols = 16;         // TMEM columns of one group
 constexpr int kMaxStages = 12;
+constexpr int kBox = 64;                    // rows of A in a copy of the experts' plain product, at most
 constexpr int kMaxExperts = 1024;
 constexpr int64_t kAcross = 16;            // (about as many tiles along the tokens run with them)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kRingBytes = 4 * (BM + kMaxTn) * BK;
-constexpr uint32_t kTurnBytes = 8 * 16 * 32 * 4;   // each epilogue warp's 16 tokens x 32 rows
+constexpr int kEpilogue = 8;                // warps
+constexpr int kTurnPitch = 36;              // (words in different banks along either way)
+constexpr uint32_t kTurnBytes = kEpilogue * 16 * kTurnPitch * 4;   // each warp's 16 tokens x 32 rows
 constexpr size_t kSmemBesides = 1024 + kTurnBytes + kScaleStages * kScaleBytes + 2 * 256 * 4 + 2 * 4 * 32 * 4 + 512;
 constexpr size_t kPlanBytes = 2 * (kMaxExperts + 4) * sizeof(int);
 static_assert(2 * kMaxTn + 2 * kScaleCols <= kTmemCols, "TMEM columns");
@@ -74,11 +78,11 @@ struct Params {
   int kb;               // k-blocks
   int wide;             // rows of the output and the residual allow 8 bytes at a time
   int tn, stages;
+  int box;              // rows of A that a copy takes (experts' plain product)
   int n_w, n_m;         // tiles along the weights; along the tokens (not of experts)
   int across;           // tiles along the weights that are gone through for all tokens before the next
   int splits;           // CTAs of a cluster that share a tile's k-blocks
   int acc_cols;         // columns of an accumulator
-  int buffers;          // sets of accumulators
   int tmem_cols;
   const int32_t *offsets, *order;
   int n_experts, top_k;
@@ -206,12 +210,8 @@ __device__ __forceinline__ void make_plan(const Params &p, const Plan &plan, int
 }
 
 // TO: type of the output, if it is not gated.
-// Warps of the epilogue: two for each 32 rows, which take 32 tokens in turn; gated one, which the
-// MMAs of two weights hide (and whose registers, with the loaders', would not go round).
-template <bool GATED>
-constexpr int kEpilogue = GATED ? 4 : 8;
 template <bool GATED, bool EXPERTS>
-constexpr int kThreadsOf = 32 * (3 + kEpilogue<GATED> + (GATED && EXPERTS ? kLoaders : 0));
+constexpr int kThreadsOf = 32 * (3 + kEpilogue + (GATED && EXPERTS ? kLoaders : 0));
 
 template <typename TO, bool GATED, bool EXPERTS>
 __global__ void __launch_bounds__(kThreadsOf<GATED, EXPERTS>, 1)
@@ -219,15 +219,15 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
               const __grid_constant__ CUtensorMap ma, Params p, DevStatus *st) {
   constexpr int W = GATED ? 2 : 1;
   constexpr bool GATHER = GATED && EXPERTS;
-  constexpr int E = kEpilogue<GATED>;
+  constexpr int E = kEpilogue;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   float *turned = (float *)(ring + kRingBytes);
   uint8_t *sscale = (uint8_t *)turned + kTurnBytes;
   float *sra = (float *)(sscale + kScaleStages * kScaleBytes);   // [256] of each token: factor,
   int *srow = (int *)(sra + 256);                                // row of the output (-1: none)
-  float *smax = (float *)(srow + 256);                           // [2][4 warps][32 tokens]
-  uint64_t *full = (uint64_t *)(smax + 2 * 4 * 32);
+  float *smax = (float *)(srow + 256);                           // [2 halves][2][4 warps][16 tokens]
+  uint64_t *full = (uint64_t *)(smax + 2 * 2 * 4 * 16);
   uint64_t *empty = full + kMaxStages;
   uint64_t *sfull = empty + kMaxStages;
   uint64_t *sempty = sfull + kScaleStages;
@@ -279,7 +279,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
   if (blockIdx.x == 0 && threadIdx.x == 0) st->status = 0;
   const int n_tiles = p.n_w * (EXPERTS ? plan.tiles[p.n_experts] : p.n_m);
   const uint32_t set_cols = (uint32_t)(W * p.acc_cols);          // accumulators of a tile
-  const uint32_t sc_cols = tmem + (uint32_t)p.buffers * set_cols;
+  const uint32_t sc_cols = tmem + 2 * set_cols;
 
   bool ok = true;                   // false once a wait has given up: the role ends
   int s = 0, n = 0;                 // producer and issuer: stage of the ring; copies
@@ -295,7 +295,8 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
         const Tile tile = tile_of<EXPERTS>(p, plan, t);
         // rows that the MMA reads: of experts, whole groups of 16
         const int rows = EXPERTS ? (tile.cols + 15) / 16 * 16 : p.tn;
-        const uint32_t bytes = (uint32_t)(W * BM + (GATHER ? 0 : rows)) * BK;
+        const int copied = GATHER ? 0 : EXPERTS ? (rows + p.box - 1) / p.box * p.box : rows;
+        const uint32_t bytes = (uint32_t)(W * BM + copied) * BK;
         for (int kb = k0; kb < k1; ++kb) {
           ok = tc::mbar_wait_compact(&empty[s], ph, waits);
           if (!ok) break;
@@ -307,7 +308,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
           if constexpr (!EXPERTS) {
             tc::tma_load_2d(base + W * BM * BK, &ma, kb * BK, tile.m0, &full[s]);
           } else if constexpr (!GATHER) {
-            for (int j = 0; j < rows; j += 16)
+            for (int j = 0; j < copied; j += p.box)
               tc::tma_load_2d(base + (W * BM + j) * BK, &ma, kb * BK, tile.m0 + j, &full[s]);
           }
           if (++s == p.stages) s = 0, ph ^= 1;
@@ -377,7 +378,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
     ph = 0;
 #pragma unroll 1
     for (int t = first; t < n_tiles && ok; t += step, ++it) {
-      const int b = p.buffers > 1 ? it & 1 : 0, use = p.buffers > 1 ? it >> 1 : it;
+      const int b = it & 1, use = it >> 1;   // accumulators in turn
       const int rows = EXPERTS ? (tile_of<EXPERTS>(p, plan, t).cols + 15) / 16 * 16 : p.tn;
       const uint32_t idesc = mx::instr_desc(rows);
       ok = tc::mbar_wait_compact(&tempty[b], (use & 1) ^ 1, waits);
@@ -465,7 +466,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
     const int q = warp & 3, lrow = q * 32 + lane, et = threadIdx.x - 64, half = (warp - 2) / 4;
     int it = 0, turn = 0;
     for (int t = first; t < n_tiles; t += step, ++it) {
-      const int b = p.buffers > 1 ? it & 1 : 0, use = p.buffers > 1 ? it >> 1 : it;
+      const int b = it & 1, use = it >> 1;   // accumulators in turn
       const Tile tile = tile_of<EXPERTS>(p, plan, t);
       const int64_t nn = (int64_t)tile.n * BM + lrow;
       const bool in = nn < p.N;
@@ -494,37 +495,109 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
       const int64_t n4 = (int64_t)tile.n * BM + q * 32 + lane % 8 * 4;
       uint2 res[8];
       auto ask = [&](int c) {
-        if (GATED || !wide || !p.residual || p.splits > 1) return;
+        if constexpr (!GATED) {
+          if (!wide || !p.residual || p.splits > 1) return;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c + lane / 8 + 4 * i < tile.cols)
-            res[i] = *reinterpret_cast<const uint2 *>((const TO *)p.residual + (int64_t)(tile.m0 + c + lane / 8 + 4 * i) * p.ldr + n4);
+          for (int i = 0; i < 8; ++i)
+            if (c + lane / 8 + 4 * i < tile.cols)
+              res[i] = *reinterpret_cast<const uint2 *>((const TO *)p.residual + (int64_t)(tile.m0 + c + lane / 8 + 4 * i) * p.ldr + n4);
+        }
       };
       ask(32 * half);
       ok = tc::mbar_wait_compact(&tfull[b], use & 1, waits);
       if (!tc::named_barrier_and(1, 32 * E, ok)) break;
       tc::tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * set_cols;
+      float *mine = turned + (warp - 2) * 16 * kTurnPitch;     // this warp's to turn
+      if (p.splits > 1) {
+        float *part = (float *)ring + lrow;
 #pragma unroll 1
-      for (int c = 32 * half; c < tile.cols; c += 8 * E) {
-        uint32_t r[W][32];
+        for (int c = 16 * half; c < tile.cols; c += 32) {
 #pragma unroll
-        for (int w = 0; w < W; ++w) tc::tmem_ld32(acc + w * p.acc_cols + (uint32_t)c, r[w]);
-        if (p.splits > 1) {
-          tc::tmem_ld_wait();
-          float *part = (float *)ring + lrow;
+          for (int w = 0; w < W; ++w) {
+            uint32_t r[16];
+            tc::tmem_ld16(acc + w * p.acc_cols + (uint32_t)c, r);
+            tc::tmem_ld_wait();
 #pragma unroll
-          for (int w = 0; w < W; ++w)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c + i < p.tn) part[(w * p.tn + c + i) * BM] = __uint_as_float(r[w][i]);
-          continue;
+            for (int i = 0; i < 16; ++i) part[(w * p.tn + c + i) * BM] = __uint_as_float(r[i]);   // (tn: whole 16s)
+          }
         }
+      } else if constexpr (GATED) {
+#pragma unroll 1
+        for (int c = 16 * half; c < tile.cols; c += 32) {
+          uint32_t r[W][16];
+#pragma unroll
+          for (int w = 0; w < W; ++w) tc::tmem_ld16(acc + w * p.acc_cols + (uint32_t)c, r[w]);
+          tc::tmem_ld_wait();
+          float v[16], u[16];
+          const float4 *ra4 = reinterpret_cast<const float4 *>(sra + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 f = ra4[i];
+            const float fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[4 * i + j] = fmaf(__uint_as_float(r[0][4 * i + j]) * rw[0], fs[j], bias[0]);
+              u[4 * i + j] = fmaf(__uint_as_float(r[W - 1][4 * i + j]) * rw[W - 1], fs[j], bias[W - 1]);
+            }
+          }
+          activate(v, p.act);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mine[i * kTurnPitch + lane] = in ? v[i] * u[i] : 0.0f;
+          __syncwarp();
+          // this lane's token, and 16 of the warp's 32 rows
+          const int token = lane % 16, rows16 = lane / 16 * 16;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4 *>(&v[4 * i]) = *reinterpret_cast<const float4 *>(mine + token * kTurnPitch + rows16 + 4 * i);
+          auto largest = [&]() {
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
+            return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          };
+          float most = largest();
+          if (__any_sync(0xffffffffu, most == INFINITY)) {
+            // infinities become NaN, which a maximum passes over
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = fp8::inf_to_nan(v[i]);
+            most = largest();
+          }
+          float *sm = smax + (half * 2 + (turn++ & 1)) * 64;
+          if (lane < 16) sm[q * 16 + lane] = most;
+          tc::named_barrier(3 + half, 128);
+          most = fmaxf(fmaxf(sm[token], sm[16 + token]), fmaxf(sm[32 + token], sm[48 + token]));
+          const int ex = fp8::block_exponent(most);
+          const float inv = fp8::pow2(-ex);
+          if (c + token < tile.cols) {
+            const int64_t row = tile.m0 + c + token;
+            const int64_t n16 = (int64_t)tile.n * BM + q * 32 + rows16;
+            if (q == 0 && lane < 16) p.oe[row * p.ldoe + tile.n] = (uint8_t)(ex + fp8::kBias);
+            uint4 codes;
+            codes.x = fp8::pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+            codes.y = fp8::pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+            codes.z = fp8::pack4(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv);
+            codes.w = fp8::pack4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv);
+            uint8_t *o = (uint8_t *)p.out + row * p.ldo + n16;   // (rows of codes are 16-byte aligned)
+            if (n16 + 16 <= p.N) {
+              *reinterpret_cast<uint4 *>(o) = codes;
+            } else {
+              const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (n16 + i < p.N) o[i] = (uint8_t)(word[i / 4] >> (8 * (i % 4)));
+            }
+          }
+          __syncwarp();
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 32 * half; c < tile.cols; c += 64) {
+          uint32_t r[W][32];
+          tc::tmem_ld32(acc + (uint32_t)c, r[0]);
         float v[32];
         const int left = tile.cols - c;                      // tokens of this chunk, if below 32
-        float *mine = turned + (warp - 2) * 16 * 32;         // this warp's to turn
         const float4 *ra4 = reinterpret_cast<const float4 *>(sra + c);
-        if constexpr (!GATED) {
           tc::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -539,18 +612,18 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
             uint2 add[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) add[i] = res[i];
-            ask(c + 8 * E);
+            ask(c + 64);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {                    // 16 tokens at a time
 #pragma unroll
-              for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = v[16 * h + i];
+              for (int i = 0; i < 16; ++i) mine[i * kTurnPitch + lane] = v[16 * h + i];
               __syncwarp();
 #pragma unroll
               for (int i = 4 * h; i < 4 * h + 4; ++i) {
                 const int j = lane / 8 + 4 * i;
                 const int64_t row = EXPERTS ? srow[c + j] : tile.m0 + c + j;
                 if (j >= left || (EXPERTS && row < 0)) continue;
-                float4 x = *reinterpret_cast<const float4 *>(mine + (j - 16 * h) * 32 + lane % 8 * 4);
+                float4 x = *reinterpret_cast<const float4 *>(mine + (j - 16 * h) * kTurnPitch + lane % 8 * 4);
                 if (p.residual) {
                   const TO *r4 = reinterpret_cast<const TO *>(&add[i]);
                   x.x += to_f32(r4[0]);
@@ -572,59 +645,6 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
               ((TO *)p.out)[row * p.ldo + nn] = out_f32<TO>(x);
             }
           }
-        } else {
-          tc::tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 f = ra4[i];
-            const float fs[4] = {f.x, f.y, f.z, f.w};
-            float u[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v[4 * i + j] = fmaf(__uint_as_float(r[0][4 * i + j]) * rw[0], fs[j], bias[0]);
-              u[j] = fmaf(__uint_as_float(r[1][4 * i + j]) * rw[1], fs[j], bias[1]);
-              r[1][4 * i + j] = __float_as_uint(u[j]);
-            }
-          }
-          activate(v, p.act);
-          float *sm = smax + (turn++ & 1) * 128;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            v[i] *= __uint_as_float(r[1][i]);
-            const uint32_t most = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(fp8::finite_abs(v[i])) : 0u);
-            if (lane == i) sm[q * 32 + i] = __uint_as_float(most);
-          }
-          tc::named_barrier(3, 128);
-          // this lane has token c + lane's exponent
-          const float most = fmaxf(fmaxf(sm[lane], sm[32 + lane]), fmaxf(sm[64 + lane], sm[96 + lane]));
-          const int ex = fp8::block_exponent(most);
-          if (q == 0 && lane < left)
-            p.oe[(int64_t)(tile.m0 + c + lane) * p.ldoe + tile.n] = (uint8_t)(ex + fp8::kBias);
-          uint8_t *o = (uint8_t *)p.out + (int64_t)(tile.m0 + c) * p.ldo;
-          uint8_t *codes = reinterpret_cast<uint8_t *>(mine);      // [32 tokens][32 rows]
-          const float inv = fp8::pow2(-ex);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float s0 = __shfl_sync(0xffffffffu, inv, i), s1 = __shfl_sync(0xffffffffu, inv, i + 1);
-            const uint32_t two = fp8::pack2(fp8::inf_to_nan(v[i]) * s0, fp8::inf_to_nan(v[i + 1]) * s1);
-            codes[i * 32 + lane] = (uint8_t)two;
-            codes[(i + 1) * 32 + lane] = (uint8_t)(two >> 8);
-          }
-          __syncwarp();
-          if (wide) {
-            // (rows of codes are 16-byte aligned)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int j = lane / 2 + 16 * i;
-              if (j < left)
-                *reinterpret_cast<uint4 *>(o + j * p.ldo + (int64_t)tile.n * BM + q * 32 + lane % 2 * 16) =
-                    *reinterpret_cast<const uint4 *>(codes + j * 32 + lane % 2 * 16);
-            }
-          } else if (in) {
-#pragma unroll 4
-            for (int j = 0; j < 32 && j < left; ++j) o[j * p.ldo + nn] = codes[j * 32 + lane];
-          }
-          __syncwarp();
         }
       }
       tc::tc_fence_before();
@@ -786,7 +806,7 @@ Shape choose(const Fp8LinearArgs &g, int dev, int sms) {
   const double once = ((double)g.M + W * used * g.N) * g.K / 3500.0;
   Shape best{16, 1};
   double best_t = 1e30;
-  for (int tn = 16; tn <= most; tn += 16) {
+  for (int tn = 16; tn <= most; tn += EXPERTS && !GATED && tn >= kBox ? kBox : 16) {
     if (!EXPERTS && tn - 16 >= g.M) break;
     const double per = EXPERTS ? rows / tn + 0.5 : (double)ceil_div(g.M, (int64_t)tn);   // tiles along the tokens
     const double tiles = n_w * used * (per < 1.0 ? 1.0 : per);
@@ -841,7 +861,6 @@ gptq_status run(const Fp8LinearArgs &g, DevStatus *st, cudaStream_t s) {
   const int64_t tiles = p.n_w * along;   // at most
   if (tiles * 8 > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
   p.acc_cols = sh.tn;
-  p.buffers = 2;
   p.tmem_cols = (int)kTmemCols;
   p.offsets = g.offsets; p.order = g.order;
   p.n_experts = g.n_experts; p.top_k = g.top_k;
@@ -849,6 +868,7 @@ gptq_status run(const Fp8LinearArgs &g, DevStatus *st, cudaStream_t s) {
   p.lost = (int)g.lost;
   const int fit = (int)(kRingBytes / (uint32_t)((W * BM + sh.tn) * BK));
   p.stages = fit < kMaxStages ? fit : kMaxStages;
+  p.box = sh.tn < kBox ? sh.tn : kBox;   // (tn is a multiple of it)
   const int64_t mats = EXPERTS ? g.n_experts : 1;
   CUtensorMap mw[2], ma;
   for (int w = 0; w < W; ++w)
@@ -857,7 +877,7 @@ gptq_status run(const Fp8LinearArgs &g, DevStatus *st, cudaStream_t s) {
       return GPTQ_ERR_UNSUPPORTED;
   if (W == 1) mw[1] = mw[0];
   if (!tc::make_tmap_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, g.a_rows, g.K, g.lda, BK,
-                        EXPERTS ? 16 : sh.tn))
+                        EXPERTS ? p.box : sh.tn))
     return GPTQ_ERR_UNSUPPORTED;
   const int64_t ctas = sh.splits > 1 ? tiles * sh.splits : (tiles < sms ? tiles : sms);
   return launch_early(linear_kernel<TO, GATED, EXPERTS>, dim3((unsigned)ctas), dim3(kThreadsOf<GATED, EXPERTS>), smem_bytes(EXPERTS),
