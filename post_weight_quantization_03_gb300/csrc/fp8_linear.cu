@@ -464,32 +464,48 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
   } else if (warp >= 2 && warp < 2 + E) {
     // ---------------- epilogue ----------------
     const int q = warp & 3, lrow = q * 32 + lane, et = threadIdx.x - 64, half = (warp - 2) / 4;
+    static_assert(32 * E >= kMaxTn, "a thread has one token's factors");
     int it = 0, turn = 0;
-    for (int t = first; t < n_tiles; t += step, ++it) {
-      const int b = it & 1, use = it >> 1;   // accumulators in turn
-      const Tile tile = tile_of<EXPERTS>(p, plan, t);
-      const int64_t nn = (int64_t)tile.n * BM + lrow;
-      const bool in = nn < p.N;
-      // the warp's 32 rows are all there, and rows of the output allow 8 bytes at a time (codes do)
-      const bool wide = (p.wide || GATED) && (int64_t)tile.n * BM + q * 32 + 32 <= p.N;
-      if (p.splits == 1) {
-        tc::named_barrier(2, 32 * E);  // the previous tile's factors have been read
-        for (int j = et; j < tile.cols; j += 32 * E) {
-          const int pos = tile.m0 + j, r = a_row<GATHER>(p, pos);
-          sra[j] = p.ra && r < p.a_rows ? p.ra[r] : 1.0f;
-          if constexpr (EXPERTS && !GATED) {
-            const int o = p.order[pos];
-            srow[j] = o >= 0 && o < p.M ? o : -1;
-          }
+    // factors of the next tile, asked for while this one is worked on: of token `et`, and of this row
+    Tile next;
+    float next_ra = 1.0f, next_rw[W], next_bias[W];
+    int next_row = -1;
+    auto fetch = [&](int t) {
+      next = tile_of<EXPERTS>(p, plan, t);
+      if (p.splits == 1 && et < next.cols) {
+        const int pos = next.m0 + et, r = a_row<GATHER>(p, pos);
+        next_ra = p.ra && r < p.a_rows ? p.ra[r] : 1.0f;
+        if constexpr (EXPERTS && !GATED) {
+          const int o = p.order[pos];
+          next_row = o >= 0 && o < p.M ? o : -1;
         }
       }
-      float rw[W], bias[W];
+      const int64_t nn = (int64_t)next.n * BM + lrow, at = (int64_t)next.e * p.N + nn;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const int64_t at = (int64_t)tile.e * p.N + nn;
-        rw[w] = p.rw[w] && in ? p.rw[w][at] : 1.0f;
-        bias[w] = p.bias[w] && in ? p.bias[w][at] : 0.0f;
+        next_rw[w] = p.rw[w] && nn < p.N ? p.rw[w][at] : 1.0f;
+        next_bias[w] = p.bias[w] && nn < p.N ? p.bias[w][at] : 0.0f;
       }
+    };
+    if (first < n_tiles) fetch(first);
+    for (int t = first; t < n_tiles; t += step, ++it) {
+      const int b = it & 1, use = it >> 1;   // accumulators in turn
+      const Tile tile = next;
+      const int64_t nn = (int64_t)tile.n * BM + lrow;
+      const bool in = nn < p.N;
+      // the warp's 32 rows are all there, and rows of the output allow 8 bytes at a time
+      const bool wide = p.wide && (int64_t)tile.n * BM + q * 32 + 32 <= p.N;
+      float rw[W], bias[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) rw[w] = next_rw[w], bias[w] = next_bias[w];
+      if (p.splits == 1) {
+        tc::named_barrier(2, 32 * E);  // the previous tile's factors have been read
+        if (et < tile.cols) {
+          sra[et] = next_ra;
+          if constexpr (EXPERTS && !GATED) srow[et] = next_row;
+        }
+      }
+      if (t + step < n_tiles) fetch(t + step);
       // the lane's four outputs of the tokens lane / 8, + 4, ... of a chunk; their residuals are asked
       // for a chunk ahead
       const int64_t n4 = (int64_t)tile.n * BM + q * 32 + lane % 8 * 4;
