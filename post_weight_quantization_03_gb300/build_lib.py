@@ -1,23 +1,28 @@
-"""Builds ``libgptq.so`` (the C-ABI CUDA library) in-tree with nvcc for sm_103a.
+"""Builds ``libgptq.so`` (the C-ABI CUDA library) in-tree with nvcc for sm_103a, and ``_marshal.so``
+(the compiled part of the Python binding, against torch's headers).
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel into ``_build/``, then linked
-into ``post_weight_quantization_03_gb300/libgptq.so``.  Rebuilds only when a source or
-header is newer than the library.  Usage: ``python -m post_weight_quantization_03_gb300.build_lib``.
+into ``post_weight_quantization_03_gb300/libgptq.so``; ``csrc/marshal.cpp`` likewise.  Rebuilds only
+when a source or header is newer than both.  Usage: ``python -m
+post_weight_quantization_03_gb300.build_lib``.
 """
 
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgptq.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -37,15 +42,32 @@ def _sources():
 
 
 def _inputs():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(CSRC, "marshal.cpp")] + \
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def _marshal_commands(nvcc, obj, out):
+    """Compiler and linker calls of ``_marshal.so``."""
+    cxx = os.environ.get("CXX") or shutil.which("g++")
+    spec = importlib.util.find_spec("torch")
+    if not cxx or spec is None:
+        raise RuntimeError("g++ and torch are required to build _marshal.so")
+    torch = list(spec.submodule_search_locations)[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(torch, "lib")
+    return ([cxx, "-O2", "-std=c++17", "-fPIC", *(f"-I{p}" for p in include), "-c", os.path.join(CSRC, "marshal.cpp"),
+             "-o", obj],
+            [cxx, "-shared", "-o", out, obj, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+             f"-Wl,-rpath,{lib}"])
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -54,7 +76,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
-    procs = []
+    marshal_obj = os.path.join(BUILD, "marshal.o")
+    compile_marshal, link_marshal = _marshal_commands(nvcc, marshal_obj, MARSHAL + ".tmp")
+    procs = [(compile_marshal[-3], subprocess.Popen(compile_marshal, stdout=subprocess.PIPE,
+                                                    stderr=subprocess.STDOUT))]
     objs = []
     for src in _sources():
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
@@ -79,9 +104,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
            "-Xlinker", "-rpath,/usr/local/cuda/lib64"]
     if verbose:
         print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
+    for link in (cmd, link_marshal):
+        r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        if r.returncode != 0:
+            raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
+    os.replace(MARSHAL + ".tmp", MARSHAL)
     os.replace(tmp, LIB)
     return LIB
 

@@ -23,7 +23,6 @@ STATUS_NAMES = {
 }
 DTYPES = {"f16": 0, "bf16": 1, "f32": 2}
 
-ACTS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3}   # gptq_act in include/gptq.h
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 _c = ctypes
@@ -1018,127 +1017,26 @@ def kv8_attention(q, cache, table, lengths, scale=None, causal=True, out=None, w
 
 
 # ---------------------------------------------------------------------------------------
-# Feed-forward blocks of quantized layers
+# Feed-forward blocks of quantized layers (their marshalling is compiled, csrc/marshal.cpp)
 # ---------------------------------------------------------------------------------------
 
-def _stream_here(gpu, device, stream):
-    """The stream of a call whose tensors are on ``gpu``, which has to be the current device: the
-    default stream's handle means the current device's."""
-    if _torch()._C._cuda_getDevice() != gpu:
-        raise ValueError("a call's tensors must be on the current device")
-    return _stream_of(device, stream)
+_MARSHAL = None
 
 
-def _fp8_a(a, a_exps, a_scale):
-    """``(rows, k, pitch of the codes, of the exponents, GPU)`` of a product's activations."""
-    torch = _torch()
-    lda = _rows_of("a", a)
-    m, k = a.shape
-    ldae = _rows_of("a_exps", a_exps, m, (k + FP8_BLOCK - 1) // FP8_BLOCK)
-    if a.dtype != torch.float8_e4m3fn or a_exps.dtype != torch.uint8:
-        raise TypeError("codes are float8_e4m3fn and exponents uint8")
-    gpu = a.get_device()
-    if gpu < 0 or a_exps.get_device() != gpu:
-        raise ValueError(_ONE_GPU)
-    if a_scale is not None:
-        if a_scale.dtype != torch.float32 or a_scale.shape != (m,) or not a_scale.is_contiguous():
-            raise ValueError(f"a_scale must be a contiguous float32 [{m}] vector")
-        if a_scale.get_device() != gpu:
-            raise ValueError(_ONE_GPU)
-    return m, k, lda, ldae, gpu
-
-
-def _fp8_w(name, w, exps, scale, bias, k, gpu, n=None, experts=None):
-    """``(n, struct)`` of a product's weights, one matrix or (``experts``) one for each."""
-    torch = _torch()
-    shape, st, eshape, es = w.shape, w.stride(), exps.shape, exps.stride()
-    kb = (k + FP8_BLOCK - 1) // FP8_BLOCK
-    if experts is None:
-        if len(shape) != 2 or shape[1] != k or st[1] != 1 or (n is not None and shape[0] != n):
-            raise ValueError(f"{name} must be a row-major [{'n' if n is None else n}, {k}] matrix")
-        rows, ld, next_codes = shape[0], st[0], 0
-        nb = (rows + FP8_BLOCK - 1) // FP8_BLOCK
-        if len(eshape) != 2 or eshape[0] != nb or eshape[1] != kb or (es[1] != 1 and kb != 1):
-            raise ValueError(f"the exponents of {name} must be a row-major [{nb}, {kb}] matrix")
-        lde, next_exps = es[0], 0
-        vector = (rows,)
-    else:
-        if len(shape) != 3 or shape[0] != experts or shape[2] != k or st[2] != 1 \
-                or (n is not None and shape[1] != n):
-            raise ValueError(f"{name} must be row-major [{experts}, {'n' if n is None else n}, {k}]")
-        rows, ld, next_codes = shape[1], st[1], st[0]
-        nb = (rows + FP8_BLOCK - 1) // FP8_BLOCK
-        if len(eshape) != 3 or eshape[0] != experts or eshape[1] != nb or eshape[2] != kb \
-                or (es[2] != 1 and kb != 1):
-            raise ValueError(f"the exponents of {name} must be row-major [{experts}, {nb}, {kb}]")
-        lde, next_exps = es[1], es[0]
-        vector = (experts, rows)
-    # a matrix of one row may have any pitch
-    if rows == 1:
-        ld = max(ld, (k + 15) & ~15)
-    if nb == 1:
-        lde = max(lde, (kb + 3) & ~3)
-    if w.dtype != torch.float8_e4m3fn or exps.dtype != torch.uint8:
-        raise TypeError("codes are float8_e4m3fn and exponents uint8")
-    if w.get_device() != gpu or exps.get_device() != gpu:
-        raise ValueError(_ONE_GPU)
-    scale_ptr = bias_ptr = None
-    if scale is not None:
-        scale_ptr = _vector(name, "scale", scale, vector, gpu, torch.float32)
-    if bias is not None:
-        bias_ptr = _vector(name, "bias", bias, vector, gpu, torch.float32)
-    return rows, Fp8Weights(w.data_ptr(), ld, next_codes, exps.data_ptr(), lde, next_exps, scale_ptr,
-                            bias_ptr)
-
-
-def _vector(name, what, t, shape, gpu, f32):
-    if t.dtype != f32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"the {what} of {name} must be contiguous float32 {list(shape)}")
-    if t.get_device() != gpu:
-        raise ValueError(_ONE_GPU)
-    return t.data_ptr()
-
-
-def _act(act):
-    code = ACTS.get(act)
-    if code is None:
-        raise ValueError(f"act must be one of {[a for a in ACTS if a]} or None")
-    return code
-
-
-def _ws_of(ws, gpu, device):
-    if ws is None:
-        return _status_block(device)
-    if ws.get_device() != gpu:
-        raise ValueError(_ONE_GPU)
-    return ws
-
-
-def _out16(out, rows, n, out_dtype, gpu, device, stream):
-    torch = _torch()
-    if out is None:
-        out = torch.empty((rows, n), dtype=out_dtype or torch.bfloat16, device=device)
-        _lend(stream, out)
-        return out, n
-    ldo = _rows_of("out", out, rows, n)
-    if out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError("out must have out_dtype")
-    if out.get_device() != gpu:
-        raise ValueError(_ONE_GPU)
-    return out, ldo
-
-
-def _plan_args(offsets, order, rows, gpu):
-    """The number of experts of ``moe_route``'s offsets and order."""
-    torch = _torch()
-    if offsets.dtype != torch.int32 or order.dtype != torch.int32:
-        raise TypeError("offsets and order must be int32")
-    if offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous() \
-            or order.shape != (rows,) or not order.is_contiguous():
-        raise ValueError(f"offsets [experts + 1] and order [{rows}] as moe_route returns them")
-    if offsets.get_device() != gpu or order.get_device() != gpu:
-        raise ValueError(_ONE_GPU)
-    return offsets.shape[0] - 1
+def _marshal():
+    """The compiled marshalling, loaded once and given the library's entry points."""
+    global _MARSHAL
+    if _MARSHAL is None:
+        lib = load()
+        _torch()
+        if not os.path.exists(build_lib.MARSHAL):
+            raise RuntimeError(f"{build_lib.MARSHAL} is missing: it must be built (build_lib.build())")
+        from . import _marshal as module
+        module.bind(tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "gptq_fp8_linear", "gptq_fp8_gated", "gptq_fp8_experts", "gptq_fp8_experts_gated",
+            "gptq_moe_route", "gptq_moe_route_workspace_bytes", "gptq_moe_combine")), _check)
+        _MARSHAL = module
+    return _MARSHAL
 
 
 def fp8_linear(a, a_exps, w, w_exps, a_scale=None, w_scale=None, bias=None, act=None, residual=None,
@@ -1147,51 +1045,15 @@ def fp8_linear(a, a_exps, w, w_exps, a_scale=None, w_scale=None, bias=None, act=
     ``[m, n]`` in float16 or bfloat16 (the default), rounded once.  ``act``: None, "relu", "silu" or
     "gelu"; ``bias``: float32 ``[n]``; ``residual``: ``[m, n]`` of the output's dtype, which may be
     ``out`` itself.  ``ws`` as for ``fp8_matmul``."""
-    m, k, lda, ldae, gpu = _fp8_a(a, a_exps, a_scale)
-    n, weights = _fp8_w("w", w, w_exps, w_scale, bias, k, gpu)
-    device = a.device
-    out, ldo = _out16(out, m, n, out_dtype, gpu, device, stream)
-    ldr = 0
-    if residual is not None:
-        ldr = _rows_of("residual", residual, m, n)
-        if residual.dtype != out.dtype:
-            raise TypeError("residual must have the output's dtype")
-        if residual.get_device() != gpu:
-            raise ValueError(_ONE_GPU)
-    ws = _ws_of(ws, gpu, device)
-    _check(load().gptq_fp8_linear(
-        a.data_ptr(), lda, a_exps.data_ptr(), ldae,
-        a_scale.data_ptr() if a_scale is not None else None, weights, _act(act),
-        residual.data_ptr() if residual is not None else None, ldr, m, n, k, out.data_ptr(),
-        _serving_dtype(out.dtype), ldo, ws.data_ptr(), ws.numel(), _stream_here(gpu, device, stream)),
-        "gptq_fp8_linear")
-    return out
-
-
-def _of_gated(name, w):
-    w = tuple(w)
-    if not 2 <= len(w) <= 4:
-        raise ValueError(f"{name} must be (codes, exps[, scale[, bias]])")
-    return w + (None,) * (4 - len(w))
+    return (_MARSHAL or _marshal()).fp8_linear(a, a_exps, w, w_exps, a_scale, w_scale, bias, act, residual,
+                                               out_dtype, out, ws, stream)
 
 
 def fp8_gated(a, a_exps, gate, up, a_scale=None, act="silu", ws=None, stream=None):
     """``(codes, exps)``, by 1 x 128 blocks, of ``act(G) * U``: G and U are the products of ``A [m, k]``
     with the weights ``gate`` and ``up``, each ``(codes [n, k], exps[, scale[, bias]])``, as
     ``fp8_linear`` takes them.  What ``fp8_matmul`` or ``fp8_linear`` take as activations."""
-    m, k, lda, ldae, gpu = _fp8_a(a, a_exps, a_scale)
-    n, g = _fp8_w("gate", *_of_gated("gate", gate), k, gpu)
-    _, u = _fp8_w("up", *_of_gated("up", up), k, gpu, n)
-    device = a.device
-    ws = _ws_of(ws, gpu, device)
-    act = _act(act)
-    codes, ldc, exps, lde = _fp8_empty(m, n, 1, device, stream)
-    _check(load().gptq_fp8_gated(
-        a.data_ptr(), lda, a_exps.data_ptr(), ldae,
-        a_scale.data_ptr() if a_scale is not None else None, g, u, act, m, n, k, codes.data_ptr(),
-        ldc, exps.data_ptr(), lde, ws.data_ptr(), ws.numel(), _stream_here(gpu, device, stream)),
-        "gptq_fp8_gated")
-    return codes, exps
+    return (_MARSHAL or _marshal()).fp8_gated(a, a_exps, gate, up, a_scale, act, ws, stream)
 
 
 def moe_route(logits, top_k, bias=None, scores="softmax", groups=1, top_groups=None, group_top=2,
@@ -1207,44 +1069,14 @@ def moe_route(logits, top_k, bias=None, scores="softmax", groups=1, top_groups=N
     expert e's from ``offsets[e]`` on: what ``fp8_experts_gated`` and ``fp8_experts`` take.
     Experts whose logit or bias is not finite are never chosen (ids of -1, weights of 0 where too few
     are left)."""
-    torch = _torch()
-    ld = _rows_of("logits", logits)
-    n, experts = logits.shape
-    gpu, device = logits.get_device(), logits.device
     if scores not in SCORES:
         raise ValueError(f"scores must be one of {list(SCORES)}")
-    if bias is not None:
-        if bias.dtype != torch.float32 or bias.shape != (experts,) or not bias.is_contiguous():
-            raise ValueError(f"bias must be a contiguous float32 [{experts}] vector")
-        if bias.get_device() != gpu:
-            raise ValueError(_ONE_GPU)
-    if gpu < 0:
-        raise ValueError(_ONE_GPU)
-    dtype, lib = _serving_dtype(logits.dtype), load()
     if groups == 1:
         top_groups, group_top = 1, 1
     elif top_groups is None:
         top_groups = groups
-    if not 1 <= top_k <= experts:
-        raise ValueError("top_k must be between 1 and the number of experts")
-    ids = torch.empty((n, top_k), dtype=torch.int32, device=device)
-    weights = torch.empty((n, top_k), dtype=torch.float32, device=device)
-    offsets = torch.empty((experts + 1,), dtype=torch.int32, device=device)
-    order = torch.empty((n * top_k,), dtype=torch.int32, device=device)
-    if ws is None:
-        need = lib.gptq_moe_route_workspace_bytes(n, experts, top_k)
-        ws = _status_block(device) if need <= 256 else torch.empty((need,), dtype=torch.uint8, device=device)
-        if need > 256:
-            _lend(stream, ws)
-    elif ws.get_device() != gpu:
-        raise ValueError(_ONE_GPU)
-    _lend(stream, ids, weights, offsets, order)
-    _check(lib.gptq_moe_route(
-        logits.data_ptr(), dtype, ld, n, experts, top_k, bias.data_ptr() if bias is not None else None,
-        SCORES[scores], groups, top_groups, group_top, 1 if renormalize else 0, scale, ids.data_ptr(),
-        weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), ws.data_ptr(), ws.numel(),
-        _stream_here(gpu, device, stream)), "gptq_moe_route")
-    return ids, weights, offsets, order
+    return (_MARSHAL or _marshal()).moe_route(logits, top_k, bias, SCORES[scores], groups, top_groups, group_top,
+                                              renormalize, scale, ws, stream)
 
 
 def fp8_experts_gated(a, a_exps, gate, up, offsets, order, top_k, a_scale=None, act="silu", ws=None,
@@ -1252,23 +1084,8 @@ def fp8_experts_gated(a, a_exps, gate, up, offsets, order, top_k, a_scale=None, 
     """``fp8_gated`` of each expert's tokens: ``gate`` and ``up`` are ``(codes [experts, n, k], exps[,
     scale[, bias]])``, ``a [tokens, k]``, ``offsets`` and ``order`` as ``moe_route`` returns them.  Row
     p of the codes belongs to position p of the order; rows after the last one are undefined."""
-    m, k, lda, ldae, gpu = _fp8_a(a, a_exps, a_scale)
-    if top_k < 1:
-        raise ValueError("top_k must be at least 1")
-    experts = _plan_args(offsets, order, m * top_k, gpu)
-    n, g = _fp8_w("gate", *_of_gated("gate", gate), k, gpu, None, experts)
-    _, u = _fp8_w("up", *_of_gated("up", up), k, gpu, n, experts)
-    device = a.device
-    ws = _ws_of(ws, gpu, device)
-    act = _act(act)
-    codes, ldc, exps, lde = _fp8_empty(m * top_k, n, 1, device, stream)
-    _check(load().gptq_fp8_experts_gated(
-        a.data_ptr(), lda, a_exps.data_ptr(), ldae,
-        a_scale.data_ptr() if a_scale is not None else None, g, u, act, experts,
-        offsets.data_ptr(), order.data_ptr(), top_k, m, n, k, codes.data_ptr(), ldc,
-        exps.data_ptr(), lde, ws.data_ptr(), ws.numel(), _stream_here(gpu, device, stream)),
-        "gptq_fp8_experts_gated")
-    return codes, exps
+    return (_MARSHAL or _marshal()).fp8_experts_gated(a, a_exps, gate, up, offsets, order, top_k, a_scale, act, ws,
+                                                      stream)
 
 
 def fp8_experts(a, a_exps, w, w_exps, offsets, order, w_scale=None, bias=None, act=None,
@@ -1277,50 +1094,12 @@ def fp8_experts(a, a_exps, w, w_exps, offsets, order, w_scale=None, bias=None, a
     its expert's weights ``w [experts, n, k]``: ``[rows, n]`` with row p at ``order[p]``, so that a
     token's rows lie together for ``moe_combine``.  Rows that the order does not name stay as they
     are.  Otherwise as ``fp8_linear``."""
-    m, k, lda, ldae, gpu = _fp8_a(a, a_exps, None)
-    experts = _plan_args(offsets, order, m, gpu)
-    n, weights = _fp8_w("w", w, w_exps, w_scale, bias, k, gpu, None, experts)
-    device = a.device
-    out, ldo = _out16(out, m, n, out_dtype, gpu, device, stream)
-    ws = _ws_of(ws, gpu, device)
-    _check(load().gptq_fp8_experts(
-        a.data_ptr(), lda, a_exps.data_ptr(), ldae, weights, _act(act), experts,
-        offsets.data_ptr(), order.data_ptr(), m, n, k, out.data_ptr(), _serving_dtype(out.dtype),
-        ldo, ws.data_ptr(), ws.numel(), _stream_here(gpu, device, stream)), "gptq_fp8_experts")
-    return out
+    return (_MARSHAL or _marshal()).fp8_experts(a, a_exps, w, w_exps, offsets, order, w_scale, bias, act, out_dtype,
+                                                out, ws, stream)
 
 
 def moe_combine(y, weights, residual=None, out=None, stream=None):
     """``residual[t] + sum_j weights[t, j] y[t * top_k + j]``, ``[tokens, d]``: the experts' outputs
     ``y [tokens * top_k, d]`` with ``moe_route``'s weights.  A row whose weight is 0 is left out,
-    whatever it holds.
-    ``out`` may be the residual."""
-    torch = _torch()
-    n, top_k = weights.shape
-    ldy = _rows_of("y", y, n * top_k)
-    d = y.shape[1]
-    if weights.dtype != torch.float32 or not weights.is_contiguous():
-        raise ValueError("weights must be a contiguous float32 [tokens, top_k] matrix")
-    ldr = 0
-    if residual is not None:
-        ldr = _rows_of("residual", residual, n, d)
-        if residual.dtype != y.dtype:
-            raise TypeError("residual must have y's dtype")
-    gpu, device = y.get_device(), y.device
-    if gpu < 0 or weights.get_device() != gpu or (residual is not None and residual.get_device() != gpu):
-        raise ValueError(_ONE_GPU)
-    if out is None:
-        out = torch.empty((n, d), dtype=y.dtype, device=device)
-        ldo = d
-        _lend(stream, out)
-    else:
-        ldo = _rows_of("out", out, n, d)
-        if out.dtype != y.dtype:
-            raise TypeError("out must have y's dtype")
-        if out.get_device() != gpu:
-            raise ValueError(_ONE_GPU)
-    _check(load().gptq_moe_combine(
-        y.data_ptr(), _serving_dtype(y.dtype), ldy, n, top_k, d, weights.data_ptr(),
-        residual.data_ptr() if residual is not None else None, ldr, out.data_ptr(), ldo,
-        _stream_here(gpu, device, stream)), "gptq_moe_combine")
-    return out
+    whatever it holds.  ``out`` may be the residual."""
+    return (_MARSHAL or _marshal()).moe_combine(y, weights, residual, out, stream)
