@@ -25,8 +25,8 @@
 //
 // 16-bit outputs are turned around likewise, so that a store writes 64 contiguous bytes of four tokens.
 //
-// Few tokens leave few tiles; the k-blocks of a tile are then split over a cluster of up to 8
-// CTAs, whose partial sums meet through distributed shared memory in rank order.
+// Few tokens leave few tiles; each cluster of up to 8 CTAs then has one, whose k-blocks they share, and
+// their partial sums meet through distributed shared memory in rank order.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -40,29 +40,24 @@ namespace {
 using mx::BK;
 using mx::BM;
 using mx::copy_scales;
-using mx::ld_cluster_f32x4;
 using mx::out_f32;
 
-constexpr int kLoaders = 8;                 // warps that copy rows by index
 constexpr int kMaxTn = 240;
 constexpr int kMaxTnGated = 112;            // two accumulators, for this tile and the next
 constexpr int kScaleStages = 4;             // groups of four k-blocks in flight
-constexpr uint32_t kScaleBytes = 4 * 512;   // weights, second weights, tokens 0..127, tokens 128..239
+// A group of scales in shared memory: weights, second weights, tokens 0..127, tokens 128..239.
+__host__ __device__ constexpr uint32_t scale_bytes(int tn) { return tn > 128 ? 4 * 512 : 3 * 512; }
 constexpr uint32_t kScaleCols = 16;         // TMEM columns of one group
 constexpr int kMaxStages = 12;
 constexpr int kBox = 64;                    // rows of A in a copy of the experts' plain product, at most
-constexpr int kMaxExperts = 1024;
 constexpr int64_t kAcross = 16;            // (about as many tiles along the tokens run with them)
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kRingBytes = 4 * (BM + kMaxTn) * BK;
-constexpr int kEpilogue = 8;                // warps
 constexpr int kTurnPitch = 36;              // (words in different banks along either way)
-constexpr uint32_t kTurnBytes = kEpilogue * 16 * kTurnPitch * 4;   // each warp's 16 tokens x 32 rows
-constexpr size_t kSmemBesides = 1024 + kTurnBytes + kScaleStages * kScaleBytes + 2 * 256 * 4 + 2 * 4 * 32 * 4 + 512;
-constexpr size_t kPlanBytes = 2 * (kMaxExperts + 4) * sizeof(int);
+constexpr size_t kSmem = 227 * 1024;        // of a CTA alone on its SM
+constexpr size_t kSmemTwo = 113 * 1024;     // of one of two
+constexpr size_t kBarBytes = 512;
 static_assert(2 * kMaxTn + 2 * kScaleCols <= kTmemCols, "TMEM columns");
 static_assert(4 * kMaxTnGated + 2 * kScaleCols <= kTmemCols, "TMEM columns");
-static_assert(kRingBytes + kSmemBesides + kPlanBytes <= 227 * 1024, "shared memory");
 
 struct Params {
   const uint8_t *a; int64_t lda, K;
@@ -84,6 +79,7 @@ struct Params {
   int splits;           // CTAs of a cluster that share a tile's k-blocks
   int acc_cols;         // columns of an accumulator
   int tmem_cols;
+  uint32_t ring_bytes;
   const int32_t *offsets, *order;
   int n_experts, top_k;
   uint64_t wait_ns;
@@ -210,24 +206,34 @@ __device__ __forceinline__ void make_plan(const Params &p, const Plan &plan, int
 }
 
 // TO: type of the output, if it is not gated.
-template <bool GATED, bool EXPERTS>
-constexpr int kThreadsOf = 32 * (3 + kEpilogue + (GATED && EXPERTS ? kLoaders : 0));
+// Shared memory of the epilogue that goes from tile to tile.
+__host__ __device__ constexpr size_t direct_bytes(int epilogue) {
+  return 2 * 256 * 4 + epilogue * 16 * kTurnPitch * 4 + 2 * 2 * 4 * 16 * 4;
+}
 
-template <typename TO, bool GATED, bool EXPERTS>
-__global__ void __launch_bounds__(kThreadsOf<GATED, EXPERTS>, 1)
+template <bool GATED, bool EXPERTS, bool ONE>
+struct Warps {
+  static constexpr int kEpilogue = ONE && GATED && EXPERTS ? 4 : 8;   // (registers of two CTAs an SM)
+  static constexpr int kLoaders = ONE ? 4 : 8;   // copy rows by index, if there is such a thing
+  static constexpr int kAll = 3 + kEpilogue + (GATED && EXPERTS ? kLoaders : 0);
+};
+
+// ONE: each cluster has one tile, whose k-blocks its CTAs share; their sums lie in shared memory, where
+// a warp of one of them adds up and finishes a token's.  Two such CTAs can be on an SM, of one call or of two in a row,
+// so that one sets itself up while the other ends.  Else a CTA goes from tile to tile, with a set of
+// accumulators for the MMAs and one for the epilogue.
+template <typename TO, bool GATED, bool EXPERTS, bool ONE>
+__global__ void __launch_bounds__(32 * Warps<GATED, EXPERTS, ONE>::kAll, ONE ? 2 : 1)
 linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ CUtensorMap mw1,
               const __grid_constant__ CUtensorMap ma, Params p, DevStatus *st) {
   constexpr int W = GATED ? 2 : 1;
   constexpr bool GATHER = GATED && EXPERTS;
-  constexpr int E = kEpilogue;
+  constexpr int E = Warps<GATED, EXPERTS, ONE>::kEpilogue, kLoaders = Warps<GATED, EXPERTS, ONE>::kLoaders;
+  constexpr int kSets = ONE ? 1 : 2;  // of accumulators
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  float *turned = (float *)(ring + kRingBytes);
-  uint8_t *sscale = (uint8_t *)turned + kTurnBytes;
-  float *sra = (float *)(sscale + kScaleStages * kScaleBytes);   // [256] of each token: factor,
-  int *srow = (int *)(sra + 256);                                // row of the output (-1: none)
-  float *smax = (float *)(srow + 256);                           // [2 halves][2][4 warps][16 tokens]
-  uint64_t *full = (uint64_t *)(smax + 2 * 2 * 4 * 16);
+  uint8_t *sscale = ring + p.ring_bytes;
+  uint64_t *full = (uint64_t *)(sscale + kScaleStages * scale_bytes(p.tn));
   uint64_t *empty = full + kMaxStages;
   uint64_t *sfull = empty + kMaxStages;
   uint64_t *sempty = sfull + kScaleStages;
@@ -235,7 +241,13 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
   uint64_t *tempty = tfull + 2;
   uint64_t *mdone = tempty + 2;       // every MMA has completed
   uint32_t *tmem_slot = (uint32_t *)(mdone + 1);
-  Plan plan{(int *)(tmem_slot + 4), (int *)(tmem_slot + 4) + kMaxExperts + 4};
+  // not ONE: of each token (256) its factor and its row of the output (-1: none); the 16 tokens x 32
+  // rows of each epilogue warp; [2 halves][2][4 warps][16 tokens]
+  float *sra = (float *)((uint8_t *)full + kBarBytes);
+  int *srow = (int *)(sra + 256);
+  float *turned = (float *)(srow + 256), *smax = turned + E * 16 * kTurnPitch;
+  int *plan_at = (int *)((uint8_t *)full + kBarBytes + (ONE ? 0 : direct_bytes(E)));
+  const Plan plan{plan_at, plan_at + p.n_experts + 4};
   const tc::Waits waits{st, &g_gave_up, p.wait_ns};
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
@@ -279,7 +291,45 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
   if (blockIdx.x == 0 && threadIdx.x == 0) st->status = 0;
   const int n_tiles = p.n_w * (EXPERTS ? plan.tiles[p.n_experts] : p.n_m);
   const uint32_t set_cols = (uint32_t)(W * p.acc_cols);          // accumulators of a tile
-  const uint32_t sc_cols = tmem + 2 * set_cols;
+  const uint32_t sc_cols = tmem + kSets * set_cols;
+
+  // ONE: what finishes this warp's token: the cluster's tokens are dealt to its CTAs in turn, a CTA's to
+  // its warps, those of the epilogue first, which ask for all of it before the sums are there.  A lane
+  // has four rows.
+  constexpr int kAll = Warps<GATED, EXPERTS, ONE>::kAll;
+  const int first_col = rank + (warp + kAll - 2) % kAll * p.splits;
+  const Tile one = ONE && first < n_tiles ? tile_of<EXPERTS>(p, plan, first) : Tile{0, 0, 0, 0};
+  const int64_t n4 = (int64_t)one.n * BM + lane * 4;
+  float fin_rw[W][4], fin_bias[W][4], fin_ra = 1.0f;
+  int64_t fin_row = -1;
+  TO fin_res[4];
+  auto ask_token = [&](int col) {
+    if (col >= one.cols) return;
+    const int pos = one.m0 + col, r = a_row<GATHER>(p, pos);
+    fin_ra = p.ra && r < p.a_rows ? p.ra[r] : 1.0f;
+    fin_row = pos;
+    if constexpr (EXPERTS && !GATED) {
+      const int o = p.order[pos];
+      fin_row = o >= 0 && o < p.M ? o : -1;
+    }
+    if constexpr (!GATED)
+      if (p.residual) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          fin_res[j] = n4 + j < p.N ? ((const TO *)p.residual)[fin_row * p.ldr + n4 + j] : out_f32<TO>(0.0f);
+      }
+  };
+  auto ask_rows = [&]() {
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t at = (int64_t)one.e * p.N + n4 + j;
+        fin_rw[w][j] = p.rw[w] && n4 + j < p.N ? p.rw[w][at] : 1.0f;
+        fin_bias[w][j] = p.bias[w] && n4 + j < p.N ? p.bias[w][at] : 0.0f;
+      }
+    ask_token(first_col);
+  };
 
   bool ok = true;                   // false once a wait has given up: the role ends
   int s = 0, n = 0;                 // producer and issuer: stage of the ring; copies
@@ -393,7 +443,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
         tc::tc_fence_after();
         // two groups of columns in turn: the scale warp's ring keeps a third group's copy from
         // starting before the first group's MMAs have completed
-        const uint32_t sc = sc_cols + (uint32_t)(g & 1) * kScaleCols, sm = sc0 + q * kScaleBytes;
+        const uint32_t sc = sc_cols + (uint32_t)(g & 1) * kScaleCols, sm = sc0 + q * scale_bytes(p.tn);
         copy_scales(sc, sm);
         if constexpr (GATED) copy_scales(sc + 4, sm + 512);
         copy_scales(sc + 8, sm + 1024);
@@ -452,11 +502,11 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
           ok = false;
           break;
         }
-        uint4 *dst = reinterpret_cast<uint4 *>(sscale + q * kScaleBytes) + lane;
+        uint4 *dst = reinterpret_cast<uint4 *>(sscale + q * scale_bytes(p.tn)) + lane;
 #pragma unroll
         for (int w = 0; w < W; ++w) dst[32 * w] = make_uint4(ww[w], ww[w], ww[w], ww[w]);
         dst[64] = make_uint4(word[0], word[1], word[2], word[3]);
-        dst[96] = make_uint4(word[4], word[5], word[6], word[7]);
+        if (p.tn > 128) dst[96] = make_uint4(word[4], word[5], word[6], word[7]);
         tc::fence_proxy_async_smem();
         tc::mbar_arrive(&sfull[q]);
       }
@@ -464,7 +514,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
   } else if (warp >= 2 && warp < 2 + E) {
     // ---------------- epilogue ----------------
     const int q = warp & 3, lrow = q * 32 + lane, et = threadIdx.x - 64, half = (warp - 2) / 4;
-    static_assert(32 * E >= kMaxTn, "a thread has one token's factors");
+    static_assert(ONE || 32 * E >= kMaxTn, "a thread has one token's factors");
     int it = 0, turn = 0;
     // factors of the next tile, asked for while this one is worked on: of token `et`, and of this row
     Tile next;
@@ -472,7 +522,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
     int next_row = -1;
     auto fetch = [&](int t) {
       next = tile_of<EXPERTS>(p, plan, t);
-      if (p.splits == 1 && et < next.cols) {
+      if (!ONE && et < next.cols) {
         const int pos = next.m0 + et, r = a_row<GATHER>(p, pos);
         next_ra = p.ra && r < p.a_rows ? p.ra[r] : 1.0f;
         if constexpr (EXPERTS && !GATED) {
@@ -482,12 +532,13 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
       }
       const int64_t nn = (int64_t)next.n * BM + lrow, at = (int64_t)next.e * p.N + nn;
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
+      for (int w = 0; w < W && !ONE; ++w) {
         next_rw[w] = p.rw[w] && nn < p.N ? p.rw[w][at] : 1.0f;
         next_bias[w] = p.bias[w] && nn < p.N ? p.bias[w][at] : 0.0f;
       }
     };
     if (first < n_tiles) fetch(first);
+    if constexpr (ONE) ask_rows();
     for (int t = first; t < n_tiles; t += step, ++it) {
       const int b = it & 1, use = it >> 1;   // accumulators in turn
       const Tile tile = next;
@@ -497,8 +548,8 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
       const bool wide = p.wide && (int64_t)tile.n * BM + q * 32 + 32 <= p.N;
       float rw[W], bias[W];
 #pragma unroll
-      for (int w = 0; w < W; ++w) rw[w] = next_rw[w], bias[w] = next_bias[w];
-      if (p.splits == 1) {
+      for (int w = 0; w < W && !ONE; ++w) rw[w] = next_rw[w], bias[w] = next_bias[w];
+      if constexpr (!ONE) {
         tc::named_barrier(2, 32 * E);  // the previous tile's factors have been read
         if (et < tile.cols) {
           sra[et] = next_ra;
@@ -511,8 +562,8 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
       const int64_t n4 = (int64_t)tile.n * BM + q * 32 + lane % 8 * 4;
       uint2 res[8];
       auto ask = [&](int c) {
-        if constexpr (!GATED) {
-          if (!wide || !p.residual || p.splits > 1) return;
+        if constexpr (!GATED && !ONE) {
+          if (!wide || !p.residual) return;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (c + lane / 8 + 4 * i < tile.cols)
@@ -525,10 +576,10 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
       tc::tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * set_cols;
       float *mine = turned + (warp - 2) * 16 * kTurnPitch;     // this warp's to turn
-      if (p.splits > 1) {
+      if constexpr (ONE) {
         float *part = (float *)ring + lrow;
 #pragma unroll 1
-        for (int c = 16 * half; c < tile.cols; c += 32) {
+        for (int c = 16 * half; c < tile.cols; c += 4 * E) {
 #pragma unroll
           for (int w = 0; w < W; ++w) {
             uint32_t r[16];
@@ -685,45 +736,25 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
     __syncwarp();
   }
   if (warp == 1) tc::tmem_dealloc(tmem, p.tmem_cols);
-  if (p.splits > 1) {
-    // one tile per cluster: the ring holds this CTA's partial sums [W][tn][128]
+  if constexpr (ONE) {
+    // the ring holds this CTA's partial sums [W][tn][128]
+    if (warp < 2 || warp >= 2 + E) ask_rows();
     tc::cluster_sync();
-    if (first < n_tiles) {
-      const Tile tile = tile_of<EXPERTS>(p, plan, first);
-      // this CTA's columns are rank, rank + splits, ...; a warp takes one, a lane four rows of it
-      const uint32_t base = tc::smem_u32(ring) + lane * 16;
-      const int64_t nn = (int64_t)tile.n * BM + lane * 4;
-      float rw[W][4], bias[W][4];
-#pragma unroll
-      for (int w = 0; w < W; ++w)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t at = (int64_t)tile.e * p.N + nn + j;
-          rw[w][j] = p.rw[w] && nn + j < p.N ? p.rw[w][at] : 1.0f;
-          bias[w][j] = p.bias[w] && nn + j < p.N ? p.bias[w][at] : 0.0f;
-        }
+    {
+      const int64_t nn = n4;
       const bool pairs = (p.ldo & 1) == 0 && ((uintptr_t)p.out & 3) == 0 && nn + 3 < p.N;
 #pragma unroll 1
-      for (int col = rank + warp * p.splits; col < tile.cols; col += kThreadsOf<GATED, EXPERTS> / 32 * p.splits) {
-        const int pos = tile.m0 + col, r = a_row<GATHER>(p, pos);
-        const float ra = p.ra && r < p.a_rows ? p.ra[r] : 1.0f;
-        int64_t row = pos;
-        if constexpr (EXPERTS && !GATED) row = p.order[pos] >= 0 && p.order[pos] < p.M ? p.order[pos] : -1;
-        TO res[4];
-        if constexpr (!GATED)
-          if (p.residual) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              res[j] = nn + j < p.N ? ((const TO *)p.residual)[row * p.ldr + nn + j] : out_f32<TO>(0.0f);
-          }
+      for (int col = first_col; col < one.cols; col += kAll * p.splits) {
+        if (col != first_col) ask_token(col);
+        const int64_t row = fin_row;
         float x[W][4];
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const uint32_t off = base + (uint32_t)(w * p.tn + col) * BM * 4;
+          const uint32_t off = tc::smem_u32(ring) + (uint32_t)(w * p.tn + col) * BM * 4 + lane * 16;
           float4 v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            v[i] = i < p.splits ? ld_cluster_f32x4(tc::mapa_shared(off, (uint32_t)i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[i] = i < p.splits ? mx::ld_cluster_f32x4(tc::mapa_shared(off, (uint32_t)i)) : make_float4(0.f, 0.f, 0.f, 0.f);
           float4 sum = v[0];
 #pragma unroll
           for (int i = 1; i < 8; ++i) {
@@ -732,10 +763,10 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
             sum.z += v[i].z;
             sum.w += v[i].w;
           }
-          x[w][0] = fmaf(sum.x * rw[w][0], ra, bias[w][0]);
-          x[w][1] = fmaf(sum.y * rw[w][1], ra, bias[w][1]);
-          x[w][2] = fmaf(sum.z * rw[w][2], ra, bias[w][2]);
-          x[w][3] = fmaf(sum.w * rw[w][3], ra, bias[w][3]);
+          x[w][0] = fmaf(sum.x * fin_rw[w][0], fin_ra, fin_bias[w][0]);
+          x[w][1] = fmaf(sum.y * fin_rw[w][1], fin_ra, fin_bias[w][1]);
+          x[w][2] = fmaf(sum.z * fin_rw[w][2], fin_ra, fin_bias[w][2]);
+          x[w][3] = fmaf(sum.w * fin_rw[w][3], fin_ra, fin_bias[w][3]);
         }
         activate(x[0], p.act);
         if constexpr (GATED) {
@@ -758,11 +789,11 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
             for (int j = 0; j < 4; ++j)
               if (nn + j < p.N) dst[j] = (uint8_t)(four >> (8 * j));
           }
-          if (lane == 0) p.oe[row * p.ldoe + tile.n] = (uint8_t)(ex + fp8::kBias);
+          if (lane == 0) p.oe[row * p.ldoe + one.n] = (uint8_t)(ex + fp8::kBias);
         } else if (row >= 0) {
           alignas(8) TO o[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = out_f32<TO>(p.residual ? x[0][j] + to_f32(res[j]) : x[0][j]);
+          for (int j = 0; j < 4; ++j) o[j] = out_f32<TO>(p.residual ? x[0][j] + to_f32(fin_res[j]) : x[0][j]);
           TO *dst = (TO *)p.out + row * p.ldo + nn;
           if (pairs) {
             reinterpret_cast<uint32_t *>(dst)[0] = reinterpret_cast<const uint32_t *>(o)[0];
@@ -775,42 +806,77 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
         }
       }
     }
-    tc::cluster_sync();  // the others have read this CTA's sums
+    tc::cluster_sync();   // the others have read this CTA's sums
   }
 }
 
-size_t smem_bytes(bool experts) { return kRingBytes + kSmemBesides + (experts ? kPlanBytes : 0); }
+// How a call's work is cut: tokens of a tile, CTAs that share its k-blocks, one tile a cluster or not,
+// and what a CTA has of its SM.
+struct Shape {
+  int tn, splits, per_sm;
+  bool one;
+  int stages, tmem_cols;
+  uint32_t ring_bytes;
+  size_t smem;
+};
 
-// Clusters of `splits` CTAs, one on an SM, that run at once.  They lie within groups of SMs, so
+// The ring of copies that fits; false where there is no room for three stages (or all k-blocks).
+//
+// A CTA that finds too little tensor memory free waits for it, and one of a cluster is waited for by
+// others that hold some: two kernels' clusters on one SM could wait for one another in a ring.  So a CTA
+// takes at least as large a share of an SM's shared memory as of its tensor memory; those that
+// fit an SM together then all have theirs.
+template <bool GATED, bool EXPERTS>
+bool lay_out(Shape &h, int64_t groups, int n_experts) {
+  constexpr int W = GATED ? 2 : 1;
+  const size_t besides = 1024 + kScaleStages * scale_bytes(h.tn) + kBarBytes +
+                         (EXPERTS ? round_up(2 * (n_experts + 4) * sizeof(int), 16) : 0) +
+                         (h.one ? 0 : direct_bytes(Warps<GATED, EXPERTS, false>::kEpilogue));
+  const size_t all = h.per_sm > 1 ? kSmemTwo : kSmem, room = all > besides ? all - besides : 0, stage = (size_t)(W * BM + h.tn) * BK;
+  const int64_t blocks = 4 * ceil_div(groups, (int64_t)h.splits);   // of a CTA, at most
+  int64_t stages = (int64_t)(room / stage);
+  if (stages > kMaxStages) stages = kMaxStages;
+  if (h.one && stages > blocks) stages = blocks;
+  h.stages = (int)stages;
+  h.ring_bytes = (uint32_t)(stages * stage);
+  const size_t sums = h.one ? (size_t)W * h.tn * BM * 4 : 0;
+  if (h.ring_bytes < sums) h.ring_bytes = (uint32_t)sums;
+  h.smem = besides + h.ring_bytes;
+  for (h.tmem_cols = 32; h.tmem_cols < (h.one ? 1 : 2) * W * h.tn + 2 * (int)kScaleCols;) h.tmem_cols *= 2;
+  const size_t share = h.tmem_cols * (kSmemTwo / 256);
+  if (h.one && h.smem < share) h.smem = share;
+  return h.smem <= all && (stages >= 3 || (h.one && stages == blocks));
+}
+
+// Clusters of `splits` CTAs, per_sm on an SM, that run at once.  They lie within groups of SMs, so
 // there is room for fewer than SMs / splits.
 template <typename TO, bool GATED, bool EXPERTS>
-int clusters_at_once(int dev, int splits, int sms) {
-  static PerDevice<9> known;
-  return known.get(dev, splits, [splits, sms]() {
+int clusters_at_once(int dev, int splits, int per_sm, int sms) {
+  static PerDevice<18> known;
+  return known.get(dev, splits + 9 * (per_sm - 1), [=]() {
+    const auto kernel = linear_kernel<TO, GATED, EXPERTS, true>;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)splits;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(splits * sms));
-    cfg.blockDim = dim3(kThreadsOf<GATED, EXPERTS>);
-    cfg.dynamicSmemBytes = smem_bytes(EXPERTS);
+    cfg.blockDim = dim3(32 * Warps<GATED, EXPERTS, true>::kAll);
+    cfg.dynamicSmemBytes = per_sm > 1 ? kSmemTwo : kSmem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, (const void *)linear_kernel<TO, GATED, EXPERTS>, &cfg) == cudaSuccess) return n;
+    if (cudaOccupancyMaxActiveClusters(&n, (const void *)kernel, &cfg) == cudaSuccess) return n;
     (void)cudaGetLastError();
     return 0;
-  }, sms / splits * 7 / 8);
+  }, per_sm * sms / splits * 7 / 8);
 }
 
-// Tile of tokens and splits of K: the least of an estimate in SM cycles, as for the plain product:
-// a k-block of a tile takes the MMAs' time or that of their issue, the memory brings each operand once
-// at 3500 bytes a cycle, L2 what the tiles fill again.  Of experts the number of tiles is not known
-// here: as many as if the rows were dealt evenly, or what there can be at most where K is split (one
-// tile a cluster).
-struct Shape { int tn, splits; };
-
+// The cut with the least of an estimate in SM cycles, as for the plain product: a k-block of a tile takes
+// the MMAs' time or that of their issue, the memory brings each operand once at 3500 bytes a cycle, L2
+// what the tiles fill again; a launch costs 6400, sums that meet 1400 + 8 a token.  Of experts the number
+// of tiles is not known here: as many as if the rows were dealt evenly, or what there can be at most where
+// each cluster has one.
 template <typename TO, bool GATED, bool EXPERTS>
 Shape choose(const Fp8LinearArgs &g, int dev, int sms) {
   constexpr int W = GATED ? 2 : 1;
@@ -820,7 +886,7 @@ Shape choose(const Fp8LinearArgs &g, int dev, int sms) {
   const double used = EXPERTS ? g.n_experts * (1.0 - pow(1.0 - 1.0 / g.n_experts, (double)g.M)) : 1.0;
   const double rows = g.M / used;
   const double once = ((double)g.M + W * used * g.N) * g.K / 3500.0;
-  Shape best{16, 1};
+  Shape best{};
   double best_t = 1e30;
   for (int tn = 16; tn <= most; tn += EXPERTS && !GATED && tn >= kBox ? kBox : 16) {
     if (!EXPERTS && tn - 16 >= g.M) break;
@@ -830,28 +896,49 @@ Shape choose(const Fp8LinearArgs &g, int dev, int sms) {
     const double mma = W * 3.45 * tn, issue = 300 + W * 1.7 * tn;
     const double c = mma > issue ? mma : issue;
     const double fill = tiles * g.K * (W * BM + tn) / 20000.0;
-    for (int s = 1; s <= 8 && s <= groups; ++s) {
-      if (s > 1 && (at_most > clusters_at_once<TO, GATED, EXPERTS>(dev, s, sms) ||
-                    (uint32_t)(W * tn * BM * 4) > kRingBytes))
+    for (int s = 1; s <= 8 && s <= groups; ++s) {   // 1: from tile to tile
+      if (s > 1 && at_most * s > 2 * sms) break;
+      Shape h{tn, s, 1, s > 1};
+      if (h.one) {
+        // alone on its SM, for copies in flight; or two, where there are that many
+        auto fits = [&]() {
+          return lay_out<GATED, EXPERTS>(h, groups, g.n_experts) &&
+                 at_most <= clusters_at_once<TO, GATED, EXPERTS>(dev, s, h.per_sm, sms);
+        };
+        if (!fits()) {
+          h.per_sm = 2;
+          if (!fits()) continue;
+        }
+      } else if (!lay_out<GATED, EXPERTS>(h, groups, g.n_experts)) {
         continue;
-      const double busy = ceil(tiles * s / sms);
-      const double work = busy * 4 * ceil_div(groups, (int64_t)s) * c;
+      }
+      const double busy = ceil(tiles * h.splits / sms);
+      const double work = busy * 4 * ceil_div(groups, (int64_t)h.splits) * c;
       double t = sqrt(work * work + (once + fill) * (once + fill));
-      t += 6400.0 + (s > 1 ? 1400.0 + 8.0 * W * tn : 0.0) + 800.0 * (busy - 1);
-      if (t < best_t) best_t = t, best = Shape{tn, s};
+      t += 6400.0 + (h.one ? 1400.0 + 8.0 * W * tn : 0.0) + (h.one ? 0.0 : 800.0 * (busy - 1));
+      if (t < best_t) best_t = t, best = h;
     }
   }
   return best;
 }
 
+template <typename TO, bool GATED, bool EXPERTS, bool ONE>
+gptq_status launch(const Shape &h, unsigned ctas, cudaStream_t s, const CUtensorMap &mw0, const CUtensorMap &mw1,
+                   const CUtensorMap &ma, const Params &p, DevStatus *st) {
+  GPTQ_TRY(ensure_smem_attr((const void *)linear_kernel<TO, GATED, EXPERTS, ONE>, (int)kSmem));
+  return launch_early(linear_kernel<TO, GATED, EXPERTS, ONE>, dim3(ctas), dim3(32 * Warps<GATED, EXPERTS, ONE>::kAll),
+                      h.smem, h.splits, s, mw0, mw1, ma, p, st);
+}
+
 template <typename TO, bool GATED, bool EXPERTS>
 gptq_status run(const Fp8LinearArgs &g, DevStatus *st, cudaStream_t s) {
   constexpr int W = GATED ? 2 : 1;
-  GPTQ_TRY(ensure_smem_attr((const void *)linear_kernel<TO, GATED, EXPERTS>, (int)smem_bytes(EXPERTS)));
   int sms = 0, dev = -1;
   GPTQ_TRY(device_sm_count(&sms));
   GPTQ_CUDA_CHECK(cudaGetDevice(&dev));
-  const Shape sh = choose<TO, GATED, EXPERTS>(g, dev, sms);
+  // (set before the clusters that fit are asked for)
+  GPTQ_TRY(ensure_smem_attr((const void *)linear_kernel<TO, GATED, EXPERTS, true>, (int)kSmem));
+  const Shape h = choose<TO, GATED, EXPERTS>(g, dev, sms);
   Params p{};
   p.a = g.a; p.lda = g.lda; p.K = g.K;
   p.ae = g.ae; p.ldae = g.ldae;
@@ -868,23 +955,20 @@ gptq_status run(const Fp8LinearArgs &g, DevStatus *st, cudaStream_t s) {
   p.a_rows = g.a_rows; p.M = g.M; p.N = g.N;
   p.act = g.act;
   p.kb = (int)ceil_div(g.K, (int64_t)BK);
-  p.tn = sh.tn;
-  p.splits = sh.splits;
+  p.tn = h.tn; p.stages = h.stages; p.splits = h.splits; p.ring_bytes = h.ring_bytes;
+  p.box = h.tn < kBox ? h.tn : kBox;   // (tn is a multiple of it)
   p.n_w = (int)ceil_div(g.N, (int64_t)BM);
-  p.n_m = (int)ceil_div(g.M, (int64_t)sh.tn);
+  p.n_m = (int)ceil_div(g.M, (int64_t)h.tn);
   p.across = (int)ceil_div(p.n_w, ceil_div(p.n_w, kAcross));
-  const int64_t along = EXPERTS ? (g.n_experts < g.M ? g.n_experts : g.M) + g.M / sh.tn : p.n_m;
+  const int64_t along = EXPERTS ? (g.n_experts < g.M ? g.n_experts : g.M) + g.M / h.tn : p.n_m;
   const int64_t tiles = p.n_w * along;   // at most
   if (tiles * 8 > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-  p.acc_cols = sh.tn;
-  p.tmem_cols = (int)kTmemCols;
+  p.acc_cols = h.tn;
+  p.tmem_cols = h.tmem_cols;
   p.offsets = g.offsets; p.order = g.order;
   p.n_experts = g.n_experts; p.top_k = g.top_k;
   p.wait_ns = g.wait_ns;
   p.lost = (int)g.lost;
-  const int fit = (int)(kRingBytes / (uint32_t)((W * BM + sh.tn) * BK));
-  p.stages = fit < kMaxStages ? fit : kMaxStages;
-  p.box = sh.tn < kBox ? sh.tn : kBox;   // (tn is a multiple of it)
   const int64_t mats = EXPERTS ? g.n_experts : 1;
   CUtensorMap mw[2], ma;
   for (int w = 0; w < W; ++w)
@@ -893,11 +977,11 @@ gptq_status run(const Fp8LinearArgs &g, DevStatus *st, cudaStream_t s) {
       return GPTQ_ERR_UNSUPPORTED;
   if (W == 1) mw[1] = mw[0];
   if (!tc::make_tmap_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, g.a_rows, g.K, g.lda, BK,
-                        EXPERTS ? p.box : sh.tn))
+                        EXPERTS ? p.box : h.tn))
     return GPTQ_ERR_UNSUPPORTED;
-  const int64_t ctas = sh.splits > 1 ? tiles * sh.splits : (tiles < sms ? tiles : sms);
-  return launch_early(linear_kernel<TO, GATED, EXPERTS>, dim3((unsigned)ctas), dim3(kThreadsOf<GATED, EXPERTS>), smem_bytes(EXPERTS),
-                      sh.splits, s, mw[0], mw[1], ma, p, st);
+  const unsigned ctas = (unsigned)(h.one ? tiles * h.splits : (tiles < sms ? tiles : sms));
+  return h.one ? launch<TO, GATED, EXPERTS, true>(h, ctas, s, mw[0], mw[1], ma, p, st)
+               : launch<TO, GATED, EXPERTS, false>(h, ctas, s, mw[0], mw[1], ma, p, st);
 }
 
 }  // namespace
