@@ -55,6 +55,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kTurnPitch = 36;              // (words in different banks along either way)
 constexpr size_t kSmem = 227 * 1024;        // of a CTA alone on its SM
 constexpr size_t kSmemTwo = 113 * 1024;     // of one of two
+constexpr size_t kSmemLeast = 40 * 1024;
 constexpr size_t kBarBytes = 512;
 static_assert(2 * kMaxTn + 2 * kScaleCols <= kTmemCols, "TMEM columns");
 static_assert(4 * kMaxTnGated + 2 * kScaleCols <= kTmemCols, "TMEM columns");
@@ -824,8 +825,9 @@ struct Shape {
 //
 // A CTA that finds too little tensor memory free waits for it, and one of a cluster is waited for by
 // others that hold some: two kernels' clusters on one SM could wait for one another in a ring.  So a CTA
-// takes at least as large a share of an SM's shared memory as of its tensor memory; those that
-// fit an SM together then all have theirs.
+// takes at least as large a share of an SM's shared memory as of its tensor memory, and more than the
+// library's kernels with all of the tensor memory leave (193 KB and up); those that fit an SM together then
+// all have theirs.
 template <bool GATED, bool EXPERTS>
 bool lay_out(Shape &h, int64_t groups, int n_experts) {
   constexpr int W = GATED ? 2 : 1;
@@ -843,8 +845,8 @@ bool lay_out(Shape &h, int64_t groups, int n_experts) {
   if (h.ring_bytes < sums) h.ring_bytes = (uint32_t)sums;
   h.smem = besides + h.ring_bytes;
   for (h.tmem_cols = 32; h.tmem_cols < (h.one ? 1 : 2) * W * h.tn + 2 * (int)kScaleCols;) h.tmem_cols *= 2;
-  const size_t share = h.tmem_cols * (kSmemTwo / 256);
-  if (h.one && h.smem < share) h.smem = share;
+  const size_t share = h.tmem_cols * (kSmemTwo / 256), least = share < kSmemLeast ? kSmemLeast : share;
+  if (h.one && h.smem < least) h.smem = least;
   return h.smem <= all && (stages >= 3 || (h.one && stages == blocks));
 }
 

@@ -118,15 +118,19 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
     sum = warp_sum(sum);
   }
   out.sum = (float)sum;
-  // Error of an fp32 c, both sides of a comparison.  A sigmoid's: 2^-24 each from the exponential (2
-  // ulp, a quarter of which gets through), the sum and the quotient.  A softmax's, relative to s,
-  // which is at most 1 / sum: VPL + 5 additions, the exponential's 2^-22 and what rounding its
-  // argument x does, x e^x <= 0.37, the quotient.  And the addition of the bias, 2^-24 |c|.
-  const float tau = p.sigmoid ? 3 * 0x1p-23f : (VPL + 14) * 0x1p-23f / (float)sum;
+  // Error of an fp32 c, both sides of a comparison.  A sigmoid's, from the quick functions: the
+  // exponential's 2^-22 and what rounding its argument does, 1.44 |x| 2^-24, of which s (1 - s) gets
+  // through: 2^-24 in all at most; the sum 2^-24, the reciprocal 2^-23.  A softmax's, relative to s, which
+  // is at most 1 / sum: VPL + 5 additions, the exponential's 2^-22 and what rounding its argument x
+  // does, x e^x <= 0.37, the reciprocal and the product.  And the addition of the bias, 2^-24 |c|.
+  const float tau = p.sigmoid ? 4 * 0x1p-23f : (VPL + 15) * 0x1p-23f / (float)sum;
   if (scored) {
+    const C inv = (C)1 / sum;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const C s = p.sigmoid ? (C)1 / ((C)1 + (C)exp(-(C)x[i])) : c[i] / sum;
+      C s;
+      if constexpr (kSingle) s = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-x[i])) : c[i] * inv;
+      else s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)x[i])) : c[i] / sum;
       const float b = p.bias && e0 + i < p.n_experts && i < p.each ? p.bias[e0 + i] : 0.0f;
       c[i] = fp8::finite(x[i]) && fp8::finite(b) ? s + (C)b : -(C)INFINITY;
     }
@@ -145,9 +149,8 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
     const bool sums = p.group_top > 1;
     K value = 0;
     auto join = [&](K &a, K &b, K oa, K ob) {
-      const K low = oa > a ? a : oa, high = ob > b ? ob : b;
-      a = oa > a ? oa : a;
-      b = low > high ? low : high;
+      b = max(min(a, oa), max(b, ob));
+      a = max(a, oa);
     };
     // with sums of scores the keys compared are the scores'; else those of the choice itself
     auto key_of = [&](int i) -> K { return !by_logit || !sums ? key[i] : key[i] ? to_key(c[i]) : 0; };
@@ -196,18 +199,24 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
   const bool watch = kSingle && !by_logit;
   const int rounds = !watch ? p.top_k : LIST ? 32 : min(p.top_k + 1, 32);
   K last = 0;
+  float gap = INFINITY, size = 0.0f;   // the least between two rounds; the largest |c|
   int j = 0;
   for (; j < rounds; ++j) {
     K mine = key[0];
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) mine = key[i] > mine ? key[i] : mine;
+    for (int i = 1; i < VPL; ++i) mine = max(mine, key[i]);
     const K best = warp_max_key(mine);
     if (best == 0) break;
-    if (watch && j > 0) {
-      const bool close = near(of_key(last), of_key(best), 1.0f);
-      if (close && !LIST) return false;
-      if (j >= p.top_k && !close) break;
-      sure = sure && !close;
+    if (watch) {
+      if constexpr (LIST) {
+        const bool close = j > 0 && near(of_key(last), of_key(best), 1.0f);
+        if (j >= p.top_k && !close) break;
+        sure = sure && !close;
+      } else {
+        const float c1 = (float)of_key(best);
+        if (j > 0) gap = fminf(gap, (float)of_key(last) - c1);
+        size = fmaxf(size, fabsf(c1));
+      }
     }
     last = best;
     const int w = __ffs(__ballot_sync(0xffffffffu, mine == best)) - 1;
@@ -222,6 +231,7 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
     at = __shfl_sync(0xffffffffu, at, w);
     if (lane == j) out.id = w * p.each + at;
   }
+  if (watch && !LIST) sure = gap > tau + 0x1p-23f * size;
   if (LIST && j < 32) out.near = j;   // (32 rounds without an end may have left one out)
   // with 32 to choose there is no round more
   return sure && !(watch && !LIST && p.top_k == 32 && p.n_experts > 32);

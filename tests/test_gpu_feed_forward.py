@@ -13,6 +13,7 @@ Tolerances, from the arithmetic each operator is allowed:
   * combine: fp32 sums of k terms: (k + 1) 2^-24 of the magnitudes, and the output's rounding.
 """
 
+import gc
 import math
 
 import numpy as np
@@ -31,6 +32,8 @@ def _lib():
     build_lib.build()
     gptq.load()
     torch.cuda.init()
+    yield
+    gc.collect()   # frames of expected errors hold tensors: others' tests look at what is allocated
 
 
 def _dev(x):
