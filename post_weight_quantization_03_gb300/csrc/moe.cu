@@ -89,14 +89,41 @@ __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
 // What a warp found for a token: lane j has the j-th chosen expert (-1: none).
 struct Chosen {
   int id;
-  int near;         // > 0: so many lanes have one, the chosen among them, but fp32 does not tell which
   float top, sum;   // largest logit; sum of exp(logit - top), where the weights need it
 };
 
-// A whole warp chooses a token's experts, c in type C; false where fp32 does not tell.  LIST: then
-// with the few that are in question.
-template <typename C, int VPL, bool LIST = false>
-__device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams &p, int lane, Chosen &out) {
+// (the type at run time: a kernel is a long one, and reads a few numbers a lane)
+__device__ __forceinline__ float logit(const RouteParams &p, int64_t at) {
+  if (p.dtype == GPTQ_F32) return ((const float *)p.logits)[at];
+  if (p.dtype == GPTQ_F16) return to_f32(((const __half *)p.logits)[at]);
+  return to_f32(((const __nv_bfloat16 *)p.logits)[at]);
+}
+// The order of a few experts whose c, of sigmoids, are too near to one another: the first n lanes' `id`.
+// In fp64, one in a lane.
+__device__ __forceinline__ int sort_near(const RouteParams &p, int64_t t, int lane, int id, int n) {
+  uint64_t key = 0;
+  if (lane < n) {
+    const double x = logit(p, t * p.ld + id);
+    key = to_key(1.0 / (1.0 + exp(-x)) + (p.bias ? (double)p.bias[id] : 0.0));
+  }
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint64_t k = __shfl_sync(0xffffffffu, key, j);
+    const int i = __shfl_sync(0xffffffffu, id, j);
+    rank += k > key || (k == key && i < id);
+  }
+  int mine = -1;
+  for (int j = 0; j < p.top_k; ++j) {
+    const uint32_t who = __ballot_sync(0xffffffffu, lane < n && rank == j);
+    const int i = __shfl_sync(0xffffffffu, id, who ? __ffs(who) - 1 : 0);
+    if (lane == j && who) mine = i;
+  }
+  return mine;
+}
+
+// A whole warp chooses token t's experts, c in type C; false where fp32 does not tell.
+template <typename C, int VPL>
+__device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams &p, int64_t t, int lane, Chosen &out) {
   using K = typename std::conditional<std::is_same<C, float>::value, uint32_t, uint64_t>::type;
   constexpr bool kSingle = std::is_same<C, float>::value;
   const bool by_logit = !p.bias;                        // the order of the c is that of the logits
@@ -192,33 +219,28 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
       if (!(open >> ((p.lanes > 0 ? lane / p.lanes : (e0 + i) / p.size) & 31) & 1)) key[i] = 0;
   }
   out.id = -1;
-  out.near = 0;
   if (!sure) return false;
-  // fp32: a round more, for the best of the others, which may be too near to the last chosen; or more
-  // while the next is too near, so that what is not among these cannot be chosen
+  // fp32: rounds go on past top_k while the next is too near to the last, so that what is not among
+  // these cannot be chosen
   const bool watch = kSingle && !by_logit;
-  const int rounds = !watch ? p.top_k : LIST ? 32 : min(p.top_k + 1, 32);
-  K last = 0;
-  float gap = INFINITY, size = 0.0f;   // the least between two rounds; the largest |c|
+  float last = 0.0f, gap = INFINITY, size = 0.0f;   // c of the round before; the least between two; the largest |c|
+  const auto bound = [&]() { return tau + 0x1p-23f * size; };
   int j = 0;
-  for (; j < rounds; ++j) {
+  for (; j < (watch ? 32 : p.top_k); ++j) {
     K mine = key[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) mine = max(mine, key[i]);
     const K best = warp_max_key(mine);
     if (best == 0) break;
     if (watch) {
-      if constexpr (LIST) {
-        const bool close = j > 0 && near(of_key(last), of_key(best), 1.0f);
-        if (j >= p.top_k && !close) break;
-        sure = sure && !close;
-      } else {
-        const float c1 = (float)of_key(best);
-        if (j > 0) gap = fminf(gap, (float)of_key(last) - c1);
-        size = fmaxf(size, fabsf(c1));
+      const float c1 = (float)of_key(best);
+      size = fmaxf(size, fabsf(c1));
+      if (j > 0) {
+        if (j >= p.top_k && last - c1 > bound()) break;
+        gap = fminf(gap, last - c1);
       }
+      last = c1;
     }
-    last = best;
     const int w = __ffs(__ballot_sync(0xffffffffu, mine == best)) - 1;
     int at = 0;
     if (lane == w) {
@@ -231,18 +253,14 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
     at = __shfl_sync(0xffffffffu, at, w);
     if (lane == j) out.id = w * p.each + at;
   }
-  if (watch && !LIST) sure = gap > tau + 0x1p-23f * size;
-  if (LIST && j < 32) out.near = j;   // (32 rounds without an end may have left one out)
-  // with 32 to choose there is no round more
-  return sure && !(watch && !LIST && p.top_k == 32 && p.n_experts > 32);
+  if (watch && (gap <= bound() || (j == 32 && p.n_experts > 32))) {
+    if (!p.sigmoid || j == 32) return false;   // (32 rounds without an end may have left one out)
+    out.id = sort_near(p, t, lane, out.id, j);
+  }
+  if (lane >= p.top_k) out.id = -1;
+  return true;
 }
 
-// (the type at run time: a kernel is a long one, and reads a few numbers a lane)
-__device__ __forceinline__ float logit(const RouteParams &p, int64_t at) {
-  if (p.dtype == GPTQ_F32) return ((const float *)p.logits)[at];
-  if (p.dtype == GPTQ_F16) return to_f32(((const __half *)p.logits)[at]);
-  return to_f32(((const __nv_bfloat16 *)p.logits)[at]);
-}
 template <typename T, int VPL>
 __device__ __forceinline__ void load_logits_of(float (&x)[VPL], const RouteParams &p, int64_t t, int lane) {
   const T *row = (const T *)p.logits + t * p.ld + lane * p.each;
@@ -254,29 +272,6 @@ __device__ __forceinline__ void load_logits(float (&x)[VPL], const RouteParams &
   if (p.dtype == GPTQ_F32) load_logits_of<float>(x, p, t, lane);
   else if (p.dtype == GPTQ_F16) load_logits_of<__half>(x, p, t, lane);
   else load_logits_of<__nv_bfloat16>(x, p, t, lane);
-}
-
-// A sigmoid's c of the few that are too near to one another, in fp64, one in a lane; their order.
-__device__ __forceinline__ int sort_near(const RouteParams &p, int64_t t, int lane, const Chosen &ch) {
-  const int id = ch.id;
-  uint64_t key = 0;
-  if (lane < ch.near) {
-    const double x = logit(p, t * p.ld + id);
-    key = to_key(1.0 / (1.0 + exp(-x)) + (p.bias ? (double)p.bias[id] : 0.0));
-  }
-  int rank = 0;
-  for (int j = 0; j < ch.near; ++j) {
-    const uint64_t k = __shfl_sync(0xffffffffu, key, j);
-    const int i = __shfl_sync(0xffffffffu, id, j);
-    rank += k > key || (k == key && i < id);
-  }
-  int mine = -1;
-  for (int j = 0; j < p.top_k; ++j) {
-    const uint32_t who = __ballot_sync(0xffffffffu, lane < ch.near && rank == j);
-    const int i = __shfl_sync(0xffffffffu, id, who ? __ffs(who) - 1 : 0);
-    if (lane == j && who) mine = i;
-  }
-  return mine;
 }
 
 // The weight of this lane's chosen expert, whose logit is x.
@@ -301,17 +296,12 @@ __device__ __forceinline__ int route_token(const RouteParams &p, int64_t t, int 
   float x[VPL];
   load_logits(x, p, t, lane);
   Chosen ch;
-  if (!choose<float, VPL, AGAIN>(x, p, lane, ch)) {
+  if (!choose<float, VPL>(x, p, t, lane, ch)) {
     if constexpr (!AGAIN) return -2;
-    if (p.sigmoid && ch.near > 0) {
-      ch.id = sort_near(p, t, lane, ch);
-    } else {
-      const float sum = ch.sum;
-      choose<double, VPL>(x, p, lane, ch);
-      ch.sum = sum;
-    }
+    const float sum = ch.sum;
+    choose<double, VPL>(x, p, t, lane, ch);
+    ch.sum = sum;
   }
-  if (lane >= p.top_k) ch.id = -1;
   const float of = ch.id >= 0 ? logit(p, t * p.ld + ch.id) : 0.0f;
   const float w = weight_of(ch, of, p);
   if (lane < p.top_k) {
@@ -325,7 +315,7 @@ __device__ __forceinline__ int route_token(const RouteParams &p, int64_t t, int 
 struct PlanSmem {
   uint32_t word[2][1024];       // of each expert: which of 64 tokens go to it
   int at[1024];                 // where its next assignment goes
-  int part[2][kPlanThreads];
+  int part[4][kPlanThreads];    // of two neighbouring experts: all, those before
   int warp[32];
 };
 
@@ -343,37 +333,36 @@ __device__ __forceinline__ void fill_words(const RouteParams &p, const int *ids,
 __device__ __forceinline__ void plan(const RouteParams &p, int mine, const int *ids, PlanSmem &sm) {
   const int tid = threadIdx.x, lane = tid % 32;
   const int t0 = mine * p.chunk, t1 = min(t0 + p.chunk, (int)p.n_tokens);
-  fill_words(p, ids, t0 * p.top_k, min(t0 + kWord, t1) * p.top_k, t0, sm);
   // an expert's assignments in all chunks, and in those before this one
-  int sum = 0, before = 0;
-  if (p.chunks == 1) {
-    if (tid < p.n_experts) sum = __popc(sm.word[0][tid]) + __popc(sm.word[1][tid]);
-  } else {
-    int span = 32;              // threads of a part: each has two experts, and every parts-th chunk
-    while (span < p.pairs) span *= 2;
-    const int parts = kPlanThreads / span, part = tid / span, e2 = tid % span;
-    int all[2] = {0, 0}, pre[2] = {0, 0};
-    if (e2 < p.pairs) {
+  int span = 32;              // threads of a part: each has two experts, and every parts-th chunk
+  while (span < p.pairs) span *= 2;
+  const int parts = kPlanThreads / span, part = tid / span, e2 = tid % span;
+  int all[2] = {0, 0}, pre[2] = {0, 0};
+  if (p.chunks > 1 && e2 < p.pairs) {
 #pragma unroll 16
-      for (int c = part; c < p.chunks; c += parts) {
-        const uint32_t two = p.counts[(int64_t)c * p.pairs + e2];
-        all[0] += two & 0xffffu;
-        all[1] += two >> 16;
-        pre[0] += c < mine ? two & 0xffffu : 0;
-        pre[1] += c < mine ? two >> 16 : 0;
-      }
+    for (int c = part; c < p.chunks; c += parts) {
+      const uint32_t two = p.counts[(int64_t)c * p.pairs + e2];
+      all[0] += two & 0xffffu;
+      all[1] += two >> 16;
+      pre[0] += c < mine ? two & 0xffffu : 0;
+      pre[1] += c < mine ? two >> 16 : 0;
     }
+  }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      sm.part[0][tid] = all[h];
-      sm.part[1][tid] = pre[h];
-      __syncthreads();
-      if (tid < p.n_experts && (tid & 1) == h)
-        for (int q = 0; q < parts; ++q) {
-          sum += sm.part[0][q * span + tid / 2];
-          before += sm.part[1][q * span + tid / 2];
-        }
-      __syncthreads();
+  for (int h = 0; h < 2; ++h) {
+    sm.part[h][tid] = all[h];
+    sm.part[2 + h][tid] = pre[h];
+  }
+  fill_words(p, ids, t0 * p.top_k, min(t0 + kWord, t1) * p.top_k, t0, sm);   // (and waits for all)
+  int sum = 0, before = 0;
+  if (tid < p.n_experts) {
+    if (p.chunks == 1) {
+      sum = __popc(sm.word[0][tid]) + __popc(sm.word[1][tid]);
+    } else {
+      for (int q = 0; q < parts; ++q) {
+        sum += sm.part[tid & 1][q * span + tid / 2];
+        before += sm.part[2 + (tid & 1)][q * span + tid / 2];
+      }
     }
   }
   int scan = sum;
