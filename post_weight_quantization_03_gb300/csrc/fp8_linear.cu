@@ -83,6 +83,7 @@ struct Params {
   uint32_t ring_bytes;
   const int32_t *offsets, *order;
   int n_experts, top_k;
+  uint32_t per_tn, per_k;   // 2^32 / tn, / top_k, rounded up: quotients of numbers below 2^23
   uint64_t wait_ns;
   int lost;             // test hook: this copy of the producer's is left out
 };
@@ -107,31 +108,43 @@ __device__ __forceinline__ void activate(float (&x)[N], int act) {
   }
 }
 
+// a / b of a below 2^22, in a third of the instructions of the exact quotient of any (each tile starts
+// with some in every role).
+__device__ __forceinline__ int quotient(int a, int b) {
+  int q = __float2int_rz(__fdividef((float)a, (float)b));
+  const int r = a - q * b;
+  return q + (r >= b) - (r < 0);
+}
+
 // k-blocks of this CTA: rank r of the cluster takes an even share of the groups of four.
 __device__ __forceinline__ void k_range(const Params &p, int rank, int &k0, int &k1) {
   const int groups = (p.kb + 3) / 4;
-  k0 = groups * rank / p.splits * 4;
-  k1 = min(groups * (rank + 1) / p.splits * 4, p.kb);
+  k0 = quotient(groups * rank, p.splits) * 4;
+  k1 = min(quotient(groups * (rank + 1), p.splits) * 4, p.kb);
 }
 
 // Where the experts' positions and tiles begin, in shared memory.
 struct Plan {
   int *at;      // [n_experts + 1] positions
   int *tiles;   // [n_experts + 1] tiles of tn positions
+  const int *order;   // of all positions: where there are few in shared memory, so that copies of rows by
+                      // index are not asked for after all of the weights' (they then came 4 us late)
 };
+constexpr int kFewPositions = 512;
 
 struct Tile {
   int e, n;             // expert; tile along the weights
   int m0, cols;         // positions
 };
 
-template <bool EXPERTS>
+// ONE: the grid is (CTAs of a cluster, tiles along the weights, along the tokens).
+template <bool EXPERTS, bool ONE>
 __device__ __forceinline__ Tile tile_of(const Params &p, const Plan &plan, int t) {
   Tile r;
   int m;
   if constexpr (EXPERTS) {
-    r.n = t % p.n_w;
-    m = t / p.n_w;
+    m = ONE ? blockIdx.z : t < (1 << 22) ? quotient(t, p.n_w) : t / p.n_w;
+    r.n = ONE ? blockIdx.y : t - m * p.n_w;
     int lo = 0, hi = p.n_experts;   // tiles[lo] <= m < tiles[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -140,16 +153,21 @@ __device__ __forceinline__ Tile tile_of(const Params &p, const Plan &plan, int t
     }
     // an expert's tiles are of even size, in whole groups of 16
     const int tiles = plan.tiles[lo + 1] - plan.tiles[lo], count = plan.at[lo + 1] - plan.at[lo];
-    const int size = ((count + tiles - 1) / tiles + 15) / 16 * 16, from = (m - plan.tiles[lo]) * size;
+    const int size = (quotient(count + tiles - 1, tiles) + 15) / 16 * 16, from = (m - plan.tiles[lo]) * size;
     r.e = lo;
     r.m0 = plan.at[lo] + from;
     r.cols = min(count - from, size);   // (above 0: size is at most tn)
   } else {
-    // runs of `across` tiles along the weights, each for all tokens
-    const int run = t / (p.across * p.n_m), n0 = run * p.across, width = min(p.across, p.n_w - n0);
-    const int in_run = t - n0 * p.n_m;
-    r.n = n0 + in_run % width;
-    m = in_run / width;
+    if constexpr (ONE) {
+      r.n = blockIdx.y;
+      m = blockIdx.z;
+    } else {
+      // runs of `across` tiles along the weights, each for all tokens
+      const int per_run = p.across * p.n_m, run = t < (1 << 22) ? quotient(t, per_run) : t / per_run;
+      const int n0 = run * p.across, width = min(p.across, p.n_w - n0), in_run = t - n0 * p.n_m;
+      m = in_run < (1 << 22) ? quotient(in_run, width) : in_run / width;
+      r.n = n0 + in_run - m * width;
+    }
     r.e = 0;
     r.m0 = m * p.tn;
     r.cols = (int)min(p.M - r.m0, (int64_t)p.tn);
@@ -159,9 +177,9 @@ __device__ __forceinline__ Tile tile_of(const Params &p, const Plan &plan, int t
 
 // A's row of a position, a_rows (read as zeros) for none.
 template <bool GATHER>
-__device__ __forceinline__ int a_row(const Params &p, int pos) {
+__device__ __forceinline__ int a_row(const Params &p, const Plan &plan, int pos) {
   if constexpr (GATHER) {
-    const int o = p.order[pos], row = o < 0 ? -1 : o / p.top_k;
+    const int o = plan.order[pos], row = o < 0 || p.top_k == 1 ? o : (int)__umulhi((uint32_t)o, p.per_k);
     return row >= 0 && row < p.a_rows ? row : (int)p.a_rows;
   }
   return pos;
@@ -169,41 +187,52 @@ __device__ __forceinline__ int a_row(const Params &p, int pos) {
 
 // One warp: the plan from the offsets, which are limited to [0, M] and read as increasing.
 __device__ __forceinline__ void make_plan(const Params &p, const Plan &plan, int lane) {
-  const int each = (p.n_experts + 31) / 32, e0 = lane * each;
+  const int each = (p.n_experts + 31) / 32, e0 = lane * each, e1 = min(e0 + each, p.n_experts);
   const int most = (int)p.M;
-  int top = 0;   // the largest offset up to this lane's last expert
-  for (int i = 0; i < each; ++i)
-    if (e0 + i <= p.n_experts) top = max(top, min(plan.at[e0 + i], most));
-  int run = top;
+  int top = 0;   // the largest offset of this lane's
+#pragma unroll 4
+  for (int e = e0; e < e1; ++e) {
+    const int o = min(p.offsets[e], most);
+    plan.at[e] = o;
+    top = max(top, o);
+  }
+  const int end = min(p.offsets[p.n_experts], most);
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, top, o);
+    if (lane >= o) top = max(top, v);
+  }
+  const int all = max(__shfl_sync(0xffffffffu, top, 31), end);
+  int at = __shfl_up_sync(0xffffffffu, top, 1);
+  if (lane == 0) at = 0;
+  int begin = all;   // of this lane's first expert
+  for (int e = e0; e < e1; ++e) {
+    plan.at[e] = at = max(at, plan.at[e]);
+    if (e == e0) begin = at;
+  }
+  int next = __shfl_down_sync(0xffffffffu, begin, 1);
+  if (lane == 31) next = all;
+  auto tiles_of = [&](int e) {
+    const int count = (e + 1 < e1 ? plan.at[e + 1] : next) - plan.at[e];
+    return (int)__umulhi((uint32_t)(count + p.tn - 1), p.per_tn);
+  };
+  int sum = 0;
+  for (int e = e0; e < e1; ++e) sum += tiles_of(e);
+  int run = sum;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
     const int v = __shfl_up_sync(0xffffffffu, run, o);
-    if (lane >= o) run = max(run, v);
+    if (lane >= o) run += v;
   }
-  int at = __shfl_up_sync(0xffffffffu, run, 1);
-  if (lane == 0) at = 0;
-  const int all = max(__shfl_sync(0xffffffffu, run, 31), min(plan.at[p.n_experts], most));
-  for (int i = 0; i < each; ++i)
-    if (e0 + i < p.n_experts) plan.at[e0 + i] = at = max(at, min(plan.at[e0 + i], most));
-  __syncwarp();
-  if (lane == 0) plan.at[p.n_experts] = all;
-  __syncwarp();
-  int mine = 0;
-  for (int i = 0; i < each; ++i)
-    if (e0 + i < p.n_experts) mine += (plan.at[e0 + i + 1] - plan.at[e0 + i] + p.tn - 1) / p.tn;
-  int sum = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const int v = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += v;
+  int tiles = run - sum;
+  for (int e = e0; e < e1; ++e) {
+    plan.tiles[e] = tiles;
+    tiles += tiles_of(e);
   }
-  int tiles = sum - mine;
-  for (int i = 0; i < each; ++i)
-    if (e0 + i < p.n_experts) {
-      plan.tiles[e0 + i] = tiles;
-      tiles += (plan.at[e0 + i + 1] - plan.at[e0 + i] + p.tn - 1) / p.tn;
-    }
-  if (lane == 31) plan.tiles[p.n_experts] = sum;
+  if (lane == 31) {
+    plan.at[p.n_experts] = all;
+    plan.tiles[p.n_experts] = run;
+  }
 }
 
 // TO: type of the output, if it is not gated.
@@ -248,13 +277,14 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
   int *srow = (int *)(sra + 256);
   float *turned = (float *)(srow + 256), *smax = turned + E * 16 * kTurnPitch;
   int *plan_at = (int *)((uint8_t *)full + kBarBytes + (ONE ? 0 : direct_bytes(E)));
-  const Plan plan{plan_at, plan_at + p.n_experts + 4};
+  int *few = plan_at + 2 * (p.n_experts + 4);   // [kFewPositions]
+  const Plan plan{plan_at, plan_at + p.n_experts + 4, p.M <= kFewPositions ? few : p.order};
   const tc::Waits waits{st, &g_gave_up, p.wait_ns};
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t stage_bytes = (uint32_t)(W * BM + p.tn) * BK;
-  const int rank = p.splits > 1 ? (int)tc::cluster_ctarank() : 0;
-  const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
+  const int rank = ONE ? blockIdx.x : 0;
+  const int first = ONE ? blockIdx.z * p.n_w + blockIdx.y : blockIdx.x, step = ONE ? INT32_MAX / 2 : gridDim.x;
   int k0, k1;
   k_range(p, rank, k0, k1);
 
@@ -277,9 +307,9 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
   if (warp == 1) tc::tmem_alloc(tmem_slot, p.tmem_cols);
   if constexpr (EXPERTS) {
     wait_for_grids();
-    for (int e = threadIdx.x; e <= p.n_experts; e += blockDim.x) plan.at[e] = p.offsets[e];
-    __syncthreads();
     if (warp == 0) make_plan(p, plan, lane);
+    else if (p.M <= kFewPositions)
+      for (int i = threadIdx.x - 32; i < (int)p.M; i += blockDim.x - 32) few[i] = p.order[i];
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -289,7 +319,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
   launch_dependents();
   // The status of the call.  A wait that gives up writes it two seconds or more after its own
   // CTA started, so this store, by the first CTA to start, comes first.
-  if (blockIdx.x == 0 && threadIdx.x == 0) st->status = 0;
+  if (threadIdx.x == 0 && blockIdx.x == 0 && (!ONE || (blockIdx.y == 0 && blockIdx.z == 0))) st->status = 0;
   const int n_tiles = p.n_w * (EXPERTS ? plan.tiles[p.n_experts] : p.n_m);
   const uint32_t set_cols = (uint32_t)(W * p.acc_cols);          // accumulators of a tile
   const uint32_t sc_cols = tmem + kSets * set_cols;
@@ -299,18 +329,18 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
   // has four rows.
   constexpr int kAll = Warps<GATED, EXPERTS, ONE>::kAll;
   const int first_col = rank + (warp + kAll - 2) % kAll * p.splits;
-  const Tile one = ONE && first < n_tiles ? tile_of<EXPERTS>(p, plan, first) : Tile{0, 0, 0, 0};
+  const Tile one = ONE && first < n_tiles ? tile_of<EXPERTS, ONE>(p, plan, first) : Tile{0, 0, 0, 0};
   const int64_t n4 = (int64_t)one.n * BM + lane * 4;
   float fin_rw[W][4], fin_bias[W][4], fin_ra = 1.0f;
   int64_t fin_row = -1;
   TO fin_res[4];
   auto ask_token = [&](int col) {
     if (col >= one.cols) return;
-    const int pos = one.m0 + col, r = a_row<GATHER>(p, pos);
+    const int pos = one.m0 + col, r = a_row<GATHER>(p, plan, pos);
     fin_ra = p.ra && r < p.a_rows ? p.ra[r] : 1.0f;
     fin_row = pos;
     if constexpr (EXPERTS && !GATED) {
-      const int o = p.order[pos];
+      const int o = plan.order[pos];
       fin_row = o >= 0 && o < p.M ? o : -1;
     }
     if constexpr (!GATED)
@@ -343,7 +373,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
       if constexpr (!GATHER) tc::tma_prefetch_desc(&ma);
 #pragma unroll 1
       for (int t = first; t < n_tiles && ok; t += step) {
-        const Tile tile = tile_of<EXPERTS>(p, plan, t);
+        const Tile tile = tile_of<EXPERTS, ONE>(p, plan, t);
         // rows that the MMA reads: of experts, whole groups of 16
         const int rows = EXPERTS ? (tile.cols + 15) / 16 * 16 : p.tn;
         const int copied = GATHER ? 0 : EXPERTS ? (rows + p.box - 1) / p.box * p.box : rows;
@@ -378,14 +408,14 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
     static_assert(kLoaders % 2 == 0, "a lane's rows are the same modulo 8");
 #pragma unroll 1
     for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile tile = tile_of<EXPERTS>(p, plan, t);
+      const Tile tile = tile_of<EXPERTS, ONE>(p, plan, t);
       const int rows = (tile.cols + 15) / 16 * 16;
       const uint8_t *src[kQuads];
       bool there[kQuads];           // (zeros for what is not)
 #pragma unroll
       for (int i = 0; i < kQuads; ++i) {
         const int j = row0 + 4 * kLoaders * i;
-        const int r = j < tile.cols ? a_row<GATHER>(p, tile.m0 + j) : (int)p.a_rows;
+        const int r = j < tile.cols ? a_row<GATHER>(p, plan, tile.m0 + j) : (int)p.a_rows;
         there[i] = r < p.a_rows;
         src[i] = p.a + (there[i] ? r * p.lda : 0) + piece * 16;
       }
@@ -430,7 +460,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
 #pragma unroll 1
     for (int t = first; t < n_tiles && ok; t += step, ++it) {
       const int b = it & 1, use = it >> 1;   // accumulators in turn
-      const int rows = EXPERTS ? (tile_of<EXPERTS>(p, plan, t).cols + 15) / 16 * 16 : p.tn;
+      const int rows = EXPERTS ? (tile_of<EXPERTS, ONE>(p, plan, t).cols + 15) / 16 * 16 : p.tn;
       const uint32_t idesc = mx::instr_desc(rows);
       ok = tc::mbar_wait_compact(&tempty[b], (use & 1) ^ 1, waits);
       if (!ok) break;
@@ -475,13 +505,13 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
     // ---------------- scales ----------------
     int g = 0;
     for (int t = first; t < n_tiles && ok; t += step) {
-      const Tile tile = tile_of<EXPERTS>(p, plan, t);
+      const Tile tile = tile_of<EXPERTS, ONE>(p, plan, t);
       int64_t row[8];               // offsets of the lane's rows (-1: none)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         row[i] = -1;
         if (lane + 32 * i < tile.cols) {
-          const int r = a_row<GATHER>(p, tile.m0 + lane + 32 * i);
+          const int r = a_row<GATHER>(p, plan, tile.m0 + lane + 32 * i);
           if (r < p.a_rows) row[i] = r * p.ldae;
         }
       }
@@ -522,12 +552,12 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
     float next_ra = 1.0f, next_rw[W], next_bias[W];
     int next_row = -1;
     auto fetch = [&](int t) {
-      next = tile_of<EXPERTS>(p, plan, t);
+      next = tile_of<EXPERTS, ONE>(p, plan, t);
       if (!ONE && et < next.cols) {
-        const int pos = next.m0 + et, r = a_row<GATHER>(p, pos);
+        const int pos = next.m0 + et, r = a_row<GATHER>(p, plan, pos);
         next_ra = p.ra && r < p.a_rows ? p.ra[r] : 1.0f;
         if constexpr (EXPERTS && !GATED) {
-          const int o = p.order[pos];
+          const int o = plan.order[pos];
           next_row = o >= 0 && o < p.M ? o : -1;
         }
       }
@@ -832,7 +862,7 @@ template <bool GATED, bool EXPERTS>
 bool lay_out(Shape &h, int64_t groups, int n_experts) {
   constexpr int W = GATED ? 2 : 1;
   const size_t besides = 1024 + kScaleStages * scale_bytes(h.tn) + kBarBytes +
-                         (EXPERTS ? round_up(2 * (n_experts + 4) * sizeof(int), 16) : 0) +
+                         (EXPERTS ? round_up((2 * (n_experts + 4) + kFewPositions) * sizeof(int), 16) : 0) +
                          (h.one ? 0 : direct_bytes(Warps<GATED, EXPERTS, false>::kEpilogue));
   const size_t all = h.per_sm > 1 ? kSmemTwo : kSmem, room = all > besides ? all - besides : 0, stage = (size_t)(W * BM + h.tn) * BK;
   const int64_t blocks = 4 * ceil_div(groups, (int64_t)h.splits);   // of a CTA, at most
@@ -925,10 +955,10 @@ Shape choose(const Fp8LinearArgs &g, int dev, int sms) {
 }
 
 template <typename TO, bool GATED, bool EXPERTS, bool ONE>
-gptq_status launch(const Shape &h, unsigned ctas, cudaStream_t s, const CUtensorMap &mw0, const CUtensorMap &mw1,
+gptq_status launch(const Shape &h, dim3 grid, cudaStream_t s, const CUtensorMap &mw0, const CUtensorMap &mw1,
                    const CUtensorMap &ma, const Params &p, DevStatus *st) {
   GPTQ_TRY(ensure_smem_attr((const void *)linear_kernel<TO, GATED, EXPERTS, ONE>, (int)kSmem));
-  return launch_early(linear_kernel<TO, GATED, EXPERTS, ONE>, dim3(ctas), dim3(32 * Warps<GATED, EXPERTS, ONE>::kAll),
+  return launch_early(linear_kernel<TO, GATED, EXPERTS, ONE>, grid, dim3(32 * Warps<GATED, EXPERTS, ONE>::kAll),
                       h.smem, h.splits, s, mw0, mw1, ma, p, st);
 }
 
@@ -969,6 +999,8 @@ gptq_status run(const Fp8LinearArgs &g, DevStatus *st, cudaStream_t s) {
   p.tmem_cols = h.tmem_cols;
   p.offsets = g.offsets; p.order = g.order;
   p.n_experts = g.n_experts; p.top_k = g.top_k;
+  p.per_tn = (uint32_t)((0xFFFFFFFFull + h.tn) / h.tn);
+  if (g.top_k > 1) p.per_k = (uint32_t)((0xFFFFFFFFull + g.top_k) / g.top_k);
   p.wait_ns = g.wait_ns;
   p.lost = (int)g.lost;
   const int64_t mats = EXPERTS ? g.n_experts : 1;
@@ -981,9 +1013,10 @@ gptq_status run(const Fp8LinearArgs &g, DevStatus *st, cudaStream_t s) {
   if (!tc::make_tmap_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, g.a_rows, g.K, g.lda, BK,
                         EXPERTS ? p.box : h.tn))
     return GPTQ_ERR_UNSUPPORTED;
-  const unsigned ctas = (unsigned)(h.one ? tiles * h.splits : (tiles < sms ? tiles : sms));
-  return h.one ? launch<TO, GATED, EXPERTS, true>(h, ctas, s, mw[0], mw[1], ma, p, st)
-               : launch<TO, GATED, EXPERTS, false>(h, ctas, s, mw[0], mw[1], ma, p, st);
+  return h.one ? launch<TO, GATED, EXPERTS, true>(h, dim3((unsigned)h.splits, (unsigned)p.n_w, (unsigned)along), s,
+                                                  mw[0], mw[1], ma, p, st)
+               : launch<TO, GATED, EXPERTS, false>(h, dim3((unsigned)(tiles < sms ? tiles : sms)), s, mw[0], mw[1],
+                                                   ma, p, st);
 }
 
 }  // namespace
