@@ -10,7 +10,7 @@
 // lowest index).  c is taken in fp32, and where two that decide something lie nearer to one
 // another than its error bound fp64 decides.  That is slow here (two operations a cycle and SM), so the
 // bound is tight, and of sigmoids only the few in question are taken again, one in a lane; a softmax's
-// need the sum too, and a sum of a group's the scores (about 10 us a token).  Without a bias the order of
+// need the sum, and so all (30 us for a token that meets it).  Without a bias the order of
 // the c is that of the logits, which are compared themselves.
 //
 // The sort is a count by expert and chunk of tokens, then for each chunk the sum of the counts before
@@ -98,13 +98,17 @@ __device__ __forceinline__ float logit(const RouteParams &p, int64_t at) {
   if (p.dtype == GPTQ_F16) return to_f32(((const __half *)p.logits)[at]);
   return to_f32(((const __nv_bfloat16 *)p.logits)[at]);
 }
+// A sigmoid's c in fp64.
+__device__ __forceinline__ double exact_c(const RouteParams &p, int64_t t, int id) {
+  return 1.0 / (1.0 + exp(-(double)logit(p, t * p.ld + id))) + (p.bias ? (double)p.bias[id] : 0.0);
+}
+
 // The order of a few experts whose c, of sigmoids, are too near to one another: the first n lanes' `id`.
 // In fp64, one in a lane.
 __device__ __forceinline__ int sort_near(const RouteParams &p, int64_t t, int lane, int id, int n) {
   uint64_t key = 0;
   if (lane < n) {
-    const double x = logit(p, t * p.ld + id);
-    key = to_key(1.0 / (1.0 + exp(-x)) + (p.bias ? (double)p.bias[id] : 0.0));
+    key = to_key(exact_c(p, t, id));
   }
   int rank = 0;
   for (int j = 0; j < n; ++j) {
@@ -121,8 +125,70 @@ __device__ __forceinline__ int sort_near(const RouteParams &p, int64_t t, int la
   return mine;
 }
 
-// A whole warp chooses token t's experts, c in type C; false where fp32 does not tell.
-template <typename C, int VPL>
+// The groups that are looked at, of sigmoids, by values in fp64 of the group_top + 1 largest c of each
+// (`score`: keys of this lane's c): one more than counts, and one in each of the group's lanes.  False
+// where the next one may belong to these too.
+template <int VPL>
+__device__ __forceinline__ bool exact_groups(uint32_t (&score)[VPL], const RouteParams &p, int64_t t, int lane, float tau,
+                                             uint32_t &open) {
+  const int base = lane / p.lanes * p.lanes, rank = lane - base, n = p.group_top + 1;
+  const uint32_t group = (p.lanes == 32 ? 0xffffffffu : (1u << p.lanes) - 1) << base;
+  int id[3] = {-1, -1, -1};
+  float first = 0.0f, last = 0.0f;   // the largest c, and the last that counts
+  bool told = true;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (r > n) break;
+    uint32_t mine = score[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) mine = max(mine, score[i]);
+    uint32_t best = mine;
+    for (int o = 1; o < p.lanes; o *= 2) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    const uint32_t who = __ballot_sync(0xffffffffu, best != 0 && mine == best) & group;
+    int at = 0;
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; --i) at = score[i] == best ? i : at;
+    const int found = __shfl_sync(0xffffffffu, lane * p.each + at, who ? __ffs(who) - 1 : lane);
+    if (who && lane == __ffs(who) - 1) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) score[i] = i == at ? 0 : score[i];
+    }
+    if (!who) continue;
+    const float c = of_key(best);
+    if (r == 0) first = c;
+    if (r == p.group_top - 1) last = c;
+    if (r < 3 && r < n) id[r] = found;
+    if (r == n) told = last - c > tau + 0x1p-23f * fmaxf(fabsf(first), fabsf(c));
+  }
+  if (!__all_sync(0xffffffffu, told)) return false;
+  uint64_t a = 0, b = 0;              // the two largest of the group
+  for (int r0 = 0; r0 < n; r0 += p.lanes) {
+    const int r = r0 + rank, mine = r == 0 ? id[0] : r == 1 ? id[1] : r == 2 && n > 2 ? id[2] : -1;
+    const uint64_t k = mine >= 0 ? to_key(exact_c(p, t, mine)) : 0;
+    b = max(b, min(a, k));
+    a = max(a, k);
+  }
+  for (int o = 1; o < p.lanes; o *= 2) {
+    const uint64_t oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
+    b = max(min(a, oa), max(b, ob));
+    a = max(a, oa);
+  }
+  uint64_t value = p.group_top > 1 && b ? to_key(of_key(a) + of_key(b)) : a;
+  if (rank != 0 || lane >= p.lanes * p.groups) value = 0;
+  open = 0;
+  for (int j = 0; j < p.top_groups; ++j) {
+    const uint64_t best = warp_max_key(value);
+    if (best == 0) break;
+    const int w = __ffs(__ballot_sync(0xffffffffu, value == best)) - 1;
+    open |= 1u << (w / p.lanes);
+    if (lane == w) value = 0;
+  }
+  return true;
+}
+
+// A whole warp chooses token t's experts, c in type C; false where fp32 does not tell.  EXACT: not for
+// groups of sigmoids that lie near to one another, which are then compared in fp64.
+template <typename C, int VPL, bool EXACT = false>
 __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams &p, int64_t t, int lane, Chosen &out) {
   using K = typename std::conditional<std::is_same<C, float>::value, uint32_t, uint64_t>::type;
   constexpr bool kSingle = std::is_same<C, float>::value;
@@ -214,6 +280,13 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
       if (lane == w) value = 0;
       last = best;
     }
+    if constexpr (EXACT)
+      if (!sure && p.sigmoid && p.lanes > 0) {
+        uint32_t score[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) score[i] = key_of(i);
+        sure = exact_groups(score, p, t, lane, tau, open);
+      }
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (!(open >> ((p.lanes > 0 ? lane / p.lanes : (e0 + i) / p.size) & 31) & 1)) key[i] = 0;
@@ -296,7 +369,7 @@ __device__ __forceinline__ int route_token(const RouteParams &p, int64_t t, int 
   float x[VPL];
   load_logits(x, p, t, lane);
   Chosen ch;
-  if (!choose<float, VPL>(x, p, t, lane, ch)) {
+  if (!choose<float, VPL, AGAIN>(x, p, t, lane, ch)) {
     if constexpr (!AGAIN) return -2;
     const float sum = ch.sum;
     choose<double, VPL>(x, p, t, lane, ch);

@@ -287,6 +287,22 @@ def test_route_where_fp32_does_not_tell(scores):
     _check_route(y, 8, torch.zeros(64), scores="sigmoid")
 
 
+@pytest.mark.parametrize("experts,groups", [(64, 8), (32, 8), (256, 8), (16, 8), (128, 32), (45, 5), (64, 2), (300, 4)])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_route_between_groups_that_are_equal_or_nearly(experts, groups, scores, group_top):
+    # every group has the same logits in an order of its own; the bias tells them apart by 1e-9, or not at all
+    rng = np.random.default_rng(experts + groups)
+    size = experts // groups
+    x = np.stack([np.concatenate([rng.permutation(v) for _ in range(groups)]) for v in rng.standard_normal((60, size))])
+    logits = torch.from_numpy(x.astype(np.float32))
+    kw = dict(scores=scores, groups=groups, top_groups=max(1, groups // 2), group_top=min(group_top, size))
+    top_k = min(4, size * kw["top_groups"])
+    _check_route(logits, top_k, **kw)
+    _check_route(logits, top_k, torch.zeros(experts), **kw)
+    _check_route(logits, top_k, torch.from_numpy((1e-9 * rng.standard_normal(experts)).astype(np.float32)), **kw)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("kw", [dict(), dict(scores="sigmoid"), dict(groups=4, top_groups=2, group_top=2), dict(renormalize=False)])
 def test_route_masks(dtype, kw):
