@@ -904,9 +904,9 @@ int clusters_at_once(int dev, int splits, int per_sm, int sms) {
   }, per_sm * sms / splits * 7 / 8);
 }
 
-// The cut with the least of an estimate in SM cycles, as for the plain product: a k-block of a tile takes
-// the MMAs' time or that of their issue, the memory brings each operand once at 3500 bytes a cycle, L2
-// what the tiles fill again; a launch costs 6400, sums that meet 1400 + 8 a token.  Of experts the number
+// The cut with the least of an estimate in SM cycles: a k-block of a tile takes the MMAs' time, that of
+// their issue, or that of its operands' way from L2 (61 bytes a cycle and SM, as measured); the memory brings
+// each operand once at 3500 bytes a cycle; a launch costs 6400, sums that meet 1400 + 8 a token.  Of experts the number
 // of tiles is not known here: as many as if the rows were dealt evenly, or what there can be at most where
 // each cluster has one.
 template <typename TO, bool GATED, bool EXPERTS>
@@ -925,9 +925,8 @@ Shape choose(const Fp8LinearArgs &g, int dev, int sms) {
     const double per = EXPERTS ? rows / tn + 0.5 : (double)ceil_div(g.M, (int64_t)tn);   // tiles along the tokens
     const double tiles = n_w * used * (per < 1.0 ? 1.0 : per);
     const int64_t at_most = n_w * (EXPERTS ? (g.n_experts < g.M ? g.n_experts : g.M) + g.M / tn : ceil_div(g.M, (int64_t)tn));
-    const double mma = W * 3.45 * tn, issue = 300 + W * 1.7 * tn;
-    const double c = mma > issue ? mma : issue;
-    const double fill = tiles * g.K * (W * BM + tn) / 20000.0;
+    const double mma = W * 3.45 * tn, issue = 300 + W * 1.7 * tn, feed = (W * BM + tn) * BK / 61.0;
+    const double c = fmax(fmax(mma, issue), feed);
     for (int s = 1; s <= 8 && s <= groups; ++s) {   // 1: from tile to tile
       if (s > 1 && at_most * s > 2 * sms) break;
       Shape h{tn, s, 1, s > 1};
@@ -946,7 +945,7 @@ Shape choose(const Fp8LinearArgs &g, int dev, int sms) {
       }
       const double busy = ceil(tiles * h.splits / sms);
       const double work = busy * 4 * ceil_div(groups, (int64_t)h.splits) * c;
-      double t = sqrt(work * work + (once + fill) * (once + fill));
+      double t = sqrt(work * work + once * once);
       t += 6400.0 + (h.one ? 1400.0 + 8.0 * W * tn : 0.0) + (h.one ? 0.0 : 800.0 * (busy - 1));
       if (t < best_t) best_t = t, best = h;
     }
