@@ -10,6 +10,7 @@
 //   warps 2..9 : epilogue, two warps for each 32 weight rows, which take tokens in turn
 //   warp 10    : scales
 //   11..18     : copy token rows (the experts' gated product)
+// (clusters that share a tile in the experts' gated product: 4 warps of epilogue, 4 that copy)
 //
 // Gated: a tile has 128 rows of both weights and two accumulators, so the 128 outputs that share an
 // exponent are one column of the tile.  A warp turns 32 rows by 16 tokens around in shared memory, so
@@ -18,15 +19,23 @@
 // Experts: a tile is (expert, up to tn of its positions, 128 weight rows).  Each CTA counts the
 // tiles from the offsets by itself.  The gated product takes its token rows by index, the other takes
 // them as they lie and stores each where the order says, so that neither the rows nor the results
-// are moved by a kernel of their own.  Rows by index are copied by four warps, 16 bytes a
-// lane, into the swizzle that the MMA reads: TMA's gather of four
-// rows takes about 80 cycles, 2300 for a k-block whose MMAs take 770 (4096 tokens of 64 experts, 4096
-// x 1376: 709 us).
+// are moved by a kernel of their own.  Rows by index are copied by eight warps, 16 bytes a lane, into the
+// swizzle that the MMA reads: TMA's gather of four rows takes about 80 cycles, 2300 for a k-block whose
+// MMAs take 770 (4096 tokens of 64 experts, 4096 x 1376: 709 us then).
 //
 // 16-bit outputs are turned around likewise, so that a store writes 64 contiguous bytes of four tokens.
 //
 // Few tokens leave few tiles; each cluster of up to 8 CTAs then has one, whose k-blocks they share, and
 // their partial sums meet through distributed shared memory in rank order.
+//
+// Bounds, and what it measured (GPU time, tokens x n x k).  Few tokens: the weights' bytes, at 5.3 to
+// 6.4 TB/s once under way, and 3.5 to 6 us for a CTA's set-up, the first copies and the end: linear 1 x
+// 4096 x 11008 10.5 us (6.7 of them the bytes), gated 24 x 11008 x 4096 17.8 (13.6), experts gated 1
+// token of 6 of 64 x 1376 x 4096 16.8 (10.1), experts out 40 tokens x 4096 x 1376 52.8, 6.8 TB/s.  Many:
+// the tensor pipe, or operands from L2 at 61 bytes a cycle and SM: gated 4096 x 11008 x 4096 238 us, 3.1
+// PFLOP/s, the pipe busy 68 % of the time (266 us in a row of calls that the power limit holds back);
+// experts gated 4096 tokens of 6 of 64 x 1376 x 4096 237 us, 2.3 PFLOP/s; linear 8192 x 11008 x 4096
+// with a residual 266 us, 2.8 PFLOP/s.
 #include <cudaTypedefs.h>
 #include <math.h>
 
