@@ -587,8 +587,8 @@ gptq_status gptq_kv8_attention(const void *q, const int64_t *q_strides, int dtyp
 /*
  * gptq_serving_status: synchronize `stream`, then return GPTQ_ERR_TIMEOUT if a bounded device wait
  * of a gptq_fp8_matmul, gptq_kv8_attention or one of the products of feed-forward blocks on the
- * current device, on whichever stream and workspace, has given up since the last such query (the outputs of that call are undefined), else
- * GPTQ_OK.  It is recorded beside the workspaces' status, which the next call on a workspace resets:
+ * current device, on whichever stream and workspace, has given up since the last such query (the
+ * outputs of that call are undefined), else GPTQ_OK.  It is recorded beside the workspaces' status, which the next call on a workspace resets:
  * a program that runs many calls asks once, after them.  (In a stream that is captured: CUDA.)
  * Errors of its own: CUDA.
  */

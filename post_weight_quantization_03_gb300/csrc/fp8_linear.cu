@@ -244,7 +244,6 @@ __device__ __forceinline__ void make_plan(const Params &p, const Plan &plan, int
   }
 }
 
-// TO: type of the output, if it is not gated.
 // Shared memory of the epilogue that goes from tile to tile.
 __host__ __device__ constexpr size_t direct_bytes(int epilogue) {
   return 2 * 256 * 4 + epilogue * 16 * kTurnPitch * 4 + 2 * 2 * 4 * 16 * 4;
@@ -260,7 +259,7 @@ struct Warps {
 // ONE: each cluster has one tile, whose k-blocks its CTAs share; their sums lie in shared memory, where
 // a warp of one of them adds up and finishes a token's.  Two such CTAs can be on an SM, of one call or of two in a row,
 // so that one sets itself up while the other ends.  Else a CTA goes from tile to tile, with a set of
-// accumulators for the MMAs and one for the epilogue.
+// accumulators for the MMAs and one for the epilogue.  TO: type of the output, if it is not gated.
 template <typename TO, bool GATED, bool EXPERTS, bool ONE>
 __global__ void __launch_bounds__(32 * Warps<GATED, EXPERTS, ONE>::kAll, ONE ? 2 : 1)
 linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ CUtensorMap mw1,
@@ -702,9 +701,9 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
         for (int c = 32 * half; c < tile.cols; c += 64) {
           uint32_t r[W][32];
           tc::tmem_ld32(acc + (uint32_t)c, r[0]);
-        float v[32];
-        const int left = tile.cols - c;                      // tokens of this chunk, if below 32
-        const float4 *ra4 = reinterpret_cast<const float4 *>(sra + c);
+          float v[32];
+          const int left = tile.cols - c;                    // tokens of this chunk, if below 32
+          const float4 *ra4 = reinterpret_cast<const float4 *>(sra + c);
           tc::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {

@@ -191,8 +191,9 @@ __device__ __forceinline__ bool exact_groups(uint32_t (&score)[VPL], const Route
   return true;
 }
 
-// A whole warp chooses token t's experts from its logits x (-inf: not to be chosen), c in type C; false where fp32 does not tell.  EXACT: not for
-// groups of sigmoids that lie near to one another, which are then compared in fp64.
+// A whole warp chooses token t's experts from its logits x (-inf: not to be chosen), c in type C; false
+// where fp32 does not tell.  EXACT: not for groups of sigmoids that lie near to one another, which are
+// then compared in fp64.
 template <typename C, int VPL, bool EXACT = false>
 __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams &p, int64_t t, int lane, Chosen &out) {
   using K = typename std::conditional<std::is_same<C, float>::value, uint32_t, uint64_t>::type;
@@ -233,8 +234,9 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
       c[i] = x[i] > -INFINITY && fp8::finite(b) ? s + (C)b : -(C)INFINITY;
     }
   }
+  // (sums of biases may overflow in fp32; their difference is then infinite or NaN, and the bound infinite)
   auto near = [&](C hi, C lo, float of) {
-    return kSingle && (float)(hi - lo) <= of * (tau + 0x1p-23f * fmaxf(fabsf((float)hi), fabsf((float)lo)));
+    return kSingle && !((float)(hi - lo) > of * (tau + 0x1p-23f * fmaxf(fabsf((float)hi), fabsf((float)lo))));
   };
   K key[VPL];
 #pragma unroll

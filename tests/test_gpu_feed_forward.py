@@ -326,6 +326,22 @@ def test_route_masks(dtype, kw):
         _check_route(torch.where(torch.isfinite(logits), logits * 0 - 90 - 3 * _randn(8, 80, 24).to(DT[dtype]), logits), 4, **kw)
 
 
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts", [24, 60, 256])
+def test_route_by_biases_of_any_size(scores, experts):
+    """Biases up to the largest numbers of the type, whose sums in a group pass them; masks by its lowest."""
+    logits = _randn(11, 40, experts)
+    big = torch.finfo(torch.float32).max
+    rng = np.random.default_rng(experts)
+    for values in ([-big, 0.0, 0.1], [-big, -0.9 * big, -0.7 * big, -0.8 * big], [big, 0.9 * big, 0.7 * big, 0.8 * big], [-big, big], [-big],
+                   [1e30, 1.1e30, -1e30], [1e-40, -1e-40, 0.0]):
+        bias = torch.from_numpy(rng.choice(np.array(values, np.float32), experts))
+        _check_route(logits, 3, bias, scores=scores)
+        for groups, top in ((4, 2), (12 if experts < 256 else 32, 3)):
+            for group_top in (1, 2):
+                _check_route(logits, 3, bias, scores=scores, groups=groups, top_groups=top, group_top=group_top)
+
+
 def test_route_of_a_view_and_on_another_stream():
     logits = _randn(9, 100, 70)
     wide = torch.full((100, 90), math.nan, device=DEV)
@@ -374,6 +390,22 @@ def test_experts_gated(tokens, experts, top_k, n, k, kind):
             t = order[lo:hi] // top_k
             want, tol = _want_gated(a[t], ae[t], gate[e], up[e], ra[t], "silu", k)
             _check_codes(codes[lo:hi], exps[lo:hi], want, tol)
+
+
+def test_experts_of_every_second_matrix():
+    n, k, tokens = 130, 300, 40
+    ws = [_weights(10 + i, n, k, bias=True) for i in range(8)]
+    stack = _experts_on_dev(ws)
+    some = (stack[0][1::2], stack[1][1::2], stack[2][1::2].contiguous(), stack[3][1::2].contiguous())
+    alone = _experts_on_dev(ws[1::2])
+    _, offsets, order = _routes(1, tokens, 4, 2)
+    a, ae = _fp8_matrix(2, tokens, k, 1, 0.5)
+    args = (_dev(offsets), _dev(order))
+    got = gptq.fp8_experts_gated(_dev_codes(a), _dev_exps(ae), some, some, *args, 2)
+    want = gptq.fp8_experts_gated(_dev_codes(a), _dev_exps(ae), alone, alone, *args, 2)
+    assert np.array_equal(_np(got[0]), _np(want[0])) and np.array_equal(_np(got[1]), _np(want[1]))
+    rows = (_dev_codes(np.repeat(a, 2, 0)), _dev_exps(np.repeat(ae, 2, 0)))
+    assert torch.equal(gptq.fp8_experts(*rows, *some[:2], *args, some[2], some[3]), gptq.fp8_experts(*rows, *alone[:2], *args, alone[2], alone[3]))
 
 
 @pytest.mark.parametrize("tokens", [15, 16, 17, 31, 48, 65, 80, 96, 97, 104, 111, 112, 113, 150, 220, 224, 240, 241, 330, 336, 448, 670, 1000])

@@ -13,8 +13,9 @@ import torch
 from oracle import serving_oracle as SO
 from post_weight_quantization_03_gb300 import build_lib, decoder, gptq
 from tests.test_gpu_canaries import PAT, Guarded
-from tests.test_gpu_feed_forward import _dev, _experts_on_dev, _on_dev, _routes, _weights
-from tests.test_gpu_serving import DEV, DT, _dev_codes, _dev_exps, _fp8_matrix, _randn
+from tests.test_gpu_feed_forward import (_check16, _check_codes, _dev, _experts_on_dev, _on_dev, _routes, _want_gated, _want_linear,
+                                         _weights)
+from tests.test_gpu_serving import DEV, DT, _dev_codes, _dev_exps, _fp8_matrix, _np, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -92,6 +93,110 @@ def test_blocks_on_two_streams_at_once():
     torch.cuda.synchronize()
     for outs, w in zip(got, want):
         assert all(torch.equal(o, w) for o in outs)
+    gptq.serving_status()
+
+
+class _Few:
+    """Products of a few tokens, whose tiles are shared by clusters of CTAs."""
+
+    def __init__(self, seed, m, n, k, experts):
+        a, ae = _fp8_matrix(seed, m, k, 1, 0.5)
+        self.a = _dev_codes(a), _dev_exps(ae)
+        self.w = _on_dev(_weights(seed + 1, n, k))
+        self.r = _randn(seed + 2, m, n, dtype="bf16").to(DEV)
+        _, offsets, order = _routes(seed, m, experts, 2)
+        self.plan = _dev(offsets), _dev(order)
+        self.ew = _experts_on_dev([_weights(seed + 3 + i, n, k) for i in range(experts)])
+        self.rows = _dev_codes(np.repeat(a, 2, 0)), _dev_exps(np.repeat(ae, 2, 0))
+
+    def __call__(self, stream=None):
+        kw = dict(stream=stream)
+        return [_u8(t) for t in (
+            gptq.fp8_linear(*self.a, *self.w[:2], w_scale=self.w[2], residual=self.r, **kw),
+            gptq.fp8_matmul(*self.a, *self.w[:2], w_scale=self.w[2], **kw),
+            *gptq.fp8_gated(*self.a, self.w, self.w, **kw),
+            *gptq.fp8_experts_gated(*self.a, self.ew, self.ew, *self.plan, 2, **kw),
+            gptq.fp8_experts(*self.rows, *self.ew[:2], *self.plan, self.ew[2], **kw))]
+
+
+def test_products_of_few_tokens_on_three_streams_at_once():
+    sets = [_Few(1, 1, 512, 4096, 4), _Few(20, 8, 640, 2048, 8), _Few(40, 3, 130, 8192, 3)]
+    want = [[t.clone() for t in s()] for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(60):
+        got.append((i % 3, sets[i % 3](streams[i % 3])))
+    torch.cuda.synchronize()
+    for i, outs in got:
+        assert all(torch.equal(o, w) for o, w in zip(outs, want[i]))
+    gptq.serving_status()
+
+
+def test_two_graphs_replayed_at_once():
+    sets = [_Few(1, 1, 512, 4096, 4), _Few(20, 8, 640, 2048, 8)]
+    blocks = [_Block(1, 40, 8, 2, 256, 200), _Block(7, 333, 16, 4, 384, 130)]
+    want = [[t.clone() for t in s()] + [b().clone()] for s, b in zip(sets, blocks)]
+    graphs, outs = [], []
+    for s, b in zip(sets, blocks):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(s() + [b()])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(x, y) for x, y in zip(o, w))
+    gptq.serving_status()
+
+
+def test_offsets_that_pass_32_bits():
+    """Outputs, token rows and experts' weights of more than 2^31 bytes: what lies past them is right."""
+    n, k, m = 4112, 32, 540_000
+    w = _on_dev(_weights(3, n, k))
+    a, ae = _fp8_matrix(1, 64, k, 1, 0.5)
+    last = _dev_codes(a), _dev_exps(ae)
+    codes, exps = torch.zeros(m, k, dtype=torch.uint8, device=DEV), torch.full((m, 4), 127, dtype=torch.uint8, device=DEV)
+    codes[-64:], exps[-64:, :1] = _u8(last[0]), last[1]
+    many = codes.view(torch.float8_e4m3fn), exps[:, :1]
+    # (K is one block: the sums of few rows and of many are the same numbers)
+    small = gptq.fp8_linear(*last, *w[:2], w_scale=w[2])
+    out = gptq.fp8_linear(*many, *w[:2], w_scale=w[2])
+    assert torch.equal(out[-64:], small) and not out[:1000].any()
+    gptq.fp8_linear(*many, *w[:2], w_scale=w[2], residual=out, out=out)
+    small = gptq.fp8_linear(*last, *w[:2], w_scale=w[2], residual=small)
+    assert torch.equal(out[-64:], small)
+    gptq.moe_combine(out, torch.ones(m, 1, device=DEV), out, out=out)
+    assert torch.equal(out[-64:], 2 * small) and not out[:1000].any()
+    del out
+    c, e = gptq.fp8_gated(*many, w, w)
+    c2, e2 = gptq.fp8_gated(*last, w, w)
+    assert torch.equal(_u8(c[-64:]), _u8(c2)) and torch.equal(e[-64:], e2)
+    # the last of those rows by index
+    ws = [_weights(30 + i, 130, n) for i in range(2)]
+    order = torch.full((m,), -1, dtype=torch.int32, device=DEV)
+    order[:64] = torch.arange(m - 1, m - 65, -1)
+    got = gptq.fp8_experts_gated(c, e, _experts_on_dev(ws), _experts_on_dev(ws), _dev(np.array([0, 40, 64], np.int32)), order, 1)
+    rows, rows_e = _np(c2)[::-1], _np(e2)[::-1]
+    for i, at in ((0, slice(0, 40)), (1, slice(40, 64))):
+        _check_codes(got[0][at], got[1][at], *_want_gated(rows[at], rows_e[at], ws[i], ws[i], None, "silu", n))
+    del c, e, got, codes, exps, many
+    # the last of 700 matrices of 2048 x 2048 bytes
+    experts, d = 700, 2048
+    stack = torch.zeros(experts, d, d, dtype=torch.uint8, device=DEV)
+    stack_e = torch.full((experts, 16, 16), 127, dtype=torch.uint8, device=DEV)
+    hw = _weights(5, d, d, scale=False)
+    stack[-1], stack_e[-1] = _u8(_dev_codes(hw[0])), _dev_exps(hw[1])
+    a, ae = _fp8_matrix(9, 20, d, 1, 0.5)
+    offsets = np.zeros(experts + 1, np.int32)
+    offsets[-1] = 20
+    y = gptq.fp8_experts(_dev_codes(a), _dev_exps(ae), stack.view(torch.float8_e4m3fn), stack_e, _dev(offsets), _dev(np.arange(20, dtype=np.int32)))
+    _check16(y, *_want_linear(a, ae, hw, None, None, None, d))
     gptq.serving_status()
 
 
