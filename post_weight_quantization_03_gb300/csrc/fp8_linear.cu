@@ -32,8 +32,8 @@
 // 6.4 TB/s once under way, and 3.5 to 6 us for a CTA's set-up, the first copies and the end: linear 1 x
 // 4096 x 11008 10.5 us (6.7 of them the bytes), gated 24 x 11008 x 4096 17.8 (13.6), experts gated 1
 // token of 6 of 64 x 1376 x 4096 16.8 (10.1), experts out 40 tokens x 4096 x 1376 52.8, 6.8 TB/s.  Many:
-// the tensor pipe, or operands from L2 at 61 bytes a cycle and SM: gated 4096 x 11008 x 4096 238 us, 3.1
-// PFLOP/s, the pipe busy 68 % of the time (266 us in a row of calls that the power limit holds back);
+// the tensor pipe at the clock that the power limit leaves: gated 4096 x 11008 x 4096 238 us, 3.1 PFLOP/s
+// (266 in a longer row of calls; a third fewer bytes from L2 changed 1 %);
 // experts gated 4096 tokens of 6 of 64 x 1376 x 4096 237 us, 2.3 PFLOP/s; linear 8192 x 11008 x 4096
 // 236 us, 3.1 PFLOP/s, with a residual 252.
 #include <cudaTypedefs.h>
