@@ -1052,7 +1052,8 @@ def fp8_linear(a, a_exps, w, w_exps, a_scale=None, w_scale=None, bias=None, act=
 def fp8_gated(a, a_exps, gate, up, a_scale=None, act="silu", ws=None, stream=None):
     """``(codes, exps)``, by 1 x 128 blocks, of ``act(G) * U``: G and U are the products of ``A [m, k]``
     with the weights ``gate`` and ``up``, each ``(codes [n, k], exps[, scale[, bias]])``, as
-    ``fp8_linear`` takes them.  What ``fp8_matmul`` or ``fp8_linear`` take as activations."""
+    ``fp8_linear`` takes them.  What ``fp8_matmul`` or ``fp8_linear`` take as activations (tensors of
+    one storage)."""
     return (_MARSHAL or _marshal()).fp8_gated(a, a_exps, gate, up, a_scale, act, ws, stream)
 
 
@@ -1068,7 +1069,7 @@ def moe_route(logits, top_k, bias=None, scores="softmax", groups=1, top_groups=N
     ``scale``.  ``order [tokens * top_k]`` lists the assignments ``token * top_k + place`` by expert,
     expert e's from ``offsets[e]`` on: what ``fp8_experts_gated`` and ``fp8_experts`` take.
     Experts whose logit or bias is not finite are never chosen (ids of -1, weights of 0 where too few
-    are left)."""
+    are left).  The four are tensors of one storage."""
     if scores not in SCORES:
         raise ValueError(f"scores must be one of {list(SCORES)}")
     if groups == 1:

@@ -200,6 +200,24 @@ def test_offsets_that_pass_32_bits():
     gptq.serving_status()
 
 
+@pytest.mark.parametrize("tokens,experts", [(0, 8), (1, 7), (33, 300)])
+@pytest.mark.parametrize("inference", [False, True])
+def test_outputs_of_a_call_do_not_share_memory(tokens, experts, inference):
+    logits = _randn(1, tokens, experts).to(DEV)
+    a, ae = _fp8_matrix(2, max(tokens, 1), 300, 1, 0.5)
+    w = _on_dev(_weights(3, 130, 300))
+    with torch.inference_mode(inference):
+        outs = [*gptq.moe_route(logits, 3), *gptq.fp8_gated(_dev_codes(a)[:tokens], _dev_exps(ae)[:tokens], w, w)]
+        want = [t.clone() for t in outs]
+        for i, t in enumerate(outs):
+            _u8(t).fill_(0x11)
+            assert all(torch.equal(_u8(x), _u8(y)) for x, y in zip(outs[i + 1:], want[i + 1:]))
+        assert [t.is_inference() for t in outs] == [inference] * 6 and not any(t.requires_grad for t in outs)
+    assert all((_u8(t) == 0x11).all() for t in outs)
+    assert [t.dtype for t in outs] == [torch.int32, torch.float32, torch.int32, torch.int32, torch.float8_e4m3fn, torch.uint8]
+    assert [tuple(t.shape) for t in outs] == [(tokens, 3), (tokens, 3), (experts + 1,), (3 * tokens,), (tokens, 130), (tokens, 2)]
+
+
 def test_calls_repeat():
     a, ae = _fp8_matrix(3, 500, 512, 1, 0.5)
     w = [_weights(10 + i, 384, 512) for i in range(8)]
