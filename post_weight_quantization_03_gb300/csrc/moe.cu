@@ -47,7 +47,8 @@ struct RouteParams {
   int size;                           // experts of a group
   int each;                           // experts of a lane
   int whole;                          // all lanes have VPL, in rows of 16-byte alignment
-  int lanes;                          // lanes of a group; 0: groups do not begin at lanes
+  int bias_whole;                     // so does the bias
+  int lanes, shift;                   // lanes of a group, 1 << shift; 0: groups do not begin at lanes
   float scale;
   int32_t *ids; float *weights; int32_t *offsets, *order;
   uint32_t *counts;                   // [chunks, pairs]: of two neighbouring experts, 16 bits each (a
@@ -136,7 +137,7 @@ __device__ __forceinline__ int sort_near(const RouteParams &p, int64_t t, int la
 template <int VPL>
 __device__ __forceinline__ bool exact_groups(uint32_t (&score)[VPL], const RouteParams &p, int64_t t, int lane, float tau,
                                              uint32_t &open) {
-  const int base = lane / p.lanes * p.lanes, rank = lane - base, n = p.group_top + 1;
+  const int rank = lane & (p.lanes - 1), base = lane - rank, n = p.group_top + 1;
   const uint32_t group = (p.lanes == 32 ? 0xffffffffu : (1u << p.lanes) - 1) << base;
   int id[3] = {-1, -1, -1};
   float first = 0.0f, last = 0.0f;   // the largest c, and the last that counts
@@ -185,7 +186,7 @@ __device__ __forceinline__ bool exact_groups(uint32_t (&score)[VPL], const Route
     const uint64_t best = warp_max_key(value);
     if (best == 0) break;
     const int w = __ffs(__ballot_sync(0xffffffffu, value == best)) - 1;
-    open |= 1u << (w / p.lanes);
+    open |= 1u << (w >> p.shift);
     if (lane == w) value = 0;
   }
   return true;
@@ -225,13 +226,25 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
   const float tau = p.sigmoid ? 4 * 0x1p-23f : (VPL + 15) * 0x1p-23f / (float)sum;
   if (scored) {
     const C inv = (C)1 / sum;
+    float bias[VPL] = {};
+    if (p.bias) {
+      if (VPL % 4 == 0 && p.bias_whole) {
+#pragma unroll
+        for (int i = 0; i < VPL; i += 4) {
+          const float4 b = *reinterpret_cast<const float4 *>(p.bias + e0 + i);
+          bias[i] = b.x, bias[i + 1] = b.y, bias[i + 2] = b.z, bias[i + 3] = b.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) bias[i] = e0 + i < p.n_experts && i < p.each ? p.bias[e0 + i] : 0.0f;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       C s;
       if constexpr (kSingle) s = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-x[i])) : c[i] * inv;
       else s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)x[i])) : c[i] / sum;
-      const float b = p.bias && e0 + i < p.n_experts && i < p.each ? p.bias[e0 + i] : 0.0f;
-      c[i] = x[i] > -INFINITY && fp8::finite(b) ? s + (C)b : -(C)INFINITY;
+      c[i] = x[i] > -INFINITY && fp8::finite(bias[i]) ? s + (C)bias[i] : -(C)INFINITY;
     }
   }
   // (sums of biases may overflow in fp32; their difference is then infinite or NaN, and the bound infinite)
@@ -261,7 +274,7 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
       for (int i = 0; i < VPL; ++i) join(a, b, key_of(i), 0);
       for (int o = 1; o < p.lanes; o *= 2) join(a, b, __shfl_xor_sync(0xffffffffu, a, o), __shfl_xor_sync(0xffffffffu, b, o));
       value = value_of(a, b);
-      if (lane % p.lanes != 0 || lane >= p.lanes * p.groups) value = 0;
+      if ((lane & (p.lanes - 1)) != 0 || lane >= p.lanes * p.groups) value = 0;
     } else {
       for (int g = 0; g < p.groups; ++g) {
         K a = 0, b = 0;
@@ -283,7 +296,7 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
         break;
       }
       const int w = __ffs(__ballot_sync(0xffffffffu, value == best)) - 1;
-      open |= 1u << (p.lanes > 0 ? w / p.lanes : w);
+      open |= 1u << (p.lanes > 0 ? w >> p.shift : w);
       if (lane == w) value = 0;
       last = best;
     }
@@ -294,9 +307,15 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
         for (int i = 0; i < VPL; ++i) score[i] = key_of(i);
         sure = exact_groups(score, p, t, lane, tau, open);
       }
+    if (p.lanes > 0) {
+      const bool in = open >> (lane >> p.shift) & 1;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (!(open >> ((p.lanes > 0 ? lane / p.lanes : (e0 + i) / p.size) & 31) & 1)) key[i] = 0;
+      for (int i = 0; i < VPL; ++i) key[i] = in ? key[i] : 0;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (!(open >> ((e0 + i) / p.size & 31) & 1)) key[i] = 0;
+    }
   }
   out.id = -1;
   if (!sure) return false;
@@ -644,8 +663,10 @@ gptq_status launch_moe_route(const MoeRouteArgs &g, void *ws, cudaStream_t s) {
   p.each = (g.n_experts + 31) / 32;
   p.whole = p.each % kVec == 0 && (p.each & (p.each - 1)) == 0 && 32 * p.each == g.n_experts &&
             fp8::alignment(g.logits, g.ld * (g.dtype == GPTQ_F32 ? 4 : 2)) == 16;
+  p.bias_whole = p.whole && fp8::alignment(g.bias, 0) == 16;
   // groups of whole lanes whose number is a power of two are joined by exchanges within them
   if (p.size % p.each == 0 && (p.size / p.each & (p.size / p.each - 1)) == 0) p.lanes = p.size / p.each;
+  while (1 << p.shift < p.lanes) ++p.shift;
   const int threads = route_threads(g.n_tokens, g.n_experts);
   p.chunk = g.n_tokens <= kOneTokens && g.n_experts <= 256 ? kOneTokens : chunk_tokens(g.n_tokens, threads);
   p.chunks = (int)ceil_div(g.n_tokens, p.chunk);
