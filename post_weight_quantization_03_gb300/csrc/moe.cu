@@ -18,9 +18,9 @@
 // expert's word of tokens, so that the result does not depend on how the GPU schedules it.  Two
 // launches, or one for up to 32 tokens.
 //
-// Measured (GPU time): 1 token of 64 experts 4.1 us and 333 of 160 9.8, launches and latencies; 8192 of
-// 256 18 us by logits and 30 by sigmoids with a bias and groups, by issue slots (1000 and 1900
-// instructions a token, of which 450 are the eight rounds; one launch for the tokens, 7 us for the order).
+// Measured (GPU time): 1 token of 64 experts 4.2 us and 333 of 160 8.1, launches and latencies; 8192 of
+// 256 16 us by logits and 23 by sigmoids with a bias and groups, by issue slots (1000 and 1630
+// instructions a token, of which 450 are the eight rounds) and the order's latencies (5 us).
 //
 // Combine: HBM-bound, one pass: 4096 x 8 rows of 4096 48 us, 6.9 TB/s; one token 1.8 us.
 #include <type_traits>
@@ -431,13 +431,16 @@ struct PlanSmem {
   int warp[32];
 };
 
-// The words of the assignments [i0, i1), which belong to the 64 tokens from t0 on.
-__device__ __forceinline__ void fill_words(const RouteParams &p, const int *ids, int i0, int i1, int t0, PlanSmem &sm) {
-  for (int e = threadIdx.x; e < p.n_experts; e += kPlanThreads) sm.word[0][e] = sm.word[1][e] = 0;
+// The words of the assignments [i0, i1), which belong to the 64 tokens from t0 on; e: the expert of this
+// thread's first.
+__device__ __forceinline__ void fill_words(const RouteParams &p, const int *ids, int i0, int i1, int t0, int e, PlanSmem &sm) {
+  for (int x = threadIdx.x; x < p.n_experts; x += kPlanThreads) sm.word[0][x] = sm.word[1][x] = 0;
   __syncthreads();
-  for (int i = i0 + threadIdx.x; i < i1; i += kPlanThreads) {
-    const int e = ids[i], t = i / p.top_k - t0;
+  for (int i = i0 + threadIdx.x; i < i1;) {
+    const int t = i / p.top_k - t0;
     if (e >= 0) atomicOr(&sm.word[t >> 5][e], 1u << (t & 31));
+    i += kPlanThreads;
+    e = i < i1 ? ids[i] : -1;
   }
   __syncthreads();
 }
@@ -445,27 +448,45 @@ __device__ __forceinline__ void fill_words(const RouteParams &p, const int *ids,
 __device__ __forceinline__ void plan(const RouteParams &p, int mine, const int *ids, PlanSmem &sm) {
   const int tid = threadIdx.x, lane = tid % 32;
   const int t0 = mine * p.chunk, t1 = min(t0 + p.chunk, (int)p.n_tokens);
+  auto expert_of = [&](int i, int end) { return i < end ? ids[i] : -1; };
+  // (asked for before the counts, all of which are asked for at once as far as they are a few: either
+  // takes 0.5 us to come)
+  const int end0 = min(t0 + kWord, t1) * p.top_k, e0 = expert_of(t0 * p.top_k + tid, end0);
   // an expert's assignments in all chunks, and in those before this one
   int span = 32;              // threads of a part: each has two experts, and every parts-th chunk
   while (span < p.pairs) span *= 2;
   const int parts = kPlanThreads / span, part = tid / span, e2 = tid % span;
   int all[2] = {0, 0}, pre[2] = {0, 0};
   if (p.chunks > 1 && e2 < p.pairs) {
-#pragma unroll 16
-    for (int c = part; c < p.chunks; c += parts) {
-      const uint32_t two = p.counts[(int64_t)c * p.pairs + e2];
-      all[0] += two & 0xffffu;
-      all[1] += two >> 16;
-      pre[0] += c < mine ? two & 0xffffu : 0;
-      pre[1] += c < mine ? two >> 16 : 0;
-    }
+    auto add_up = [&](auto batch) {
+      constexpr int n = decltype(batch)::value;
+      for (int c0 = part; c0 < p.chunks; c0 += n * parts) {
+        const uint32_t *from = p.counts + c0 * p.pairs + e2;
+        const int step = parts * p.pairs;
+        uint32_t two[n];
+#pragma unroll
+        for (int i = 0; i < n; ++i) two[i] = c0 + i * parts < p.chunks ? from[i * step] : 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          const uint32_t before = c0 + i * parts < mine ? two[i] : 0;
+          all[0] += two[i] & 0xffffu;
+          all[1] += two[i] >> 16;
+          pre[0] += before & 0xffffu;
+          pre[1] += before >> 16;
+        }
+      }
+    };
+    // (152 chunks by the 8 parts of 256 experts are 19; batches of 20 cost 1 us more where there are 3)
+    if (p.chunks <= 4 * parts) add_up(std::integral_constant<int, 4>());
+    else if (p.chunks <= 8 * parts) add_up(std::integral_constant<int, 8>());
+    else add_up(std::integral_constant<int, 20>());
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     sm.part[h][tid] = all[h];
     sm.part[2 + h][tid] = pre[h];
   }
-  fill_words(p, ids, t0 * p.top_k, min(t0 + kWord, t1) * p.top_k, t0, sm);   // (and waits for all)
+  fill_words(p, ids, t0 * p.top_k, end0, t0, e0, sm);   // (and waits for all)
   int sum = 0, before = 0;
   if (tid < p.n_experts) {
     if (p.chunks == 1) {
@@ -501,7 +522,7 @@ __device__ __forceinline__ void plan(const RouteParams &p, int mine, const int *
   __syncthreads();
   for (int w0 = t0; w0 < t1; w0 += kWord) {
     const int i0 = w0 * p.top_k, i1 = min(w0 + kWord, t1) * p.top_k;
-    if (w0 > t0) fill_words(p, ids, i0, i1, w0, sm);
+    if (w0 > t0) fill_words(p, ids, i0, i1, w0, expert_of(i0 + tid, i1), sm);
     for (int i = i0 + tid; i < i1; i += kPlanThreads) {
       const int e = ids[i], t = i / p.top_k - w0;
       if (e >= 0) {
