@@ -247,10 +247,6 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
       c[i] = x[i] > -INFINITY && fp8::finite(bias[i]) ? s + (C)bias[i] : -(C)INFINITY;
     }
   }
-  // (sums of biases may overflow in fp32; their difference is then infinite or NaN, and the bound infinite)
-  auto near = [&](C hi, C lo, float of) {
-    return kSingle && !((float)(hi - lo) > of * (tau + 0x1p-23f * fmaxf(fabsf((float)hi), fabsf((float)lo))));
-  };
   K key[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -268,12 +264,22 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
     // with sums of scores the keys compared are the scores'; else those of the choice itself
     auto key_of = [&](int i) -> K { return !by_logit || !sums ? key[i] : key[i] ? to_key(c[i]) : 0; };
     auto value_of = [&](K a, K b) -> K { return sums && b ? to_key(of_key(a) + of_key(b)) : a; };
+    // Error of a value in fp32: that of each c in it (tau / 2), and 2^-24 of their magnitudes for the
+    // addition of the bias, of the sum, and of what is compared below.  Of the summands' magnitudes: where
+    // biases of opposite signs cancel the sum's is far below what rounding them left.  (Finite, though
+    // the sum may not be.)
+    auto error_of = [&](K a, K b) -> float {
+      constexpr float k = 0x1.9p-23f;   // (3 2^-24, and its own rounding)
+      return (sums ? tau : 0.5f * tau) + k * fabsf((float)of_key(a)) + (sums && b ? k * fabsf((float)of_key(b)) : 0.0f);
+    };
+    float error = 0.0f;
     if (p.lanes > 0) {
       K a = 0, b = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) join(a, b, key_of(i), 0);
       for (int o = 1; o < p.lanes; o *= 2) join(a, b, __shfl_xor_sync(0xffffffffu, a, o), __shfl_xor_sync(0xffffffffu, b, o));
       value = value_of(a, b);
+      if constexpr (kSingle) error = error_of(a, b);
       if ((lane & (p.lanes - 1)) != 0 || lane >= p.lanes * p.groups) value = 0;
     } else {
       for (int g = 0; g < p.groups; ++g) {
@@ -283,23 +289,31 @@ __device__ __forceinline__ bool choose(const float (&x)[VPL], const RouteParams 
           if (i < p.each && e0 + i >= g * p.size && e0 + i < (g + 1) * p.size) join(a, b, key_of(i), 0);
 #pragma unroll
         for (int o = 16; o; o >>= 1) join(a, b, __shfl_xor_sync(0xffffffffu, a, o), __shfl_xor_sync(0xffffffffu, b, o));
-        if (lane == g) value = value_of(a, b);
+        if (lane == g) {
+          value = value_of(a, b);
+          if constexpr (kSingle) error = error_of(a, b);
+        }
       }
     }
     uint32_t open = 0;
-    K last = 0;
-    for (int j = 0; j <= p.top_groups && j < p.groups; ++j) {
+    const K valued = value;
+    for (int j = 0; j < p.top_groups; ++j) {
       const K best = warp_max_key(value);
       if (best == 0) break;
-      if (j == p.top_groups) {
-        if ((!by_logit || sums) && near(of_key(last), of_key(best), sums ? 2.0f : 1.0f)) sure = false;
-        break;
-      }
       const int w = __ffs(__ballot_sync(0xffffffffu, value == best)) - 1;
       open |= 1u << (p.lanes > 0 ? w >> p.shift : w);
       if (lane == w) value = 0;
-      last = best;
     }
+    if constexpr (kSingle)
+      if (!by_logit || sums) {
+        // fp32 tells if the least that an open group may have is above the most of all others.  (A value
+        // past fp32's range is at least, or at most, its largest number.)
+        constexpr float kLargest = 0x1.fffffep127f;
+        const float v = of_key(valued);
+        const uint32_t least = valued && !value ? to_key(fminf(v, kLargest) - error) : 0xffffffffu;
+        const uint32_t most = value ? to_key(fmaxf(v, -kLargest) + error) : 0;
+        sure = __reduce_min_sync(0xffffffffu, least) > __reduce_max_sync(0xffffffffu, most);
+      }
     if constexpr (EXACT)
       if (!sure && p.sigmoid && p.lanes > 0) {
         uint32_t score[VPL];

@@ -342,6 +342,20 @@ def test_route_by_biases_of_any_size(scores, experts):
                 _check_route(logits, 3, bias, scores=scores, groups=groups, top_groups=top, group_top=group_top)
 
 
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups", [(8, 4), (64, 32), (45, 5), (96, 8)])
+@pytest.mark.parametrize("uneven", [False, True])
+def test_route_by_groups_whose_sums_cancel(scores, experts, groups, uneven):
+    """The two largest of a group with biases of opposite signs: their sum is small, what rounding them leaves is not."""
+    rng = np.random.default_rng(experts + uneven)
+    logits = torch.from_numpy((1.5 * rng.standard_normal((1500, experts))).astype(np.float32))
+    for size in (1e2, 1e3, 1e4, 1e5, 1e6):
+        of_group = size * (3e-3 ** rng.random(groups) if uneven else np.ones(groups))
+        bias = np.repeat(-of_group[:, None], experts // groups, 1)
+        bias[:, 0] = of_group
+        _check_route(logits, 2, torch.from_numpy(bias.reshape(-1).astype(np.float32)), scores=scores, groups=groups, top_groups=1, group_top=2)
+
+
 def test_route_of_a_view_and_on_another_stream():
     logits = _randn(9, 100, 70)
     wide = torch.full((100, 90), math.nan, device=DEV)
