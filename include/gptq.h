@@ -693,8 +693,10 @@ gptq_status gptq_fp8_gated(const uint8_t *a, int64_t lda, const uint8_t *a_exps,
  *         choice is that of 64-bit arithmetic: c nearer to one another than fp32 tells are taken
  *         again in fp64.
  *   weights: s of the chosen experts, with renormalize over their sum, times scale.
- * An expert whose logit or bias is not finite is never chosen and adds nothing to the softmax's sum;
- * where too few are left, the last ids of the token are -1 and their weights 0.
+ * An expert whose logit or bias is not finite is never chosen; where too few are left, the last ids
+ * of the token are -1 and their weights 0.  A logit that is not finite adds nothing to the softmax's
+ * sum; a bias, finite or not, has no part in the scores: an expert that only its bias leaves out
+ * keeps its part of the sum (and so of weights that are not renormalized).
  *
  *   logits     [n_tokens, ld] of dtype (F16, BF16, F32), ld >= n_experts.
  *   bias       [n_experts] fp32 or NULL.   scores: 0 softmax, 1 sigmoid.

@@ -1069,7 +1069,8 @@ def moe_route(logits, top_k, bias=None, scores="softmax", groups=1, top_groups=N
     ``scale``.  ``order [tokens * top_k]`` lists the assignments ``token * top_k + place`` by expert,
     expert e's from ``offsets[e]`` on: what ``fp8_experts_gated`` and ``fp8_experts`` take.
     Experts whose logit or bias is not finite are never chosen (ids of -1, weights of 0 where too few
-    are left).  The four are tensors of one storage."""
+    are left); one that only its bias leaves out keeps its part of the softmax's sum.  The four are
+    tensors of one storage."""
     if scores not in SCORES:
         raise ValueError(f"scores must be one of {list(SCORES)}")
     if groups == 1:

@@ -326,6 +326,19 @@ def test_route_masks(dtype, kw):
         _check_route(torch.where(torch.isfinite(logits), logits * 0 - 90 - 3 * _randn(8, 80, 24).to(DT[dtype]), logits), 4, **kw)
 
 
+@pytest.mark.parametrize("mask", [-math.inf, math.nan])
+@pytest.mark.parametrize("by", ["bias", "logit"])
+@pytest.mark.parametrize("tokens", [1, 70])
+def test_route_with_an_expert_left_out_of_the_choice_or_of_the_sum(mask, by, tokens):
+    """Weights written out: a bias leaves an expert out of the choice alone, a logit out of the softmax's sum too."""
+    logits, bias = torch.tensor([[1.0, 2.0, 3.0]]).repeat(tokens, 1), torch.zeros(3)
+    (bias if by == "bias" else logits[0])[2] = mask
+    ids, weights, offsets, _ = gptq.moe_route(logits.to(DEV), 2, bias.to(DEV), renormalize=False)
+    assert ids[0].tolist() == [1, 0] and (by == "logit" or offsets.tolist() == [0, tokens, 2 * tokens, 2 * tokens])
+    want = [0.24472847105479764, 0.09003057317038045] if by == "bias" else [0.7310585786300049, 0.2689414213699951]
+    np.testing.assert_allclose(weights[0].cpu().numpy(), want, rtol=2.0 ** -20)
+
+
 @pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("experts", [24, 60, 256])
 def test_route_by_biases_of_any_size(scores, experts):

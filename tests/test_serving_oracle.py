@@ -76,3 +76,13 @@ def test_attention_of_a_uniform_cache_is_the_mean():
     assert np.all(out[0, 0] == 0) and np.allclose(out[0, 2, 1], V[:2].mean(0))
     out, _, _ = SO.kv_attention(q, (kc, vc, ones, ones), np.array([[-1, 0]], np.int32), np.array([128]))
     np.testing.assert_allclose(out[0, 2, 1], V[64:].mean(0), rtol=1e-12)
+
+
+def test_route_leaves_out_by_bias_or_by_logit():
+    # weights written out: a bias has no part in the softmax's sum, a logit that is not finite adds nothing to it
+    x = np.array([[1.0, 2.0, 3.0]])
+    ids, weights, offsets, _ = SO.route(x, 2, np.array([0, 0, -math.inf]), renormalize=False)
+    assert ids.tolist() == [[1, 0]] and offsets.tolist() == [0, 1, 2, 2]
+    np.testing.assert_allclose(weights, [[0.24472847105479764, 0.09003057317038045]], rtol=1e-14)
+    ids, weights, _, _ = SO.route(np.array([[1.0, 2.0, -math.inf]]), 2, np.zeros(3), renormalize=False)
+    np.testing.assert_allclose(weights, [[0.7310585786300049, 0.2689414213699951]], rtol=1e-14)
