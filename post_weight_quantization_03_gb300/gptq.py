@@ -1030,7 +1030,12 @@ def _marshal():
         lib = load()
         _torch()
         if not os.path.exists(build_lib.MARSHAL):
-            raise RuntimeError(f"{build_lib.MARSHAL} is missing: it must be built (build_lib.build())")
+            raise RuntimeError(f"{build_lib.MARSHAL} is missing: it must be built (build_lib.build(); needs g++ and "
+                               "torch's headers)")
+        built, here = build_lib.marshal_built_against(), build_lib.marshal_tag()
+        if built not in (None, here):
+            raise RuntimeError(f"{build_lib.MARSHAL} was built against {built}, this is {here}: it must be built again "
+                               "(build_lib.build())")
         from . import _marshal as module
         module.bind(tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "gptq_fp8_linear", "gptq_fp8_gated", "gptq_fp8_experts", "gptq_fp8_experts_gated",
