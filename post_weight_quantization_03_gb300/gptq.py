@@ -739,12 +739,15 @@ def _fp8_empty(rows, d, row_block, device, stream):
     torch = _torch()
     pitch, kb = (d + 15) & ~15, (d + FP8_BLOCK - 1) // FP8_BLOCK
     erows, epitch = (rows + row_block - 1) // row_block, (kb + 3) & ~3
-    # (one torch operation each: in a loop of calls every one takes 3 us of host time.  The kernels read
-    # a last row's exponents by words; torch's allocations end at multiples of 512 bytes)
-    codes = torch.empty_strided((rows, d), (pitch, 1), dtype=torch.float8_e4m3fn, device=device)
-    exps = torch.empty_strided((erows, kb), (epitch, 1), dtype=torch.uint8, device=device)
+    # (the last row has its whole pitch too: the kernels read exponents by words)
+    codes = torch.empty((rows, pitch), dtype=torch.float8_e4m3fn, device=device)
+    exps = torch.empty((erows, epitch), dtype=torch.uint8, device=device)
     if stream is not None:
         _lend(stream, codes, exps)
+    if pitch != d:
+        codes = codes.as_strided((rows, d), (pitch, 1))
+    if epitch != kb:
+        exps = exps.as_strided((erows, kb), (epitch, 1))
     return codes, pitch, exps, epitch
 
 

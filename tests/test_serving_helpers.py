@@ -69,3 +69,14 @@ def test_row_blocks():
         gptq.fp8_quantize(_empty(4, 64), 0)
     with pytest.raises(ValueError):
         gptq.fp8_quantize(_empty(4, 64), 64)
+
+
+@pytest.mark.parametrize("rows,d", [(1, 1), (1, 300), (5, 128), (5, 130), (130, 1000), (0, 300), (256, 4096)])
+@pytest.mark.parametrize("row_block", [1, 128])
+def test_coded_matrices_have_their_last_rows_whole_pitch(rows, d, row_block):
+    # the kernels read a row's exponents by words of four, also the last row's
+    codes, pitch, exps, epitch = gptq._fp8_empty(rows, d, row_block, torch.device("cpu"), None)
+    erows, kb = -(-rows // row_block), -(-d // 128)
+    assert codes.shape == (rows, d) and exps.shape == (erows, kb) and pitch % 16 == 0 and epitch % 4 == 0
+    assert codes.untyped_storage().nbytes() >= rows * pitch and exps.untyped_storage().nbytes() >= erows * epitch
+    assert (rows < 2 or codes.stride() == (pitch, 1)) and (erows < 2 or exps.stride() == (epitch, 1))
