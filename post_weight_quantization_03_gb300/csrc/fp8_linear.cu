@@ -184,6 +184,11 @@ __device__ __forceinline__ Tile tile_of(const Params &p, const Plan &plan, int t
   return r;
 }
 
+// The word of a row's last one to three exponents.
+__device__ __forceinline__ uint32_t last_exponents(const uint8_t *from, int n) {
+  return (uint32_t)from[0] | (n > 1 ? (uint32_t)from[1] << 8 : 0u) | (n > 2 ? (uint32_t)from[2] << 16 : 0u);
+}
+
 // A's row of a position, a_rows (read as zeros) for none.
 template <bool GATHER>
 __device__ __forceinline__ int a_row(const Params &p, const Plan &plan, int pos) {
@@ -529,11 +534,19 @@ linear_kernel(const __grid_constant__ CUtensorMap mw0, const __grid_constant__ C
 #pragma unroll 1
       for (int sb = k0 / 4; 4 * sb < k1; ++sb, ++g) {
         uint32_t word[8], ww[W];
+        if (4 * sb + 4 <= p.kb) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          word[i] = row[i] >= 0 ? *reinterpret_cast<const uint32_t *>(p.ae + row[i] + 4 * sb) : 0x7F7F7F7Fu;
+          for (int i = 0; i < 8; ++i)
+            word[i] = row[i] >= 0 ? *reinterpret_cast<const uint32_t *>(p.ae + row[i] + 4 * sb) : 0x7F7F7F7Fu;
 #pragma unroll
-        for (int w = 0; w < W; ++w) ww[w] = *reinterpret_cast<const uint32_t *>(we[w] + 4 * sb);
+          for (int w = 0; w < W; ++w) ww[w] = *reinterpret_cast<const uint32_t *>(we[w] + 4 * sb);
+        } else {
+          // what lies behind a row's last exponent need not be there (a matrix of one row has any pitch)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) word[i] = row[i] >= 0 ? last_exponents(p.ae + row[i] + 4 * sb, p.kb - 4 * sb) : 0x7F7F7F7Fu;
+#pragma unroll
+          for (int w = 0; w < W; ++w) ww[w] = last_exponents(we[w] + 4 * sb, p.kb - 4 * sb);
+        }
         const int q = g % kScaleStages;
         // two TMEM groups: wait for the MMAs of two groups back, not only for this slot's
         if (g >= 2) ok = tc::mbar_wait_compact(&sempty[(g - 2) % kScaleStages], ((g - 2) / kScaleStages) & 1, waits);

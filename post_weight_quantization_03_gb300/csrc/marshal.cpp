@@ -156,12 +156,12 @@ Weights weights(const char *name, const at::Tensor &w, const at::Tensor &e, cons
   floats(scale, "the scale of " + std::string(name), shape, gpu);
   floats(bias, "the bias of " + std::string(name), shape, gpu);
   Weights r{rows, {}};
+  // (the step from the only row to the next has no meaning: any will do that the library takes)
   r.w.codes = bytes(w);
-  // a matrix of one row may have any pitch
-  r.w.ld = rows == 1 ? std::max(w.stride(lead), (k + 15) & ~(int64_t)15) : w.stride(lead);
+  r.w.ld = rows == 1 ? (k + 15) & ~(int64_t)15 : w.stride(lead);
   r.w.next_codes = lead ? w.stride(0) : 0;
   r.w.exps = bytes(e);
-  r.w.ld_exps = nb == 1 ? std::max(e.stride(lead), (kb + 3) & ~(int64_t)3) : e.stride(lead);
+  r.w.ld_exps = nb == 1 ? (kb + 3) & ~(int64_t)3 : e.stride(lead);
   r.w.next_exps = lead ? e.stride(0) : 0;
   r.w.scale = cptr<float>(scale);
   r.w.bias = cptr<float>(bias);
@@ -253,8 +253,7 @@ class Together {
   at::Tensor all_;
 };
 
-// Codes and exponents [rows, n] in the pitches that the library asks for.  (The kernels read a last
-// row's exponents by words, for which there is room.)
+// Codes and exponents [rows, n] in the pitches that the library asks for, the last row's whole.
 struct Coded {
   at::Tensor codes, exps;
   int64_t ldc, lde;

@@ -435,6 +435,39 @@ def test_experts_of_every_second_matrix():
     assert torch.equal(gptq.fp8_experts(*rows, *some[:2], *args, some[2], some[3]), gptq.fp8_experts(*rows, *alone[:2], *args, alone[2], alone[3]))
 
 
+@pytest.mark.parametrize("n", [1, 100])
+def test_weights_of_one_row_of_blocks_in_any_pitch(n):
+    k, experts, tokens = 300, 4, 20
+    a, ae = _fp8_matrix(2, tokens, k, 1, 0.5)
+    A = _dev_codes(a), _dev_exps(ae)
+    ws = [_weights(10 + i, n, k) for i in range(experts)]
+    codes, exps, scale, _ = _experts_on_dev(ws)
+    _, offsets, order = _routes(1, tokens, experts, 1)
+    plan = _dev(offsets), _dev(order)
+
+    def call(c, e):
+        return gptq.fp8_experts(*A, c, e, *plan, scale)
+
+    want, one = call(codes, exps), gptq.fp8_linear(*A, codes[0], exps[0], w_scale=scale[0])
+    # the step from a matrix's only row to the next has no meaning: it may pass the one between matrices
+    across = torch.full((1, experts, 8), 255, dtype=torch.uint8, device=DEV).transpose(0, 1)[:, :, :3].copy_(exps)
+    assert across.stride(1) > across.stride(0) and torch.equal(call(codes, across), want)
+    if n == 1:
+        rows = torch.zeros(1, experts, 320, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn).transpose(0, 1)[:, :, :k]
+        rows.view(torch.uint8).copy_(codes.view(torch.uint8))
+        assert rows.stride(1) > rows.stride(0) and torch.equal(call(rows, exps), want)
+    # exponents that end with their storage, as a clone of one row does
+    short = torch.full((4 * experts - 1,), 255, dtype=torch.uint8, device=DEV)
+    assert torch.equal(call(codes, short.as_strided((experts, 1, 3), (4, 3, 1)).copy_(exps)), want)
+    alone = exps[0].clone()
+    assert alone.untyped_storage().nbytes() == 3 and torch.equal(gptq.fp8_linear(*A, codes[0], alone, w_scale=scale[0]), one)
+    w = codes[0], exps[0], scale[0]
+    for m in (1, tokens):
+        x, xe = A[0][:m], A[1][:m]
+        got, again = (gptq.fp8_gated(x, t, (w[0], u, w[2]), (w[0], u, w[2])) for t, u in ((xe, w[1]), (xe.clone() if m == 1 else xe, alone)))
+        assert np.array_equal(_np(got[0]), _np(again[0])) and torch.equal(got[1], again[1])
+
+
 @pytest.mark.parametrize("tokens", [15, 16, 17, 31, 48, 65, 80, 96, 97, 104, 111, 112, 113, 150, 220, 224, 240, 241, 330, 336, 448, 670, 1000])
 def test_experts_tiles_of_every_size(tokens):
     """One expert of `tokens` rows and a second of a few: tiles of all sizes, and rows at every place in them."""
