@@ -291,6 +291,67 @@ def test_experts_write_their_rows_alone(tokens, experts, top_k, n, k):
     assert bool((o[:, n * 2:] == PAT).all()) and bool((o[unnamed] == PAT).all())
 
 
+def _bad_plans(rng, experts, rows):
+    """Offsets that fall, are out of range or both."""
+    sorted_ = np.sort(rng.integers(0, rows + 1, experts + 1))
+    wild = sorted_.copy()
+    wild[rng.integers(0, experts + 1, 2)] = 2 ** 31 - 1, -2 ** 31
+    yield from (np.zeros(experts + 1), sorted_[::-1], sorted_ + rows // 3, sorted_ - rows // 3, wild, rng.integers(-rows, 2 * rows, experts + 1),
+                np.where(np.arange(experts + 1) < experts, sorted_, -7))
+
+
+@pytest.mark.parametrize("tokens,experts,top_k,n,k", [(1, 4, 2, 200, 300), (40, 6, 2, 200, 256), (300, 40, 2, 130, 384), (400, 3, 3, 257, 128)])
+def test_experts_by_a_plan_that_makes_no_sense(tokens, experts, top_k, n, k):
+    """Offsets are limited to the rows there are and read as increasing; an order that names no row of A stands for
+    zeros, one that names no row of the output for none.  What no position names stays as it was."""
+    rows = tokens * top_k
+    rng = np.random.default_rng(tokens)
+    hw = [_weights(10 + i, n, k) for i in range(experts)]
+    w = _experts_on_dev(hw)
+    a, ae = _fp8_matrix(2, tokens, k, 1, 0.5)
+    x, xe = _fp8_matrix(3, rows, k, 1, 0.5)
+    A, AE, X, XE = _dev_codes(a), _dev_exps(ae), _dev_codes(x), _dev_exps(xe)
+    ws = gptq.workspace(256, DEV)
+    tail = (_p(ws), 256, gptq._stream(None))
+    ldc, lde, nb = -(-n // 16) * 16 + 16, -(-(-(-n // 128)) // 4) * 4 + 4, -(-n // 128)
+    for offsets in _bad_plans(rng, experts, rows):
+        offsets = offsets.astype(np.int32)
+        order = rng.permutation(rows).astype(np.int32)
+        for at, bad in zip(rng.permutation(rows), (-5, 10 ** 9, rows, -2 ** 31, 2 ** 31 - 1)):
+            order[at] = bad
+        O, R = _dev(offsets), _dev(order)
+        codes, exps, out = Guarded(rows * ldc), Guarded(rows * lde), Guarded(rows * (n + 3) * 2)
+        _ok(gptq.gptq_fp8_experts_gated(_p(A), A.stride(0), _p(AE), AE.stride(0), None, _struct(w, True), _struct(w, True), 2, experts, _p(O),
+                                        _p(R), top_k, tokens, n, k, codes.ptr, ldc, exps.ptr, lde, *tail))
+        _ok(gptq.gptq_fp8_experts(_p(X), X.stride(0), _p(XE), XE.stride(0), _struct(w, True), 0, experts, _p(O), _p(R), rows, n, k, out.ptr, 1,
+                                  n + 3, *tail))
+        assert codes.intact() and exps.intact() and out.intact()
+        c, e = codes.view(torch.uint8, (rows, ldc)), exps.view(torch.uint8, (rows, lde))
+        o = out.view(torch.uint8, (rows, (n + 3) * 2))
+        assert bool((c[:, n:] == PAT).all()) and bool((e[:, nb:] == PAT).all()) and bool((o[:, n * 2:] == PAT).all())
+        begins = np.maximum.accumulate(np.clip(offsets.astype(np.int64), 0, rows))
+        none = np.r_[0:begins[0], begins[-1]:rows]
+        assert bool((c[_dev(none)] == PAT).all()) and bool((e[_dev(none)] == PAT).all())
+        named = order[begins[0]:begins[-1]]
+        unnamed = np.setdiff1d(np.arange(rows), named)
+        assert bool((o[_dev(unnamed)] == PAT).all())
+        values = o[:, :n * 2].contiguous().view(torch.bfloat16)
+        for i in range(experts):
+            at = np.arange(begins[i], begins[i + 1])
+            if len(at) == 0:
+                continue
+            token = order[at].astype(np.int64) // top_k
+            there = (token >= 0) & (token < tokens)
+            token = np.where(there, token, 0)
+            z = np.where(there[:, None], a[token], 0).astype(np.uint8)
+            _check_codes(c[_dev(at)][:, :n].view(torch.float8_e4m3fn), e[_dev(at)][:, :nb], *_want_gated(z, ae[token], hw[i], hw[i], None, "silu", k))
+            at = at[(order[at] >= 0) & (order[at] < rows)]
+            if len(at):
+                want, tol = _want_linear(x[at], xe[at], hw[i], None, None, None, k)
+                _check16(values[_dev(order[at].astype(np.int64))], want, tol)
+    gptq.serving_status()
+
+
 @pytest.mark.parametrize("tokens,experts,top_k,d", [(1, 7, 3, 5), (33, 100, 8, 130), (3000, 17, 2, 64), (9000, 64, 4, 8)])
 def test_routing_and_combine_write_their_rows_alone(tokens, experts, top_k, d):
     logits = _randn(1, tokens, experts).to(DEV)
