@@ -626,7 +626,7 @@ gptq_status gptq_debug_kv8_attention_lost_copy(
  * ====================================================================================== */
 
 /* Activation functions, taken in fp32: x, max(x, 0) (NaN stays), x / (1 + exp(-x)),
- * x (1 + erf(x / sqrt 2)) / 2. */
+ * x (1 + erf(x / sqrt 2)) / 2.  (SILU of less than about -87, below 2^-119 in magnitude, is 0.) */
 typedef enum gptq_act {
   GPTQ_ACT_NONE = 0, GPTQ_ACT_RELU = 1, GPTQ_ACT_SILU = 2, GPTQ_ACT_GELU = 3
 } gptq_act;

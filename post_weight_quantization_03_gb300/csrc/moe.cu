@@ -11,7 +11,8 @@
 // another than its error bound fp64 decides.  That is slow here (two operations a cycle and SM), so the
 // bound is tight, and of sigmoids only the few in question are taken again, one in a lane; a softmax's
 // need the sum, and so all (30 us for a token that meets it).  Without a bias the order of
-// the c is that of the logits, which are compared themselves.
+// the c is that of the logits, which are compared themselves.  Between groups the bound is one for each,
+// by the magnitudes of the c that it sums: these may cancel.
 //
 // The sort is a count by expert and chunk of tokens, then for each chunk the sum of the counts before
 // it.  Within 64 tokens an assignment's place among its expert's is the number of lower bits in the
@@ -19,10 +20,12 @@
 // launches, or one for up to 32 tokens.
 //
 // Measured (GPU time): 1 token of 64 experts 4.2 us and 333 of 160 8.1, launches and latencies; 8192 of
-// 256 16 us by logits and 23 by sigmoids with a bias and groups, by issue slots (1000 and 1630
-// instructions a token, of which 450 are the eight rounds) and the order's latencies (5 us).
+// 256 16 us by logits and 23 by sigmoids with a bias and groups, by issue slots (1000 and 1610
+// instructions a token, of which 450 are the eight rounds) and the order's latencies (5 us); 39 by a softmax
+// with a bias and groups, whose tokens that fp32 does not tell are taken again whole.
 //
-// Combine: HBM-bound, one pass: 4096 x 8 rows of 4096 48 us, 6.9 TB/s; one token 1.8 us.
+// Combine: HBM-bound, one pass: 4096 x 8 rows of 4096 48 us, 6.9 TB/s of operands and outputs (some of which
+// are still in L2 when it ends); one token 1.8 us.
 #include <type_traits>
 
 #include "fp8.cuh"
@@ -34,7 +37,7 @@ namespace {
 using fp8::kVec;
 using fp8::Raw8;
 
-constexpr int kMaxChunks = 152;       // of tokens: one for each SM
+constexpr int kMaxChunks = 152;       // of tokens: one for each SM of a GB300 (the workspace's size asks no device)
 constexpr int kWord = 64;             // tokens that are sorted at once
 constexpr int kPlanThreads = 1024;
 constexpr int kOneTokens = 32;        // up to these, one CTA does everything
