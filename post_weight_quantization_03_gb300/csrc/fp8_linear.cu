@@ -28,17 +28,18 @@
 // Few tokens leave few tiles; each cluster of up to 8 CTAs then has one, whose k-blocks they share, and
 // their partial sums meet through distributed shared memory in rank order.
 //
-// Bounds, and what it measured (GPU time, tokens x n x k; TB/s: bytes of operands by time).  Few tokens:
-// the weights' bytes, at 5.3 to 6.4 TB/s once under way, and 3.5 to 6 us for a CTA's set-up, the first copies and the end: linear 1 x
-// 4096 x 11008 10.5 us (6.7 of them the bytes), gated 24 x 11008 x 4096 17.8 (13.6), experts gated 1
-// token of 6 of 64 x 1376 x 4096 16.8 (10.1), experts out 40 tokens x 4096 x 1376 52.8, 6.8 TB/s.  Many:
-// the tensor pipe, active in 69 % of the cycles of gated 4096 x 11008 x 4096: 238 us, 3.1 PFLOP/s (270
-// in a longer row of calls, at the power limit; what idles the pipe has not been found: a third fewer
-// bytes from L2 changed 1 %).  The experts' tiles have fewer tokens for their weights' way from L2: gated
-// 4096 tokens of 6 of 64 x 1376 x 4096 237 us, 2.3 PFLOP/s, 53 %.  linear 8192 x 11008 x 4096 234 us, 3.2
-// PFLOP/s, with a residual 252.  Short K: the epilogue, which takes as long however few the MMAs are:
-// linear 24576 x 4096 x 1376 124 us (x 128: 98), experts out 4096 tokens x 4096 x 1376 170 (x 128: 138),
-// gated 4096 x 11008 x 1024 109 (x 256: 98).
+// Bounds, and what it measured (GPU time, tokens x n x k; TB/s: bytes of operands by time).  Few
+// tokens: the weights' bytes, at 5.3 to 6.4 TB/s once under way, and 3.5 to 6 us for a CTA's set-up,
+// the first copies and the end: linear 1 x 4096 x 11008 10.5 us (6.7 of them the bytes), gated 24 x
+// 11008 x 4096 17.8 (13.6), experts gated 1 token of 6 of 64 x 1376 x 4096 16.8 (10.1), experts out 40
+// tokens x 4096 x 1376 52.8, 6.8 TB/s.  Many: the tensor pipe, active in 69 % of the cycles of gated
+// 4096 x 11008 x 4096: 238 us, 3.1 PFLOP/s (270 in a longer row of calls, at the power limit; what
+// idles the pipe has not been found: a third fewer bytes from L2 changed 1 %).  The experts' tiles
+// have fewer tokens for their weights' way from L2: gated 4096 tokens of 6 of 64 x 1376 x 4096 237 us,
+// 2.3 PFLOP/s, 53 %.  linear 8192 x 11008 x 4096 234 us, 3.2 PFLOP/s, with a residual 252.  Short K:
+// the epilogue, which takes as long however few the MMAs are: linear 24576 x 4096 x 1376 124 us (x
+// 128: 98), experts out 4096 tokens x 4096 x 1376 170 (x 128: 138), gated 4096 x 11008 x 1024 109 (x
+// 256: 98).
 #include <cudaTypedefs.h>
 #include <math.h>
 
