@@ -208,12 +208,18 @@ Run run_on(PyObject *stream, int gpu) {
   return {(gptq_stream_t)raw, c10::cuda::getStreamFromExternal((cudaStream_t)raw, (c10::DeviceIndex)gpu)};
 }
 
+// Elements of a workspace are counted as its bytes: it has to hold them.
+void holds(const at::Tensor &ws, int gpu) {
+  if (!ws.is_contiguous()) value_error("ws must be contiguous");
+  on(ws, gpu);
+}
+
 // The workspace given, or one block for each device: its status is not read back (serving_status tells
 // of a wait that gave up).  Never freed: the process may end after CUDA has.
 const at::Tensor &workspace(const at::Tensor &ws, const at::Tensor &like, int gpu) {
   static at::Tensor *blocks[128] = {};
   if (ws.defined()) {
-    on(ws, gpu);
+    holds(ws, gpu);
     return ws;
   }
   if (gpu >= 128) value_error("more devices than a status block is kept for");
@@ -430,7 +436,7 @@ PyObject *route(PyObject *const *v) {
   const Run run = run_on(v[10], gpu);
   const size_t need = g_entry.route_ws(n, (int)std::min(n_experts, (int64_t)INT32_MAX), top_k);
   const at::Tensor given = maybe(v[9], "ws");
-  if (given.defined()) on(given, gpu);
+  if (given.defined()) holds(given, gpu);
   const int64_t ws_bytes = given.defined() ? given.numel() : (int64_t)need;
   Together all;
   const int64_t at_ids = all.add(4 * n * top_k), at_w = all.add(4 * n * top_k), at_offsets = all.add(4 * (n_experts + 1));

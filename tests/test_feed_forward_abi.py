@@ -189,3 +189,23 @@ def test_helpers_refuse_what_does_not_match():
                dict(top_k=2, scale=float("inf"))):
         with pytest.raises(gptq.GptqError, match="INVALID_ARG"):
             gptq.moe_route(torch.zeros(4, 8, device=dev), **kw)
+
+
+@pytest.mark.gpu
+def test_helpers_refuse_workspaces_that_do_not_hold_their_elements():
+    import torch
+    dev = "cuda:0"
+    f8, u8 = torch.float8_e4m3fn, torch.uint8
+    a, ae = torch.zeros(4, 256, dtype=u8, device=dev).view(f8), torch.zeros(4, 4, dtype=u8, device=dev)[:, :2]
+    w, we = torch.zeros(130, 256, dtype=u8, device=dev).view(f8), torch.zeros(2, 4, dtype=u8, device=dev)[:, :2]
+    one = torch.zeros(1, dtype=u8, device=dev).expand(1 << 20)          # a million elements in one byte
+    offsets, order = torch.zeros(2, dtype=torch.int32, device=dev), torch.zeros(4, dtype=torch.int32, device=dev)
+    for call in (lambda: gptq.fp8_linear(a, ae, w, we, ws=one), lambda: gptq.fp8_gated(a, ae, (w, we), (w, we), ws=one),
+                 lambda: gptq.fp8_experts_gated(a, ae, (w[None], we[None]), (w[None], we[None]), offsets, order, 1, ws=one),
+                 lambda: gptq.fp8_experts(a, ae, w[None], we[None], offsets, order, ws=one),
+                 lambda: gptq.moe_route(torch.zeros(400, 8, device=dev), 2, ws=one)):
+        with pytest.raises(ValueError, match="contiguous"):
+            call()
+    assert gptq.moe_route(torch.zeros(400, 8, device=dev), 2, ws=torch.zeros(1 << 16, dtype=u8, device=dev))[0].shape == (400, 2)
+    gptq.fp8_linear(a, ae, w, we, ws=torch.zeros(256, dtype=u8, device=dev))
+    torch.cuda.synchronize()
